@@ -1,5 +1,5 @@
 """ctypes binding of libdgemm_gb300.so, one Python function per C entry point
-(include/gemm.h), with the same names and arguments.  Pointers are plain ints
+(include/gemm.h, include/gemm_experts.h), with the same names and arguments.  Pointers are plain ints
 (device addresses), streams are ints (cudaStream_t); every function returns
 the C status code.  No arithmetic happens here.
 """
@@ -129,6 +129,20 @@ _SIGNATURES = {
     "gemm_bf16_static_workspace": ([_i64, _i64, _i64, _vp, _i64, _i32, _vp, _i64, _i32, _vp,
                                     _i64, _i32, _i32, _f32, _f32, _vp, _i32, _i32, _vp], _i32),
     "gemm_build_flags": ([], _i32),
+    "gemm_grouped": ([_i32, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i32, _i64, _vp, _i64,
+                      _i32, _vp, _f32, _f32, _vp, _i64, _i32, _vp, _sz, _vp], _i32),
+    "gemm_grouped_workspace_size": ([_i32, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i32,
+                                     _i64], _sz),
+    "gemm_grouped_wgrad": ([_i32, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i64,
+                            _i32, _vp, _f32, _f32, _vp, _sz, _vp], _i32),
+    "gemm_grouped_wgrad_workspace_size": ([_i32, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64],
+                                          _sz),
+    "gemm_newton_schulz": ([_i32, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _i32, _i32,
+                            _f32, _f32, _f32, _f32, _vp, _sz, _vp], _i32),
+    "gemm_newton_schulz_workspace_size": ([_i64, _i64, _i64], _sz),
+    "gemm_w4": ([_i32, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i32, _vp, _i64, _i32,
+                 _vp, _vp, _i64, _i32, _vp, _sz, _vp], _i32),
+    "gemm_w4_workspace_size": ([_i32, _i64, _i64, _i64, _i64, _vp, _i64, _i32], _sz),
     "gemm_debug_count_writes": ([_vp, _i64], _i32),
 }
 # size of the library-owned scratch array used by gemm_bf16_static_workspace
@@ -261,6 +275,51 @@ def gemm_strided_plan_query(ab_dtype, batch, M, N, K, A, a_rs, a_cs, stride_a, B
                                        beta, bias, epi, split_k, workspace_bytes,
                                        ctypes.byref(plan))
     return st, plan
+
+
+def gemm_grouped(ab_dtype, groups, T, N, K, A, lda, B, ldb, lb, stride_b, C, ldc, c_dtype, offsets,
+                 alpha, beta, bias, stride_bias, epi, workspace, workspace_bytes, stream) -> int:
+    return lib().gemm_grouped(ab_dtype, groups, T, N, K, A, lda, B, ldb, lb, stride_b, C, ldc,
+                              c_dtype, offsets, alpha, beta, bias, stride_bias, epi, workspace,
+                              workspace_bytes, stream)
+
+
+def gemm_grouped_workspace_size(ab_dtype, groups, T, N, K, A, lda, B, ldb, lb, stride_b) -> int:
+    return lib().gemm_grouped_workspace_size(ab_dtype, groups, T, N, K, A, lda, B, ldb, lb,
+                                             stride_b)
+
+
+def gemm_grouped_wgrad(ab_dtype, groups, T, M, N, A, lda, D, ldd, C, ldc, stride_c, c_dtype,
+                       offsets, alpha, beta, workspace, workspace_bytes, stream) -> int:
+    return lib().gemm_grouped_wgrad(ab_dtype, groups, T, M, N, A, lda, D, ldd, C, ldc, stride_c,
+                                    c_dtype, offsets, alpha, beta, workspace, workspace_bytes,
+                                    stream)
+
+
+def gemm_grouped_wgrad_workspace_size(ab_dtype, groups, T, M, N, A, lda, D, ldd) -> int:
+    return lib().gemm_grouped_wgrad_workspace_size(ab_dtype, groups, T, M, N, A, lda, D, ldd)
+
+
+def gemm_newton_schulz(g_dtype, batch, M, N, G, ldg, stride_g, O, ldo, stride_o, o_dtype, steps,
+                       a, b, c, eps, workspace, workspace_bytes, stream) -> int:
+    return lib().gemm_newton_schulz(g_dtype, batch, M, N, G, ldg, stride_g, O, ldo, stride_o,
+                                    o_dtype, steps, a, b, c, eps, workspace, workspace_bytes,
+                                    stream)
+
+
+def gemm_newton_schulz_workspace_size(batch, M, N) -> int:
+    return lib().gemm_newton_schulz_workspace_size(batch, M, N)
+
+
+def gemm_w4(ab_dtype, groups, T, N, K, A, lda, Q, scales, zeros, group, C, ldc, c_dtype, offsets,
+            bias, stride_bias, epi, workspace, workspace_bytes, stream) -> int:
+    return lib().gemm_w4(ab_dtype, groups, T, N, K, A, lda, Q, scales, zeros, group, C, ldc,
+                         c_dtype, offsets, bias, stride_bias, epi, workspace, workspace_bytes,
+                         stream)
+
+
+def gemm_w4_workspace_size(ab_dtype, groups, T, N, K, A, lda, c_dtype) -> int:
+    return lib().gemm_w4_workspace_size(ab_dtype, groups, T, N, K, A, lda, c_dtype)
 
 
 def gemm_build_flags() -> int:

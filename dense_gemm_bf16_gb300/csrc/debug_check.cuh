@@ -21,9 +21,11 @@
 
 namespace dg {
 
-// Status word: bit 0 a bounded wait expired; bits 8-10 a failed debug check.
+// Status word: bit 0 a bounded wait expired; bit 1 bad group offsets in device
+// memory; bits 8-10 a failed debug check.
 enum : int {
     STATUS_TIMEOUT = 1,
+    STATUS_BAD_OFFSETS = 2,        // group offsets that do not ascend inside the rows
     STATUS_CHECK_BOUNDS = 1 << 8,  // a global address outside its buffer
     STATUS_CHECK_UNIT = 1 << 9,    // a decoded work unit outside the problem
     STATUS_CHECK_ALIGN = 1 << 10,  // a misaligned address (shared or global)

@@ -12,6 +12,7 @@
 #include "gemm.h"
 #include "internal.h"
 #include "ptx.cuh"
+#include "ragged.h"
 #include "span_check.h"
 #include "tile_order.h"
 
@@ -98,6 +99,10 @@ gemm_status_t device_state(DevState** out) {
             for (int bn : kBlockN)
                 if (e == cudaSuccess) e = tc_prepare(bn);
             if (e == cudaSuccess) e = sgemm_prepare();
+            if (e == cudaSuccess) e = rg_prepare_rows();
+            if (e == cudaSuccess) e = rg_prepare_wgrad();
+            if (e == cudaSuccess) e = rg_prepare_sym();
+            if (e == cudaSuccess) e = w4_prepare();
             if (e == cudaSuccess) {
                 d.max_pairs[2][0] = tc_max_pairs(128, 2);
                 d.max_pairs[2][1] = tc_max_pairs(256, 2);
@@ -1044,6 +1049,64 @@ Call make_call(int ab, int64_t batch, int64_t M, int64_t N, int64_t K, const voi
 }
 
 }  // namespace
+
+// ---------------------------------------------------------------- shared with the expert-layer entry points
+
+namespace {
+void fill_info(const DevState& d, DeviceInfo* out) {
+    out->sm_count = d.sm_count;
+    out->max_pairs = d.max_pairs[2][1] > 0 ? d.max_pairs[2][1] : d.sm_count / 2;
+    out->status = d.status;
+}
+}  // namespace
+
+gemm_status_t device_info(DeviceInfo* out) {
+    DevState* d = nullptr;
+    const gemm_status_t st = device_state(&d);
+    if (st == GEMM_OK) fill_info(*d, out);
+    return st;
+}
+
+uint64_t option_timeout_ns() { return static_cast<uint64_t>(g_opt_timeout_us.load()) * 1000ull; }
+
+int take_test_stall() { return static_cast<int>(g_opt_test_stall.exchange(0)); }
+
+namespace {
+bool encode_map(CUtensorMap* map, CUtensorMapDataType type, const void* ptr, int64_t inner,
+                int64_t outer, int64_t depth, int64_t outer_stride, int64_t depth_stride,
+                uint32_t box_inner, uint32_t box_outer) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer),
+                          static_cast<cuuint64_t>(depth)};
+    // (a stride of 0 is not encodable; a map of depth 1 never uses its own)
+    if (depth_stride == 0) depth_stride = outer_stride;
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(outer_stride),
+                             static_cast<cuuint64_t>(depth_stride)};
+    cuuint32_t box[3] = {box_inner, box_outer, 1u};
+    cuuint32_t estr[3] = {1u, 1u, 1u};
+    return fn(map, type, 3u, const_cast<void*>(ptr), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+}  // namespace
+
+bool encode_map16(CUtensorMap* map, int dt, const void* ptr, int64_t inner, int64_t outer,
+                  int64_t depth, int64_t outer_stride, int64_t depth_stride, uint32_t box_inner,
+                  uint32_t box_outer) {
+    return encode_map(map, dt == DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                      ptr, inner, outer, depth, outer_stride, depth_stride, box_inner, box_outer);
+}
+
+bool encode_map8(CUtensorMap* map, const void* ptr, int64_t inner, int64_t outer, int64_t depth,
+                 int64_t outer_stride, int64_t depth_stride, uint32_t box_inner,
+                 uint32_t box_outer) {
+    return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, ptr, inner, outer, depth, outer_stride,
+                      depth_stride, box_inner, box_outer);
+}
+
 }  // namespace dg
 
 using namespace dg;
@@ -1164,8 +1227,11 @@ gemm_status_t gemm_check_device_status(gemm_stream_t stream) {
         const int zero = 0;
         if (cudaMemcpy(d->status, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess)
             return GEMM_ERR_CUDA;
-        // bits 8 and up: a failed device-side check (debug build); bit 0: a wait expired
-        return (v & ~0xFF) ? GEMM_ERR_DEVICE_CHECK : GEMM_ERR_TIMEOUT;
+        // bits 8 and up: a failed device-side check (debug build); bit 0: a wait
+        // expired; bit 1: bad group offsets in device memory
+        if (v & ~0xFF) return GEMM_ERR_DEVICE_CHECK;
+        return (v & STATUS_BAD_OFFSETS) && !(v & STATUS_TIMEOUT) ? GEMM_ERR_INVALID_ARG
+                                                                 : GEMM_ERR_TIMEOUT;
     }
     return GEMM_OK;
 }

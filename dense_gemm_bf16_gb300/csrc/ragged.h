@@ -1,0 +1,158 @@
+// Declarations of the ragged-product kernel (grouped products, their weight
+// gradient, the symmetric products of the orthogonalised update) and of the
+// host helpers that the expert-layer entry points share (not part of the ABI).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "gemm.h"
+#include "internal.h"
+
+namespace dg {
+
+// What a tile of the ragged kernel is (see ragged_kernel.cuh).
+enum : int { RG_ROWS = 0, RG_WGRAD = 1, RG_SYM = 2 };
+
+// Output D[col][lane]: the lane operand's rows are the output's contiguous
+// dimension, the column operand's rows its rows.
+struct RgParams {
+    CUtensorMap tmap_a;      // lane operand, three-dimensional (z: group or 0)
+    CUtensorMap tmap_b;      // column operand, whole-tile boxes
+    CUtensorMap tmap_b32;    // column operand, K-major: boxes of 32 rows
+    const int32_t* offsets;  // [groups + 1] on the device, or null: equal groups
+    int32_t groups;
+    int32_t rows;            // T: rows that the offsets index (RG_ROWS, RG_WGRAD)
+    int32_t n_lane;          // output columns
+    int32_t n_col;           // output rows of a group where all groups have as many
+    int32_t K;               // contraction extent (RG_ROWS, RG_SYM)
+    int32_t lane_tiles;      // ceil(n_lane / lanes of a tile)
+    int32_t col_tile;        // columns of a tile at most (a multiple of 32)
+    int32_t total_tiles;     // equal groups and RG_WGRAD; else 0 (found on the device)
+    int32_t a_mn, b_mn;      // 1: operand stored with its rows contiguous (MN-major)
+    int32_t a_z, b_z;        // 1: the operand's z coordinate is the group
+    int32_t maps;            // 1: the tensor maps are set (some contraction is not empty)
+    uint32_t idesc;          // instruction descriptor without its N field
+    void* C;                 // output
+    const void* Cin;         // beta's input, same type and shape as C
+    int64_t ldc, stride_c, ldcin, stride_cin;
+    int32_t c_dtype, cin_dtype;  // types of one size
+    int32_t c_vec;           // C (and Cin) rows start on 16-byte boundaries
+    float alpha, beta;
+    const float* bias;       // [groups][n_lane] with stride_bias, or null
+    int64_t stride_bias;
+    int32_t act;
+    int32_t pdl;             // 1: wait for the grid before this one on the stream
+    int32_t test_stall;      // test only: leave one stage unfilled
+    int* status;
+    uint64_t timeout_ns;
+#if DG_DEBUG
+    int64_t dbg_c_elems;     // elements of C from C that the call may touch
+#endif
+};
+
+// Kernel variants: CTAs per tile (1, or 2 with cta_group::2 MMAs) and columns
+// of a tile at most; lanes are 128 per CTA.
+cudaError_t rg_launch_rows(int cg, int bt, const RgParams& p, int grid, cudaStream_t stream);
+cudaError_t rg_launch_wgrad(int cg, int bt, const RgParams& p, int grid, cudaStream_t stream);
+cudaError_t rg_launch_sym(int cg, int bt, const RgParams& p, int grid, cudaStream_t stream);
+cudaError_t rg_prepare_rows();   // kernel attributes (once per device)
+cudaError_t rg_prepare_wgrad();
+cudaError_t rg_prepare_sym();
+
+// ---- host helpers (gemm_api.cu)
+struct DeviceInfo {
+    int sm_count;
+    int max_pairs;     // two-CTA clusters resident at once
+    int* status;       // device error word
+};
+gemm_status_t device_info(DeviceInfo* out);   // the current device
+uint64_t option_timeout_ns();
+int take_test_stall();
+
+// Three-dimensional tensor map of 16-bit elements (inner, outer, depth), 128-byte
+// swizzled; strides in bytes.  False on failure.
+bool encode_map16(CUtensorMap* map, int dt, const void* ptr, int64_t inner, int64_t outer,
+                  int64_t depth, int64_t outer_stride, int64_t depth_stride, uint32_t box_inner,
+                  uint32_t box_outer);
+// ... of bytes, two-dimensional boxes of one z
+bool encode_map8(CUtensorMap* map, const void* ptr, int64_t inner, int64_t outer, int64_t depth,
+                 int64_t outer_stride, int64_t depth_stride, uint32_t box_inner,
+                 uint32_t box_outer);
+
+// One ragged product, from checked arguments (experts_api.cu): the lane
+// operand `a` and the column operand `b` as stored matrices.
+struct RgOperand {
+    const void* ptr;
+    int64_t ld;        // elements, a multiple of 8
+    int64_t stride;    // elements between groups (0: one matrix)
+    bool mn;           // stored with its rows contiguous
+    int64_t rows;      // rows in its role (lanes or columns)
+    int64_t k;         // contraction extent as stored
+};
+struct RgProblem {
+    int form;
+    int dt;            // DT_BF16 or DT_F16 operands
+    int64_t groups, T, n_lane, n_col, K;
+    const int32_t* offsets;
+    RgOperand a, b;
+    void* C;
+    const void* Cin;
+    int64_t ldc, stride_c, ldcin, stride_cin;
+    int c_dtype, cin_dtype;  // cin_dtype: read where beta != 0, of c_dtype's size
+    float alpha, beta;
+    const float* bias;
+    int64_t stride_bias;
+    int act;
+    bool pdl;
+};
+gemm_status_t rg_run(const RgProblem& q, const DeviceInfo& d, cudaStream_t stream);
+
+// ---- 4-bit weights (w4.cu)
+struct W4Params {
+    CUtensorMap tmap_q;      // [groups][N][K / 2] bytes, boxes of 128 bytes x 64 rows
+    CUtensorMap tmap_x;      // [T][K], boxes of 64 x the tokens of a tile
+    const uint8_t* q;
+    const void* scales;
+    const uint8_t* zeros;
+    const int32_t* offsets;  // or null
+    int32_t groups, T, N, K, group;
+    int32_t slots;           // groups a launch provides for (with offsets: the non-empty ones)
+    int32_t n_tiles, splits;
+    void* C;
+    int64_t ldc;
+    int32_t c_dtype;
+    const float* bias;
+    int64_t stride_bias;
+    int32_t act;
+    int* status;
+    uint64_t timeout_ns;
+#if DG_DEBUG
+    int64_t dbg_c_elems;
+#endif
+};
+cudaError_t w4_launch(int dt, int tokens, const W4Params& p, cudaStream_t stream);
+cudaError_t w4_prepare();
+// Dense [groups][N][K] weights of type dt: (q - z) * s, rounded once.
+cudaError_t w4_dequantise(int dt, const uint8_t* q, const void* scales, const uint8_t* zeros,
+                          int64_t rows, int64_t K, int group, void* out, cudaStream_t stream);
+
+// ---- element-wise passes of the orthogonalised update (newton_schulz.cu)
+struct NsParams {
+    const void* G;
+    int64_t ldg, stride_g;
+    int32_t g_dtype, g_vec;
+    int64_t batch;
+    int32_t M, N;
+    int32_t parts;           // blocks per matrix
+    float* partials;         // [batch][parts][3]
+    void* X;                 // fp16, [batch][M][ldx]
+    int64_t ldx;
+    float eps, scale;
+};
+cudaError_t ns_norm_launch(const NsParams& p, cudaStream_t stream);
+cudaError_t ns_scale_launch(const NsParams& p, cudaStream_t stream);
+
+}  // namespace dg
