@@ -128,17 +128,23 @@ gemm_status_t rg_run(const RgProblem& q, const DeviceInfo& d, cudaStream_t strea
     p.b_z = bz > 1;
     p.maps = q.form == RG_WGRAD ? q.T > 0 : q.K > 0;
     if (p.maps) {
+        // MN-major boxes bring two 64-deep K blocks; K-major ones too where K is a
+        // whole number of blocks, else one block each
+        p.a_k4 = !q.a.mn && q.a.k % 64 == 0;
+        p.b_k4 = !q.b.mn && q.b.k % 64 == 0;
+        auto k_major = [&](CUtensorMap* map, const RgOperand& o, int64_t z, bool k4, int rows) {
+            return k4 ? encode_map16_k4(map, q.dt, o.ptr, o.k, o.rows, z, o.ld * 2, o.stride * 2, rows)
+                      : encode_map16(map, q.dt, o.ptr, o.k, o.rows, z, o.ld * 2, o.stride * 2, 64,
+                                     rows);
+        };
+        auto mn_major = [&](CUtensorMap* map, const RgOperand& o, int64_t z) {
+            return encode_map16(map, q.dt, o.ptr, o.rows, o.k, z, o.ld * 2, o.stride * 2, 64, 128);
+        };
         const bool ok =
-            (q.a.mn ? encode_map16(&p.tmap_a, q.dt, q.a.ptr, q.a.rows, q.a.k, az, q.a.ld * 2,
-                                   q.a.stride * 2, 64, 64)
-                    : encode_map16(&p.tmap_a, q.dt, q.a.ptr, q.a.k, q.a.rows, az, q.a.ld * 2,
-                                   q.a.stride * 2, 64, 128)) &&
-            (q.b.mn ? encode_map16(&p.tmap_b, q.dt, q.b.ptr, q.b.rows, q.b.k, bz, q.b.ld * 2,
-                                   q.b.stride * 2, 64, 64)
-                    : encode_map16(&p.tmap_b, q.dt, q.b.ptr, q.b.k, q.b.rows, bz, q.b.ld * 2,
-                                   q.b.stride * 2, 64, static_cast<uint32_t>(bt / cg)) &&
-                          encode_map16(&p.tmap_b32, q.dt, q.b.ptr, q.b.k, q.b.rows, bz,
-                                       q.b.ld * 2, q.b.stride * 2, 64, 32));
+            (q.a.mn ? mn_major(&p.tmap_a, q.a, az) : k_major(&p.tmap_a, q.a, az, p.a_k4, 128)) &&
+            (q.b.mn ? mn_major(&p.tmap_b, q.b, bz)
+                    : k_major(&p.tmap_b, q.b, bz, p.b_k4, bt / cg) &&
+                          k_major(&p.tmap_b32, q.b, bz, false, 32));
         if (!ok) return GEMM_ERR_CUDA;
     }
     p.idesc = make_idesc_f16(q.dt == DT_BF16, q.a.mn, q.b.mn, 128 * cg, 0);

@@ -1100,6 +1100,23 @@ bool encode_map16(CUtensorMap* map, int dt, const void* ptr, int64_t inner, int6
                       ptr, inner, outer, depth, outer_stride, depth_stride, box_inner, box_outer);
 }
 
+bool encode_map16_k4(CUtensorMap* map, int dt, const void* ptr, int64_t k, int64_t rows,
+                     int64_t depth, int64_t row_stride, int64_t depth_stride, uint32_t box_rows) {
+    auto fn = encode_fn();
+    if (!fn || k % 64 != 0) return false;
+    if (depth_stride == 0) depth_stride = row_stride;  // (depth 1: never used)
+    cuuint64_t dims[4] = {64u, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(k / 64),
+                          static_cast<cuuint64_t>(depth)};
+    cuuint64_t strides[3] = {static_cast<cuuint64_t>(row_stride), 128u,
+                             static_cast<cuuint64_t>(depth_stride)};
+    cuuint32_t box[4] = {64u, box_rows, 2u, 1u};
+    cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    return fn(map, dt == DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+              4u, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool encode_map8(CUtensorMap* map, const void* ptr, int64_t inner, int64_t outer, int64_t depth,
                  int64_t outer_stride, int64_t depth_stride, uint32_t box_inner,
                  uint32_t box_outer) {

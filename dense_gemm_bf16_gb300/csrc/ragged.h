@@ -19,9 +19,9 @@ enum : int { RG_ROWS = 0, RG_WGRAD = 1, RG_SYM = 2 };
 // Output D[col][lane]: the lane operand's rows are the output's contiguous
 // dimension, the column operand's rows its rows.
 struct RgParams {
-    CUtensorMap tmap_a;      // lane operand, three-dimensional (z: group or 0)
+    CUtensorMap tmap_a;      // lane operand, (inner, outer, z: group or 0)
     CUtensorMap tmap_b;      // column operand, whole-tile boxes
-    CUtensorMap tmap_b32;    // column operand, K-major: boxes of 32 rows
+    CUtensorMap tmap_b32;    // column operand, K-major: (K, rows, z), boxes of 64 x 32
     const int32_t* offsets;  // [groups + 1] on the device, or null: equal groups
     int32_t groups;
     int32_t rows;            // T: rows that the offsets index (RG_ROWS, RG_WGRAD)
@@ -32,6 +32,7 @@ struct RgParams {
     int32_t col_tile;        // columns of a tile at most (a multiple of 32)
     int32_t total_tiles;     // equal groups and RG_WGRAD; else 0 (found on the device)
     int32_t a_mn, b_mn;      // 1: operand stored with its rows contiguous (MN-major)
+    int32_t a_k4, b_k4;      // 1: K-major map is (64 K, rows, K blocks, z): two blocks a load
     int32_t a_z, b_z;        // 1: the operand's z coordinate is the group
     int32_t maps;            // 1: the tensor maps are set (some contraction is not empty)
     uint32_t idesc;          // instruction descriptor without its N field
@@ -77,6 +78,10 @@ int take_test_stall();
 bool encode_map16(CUtensorMap* map, int dt, const void* ptr, int64_t inner, int64_t outer,
                   int64_t depth, int64_t outer_stride, int64_t depth_stride, uint32_t box_inner,
                   uint32_t box_outer);
+// K-major matrix with a whole number of 64-wide K blocks as (64, rows, K blocks,
+// depth), in boxes of 64 x box_rows x 2 blocks.
+bool encode_map16_k4(CUtensorMap* map, int dt, const void* ptr, int64_t k, int64_t rows,
+                     int64_t depth, int64_t row_stride, int64_t depth_stride, uint32_t box_rows);
 // ... of bytes, two-dimensional boxes of one z
 bool encode_map8(CUtensorMap* map, const void* ptr, int64_t inner, int64_t outer, int64_t depth,
                  int64_t outer_stride, int64_t depth_stride, uint32_t box_inner,

@@ -25,10 +25,16 @@
 // Warps: 0 TMA producer, 1 MMA issuer (and the zeroing of ragged tails),
 // 2-9 epilogue, two per tensor-memory lane quarter taking 32-column chunks in
 // turn.  Two accumulators let a tile's epilogue overlap the next main loop.
-// The output's contiguous dimension runs along the lanes, so a chunk goes
-// through a shared-memory tile of 16 columns by 32 lanes (rows of 36 words:
-// conflict-free both ways) and leaves as 16-byte stores along the lanes; rows
-// of another group are masked per column.
+// The output's contiguous dimension runs along the lanes.  A 16-bit chunk is
+// read from tensor memory in the MMA-fragment layout, turned by transposing
+// 8 x 8 matrix stores into a shared-memory tile of 32 columns by 32 lanes (rows
+// of 64 bytes, 16-byte parts swizzled by the row: conflict-free both ways) and
+// leaves as 16-byte stores along the lanes; beta * Cin takes the same way in.
+// An fp32 chunk is read one lane per thread and stored directly: 32 lanes are
+// 128 contiguous bytes.  Rows of another group are masked per column.  (A
+// first form that turned fp32 values through padded rows with 4-byte stores
+// took 10.6 thousand cycles for a CTA's 128 x 256 tile, more than the main
+// loop of K = 1024.)
 //
 // Work: tiles are dealt round robin to CTAs (pairs).  Where group sizes are on
 // the device, each warp finds its tile by a 32-group window of prefix sums held
@@ -47,17 +53,18 @@ namespace dg {
 namespace {
 
 constexpr uint32_t kRgMaxSmem = 232448;  // 227 KB opt-in limit per CTA
-constexpr int RG_LD = 36;                // words per staged column
 
 template <int CG, int BT>
 struct RgCfg {
     static constexpr int B_ROWS = BT / CG;  // column-operand rows a CTA holds
-    static constexpr uint32_t A_BYTES = 128 * 128;
-    static constexpr uint32_t B_BYTES = B_ROWS * 128;
+    // a stage holds two 64-deep K blocks: half as many waits, loads and commits
+    // for the single threads that issue them
+    static constexpr uint32_t A_BYTES = 2 * 128 * 128;
+    static constexpr uint32_t B_BYTES = 2 * B_ROWS * 128;
     static constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int EPI_WARPS = 8;
     static constexpr int THREADS = 64 + 32 * EPI_WARPS;
-    static constexpr uint32_t EPI_WARP = 16 * RG_LD * 4;
+    static constexpr uint32_t EPI_WARP = 2 * 2048;  // two tiles of 32 x 32 16-bit elements
     static constexpr uint32_t EPI_SMEM = EPI_WARPS * EPI_WARP;
     static constexpr uint32_t BAR_BYTES = 512;
     static constexpr int FIT = (kRgMaxSmem - 1024 - BAR_BYTES - EPI_SMEM) / STAGE_BYTES;
@@ -226,53 +233,202 @@ __device__ __forceinline__ bool rg_span_ok(const RgParams& p, int64_t off, int n
 #endif
 }
 
-// NV (8 for 16-bit outputs, 4 for fp32: 16 bytes) neighbouring outputs of one
-// output row, columns n .. n + NV - 1 of which those below n_lane exist.
-// beta * Cin is added here unless MIRROR (RG_SYM adds it before).
-template <int NV, bool MIRROR>
-__device__ __forceinline__ void rg_store(const RgParams& p, int64_t off, int64_t off_in, int n,
-                                         float (&v)[NV]) {
-    const bool whole = p.c_vec && n + NV <= p.n_lane;
-    const bool beta = !MIRROR && p.beta != 0.0f;
-    constexpr int ES = NV == 8 ? 2 : 4;
-    if (!rg_span_ok(p, off, n + NV <= p.n_lane ? NV : p.n_lane - n)) return;
-    if (whole) {
-        char* dst = static_cast<char*>(p.C) + off * ES;
-        if (beta) {
-            const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const char*>(p.Cin) + off_in * ES);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-            if constexpr (NV == 8) {
+// Byte offset of 16-byte part `part` of row `row` in a staged 32 x 32 tile.
+__device__ __forceinline__ uint32_t rg_at(int row, int part) {
+    return static_cast<uint32_t>(row * 64 + ((part ^ ((row >> 1) & 3)) << 4));
+}
+
+// Elements off .. off + 7 of Cin, of which `n` exist (16-bit types).
+__device__ __forceinline__ uint4 rg_load8(const RgParams& p, int64_t off, int n) {
+    const char* src = static_cast<const char*>(p.Cin) + off * 2;
+    if (p.c_vec && n >= 8) return *reinterpret_cast<const uint4*>(src);
+    uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 f = rg_unpack(p.cin_dtype, w[i]);
-                    v[2 * i] = fmaf(p.beta, f.x, v[2 * i]);
-                    v[2 * i + 1] = fmaf(p.beta, f.y, v[2 * i + 1]);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = fmaf(p.beta, __uint_as_float(w[i]), v[i]);
-            }
-            act_inplace<NV>(v, p.act);
-        }
-        uint4 o;
-        if constexpr (NV == 8)
-            o = make_uint4(rg_pack(p.c_dtype, v[0], v[1]), rg_pack(p.c_dtype, v[2], v[3]),
-                           rg_pack(p.c_dtype, v[4], v[5]), rg_pack(p.c_dtype, v[6], v[7]));
-        else
-            o = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                           __float_as_uint(v[3]));
-        *reinterpret_cast<uint4*>(dst) = o;
+    for (int i = 0; i < 8; ++i)
+        if (i < n)
+            w[i >> 1] |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(src + 2 * i))
+                         << (16 * (i & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ void rg_store8(const RgParams& p, int64_t off, int n, uint4 v) {
+    if (!rg_span_ok(p, off, n < 8 ? n : 8)) return;
+    char* dst = static_cast<char*>(p.C) + off * 2;
+    if (p.c_vec && n >= 8) {
+        *reinterpret_cast<uint4*>(dst) = v;
         return;
     }
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        if (n + i >= p.n_lane) break;
-        float x = v[i];
-        if (beta) {
-            x = fmaf(p.beta, load_elem(static_cast<const char*>(p.Cin) + (off_in + i) * ES, p.cin_dtype), x);
-            x = apply_act(x, p.act);
+    for (int i = 0; i < 8; ++i)
+        if (i < n)
+            *reinterpret_cast<uint16_t*>(dst + 2 * i) =
+                static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+}
+
+// Epilogue of a warp's 32 lanes (output columns nl0 ..) of tile w for a 16-bit
+// C: the 32-column chunks half, half + 2, ...; `release` runs once the
+// accumulator has been read.
+template <int FORM, typename Release>
+__device__ __forceinline__ void rg_out16(const RgParams& p, const RgTile& w, uint32_t tmem_row,
+                                         int nl0, int half, int lane, uint8_t* buf, bool empty,
+                                         Release release) {
+    const int64_t c_base = w.group * p.stride_c + nl0;
+    const int64_t in_base = w.group * p.stride_cin + nl0;
+    const bool beta = p.beta != 0.0f;
+    const int pcol = lane >> 2, part = lane & 3;  // this lane's 16 bytes of a staged tile
+    const int nn = p.n_lane - nl0 - 8 * part;     // of which this many columns exist
+    const uint32_t s_out = smem_u32(buf), s_in = s_out + 2048u;
+    float bias[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int n = nl0 + 8 * i + pcol;
+        bias[i] = p.bias && n < p.n_lane ? __ldg(p.bias + w.group * p.stride_bias + n) : 0.0f;
+    }
+    uint4 cin[4];
+    auto load_in = [&](int c0) {
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+            const int c = c0 + 8 * it + pcol;
+            cin[it] = c < w.ncols && nn > 0
+                          ? rg_load8(p, in_base + (w.out_row + c) * p.ldcin + 8 * part, nn)
+                          : make_uint4(0, 0, 0, 0);
         }
-        store_elem(static_cast<char*>(p.C) + (off + i) * ES, p.c_dtype, x);
+    };
+    uint32_t r[32];
+    auto load_acc = [&](int c0) {
+        tmem_ld_16x256_x4(tmem_row + static_cast<uint32_t>(c0), r, 0);
+        tmem_ld_16x256_x4(tmem_row + (16u << 16) + static_cast<uint32_t>(c0), r, 1);
+    };
+    const int first = half * 32;
+    if (first >= w.ncols || nl0 >= p.n_lane) {
+        release();
+        return;
+    }
+    if (beta) load_in(first);
+#pragma unroll 1
+    for (int c0 = first; c0 < w.ncols; c0 += 64) {
+        if (empty) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = 0u;
+        } else {
+            load_acc(c0);
+            tmem_ld_wait(r);
+        }
+        float v[32];  // as the accumulator: [16-lane half][8-column block][2 lanes x 2 columns]
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            v[i] = fmaf(p.alpha, __uint_as_float(r[i]), bias[(i >> 4) * 2 + ((i >> 1) & 1)]);
+        const bool more = c0 + 64 < w.ncols;
+        if (!more && !empty) release();
+        if (beta) {
+            __syncwarp();
+#pragma unroll
+            for (int it = 0; it < 4; ++it)
+                *reinterpret_cast<uint4*>(buf + 2048 + rg_at(8 * it + pcol, part)) = cin[it];
+            if (more) load_in(c0 + 64);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t u[4];
+                ldmatrix_x4_trans(s_in + rg_at(8 * i + (lane & 7), lane >> 3), u[0], u[1], u[2], u[3]);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const float2 f = rg_unpack(p.cin_dtype, u[m]);
+                    float* x = v + 16 * (m >> 1) + 4 * i + 2 * (m & 1);
+                    x[0] = fmaf(p.beta, f.x, x[0]);
+                    x[1] = fmaf(p.beta, f.y, x[1]);
+                }
+            }
+        }
+        act_inplace<32>(v, p.act);
+        uint32_t pk[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const float* x = v + 16 * (m >> 1) + 4 * i + 2 * (m & 1);
+                pk[i][m] = rg_pack(p.c_dtype, x[0], x[1]);
+            }
+        __syncwarp();  // the previous chunk has left the staged tiles
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            stmatrix_x4_trans(s_out + rg_at(8 * i + (lane & 7), lane >> 3), pk[i][0], pk[i][1],
+                              pk[i][2], pk[i][3]);
+            // the mirrored tile: lanes as rows (an off-diagonal tile's columns all exist)
+            if (FORM == RG_SYM && !w.diag)
+                stmatrix_x4(s_in + rg_at(lane, i), pk[i][0], pk[i][1], pk[i][2], pk[i][3]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+            const int c = c0 + 8 * it + pcol;
+            const uint32_t at = rg_at(8 * it + pcol, part);
+            if (c < w.ncols && nn > 0)
+                rg_store8(p, c_base + (w.out_row + c) * p.ldc + 8 * part, nn,
+                          *reinterpret_cast<const uint4*>(buf + at));
+            if (FORM == RG_SYM && !w.diag && nl0 + 8 * it + pcol < p.n_lane)
+                rg_store8(p, w.group * p.stride_c + (nl0 + 8 * it + pcol) * p.ldc + w.col0 + c0 +
+                                 8 * part,
+                          8, *reinterpret_cast<const uint4*>(buf + 2048 + at));
+        }
+    }
+}
+
+// The same for an fp32 C: one lane (output column) per thread, stores of 32
+// neighbouring columns of one row.
+template <typename Release>
+__device__ __forceinline__ void rg_out32(const RgParams& p, const RgTile& w, uint32_t tmem_row,
+                                         int nl0, int half, int lane, bool empty,
+                                         Release release) {
+    const int n = nl0 + lane;
+    const int first = half * 32;
+    if (first >= w.ncols || nl0 >= p.n_lane) {
+        release();
+        return;
+    }
+    const bool in = n < p.n_lane;
+    const float bias = p.bias && in ? __ldg(p.bias + w.group * p.stride_bias + n) : 0.0f;
+    const bool beta = p.beta != 0.0f;
+    uint32_t r[32];
+#pragma unroll 1
+    for (int c0 = first; c0 < w.ncols; c0 += 64) {
+        if (empty) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = 0u;
+        } else {
+            tmem_ld_x32(tmem_row + static_cast<uint32_t>(c0), r);
+            tmem_ld_wait(r);
+        }
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = fmaf(p.alpha, __uint_as_float(r[i]), bias);
+        const bool more = c0 + 64 < w.ncols;
+        if (!more && !empty) release();
+        const int64_t row = w.out_row + c0;
+        if (beta && in) {
+            const float* src = static_cast<const float*>(p.Cin) + w.group * p.stride_cin +
+                               row * p.ldcin + n;
+            float f[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) f[i] = c0 + i < w.ncols ? src[i * p.ldcin] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = fmaf(p.beta, f[i], v[i]);
+        }
+        act_inplace<32>(v, p.act);
+        if (!in) continue;
+        const int64_t off = w.group * p.stride_c + row * p.ldc + n;
+        float* dst = static_cast<float*>(p.C) + off;
+        const int left = w.ncols - c0;
+        if (left >= 32) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (rg_span_ok(p, off + i * p.ldc, 1)) dst[i * p.ldc] = v[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (i < left && rg_span_ok(p, off + i * p.ldc, 1)) dst[i * p.ldc] = v[i];
+        }
     }
 }
 
@@ -359,13 +515,15 @@ __global__ void __launch_bounds__(RgCfg<CG, BT>::THREADS, 1)
                 const int rows_b = w.n_mma / CG;  // column rows of this CTA
                 const int b_row = w.b_row + static_cast<int>(rank) * rows_b;
                 const int za = p.a_z ? w.group : 0, zb = p.b_z ? w.group : 0;
-                // K-major columns: one whole-tile box, or 32-row boxes where those are fewer bytes
-                const bool big = p.b_mn == 0 && 4 * rows_b > 3 * C::B_ROWS;
-                const int nb = p.b_mn ? rows_b / 64 : (big ? 1 : (rows_b + 31) / 32);
-                const uint32_t b_bytes = p.b_mn ? nb * 8192u : (big ? C::B_BYTES : nb * 4096u);
+                const bool a_mn = p.a_mn, b_mn = p.b_mn, a_k4 = p.a_k4, b_k4 = p.b_k4;
+                // K-major columns: whole-tile boxes, or 32-row boxes where those are fewer bytes
+                const bool big = !b_mn && 4 * rows_b > 3 * C::B_ROWS;
+                const int nb = b_mn ? rows_b / 64 : (big ? 1 : (rows_b + 31) / 32);
+                const uint32_t b_bytes = b_mn ? nb * 16384u : (big ? C::B_BYTES : nb * 8192u);
+                const CUtensorMap* map_b = big || b_mn ? &p.tmap_b : &p.tmap_b32;
                 const uint32_t bytes = C::A_BYTES + b_bytes;
-                const int kblocks = (w.klen + 63) / 64;
-                for (int kb = 0; kb < kblocks; ++kb) {
+                const int ksteps = (w.klen + 127) / 128;
+                for (int ks = 0; ks < ksteps; ++ks) {
                     if (!mbar_wait(empty0 + 8u * stage, phase ^ 1u, abort_flag, p.status, p.timeout_ns)) {
                         ok = false;
                         break;
@@ -376,7 +534,7 @@ __global__ void __launch_bounds__(RgCfg<CG, BT>::THREADS, 1)
                     }
                     const uint32_t fb = full0 + 8u * stage;
                     // a ragged tail lands on each CTA's own barrier, for the zeroing
-                    const bool tail = FORM == RG_WGRAD && kb == kblocks - 1 && (w.klen & 15) != 0;
+                    const bool tail = FORM == RG_WGRAD && ks == ksteps - 1 && (w.klen & 15) != 0;
                     uint32_t bar;
                     if (tail) {
                         mbar_arrive_expect_tx(tail0 + 8u * stage, bytes);
@@ -396,21 +554,34 @@ __global__ void __launch_bounds__(RgCfg<CG, BT>::THREADS, 1)
                     };
                     const uint32_t a_dst = sA0 + stage * C::A_BYTES;
                     const uint32_t b_dst = sB0 + stage * C::B_BYTES;
-                    const int k = w.k0 + kb * 64;
-                    if (p.a_mn) {
+                    const int k = w.k0 + ks * 128;
+                    // K-major: the second block's rows follow the first's; MN-major:
+                    // 64-wide atom columns of 128 K rows (16 KB)
+                    if (a_k4) {
+                        tma_load_4d_cg<CG>(a_dst, &p.tmap_a, bar, 0, w.lane0, 2 * ks, za, pol);
+                    } else if (a_mn) {
                         load(a_dst, &p.tmap_a, w.lane0, k, za);
-                        load(a_dst + 8192u, &p.tmap_a, w.lane0 + 64, k, za);
+                        load(a_dst + 16384u, &p.tmap_a, w.lane0 + 64, k, za);
                     } else {
                         load(a_dst, &p.tmap_a, k, w.lane0, za);
+                        load(a_dst + 16384u, &p.tmap_a, k + 64, w.lane0, za);
                     }
-                    if (p.b_mn) {
+                    if (b_mn) {
                         for (int h = 0; h < nb; ++h)
-                            load(b_dst + 8192u * h, &p.tmap_b, b_row + 64 * h, k, zb);
+                            load(b_dst + 16384u * h, map_b, b_row + 64 * h, k, zb);
                     } else if (big) {
-                        load(b_dst, &p.tmap_b, k, b_row, zb);
+                        if (b_k4) {
+                            tma_load_4d_cg<CG>(b_dst, map_b, bar, 0, b_row, 2 * ks, zb, pol);
+                        } else {
+                            load(b_dst, map_b, k, b_row, zb);
+                            load(b_dst + C::B_BYTES / 2, map_b, k + 64, b_row, zb);
+                        }
                     } else {
-                        for (int h = 0; h < nb; ++h)
-                            load(b_dst + 4096u * h, &p.tmap_b32, k, b_row + 32 * h, zb);
+                        // (32-row boxes one block at a time: the blocks lie B_BYTES / 2 apart)
+                        for (int h = 0; h < nb; ++h) {
+                            load(b_dst + 4096u * h, map_b, k, b_row + 32 * h, zb);
+                            load(b_dst + C::B_BYTES / 2 + 4096u * h, map_b, k + 64, b_row + 32 * h, zb);
+                        }
                     }
                     ++armed;
                     if (++stage == C::STAGES) {
@@ -451,90 +622,106 @@ __global__ void __launch_bounds__(RgCfg<CG, BT>::THREADS, 1)
         uint32_t aphase = 0;
         bool issued = false, ok = true;
         const bool a_mn = p.a_mn != 0, b_mn = p.b_mn != 0;
-        const uint32_t a_lbo = a_mn ? 8192u : 16u, b_lbo = b_mn ? 8192u : 16u;
-        const uint32_t a_step = a_mn ? 2048u : 32u, b_step = b_mn ? 2048u : 32u;
+        // descriptors of stage 0; a stage or K = 16 step adds to their address fields
+        // (in 16 bytes; K-major: 32 bytes a step inside a block, MN-major: 16 rows)
+        const uint64_t a_desc0 = smem_desc_sw128(sA0, a_mn ? 16384u : 16u, 1024u);
+        const uint64_t b_desc0 = smem_desc_sw128(sB0, b_mn ? 16384u : 16u, 1024u);
+        const uint32_t a_step = a_mn ? 128u : 2u, b_step = b_mn ? 128u : 2u;
+        const uint32_t a_block = a_mn ? 512u : C::A_BYTES >> 5, b_block = b_mn ? 512u : C::B_BYTES >> 5;
+        const bool issuer = CG == 1 || leader;
         for (int t = cl; ok && rg_tile<CG, FORM>(p, walk, t, lane, rank, w); t += ncl) {
-            const int kblocks = (w.klen + 63) / 64;
-            if (kblocks == 0) continue;  // no rows: the epilogue writes zeros
-            const bool issuer = CG == 1 || leader;
-            if (issuer) {
-                if (!rg_warp_wait(tempty0 + 8u * abuf, aphase ^ 1u, lane, abort_flag, p)) {
+            const int ksteps = (w.klen + 127) / 128;
+            if (ksteps == 0) continue;  // no rows: the epilogue writes zeros
+            if (!issuer && FORM != RG_WGRAD) continue;
+            const bool tail = FORM == RG_WGRAD && (w.klen & 15) != 0;
+            const int whole = ksteps - (tail ? 1 : 0);  // stages the MMA reads as they are
+            const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(abuf * BT);
+            const uint32_t idesc = p.idesc | (static_cast<uint32_t>(w.n_mma >> 3) << 17);
+            auto issue = [&](int ks, int steps) {
+                const uint64_t ad = a_desc0 + static_cast<uint32_t>(stage) * (C::A_BYTES >> 4);
+                const uint64_t bd = b_desc0 + static_cast<uint32_t>(stage) * (C::B_BYTES >> 4);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k < steps)
+                        umma_f16_cg<CG>(d_tmem, ad + (k >> 2) * a_block + (k & 3) * a_step,
+                                        bd + (k >> 2) * b_block + (k & 3) * b_step, idesc,
+                                        (ks > 0 || k > 0) ? 1u : 0u);
+                if constexpr (CG > 1)
+                    umma_commit_mc_cg<CG>(empty0 + 8u * stage, kPair);
+                else
+                    umma_commit_cg<CG>(empty0 + 8u * stage);
+                if (ks == ksteps - 1) {
+                    if constexpr (CG > 1)
+                        umma_commit_mc_cg<CG>(tfull0 + 8u * abuf, kPair);
+                    else
+                        umma_commit_cg<CG>(tfull0 + 8u * abuf);
+                }
+            };
+            if (!issuer) {
+                stage += whole;  // (the peer only counts them)
+                while (stage >= C::STAGES) stage -= C::STAGES;
+            } else {
+                if (lane == 0) {
+                    ok = mbar_wait(tempty0 + 8u * abuf, aphase ^ 1u, abort_flag, p.status, p.timeout_ns);
+                    if (ok) tc_fence_after_sync();
+                    for (int ks = 0; ok && ks < whole; ++ks) {
+                        ok = mbar_wait(full0 + 8u * stage, phase, abort_flag, p.status, p.timeout_ns);
+                        if (!ok) break;
+                        tc_fence_after_sync();
+                        const int left = w.klen - ks * 128;
+                        issue(ks, left >= 128 ? 8 : (left + 15) / 16);
+                        issued = true;
+                        if (++stage == C::STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                }
+                __syncwarp();
+                if (FORM == RG_WGRAD) {
+                    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                    stage = __shfl_sync(0xffffffffu, stage, 0);
+                    phase = __shfl_sync(0xffffffffu, phase, 0);
+                    if (!ok) break;
+                }
+            }
+            if (FORM == RG_WGRAD && tail) {
+                if (!rg_warp_wait(tail0 + 8u * stage, tail_phase >> stage & 1u, lane, abort_flag, p)) {
                     ok = false;
                     break;
                 }
-                tc_fence_after_sync();
-            }
-            const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(abuf * BT);
-            const uint32_t idesc = p.idesc | (static_cast<uint32_t>(w.n_mma >> 3) << 17);
-            if (!issuer && FORM != RG_WGRAD) continue;
-            for (int kb = 0; kb < kblocks; ++kb) {
-                const bool tail = FORM == RG_WGRAD && kb == kblocks - 1 && (w.klen & 15) != 0;
-                if (issuer) {
-                    if (!rg_warp_wait(full0 + 8u * stage, phase, lane, abort_flag, p)) {
-                        ok = false;
-                        break;
-                    }
+                __syncwarp();
+                // rows klen % 128 .. up to the end of the last K = 16 step: one row is
+                // 128 bytes of every 64-wide atom column (whole rows, so the swizzle
+                // inside them does not matter)
+                const int v = w.klen - whole * 128;
+                const int nz = ((v + 15) & ~15) - v;
+                const int acols = 2 + w.n_mma / CG / 64;
+                for (int i = lane; i < acols * nz * 8; i += 32) {
+                    const int chunk = i & 7, r = v + (i >> 3) % nz, col = (i >> 3) / nz;
+                    const uint32_t base =
+                        col < 2 ? stage * C::A_BYTES + col * 16384u
+                                : C::STAGES * C::A_BYTES + stage * C::B_BYTES + (col - 2) * 16384u;
+                    *reinterpret_cast<uint4*>(smem + base + r * 128 + chunk * 16) =
+                        make_uint4(0, 0, 0, 0);
                 }
-                if (tail) {
-                    if (!rg_warp_wait(tail0 + 8u * stage, tail_phase >> stage & 1u, lane,
-                                      abort_flag, p)) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (!issuer) {
+                    if (lane == 0) mbar_arrive_remote(mapa_shared(peer_tail0 + 8u * stage, 0u));
+                } else {
+                    if (!rg_warp_wait(full0 + 8u * stage, phase, lane, abort_flag, p) ||
+                        (CG == 2 && !rg_warp_wait(peer_tail0 + 8u * stage, tail_phase >> stage & 1u,
+                                                  lane, abort_flag, p))) {
                         ok = false;
                         break;
-                    }
-                    __syncwarp();
-                    // rows klen % 64 .. up to the end of the last K = 16 step: one
-                    // row is 128 bytes of every 64-wide atom column (whole rows,
-                    // so the swizzle inside them does not matter)
-                    const int v = w.klen - kb * 64;
-                    const int nz = ((v + 15) & ~15) - v;
-                    const int acols = 2 + w.n_mma / CG / 64;
-                    for (int i = lane; i < acols * nz * 8; i += 32) {
-                        const int chunk = i & 7, r = v + (i >> 3) % nz, col = (i >> 3) / nz;
-                        const uint32_t base =
-                            col < 2 ? stage * C::A_BYTES + col * 8192u
-                                    : C::STAGES * C::A_BYTES + stage * C::B_BYTES + (col - 2) * 8192u;
-                        *reinterpret_cast<uint4*>(smem + base + r * 128 + chunk * 16) =
-                            make_uint4(0, 0, 0, 0);
                     }
                     fence_proxy_async_smem();
-                    __syncwarp();
-                    if (CG == 2 && !leader) {
-                        if (lane == 0) mbar_arrive_remote(mapa_shared(peer_tail0 + 8u * stage, 0u));
-                    } else if (CG == 2) {
-                        if (!rg_warp_wait(peer_tail0 + 8u * stage, tail_phase >> stage & 1u, lane,
-                                          abort_flag, p)) {
-                            ok = false;
-                            break;
-                        }
-                        fence_proxy_async_smem();
-                    }
-                    tail_phase ^= 1u << stage;
-                }
-                if (issuer) {
                     tc_fence_after_sync();
-                    if (lane == 0) {
-                        const uint32_t a_base = sA0 + stage * C::A_BYTES;
-                        const uint32_t b_base = sB0 + stage * C::B_BYTES;
-                        const int left = w.klen - kb * 64;
-                        const int steps = left >= 64 ? 4 : (left + 15) / 16;
-                        for (int k = 0; k < steps; ++k)
-                            umma_f16_cg<CG>(d_tmem,
-                                            smem_desc_sw128(a_base + k * a_step, a_lbo, 1024u),
-                                            smem_desc_sw128(b_base + k * b_step, b_lbo, 1024u),
-                                            idesc, (kb > 0 || k > 0) ? 1u : 0u);
-                        if constexpr (CG > 1)
-                            umma_commit_mc_cg<CG>(empty0 + 8u * stage, kPair);
-                        else
-                            umma_commit_cg<CG>(empty0 + 8u * stage);
-                        if (kb == kblocks - 1) {
-                            if constexpr (CG > 1)
-                                umma_commit_mc_cg<CG>(tfull0 + 8u * abuf, kPair);
-                            else
-                                umma_commit_cg<CG>(tfull0 + 8u * abuf);
-                        }
-                    }
+                    if (lane == 0) issue(whole, (v + 15) / 16);
                     issued = true;
                 }
+                tail_phase ^= 1u << stage;
                 if (++stage == C::STAGES) {
                     stage = 0;
                     phase ^= 1u;
@@ -544,6 +731,7 @@ __global__ void __launch_bounds__(RgCfg<CG, BT>::THREADS, 1)
                 abuf = 0;
                 aphase ^= 1u;
             }
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         }
         if (issued && lane == 0) {
             umma_commit_cg<CG>(drain_bar);
@@ -555,120 +743,30 @@ __global__ void __launch_bounds__(RgCfg<CG, BT>::THREADS, 1)
         const int q = warp & 3;           // tensor-memory lane quarter of this warp
         const int half = (warp - 2) >> 2; // which 32-column chunks it takes
         const uint32_t lane_field = static_cast<uint32_t>(q * 32) << 16;
-        float* stg = reinterpret_cast<float*>(epi_smem + (warp - 2) * C::EPI_WARP);
+        uint8_t* buf = epi_smem + (warp - 2) * C::EPI_WARP;
         int abuf = 0;
         uint32_t aphase = 0;
-        const bool late = p.beta != 0.0f && FORM != RG_SYM;  // beta * Cin read at the stores
         for (int t = cl; rg_tile<CG, FORM>(p, walk, t, lane, rank, w); t += ncl) {
             const bool empty = w.klen == 0;
-            const int nl0 = w.lane0 + q * 32;   // first output column of this warp
-            const int n = nl0 + lane;
-            const float bias = p.bias && n < p.n_lane ? p.bias[w.group * p.stride_bias + n] : 0.0f;
+            const int nl0 = w.lane0 + q * 32;  // first output column of this warp
             if (!empty) {
                 if (!rg_warp_wait(tfull0 + 8u * abuf, aphase, lane, abort_flag, p)) break;
                 tc_fence_after_sync();
             }
             const uint32_t tmem_row = tmem_base + lane_field + static_cast<uint32_t>(abuf * BT);
-            if (nl0 < p.n_lane) {
-#pragma unroll 1
-                for (int c0 = half * 32; c0 < w.ncols; c0 += 64) {
-                    uint32_t r[32];
-                    if (!empty) {
-                        tmem_ld_x32(tmem_row + static_cast<uint32_t>(c0), r);
-                        tmem_ld_wait(r);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) r[i] = 0u;
-                    }
-                    float v[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = fmaf(p.alpha, __uint_as_float(r[i]), bias);
-                    if constexpr (FORM == RG_SYM) {
-                        // Cin is symmetric: its row n, columns of this chunk
-                        if (p.beta != 0.0f && n < p.n_lane) {
-                            const char* src = static_cast<const char*>(p.Cin) +
-                                              (w.group * p.stride_cin + n * p.ldcin + w.col0 + c0) * 2;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                if (w.col0 + c0 + 8 * i >= p.n_lane) break;
-                                const uint4 u = *reinterpret_cast<const uint4*>(src + 16 * i);
-                                const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    const float2 f = rg_unpack(p.cin_dtype, uw[j]);
-                                    v[8 * i + 2 * j] = fmaf(p.beta, f.x, v[8 * i + 2 * j]);
-                                    v[8 * i + 2 * j + 1] = fmaf(p.beta, f.y, v[8 * i + 2 * j + 1]);
-                                }
-                            }
-                        }
-                        // the mirrored tile: this lane's row, 64 bytes (an
-                        // off-diagonal tile's columns all exist)
-                        if (!w.diag && n < p.n_lane) {
-                            const int64_t off = w.group * p.stride_c + n * p.ldc + w.col0 + c0;
-                            if (rg_span_ok(p, off, 32)) {
-                                char* dst = static_cast<char*>(p.C) + off * 2;
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    *reinterpret_cast<uint4*>(dst + 16 * i) = make_uint4(
-                                        rg_pack(p.c_dtype, v[8 * i], v[8 * i + 1]),
-                                        rg_pack(p.c_dtype, v[8 * i + 2], v[8 * i + 3]),
-                                        rg_pack(p.c_dtype, v[8 * i + 4], v[8 * i + 5]),
-                                        rg_pack(p.c_dtype, v[8 * i + 6], v[8 * i + 7]));
-                            }
-                        }
-                    }
-                    if (!late) act_inplace<32>(v, p.act);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        __syncwarp();
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) stg[i * RG_LD + lane] = v[16 * h + i];
-                        __syncwarp();
-                        const int cbase = c0 + 16 * h;
-                        if (p.c_dtype == DT_F32) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int c = 4 * i + (lane >> 3), n4 = (lane & 7) * 4;
-                                if (cbase + c < w.ncols && nl0 + n4 < p.n_lane) {
-                                    const float4 f = *reinterpret_cast<const float4*>(stg + c * RG_LD + n4);
-                                    float o[4] = {f.x, f.y, f.z, f.w};
-                                    const int64_t row = w.out_row + cbase + c;
-                                    const int64_t nn = nl0 + n4;
-                                    rg_store<4, FORM == RG_SYM>(p, w.group * p.stride_c + row * p.ldc + nn,
-                                                w.group * p.stride_cin + row * p.ldcin + nn,
-                                                nl0 + n4, o);
-                                }
-                            }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const int c = 8 * i + (lane >> 2), n8 = (lane & 3) * 8;
-                                if (cbase + c < w.ncols && nl0 + n8 < p.n_lane) {
-                                    const float4 f = *reinterpret_cast<const float4*>(stg + c * RG_LD + n8);
-                                    const float4 g =
-                                        *reinterpret_cast<const float4*>(stg + c * RG_LD + n8 + 4);
-                                    float o[8] = {f.x, f.y, f.z, f.w, g.x, g.y, g.z, g.w};
-                                    const int64_t row = w.out_row + cbase + c;
-                                    const int64_t nn = nl0 + n8;
-                                    rg_store<8, FORM == RG_SYM>(p, w.group * p.stride_c + row * p.ldc + nn,
-                                                w.group * p.stride_cin + row * p.ldcin + nn,
-                                                nl0 + n8, o);
-                                }
-                            }
-                        }
-                    }
-                }
-            }
-            if (empty) continue;
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) {
-                if (CG == 2 && !leader)
-                    mbar_arrive_remote(mapa_shared(tempty0 + 8u * abuf, 0u));
-                else
-                    mbar_arrive(tempty0 + 8u * abuf);
-            }
-            if (++abuf == 2) {
+            // the accumulator goes back to the MMA warp as soon as it is in registers
+            auto release = [&]() {
+                if (empty) return;
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_relaxed(mapa_shared(tempty0 + 8u * abuf, 0u));
+            };
+            if (p.c_dtype == DT_F32)
+                rg_out32(p, w, tmem_row, nl0, half, lane, empty, release);
+            else
+                rg_out16<FORM>(p, w, tmem_row, nl0, half, lane, buf, empty, release);
+            if (!empty && ++abuf == 2) {
                 abuf = 0;
                 aphase ^= 1u;
             }
