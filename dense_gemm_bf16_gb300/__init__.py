@@ -44,5 +44,7 @@ def __getattr__(name):
     if name in _EXPERTS or name == "experts":
         import importlib
         experts = importlib.import_module(".experts", __name__)
-        return experts if name == "experts" else getattr(experts, name)
+        for n in _EXPERTS:  # later uses find them without coming here
+            globals()[n] = getattr(experts, n)
+        return experts if name == "experts" else globals()[name]
     raise AttributeError(name)

@@ -626,9 +626,11 @@ gemm_status_t gemm_w4(gemm_dtype_t ab_dtype, int64_t groups, int64_t T, int64_t 
     const int64_t avg = cdiv(T, groups);
     const int64_t want = offsets ? (T < 2 * avg ? T : 2 * avg) : T;
     const int tokens = want <= 8 ? 8 : (want <= 16 ? 16 : (want <= 32 ? 32 : 64));
+    const int rt = w4_rows(tokens);
     W4Params p;
     std::memset(&p, 0, sizeof(p));
-    if (!encode_map8(&p.tmap_q, Q, K / 2, N, groups, K / 2, N * (K / 2), 128, 64) ||
+    if (!encode_map8(&p.tmap_q, Q, K / 2, N, groups, K / 2, N * (K / 2), 128,
+                     static_cast<uint32_t>(rt)) ||
         !encode_map16(&p.tmap_x, ab_dtype, a.ptr, K, T, 1, a.ld * 2, 0, 64,
                       static_cast<uint32_t>(tokens)))
         return GEMM_ERR_CUDA;
@@ -641,17 +643,21 @@ gemm_status_t gemm_w4(gemm_dtype_t ab_dtype, int64_t groups, int64_t T, int64_t 
     p.N = static_cast<int32_t>(N);
     p.K = static_cast<int32_t>(K);
     p.group = group;
-    p.slots = static_cast<int32_t>(groups < T ? groups : T);
-    const int64_t n_tiles = cdiv(N, 64), chunks = cdiv(K, 256);
-    // K slices (one CTA each, a cluster per tile): enough CTAs for three on
-    // every SM, each with at least two 256-wide steps
+    const int64_t n_tiles = cdiv(N, rt), steps = cdiv(K, 256);
+    // units there may be: full token tiles and one more for each non-empty group
+    const int64_t units = n_tiles * (T / tokens + (groups < T ? groups : T));
+    if (units > kLim) return GEMM_ERR_UNSUPPORTED;
+    // K slices (a cluster per unit) where the units would leave SMs idle, each of
+    // at least two 256-wide steps
     int splits = 1;
-    while (splits < 8 && n_tiles * p.slots * splits * 2 <= 4 * d.sm_count &&
-           chunks >= splits * 4)
-        splits *= 2;
+    if (!offsets)
+        while (splits < 8 && n_tiles * cdiv(T, tokens) * splits * 2 <= d.sm_count &&
+               steps >= splits * 4)
+            splits *= 2;
     p.n_tiles = static_cast<int32_t>(n_tiles);
     p.splits = splits;
-    if (n_tiles * p.slots * splits > kLim) return GEMM_ERR_UNSUPPORTED;
+    p.grid = static_cast<int32_t>(splits > 1 ? n_tiles * cdiv(T, tokens)
+                                             : (units < d.sm_count ? units : d.sm_count));
     p.C = C;
     p.ldc = ldc;
     p.c_dtype = c_dtype;

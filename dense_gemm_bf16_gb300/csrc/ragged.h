@@ -117,15 +117,15 @@ gemm_status_t rg_run(const RgProblem& q, const DeviceInfo& d, cudaStream_t strea
 
 // ---- 4-bit weights (w4.cu)
 struct W4Params {
-    CUtensorMap tmap_q;      // [groups][N][K / 2] bytes, boxes of 128 bytes x 64 rows
+    CUtensorMap tmap_q;      // [groups][N][K / 2] bytes, boxes of 128 bytes x w4_rows() rows
     CUtensorMap tmap_x;      // [T][K], boxes of 64 x the tokens of a tile
     const uint8_t* q;
     const void* scales;
     const uint8_t* zeros;
     const int32_t* offsets;  // or null
     int32_t groups, T, N, K, group;
-    int32_t slots;           // groups a launch provides for (with offsets: the non-empty ones)
-    int32_t n_tiles, splits;
+    int32_t n_tiles, splits; // row tiles; CTAs (K slices) of a cluster
+    int32_t grid;            // clusters
     void* C;
     int64_t ldc;
     int32_t c_dtype;
@@ -138,6 +138,7 @@ struct W4Params {
     int64_t dbg_c_elems;
 #endif
 };
+int w4_rows(int tokens);  // weight rows of a unit of `tokens` token columns
 cudaError_t w4_launch(int dt, int tokens, const W4Params& p, cudaStream_t stream);
 cudaError_t w4_prepare();
 // Dense [groups][N][K] weights of type dt: (q - z) * s, rounded once.

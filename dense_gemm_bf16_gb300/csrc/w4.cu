@@ -3,28 +3,27 @@
 //
 //   y[t, n] = sum_G s[n, G] * sum_{k in G} x[t, k] (q[n, k] - z[n, G])
 //
-// With few tokens the call is bound by the N K / 2 bytes of weights.  So a CTA
-// streams 64 rows of them through a ring of TMA boxes (128 bytes = 256 weights
-// of 64 rows, 8 KB a stage, filled by one producer warp), and four consumer
-// warps keep 16 rows each.  The arithmetic stays ahead of the loads by going
-// through mma.sync m16n8k16 with the weights on its M side: a 4-bit integer is
-// an exact bf16 (fp16) number, made from two bits operations and one packed
-// subtraction for every two weights, and the tokens are the 8 columns.  The
-// products x (q - z) are summed in fp32 and scaled by s once per group, so the
-// direct form rounds nothing but its output.
+// With few tokens the call is bound by the N K / 2 bytes of weights.  One CTA per
+// SM streams 64 (128 for more than 16 tokens) rows of them through a ring of TMA
+// boxes (128 bytes = 256 weights of a row, with the same 256 columns of the
+// tokens), filled by one producer warp that runs ahead over the CTA's units.
+// Sixteen (eight) consumer warps split a stage: 16 rows by 64 to 256 weights each.  The
+// arithmetic stays near the loads by going through mma.sync m16n8k16 with the
+// weights on its M side: a 4-bit integer is an exact bf16 (fp16) number, made by
+// a byte permute, one masking and one packed subtraction for every two weights,
+// and the tokens are the 8 columns.  The products x (q - z) are summed in fp32
+// and scaled by s once per group, so nothing is rounded but the output.  What
+// bounds it is issue slots: about 34 instructions for 16 rows x 32 weights.
 //
 // The sum over k may be taken in any order, so lane t of a quad takes the 8
-// weights of 32-bit word t of a 16-byte chunk (32 weights) in the order that
-// masking leaves them, (0,4) (1,5) (2,6) (3,7), and the same 8 tokens' values,
-// paired by byte permutes.  The boxes are 128-byte swizzled, which makes the
-// word reads of 8 rows x 4 words conflict-free.
+// weights of 32-bit word t of a 16-byte chunk (32 weights) and 8 values of its
+// token.  The boxes are 128-byte swizzled, which makes the word reads of 8 rows
+// x 4 words conflict-free.
 //
-// K is cut over the CTAs of a cluster (at most 8); their fp32 sums meet in
-// distributed shared memory and are added in rank order, so results repeat.
-// Scales (and zero points) of up to 4096 weights' columns are staged in shared
-// memory at a time.
-//
-// All waits are bounded, as in the other kernels.
+// Units (group, 64 rows, tokens of a tile) are dealt round robin; where they are
+// fewer than half of the SMs, K is cut over the CTAs of a cluster (at most 8),
+// whose fp32 sums meet in distributed shared memory and are added in rank order,
+// so results repeat.  All waits are bounded, as in the other kernels.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -35,26 +34,26 @@
 namespace dg {
 namespace {
 
-constexpr int W4_ROWS = 64;      // weight rows (outputs) of a CTA
 constexpr int W4_STEP = 256;     // weights of a row per stage
-constexpr int W4_PANEL = 4096;   // weights of a row whose scales are staged at once
-constexpr int W4_THREADS = 160;  // warp 0 producer, warps 1-4 consumers
 
-template <int MT, int GROUP>
+template <int MT>
 struct W4Cfg {
-    static constexpr uint32_t Q_BYTES = W4_ROWS * 128;
-    static constexpr uint32_t X_BOX = MT * 128;  // 64 values of MT tokens
+    // (64 tokens' sums take the registers of half as many warps)
+    static constexpr int WARPS = MT == 64 ? 8 : 16;  // consumer warps
+    static constexpr int THREADS = 32 * (WARPS + 1); // and the producer, warp 0
+    static constexpr int RT = MT <= 16 ? 64 : 128;   // weight rows (outputs) of a unit
+    static constexpr int RG = RT / 16;               // row groups of a stage
+    static constexpr int KQ = WARPS / RG;            // K parts of a stage
+    static constexpr int CPW = 8 / KQ;              // 16-byte chunks of a warp's rows
+    static constexpr uint32_t Q_BYTES = RT * 128;
+    static constexpr uint32_t X_BOX = MT * 128;     // 64 values of MT tokens
     static constexpr uint32_t STAGE = Q_BYTES + 4 * X_BOX;
-    static constexpr int STAGES = MT == 8 ? 5 : 4;
-    static constexpr int GROUPS = W4_PANEL / GROUP;
-    static constexpr int S_LD = GROUPS + 2;  // (one word more than a multiple of 32 banks)
-    static constexpr int Z_LD = GROUPS + 4;
-    static constexpr uint32_t S_BYTES = W4_ROWS * S_LD * 2;
-    static constexpr uint32_t Z_BYTES = W4_ROWS * Z_LD;
-    static constexpr int R_LD = W4_ROWS + 4;
-    static constexpr uint32_t R_BYTES = MT * R_LD * 4;
-    static constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE + S_BYTES + Z_BYTES + R_BYTES + 256;
-    static_assert(S_BYTES % 16 == 0 && Z_BYTES % 16 == 0 && R_BYTES % 16 == 0, "alignment");
+    static constexpr int R_LD = RT + 4;
+    static constexpr uint32_t R_BYTES = KQ * MT * R_LD * 4;
+    static constexpr int FIT = (232448 - 1024 - 512 - R_BYTES) / STAGE;
+    static constexpr int STAGES = FIT > 16 ? 16 : FIT;
+    static constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE + R_BYTES + 512;
+    static_assert(STAGES >= 3 && (2 * STAGES + 1) * 8 <= 512, "ring");
 };
 
 template <int DT>
@@ -74,14 +73,13 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The pair of 4-bit values at bits 0-3 and 16-19 of w as 16-bit floats minus
-// the pair `sub`: or-ing q into the mantissa of 128 (bf16) or 1024 (fp16), where
-// one unit is the last bit, gives 128 + q (1024 + q) exactly, and sub holds
-// 128 + z (1024 + z).
-template <int DT>
-__device__ __forceinline__ uint32_t w4_pair(uint32_t w, uint32_t sub) {
+// Weights 2 j and 2 j + 1 of word w (w4 = w >> 4) as 16-bit floats minus the pair
+// `sub`: or-ing q into the mantissa of 128 (bf16) or 1024 (fp16), where one unit is
+// the last bit, gives 128 + q (1024 + q) exactly, and sub holds 128 + z (1024 + z).
+template <int DT, int J>
+__device__ __forceinline__ uint32_t w4_pair(uint32_t w, uint32_t w4, uint32_t sub) {
     constexpr uint32_t magic = DT == DT_BF16 ? 0x43004300u : 0x64006400u;
-    const uint32_t v = (w & 0x000F000Fu) | magic;
+    const uint32_t v = (__byte_perm(w, w4, 0x4400 + 0x1111 * J) & 0x000F000Fu) | magic;
     if constexpr (DT == DT_BF16) {
         const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v),
                                          *reinterpret_cast<const __nv_bfloat162*>(&sub));
@@ -110,97 +108,143 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
     return v;
 }
 
-// The slot-th non-empty group (whole warp), or -1; with its rows.
-__device__ __forceinline__ int w4_group(const W4Params& p, int slot, int lane, int& row0, int& rows) {
-    if (!p.offsets) {
-        row0 = 0;
-        rows = p.T;
-        return 0;
-    }
-    int seen = 0;
-    for (int base = 0; base < p.groups; base += 32) {
-        const int g = base + lane;
-        int lo = 0, hi = 0;
-        if (g < p.groups) {
+// The units in order: group by group, its row tiles, the token tiles of one row
+// tile after another.  One group per lane, a window of 32 groups at a time.
+struct W4Walk {
+    int base, before, incl, row0, rows;
+    bool last;  // no group follows the window
+};
+
+template <int MT>
+__device__ __forceinline__ void w4_window(const W4Params& p, W4Walk& w, int lane) {
+    const int g = w.base + lane;
+    int lo = 0, hi = 0;
+    if (g < p.groups) {
+        if (p.offsets) {
             lo = __ldg(p.offsets + g);
             hi = __ldg(p.offsets + g + 1);
-            if (lo < 0 || hi < lo || hi > p.T) {
-                if (p.status) atomicOr(p.status, STATUS_BAD_OFFSETS);
-                lo = lo < 0 ? 0 : (lo > p.T ? p.T : lo);
-                hi = hi < lo ? lo : (hi > p.T ? p.T : hi);
-            }
+        } else {
+            hi = p.T;
         }
-        const uint32_t m = __ballot_sync(0xffffffffu, hi > lo);
-        const int n = __popc(m);
-        if (slot < seen + n) {
-            const int l = __fns(m, 0, slot - seen + 1);
-            row0 = __shfl_sync(0xffffffffu, lo, l);
-            rows = __shfl_sync(0xffffffffu, hi - lo, l);
-            return base + l;
-        }
-        seen += n;
     }
-    return -1;
+    // offsets that do not ascend inside [0, T]: reported, and the groups from
+    // there on have no rows
+    const uint32_t bad = __ballot_sync(0xffffffffu, lo < 0 || hi < lo || hi > p.T);
+    w.last = bad != 0 || w.base + 32 >= p.groups;
+    if (bad) {
+        if (lane == 0 && p.status) atomicOr(p.status, STATUS_BAD_OFFSETS);
+        if (lane >= __ffs(bad) - 1) lo = hi = 0;
+    }
+    w.row0 = lo;
+    w.rows = hi - lo;
+    int units = (w.rows + MT - 1) / MT * p.n_tiles;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, units, d);
+        if (lane >= d) units += o;
+    }
+    w.incl = units;
 }
 
+struct W4Unit {
+    int group, n0, row0, tokens;  // first output row; first token row, tokens
+};
+
+template <int MT>
+__device__ __forceinline__ bool w4_unit(const W4Params& p, W4Walk& w, int u, int lane, W4Unit& o) {
+    int total = __shfl_sync(0xffffffffu, w.incl, 31);
+    while (u - w.before >= total) {
+        if (w.last) return false;
+        w.before += total;
+        w.base += 32;
+        w4_window<MT>(p, w, lane);
+        total = __shfl_sync(0xffffffffu, w.incl, 31);
+    }
+    const uint32_t m = __ballot_sync(0xffffffffu, w.incl > u - w.before);
+    const int l = __ffs(m) - 1;
+    const int rows = __shfl_sync(0xffffffffu, w.rows, l);
+    const int row0 = __shfl_sync(0xffffffffu, w.row0, l);
+    const int incl = __shfl_sync(0xffffffffu, w.incl, l);
+    const int chunks = (rows + MT - 1) / MT;
+    const int r = u - w.before - (incl - chunks * p.n_tiles);
+    const int tile = r / chunks;
+    const int t0 = (r - tile * chunks) * MT;
+    o.group = w.base + l;
+    o.n0 = tile * W4Cfg<MT>::RT;
+    o.row0 = row0 + t0;
+    o.tokens = rows - t0 < MT ? rows - t0 : MT;
+    return true;
+}
+
+// Scales and zero points of a warp's two rows r, r + 8 for one stage, as loaded.
+template <int NG>
+struct W4Scales {
+    uint16_t s[2][NG];
+    uint8_t z[2][NG];
+};
+
 template <int DT, int MT, int GROUP>
-__global__ void __launch_bounds__(W4_THREADS) w4_kernel(const __grid_constant__ W4Params p) {
-    using C = W4Cfg<MT, GROUP>;
+__global__ void __launch_bounds__(W4Cfg<MT>::THREADS, 1) w4_kernel(const __grid_constant__ W4Params p) {
+    using C = W4Cfg<MT>;
     constexpr int NT = MT / 8;
-    constexpr int CPG = GROUP / 32;  // 16-byte chunks per group
+    constexpr int CPG = GROUP / 32;                       // chunks per group
+    constexpr int CG = CPG < C::CPW ? CPG : C::CPW;       // chunks a warp scales at once
+    constexpr int NG = C::CPW / CG;                       // scales per row and stage
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint16_t* s_sm = reinterpret_cast<uint16_t*>(smem + C::STAGES * C::STAGE);
-    uint8_t* z_sm = reinterpret_cast<uint8_t*>(s_sm) + C::S_BYTES;
-    float* red = reinterpret_cast<float*>(z_sm + C::Z_BYTES);
+    float* red = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE);
     uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(red) + C::R_BYTES);
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8u * C::STAGES;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 2 * C::STAGES);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = p.splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int u0 = static_cast<int>(blockIdx.x) / p.splits;
+    const int nu = static_cast<int>(gridDim.x) / p.splits;
 
-    const int unit = static_cast<int>(blockIdx.x) / p.splits;
-    const int rank = static_cast<int>(blockIdx.x) - unit * p.splits;
-    const int slot = unit / p.n_tiles;
-    const int n0 = (unit - slot * p.n_tiles) * W4_ROWS;
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(full0 + 8u * s, 1);
-            mbar_init(empty0 + 8u * s, 4);
+            mbar_init(empty0 + 8u * s, C::WARPS);
         }
         *abort_flag = 0;
         fence_mbar_init();
+    }
+    if (threadIdx.x == 32) {
         prefetch_tmap(&p.tmap_q);
         prefetch_tmap(&p.tmap_x);
     }
-    int row0 = 0, rows = 0;
-    const int g = w4_group(p, slot, lane, row0, rows);
+    W4Walk walk{0, 0, 0, 0, 0, false};
+    w4_window<MT>(p, walk, lane);
     __syncthreads();
-    if (g < 0) return;  // (every CTA of the cluster alike)
 
     const int steps = (p.K + W4_STEP - 1) / W4_STEP;
     const int st0 = static_cast<int>(static_cast<int64_t>(steps) * rank / p.splits);
     const int st1 = static_cast<int>(static_cast<int64_t>(steps) * (rank + 1) / p.splits);
     int stage = 0;
-    uint32_t phase = 0;
-    uint32_t armed = 0;
+    uint32_t phase = 0, armed = 0;
+    W4Unit w;
 
-    for (int t0 = 0; t0 < rows; t0 += MT) {
-        if (warp == 0) {
+    if (warp == 0) {
+        // ------------------------------------------------ producer
+        bool ok = true;
+        for (int u = u0; ok && w4_unit<MT>(p, walk, u, lane, w); u += nu) {
             if (lane == 0) {
-                const uint64_t pol_q = rows <= MT ? l2_policy_evict_first() : l2_policy_evict_normal();
+                const uint64_t pol_q = l2_policy_evict_first();
                 const uint64_t pol_x = l2_policy_evict_last();
                 for (int st = st0; st < st1; ++st) {
-                    if (!mbar_wait(empty0 + 8u * stage, phase ^ 1u, abort_flag, p.status, p.timeout_ns))
+                    if (!mbar_wait(empty0 + 8u * stage, phase ^ 1u, abort_flag, p.status, p.timeout_ns)) {
+                        ok = false;
                         break;
+                    }
                     const uint32_t fb = full0 + 8u * stage;
                     mbar_arrive_expect_tx(fb, C::STAGE);
                     const uint32_t dst = smem_u32(smem) + stage * C::STAGE;
-                    tma_load_3d(dst, &p.tmap_q, fb, st * 128, n0, g, pol_q);
+                    tma_load_3d(dst, &p.tmap_q, fb, st * 128, w.n0, w.group, pol_q);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         tma_load_3d(dst + C::Q_BYTES + i * C::X_BOX, &p.tmap_x, fb,
-                                    st * W4_STEP + 64 * i, row0 + t0, 0, pol_x);
+                                    st * W4_STEP + 64 * i, w.row0, 0, pol_x);
                     ++armed;
                     if (++stage == C::STAGES) {
                         stage = 0;
@@ -208,86 +252,112 @@ __global__ void __launch_bounds__(W4_THREADS) w4_kernel(const __grid_constant__ 
                     }
                 }
             }
-            __syncwarp();
-        } else {
-            const int cw = warp - 1, gr = lane >> 2, t = lane & 3;
-            const int r = cw * 16 + gr;  // rows r and r + 8 of the CTA's 64
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            if (p.splits > 1) {
+                // the consumers' two cluster barriers of the unit
+                cluster_sync();
+                cluster_sync();
+                if (!ok) break;
+            }
+        }
+        // every issued copy lands before the CTA exits
+        if (lane == 0)
+            for (int s = 0; s < C::STAGES && static_cast<uint32_t>(s) < armed; ++s) {
+                const uint32_t fills = (armed - 1u - s) / C::STAGES + 1u;
+                const uint64_t begin = globaltimer_ns();
+                while (!mbar_try_wait(full0 + 8u * s, (fills - 1u) & 1u))
+                    if (globaltimer_ns() - begin > p.timeout_ns) break;
+            }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------ consumers
+        const int cw = warp - 1, gr = lane >> 2, t = lane & 3;
+        const int rg = cw % C::RG, kq = cw / C::RG;
+        const int r = rg * 16 + gr;  // rows r and r + 8 of the unit
+        const int kg = p.K / GROUP;
+        const int chunk0 = kq * C::CPW;
+        // word t of chunk c of row r of a stage: the chunk is swizzled by the row
+        const uint32_t q_at = static_cast<uint32_t>(r * 128 + t * 4);
+        bool ok = true;
+        for (int u = u0; w4_unit<MT>(p, walk, u, lane, w); u += nu) {
             float total[NT][4];
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) total[j][i] = 0.0f;
-            const int kg = p.K / GROUP;
-            int panel = -1;
-            bool ok = true;
-            for (int st = st0; ok && st < st1; ++st) {
-                const int in_panel = st - st0;
-                if (in_panel / (W4_PANEL / W4_STEP) != panel) {
-                    // stage the scales of the next panel (each warp its own 16 rows)
-                    panel = in_panel / (W4_PANEL / W4_STEP);
-                    const int gp0 = (st0 + panel * (W4_PANEL / W4_STEP)) * (W4_STEP / GROUP);
-                    int n_g = (st1 - st) * (W4_STEP / GROUP);
-                    if (n_g > C::GROUPS) n_g = C::GROUPS;
-                    const int64_t base = (static_cast<int64_t>(g) * p.N + n0) * kg;
-                    __syncwarp();
-                    const uint16_t* src = static_cast<const uint16_t*>(p.scales);
-#pragma unroll 4
-                    for (int i = lane; i < 16 * n_g; i += 32) {
-                        const int rr = cw * 16 + i / n_g, gg = i % n_g;
-                        const bool in = n0 + rr < p.N && gp0 + gg < kg;
-                        const int64_t at = base + static_cast<int64_t>(rr) * kg + gp0 + gg;
-                        s_sm[rr * C::S_LD + gg] = in ? __ldg(src + at) : static_cast<uint16_t>(0);
-                        if (p.zeros) z_sm[rr * C::Z_LD + gg] = in ? __ldg(p.zeros + at) : static_cast<uint8_t>(8);
+            // (rows past N and groups past K read the last ones: their sums are
+            // not stored, or multiply zeros)
+            const int n_lo = w.n0 + r < p.N ? w.n0 + r : p.N - 1;
+            const int n_hi = w.n0 + r + 8 < p.N ? w.n0 + r + 8 : p.N - 1;
+            const int64_t at_lo = (static_cast<int64_t>(w.group) * p.N + n_lo) * kg;
+            const int64_t at_hi = (static_cast<int64_t>(w.group) * p.N + n_hi) * kg;
+            const uint16_t* scales = static_cast<const uint16_t*>(p.scales);
+            auto fetch = [&](int st, W4Scales<NG>& v) {
+#pragma unroll
+                for (int i = 0; i < NG; ++i) {
+                    int gi = (st * W4_STEP + (chunk0 + i * CG) * 32) / GROUP;
+                    gi = gi < kg ? gi : kg - 1;
+                    v.s[0][i] = __ldg(scales + at_lo + gi);
+                    v.s[1][i] = __ldg(scales + at_hi + gi);
+                    if (p.zeros) {
+                        v.z[0][i] = __ldg(p.zeros + at_lo + gi);
+                        v.z[1][i] = __ldg(p.zeros + at_hi + gi);
                     }
-                    __syncwarp();
                 }
-                int got = 1;
-                if (lane == 0)
-                    got = mbar_wait(full0 + 8u * stage, phase, abort_flag, p.status, p.timeout_ns) ? 1 : 0;
-                ok = __shfl_sync(0xffffffffu, got, 0) != 0;
+            };
+            W4Scales<NG> cur, nxt;
+            if (st0 < st1) fetch(st0, nxt);
+            for (int st = st0; ok && st < st1; ++st) {
+                cur = nxt;
+                if (st + 1 < st1) fetch(st + 1, nxt);
+                ok = mbar_wait(full0 + 8u * stage, phase, abort_flag, p.status, p.timeout_ns);
+                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                // (every lane's reads below follow the barrier's completion)
-                mbar_try_wait(full0 + 8u * stage, phase);
                 const uint8_t* qs = smem + stage * C::STAGE;
                 const uint8_t* xs = qs + C::Q_BYTES;
-                const int gl0 = (in_panel % (W4_PANEL / W4_STEP)) * (W4_STEP / GROUP);
 #pragma unroll
-                for (int gg = 0; gg < W4_STEP / GROUP; ++gg) {
-                    float acc[NT][4];
+                for (int gg = 0; gg < NG; ++gg) {
+                    // two chains of sums where one tile of tokens gives no other
+                    float acc[NT][4], acc2[4];
 #pragma unroll
                     for (int j = 0; j < NT; ++j)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
-                    const int gl = gl0 + gg;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc2[i] = 0.0f;
                     uint32_t sub_lo = w4_sub<DT>(8), sub_hi = sub_lo;
                     if (p.zeros) {
-                        sub_lo = w4_sub<DT>(z_sm[r * C::Z_LD + gl] & 15);
-                        sub_hi = w4_sub<DT>(z_sm[(r + 8) * C::Z_LD + gl] & 15);
+                        sub_lo = w4_sub<DT>(cur.z[0][gg] & 15);
+                        sub_hi = w4_sub<DT>(cur.z[1][gg] & 15);
                     }
-                    const float s_lo = w4_float<DT>(s_sm[r * C::S_LD + gl]);
-                    const float s_hi = w4_float<DT>(s_sm[(r + 8) * C::S_LD + gl]);
 #pragma unroll
-                    for (int cc = 0; cc < CPG; ++cc) {
-                        const int c = gg * CPG + cc;
-                        const uint32_t at = static_cast<uint32_t>((c ^ gr) << 4) + t * 4;
-                        const uint32_t lo = *reinterpret_cast<const uint32_t*>(qs + r * 128 + at);
-                        const uint32_t hi = *reinterpret_cast<const uint32_t*>(qs + (r + 8) * 128 + at);
-                        const uint32_t a1[4] = {w4_pair<DT>(lo, sub_lo), w4_pair<DT>(hi, sub_hi),
-                                                w4_pair<DT>(lo >> 4, sub_lo),
-                                                w4_pair<DT>(hi >> 4, sub_hi)};
-                        const uint32_t a2[4] = {
-                            w4_pair<DT>(lo >> 8, sub_lo), w4_pair<DT>(hi >> 8, sub_hi),
-                            w4_pair<DT>(lo >> 12, sub_lo), w4_pair<DT>(hi >> 12, sub_hi)};
+                    for (int cc = 0; cc < CG; ++cc) {
+                        const int c = chunk0 + gg * CG + cc;
+                        const uint8_t* src = qs + (q_at + static_cast<uint32_t>((c ^ gr) << 4));
+                        const uint32_t lo = *reinterpret_cast<const uint32_t*>(src);
+                        const uint32_t hi = *reinterpret_cast<const uint32_t*>(src + 1024);
+                        const uint32_t lo4 = lo >> 4, hi4 = hi >> 4;
+                        const uint32_t a1[4] = {w4_pair<DT, 0>(lo, lo4, sub_lo),
+                                                w4_pair<DT, 0>(hi, hi4, sub_hi),
+                                                w4_pair<DT, 1>(lo, lo4, sub_lo),
+                                                w4_pair<DT, 1>(hi, hi4, sub_hi)};
+                        const uint32_t a2[4] = {w4_pair<DT, 2>(lo, lo4, sub_lo),
+                                                w4_pair<DT, 2>(hi, hi4, sub_hi),
+                                                w4_pair<DT, 3>(lo, lo4, sub_lo),
+                                                w4_pair<DT, 3>(hi, hi4, sub_hi)};
+                        const uint8_t* xsrc = xs + (c >> 1) * C::X_BOX + gr * 128 +
+                                              ((((c & 1) * 4 + t) ^ gr) << 4);
 #pragma unroll
                         for (int j = 0; j < NT; ++j) {
-                            const uint4 x = *reinterpret_cast<const uint4*>(
-                                xs + (c >> 1) * C::X_BOX + (8 * j + gr) * 128 +
-                                ((((c & 1) * 4 + t) ^ gr) << 4));
-                            mma16816<DT>(acc[j], a1, __byte_perm(x.x, x.z, 0x5410),
-                                         __byte_perm(x.x, x.z, 0x7632));
-                            mma16816<DT>(acc[j], a2, __byte_perm(x.y, x.w, 0x5410),
-                                         __byte_perm(x.y, x.w, 0x7632));
+                            const uint4 x = *reinterpret_cast<const uint4*>(xsrc + 1024 * j);
+                            mma16816<DT>(acc[j], a1, x.x, x.y);
+                            mma16816<DT>(NT == 1 ? acc2 : acc[j], a2, x.z, x.w);
                         }
+                    }
+                    const float s_lo = w4_float<DT>(cur.s[0][gg]), s_hi = w4_float<DT>(cur.s[1][gg]);
+                    if (NT == 1) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[0][i] += acc2[i];
                     }
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
@@ -304,66 +374,65 @@ __global__ void __launch_bounds__(W4_THREADS) w4_kernel(const __grid_constant__ 
                     phase ^= 1u;
                 }
             }
-            // [token][row] sums of this CTA
+            // [K part][token][row] sums of this CTA
+            float* part = red + kq * MT * C::R_LD;
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                red[(8 * j + 2 * t) * C::R_LD + r] = total[j][0];
-                red[(8 * j + 2 * t + 1) * C::R_LD + r] = total[j][1];
-                red[(8 * j + 2 * t) * C::R_LD + r + 8] = total[j][2];
-                red[(8 * j + 2 * t + 1) * C::R_LD + r + 8] = total[j][3];
+                part[(8 * j + 2 * t) * C::R_LD + r] = total[j][0];
+                part[(8 * j + 2 * t + 1) * C::R_LD + r] = total[j][1];
+                part[(8 * j + 2 * t) * C::R_LD + r + 8] = total[j][2];
+                part[(8 * j + 2 * t + 1) * C::R_LD + r + 8] = total[j][3];
             }
-        }
-        if (p.splits > 1)
-            cluster_sync();
-        else
-            __syncthreads();
-        // each CTA of the cluster adds and writes its share of the 64 rows
-        const int share = W4_ROWS / p.splits;
-        const int nt = rows - t0 < MT ? rows - t0 : MT;
-        if (!*abort_flag) {
-            for (int i = threadIdx.x; i < nt * share; i += W4_THREADS) {
-                const int tok = i / share, rr = rank * share + i % share;
-                const int n = n0 + rr;
-                if (n >= p.N) continue;
-                float v = 0.0f;
-                if (p.splits > 1) {
-                    const uint32_t at = smem_u32(red + tok * C::R_LD + rr);
-                    for (int k = 0; k < p.splits; ++k)
-                        v += ld_cluster_f32(mapa_shared(at, static_cast<uint32_t>(k)));
-                } else {
-                    v = red[tok * C::R_LD + rr];
-                }
-                if (p.bias) v += p.bias[g * p.stride_bias + n];
-                v = apply_act(v, p.act);
-                const int64_t off = static_cast<int64_t>(row0 + t0 + tok) * p.ldc + n;
+            auto sync = [&]() {
+                if (p.splits > 1)
+                    cluster_sync();
+                else
+                    asm volatile("bar.sync 1, %0;" ::"n"(32 * C::WARPS) : "memory");
+            };
+            sync();
+            // each CTA of the cluster adds and writes its share of the rows
+            const int share = C::RT / p.splits;
+            if (!*abort_flag) {
+                for (int i = threadIdx.x - 32; i < w.tokens * share; i += 32 * C::WARPS) {
+                    const int tok = i / share, rr = rank * share + i % share;
+                    const int n = w.n0 + rr;
+                    if (n >= p.N) continue;
+                    const float* src = red + tok * C::R_LD + rr;
+                    float v = 0.0f;
+                    if (p.splits > 1) {
+                        for (int k = 0; k < p.splits; ++k) {
+                            const uint32_t at = mapa_shared(smem_u32(src), static_cast<uint32_t>(k));
+#pragma unroll
+                            for (int m = 0; m < C::KQ; ++m)
+                                v += ld_cluster_f32(at + 4u * m * MT * C::R_LD);
+                        }
+                    } else {
+#pragma unroll
+                        for (int m = 0; m < C::KQ; ++m) v += src[m * MT * C::R_LD];
+                    }
+                    if (p.bias) v += __ldg(p.bias + w.group * p.stride_bias + n);
+                    v = apply_act(v, p.act);
+                    const int64_t off = static_cast<int64_t>(w.row0 + tok) * p.ldc + n;
 #if DG_DEBUG
-                if (!DG_CHECK(off >= 0 && off < p.dbg_c_elems, p.status, STATUS_CHECK_BOUNDS)) continue;
+                    if (!DG_CHECK(off >= 0 && off < p.dbg_c_elems, p.status, STATUS_CHECK_BOUNDS))
+                        continue;
 #endif
-                store_elem(static_cast<char*>(p.C) + off * dt_size(p.c_dtype), p.c_dtype, v);
+                    store_elem(static_cast<char*>(p.C) + off * dt_size(p.c_dtype), p.c_dtype, v);
+                }
             }
+            // the sums are read before the next unit's (or the exit) replace them;
+            // after a failed wait (ok stays false) the units' barriers still run
+            sync();
         }
-        // the sums are read before the next tokens' (or the exit) replace them
-        if (p.splits > 1)
-            cluster_sync();
-        else
-            __syncthreads();
     }
-    // every issued copy lands before the CTA exits
-    if (warp == 0 && lane == 0)
-        for (int s = 0; s < C::STAGES && static_cast<uint32_t>(s) < armed; ++s) {
-            const uint32_t fills = (armed - 1u - s) / C::STAGES + 1u;
-            const uint64_t begin = globaltimer_ns();
-            while (!mbar_try_wait(full0 + 8u * s, (fills - 1u) & 1u))
-                if (globaltimer_ns() - begin > p.timeout_ns) break;
-        }
 }
 
 template <int DT, int MT, int GROUP>
 cudaError_t launch_one(const W4Params& p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.n_tiles) * p.slots * p.splits);
-    cfg.blockDim = dim3(W4_THREADS);
-    cfg.dynamicSmemBytes = W4Cfg<MT, GROUP>::SMEM;
+    cfg.gridDim = dim3(static_cast<unsigned>(p.grid) * p.splits);
+    cfg.blockDim = dim3(W4Cfg<MT>::THREADS);
+    cfg.dynamicSmemBytes = W4Cfg<MT>::SMEM;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -394,7 +463,7 @@ template <int DT, int MT, int GROUP>
 cudaError_t prepare_one() {
     return cudaFuncSetAttribute(w4_kernel<DT, MT, GROUP>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(W4Cfg<MT, GROUP>::SMEM));
+                                static_cast<int>(W4Cfg<MT>::SMEM));
 }
 
 template <int DT, int MT>
@@ -445,6 +514,8 @@ __global__ void __launch_bounds__(256) w4_dequantise_kernel(const uint32_t* q, c
 }
 
 }  // namespace
+
+int w4_rows(int tokens) { return tokens <= 16 ? W4Cfg<8>::RT : W4Cfg<64>::RT; }
 
 cudaError_t w4_launch(int dt, int tokens, const W4Params& p, cudaStream_t stream) {
     return dt == DT_BF16 ? launch_tokens<DT_BF16>(tokens, p, stream)

@@ -1,58 +1,81 @@
 """Tensor-level calls of the expert-layer operators (include/gemm_experts.h):
 reads pointers, leading dimensions and strides off torch tensors and calls the
 C entry points.  PyTorch only provides device memory and the current stream.
+
+A decoding step calls these with kernels of ten microseconds, so the checks are
+written to cost little: plain dictionaries and integers, no work for arguments
+that are not given.
 """
 from __future__ import annotations
 
 import torch
 
 from . import _abi
-from .api import _DT, _EPI, check, matrix_desc
-from ._abi import Epi, Layout
+from .api import _DT, _EPI, check
+from ._abi import Epi
+
+_CODE = {dt: int(v) for dt, v in _DT.items()}
+_CODE16 = {dt: v for dt, v in _CODE.items() if dt != torch.float32}
+_EPI_CODE = {name: int(v) for name, v in _EPI.items()}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _cuda(**tensors):
-    """Every buffer on one CUDA device: the kernels read device pointers."""
-    dev = next(t.device for t in tensors.values() if t is not None)
-    for name, t in tensors.items():
-        if t is not None and (not t.is_cuda or t.device != dev):
-            where = dev if dev.type == "cuda" else "one CUDA device"
-            raise ValueError(f"{name} must be a CUDA tensor on {where} (it is on {t.device})")
+def _fn(name):
+    """The library's function itself (loaded once)."""
+    fn = _fns.get(name)
+    if fn is None:
+        fn = _fns[name] = getattr(_abi.lib(), name)
+    return fn
+
+
+_fns: dict = {}
+
+
+def _device(first, *others):
+    """The CUDA device of `first`, on which every other buffer has to be: the
+    kernels read device pointers.  Buffers come as (name, tensor or None)."""
+    dev = first[1].device
+    if dev.type != "cuda":
+        raise ValueError(f"{first[0]} must be a CUDA tensor on one CUDA device (it is on {dev})")
+    for name, t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} must be a CUDA tensor on {dev} (it is on {t.device})")
     return dev
 
 
-def _rows(name, t, what="a 2-D tensor"):
-    """(pointer, leading dimension) of a row-major matrix with unit inner stride."""
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be {what}")
-    try:
-        ptr, ld, layout, _, _ = matrix_desc(t)
-    except ValueError:
-        layout = None
-    if layout != Layout.ROW_MAJOR:
-        raise ValueError(f"{name} must be row-major with unit inner stride "
-                         f"(shape {tuple(t.shape)}, strides {tuple(t.stride())})")
-    return ptr, ld
+def _ld(name, t):
+    """Leading dimension of a row-major matrix (the last two dimensions of t)
+    with unit inner stride and rows that do not overlap."""
+    r, c = t.shape[-2:]
+    s = t.stride()
+    if (s[-1] == 1 or c <= 1) and (r <= 1 or s[-2] >= c):
+        return s[-2] if r > 1 and s[-2] > 0 else max(c, 1)
+    raise ValueError(f"{name} must be row-major with unit inner stride "
+                     f"(shape {tuple(t.shape)}, strides {tuple(s)})")
 
 
 def _offsets(offsets, groups):
     if offsets.dtype != torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous():
         raise ValueError("offsets must be a contiguous int32 vector")
-    if offsets.numel() != groups + 1:
+    if offsets.shape[0] != groups + 1:
         raise ValueError(f"offsets must hold groups + 1 = {groups + 1} values "
-                         f"(it holds {offsets.numel()})")
+                         f"(it holds {offsets.shape[0]})")
     return offsets.data_ptr()
 
 
 def _epilogue(epilogue, bias, groups, N):
     """(epilogue, bias pointer, bias stride): bias [N] or [groups, N]."""
+    if bias is None and (epilogue is None or epilogue == "none"):
+        return 0, 0, 0
     if epilogue is None:
-        epilogue = "bias" if bias is not None else "none"
-    epi = epilogue if isinstance(epilogue, Epi) else _EPI.get(str(epilogue).lower())
+        epilogue = "bias"
+    epi = _EPI_CODE.get(epilogue) if isinstance(epilogue, str) else int(epilogue)
+    if epi is None and isinstance(epilogue, str):
+        epi = _EPI_CODE.get(epilogue.lower())
     if epi is None:
         raise ValueError(f"unknown epilogue {epilogue!r}; one of {sorted(_EPI)}")
-    if bool(epi & Epi.BIAS) != (bias is not None):
-        raise ValueError(f"epilogue {epi.name.lower()} " +
+    if bool(epi & 1) != (bias is not None):
+        raise ValueError(f"epilogue {Epi(epi).name.lower()} " +
                          ("needs a bias" if bias is None else "takes no bias"))
     if bias is None:
         return epi, 0, 0
@@ -64,10 +87,12 @@ def _epilogue(epilogue, bias, groups, N):
 
 
 def _out(name, out, shape, dtype, device, types):
-    if dtype is not None and dtype not in types:
-        raise TypeError(f"{name} must be one of {', '.join(str(t) for t in types)}")
     if out is None:
-        return torch.empty(shape, dtype=dtype or types[0], device=device)
+        if dtype is None:
+            dtype = types[0]
+        elif dtype not in types:
+            raise TypeError(f"{name} must be one of {', '.join(str(t) for t in types)}")
+        return torch.empty(shape, dtype=dtype, device=device)
     if tuple(out.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)} (it has {tuple(out.shape)})")
     if out.dtype not in types or (dtype is not None and out.dtype != dtype):
@@ -75,22 +100,28 @@ def _out(name, out, shape, dtype, device, types):
     return out
 
 
-def _pair(A, B, names="A and B"):
-    if A.dtype != B.dtype or A.dtype not in (torch.bfloat16, torch.float16):
+def _code16(A, B, names="A and B"):
+    code = _CODE16.get(A.dtype)
+    if code is None or A.dtype != B.dtype:
         raise TypeError(f"{names} must share one dtype, bfloat16 or float16")
-    return A.dtype
+    return code
 
 
 def _scratch(workspace, need, device):
-    if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    """(workspace kept alive, pointer, bytes)."""
     if workspace is None:
-        return None, 0, 0
+        if need == 0:
+            return None, 0, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _stream(stream, device):
-    return torch.cuda.current_stream(device).cuda_stream if stream is None else stream
+    if stream is not None:
+        return stream
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def grouped_gemm(A: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor,
@@ -105,28 +136,39 @@ def grouped_gemm(A: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor,
     A's dtype; rows of no group are not written); bias: fp32 [N] or [groups, N].
     ``epilogue`` is a name as in ``gemm``.
     """
-    dtype = _pair(A, B)
+    dt = _code16(A, B)
     if A.dim() != 2 or B.dim() != 3 or A.shape[1] != B.shape[1]:
         raise ValueError(f"shape mismatch: A{tuple(A.shape)} B{tuple(B.shape)}")
-    dev = _cuda(A=A, B=B, offsets=offsets, C=C, bias=bias, workspace=workspace)
+    dev = _device(("A", A), ("B", B), ("offsets", offsets), ("C", C), ("bias", bias),
+                  ("workspace", workspace))
     T, K = A.shape
     groups, _, N = B.shape
     if C is None and beta != 0.0:
         raise ValueError("beta != 0 needs an input C")
-    C = _out("C", C, (T, N), out_dtype, dev, (dtype, torch.float32))
+    C = _out("C", C, (T, N), out_dtype, dev, (A.dtype, torch.float32))
     epi, bias_ptr, stride_bias = _epilogue(epilogue, bias, groups, N)
-    pa, lda = _rows("A", A)
-    pb, ldb, lb, _, sb = matrix_desc(B)
-    pc, ldc = _rows("C", C)
+    lda, ldc = _ld("A", A), _ld("C", C)
+    sb, s1, s2 = B.stride()
+    if groups <= 1:
+        sb = 0
+    if (s2 == 1 or N <= 1) and (K <= 1 or s1 >= N):
+        lb, ldb = 0, (s1 if K > 1 else max(N, 1))
+    elif (s1 == 1 or K <= 1) and (N <= 1 or s2 >= K):
+        lb, ldb = 1, (s2 if N > 1 else max(K, 1))
+    else:
+        raise ValueError("B must hold row- or column-major matrices with unit inner stride "
+                         f"(shape {tuple(B.shape)}, strides {tuple(B.stride())})")
     off = _offsets(offsets, groups)
-    dt = int(_DT[dtype])
+    pa, pb = A.data_ptr(), B.data_ptr()
     need = 0
-    if workspace is None:
-        need = _abi.gemm_grouped_workspace_size(dt, groups, T, N, K, pa, lda, pb, ldb, int(lb), sb)
+    if workspace is None and (pa | pb | (lda | ldb | sb) * 2) & 15:
+        need = _abi.gemm_grouped_workspace_size(dt, groups, T, N, K, pa, lda, pb, ldb, lb, sb)
     workspace, ws, ws_bytes = _scratch(workspace, need, dev)
-    check(_abi.gemm_grouped(dt, groups, T, N, K, pa, lda, pb, ldb, int(lb), sb, pc, ldc,
-                            int(_DT[C.dtype]), off, float(alpha), float(beta), bias_ptr,
-                            stride_bias, int(epi), ws, ws_bytes, _stream(stream, dev)))
+    st = _fn("gemm_grouped")(dt, groups, T, N, K, pa, lda, pb, ldb, lb, sb, C.data_ptr(), ldc,
+                             _CODE[C.dtype], off, alpha, beta, bias_ptr, stride_bias, epi, ws,
+                             ws_bytes, _stream(stream, dev))
+    if st:
+        check(st)
     return C
 
 
@@ -136,10 +178,10 @@ def grouped_gemm_wgrad(A: torch.Tensor, D: torch.Tensor, offsets: torch.Tensor,
     """C[e] <- alpha * A_e^T @ D_e + beta * C[e], the weights' gradient of
     ``grouped_gemm``: A [T, M] and D [T, N] row-major, C [groups, M, N] (a group
     without rows gives beta * C[e])."""
-    dtype = _pair(A, D, "A and D")
+    dt = _code16(A, D, "A and D")
     if A.dim() != 2 or D.dim() != 2 or A.shape[0] != D.shape[0]:
         raise ValueError(f"shape mismatch: A{tuple(A.shape)} D{tuple(D.shape)}")
-    dev = _cuda(A=A, D=D, offsets=offsets, C=C, workspace=workspace)
+    dev = _device(("A", A), ("D", D), ("offsets", offsets), ("C", C), ("workspace", workspace))
     T, M = A.shape
     N = D.shape[1]
     groups = offsets.numel() - 1
@@ -147,21 +189,19 @@ def grouped_gemm_wgrad(A: torch.Tensor, D: torch.Tensor, offsets: torch.Tensor,
         raise ValueError("offsets must hold groups + 1 values")
     if C is None and beta != 0.0:
         raise ValueError("beta != 0 needs an input C")
-    C = _out("C", C, (groups, M, N), out_dtype, dev, (dtype, torch.float32))
-    pa, lda = _rows("A", A)
-    pd, ldd = _rows("D", D)
-    pc, ldc, lc, _, sc = matrix_desc(C)
-    if lc != Layout.ROW_MAJOR:
-        raise ValueError("C must hold row-major matrices")
+    C = _out("C", C, (groups, M, N), out_dtype, dev, (A.dtype, torch.float32))
+    lda, ldd, ldc = _ld("A", A), _ld("D", D), _ld("C", C)
     off = _offsets(offsets, groups)
-    dt = int(_DT[dtype])
+    pa, pd = A.data_ptr(), D.data_ptr()
     need = 0
-    if workspace is None:
+    if workspace is None and (pa | pd | (lda | ldd) * 2) & 15:
         need = _abi.gemm_grouped_wgrad_workspace_size(dt, groups, T, M, N, pa, lda, pd, ldd)
     workspace, ws, ws_bytes = _scratch(workspace, need, dev)
-    check(_abi.gemm_grouped_wgrad(dt, groups, T, M, N, pa, lda, pd, ldd, pc, ldc, sc,
-                                  int(_DT[C.dtype]), off, float(alpha), float(beta), ws, ws_bytes,
-                                  _stream(stream, dev)))
+    st = _fn("gemm_grouped_wgrad")(dt, groups, T, M, N, pa, lda, pd, ldd, C.data_ptr(), ldc,
+                                   C.stride(0) if groups > 1 else 0, _CODE[C.dtype], off, alpha,
+                                   beta, ws, ws_bytes, _stream(stream, dev))
+    if st:
+        check(st)
     return C
 
 
@@ -171,26 +211,26 @@ def newton_schulz(G: torch.Tensor, out: torch.Tensor | None = None, *, steps=5,
     """The orthogonalised form of G ([M, N], or [batch, M, N] matrix by matrix):
     X = G / (||G||_F + eps), then ``steps`` times X = a X + (b S + c S S) X with
     S = X X^T.  G is fp32, bf16 or fp16; the result bf16 (default) or fp16."""
-    if G.dtype not in _DT:
+    if G.dtype not in _CODE:
         raise TypeError("G must be bfloat16, float16 or float32")
     if G.dim() not in (2, 3):
         raise ValueError("G must be a 2-D or 3-D tensor")
     if len(coefficients) != 3:
         raise ValueError("coefficients must be three numbers")
-    dev = _cuda(G=G, out=out, workspace=workspace)
+    dev = _device(("G", G), ("out", out), ("workspace", workspace))
     out = _out("out", out, G.shape, out_dtype, dev, (torch.bfloat16, torch.float16))
     batch = G.shape[0] if G.dim() == 3 else 1
     M, N = G.shape[-2:]
-    pg, ldg, lg, _, sg = matrix_desc(G)
-    po, ldo, lo, _, so = matrix_desc(out)
-    if lg != Layout.ROW_MAJOR or lo != Layout.ROW_MAJOR:
-        raise ValueError("G and out must hold row-major matrices")
+    ldg, ldo = _ld("G", G), _ld("out", out)
+    sg, so = (G.stride(0), out.stride(0)) if batch > 1 else (0, 0)
     need = _abi.gemm_newton_schulz_workspace_size(batch, M, N) if workspace is None else 0
     workspace, ws, ws_bytes = _scratch(workspace, need, dev)
-    a, b, c = (float(v) for v in coefficients)
-    check(_abi.gemm_newton_schulz(int(_DT[G.dtype]), batch, M, N, pg, ldg, sg, po, ldo, so,
-                                  int(_DT[out.dtype]), int(steps), a, b, c, float(eps), ws,
-                                  ws_bytes, _stream(stream, dev)))
+    a, b, c = coefficients
+    st = _fn("gemm_newton_schulz")(_CODE[G.dtype], batch, M, N, G.data_ptr(), ldg, sg,
+                                   out.data_ptr(), ldo, so, _CODE[out.dtype], steps, a, b, c, eps,
+                                   ws, ws_bytes, _stream(stream, dev))
+    if st:
+        check(st)
     return out
 
 
@@ -206,13 +246,13 @@ def w4_gemm(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, *, zeros=Non
     With ``offsets`` (int32 [experts + 1]) q, scales and zeros carry a leading
     expert dimension and rows offsets[e] .. offsets[e + 1] - 1 use expert e.
     """
-    dtype = _pair(x, scales, "x and scales")
+    dt = _code16(x, scales, "x and scales")
     lead = 3 if offsets is not None else 2
     if x.dim() != 2 or q.dim() != lead or scales.dim() != lead:
         raise ValueError(f"x must be 2-D, q and scales {lead}-D "
                          f"({'with' if lead == 3 else 'without'} offsets)")
-    dev = _cuda(x=x, q=q, scales=scales, zeros=zeros, offsets=offsets, out=out, bias=bias,
-                workspace=workspace)
+    dev = _device(("x", x), ("q", q), ("scales", scales), ("zeros", zeros), ("offsets", offsets),
+                  ("out", out), ("bias", bias), ("workspace", workspace))
     T, K = x.shape
     groups = q.shape[0] if lead == 3 else 1
     N = q.shape[-2]
@@ -227,15 +267,19 @@ def w4_gemm(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, *, zeros=Non
     for name, t in (("q", q), ("scales", scales), ("zeros", zeros)):
         if t is not None and not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-    out = _out("out", out, (T, N), out_dtype, dev, (dtype, torch.float32))
+    out = _out("out", out, (T, N), out_dtype, dev, (x.dtype, torch.float32))
     epi, bias_ptr, stride_bias = _epilogue(epilogue, bias, groups, N)
-    px, ldx = _rows("x", x)
-    po, ldo = _rows("out", out)
+    ldx, ldo = _ld("x", x), _ld("out", out)
     off = _offsets(offsets, groups) if offsets is not None else 0
-    dt, odt = int(_DT[dtype]), int(_DT[out.dtype])
-    need = _abi.gemm_w4_workspace_size(dt, groups, T, N, K, px, ldx, odt) if workspace is None else 0
+    px, odt = x.data_ptr(), _CODE[out.dtype]
+    need = 0
+    if workspace is None and ((px | ldx * 2) & 15 or T > groups):
+        need = _abi.gemm_w4_workspace_size(dt, groups, T, N, K, px, ldx, odt)
     workspace, ws, ws_bytes = _scratch(workspace, need, dev)
-    check(_abi.gemm_w4(dt, groups, T, N, K, px, ldx, q.data_ptr(), scales.data_ptr(),
-                       0 if zeros is None else zeros.data_ptr(), K // n_groups, po, ldo, odt, off,
-                       bias_ptr, stride_bias, int(epi), ws, ws_bytes, _stream(stream, dev)))
+    st = _fn("gemm_w4")(dt, groups, T, N, K, px, ldx, q.data_ptr(), scales.data_ptr(),
+                        0 if zeros is None else zeros.data_ptr(), K // n_groups, out.data_ptr(),
+                        ldo, odt, off, bias_ptr, stride_bias, epi, ws, ws_bytes,
+                        _stream(stream, dev))
+    if st:
+        check(st)
     return out

@@ -12,9 +12,9 @@
  * operands (none when they are equal).  Rows that belong to no group are
  * neither read as results nor written.  The offsets are read by the kernels,
  * never by the host, so a call needs no synchronisation with whatever computes
- * them.  Offsets that descend, or leave [0, T], are clamped (no access leaves
- * the operands) and reported: gemm_check_device_status then returns
- * GEMM_ERR_INVALID_ARG.
+ * them.  Offsets that descend or leave [0, T] are reported:
+ * gemm_check_device_status then returns GEMM_ERR_INVALID_ARG, and the groups
+ * from the first such one on (gemm_grouped_wgrad: that group) count as empty.
  */
 #ifndef DGEMM_GB300_GEMM_EXPERTS_H
 #define DGEMM_GB300_GEMM_EXPERTS_H
