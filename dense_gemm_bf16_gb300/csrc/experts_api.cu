@@ -626,13 +626,18 @@ gemm_status_t gemm_w4(gemm_dtype_t ab_dtype, int64_t groups, int64_t T, int64_t 
     const int64_t avg = cdiv(T, groups);
     const int64_t want = offsets ? (T < 2 * avg ? T : 2 * avg) : T;
     const int tokens = want <= 8 ? 8 : (want <= 16 ? 16 : (want <= 32 ? 32 : 64));
-    const int rt = w4_rows(tokens);
+    const W4Shape shape = w4_shape(tokens, group);
     W4Params p;
     std::memset(&p, 0, sizeof(p));
-    if (!encode_map8(&p.tmap_q, Q, K / 2, N, groups, K / 2, N * (K / 2), 128,
-                     static_cast<uint32_t>(rt)) ||
-        !encode_map16(&p.tmap_x, ab_dtype, a.ptr, K, T, 1, a.ld * 2, 0, 64,
-                      static_cast<uint32_t>(tokens)))
+    p.q4 = K % 256 == 0;
+    p.x4 = K % 64 == 0;
+    if (!encode_map8(&p.tmap_q, Q, K / 2, N, groups, static_cast<uint32_t>(shape.rows),
+                     p.q4 ? static_cast<uint32_t>(shape.blocks) : 0u) ||
+        !(p.x4 ? encode_map16_blocks(&p.tmap_x, ab_dtype, a.ptr, K, T, a.ld * 2,
+                                     static_cast<uint32_t>(tokens),
+                                     static_cast<uint32_t>(4 * shape.blocks))
+               : encode_map16(&p.tmap_x, ab_dtype, a.ptr, K, T, 1, a.ld * 2, 0, 64,
+                              static_cast<uint32_t>(tokens))))
         return GEMM_ERR_CUDA;
     p.q = Q;
     p.scales = scales;
@@ -643,16 +648,19 @@ gemm_status_t gemm_w4(gemm_dtype_t ab_dtype, int64_t groups, int64_t T, int64_t 
     p.N = static_cast<int32_t>(N);
     p.K = static_cast<int32_t>(K);
     p.group = group;
-    const int64_t n_tiles = cdiv(N, rt), steps = cdiv(K, 256);
+    const int stage_k = 256 * shape.blocks;
+    p.vec = K % stage_k == 0 && aligned(scales, 16) && (!zeros || aligned(zeros, 8));
+    const int64_t n_tiles = cdiv(N, shape.rows), steps = cdiv(K, stage_k);
     // units there may be: full token tiles and one more for each non-empty group
     const int64_t units = n_tiles * (T / tokens + (groups < T ? groups : T));
     if (units > kLim) return GEMM_ERR_UNSUPPORTED;
     // K slices (a cluster per unit) where the units would leave SMs idle, each of
-    // at least two 256-wide steps
+    // at least one stage for every set of consumer warps.  (Clusters of 8 do not all
+    // fit at once: N = 1024, K = 8192 took 11.9 us in 8 slices.)
     int splits = 1;
     if (!offsets)
-        while (splits < 8 && n_tiles * cdiv(T, tokens) * splits * 2 <= d.sm_count &&
-               steps >= splits * 4)
+        while (splits < 4 && n_tiles * cdiv(T, tokens) * splits * 2 <= d.sm_count &&
+               steps >= splits * 8)
             splits *= 2;
     p.n_tiles = static_cast<int32_t>(n_tiles);
     p.splits = splits;

@@ -1117,11 +1117,36 @@ bool encode_map16_k4(CUtensorMap* map, int dt, const void* ptr, int64_t k, int64
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool encode_map8(CUtensorMap* map, const void* ptr, int64_t inner, int64_t outer, int64_t depth,
-                 int64_t outer_stride, int64_t depth_stride, uint32_t box_inner,
-                 uint32_t box_outer) {
-    return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, ptr, inner, outer, depth, outer_stride,
-                      depth_stride, box_inner, box_outer);
+bool encode_map8(CUtensorMap* map, const void* ptr, int64_t inner, int64_t rows, int64_t depth,
+                 uint32_t box_rows, uint32_t box_blocks) {
+    if (box_blocks == 0)
+        return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, ptr, inner, rows, depth, inner,
+                          rows * inner, 128, box_rows);
+    auto fn = encode_fn();
+    if (!fn || inner % 128 != 0) return false;
+    cuuint64_t dims[4] = {128u, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(inner / 128),
+                          static_cast<cuuint64_t>(depth)};
+    cuuint64_t strides[3] = {static_cast<cuuint64_t>(inner), 128u,
+                             static_cast<cuuint64_t>(rows * inner)};
+    cuuint32_t box[4] = {128u, box_rows, box_blocks, 1u};
+    cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4u, const_cast<void*>(ptr), dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_map16_blocks(CUtensorMap* map, int dt, const void* ptr, int64_t k, int64_t rows,
+                         int64_t row_stride, uint32_t box_rows, uint32_t box_blocks) {
+    auto fn = encode_fn();
+    if (!fn || k % 64 != 0) return false;
+    cuuint64_t dims[3] = {64u, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(k / 64)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_stride), 128u};
+    cuuint32_t box[3] = {64u, box_rows, box_blocks};
+    cuuint32_t estr[3] = {1u, 1u, 1u};
+    return fn(map, dt == DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+              3u, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace dg

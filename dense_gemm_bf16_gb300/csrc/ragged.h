@@ -82,10 +82,13 @@ bool encode_map16(CUtensorMap* map, int dt, const void* ptr, int64_t inner, int6
 // depth), in boxes of 64 x box_rows x 2 blocks.
 bool encode_map16_k4(CUtensorMap* map, int dt, const void* ptr, int64_t k, int64_t rows,
                      int64_t depth, int64_t row_stride, int64_t depth_stride, uint32_t box_rows);
-// ... of bytes, two-dimensional boxes of one z
-bool encode_map8(CUtensorMap* map, const void* ptr, int64_t inner, int64_t outer, int64_t depth,
-                 int64_t outer_stride, int64_t depth_stride, uint32_t box_inner,
-                 uint32_t box_outer);
+// Bytes in 128-byte blocks: (128, rows, blocks, depth) in boxes of `box_blocks`
+// blocks, or (bytes, rows, depth) with box_blocks == 0.
+bool encode_map8(CUtensorMap* map, const void* ptr, int64_t inner, int64_t rows, int64_t depth,
+                 uint32_t box_rows, uint32_t box_blocks);
+// 16-bit rows in 64-wide blocks: (64, rows, blocks) in boxes of `box_blocks` blocks.
+bool encode_map16_blocks(CUtensorMap* map, int dt, const void* ptr, int64_t k, int64_t rows,
+                         int64_t row_stride, uint32_t box_rows, uint32_t box_blocks);
 
 // One ragged product, from checked arguments (experts_api.cu): the lane
 // operand `a` and the column operand `b` as stored matrices.
@@ -117,13 +120,15 @@ gemm_status_t rg_run(const RgProblem& q, const DeviceInfo& d, cudaStream_t strea
 
 // ---- 4-bit weights (w4.cu)
 struct W4Params {
-    CUtensorMap tmap_q;      // [groups][N][K / 2] bytes, boxes of 128 bytes x w4_rows() rows
-    CUtensorMap tmap_x;      // [T][K], boxes of 64 x the tokens of a tile
+    CUtensorMap tmap_q;      // [groups][N][K / 2] bytes, boxes of 128 bytes x rows (x blocks)
+    CUtensorMap tmap_x;      // [T][K], boxes of 64 x the tokens of a tile (x blocks)
     const uint8_t* q;
     const void* scales;
     const uint8_t* zeros;
     const int32_t* offsets;  // or null
     int32_t groups, T, N, K, group;
+    int32_t vec;             // 1: scales and zeros of a stage load as vectors
+    int32_t q4, x4;          // 1: the map has blocks as a dimension, a stage is one load
     int32_t n_tiles, splits; // row tiles; CTAs (K slices) of a cluster
     int32_t grid;            // clusters
     void* C;
@@ -138,7 +143,12 @@ struct W4Params {
     int64_t dbg_c_elems;
 #endif
 };
-int w4_rows(int tokens);  // weight rows of a unit of `tokens` token columns
+// Shape of the kernel for `tokens` token columns and a scale per `group` weights: weight rows of a unit, and
+// 256-weight blocks of a stage.
+struct W4Shape {
+    int rows, blocks;
+};
+W4Shape w4_shape(int tokens, int group);
 cudaError_t w4_launch(int dt, int tokens, const W4Params& p, cudaStream_t stream);
 cudaError_t w4_prepare();
 // Dense [groups][N][K] weights of type dt: (q - z) * s, rounded once.

@@ -7,7 +7,8 @@
 // SM streams 64 (128 for more than 16 tokens) rows of them through a ring of TMA
 // boxes (128 bytes = 256 weights of a row, with the same 256 columns of the
 // tokens), filled by one producer warp that runs ahead over the CTA's units.
-// Sixteen (eight) consumer warps split a stage: 16 rows by 64 to 256 weights each.  The
+// Of its sixteen (eight) consumer warps, each set of RT / 16 takes a range of the
+// stages of its own, a warp 16 rows by a whole stage (512 or 256 weights).  The
 // arithmetic stays near the loads by going through mma.sync m16n8k16 with the
 // weights on its M side: a 4-bit integer is an exact bf16 (fp16) number, made by
 // a byte permute, one masking and one packed subtraction for every two weights,
@@ -34,26 +35,27 @@
 namespace dg {
 namespace {
 
-constexpr int W4_STEP = 256;     // weights of a row per stage
-
-template <int MT>
+template <int MT, int GROUP>
 struct W4Cfg {
-    // (64 tokens' sums take the registers of half as many warps)
-    static constexpr int WARPS = MT == 64 ? 8 : 16;  // consumer warps
+    static constexpr int WARPS = MT <= 16 ? 16 : 8;  // consumer warps
     static constexpr int THREADS = 32 * (WARPS + 1); // and the producer, warp 0
     static constexpr int RT = MT <= 16 ? 64 : 128;   // weight rows (outputs) of a unit
     static constexpr int RG = RT / 16;               // row groups of a stage
-    static constexpr int KQ = WARPS / RG;            // K parts of a stage
-    static constexpr int CPW = 8 / KQ;              // 16-byte chunks of a warp's rows
-    static constexpr uint32_t Q_BYTES = RT * 128;
-    static constexpr uint32_t X_BOX = MT * 128;     // 64 values of MT tokens
-    static constexpr uint32_t STAGE = Q_BYTES + 4 * X_BOX;
+    static constexpr int SG = WARPS / RG;            // stages in work at once
+    // 256-weight blocks of a stage (one where many tokens' or groups' values take
+    // the registers)
+    static constexpr int BLK = MT <= 16 && GROUP > 32 ? 2 : 1;
+    static constexpr int STEP = 256 * BLK;           // weights of a row per stage
+    static constexpr uint32_t Q_BYTES = RT * 128;    // of a block
+    static constexpr uint32_t X_BOX = MT * 128;      // 64 values of MT tokens
+    static constexpr uint32_t STAGE = BLK * (Q_BYTES + 4 * X_BOX);
     static constexpr int R_LD = RT + 4;
-    static constexpr uint32_t R_BYTES = KQ * MT * R_LD * 4;
+    static constexpr uint32_t R_BYTES = SG * MT * R_LD * 4;
     static constexpr int FIT = (232448 - 1024 - 512 - R_BYTES) / STAGE;
     static constexpr int STAGES = FIT > 16 ? 16 : FIT;
     static constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE + R_BYTES + 512;
     static_assert(STAGES >= 3 && (2 * STAGES + 1) * 8 <= 512, "ring");
+    static_assert(Q_BYTES % 1024 == 0 && X_BOX % 1024 == 0, "swizzle atoms");
 };
 
 template <int DT>
@@ -71,6 +73,24 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
             "{%8,%9}, {%0,%1,%2,%3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The same onto zero.
+template <int DT>
+__device__ __forceinline__ void mma16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                               uint32_t b1) {
+    if constexpr (DT == DT_BF16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%10,%10,%10,%10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%10,%10,%10,%10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // Weights 2 j and 2 j + 1 of word w (w4 = w >> 4) as 16-bit floats minus the pair
@@ -91,9 +111,17 @@ __device__ __forceinline__ uint32_t w4_pair(uint32_t w, uint32_t w4, uint32_t su
     }
 }
 
+// 128 + z (1024 + z) twice, for the default and for byte `i` of four zero points
+// (0 .. 15 each).
 template <int DT>
 __device__ __forceinline__ uint32_t w4_sub(int z) {
     return (DT == DT_BF16 ? 0x43004300u : 0x64006400u) + static_cast<uint32_t>(z) * 0x00010001u;
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t w4_sub(uint32_t z, int i) {
+    return (__byte_perm(z, 0u, 0x4040 + 0x0101 * i) & 0x000F000Fu) |
+           (DT == DT_BF16 ? 0x43004300u : 0x64006400u);
 }
 
 template <int DT>
@@ -170,26 +198,75 @@ __device__ __forceinline__ bool w4_unit(const W4Params& p, W4Walk& w, int u, int
     const int tile = r / chunks;
     const int t0 = (r - tile * chunks) * MT;
     o.group = w.base + l;
-    o.n0 = tile * W4Cfg<MT>::RT;
+    o.n0 = tile * W4Cfg<MT, 128>::RT;
     o.row0 = row0 + t0;
     o.tokens = rows - t0 < MT ? rows - t0 : MT;
     return true;
 }
 
-// Scales and zero points of a warp's two rows r, r + 8 for one stage, as loaded.
+// Scales and zero points of a warp's rows r, r + 8 for one stage, as loaded:
+// NG neighbouring 16-bit scales and bytes of each row.
 template <int NG>
 struct W4Scales {
-    uint16_t s[2][NG];
-    uint8_t z[2][NG];
+    uint32_t s[2][NG / 2];
+    uint32_t z[2][(NG + 3) / 4];
 };
 
+// (vec: every stage's groups of a row start on a 16-byte boundary, or on their size)
+template <int NG>
+__device__ __forceinline__ void w4_fetch(const W4Params& p, int64_t row, int gi, int kg, int i,
+                                         W4Scales<NG>& v) {
+    const uint16_t* s = static_cast<const uint16_t*>(p.scales) + row * kg;
+    const uint8_t* z = p.zeros + row * kg;
+    if (p.vec && gi + NG <= kg) {
+        if constexpr (NG >= 8) {
+#pragma unroll
+            for (int k = 0; k < NG / 8; ++k) {
+                const uint4 u = __ldg(reinterpret_cast<const uint4*>(s + gi) + k);
+                v.s[i][4 * k] = u.x; v.s[i][4 * k + 1] = u.y;
+                v.s[i][4 * k + 2] = u.z; v.s[i][4 * k + 3] = u.w;
+            }
+        } else if constexpr (NG == 4) {
+            const uint2 u = __ldg(reinterpret_cast<const uint2*>(s + gi));
+            v.s[i][0] = u.x; v.s[i][1] = u.y;
+        } else {
+            v.s[i][0] = __ldg(reinterpret_cast<const uint32_t*>(s + gi));
+        }
+        if (p.zeros) {
+            if constexpr (NG >= 8) {
+#pragma unroll
+                for (int k = 0; k < NG / 8; ++k) {
+                    const uint2 u = __ldg(reinterpret_cast<const uint2*>(z + gi) + k);
+                    v.z[i][2 * k] = u.x; v.z[i][2 * k + 1] = u.y;
+                }
+            } else if constexpr (NG == 4) {
+                v.z[i][0] = __ldg(reinterpret_cast<const uint32_t*>(z + gi));
+            } else {
+                v.z[i][0] = __ldg(reinterpret_cast<const uint16_t*>(z + gi));
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < NG / 2; ++k) v.s[i][k] = 0u;
+#pragma unroll
+    for (int k = 0; k < (NG + 3) / 4; ++k) v.z[i][k] = 0u;
+#pragma unroll
+    for (int k = 0; k < NG; ++k) {
+        // (groups past K read the last one: they multiply zeros)
+        const int g = gi + k < kg ? gi + k : kg - 1;
+        v.s[i][k / 2] |= static_cast<uint32_t>(__ldg(s + g)) << (16 * (k & 1));
+        if (p.zeros) v.z[i][k / 4] |= static_cast<uint32_t>(__ldg(z + g)) << (8 * (k & 3));
+    }
+}
+
 template <int DT, int MT, int GROUP>
-__global__ void __launch_bounds__(W4Cfg<MT>::THREADS, 1) w4_kernel(const __grid_constant__ W4Params p) {
-    using C = W4Cfg<MT>;
+__global__ void __launch_bounds__(W4Cfg<MT, GROUP>::THREADS, 1) w4_kernel(const __grid_constant__ W4Params p) {
+    using C = W4Cfg<MT, GROUP>;
     constexpr int NT = MT / 8;
-    constexpr int CPG = GROUP / 32;                       // chunks per group
-    constexpr int CG = CPG < C::CPW ? CPG : C::CPW;       // chunks a warp scales at once
-    constexpr int NG = C::CPW / CG;                       // scales per row and stage
+    constexpr int CPG = GROUP / 32;        // 16-byte chunks per group
+    constexpr int NG = C::STEP / GROUP;    // groups of a row per stage
+    constexpr int NGB = 256 / GROUP;       // ... per block
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -205,7 +282,7 @@ __global__ void __launch_bounds__(W4Cfg<MT>::THREADS, 1) w4_kernel(const __grid_
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(full0 + 8u * s, 1);
-            mbar_init(empty0 + 8u * s, C::WARPS);
+            mbar_init(empty0 + 8u * s, C::RG);
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -218,39 +295,60 @@ __global__ void __launch_bounds__(W4Cfg<MT>::THREADS, 1) w4_kernel(const __grid_
     w4_window<MT>(p, walk, lane);
     __syncthreads();
 
-    const int steps = (p.K + W4_STEP - 1) / W4_STEP;
+    // Stages of this CTA's K slice.  Each set of consumer warps walks a range of its
+    // own, so that its scales come as neighbours; the ring holds the sets' first
+    // stages, their second ones, and so on (the ranges' lengths differ by one at most).
+    const int steps = (p.K + C::STEP - 1) / C::STEP;
     const int st0 = static_cast<int>(static_cast<int64_t>(steps) * rank / p.splits);
     const int st1 = static_cast<int>(static_cast<int64_t>(steps) * (rank + 1) / p.splits);
-    int stage = 0;
-    uint32_t phase = 0, armed = 0;
     W4Unit w;
 
     if (warp == 0) {
         // ------------------------------------------------ producer
+        int stage = 0;
+        uint32_t phase = 0, armed = 0;
         bool ok = true;
         for (int u = u0; ok && w4_unit<MT>(p, walk, u, lane, w); u += nu) {
             if (lane == 0) {
                 const uint64_t pol_q = l2_policy_evict_first();
                 const uint64_t pol_x = l2_policy_evict_last();
-                for (int st = st0; st < st1; ++st) {
-                    if (!mbar_wait(empty0 + 8u * stage, phase ^ 1u, abort_flag, p.status, p.timeout_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t fb = full0 + 8u * stage;
-                    mbar_arrive_expect_tx(fb, C::STAGE);
-                    const uint32_t dst = smem_u32(smem) + stage * C::STAGE;
-                    tma_load_3d(dst, &p.tmap_q, fb, st * 128, w.n0, w.group, pol_q);
+                const int n = st1 - st0;
+                for (int i = 0, round = 0; ok && i < n; ++round)
+                    for (int k = 0; k < C::SG; ++k) {
+                        const int st = st0 + n * k / C::SG + round;
+                        if (st >= st0 + n * (k + 1) / C::SG) continue;
+                        if (!mbar_wait(empty0 + 8u * stage, phase ^ 1u, abort_flag, p.status,
+                                       p.timeout_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t fb = full0 + 8u * stage;
+                        mbar_arrive_expect_tx(fb, C::STAGE);
+                        const uint32_t dst = smem_u32(smem) + stage * C::STAGE;
+                        const uint32_t xdst = dst + C::BLK * C::Q_BYTES;
+                        if (p.q4) {
+                            tma_load_4d_cg<1>(dst, &p.tmap_q, fb, 0, w.n0, st * C::BLK, w.group, pol_q);
+                        } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        tma_load_3d(dst + C::Q_BYTES + i * C::X_BOX, &p.tmap_x, fb,
-                                    st * W4_STEP + 64 * i, w.row0, 0, pol_x);
-                    ++armed;
-                    if (++stage == C::STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
+                            for (int j = 0; j < C::BLK; ++j)
+                                tma_load_3d(dst + j * C::Q_BYTES, &p.tmap_q, fb,
+                                            (st * C::BLK + j) * 128, w.n0, w.group, pol_q);
+                        }
+                        if (p.x4) {
+                            tma_load_3d(xdst, &p.tmap_x, fb, 0, w.row0, st * C::BLK * 4, pol_x);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 4 * C::BLK; ++j)
+                                tma_load_3d(xdst + j * C::X_BOX, &p.tmap_x, fb,
+                                            st * C::STEP + 64 * j, w.row0, 0, pol_x);
+                        }
+                        ++armed;
+                        ++i;
+                        if (++stage == C::STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
                     }
-                }
             }
             ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
             if (p.splits > 1) {
@@ -272,67 +370,74 @@ __global__ void __launch_bounds__(W4Cfg<MT>::THREADS, 1) w4_kernel(const __grid_
     } else {
         // ------------------------------------------------ consumers
         const int cw = warp - 1, gr = lane >> 2, t = lane & 3;
-        const int rg = cw % C::RG, kq = cw / C::RG;
+        const int rg = cw % C::RG, sg = cw / C::RG;
         const int r = rg * 16 + gr;  // rows r and r + 8 of the unit
         const int kg = p.K / GROUP;
-        const int chunk0 = kq * C::CPW;
         // word t of chunk c of row r of a stage: the chunk is swizzled by the row
         const uint32_t q_at = static_cast<uint32_t>(r * 128 + t * 4);
         bool ok = true;
-        for (int u = u0; w4_unit<MT>(p, walk, u, lane, w); u += nu) {
+        uint32_t it0 = 0;  // stages of the units before
+        const int n = st1 - st0;
+        const int a0 = st0 + n * sg / C::SG, a1 = st0 + n * (sg + 1) / C::SG;
+        const int shortest = n / C::SG;  // stages of the shorter ranges
+        int longer_before = 0;           // sets before this one that have one more
+#pragma unroll
+        for (int k = 0; k < C::SG; ++k)
+            if (k < sg && n * (k + 1) / C::SG - n * k / C::SG > shortest) ++longer_before;
+        W4Scales<NG> cur, nxt;
+        int64_t row_lo, row_hi;
+        // the unit's rows of scales, and its first stage's ones
+        auto open_unit = [&](const W4Unit& v) {
+            // (rows past N read the last one: their sums are not stored)
+            const int n_lo = v.n0 + r < p.N ? v.n0 + r : p.N - 1;
+            const int n_hi = v.n0 + r + 8 < p.N ? v.n0 + r + 8 : p.N - 1;
+            row_lo = static_cast<int64_t>(v.group) * p.N + n_lo;
+            row_hi = static_cast<int64_t>(v.group) * p.N + n_hi;
+        };
+        auto fetch = [&](int st) {
+            w4_fetch<NG>(p, row_lo, st * NG, kg, 0, nxt);
+            w4_fetch<NG>(p, row_hi, st * NG, kg, 1, nxt);
+        };
+        bool have = w4_unit<MT>(p, walk, u0, lane, w);
+        if (have) {
+            open_unit(w);
+            if (a0 < a1) fetch(a0);
+        }
+        for (int u = u0; have; u += nu, it0 += st1 - st0) {
             float total[NT][4];
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) total[j][i] = 0.0f;
-            // (rows past N and groups past K read the last ones: their sums are
-            // not stored, or multiply zeros)
-            const int n_lo = w.n0 + r < p.N ? w.n0 + r : p.N - 1;
-            const int n_hi = w.n0 + r + 8 < p.N ? w.n0 + r + 8 : p.N - 1;
-            const int64_t at_lo = (static_cast<int64_t>(w.group) * p.N + n_lo) * kg;
-            const int64_t at_hi = (static_cast<int64_t>(w.group) * p.N + n_hi) * kg;
-            const uint16_t* scales = static_cast<const uint16_t*>(p.scales);
-            auto fetch = [&](int st, W4Scales<NG>& v) {
-#pragma unroll
-                for (int i = 0; i < NG; ++i) {
-                    int gi = (st * W4_STEP + (chunk0 + i * CG) * 32) / GROUP;
-                    gi = gi < kg ? gi : kg - 1;
-                    v.s[0][i] = __ldg(scales + at_lo + gi);
-                    v.s[1][i] = __ldg(scales + at_hi + gi);
-                    if (p.zeros) {
-                        v.z[0][i] = __ldg(p.zeros + at_lo + gi);
-                        v.z[1][i] = __ldg(p.zeros + at_hi + gi);
-                    }
-                }
-            };
-            W4Scales<NG> cur, nxt;
-            if (st0 < st1) fetch(st0, nxt);
-            for (int st = st0; ok && st < st1; ++st) {
+            for (int st = a0; ok && st < a1; ++st) {
+                const int round = st - a0;
+                const uint32_t it = it0 + static_cast<uint32_t>(
+                                              round * C::SG + (round < shortest ? sg : longer_before));
+                const uint32_t turn = it / C::STAGES;
+                const uint32_t stage = it - turn * C::STAGES;
                 cur = nxt;
-                if (st + 1 < st1) fetch(st + 1, nxt);
-                ok = mbar_wait(full0 + 8u * stage, phase, abort_flag, p.status, p.timeout_ns);
+                if (st + 1 < a1) fetch(st + 1);
+                ok = mbar_wait(full0 + 8u * stage, turn & 1u, abort_flag, p.status, p.timeout_ns);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 const uint8_t* qs = smem + stage * C::STAGE;
-                const uint8_t* xs = qs + C::Q_BYTES;
+                const uint8_t* xs = qs + C::BLK * C::Q_BYTES;
+#pragma unroll 1
+                for (int blk = 0; blk < C::BLK; ++blk, qs += C::Q_BYTES, xs += 4 * C::X_BOX) {
 #pragma unroll
-                for (int gg = 0; gg < NG; ++gg) {
-                    // two chains of sums where one tile of tokens gives no other
+                for (int gg = 0; gg < NGB; ++gg) {
+                    // (two chains of sums where neither tokens nor a short group give
+                    // independent ones)
+                    constexpr bool two = NT == 1 && CPG > 1;
                     float acc[NT][4], acc2[4];
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc2[i] = 0.0f;
                     uint32_t sub_lo = w4_sub<DT>(8), sub_hi = sub_lo;
                     if (p.zeros) {
-                        sub_lo = w4_sub<DT>(cur.z[0][gg] & 15);
-                        sub_hi = w4_sub<DT>(cur.z[1][gg] & 15);
+                        sub_lo = w4_sub<DT>(cur.z[0][gg / 4], gg & 3);
+                        sub_hi = w4_sub<DT>(cur.z[1][gg / 4], gg & 3);
                     }
 #pragma unroll
-                    for (int cc = 0; cc < CG; ++cc) {
-                        const int c = chunk0 + gg * CG + cc;
+                    for (int cc = 0; cc < CPG; ++cc) {
+                        const int c = gg * CPG + cc;
                         const uint8_t* src = qs + (q_at + static_cast<uint32_t>((c ^ gr) << 4));
                         const uint32_t lo = *reinterpret_cast<const uint32_t*>(src);
                         const uint32_t hi = *reinterpret_cast<const uint32_t*>(src + 1024);
@@ -349,13 +454,25 @@ __global__ void __launch_bounds__(W4Cfg<MT>::THREADS, 1) w4_kernel(const __grid_
                                               ((((c & 1) * 4 + t) ^ gr) << 4);
 #pragma unroll
                         for (int j = 0; j < NT; ++j) {
-                            const uint4 x = *reinterpret_cast<const uint4*>(xsrc + 1024 * j);
-                            mma16816<DT>(acc[j], a1, x.x, x.y);
-                            mma16816<DT>(NT == 1 ? acc2 : acc[j], a2, x.z, x.w);
+                            // (one tile: only the lanes of tokens that exist load)
+                            uint4 x = make_uint4(0, 0, 0, 0);
+                            if (NT > 1 || gr < w.tokens)
+                                x = *reinterpret_cast<const uint4*>(xsrc + 1024 * j);
+                            if (cc == 0)
+                                mma16816_first<DT>(acc[j], a1, x.x, x.y);
+                            else
+                                mma16816<DT>(acc[j], a1, x.x, x.y);
+                            if (two && cc == 0)
+                                mma16816_first<DT>(acc2, a2, x.z, x.w);
+                            else
+                                mma16816<DT>(two ? acc2 : acc[j], a2, x.z, x.w);
                         }
                     }
-                    const float s_lo = w4_float<DT>(cur.s[0][gg]), s_hi = w4_float<DT>(cur.s[1][gg]);
-                    if (NT == 1) {
+                    const float s_lo = w4_float<DT>(
+                        static_cast<uint16_t>(cur.s[0][gg / 2] >> (16 * (gg & 1))));
+                    const float s_hi = w4_float<DT>(
+                        static_cast<uint16_t>(cur.s[1][gg / 2] >> (16 * (gg & 1))));
+                    if (two) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) acc[0][i] += acc2[i];
                     }
@@ -367,15 +484,32 @@ __global__ void __launch_bounds__(W4Cfg<MT>::THREADS, 1) w4_kernel(const __grid_
                         total[j][3] = fmaf(s_hi, acc[j][3], total[j][3]);
                     }
                 }
+                    // the next block's scales move to the front
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                        for (int k = 0; C::BLK > 1 && k < NGB / 2; ++k)
+                            cur.s[i][k] = cur.s[i][k + NGB / 2];
+                        if constexpr (C::BLK > 1 && NGB >= 4) {
+#pragma unroll
+                            for (int k = 0; k < NGB / 4; ++k) cur.z[i][k] = cur.z[i][k + NGB / 4];
+                        } else if constexpr (C::BLK > 1) {
+                            cur.z[i][0] >>= 16;
+                        }
+                    }
+                }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty0 + 8u * stage);
-                if (++stage == C::STAGES) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
             }
-            // [K part][token][row] sums of this CTA
-            float* part = red + kq * MT * C::R_LD;
+            // the next unit's first scales are on their way while this one's sums meet
+            const W4Unit done = w;
+            have = w4_unit<MT>(p, walk, u + nu, lane, w);
+            if (have) {
+                open_unit(w);
+                if (a0 < a1) fetch(a0);
+            }
+            // [stage set][token][row] sums of this CTA
+            float* part = red + sg * MT * C::R_LD;
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 part[(8 * j + 2 * t) * C::R_LD + r] = total[j][0];
@@ -393,9 +527,9 @@ __global__ void __launch_bounds__(W4Cfg<MT>::THREADS, 1) w4_kernel(const __grid_
             // each CTA of the cluster adds and writes its share of the rows
             const int share = C::RT / p.splits;
             if (!*abort_flag) {
-                for (int i = threadIdx.x - 32; i < w.tokens * share; i += 32 * C::WARPS) {
+                for (int i = threadIdx.x - 32; i < done.tokens * share; i += 32 * C::WARPS) {
                     const int tok = i / share, rr = rank * share + i % share;
-                    const int n = w.n0 + rr;
+                    const int n = done.n0 + rr;
                     if (n >= p.N) continue;
                     const float* src = red + tok * C::R_LD + rr;
                     float v = 0.0f;
@@ -403,16 +537,16 @@ __global__ void __launch_bounds__(W4Cfg<MT>::THREADS, 1) w4_kernel(const __grid_
                         for (int k = 0; k < p.splits; ++k) {
                             const uint32_t at = mapa_shared(smem_u32(src), static_cast<uint32_t>(k));
 #pragma unroll
-                            for (int m = 0; m < C::KQ; ++m)
+                            for (int m = 0; m < C::SG; ++m)
                                 v += ld_cluster_f32(at + 4u * m * MT * C::R_LD);
                         }
                     } else {
 #pragma unroll
-                        for (int m = 0; m < C::KQ; ++m) v += src[m * MT * C::R_LD];
+                        for (int m = 0; m < C::SG; ++m) v += src[m * MT * C::R_LD];
                     }
-                    if (p.bias) v += __ldg(p.bias + w.group * p.stride_bias + n);
+                    if (p.bias) v += __ldg(p.bias + done.group * p.stride_bias + n);
                     v = apply_act(v, p.act);
-                    const int64_t off = static_cast<int64_t>(w.row0 + tok) * p.ldc + n;
+                    const int64_t off = static_cast<int64_t>(done.row0 + tok) * p.ldc + n;
 #if DG_DEBUG
                     if (!DG_CHECK(off >= 0 && off < p.dbg_c_elems, p.status, STATUS_CHECK_BOUNDS))
                         continue;
@@ -431,8 +565,8 @@ template <int DT, int MT, int GROUP>
 cudaError_t launch_one(const W4Params& p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.grid) * p.splits);
-    cfg.blockDim = dim3(W4Cfg<MT>::THREADS);
-    cfg.dynamicSmemBytes = W4Cfg<MT>::SMEM;
+    cfg.blockDim = dim3(W4Cfg<MT, GROUP>::THREADS);
+    cfg.dynamicSmemBytes = W4Cfg<MT, GROUP>::SMEM;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -463,7 +597,7 @@ template <int DT, int MT, int GROUP>
 cudaError_t prepare_one() {
     return cudaFuncSetAttribute(w4_kernel<DT, MT, GROUP>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(W4Cfg<MT>::SMEM));
+                                static_cast<int>(W4Cfg<MT, GROUP>::SMEM));
 }
 
 template <int DT, int MT>
@@ -515,7 +649,10 @@ __global__ void __launch_bounds__(256) w4_dequantise_kernel(const uint32_t* q, c
 
 }  // namespace
 
-int w4_rows(int tokens) { return tokens <= 16 ? W4Cfg<8>::RT : W4Cfg<64>::RT; }
+W4Shape w4_shape(int tokens, int group) {
+    if (tokens > 16) return W4Shape{W4Cfg<64, 128>::RT, W4Cfg<64, 128>::BLK};
+    return W4Shape{W4Cfg<16, 128>::RT, group > 32 ? W4Cfg<16, 128>::BLK : W4Cfg<16, 32>::BLK};
+}
 
 cudaError_t w4_launch(int dt, int tokens, const W4Params& p, cudaStream_t stream) {
     return dt == DT_BF16 ? launch_tokens<DT_BF16>(tokens, p, stream)
