@@ -96,10 +96,25 @@ __device__ __forceinline__ void mma16816_first(float (&d)[4], const uint32_t (&a
 // Weights 2 j and 2 j + 1 of word w (w4 = w >> 4) as 16-bit floats minus the pair
 // `sub`: or-ing q into the mantissa of 128 (bf16) or 1024 (fp16), where one unit is
 // the last bit, gives 128 + q (1024 + q) exactly, and sub holds 128 + z (1024 + z).
+struct W4Bits {
+    uint32_t mask, magic;
+};
+
+template <int DT>
+__device__ __forceinline__ W4Bits w4_bits() {
+    W4Bits k;
+    asm volatile("mov.b32 %0, 0x000F000F;" : "=r"(k.mask));
+    asm volatile("mov.b32 %0, %1;" : "=r"(k.magic) : "n"(DT == DT_BF16 ? 0x43004300 : 0x64006400));
+    return k;
+}
+
 template <int DT, int J>
-__device__ __forceinline__ uint32_t w4_pair(uint32_t w, uint32_t w4, uint32_t sub) {
-    constexpr uint32_t magic = DT == DT_BF16 ? 0x43004300u : 0x64006400u;
-    const uint32_t v = (__byte_perm(w, w4, 0x4400 + 0x1111 * J) & 0x000F000Fu) | magic;
+__device__ __forceinline__ uint32_t w4_pair(uint32_t w, uint32_t w4, uint32_t sub, W4Bits k) {
+    // (one three-input operation: mask and magic stay in registers)
+    uint32_t v;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;"
+        : "=r"(v)
+        : "r"(__byte_perm(w, w4, 0x4400 + 0x1111 * J)), "r"(k.mask), "r"(k.magic));
     if constexpr (DT == DT_BF16) {
         const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v),
                                          *reinterpret_cast<const __nv_bfloat162*>(&sub));
@@ -375,6 +390,7 @@ __global__ void __launch_bounds__(W4Cfg<MT, GROUP>::THREADS, 1) w4_kernel(const 
         const int kg = p.K / GROUP;
         // word t of chunk c of row r of a stage: the chunk is swizzled by the row
         const uint32_t q_at = static_cast<uint32_t>(r * 128 + t * 4);
+        const W4Bits bits = w4_bits<DT>();
         bool ok = true;
         uint32_t it0 = 0;  // stages of the units before
         const int n = st1 - st0;
@@ -409,6 +425,10 @@ __global__ void __launch_bounds__(W4Cfg<MT, GROUP>::THREADS, 1) w4_kernel(const 
             for (int j = 0; j < NT; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) total[j][i] = 0.0f;
+            // (one tile of tokens: the lanes of those that do not exist read the first
+            // one's values along with its lane; a column of the product has only its
+            // own token)
+            const int xr = NT > 1 || gr < w.tokens ? gr : 0;
             for (int st = a0; ok && st < a1; ++st) {
                 const int round = st - a0;
                 const uint32_t it = it0 + static_cast<uint32_t>(
@@ -442,22 +462,19 @@ __global__ void __launch_bounds__(W4Cfg<MT, GROUP>::THREADS, 1) w4_kernel(const 
                         const uint32_t lo = *reinterpret_cast<const uint32_t*>(src);
                         const uint32_t hi = *reinterpret_cast<const uint32_t*>(src + 1024);
                         const uint32_t lo4 = lo >> 4, hi4 = hi >> 4;
-                        const uint32_t a1[4] = {w4_pair<DT, 0>(lo, lo4, sub_lo),
-                                                w4_pair<DT, 0>(hi, hi4, sub_hi),
-                                                w4_pair<DT, 1>(lo, lo4, sub_lo),
-                                                w4_pair<DT, 1>(hi, hi4, sub_hi)};
-                        const uint32_t a2[4] = {w4_pair<DT, 2>(lo, lo4, sub_lo),
-                                                w4_pair<DT, 2>(hi, hi4, sub_hi),
-                                                w4_pair<DT, 3>(lo, lo4, sub_lo),
-                                                w4_pair<DT, 3>(hi, hi4, sub_hi)};
-                        const uint8_t* xsrc = xs + (c >> 1) * C::X_BOX + gr * 128 +
-                                              ((((c & 1) * 4 + t) ^ gr) << 4);
+                        const uint32_t a1[4] = {w4_pair<DT, 0>(lo, lo4, sub_lo, bits),
+                                                w4_pair<DT, 0>(hi, hi4, sub_hi, bits),
+                                                w4_pair<DT, 1>(lo, lo4, sub_lo, bits),
+                                                w4_pair<DT, 1>(hi, hi4, sub_hi, bits)};
+                        const uint32_t a2[4] = {w4_pair<DT, 2>(lo, lo4, sub_lo, bits),
+                                                w4_pair<DT, 2>(hi, hi4, sub_hi, bits),
+                                                w4_pair<DT, 3>(lo, lo4, sub_lo, bits),
+                                                w4_pair<DT, 3>(hi, hi4, sub_hi, bits)};
+                        const uint8_t* xsrc = xs + (c >> 1) * C::X_BOX + xr * 128 +
+                                              ((((c & 1) * 4 + t) ^ xr) << 4);
 #pragma unroll
                         for (int j = 0; j < NT; ++j) {
-                            // (one tile: only the lanes of tokens that exist load)
-                            uint4 x = make_uint4(0, 0, 0, 0);
-                            if (NT > 1 || gr < w.tokens)
-                                x = *reinterpret_cast<const uint4*>(xsrc + 1024 * j);
+                            const uint4 x = *reinterpret_cast<const uint4*>(xsrc + 1024 * j);
                             if (cc == 0)
                                 mma16816_first<DT>(acc[j], a1, x.x, x.y);
                             else
