@@ -3,6 +3,7 @@
 #include <stdint.h>
 
 #include <cstring>
+#include <new>
 
 #include "gemm_experts.h"
 #include "internal.h"
@@ -85,21 +86,27 @@ bool c_ok(const void* C, int64_t rows, int64_t cols, int64_t ld, int64_t depth, 
 
 // ---------------------------------------------------------------- the ragged kernel's launches
 
-gemm_status_t rg_run(const RgProblem& q, const DeviceInfo& d, cudaStream_t stream) {
-    RgParams p;
-    std::memset(&p, 0, sizeof(p));
-    // Variant: how many lanes (128 or, in pairs, 256) and columns a tile has.
-    int cg = 2, bt = 256;
+// Lanes (128 per CTA) and columns of a tile: CTA pairs with 256 x 256 tiles where
+// they fill at least half of the GPU, narrower single-CTA tiles for few rows.
+void rg_variant(const RgProblem& q, const DeviceInfo& d, int* cg, int* bt) {
     const int64_t cols = q.form == RG_ROWS && q.offsets ? cdiv(q.T, q.groups) : q.n_col;
+    *cg = 2;
+    *bt = 256;
     if (q.form == RG_ROWS && cols <= 32) {
-        cg = 1, bt = 32;
+        *cg = 1, *bt = 32;
     } else if (cols <= 128 || q.n_lane <= 128) {
-        cg = 1, bt = 128;
+        *cg = 1, *bt = 128;
     } else {
         const int64_t tiles = q.groups * cdiv(q.n_lane, 256) *
                               (q.form == RG_SYM ? (cdiv(cols, 256) + 1) / 2 : cdiv(cols, 256));
-        if (tiles < d.max_pairs / 2) cg = 1, bt = 128;
+        if (tiles < d.max_pairs / 2) *cg = 1, *bt = 128;
     }
+}
+
+gemm_status_t rg_fill(const RgProblem& q, const DeviceInfo& d, int cg, int bt, RgParams* out,
+                      int64_t* tiles) {
+    RgParams& p = *out;
+    std::memset(&p, 0, sizeof(p));
     const int64_t lanes = 128 * cg;
     const int64_t lane_tiles = cdiv(q.n_lane, lanes);
     p.col_tile = bt;
@@ -109,10 +116,26 @@ gemm_status_t rg_run(const RgProblem& q, const DeviceInfo& d, cudaStream_t strea
     } else if (q.form == RG_SYM) {
         total = bound = q.groups * (lane_tiles * (lane_tiles + 1) / 2);
     } else {
-        total = bound = q.groups * lane_tiles * cdiv(q.n_col, bt);
+        if (q.form == RG_ROWS) {
+            // equal groups: the tile width (a multiple of 32) whose waves over the
+            // GPU take the fewest columns, a tile's own cost counted as 24 more
+            const int64_t P = cg == 2 ? d.max_pairs : d.sm_count;
+            const int64_t n0 = cdiv(q.n_col, bt);
+            int64_t best = INT64_MAX;
+            for (int64_t n = n0; n <= 2 * n0; ++n) {
+                const int64_t w = round_up(cdiv(q.n_col, n), 32);
+                const int64_t cost = cdiv(q.groups * lane_tiles * cdiv(q.n_col, w), P) * (w + 24);
+                if (cost < best) {
+                    best = cost;
+                    p.col_tile = static_cast<int32_t>(w);
+                }
+            }
+        }
+        total = bound = q.groups * lane_tiles * cdiv(q.n_col, p.col_tile);
     }
     // (the triangle's index arithmetic takes up to 32767 tile rows)
     if (bound > kLim || (q.form == RG_SYM && lane_tiles > 32767)) return GEMM_ERR_UNSUPPORTED;
+    *tiles = bound;
     p.total_tiles = static_cast<int32_t>(total);
     p.offsets = q.offsets;
     p.groups = static_cast<int32_t>(q.groups);
@@ -165,7 +188,6 @@ gemm_status_t rg_run(const RgProblem& q, const DeviceInfo& d, cudaStream_t strea
     p.bias = q.bias;
     p.stride_bias = q.stride_bias;
     p.act = q.act;
-    p.pdl = q.pdl;
     p.status = d.status;
     p.timeout_ns = option_timeout_ns();
     p.test_stall = take_test_stall();
@@ -174,16 +196,21 @@ gemm_status_t rg_run(const RgProblem& q, const DeviceInfo& d, cudaStream_t strea
     p.dbg_c_elems = (q.offsets && q.form == RG_ROWS ? 0 : (q.groups - 1) * q.stride_c) +
                     (out_rows - 1) * q.ldc + (q.form == RG_SYM ? q.ldc : q.n_lane);
 #endif
+    return GEMM_OK;
+}
+
+gemm_status_t rg_run(const RgProblem& q, const DeviceInfo& d, cudaStream_t stream) {
+    int cg, bt;
+    rg_variant(q, d, &cg, &bt);
+    RgParams p;
+    int64_t tiles = 0;
+    const gemm_status_t st = rg_fill(q, d, cg, bt, &p, &tiles);
+    if (st != GEMM_OK) return st;
     int64_t grid = cg == 2 ? d.max_pairs : d.sm_count;
-    if (bound < grid) grid = bound;
+    if (tiles < grid) grid = tiles;
     const int ctas = static_cast<int>(grid * cg);
-    cudaError_t e;
-    if (q.form == RG_ROWS)
-        e = rg_launch_rows(cg, bt, p, ctas, stream);
-    else if (q.form == RG_WGRAD)
-        e = rg_launch_wgrad(cg, bt, p, ctas, stream);
-    else
-        e = rg_launch_sym(cg, bt, p, ctas, stream);
+    const cudaError_t e = q.form == RG_ROWS ? rg_launch_rows(cg, bt, p, ctas, stream)
+                                            : rg_launch_wgrad(cg, bt, p, ctas, stream);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return GEMM_ERR_CUDA;
@@ -402,7 +429,7 @@ bool ns_layout(int64_t batch, int64_t M, int64_t N, NsLayout* l) {
     l->x_bytes = static_cast<size_t>(round_up(batch * M * l->ldx * 2, 256));
     l->s_bytes = static_cast<size_t>(round_up(batch * l->side * l->lds * 2, 256));
     l->part_bytes = static_cast<size_t>(round_up(batch * parts * 12, 256));
-    l->total = 2 * l->x_bytes + 2 * l->s_bytes + l->part_bytes;
+    l->total = 2 * l->x_bytes + 2 * l->s_bytes + l->part_bytes + 256;
     return true;
 }
 
@@ -458,14 +485,28 @@ gemm_status_t gemm_newton_schulz(gemm_dtype_t g_dtype, int64_t batch, int64_t M,
     n.ldx = l.ldx;
     n.eps = eps;
     n.scale = kNsX;
-    if (ns_norm_launch(n, s) != cudaSuccess || ns_scale_launch(n, s) != cudaSuccess)
-        return GEMM_ERR_CUDA;
-
+    n.arrived = reinterpret_cast<unsigned int*>(P + l.s_bytes + l.part_bytes);
     const bool wide = M <= N;
     const int64_t xs = batch > 1 ? M * l.ldx : 0, ss = batch > 1 ? l.side * l.lds : 0;
-    for (int it = 0; it < steps; ++it) {
-        const void* X = x[it & 1];
-        const bool last = it == steps - 1;
+    int cg = 0, bt = 0;
+    int64_t most = 0;
+    auto add = [&](const RgProblem& q, RgParams* out) {
+        if (cg == 0) {
+            rg_variant(q, d, &cg, &bt);
+            if (bt == 32) bt = 128;  // (the sequence has two shapes)
+        }
+        int64_t tiles = 0;
+        const gemm_status_t e = rg_fill(q, d, cg, bt, out, &tiles);
+        if (tiles > most) most = tiles;
+        return e;
+    };
+    RgSeq* seq = new (std::nothrow) RgSeq;
+    if (!seq) return GEMM_ERR_CUDA;
+    std::memset(seq, 0, sizeof(*seq));
+    seq->steps = steps;
+    seq->arrived = n.arrived;
+    for (int odd = 0; odd < 2 && st == GEMM_OK; ++odd) {
+        const void* X = x[odd];
         // S = X X^T (K-major) or X^T X (MN-major), times kNsS
         RgProblem q{};
         q.form = RG_SYM;
@@ -479,9 +520,7 @@ gemm_status_t gemm_newton_schulz(gemm_dtype_t g_dtype, int64_t batch, int64_t M,
         q.stride_c = q.stride_cin = ss;
         q.c_dtype = q.cin_dtype = DT_F16;
         q.alpha = kNsS / (kNsX * kNsX);
-        q.pdl = true;
-        st = rg_run(q, d, s);
-        if (st != GEMM_OK) return st;
+        st = add(q, &seq->ph[3 * odd]);
         // P = b S + c S S, times kNsS
         q.K = l.side;
         q.a = q.b = RgOperand{S, l.lds, ss, false, l.side, l.side};
@@ -489,8 +528,7 @@ gemm_status_t gemm_newton_schulz(gemm_dtype_t g_dtype, int64_t batch, int64_t M,
         q.Cin = S;
         q.alpha = c / kNsS;
         q.beta = b;
-        st = rg_run(q, d, s);
-        if (st != GEMM_OK) return st;
+        if (st == GEMM_OK) st = add(q, &seq->ph[3 * odd + 1]);
         // X <- a X + P X, or a X + X P
         RgProblem u{};
         u.form = RG_ROWS;
@@ -507,24 +545,32 @@ gemm_status_t gemm_newton_schulz(gemm_dtype_t g_dtype, int64_t batch, int64_t M,
         u.stride_cin = xs;
         u.alpha = 1.0f / kNsS;
         u.beta = a;
-        u.c_dtype = DT_F16;
-        u.C = x[(it + 1) & 1];
+        u.c_dtype = u.cin_dtype = DT_F16;
+        u.C = x[1 - odd];
         u.ldc = l.ldx;
         u.stride_c = xs;
-        u.pdl = true;
-        if (last) {
+        if (st == GEMM_OK) st = add(u, &seq->ph[3 * odd + 2]);
+        if (((steps - 1) & 1) == odd) {
             u.alpha /= kNsX;
             u.beta /= kNsX;
             u.C = O;
             u.ldc = ldo;
             u.stride_c = batch > 1 ? stride_o : 0;
             u.c_dtype = o_dtype;
+            if (st == GEMM_OK) st = add(u, &seq->ph[6]);
         }
-        u.cin_dtype = DT_F16;
-        st = rg_run(u, d, s);
-        if (st != GEMM_OK) return st;
     }
-    return GEMM_OK;
+    if (st == GEMM_OK) {
+        int64_t grid = cg == 2 ? d.max_pairs : d.sm_count;
+        if (most < grid) grid = most;
+        if (ns_norm_launch(n, s) != cudaSuccess || ns_scale_launch(n, s) != cudaSuccess ||
+            rg_launch_seq(cg, bt, *seq, static_cast<int>(grid * cg), s) != cudaSuccess) {
+            cudaGetLastError();
+            st = GEMM_ERR_CUDA;
+        }
+    }
+    delete seq;
+    return st;
 }
 
 // ---------------------------------------------------------------- 4-bit weights

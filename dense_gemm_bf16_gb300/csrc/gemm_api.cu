@@ -101,7 +101,7 @@ gemm_status_t device_state(DevState** out) {
             if (e == cudaSuccess) e = sgemm_prepare();
             if (e == cudaSuccess) e = rg_prepare_rows();
             if (e == cudaSuccess) e = rg_prepare_wgrad();
-            if (e == cudaSuccess) e = rg_prepare_sym();
+            if (e == cudaSuccess) e = rg_prepare_seq();
             if (e == cudaSuccess) e = w4_prepare();
             if (e == cudaSuccess) {
                 d.max_pairs[2][0] = tc_max_pairs(128, 2);

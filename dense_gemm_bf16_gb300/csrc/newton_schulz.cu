@@ -118,6 +118,7 @@ __global__ void __launch_bounds__(kThreads) ns_scale_kernel(const NsParams p) {
             factor = static_cast<float>(p.scale / (sqrt(sq) + static_cast<double>(p.eps)));
         }
     }
+    if (blockIdx.x == 0 && threadIdx.x == 32) *p.arrived = 0u;
     __syncthreads();
     const float f = factor;
     __half* X = static_cast<__half*>(p.X) + b * p.M * p.ldx;

@@ -45,7 +45,6 @@ struct RgParams {
     const float* bias;       // [groups][n_lane] with stride_bias, or null
     int64_t stride_bias;
     int32_t act;
-    int32_t pdl;             // 1: wait for the grid before this one on the stream
     int32_t test_stall;      // test only: leave one stage unfilled
     int* status;
     uint64_t timeout_ns;
@@ -58,10 +57,20 @@ struct RgParams {
 // of a tile at most; lanes are 128 per CTA.
 cudaError_t rg_launch_rows(int cg, int bt, const RgParams& p, int grid, cudaStream_t stream);
 cudaError_t rg_launch_wgrad(int cg, int bt, const RgParams& p, int grid, cudaStream_t stream);
-cudaError_t rg_launch_sym(int cg, int bt, const RgParams& p, int grid, cudaStream_t stream);
 cudaError_t rg_prepare_rows();   // kernel attributes (once per device)
 cudaError_t rg_prepare_wgrad();
-cudaError_t rg_prepare_sym();
+
+// A sequence of products in one cooperative launch, with a barrier over the grid
+// between them: `steps` times the three products of a Newton-Schulz step.  ph[0..2]
+// serve even steps, ph[3..5] odd ones (the state alternates between two buffers),
+// ph[6] is the last step's third product.
+struct RgSeq {
+    RgParams ph[7];
+    int32_t steps;
+    unsigned int* arrived;   // one word, zero at the start: CTAs that finished a product
+};
+cudaError_t rg_launch_seq(int cg, int bt, const RgSeq& q, int grid, cudaStream_t stream);
+cudaError_t rg_prepare_seq();
 
 // ---- host helpers (gemm_api.cu)
 struct DeviceInfo {
@@ -114,8 +123,12 @@ struct RgProblem {
     const float* bias;
     int64_t stride_bias;
     int act;
-    bool pdl;
 };
+// The kernel variant a problem takes (CTAs per tile, columns), its parameters, and
+// a bound on its tiles.
+void rg_variant(const RgProblem& q, const DeviceInfo& d, int* cg, int* bt);
+gemm_status_t rg_fill(const RgProblem& q, const DeviceInfo& d, int cg, int bt, RgParams* p,
+                      int64_t* tiles);
 gemm_status_t rg_run(const RgProblem& q, const DeviceInfo& d, cudaStream_t stream);
 
 // ---- 4-bit weights (w4.cu)
@@ -167,6 +180,7 @@ struct NsParams {
     void* X;                 // fp16, [batch][M][ldx]
     int64_t ldx;
     float eps, scale;
+    unsigned int* arrived;   // zeroed for the sequence that follows
 };
 cudaError_t ns_norm_launch(const NsParams& p, cudaStream_t stream);
 cudaError_t ns_scale_launch(const NsParams& p, cudaStream_t stream);

@@ -260,12 +260,13 @@ __device__ __forceinline__ uint32_t rg_at(int row, int part) {
 // Elements off .. off + 7 of Cin, of which `n` exist (16-bit types).
 __device__ __forceinline__ uint4 rg_load8(const RgParams& p, int64_t off, int n) {
     const char* src = static_cast<const char*>(p.Cin) + off * 2;
-    if (p.c_vec && n >= 8) return *reinterpret_cast<const uint4*>(src);
+    // (through L2: in a sequence of products other SMs wrote Cin in the same launch)
+    if (p.c_vec && n >= 8) return __ldcg(reinterpret_cast<const uint4*>(src));
     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (i < n)
-            w[i >> 1] |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(src + 2 * i))
+            w[i >> 1] |= static_cast<uint32_t>(__ldcg(reinterpret_cast<const uint16_t*>(src + 2 * i)))
                          << (16 * (i & 1));
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -451,49 +452,361 @@ __device__ __forceinline__ void rg_out32(const RgParams& p, const RgTile& w, uin
     }
 }
 
+// What the roles of a CTA share.
+struct RgCta {
+    uint8_t* smem;
+    uint32_t sA0, sB0;
+    uint32_t full0, empty0, tail0, peer_tail0, tfull0, tempty0, drain_bar;
+    uint32_t tmem_base;
+    volatile int* abort_flag;
+    uint32_t rank;   // CTA of the pair
+    bool leader;
+    int cl, ncl;     // this cluster, clusters of the grid
+    int lane;
+};
+
+// Where a role stands in the ring and the accumulators.
+struct RgRole {
+    int stage = 0;
+    uint32_t phase = 0;
+    uint32_t armed = 0;                    // producer: stages filled
+    uint32_t tail_used = 0, tail_odd = 0;  // ... per stage: tails armed; an odd number of them
+    uint32_t tail_phase = 0;               // MMA warp: one bit per stage
+    int abuf = 0;
+    uint32_t aphase = 0;
+    bool issued = false, ok = true;
+};
+
+// ------------------------------------------------ TMA producer (a warp)
 template <int CG, int BT, int FORM>
-__global__ void __launch_bounds__(RgCfg<CG, BT>::THREADS, 1)
-    ragged_kernel(const __grid_constant__ RgParams p) {
+__device__ __forceinline__ void rg_produce(const RgParams& p, const RgCta& x, RgRole& r) {
+    using C = RgCfg<CG, BT>;
+    const uint64_t pol = l2_policy_evict_normal();
+    RgWalk walk{0, 0, 0, 0, 0, false};
+    if (FORM == RG_ROWS && p.offsets) rg_window(p, walk, x.lane);
+    RgTile w;
+    for (int t = x.cl; r.ok && rg_tile<CG, FORM>(p, walk, t, x.lane, x.rank, w); t += x.ncl) {
+        if (x.lane == 0) {
+            const int rows_b = w.n_mma / CG;  // column rows of this CTA
+            const int b_row = w.b_row + static_cast<int>(x.rank) * rows_b;
+            const int za = p.a_z ? w.group : 0, zb = p.b_z ? w.group : 0;
+            const bool a_mn = p.a_mn, b_mn = p.b_mn, a_k4 = p.a_k4, b_k4 = p.b_k4;
+            // K-major columns: whole-tile boxes, or 32-row boxes where those are fewer bytes
+            const bool big = !b_mn && 4 * rows_b > 3 * C::B_ROWS;
+            const int nb = b_mn ? rows_b / 64 : (big ? 1 : (rows_b + 31) / 32);
+            const uint32_t b_bytes = b_mn ? nb * 16384u : (big ? C::B_BYTES : nb * 8192u);
+            const CUtensorMap* map_b = big || b_mn ? &p.tmap_b : &p.tmap_b32;
+            const uint32_t bytes = C::A_BYTES + b_bytes;
+            const int ksteps = (w.klen + 127) / 128;
+            for (int ks = 0; ks < ksteps; ++ks) {
+                if (!mbar_wait(x.empty0 + 8u * r.stage, r.phase ^ 1u, x.abort_flag, p.status, p.timeout_ns)) {
+                    r.ok = false;
+                    break;
+                }
+                if (p.test_stall == 1 && r.armed == 0) {
+                    r.ok = false;  // test only: the MMA warp's bounded wait must expire
+                    break;
+                }
+                const uint32_t fb = x.full0 + 8u * r.stage;
+                // a ragged tail lands on each CTA's own barrier, for the zeroing
+                const bool tail = FORM == RG_WGRAD && ks == ksteps - 1 && (w.klen & 15) != 0;
+                uint32_t bar;
+                if (tail) {
+                    mbar_arrive_expect_tx(x.tail0 + 8u * r.stage, bytes);
+                    if (x.leader) mbar_arrive(fb);
+                    bar = x.tail0 + 8u * r.stage;
+                    r.tail_used |= 1u << r.stage;
+                    r.tail_odd ^= 1u << r.stage;
+                } else {
+                    if (x.leader) mbar_arrive_expect_tx(fb, CG * bytes);
+                    bar = CG == 1 || x.leader ? fb : mapa_shared(fb, 0u);
+                }
+                auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y, int z) {
+                    if constexpr (CG == 2)
+                        tma_load_3d_pair(dst, map, bar, x, y, z, pol);
+                    else
+                        tma_load_3d(dst, map, bar, x, y, z, pol);
+                };
+                const uint32_t a_dst = x.sA0 + r.stage * C::A_BYTES;
+                const uint32_t b_dst = x.sB0 + r.stage * C::B_BYTES;
+                const int k = w.k0 + ks * 128;
+                // K-major: the second block's rows follow the first's; MN-major:
+                // 64-wide atom columns of 128 K rows (16 KB)
+                if (a_k4) {
+                    tma_load_4d_cg<CG>(a_dst, &p.tmap_a, bar, 0, w.lane0, 2 * ks, za, pol);
+                } else if (a_mn) {
+                    load(a_dst, &p.tmap_a, w.lane0, k, za);
+                    load(a_dst + 16384u, &p.tmap_a, w.lane0 + 64, k, za);
+                } else {
+                    load(a_dst, &p.tmap_a, k, w.lane0, za);
+                    load(a_dst + 16384u, &p.tmap_a, k + 64, w.lane0, za);
+                }
+                if (b_mn) {
+                    for (int h = 0; h < nb; ++h)
+                        load(b_dst + 16384u * h, map_b, b_row + 64 * h, k, zb);
+                } else if (big) {
+                    if (b_k4) {
+                        tma_load_4d_cg<CG>(b_dst, map_b, bar, 0, b_row, 2 * ks, zb, pol);
+                    } else {
+                        load(b_dst, map_b, k, b_row, zb);
+                        load(b_dst + C::B_BYTES / 2, map_b, k + 64, b_row, zb);
+                    }
+                } else {
+                    // (32-row boxes one block at a time: the blocks lie B_BYTES / 2 apart)
+                    for (int h = 0; h < nb; ++h) {
+                        load(b_dst + 4096u * h, map_b, k, b_row + 32 * h, zb);
+                        load(b_dst + C::B_BYTES / 2 + 4096u * h, map_b, k + 64, b_row + 32 * h, zb);
+                    }
+                }
+                ++r.armed;
+                if (++r.stage == C::STAGES) {
+                    r.stage = 0;
+                    r.phase ^= 1u;
+                }
+            }
+        }
+        r.ok = __shfl_sync(0xffffffffu, r.ok ? 1 : 0, 0) != 0;
+    }
+}
+
+// Every issued copy lands before the CTA exits.  A pair's peer completes its
+// copies on the leader's barriers: after a normal run the leader has consumed
+// them before the final cluster barrier; after an abort the peer gives them a
+// fixed time.
+template <int CG, int BT>
+__device__ __forceinline__ void rg_produce_end(const RgParams& p, const RgCta& x, const RgRole& r) {
+    using C = RgCfg<CG, BT>;
+    if (x.lane != 0) return;
+    for (int s = 0; s < C::STAGES; ++s)
+        if (r.tail_used >> s & 1u)  // an odd count: its last phase has parity 0
+            rg_drain(x.tail0 + 8u * s, (r.tail_odd >> s & 1u) ^ 1u, p.timeout_ns);
+    if (CG == 2 && !x.leader) {
+        if (!r.ok) {
+            const uint64_t t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < 200000ull) {
+            }
+        }
+    } else {
+        for (int s = 0; s < C::STAGES && static_cast<uint32_t>(s) < r.armed; ++s) {
+            const uint32_t fills = (r.armed - 1u - s) / C::STAGES + 1u;
+            rg_drain(x.full0 + 8u * s, (fills - 1u) & 1u, p.timeout_ns);
+        }
+    }
+}
+
+// ------------------------------------------------ MMA issuer (a warp)
+// The pair's peer walks the same tiles for the tails only.
+template <int CG, int BT, int FORM>
+__device__ __forceinline__ void rg_issue(const RgParams& p, const RgCta& x, RgRole& r) {
     using C = RgCfg<CG, BT>;
     constexpr uint16_t kPair = 3u;
-    const uint32_t rank = CG > 1 ? cluster_ctarank() : 0u;
-    const bool leader = rank == 0;
-    const int cl = static_cast<int>(blockIdx.x) / CG;
-    const int ncl = static_cast<int>(gridDim.x) / CG;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    const uint32_t sA0 = smem_u32(smem);
-    const uint32_t sB0 = sA0 + C::STAGES * C::A_BYTES;
-    uint8_t* epi_smem = smem + C::STAGES * C::STAGE_BYTES;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(epi_smem + C::EPI_SMEM);
+    const bool a_mn = p.a_mn != 0, b_mn = p.b_mn != 0;
+    // descriptors of stage 0; a stage or K = 16 step adds to their address fields
+    // (in 16 bytes; K-major: 32 bytes a step inside a block, MN-major: 16 rows)
+    const uint64_t a_desc0 = smem_desc_sw128(x.sA0, a_mn ? 16384u : 16u, 1024u);
+    const uint64_t b_desc0 = smem_desc_sw128(x.sB0, b_mn ? 16384u : 16u, 1024u);
+    const uint32_t a_step = a_mn ? 128u : 2u, b_step = b_mn ? 128u : 2u;
+    const uint32_t a_block = a_mn ? 512u : C::A_BYTES >> 5, b_block = b_mn ? 512u : C::B_BYTES >> 5;
+    const bool issuer = CG == 1 || x.leader;
+    RgWalk walk{0, 0, 0, 0, 0, false};
+    if (FORM == RG_ROWS && p.offsets) rg_window(p, walk, x.lane);
+    RgTile w;
+    for (int t = x.cl; r.ok && rg_tile<CG, FORM>(p, walk, t, x.lane, x.rank, w); t += x.ncl) {
+        const int ksteps = (w.klen + 127) / 128;
+        if (ksteps == 0) continue;  // no rows: the epilogue writes zeros
+        if (!issuer && FORM != RG_WGRAD) continue;
+        const bool tail = FORM == RG_WGRAD && (w.klen & 15) != 0;
+        const int whole = ksteps - (tail ? 1 : 0);  // stages the MMA reads as they are
+        const uint32_t d_tmem = x.tmem_base + static_cast<uint32_t>(r.abuf * BT);
+        const uint32_t idesc = p.idesc | (static_cast<uint32_t>(w.n_mma >> 3) << 17);
+        auto issue = [&](int ks, int steps) {
+            const uint64_t ad = a_desc0 + static_cast<uint32_t>(r.stage) * (C::A_BYTES >> 4);
+            const uint64_t bd = b_desc0 + static_cast<uint32_t>(r.stage) * (C::B_BYTES >> 4);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k < steps)
+                    umma_f16_cg<CG>(d_tmem, ad + (k >> 2) * a_block + (k & 3) * a_step,
+                                    bd + (k >> 2) * b_block + (k & 3) * b_step, idesc,
+                                    (ks > 0 || k > 0) ? 1u : 0u);
+            if constexpr (CG > 1)
+                umma_commit_mc_cg<CG>(x.empty0 + 8u * r.stage, kPair);
+            else
+                umma_commit_cg<CG>(x.empty0 + 8u * r.stage);
+            if (ks == ksteps - 1) {
+                if constexpr (CG > 1)
+                    umma_commit_mc_cg<CG>(x.tfull0 + 8u * r.abuf, kPair);
+                else
+                    umma_commit_cg<CG>(x.tfull0 + 8u * r.abuf);
+            }
+        };
+        if (!issuer) {
+            r.stage += whole;  // (the peer only counts them)
+            while (r.stage >= C::STAGES) r.stage -= C::STAGES;
+        } else {
+            if (x.lane == 0) {
+                r.ok = mbar_wait(x.tempty0 + 8u * r.abuf, r.aphase ^ 1u, x.abort_flag, p.status, p.timeout_ns);
+                if (r.ok) tc_fence_after_sync();
+                for (int ks = 0; r.ok && ks < whole; ++ks) {
+                    r.ok = mbar_wait(x.full0 + 8u * r.stage, r.phase, x.abort_flag, p.status, p.timeout_ns);
+                    if (!r.ok) break;
+                    tc_fence_after_sync();
+                    const int left = w.klen - ks * 128;
+                    issue(ks, left >= 128 ? 8 : (left + 15) / 16);
+                    r.issued = true;
+                    if (++r.stage == C::STAGES) {
+                        r.stage = 0;
+                        r.phase ^= 1u;
+                    }
+                }
+            }
+            __syncwarp();
+            if (FORM == RG_WGRAD) {
+                r.ok = __shfl_sync(0xffffffffu, r.ok ? 1 : 0, 0) != 0;
+                r.stage = __shfl_sync(0xffffffffu, r.stage, 0);
+                r.phase = __shfl_sync(0xffffffffu, r.phase, 0);
+                if (!r.ok) break;
+            }
+        }
+        if (FORM == RG_WGRAD && tail) {
+            if (!rg_warp_wait(x.tail0 + 8u * r.stage, r.tail_phase >> r.stage & 1u, x.lane, x.abort_flag, p)) {
+                r.ok = false;
+                break;
+            }
+            __syncwarp();
+            // rows klen % 128 .. up to the end of the last K = 16 step: one row is
+            // 128 bytes of every 64-wide atom column (whole rows, so the swizzle
+            // inside them does not matter)
+            const int v = w.klen - whole * 128;
+            const int nz = ((v + 15) & ~15) - v;
+            const int acols = 2 + w.n_mma / CG / 64;
+            for (int i = x.lane; i < acols * nz * 8; i += 32) {
+                const int chunk = i & 7, row = v + (i >> 3) % nz, col = (i >> 3) / nz;
+                const uint32_t base =
+                    col < 2 ? r.stage * C::A_BYTES + col * 16384u
+                            : C::STAGES * C::A_BYTES + r.stage * C::B_BYTES + (col - 2) * 16384u;
+                *reinterpret_cast<uint4*>(x.smem + base + row * 128 + chunk * 16) =
+                    make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (!issuer) {
+                if (x.lane == 0) mbar_arrive_remote(mapa_shared(x.peer_tail0 + 8u * r.stage, 0u));
+            } else {
+                if (!rg_warp_wait(x.full0 + 8u * r.stage, r.phase, x.lane, x.abort_flag, p) ||
+                    (CG == 2 && !rg_warp_wait(x.peer_tail0 + 8u * r.stage, r.tail_phase >> r.stage & 1u,
+                                              x.lane, x.abort_flag, p))) {
+                    r.ok = false;
+                    break;
+                }
+                fence_proxy_async_smem();
+                tc_fence_after_sync();
+                if (x.lane == 0) issue(whole, (v + 15) / 16);
+                r.issued = true;
+            }
+            r.tail_phase ^= 1u << r.stage;
+            if (++r.stage == C::STAGES) {
+                r.stage = 0;
+                r.phase ^= 1u;
+            }
+        }
+        if (++r.abuf == 2) {
+            r.abuf = 0;
+            r.aphase ^= 1u;
+        }
+        r.ok = __shfl_sync(0xffffffffu, r.ok ? 1 : 0, 0) != 0;
+    }
+}
+
+// All MMAs complete before tensor memory is released.
+template <int CG>
+__device__ __forceinline__ void rg_issue_end(const RgParams& p, const RgCta& x, const RgRole& r) {
+    if (r.issued && x.lane == 0) {
+        umma_commit_cg<CG>(x.drain_bar);
+        rg_drain(x.drain_bar, 0u, p.timeout_ns);
+    }
+    __syncwarp();
+}
+
+// ------------------------------------------------ epilogue (a warp of eight)
+template <int CG, int BT, int FORM>
+__device__ __forceinline__ void rg_epilogue(const RgParams& p, const RgCta& x, RgRole& r, int warp,
+                                            uint8_t* buf) {
+    // (r.ok goes false, and stays so, when a wait gave up)
+    const int q = warp & 3;            // tensor-memory lane quarter of this warp
+    const int half = (warp - 2) >> 2;  // which 32-column chunks it takes
+    const uint32_t lane_field = static_cast<uint32_t>(q * 32) << 16;
+    RgWalk walk{0, 0, 0, 0, 0, false};
+    if (FORM == RG_ROWS && p.offsets) rg_window(p, walk, x.lane);
+    RgTile w;
+    for (int t = x.cl; rg_tile<CG, FORM>(p, walk, t, x.lane, x.rank, w); t += x.ncl) {
+        const bool empty = w.klen == 0;
+        const int nl0 = w.lane0 + q * 32;  // first output column of this warp
+        if (!empty) {
+            r.ok = rg_warp_wait(x.tfull0 + 8u * r.abuf, r.aphase, x.lane, x.abort_flag, p);
+            if (!r.ok) break;
+            tc_fence_after_sync();
+        }
+        const uint32_t tmem_row = x.tmem_base + lane_field + static_cast<uint32_t>(r.abuf * BT);
+        // the accumulator goes back to the MMA warp as soon as it is in registers
+        auto release = [&]() {
+            if (empty) return;
+            tc_fence_before_sync();
+            __syncwarp();
+            if (x.lane == 0)
+                mbar_arrive_relaxed(mapa_shared(x.tempty0 + 8u * r.abuf, 0u));
+        };
+        if (p.c_dtype == DT_F32)
+            rg_out32(p, w, tmem_row, nl0, half, x.lane, empty, release);
+        else
+            rg_out16<FORM>(p, w, tmem_row, nl0, half, x.lane, buf, empty, release);
+        if (!empty && ++r.abuf == 2) {
+            r.abuf = 0;
+            r.aphase ^= 1u;
+        }
+    }
+    __syncwarp();
+}
+
+// Barriers, tensor memory and the CTA's view of them (all threads).
+template <int CG, int BT>
+__device__ __forceinline__ RgCta rg_setup(const RgParams& p, uint8_t* smem_raw) {
+    using C = RgCfg<CG, BT>;
+    RgCta x;
+    x.rank = CG > 1 ? cluster_ctarank() : 0u;
+    x.leader = x.rank == 0;
+    x.cl = static_cast<int>(blockIdx.x) / CG;
+    x.ncl = static_cast<int>(gridDim.x) / CG;
+    x.lane = threadIdx.x & 31;
+    x.smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                        ~static_cast<uintptr_t>(1023));
+    x.sA0 = smem_u32(x.smem);
+    x.sB0 = x.sA0 + C::STAGES * C::A_BYTES;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(x.smem + C::STAGES * C::STAGE_BYTES + C::EPI_SMEM);
     // full[STAGES], empty[STAGES], tail[STAGES], peer_tail[STAGES], tmem_full[2],
     // tmem_empty[2], drain
-    const uint32_t full0 = smem_u32(bars);
-    const uint32_t empty0 = full0 + 8u * C::STAGES;
-    const uint32_t tail0 = full0 + 16u * C::STAGES;
-    const uint32_t peer_tail0 = full0 + 24u * C::STAGES;
-    const uint32_t tfull0 = full0 + 32u * C::STAGES;
-    const uint32_t tempty0 = tfull0 + 16u;
-    const uint32_t drain_bar = tempty0 + 16u;
+    x.full0 = smem_u32(bars);
+    x.empty0 = x.full0 + 8u * C::STAGES;
+    x.tail0 = x.full0 + 16u * C::STAGES;
+    x.peer_tail0 = x.full0 + 24u * C::STAGES;
+    x.tfull0 = x.full0 + 32u * C::STAGES;
+    x.tempty0 = x.tfull0 + 16u;
+    x.drain_bar = x.tempty0 + 16u;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 4 * C::STAGES + 5);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    x.abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5;
-    const int lane = threadIdx.x & 31;
-
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(full0 + 8u * s, 1);
-            mbar_init(empty0 + 8u * s, 1);
-            mbar_init(tail0 + 8u * s, 1);
-            mbar_init(peer_tail0 + 8u * s, 1);
+            mbar_init(x.full0 + 8u * s, 1);
+            mbar_init(x.empty0 + 8u * s, 1);
+            mbar_init(x.tail0 + 8u * s, 1);
+            mbar_init(x.peer_tail0 + 8u * s, 1);
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(tfull0 + 8u * b, 1);
-            mbar_init(tempty0 + 8u * b, CG * C::EPI_WARPS);
+            mbar_init(x.tfull0 + 8u * b, 1);
+            mbar_init(x.tempty0 + 8u * b, CG * C::EPI_WARPS);
         }
-        mbar_init(drain_bar, 1);
-        *abort_flag = 0;
+        mbar_init(x.drain_bar, 1);
+        *x.abort_flag = 0;
         fence_mbar_init();
         if (p.maps) {
             prefetch_tmap(&p.tmap_a);
@@ -511,294 +824,40 @@ __global__ void __launch_bounds__(RgCfg<CG, BT>::THREADS, 1)
     else
         __syncthreads();
     tc_fence_after_sync();
-    const uint32_t tmem_base = *tmem_slot;
-    if (p.pdl) {
-        griddep_launch_dependents();
-        griddep_wait();
-        fence_proxy_async_global();  // the previous grid's plain stores, read by TMA below
-    }
+    x.tmem_base = *tmem_slot;
+    return x;
+}
 
-    RgWalk walk{0, 0, 0, 0, 0, false};
-    if (FORM == RG_ROWS && p.offsets) rg_window(p, walk, lane);
-    RgTile w;
-
-    if (warp == 0) {
-        // ------------------------------------------------ TMA producer
-        const uint64_t pol = l2_policy_evict_normal();
-        int stage = 0;
-        uint32_t phase = 0, armed = 0;
-        uint32_t tail_used = 0, tail_odd = 0;  // per stage: tails armed; an odd number of them
-        bool ok = true;
-        for (int t = cl; ok && rg_tile<CG, FORM>(p, walk, t, lane, rank, w); t += ncl) {
-            if (lane == 0) {
-                const int rows_b = w.n_mma / CG;  // column rows of this CTA
-                const int b_row = w.b_row + static_cast<int>(rank) * rows_b;
-                const int za = p.a_z ? w.group : 0, zb = p.b_z ? w.group : 0;
-                const bool a_mn = p.a_mn, b_mn = p.b_mn, a_k4 = p.a_k4, b_k4 = p.b_k4;
-                // K-major columns: whole-tile boxes, or 32-row boxes where those are fewer bytes
-                const bool big = !b_mn && 4 * rows_b > 3 * C::B_ROWS;
-                const int nb = b_mn ? rows_b / 64 : (big ? 1 : (rows_b + 31) / 32);
-                const uint32_t b_bytes = b_mn ? nb * 16384u : (big ? C::B_BYTES : nb * 8192u);
-                const CUtensorMap* map_b = big || b_mn ? &p.tmap_b : &p.tmap_b32;
-                const uint32_t bytes = C::A_BYTES + b_bytes;
-                const int ksteps = (w.klen + 127) / 128;
-                for (int ks = 0; ks < ksteps; ++ks) {
-                    if (!mbar_wait(empty0 + 8u * stage, phase ^ 1u, abort_flag, p.status, p.timeout_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    if (p.test_stall == 1 && armed == 0) {
-                        ok = false;  // test only: the MMA warp's bounded wait must expire
-                        break;
-                    }
-                    const uint32_t fb = full0 + 8u * stage;
-                    // a ragged tail lands on each CTA's own barrier, for the zeroing
-                    const bool tail = FORM == RG_WGRAD && ks == ksteps - 1 && (w.klen & 15) != 0;
-                    uint32_t bar;
-                    if (tail) {
-                        mbar_arrive_expect_tx(tail0 + 8u * stage, bytes);
-                        if (leader) mbar_arrive(fb);
-                        bar = tail0 + 8u * stage;
-                        tail_used |= 1u << stage;
-                        tail_odd ^= 1u << stage;
-                    } else {
-                        if (leader) mbar_arrive_expect_tx(fb, CG * bytes);
-                        bar = CG == 1 || leader ? fb : mapa_shared(fb, 0u);
-                    }
-                    auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y, int z) {
-                        if constexpr (CG == 2)
-                            tma_load_3d_pair(dst, map, bar, x, y, z, pol);
-                        else
-                            tma_load_3d(dst, map, bar, x, y, z, pol);
-                    };
-                    const uint32_t a_dst = sA0 + stage * C::A_BYTES;
-                    const uint32_t b_dst = sB0 + stage * C::B_BYTES;
-                    const int k = w.k0 + ks * 128;
-                    // K-major: the second block's rows follow the first's; MN-major:
-                    // 64-wide atom columns of 128 K rows (16 KB)
-                    if (a_k4) {
-                        tma_load_4d_cg<CG>(a_dst, &p.tmap_a, bar, 0, w.lane0, 2 * ks, za, pol);
-                    } else if (a_mn) {
-                        load(a_dst, &p.tmap_a, w.lane0, k, za);
-                        load(a_dst + 16384u, &p.tmap_a, w.lane0 + 64, k, za);
-                    } else {
-                        load(a_dst, &p.tmap_a, k, w.lane0, za);
-                        load(a_dst + 16384u, &p.tmap_a, k + 64, w.lane0, za);
-                    }
-                    if (b_mn) {
-                        for (int h = 0; h < nb; ++h)
-                            load(b_dst + 16384u * h, map_b, b_row + 64 * h, k, zb);
-                    } else if (big) {
-                        if (b_k4) {
-                            tma_load_4d_cg<CG>(b_dst, map_b, bar, 0, b_row, 2 * ks, zb, pol);
-                        } else {
-                            load(b_dst, map_b, k, b_row, zb);
-                            load(b_dst + C::B_BYTES / 2, map_b, k + 64, b_row, zb);
-                        }
-                    } else {
-                        // (32-row boxes one block at a time: the blocks lie B_BYTES / 2 apart)
-                        for (int h = 0; h < nb; ++h) {
-                            load(b_dst + 4096u * h, map_b, k, b_row + 32 * h, zb);
-                            load(b_dst + C::B_BYTES / 2 + 4096u * h, map_b, k + 64, b_row + 32 * h, zb);
-                        }
-                    }
-                    ++armed;
-                    if (++stage == C::STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                }
-            }
-            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-        }
-        // Every issued copy lands before the CTA exits.  A pair's peer completes
-        // its copies on the leader's barriers: after a normal run the leader has
-        // consumed them before the final cluster barrier; after an abort the
-        // peer gives them a fixed time.
-        if (lane == 0) {
-            for (int s = 0; s < C::STAGES; ++s)
-                if (tail_used >> s & 1u)  // an odd count: its last phase has parity 0
-                    rg_drain(tail0 + 8u * s, (tail_odd >> s & 1u) ^ 1u, p.timeout_ns);
-            if (CG == 2 && !leader) {
-                if (!ok) {
-                    const uint64_t t0 = globaltimer_ns();
-                    while (globaltimer_ns() - t0 < 200000ull) {
-                    }
-                }
-            } else {
-                for (int s = 0; s < C::STAGES && static_cast<uint32_t>(s) < armed; ++s) {
-                    const uint32_t fills = (armed - 1u - s) / C::STAGES + 1u;
-                    rg_drain(full0 + 8u * s, (fills - 1u) & 1u, p.timeout_ns);
-                }
-            }
-        }
-    } else if (warp == 1) {
-        // ------------------------------------------------ MMA issuer
-        // (the pair's peer walks the same tiles for the tails only)
-        int stage = 0;
-        uint32_t phase = 0, tail_phase = 0;  // tail_phase: one bit per stage
-        int abuf = 0;
-        uint32_t aphase = 0;
-        bool issued = false, ok = true;
-        const bool a_mn = p.a_mn != 0, b_mn = p.b_mn != 0;
-        // descriptors of stage 0; a stage or K = 16 step adds to their address fields
-        // (in 16 bytes; K-major: 32 bytes a step inside a block, MN-major: 16 rows)
-        const uint64_t a_desc0 = smem_desc_sw128(sA0, a_mn ? 16384u : 16u, 1024u);
-        const uint64_t b_desc0 = smem_desc_sw128(sB0, b_mn ? 16384u : 16u, 1024u);
-        const uint32_t a_step = a_mn ? 128u : 2u, b_step = b_mn ? 128u : 2u;
-        const uint32_t a_block = a_mn ? 512u : C::A_BYTES >> 5, b_block = b_mn ? 512u : C::B_BYTES >> 5;
-        const bool issuer = CG == 1 || leader;
-        for (int t = cl; ok && rg_tile<CG, FORM>(p, walk, t, lane, rank, w); t += ncl) {
-            const int ksteps = (w.klen + 127) / 128;
-            if (ksteps == 0) continue;  // no rows: the epilogue writes zeros
-            if (!issuer && FORM != RG_WGRAD) continue;
-            const bool tail = FORM == RG_WGRAD && (w.klen & 15) != 0;
-            const int whole = ksteps - (tail ? 1 : 0);  // stages the MMA reads as they are
-            const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(abuf * BT);
-            const uint32_t idesc = p.idesc | (static_cast<uint32_t>(w.n_mma >> 3) << 17);
-            auto issue = [&](int ks, int steps) {
-                const uint64_t ad = a_desc0 + static_cast<uint32_t>(stage) * (C::A_BYTES >> 4);
-                const uint64_t bd = b_desc0 + static_cast<uint32_t>(stage) * (C::B_BYTES >> 4);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (k < steps)
-                        umma_f16_cg<CG>(d_tmem, ad + (k >> 2) * a_block + (k & 3) * a_step,
-                                        bd + (k >> 2) * b_block + (k & 3) * b_step, idesc,
-                                        (ks > 0 || k > 0) ? 1u : 0u);
-                if constexpr (CG > 1)
-                    umma_commit_mc_cg<CG>(empty0 + 8u * stage, kPair);
-                else
-                    umma_commit_cg<CG>(empty0 + 8u * stage);
-                if (ks == ksteps - 1) {
-                    if constexpr (CG > 1)
-                        umma_commit_mc_cg<CG>(tfull0 + 8u * abuf, kPair);
-                    else
-                        umma_commit_cg<CG>(tfull0 + 8u * abuf);
-                }
-            };
-            if (!issuer) {
-                stage += whole;  // (the peer only counts them)
-                while (stage >= C::STAGES) stage -= C::STAGES;
-            } else {
-                if (lane == 0) {
-                    ok = mbar_wait(tempty0 + 8u * abuf, aphase ^ 1u, abort_flag, p.status, p.timeout_ns);
-                    if (ok) tc_fence_after_sync();
-                    for (int ks = 0; ok && ks < whole; ++ks) {
-                        ok = mbar_wait(full0 + 8u * stage, phase, abort_flag, p.status, p.timeout_ns);
-                        if (!ok) break;
-                        tc_fence_after_sync();
-                        const int left = w.klen - ks * 128;
-                        issue(ks, left >= 128 ? 8 : (left + 15) / 16);
-                        issued = true;
-                        if (++stage == C::STAGES) {
-                            stage = 0;
-                            phase ^= 1u;
-                        }
-                    }
-                }
-                __syncwarp();
-                if (FORM == RG_WGRAD) {
-                    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-                    stage = __shfl_sync(0xffffffffu, stage, 0);
-                    phase = __shfl_sync(0xffffffffu, phase, 0);
-                    if (!ok) break;
-                }
-            }
-            if (FORM == RG_WGRAD && tail) {
-                if (!rg_warp_wait(tail0 + 8u * stage, tail_phase >> stage & 1u, lane, abort_flag, p)) {
-                    ok = false;
-                    break;
-                }
-                __syncwarp();
-                // rows klen % 128 .. up to the end of the last K = 16 step: one row is
-                // 128 bytes of every 64-wide atom column (whole rows, so the swizzle
-                // inside them does not matter)
-                const int v = w.klen - whole * 128;
-                const int nz = ((v + 15) & ~15) - v;
-                const int acols = 2 + w.n_mma / CG / 64;
-                for (int i = lane; i < acols * nz * 8; i += 32) {
-                    const int chunk = i & 7, r = v + (i >> 3) % nz, col = (i >> 3) / nz;
-                    const uint32_t base =
-                        col < 2 ? stage * C::A_BYTES + col * 16384u
-                                : C::STAGES * C::A_BYTES + stage * C::B_BYTES + (col - 2) * 16384u;
-                    *reinterpret_cast<uint4*>(smem + base + r * 128 + chunk * 16) =
-                        make_uint4(0, 0, 0, 0);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (!issuer) {
-                    if (lane == 0) mbar_arrive_remote(mapa_shared(peer_tail0 + 8u * stage, 0u));
-                } else {
-                    if (!rg_warp_wait(full0 + 8u * stage, phase, lane, abort_flag, p) ||
-                        (CG == 2 && !rg_warp_wait(peer_tail0 + 8u * stage, tail_phase >> stage & 1u,
-                                                  lane, abort_flag, p))) {
-                        ok = false;
-                        break;
-                    }
-                    fence_proxy_async_smem();
-                    tc_fence_after_sync();
-                    if (lane == 0) issue(whole, (v + 15) / 16);
-                    issued = true;
-                }
-                tail_phase ^= 1u << stage;
-                if (++stage == C::STAGES) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
-            }
-            if (++abuf == 2) {
-                abuf = 0;
-                aphase ^= 1u;
-            }
-            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-        }
-        if (issued && lane == 0) {
-            umma_commit_cg<CG>(drain_bar);
-            rg_drain(drain_bar, 0u, p.timeout_ns);
-        }
-        __syncwarp();
-    } else {
-        // ------------------------------------------------ epilogue
-        const int q = warp & 3;           // tensor-memory lane quarter of this warp
-        const int half = (warp - 2) >> 2; // which 32-column chunks it takes
-        const uint32_t lane_field = static_cast<uint32_t>(q * 32) << 16;
-        uint8_t* buf = epi_smem + (warp - 2) * C::EPI_WARP;
-        int abuf = 0;
-        uint32_t aphase = 0;
-        for (int t = cl; rg_tile<CG, FORM>(p, walk, t, lane, rank, w); t += ncl) {
-            const bool empty = w.klen == 0;
-            const int nl0 = w.lane0 + q * 32;  // first output column of this warp
-            if (!empty) {
-                if (!rg_warp_wait(tfull0 + 8u * abuf, aphase, lane, abort_flag, p)) break;
-                tc_fence_after_sync();
-            }
-            const uint32_t tmem_row = tmem_base + lane_field + static_cast<uint32_t>(abuf * BT);
-            // the accumulator goes back to the MMA warp as soon as it is in registers
-            auto release = [&]() {
-                if (empty) return;
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive_relaxed(mapa_shared(tempty0 + 8u * abuf, 0u));
-            };
-            if (p.c_dtype == DT_F32)
-                rg_out32(p, w, tmem_row, nl0, half, lane, empty, release);
-            else
-                rg_out16<FORM>(p, w, tmem_row, nl0, half, lane, buf, empty, release);
-            if (!empty && ++abuf == 2) {
-                abuf = 0;
-                aphase ^= 1u;
-            }
-        }
-        __syncwarp();
-    }
+template <int CG, int BT>
+__device__ __forceinline__ void rg_teardown(const RgCta& x) {
     tc_fence_before_sync();
     __syncthreads();
     if constexpr (CG > 1) cluster_sync();
-    if (warp == 1) {
+    if ((threadIdx.x >> 5) == 1) {
         tc_fence_after_sync();
-        tmem_dealloc_cg<CG>(tmem_base, C::TMEM_COLS);
+        tmem_dealloc_cg<CG>(x.tmem_base, RgCfg<CG, BT>::TMEM_COLS);
     }
+}
+
+template <int CG, int BT, int FORM>
+__global__ void __launch_bounds__(RgCfg<CG, BT>::THREADS, 1)
+    ragged_kernel(const __grid_constant__ RgParams p) {
+    using C = RgCfg<CG, BT>;
+    extern __shared__ uint8_t smem_raw[];
+    const RgCta x = rg_setup<CG, BT>(p, smem_raw);
+    const int warp = threadIdx.x >> 5;
+    RgRole r;
+    if (warp == 0) {
+        rg_produce<CG, BT, FORM>(p, x, r);
+        rg_produce_end<CG, BT>(p, x, r);
+    } else if (warp == 1) {
+        rg_issue<CG, BT, FORM>(p, x, r);
+        rg_issue_end<CG>(p, x, r);
+    } else {
+        rg_epilogue<CG, BT, FORM>(p, x, r, warp,
+                                  x.smem + C::STAGES * C::STAGE_BYTES + (warp - 2) * C::EPI_WARP);
+    }
+    rg_teardown<CG, BT>(x);
 }
 
 template <int CG, int BT, int FORM>
@@ -808,18 +867,13 @@ cudaError_t rg_launch(const RgParams& p, int grid, cudaStream_t stream) {
     cfg.blockDim = dim3(RgCfg<CG, BT>::THREADS);
     cfg.dynamicSmemBytes = RgCfg<CG, BT>::SMEM;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
     unsigned n = 0;
     if (CG > 1) {
         attr[n].id = cudaLaunchAttributeClusterDimension;
         attr[n].val.clusterDim.x = CG;
         attr[n].val.clusterDim.y = 1;
         attr[n].val.clusterDim.z = 1;
-        ++n;
-    }
-    if (p.pdl) {
-        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[n].val.programmaticStreamSerializationAllowed = 1;
         ++n;
     }
     cfg.attrs = attr;
