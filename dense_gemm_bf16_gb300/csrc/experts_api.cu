@@ -86,6 +86,17 @@ bool c_ok(const void* C, int64_t rows, int64_t cols, int64_t ld, int64_t depth, 
 
 // ---------------------------------------------------------------- the ragged kernel's launches
 
+// With l = ceil(log2 d) and m = floor(2^(31 + l) / d) + 1, n m / 2^(31 + l) exceeds
+// n / d by less than n / 2^(31 + l) < 1 / d, so its integer part is n / d.
+static RgDiv make_div(int64_t d) {
+    if (d < 1) d = 1;
+    uint32_t l = 0;
+    while ((int64_t(1) << l) < d) ++l;
+    if (l == 0) return RgDiv{0u, 0u};  // (division by 1)
+    const uint64_t m = (uint64_t(1) << (31 + l)) / static_cast<uint64_t>(d) + 1;
+    return RgDiv{static_cast<uint32_t>(m), l - 1};
+}
+
 // Lanes (128 per CTA) and columns of a tile: CTA pairs with 256 x 256 tiles where
 // they fill at least half of the GPU, narrower single-CTA tiles for few rows.
 void rg_variant(const RgProblem& q, const DeviceInfo& d, int* cg, int* bt) {
@@ -137,6 +148,10 @@ gemm_status_t rg_fill(const RgProblem& q, const DeviceInfo& d, int cg, int bt, R
     if (bound > kLim || (q.form == RG_SYM && lane_tiles > 32767)) return GEMM_ERR_UNSUPPORTED;
     *tiles = bound;
     p.total_tiles = static_cast<int32_t>(total);
+    p.per_group = static_cast<int32_t>(q.groups > 0 ? total / q.groups : 0);
+    p.chunks = static_cast<int32_t>(lane_tiles > 0 ? p.per_group / lane_tiles : 0);
+    p.div_group = make_div(p.per_group);
+    p.div_band = make_div(RG_BAND * lane_tiles);
     p.offsets = q.offsets;
     p.groups = static_cast<int32_t>(q.groups);
     p.rows = static_cast<int32_t>(q.T);

@@ -91,6 +91,28 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
     }
 }
 
+// mbar_wait for short waits on a critical path: the timer, whose read takes about
+// as long as a poll, is first read after 64 polls.
+__device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity,
+                                                volatile int* abort_flag, int* status,
+                                                uint64_t timeout_ns) {
+    uint64_t t0 = 0;
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 63u) == 0) {
+            if (*abort_flag) return false;
+            const uint64_t now = globaltimer_ns();
+            if (t0 == 0) {
+                t0 = now;
+            } else if (now - t0 > timeout_ns) {
+                *abort_flag = 1;
+                if (status) DG_SET_TIMEOUT(status);
+                return false;
+            }
+        }
+    }
+}
+
 // ---------------------------------------------------------------- TMA
 
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap* m) {

@@ -15,6 +15,12 @@ namespace dg {
 
 // What a tile of the ragged kernel is (see ragged_kernel.cuh).
 enum : int { RG_ROWS = 0, RG_WGRAD = 1, RG_SYM = 2 };
+constexpr int RG_BAND = 8;  // column tiles of a band (see rg_band)
+
+// n / d for 0 <= n < 2^31 as one multiplication (d fixed at the launch).
+struct RgDiv {
+    uint32_t m, s;
+};
 
 // Output D[col][lane]: the lane operand's rows are the output's contiguous
 // dimension, the column operand's rows its rows.
@@ -31,6 +37,10 @@ struct RgParams {
     int32_t lane_tiles;      // ceil(n_lane / lanes of a tile)
     int32_t col_tile;        // columns of a tile at most (a multiple of 32)
     int32_t total_tiles;     // equal groups and RG_WGRAD; else 0 (found on the device)
+    int32_t per_group;       // ... of one group
+    int32_t chunks;          // ... column tiles of one group
+    RgDiv div_group;         // by per_group
+    RgDiv div_band;          // by RG_BAND * lane_tiles
     int32_t a_mn, b_mn;      // 1: operand stored with its rows contiguous (MN-major)
     int32_t a_k4, b_k4;      // 1: K-major map is (64 K, rows, K blocks, z): two blocks a load
     int32_t a_z, b_z;        // 1: the operand's z coordinate is the group

@@ -73,7 +73,7 @@ struct RgCfg {
     static constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE_BYTES + EPI_SMEM + BAR_BYTES;
     static_assert(BT % 32 == 0 && BT <= 256 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "tile width");
     static_assert(CG == 1 || BT == 256, "pairs take 256-column tiles (two 64-wide atoms per CTA)");
-    static_assert((4 * STAGES + 5) * 8 + 8 <= BAR_BYTES, "barrier area too small");
+    static_assert((4 * STAGES + 6) * 8 + 8 <= BAR_BYTES, "barrier area too small");
 };
 
 struct RgTile {
@@ -129,18 +129,57 @@ __device__ __forceinline__ void rg_window(const RgParams& p, RgWalk& w, int lane
 // the chunks of one lane tile after another, so that the tiles in flight at
 // once (76 pairs) share few operand panels (16384 x 4096 x 8192 in one group:
 // 643 us against 759 us with all 64 chunks in one band).
-constexpr int RG_BAND = 8;
-__device__ __forceinline__ void rg_band(int r, int chunks, int lane_tiles, int& lt, int& c) {
-    const int band = r / (RG_BAND * lane_tiles);
-    const int c0 = band * RG_BAND;
-    const int width = chunks - c0 < RG_BAND ? chunks - c0 : RG_BAND;
-    const int in = r - c0 * lane_tiles;
-    lt = in / width;
-    c = c0 + in - lt * width;
+__device__ __forceinline__ int rg_div(int n, RgDiv d) {
+    return d.m == 0u ? n : static_cast<int>(__umulhi(static_cast<uint32_t>(n), d.m) >> d.s);
+}
+__device__ __forceinline__ void rg_band(const RgParams& p, int r, int chunks, int& lt, int& c) {
+    const int c0 = rg_div(r, p.div_band) * RG_BAND;
+    const int in = r - c0 * p.lane_tiles;
+    if (chunks - c0 >= RG_BAND) {
+        lt = in / RG_BAND;
+        c = c0 + in % RG_BAND;
+    } else {
+        lt = in / (chunks - c0);
+        c = c0 + in - lt * (chunks - c0);
+    }
+}
+
+// RG_WGRAD takes the 32 groups of a window by descending row counts (w.incl: this
+// lane's place), so that the tiles dealt last are the short ones: 16 groups of
+// unequal size took 267 us in their own order and WGSORT by size.
+__device__ __forceinline__ void rg_sort(const RgParams& p, RgWalk& w, int lane) {
+    const int g = w.base + lane;
+    int lo = 0, hi = 0;
+    if (g < p.groups && p.offsets) {  // (no offsets: alpha == 0 or no rows)
+        lo = __ldg(p.offsets + g);
+        hi = __ldg(p.offsets + g + 1);
+    }
+    if (lo < 0 || hi < lo || hi > p.rows) {
+        if (p.status) atomicOr(p.status, STATUS_BAD_OFFSETS);
+        lo = hi = 0;
+    }
+    w.row0 = lo;
+    w.rows = hi - lo;
+    const int key = g < p.groups ? w.rows : -1;
+    int place = 0;
+#pragma unroll 8
+    for (int j = 0; j < 32; ++j) {
+        const int k = __shfl_sync(0xffffffffu, key, j);
+        place += (k > key || (k == key && j < lane)) ? 1 : 0;
+    }
+    w.incl = place;
+}
+
+template <int FORM>
+__device__ __forceinline__ RgWalk rg_begin(const RgParams& p, int lane) {
+    RgWalk w{0, 0, 0, 0, 0, false};
+    if (FORM == RG_ROWS && p.offsets) rg_window(p, w, lane);
+    if (FORM == RG_WGRAD) rg_sort(p, w, lane);
+    return w;
 }
 
 // Tile t of the problem, by a whole (converged) warp; false past the last one.
-template <int CG, int FORM>
+template <int CG, int BT, int FORM>
 __device__ __forceinline__ bool rg_tile(const RgParams& p, RgWalk& w, int t, int lane,
                                         uint32_t rank, RgTile& o) {
     constexpr int LANES = 128 * CG;
@@ -162,10 +201,10 @@ __device__ __forceinline__ bool rg_tile(const RgParams& p, RgWalk& w, int t, int
         const int rows = __shfl_sync(0xffffffffu, w.rows, l);
         const int row0 = __shfl_sync(0xffffffffu, w.row0, l);
         const int incl = __shfl_sync(0xffffffffu, w.incl, l);
-        const int chunks = (rows + p.col_tile - 1) / p.col_tile;
+        const int chunks = (rows + BT - 1) / BT;  // (col_tile is BT here)
         const int r = t - w.before - (incl - chunks * p.lane_tiles);
         int lt, c;
-        rg_band(r, chunks, p.lane_tiles, lt, c);
+        rg_band(p, r, chunks, lt, c);
         const int width = ((rows + chunks - 1) / chunks + GRAN - 1) / GRAN * GRAN;
         o.group = w.base + l;
         o.lane0 = lt * LANES + static_cast<int>(rank) * 128;
@@ -174,9 +213,8 @@ __device__ __forceinline__ bool rg_tile(const RgParams& p, RgWalk& w, int t, int
         o.b_row = o.out_row = row0 + o.col0;
     } else {
         if (t >= p.total_tiles) return false;
-        const int per_group = p.total_tiles / p.groups;
-        o.group = t / per_group;
-        const int r = t - o.group * per_group;
+        o.group = rg_div(t, p.div_group);
+        const int r = t - o.group * p.per_group;
         if (FORM == RG_SYM) {
             int i = static_cast<int>((sqrtf(8.0f * static_cast<float>(r) + 1.0f) - 1.0f) * 0.5f);
             while (i * (i + 1) / 2 > r) --i;
@@ -186,26 +224,22 @@ __device__ __forceinline__ bool rg_tile(const RgParams& p, RgWalk& w, int t, int
             o.lane0 = i * LANES + static_cast<int>(rank) * 128;
             o.col0 = j * p.col_tile;
         } else {
-            const int chunks = per_group / p.lane_tiles;
             int lt, c;
-            rg_band(r, chunks, p.lane_tiles, lt, c);
+            rg_band(p, r, p.chunks, lt, c);
             o.lane0 = lt * LANES + static_cast<int>(rank) * 128;
             o.col0 = c * p.col_tile;
         }
         o.ncols = p.n_col - o.col0 < p.col_tile ? p.n_col - o.col0 : p.col_tile;
         o.b_row = o.out_row = o.col0;
         if (FORM == RG_WGRAD) {
-            int lo = 0, hi = 0;
-            if (p.offsets) {  // (none: alpha == 0 or no rows)
-                lo = __ldg(p.offsets + o.group);
-                hi = __ldg(p.offsets + o.group + 1);
-                if (lo < 0 || hi < lo || hi > p.rows) {
-                    if (lane == 0 && p.status) atomicOr(p.status, STATUS_BAD_OFFSETS);
-                    lo = hi = 0;
-                }
+            while (o.group >= w.base + 32) {
+                w.base += 32;
+                rg_sort(p, w, lane);
             }
-            o.k0 = lo;
-            o.klen = hi - lo;
+            const int l = __ffs(__ballot_sync(0xffffffffu, w.incl == o.group - w.base)) - 1;
+            o.group = w.base + l;
+            o.k0 = __shfl_sync(0xffffffffu, w.row0, l);
+            o.klen = __shfl_sync(0xffffffffu, w.rows, l);
         }
     }
     // MN-major columns come in 64-wide swizzle atoms per CTA
@@ -218,7 +252,7 @@ __device__ __forceinline__ bool rg_tile(const RgParams& p, RgWalk& w, int t, int
 __device__ __forceinline__ bool rg_warp_wait(uint32_t bar, uint32_t parity, int lane,
                                              volatile int* abort_flag, const RgParams& p) {
     int ok = 1;
-    if (lane == 0) ok = mbar_wait(bar, parity, abort_flag, p.status, p.timeout_ns) ? 1 : 0;
+    if (lane == 0) ok = mbar_wait_short(bar, parity, abort_flag, p.status, p.timeout_ns) ? 1 : 0;
     return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
@@ -257,11 +291,9 @@ __device__ __forceinline__ uint32_t rg_at(int row, int part) {
     return static_cast<uint32_t>(row * 64 + ((part ^ ((row >> 1) & 3)) << 4));
 }
 
-// Elements off .. off + 7 of Cin, of which `n` exist (16-bit types).
-__device__ __forceinline__ uint4 rg_load8(const RgParams& p, int64_t off, int n) {
-    const char* src = static_cast<const char*>(p.Cin) + off * 2;
-    // (through L2: in a sequence of products other SMs wrote Cin in the same launch)
-    if (p.c_vec && n >= 8) return __ldcg(reinterpret_cast<const uint4*>(src));
+// Eight 16-bit elements of which `n` exist, one at a time (out of line, so that
+// the epilogue's common path stays short in the instruction cache).
+__device__ __noinline__ uint4 rg_load8_slow(const char* src, int n) {
     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -271,13 +303,7 @@ __device__ __forceinline__ uint4 rg_load8(const RgParams& p, int64_t off, int n)
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ void rg_store8(const RgParams& p, int64_t off, int n, uint4 v) {
-    if (!rg_span_ok(p, off, n < 8 ? n : 8)) return;
-    char* dst = static_cast<char*>(p.C) + off * 2;
-    if (p.c_vec && n >= 8) {
-        *reinterpret_cast<uint4*>(dst) = v;
-        return;
-    }
+__device__ __noinline__ void rg_store8_slow(char* dst, int n, uint4 v) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -286,19 +312,73 @@ __device__ __forceinline__ void rg_store8(const RgParams& p, int64_t off, int n,
                 static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
 }
 
+__device__ __noinline__ float rg_gelu_erf(float x) { return gelu_erf(x); }
+
+// The activation over 32 values.
+__device__ __forceinline__ void rg_act(float (&v)[32], int act) {
+    if (act == ACT_GELU_TANH) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = gelu_tanh(v[i]);
+    } else if (act == ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = relu(v[i]);
+    } else if (act == ACT_GELU_ERF) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = rg_gelu_erf(v[i]);
+    }
+}
+
+// Elements off .. off + 7 of Cin, of which `n` exist (16-bit types); through L2: in
+// a sequence of products other SMs wrote Cin in the same launch.
+__device__ __forceinline__ uint4 rg_load8(const RgParams& p, int64_t off, int n) {
+    const char* src = static_cast<const char*>(p.Cin) + off * 2;
+    if (p.c_vec && n >= 8) return __ldcg(reinterpret_cast<const uint4*>(src));
+    return rg_load8_slow(src, n);
+}
+
+__device__ __forceinline__ void rg_store8(const RgParams& p, int64_t off, int n, uint4 v) {
+    if (!rg_span_ok(p, off, n < 8 ? n : 8)) return;
+    char* dst = static_cast<char*>(p.C) + off * 2;
+    if (p.c_vec && n >= 8)
+        *reinterpret_cast<uint4*>(dst) = v;
+    else
+        rg_store8_slow(dst, n, v);
+}
+
+// A chunk's accumulators (two 16-lane loads of 32 columns) to values:
+// [16-lane half][8-column block][2 lanes x 2 columns], bias by lane.
+__device__ __forceinline__ void rg_values(const RgParams& p, const uint32_t (&r)[32],
+                                          const float (&bias)[4], float (&v)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        v[i] = fmaf(p.alpha, __uint_as_float(r[i]), bias[(i >> 4) * 2 + ((i >> 1) & 1)]);
+}
+
+// Values to packed 16-bit pairs, pk[column block][8-lane part].
+__device__ __forceinline__ void rg_pack16(int dt, const float (&v)[32], uint32_t (&pk)[4][4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const float* x = v + 16 * (m >> 1) + 4 * i + 2 * (m & 1);
+            pk[i][m] = rg_pack(dt, x[0], x[1]);
+        }
+}
+
 // Epilogue of a warp's 32 lanes (output columns nl0 ..) of tile w for a 16-bit
-// C: the 32-column chunks half, half + 2, ...; `release` runs once the
-// accumulator has been read.
-template <int FORM, typename Release>
+// C: the 32-column chunks half, half + 2, ...  `ready` waits for the accumulator
+// (false: gave up); `release` runs once it has been read.
+template <int FORM, bool ACT, typename Ready, typename Release>
 __device__ __forceinline__ void rg_out16(const RgParams& p, const RgTile& w, uint32_t tmem_row,
                                          int nl0, int half, int lane, uint8_t* buf, bool empty,
-                                         Release release) {
+                                         Ready ready, Release release) {
     const int64_t c_base = w.group * p.stride_c + nl0;
     const int64_t in_base = w.group * p.stride_cin + nl0;
     const bool beta = p.beta != 0.0f;
     const int pcol = lane >> 2, part = lane & 3;  // this lane's 16 bytes of a staged tile
     const int nn = p.n_lane - nl0 - 8 * part;     // of which this many columns exist
     const uint32_t s_out = smem_u32(buf), s_in = s_out + 2048u;
+    const uint32_t mat = rg_at(lane & 7, lane >> 3);  // this lane's row of a transposed store
     float bias[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -315,34 +395,77 @@ __device__ __forceinline__ void rg_out16(const RgParams& p, const RgTile& w, uin
                           : make_uint4(0, 0, 0, 0);
         }
     };
-    uint32_t r[32];
-    auto load_acc = [&](int c0) {
-        tmem_ld_16x256_x4(tmem_row + static_cast<uint32_t>(c0), r, 0);
-        tmem_ld_16x256_x4(tmem_row + (16u << 16) + static_cast<uint32_t>(c0), r, 1);
-    };
-    const int first = half * 32;
-    if (first >= w.ncols || nl0 >= p.n_lane) {
-        release();
-        return;
-    }
-    if (beta) load_in(first);
-#pragma unroll 1
-    for (int c0 = first; c0 < w.ncols; c0 += 64) {
+    auto load_acc = [&](int c0, uint32_t (&r)[32]) {
         if (empty) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) r[i] = 0u;
         } else {
-            load_acc(c0);
-            tmem_ld_wait(r);
+            tmem_ld_16x256_x4(tmem_row + static_cast<uint32_t>(c0), r, 0);
+            tmem_ld_16x256_x4(tmem_row + (16u << 16) + static_cast<uint32_t>(c0), r, 1);
         }
-        float v[32];  // as the accumulator: [16-lane half][8-column block][2 lanes x 2 columns]
+    };
+    // a staged tile's four 16-byte parts of this lane, to rows c0 .. of C
+    auto store_tile = [&](int c0, uint32_t tile) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            v[i] = fmaf(p.alpha, __uint_as_float(r[i]), bias[(i >> 4) * 2 + ((i >> 1) & 1)]);
-        const bool more = c0 + 64 < w.ncols;
-        if (!more && !empty) release();
-        if (beta) {
+        for (int it = 0; it < 4; ++it) {
+            const int c = c0 + 8 * it + pcol;
+            if (c < w.ncols && nn > 0)
+                rg_store8(p, c_base + (w.out_row + c) * p.ldc + 8 * part, nn,
+                          *reinterpret_cast<const uint4*>(buf + tile + rg_at(8 * it + pcol, part)));
+        }
+    };
+    const int first = half * 32;
+    if (first >= w.ncols || nl0 >= p.n_lane) {
+        if (ready()) release();
+        return;
+    }
+    if (FORM != RG_SYM && !beta) {
+        // two chunks at a time, one in each staged tile
+        if (!ready()) return;
+#pragma unroll 1
+        for (int c0 = first; c0 < w.ncols; c0 += 128) {
+            const bool two = c0 + 64 < w.ncols;
+            uint32_t r0[32], r1[32], pk[4][4];
+            float v[32];
+            load_acc(c0, r0);
+            if (two) load_acc(c0 + 64, r1);
+            if (!empty) tmem_ld_wait2(r0, r1);
+            if (c0 + 128 >= w.ncols) release();
+            __syncwarp();  // the previous chunks have left the staged tiles
+            rg_values(p, r0, bias, v);
+            if (ACT) rg_act(v, p.act);
+            rg_pack16(p.c_dtype, v, pk);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                stmatrix_x4_trans(s_out + mat + 512u * i, pk[i][0], pk[i][1], pk[i][2], pk[i][3]);
+            if (two) {
+                rg_values(p, r1, bias, v);
+                if (ACT) rg_act(v, p.act);
+                rg_pack16(p.c_dtype, v, pk);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    stmatrix_x4_trans(s_in + mat + 512u * i, pk[i][0], pk[i][1], pk[i][2],
+                                      pk[i][3]);
+            }
             __syncwarp();
+            store_tile(c0, 0u);
+            if (two) store_tile(c0 + 64, 2048u);
+        }
+        return;
+    }
+    if (beta) load_in(first);
+    if (!ready()) return;
+#pragma unroll 1
+    for (int c0 = first; c0 < w.ncols; c0 += 64) {
+        uint32_t r[32], pk[4][4];
+        float v[32];
+        load_acc(c0, r);
+        if (!empty) tmem_ld_wait(r);
+        const bool more = c0 + 64 < w.ncols;
+        if (!more) release();
+        rg_values(p, r, bias, v);
+        __syncwarp();  // the previous chunk has left the staged tiles
+        if (beta) {
 #pragma unroll
             for (int it = 0; it < 4; ++it)
                 *reinterpret_cast<uint4*>(buf + 2048 + rg_at(8 * it + pcol, part)) = cin[it];
@@ -351,7 +474,7 @@ __device__ __forceinline__ void rg_out16(const RgParams& p, const RgTile& w, uin
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 uint32_t u[4];
-                ldmatrix_x4_trans(s_in + rg_at(8 * i + (lane & 7), lane >> 3), u[0], u[1], u[2], u[3]);
+                ldmatrix_x4_trans(s_in + mat + 512u * i, u[0], u[1], u[2], u[3]);
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
                     const float2 f = rg_unpack(p.cin_dtype, u[m]);
@@ -360,47 +483,38 @@ __device__ __forceinline__ void rg_out16(const RgParams& p, const RgTile& w, uin
                     x[1] = fmaf(p.beta, f.y, x[1]);
                 }
             }
+            if (FORM == RG_SYM) __syncwarp();  // (the mirrored tile takes Cin's place)
         }
-        act_inplace<32>(v, p.act);
-        uint32_t pk[4][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const float* x = v + 16 * (m >> 1) + 4 * i + 2 * (m & 1);
-                pk[i][m] = rg_pack(p.c_dtype, x[0], x[1]);
-            }
-        __syncwarp();  // the previous chunk has left the staged tiles
+        if (ACT) rg_act(v, p.act);
+        rg_pack16(p.c_dtype, v, pk);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            stmatrix_x4_trans(s_out + rg_at(8 * i + (lane & 7), lane >> 3), pk[i][0], pk[i][1],
-                              pk[i][2], pk[i][3]);
+            stmatrix_x4_trans(s_out + mat + 512u * i, pk[i][0], pk[i][1], pk[i][2], pk[i][3]);
             // the mirrored tile: lanes as rows (an off-diagonal tile's columns all exist)
             if (FORM == RG_SYM && !w.diag)
                 stmatrix_x4(s_in + rg_at(lane, i), pk[i][0], pk[i][1], pk[i][2], pk[i][3]);
         }
         __syncwarp();
+        store_tile(c0, 0u);
+        if (FORM == RG_SYM && !w.diag) {
 #pragma unroll
-        for (int it = 0; it < 4; ++it) {
-            const int c = c0 + 8 * it + pcol;
-            const uint32_t at = rg_at(8 * it + pcol, part);
-            if (c < w.ncols && nn > 0)
-                rg_store8(p, c_base + (w.out_row + c) * p.ldc + 8 * part, nn,
-                          *reinterpret_cast<const uint4*>(buf + at));
-            if (FORM == RG_SYM && !w.diag && nl0 + 8 * it + pcol < p.n_lane)
-                rg_store8(p, w.group * p.stride_c + (nl0 + 8 * it + pcol) * p.ldc + w.col0 + c0 +
-                                 8 * part,
-                          8, *reinterpret_cast<const uint4*>(buf + 2048 + at));
+            for (int it = 0; it < 4; ++it)
+                if (nl0 + 8 * it + pcol < p.n_lane)
+                    rg_store8(p, w.group * p.stride_c + (nl0 + 8 * it + pcol) * p.ldc + w.col0 +
+                                     c0 + 8 * part,
+                              8, *reinterpret_cast<const uint4*>(buf + 2048 +
+                                                                 rg_at(8 * it + pcol, part)));
         }
     }
 }
 
 // The same for an fp32 C: one lane (output column) per thread, stores of 32
 // neighbouring columns of one row.
-template <typename Release>
+template <bool ACT, typename Ready, typename Release>
 __device__ __forceinline__ void rg_out32(const RgParams& p, const RgTile& w, uint32_t tmem_row,
-                                         int nl0, int half, int lane, bool empty,
+                                         int nl0, int half, int lane, bool empty, Ready ready,
                                          Release release) {
+    if (!ready()) return;
     const int n = nl0 + lane;
     const int first = half * 32;
     if (first >= w.ncols || nl0 >= p.n_lane) {
@@ -435,7 +549,7 @@ __device__ __forceinline__ void rg_out32(const RgParams& p, const RgTile& w, uin
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = fmaf(p.beta, f[i], v[i]);
         }
-        act_inplace<32>(v, p.act);
+        if (ACT) rg_act(v, p.act);
         if (!in) continue;
         const int64_t off = w.group * p.stride_c + row * p.ldc + n;
         float* dst = static_cast<float*>(p.C) + off;
@@ -456,7 +570,7 @@ __device__ __forceinline__ void rg_out32(const RgParams& p, const RgTile& w, uin
 struct RgCta {
     uint8_t* smem;
     uint32_t sA0, sB0;
-    uint32_t full0, empty0, tail0, peer_tail0, tfull0, tempty0, drain_bar;
+    uint32_t full0, empty0, tail0, peer_tail0, tfull0, tempty0, drain_bar, gate_bar;
     uint32_t tmem_base;
     volatile int* abort_flag;
     uint32_t rank;   // CTA of the pair
@@ -478,14 +592,14 @@ struct RgRole {
 };
 
 // ------------------------------------------------ TMA producer (a warp)
-template <int CG, int BT, int FORM>
-__device__ __forceinline__ void rg_produce(const RgParams& p, const RgCta& x, RgRole& r) {
+// `gate` runs before the first load (false: gave up), once the first tile is known.
+template <int CG, int BT, int FORM, typename Gate>
+__device__ __forceinline__ void rg_produce(const RgParams& p, const RgCta& x, RgRole& r, Gate gate) {
     using C = RgCfg<CG, BT>;
     const uint64_t pol = l2_policy_evict_normal();
-    RgWalk walk{0, 0, 0, 0, 0, false};
-    if (FORM == RG_ROWS && p.offsets) rg_window(p, walk, x.lane);
+    RgWalk walk = rg_begin<FORM>(p, x.lane);
     RgTile w;
-    for (int t = x.cl; r.ok && rg_tile<CG, FORM>(p, walk, t, x.lane, x.rank, w); t += x.ncl) {
+    for (int t = x.cl; r.ok && rg_tile<CG, BT, FORM>(p, walk, t, x.lane, x.rank, w); t += x.ncl) {
         if (x.lane == 0) {
             const int rows_b = w.n_mma / CG;  // column rows of this CTA
             const int b_row = w.b_row + static_cast<int>(x.rank) * rows_b;
@@ -498,8 +612,9 @@ __device__ __forceinline__ void rg_produce(const RgParams& p, const RgCta& x, Rg
             const CUtensorMap* map_b = big || b_mn ? &p.tmap_b : &p.tmap_b32;
             const uint32_t bytes = C::A_BYTES + b_bytes;
             const int ksteps = (w.klen + 127) / 128;
-            for (int ks = 0; ks < ksteps; ++ks) {
-                if (!mbar_wait(x.empty0 + 8u * r.stage, r.phase ^ 1u, x.abort_flag, p.status, p.timeout_ns)) {
+            if (t == x.cl && !gate()) r.ok = false;
+            for (int ks = 0; r.ok && ks < ksteps; ++ks) {
+                if (!mbar_wait_short(x.empty0 + 8u * r.stage, r.phase ^ 1u, x.abort_flag, p.status, p.timeout_ns)) {
                     r.ok = false;
                     break;
                 }
@@ -608,10 +723,9 @@ __device__ __forceinline__ void rg_issue(const RgParams& p, const RgCta& x, RgRo
     const uint32_t a_step = a_mn ? 128u : 2u, b_step = b_mn ? 128u : 2u;
     const uint32_t a_block = a_mn ? 512u : C::A_BYTES >> 5, b_block = b_mn ? 512u : C::B_BYTES >> 5;
     const bool issuer = CG == 1 || x.leader;
-    RgWalk walk{0, 0, 0, 0, 0, false};
-    if (FORM == RG_ROWS && p.offsets) rg_window(p, walk, x.lane);
+    RgWalk walk = rg_begin<FORM>(p, x.lane);
     RgTile w;
-    for (int t = x.cl; r.ok && rg_tile<CG, FORM>(p, walk, t, x.lane, x.rank, w); t += x.ncl) {
+    for (int t = x.cl; r.ok && rg_tile<CG, BT, FORM>(p, walk, t, x.lane, x.rank, w); t += x.ncl) {
         const int ksteps = (w.klen + 127) / 128;
         if (ksteps == 0) continue;  // no rows: the epilogue writes zeros
         if (!issuer && FORM != RG_WGRAD) continue;
@@ -644,10 +758,10 @@ __device__ __forceinline__ void rg_issue(const RgParams& p, const RgCta& x, RgRo
             while (r.stage >= C::STAGES) r.stage -= C::STAGES;
         } else {
             if (x.lane == 0) {
-                r.ok = mbar_wait(x.tempty0 + 8u * r.abuf, r.aphase ^ 1u, x.abort_flag, p.status, p.timeout_ns);
+                r.ok = mbar_wait_short(x.tempty0 + 8u * r.abuf, r.aphase ^ 1u, x.abort_flag, p.status, p.timeout_ns);
                 if (r.ok) tc_fence_after_sync();
                 for (int ks = 0; r.ok && ks < whole; ++ks) {
-                    r.ok = mbar_wait(x.full0 + 8u * r.stage, r.phase, x.abort_flag, p.status, p.timeout_ns);
+                    r.ok = mbar_wait_short(x.full0 + 8u * r.stage, r.phase, x.abort_flag, p.status, p.timeout_ns);
                     if (!r.ok) break;
                     tc_fence_after_sync();
                     const int left = w.klen - ks * 128;
@@ -728,24 +842,28 @@ __device__ __forceinline__ void rg_issue_end(const RgParams& p, const RgCta& x, 
 }
 
 // ------------------------------------------------ epilogue (a warp of eight)
-template <int CG, int BT, int FORM>
+template <int CG, int BT, int FORM, bool ACT, typename Gate>
 __device__ __forceinline__ void rg_epilogue(const RgParams& p, const RgCta& x, RgRole& r, int warp,
-                                            uint8_t* buf) {
-    // (r.ok goes false, and stays so, when a wait gave up)
+                                            uint8_t* buf, Gate gate) {
+    // (gate: before the first tile's Cin is read; r.ok goes false, and stays so, when a wait gave up)
     const int q = warp & 3;            // tensor-memory lane quarter of this warp
     const int half = (warp - 2) >> 2;  // which 32-column chunks it takes
     const uint32_t lane_field = static_cast<uint32_t>(q * 32) << 16;
-    RgWalk walk{0, 0, 0, 0, 0, false};
-    if (FORM == RG_ROWS && p.offsets) rg_window(p, walk, x.lane);
+    RgWalk walk = rg_begin<FORM>(p, x.lane);
     RgTile w;
-    for (int t = x.cl; rg_tile<CG, FORM>(p, walk, t, x.lane, x.rank, w); t += x.ncl) {
+    for (int t = x.cl; rg_tile<CG, BT, FORM>(p, walk, t, x.lane, x.rank, w); t += x.ncl) {
+        if (t == x.cl && !gate()) {
+            r.ok = false;
+            break;
+        }
         const bool empty = w.klen == 0;
         const int nl0 = w.lane0 + q * 32;  // first output column of this warp
-        if (!empty) {
+        auto ready = [&]() {
+            if (empty) return true;
             r.ok = rg_warp_wait(x.tfull0 + 8u * r.abuf, r.aphase, x.lane, x.abort_flag, p);
-            if (!r.ok) break;
             tc_fence_after_sync();
-        }
+            return r.ok;
+        };
         const uint32_t tmem_row = x.tmem_base + lane_field + static_cast<uint32_t>(r.abuf * BT);
         // the accumulator goes back to the MMA warp as soon as it is in registers
         auto release = [&]() {
@@ -756,9 +874,10 @@ __device__ __forceinline__ void rg_epilogue(const RgParams& p, const RgCta& x, R
                 mbar_arrive_relaxed(mapa_shared(x.tempty0 + 8u * r.abuf, 0u));
         };
         if (p.c_dtype == DT_F32)
-            rg_out32(p, w, tmem_row, nl0, half, x.lane, empty, release);
+            rg_out32<ACT>(p, w, tmem_row, nl0, half, x.lane, empty, ready, release);
         else
-            rg_out16<FORM>(p, w, tmem_row, nl0, half, x.lane, buf, empty, release);
+            rg_out16<FORM, ACT>(p, w, tmem_row, nl0, half, x.lane, buf, empty, ready, release);
+        if (!r.ok) break;
         if (!empty && ++r.abuf == 2) {
             r.abuf = 0;
             r.aphase ^= 1u;
@@ -783,7 +902,7 @@ __device__ __forceinline__ RgCta rg_setup(const RgParams& p, uint8_t* smem_raw) 
     x.sB0 = x.sA0 + C::STAGES * C::A_BYTES;
     uint64_t* bars = reinterpret_cast<uint64_t*>(x.smem + C::STAGES * C::STAGE_BYTES + C::EPI_SMEM);
     // full[STAGES], empty[STAGES], tail[STAGES], peer_tail[STAGES], tmem_full[2],
-    // tmem_empty[2], drain
+    // tmem_empty[2], drain, gate
     x.full0 = smem_u32(bars);
     x.empty0 = x.full0 + 8u * C::STAGES;
     x.tail0 = x.full0 + 16u * C::STAGES;
@@ -791,7 +910,8 @@ __device__ __forceinline__ RgCta rg_setup(const RgParams& p, uint8_t* smem_raw) 
     x.tfull0 = x.full0 + 32u * C::STAGES;
     x.tempty0 = x.tfull0 + 16u;
     x.drain_bar = x.tempty0 + 16u;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 4 * C::STAGES + 5);
+    x.gate_bar = x.drain_bar + 8u;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 4 * C::STAGES + 6);
     x.abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
@@ -806,6 +926,7 @@ __device__ __forceinline__ RgCta rg_setup(const RgParams& p, uint8_t* smem_raw) 
             mbar_init(x.tempty0 + 8u * b, CG * C::EPI_WARPS);
         }
         mbar_init(x.drain_bar, 1);
+        mbar_init(x.gate_bar, 1);  // a sequence's producer has seen the product before
         *x.abort_flag = 0;
         fence_mbar_init();
         if (p.maps) {
@@ -848,14 +969,15 @@ __global__ void __launch_bounds__(RgCfg<CG, BT>::THREADS, 1)
     const int warp = threadIdx.x >> 5;
     RgRole r;
     if (warp == 0) {
-        rg_produce<CG, BT, FORM>(p, x, r);
+        rg_produce<CG, BT, FORM>(p, x, r, [] { return true; });
         rg_produce_end<CG, BT>(p, x, r);
     } else if (warp == 1) {
         rg_issue<CG, BT, FORM>(p, x, r);
         rg_issue_end<CG>(p, x, r);
     } else {
-        rg_epilogue<CG, BT, FORM>(p, x, r, warp,
-                                  x.smem + C::STAGES * C::STAGE_BYTES + (warp - 2) * C::EPI_WARP);
+        rg_epilogue<CG, BT, FORM, FORM == RG_ROWS>(
+            p, x, r, warp, x.smem + C::STAGES * C::STAGE_BYTES + (warp - 2) * C::EPI_WARP,
+            [] { return true; });
     }
     rg_teardown<CG, BT>(x);
 }

@@ -16,14 +16,16 @@ namespace {
 // Waits (bounded) until `target` CTA arrivals have been counted.
 __device__ __forceinline__ bool seq_wait(const unsigned int* arrived, unsigned int target,
                                          const RgParams& p, volatile int* abort_flag) {
-    const uint64_t t0 = globaltimer_ns();
+    uint64_t t0 = 0;
     for (uint32_t it = 1;; ++it) {
         unsigned int v;
         asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(arrived) : "memory");
         if (v >= target) return true;
         if ((it & 15u) == 0) {
             if (*abort_flag) return false;
-            if (globaltimer_ns() - t0 > p.timeout_ns) {
+            const uint64_t now = globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > p.timeout_ns) {
                 *abort_flag = 1;
                 if (p.status) DG_SET_TIMEOUT(p.status);
                 return false;
@@ -47,23 +49,25 @@ __global__ void __launch_bounds__(RgCfg<CG, BT>::THREADS, 1)
     if (warp == 0) {
         for (int step = 0; r.ok && step < q.steps; ++step)
 #pragma unroll 1
-            for (int k = 0; k < 3; ++k) {
+            for (int k = 0; r.ok && k < 3; ++k) {
                 const RgParams& p = q.ph[seq_phase(q, step, k)];
                 const unsigned int done = static_cast<unsigned int>(3 * step + k);
-                if (x.lane == 0 && r.ok) {
+                // (lane 0, with the first tile of the product already known)
+                auto gate = [&]() {
+                    if (done == 0) return true;
+                    if (!seq_wait(q.arrived, done * gridDim.x, p, x.abort_flag)) return false;
+                    fence_proxy_async_global();  // plain stores before, TMA reads after
+                    mbar_arrive(x.gate_bar);
+                    return true;
+                };
+                if (x.lane == 0) {
                     prefetch_tmap(&p.tmap_a);
                     prefetch_tmap(&p.tmap_b);
-                    if (done > 0) {
-                        r.ok = seq_wait(q.arrived, done * gridDim.x, p, x.abort_flag);
-                        fence_proxy_async_global();  // plain stores before, TMA reads after
-                    }
                 }
-                r.ok = __shfl_sync(0xffffffffu, r.ok ? 1 : 0, 0) != 0;
-                if (!r.ok) break;
                 if (k == 2)
-                    rg_produce<CG, BT, RG_ROWS>(p, x, r);
+                    rg_produce<CG, BT, RG_ROWS>(p, x, r, gate);
                 else
-                    rg_produce<CG, BT, RG_SYM>(p, x, r);
+                    rg_produce<CG, BT, RG_SYM>(p, x, r, gate);
             }
         rg_produce_end<CG, BT>(q.ph[0], x, r);
     } else if (warp == 1) {
@@ -79,26 +83,33 @@ __global__ void __launch_bounds__(RgCfg<CG, BT>::THREADS, 1)
         rg_issue_end<CG>(q.ph[0], x, r);
     } else {
         uint8_t* buf = x.smem + C::STAGES * C::STAGE_BYTES + (warp - 2) * C::EPI_WARP;
+        uint32_t gate_phase = 0;
         for (int step = 0; step < q.steps; ++step)
 #pragma unroll 1
             for (int k = 0; k < 3; ++k) {
                 const RgParams& p = q.ph[seq_phase(q, step, k)];
+                const unsigned int done = static_cast<unsigned int>(3 * step + k);
+                const bool tile = x.cl < p.total_tiles;  // this CTA has a tile of the product
+                auto gate = [&]() {
+                    if (done == 0) return true;
+                    const bool ok = rg_warp_wait(x.gate_bar, gate_phase, x.lane, x.abort_flag, p);
+                    gate_phase ^= 1u;
+                    return ok;
+                };
                 // (after a failed wait the barriers below still run, so that no
                 // warp is left at them)
                 if (r.ok) {
                     if (k == 2)
-                        rg_epilogue<CG, BT, RG_ROWS>(p, x, r, warp, buf);
+                        rg_epilogue<CG, BT, RG_ROWS, false>(p, x, r, warp, buf, gate);
                     else
-                        rg_epilogue<CG, BT, RG_SYM>(p, x, r, warp, buf);
+                        rg_epilogue<CG, BT, RG_SYM, false>(p, x, r, warp, buf, gate);
                 }
                 fence_proxy_async_global();  // this thread's stores before TMA reads of others
                 asm volatile("bar.sync 2, %0;" ::"n"(32 * C::EPI_WARPS) : "memory");
                 if (threadIdx.x == 64) {
                     // (a CTA without a tile must not count for this product before
                     // every CTA has finished the one before)
-                    const unsigned int done = static_cast<unsigned int>(3 * step + k);
-                    seq_wait(q.arrived, done * gridDim.x, p, x.abort_flag);
-                    __threadfence();
+                    if (!tile) seq_wait(q.arrived, done * gridDim.x, p, x.abort_flag);
                     asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(q.arrived)
                                  : "memory");
                 }

@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(W4Cfg<MT, GROUP>::THREADS, 1) w4_kernel(const 
                     for (int k = 0; k < C::SG; ++k) {
                         const int st = st0 + n * k / C::SG + round;
                         if (st >= st0 + n * (k + 1) / C::SG) continue;
-                        if (!mbar_wait(empty0 + 8u * stage, phase ^ 1u, abort_flag, p.status,
+                        if (!mbar_wait_short(empty0 + 8u * stage, phase ^ 1u, abort_flag, p.status,
                                        p.timeout_ns)) {
                             ok = false;
                             break;
@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(W4Cfg<MT, GROUP>::THREADS, 1) w4_kernel(const 
                 const uint32_t stage = it - turn * C::STAGES;
                 cur = nxt;
                 if (st + 1 < a1) fetch(st + 1);
-                ok = mbar_wait(full0 + 8u * stage, turn & 1u, abort_flag, p.status, p.timeout_ns);
+                ok = mbar_wait_short(full0 + 8u * stage, turn & 1u, abort_flag, p.status, p.timeout_ns);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 const uint8_t* qs = smem + stage * C::STAGE;
