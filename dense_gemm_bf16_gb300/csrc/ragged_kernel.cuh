@@ -144,37 +144,10 @@ __device__ __forceinline__ void rg_band(const RgParams& p, int r, int chunks, in
     }
 }
 
-// RG_WGRAD takes the 32 groups of a window by descending row counts (w.incl: this
-// lane's place), so that the tiles dealt last are the short ones: 16 groups of
-// unequal size took 267 us in their own order and WGSORT by size.
-__device__ __forceinline__ void rg_sort(const RgParams& p, RgWalk& w, int lane) {
-    const int g = w.base + lane;
-    int lo = 0, hi = 0;
-    if (g < p.groups && p.offsets) {  // (no offsets: alpha == 0 or no rows)
-        lo = __ldg(p.offsets + g);
-        hi = __ldg(p.offsets + g + 1);
-    }
-    if (lo < 0 || hi < lo || hi > p.rows) {
-        if (p.status) atomicOr(p.status, STATUS_BAD_OFFSETS);
-        lo = hi = 0;
-    }
-    w.row0 = lo;
-    w.rows = hi - lo;
-    const int key = g < p.groups ? w.rows : -1;
-    int place = 0;
-#pragma unroll 8
-    for (int j = 0; j < 32; ++j) {
-        const int k = __shfl_sync(0xffffffffu, key, j);
-        place += (k > key || (k == key && j < lane)) ? 1 : 0;
-    }
-    w.incl = place;
-}
-
 template <int FORM>
 __device__ __forceinline__ RgWalk rg_begin(const RgParams& p, int lane) {
     RgWalk w{0, 0, 0, 0, 0, false};
     if (FORM == RG_ROWS && p.offsets) rg_window(p, w, lane);
-    if (FORM == RG_WGRAD) rg_sort(p, w, lane);
     return w;
 }
 
@@ -232,14 +205,17 @@ __device__ __forceinline__ bool rg_tile(const RgParams& p, RgWalk& w, int t, int
         o.ncols = p.n_col - o.col0 < p.col_tile ? p.n_col - o.col0 : p.col_tile;
         o.b_row = o.out_row = o.col0;
         if (FORM == RG_WGRAD) {
-            while (o.group >= w.base + 32) {
-                w.base += 32;
-                rg_sort(p, w, lane);
+            int lo = 0, hi = 0;
+            if (p.offsets) {  // (none: alpha == 0 or no rows)
+                lo = __ldg(p.offsets + o.group);
+                hi = __ldg(p.offsets + o.group + 1);
+                if (lo < 0 || hi < lo || hi > p.rows) {
+                    if (lane == 0 && p.status) atomicOr(p.status, STATUS_BAD_OFFSETS);
+                    lo = hi = 0;
+                }
             }
-            const int l = __ffs(__ballot_sync(0xffffffffu, w.incl == o.group - w.base)) - 1;
-            o.group = w.base + l;
-            o.k0 = __shfl_sync(0xffffffffu, w.row0, l);
-            o.klen = __shfl_sync(0xffffffffu, w.rows, l);
+            o.k0 = lo;
+            o.klen = hi - lo;
         }
     }
     // MN-major columns come in 64-wide swizzle atoms per CTA
@@ -736,48 +712,57 @@ __device__ __forceinline__ void rg_issue(const RgParams& p, const RgCta& x, RgRo
         auto issue = [&](int ks, int steps) {
             const uint64_t ad = a_desc0 + static_cast<uint32_t>(r.stage) * (C::A_BYTES >> 4);
             const uint64_t bd = b_desc0 + static_cast<uint32_t>(r.stage) * (C::B_BYTES >> 4);
+            const uint32_t empty = x.empty0 + 8u * r.stage;
+            if (x.lane == 0) {
+                if (steps == 8) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (k < steps)
-                    umma_f16_cg<CG>(d_tmem, ad + (k >> 2) * a_block + (k & 3) * a_step,
-                                    bd + (k >> 2) * b_block + (k & 3) * b_step, idesc,
-                                    (ks > 0 || k > 0) ? 1u : 0u);
-            if constexpr (CG > 1)
-                umma_commit_mc_cg<CG>(x.empty0 + 8u * r.stage, kPair);
-            else
-                umma_commit_cg<CG>(x.empty0 + 8u * r.stage);
-            if (ks == ksteps - 1) {
+                    for (int k = 0; k < 8; ++k)
+                        umma_f16_cg<CG>(d_tmem, ad + (k >> 2) * a_block + (k & 3) * a_step,
+                                        bd + (k >> 2) * b_block + (k & 3) * b_step, idesc,
+                                        (ks > 0 || k > 0) ? 1u : 0u);
+                } else {
+                    for (int k = 0; k < steps; ++k)
+                        umma_f16_cg<CG>(d_tmem, ad + (k >> 2) * a_block + (k & 3) * a_step,
+                                        bd + (k >> 2) * b_block + (k & 3) * b_step, idesc,
+                                        (ks > 0 || k > 0) ? 1u : 0u);
+                }
                 if constexpr (CG > 1)
-                    umma_commit_mc_cg<CG>(x.tfull0 + 8u * r.abuf, kPair);
+                    umma_commit_mc_cg<CG>(empty, kPair);
                 else
-                    umma_commit_cg<CG>(x.tfull0 + 8u * r.abuf);
+                    umma_commit_cg<CG>(empty);
+                if (ks == ksteps - 1) {
+                    if constexpr (CG > 1)
+                        umma_commit_mc_cg<CG>(x.tfull0 + 8u * r.abuf, kPair);
+                    else
+                        umma_commit_cg<CG>(x.tfull0 + 8u * r.abuf);
+                }
             }
         };
         if (!issuer) {
             r.stage += whole;  // (the peer only counts them)
             while (r.stage >= C::STAGES) r.stage -= C::STAGES;
         } else {
-            if (x.lane == 0) {
-                r.ok = mbar_wait_short(x.tempty0 + 8u * r.abuf, r.aphase ^ 1u, x.abort_flag, p.status, p.timeout_ns);
-                if (r.ok) tc_fence_after_sync();
-                for (int ks = 0; r.ok && ks < whole; ++ks) {
-                    r.ok = mbar_wait_short(x.full0 + 8u * r.stage, r.phase, x.abort_flag, p.status, p.timeout_ns);
-                    if (!r.ok) break;
-                    tc_fence_after_sync();
-                    const int left = w.klen - ks * 128;
-                    issue(ks, left >= 128 ? 8 : (left + 15) / 16);
-                    r.issued = true;
-                    if (++r.stage == C::STAGES) {
-                        r.stage = 0;
-                        r.phase ^= 1u;
-                    }
+            // The whole warp walks the stages and one lane issues, so that the
+            // stage's addresses stay in uniform registers.
+            r.ok = mbar_wait_short(x.tempty0 + 8u * r.abuf, r.aphase ^ 1u, x.abort_flag, p.status,
+                                   p.timeout_ns);
+            if (r.ok) tc_fence_after_sync();
+            for (int ks = 0; r.ok && ks < whole; ++ks) {
+                r.ok = mbar_wait_short(x.full0 + 8u * r.stage, r.phase, x.abort_flag, p.status,
+                                       p.timeout_ns);
+                if (!r.ok) break;
+                tc_fence_after_sync();
+                const int left = w.klen - ks * 128;
+                issue(ks, left >= 128 ? 8 : (left + 15) / 16);
+                r.issued = true;
+                if (++r.stage == C::STAGES) {
+                    r.stage = 0;
+                    r.phase ^= 1u;
                 }
             }
             __syncwarp();
             if (FORM == RG_WGRAD) {
-                r.ok = __shfl_sync(0xffffffffu, r.ok ? 1 : 0, 0) != 0;
-                r.stage = __shfl_sync(0xffffffffu, r.stage, 0);
-                r.phase = __shfl_sync(0xffffffffu, r.phase, 0);
+                r.ok = __all_sync(0xffffffffu, r.ok) != 0;
                 if (!r.ok) break;
             }
         }
@@ -793,13 +778,13 @@ __device__ __forceinline__ void rg_issue(const RgParams& p, const RgCta& x, RgRo
             const int v = w.klen - whole * 128;
             const int nz = ((v + 15) & ~15) - v;
             const int acols = 2 + w.n_mma / CG / 64;
-            for (int i = x.lane; i < acols * nz * 8; i += 32) {
-                const int chunk = i & 7, row = v + (i >> 3) % nz, col = (i >> 3) / nz;
+            for (int col = 0; col < acols; ++col) {
                 const uint32_t base =
                     col < 2 ? r.stage * C::A_BYTES + col * 16384u
                             : C::STAGES * C::A_BYTES + r.stage * C::B_BYTES + (col - 2) * 16384u;
-                *reinterpret_cast<uint4*>(x.smem + base + row * 128 + chunk * 16) =
-                    make_uint4(0, 0, 0, 0);
+                for (int row = x.lane >> 3; row < nz; row += 4)
+                    *reinterpret_cast<uint4*>(x.smem + base + (v + row) * 128 + (x.lane & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -814,7 +799,7 @@ __device__ __forceinline__ void rg_issue(const RgParams& p, const RgCta& x, RgRo
                 }
                 fence_proxy_async_smem();
                 tc_fence_after_sync();
-                if (x.lane == 0) issue(whole, (v + 15) / 16);
+                issue(whole, (v + 15) / 16);
                 r.issued = true;
             }
             r.tail_phase ^= 1u << r.stage;
