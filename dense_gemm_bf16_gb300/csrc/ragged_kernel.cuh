@@ -576,51 +576,50 @@ __device__ __forceinline__ void rg_produce(const RgParams& p, const RgCta& x, Rg
     RgWalk walk = rg_begin<FORM>(p, x.lane);
     RgTile w;
     for (int t = x.cl; r.ok && rg_tile<CG, BT, FORM>(p, walk, t, x.lane, x.rank, w); t += x.ncl) {
-        if (x.lane == 0) {
-            const int rows_b = w.n_mma / CG;  // column rows of this CTA
-            const int b_row = w.b_row + static_cast<int>(x.rank) * rows_b;
-            const int za = p.a_z ? w.group : 0, zb = p.b_z ? w.group : 0;
-            const bool a_mn = p.a_mn, b_mn = p.b_mn, a_k4 = p.a_k4, b_k4 = p.b_k4;
-            // K-major columns: whole-tile boxes, or 32-row boxes where those are fewer bytes
-            const bool big = !b_mn && 4 * rows_b > 3 * C::B_ROWS;
-            const int nb = b_mn ? rows_b / 64 : (big ? 1 : (rows_b + 31) / 32);
-            const uint32_t b_bytes = b_mn ? nb * 16384u : (big ? C::B_BYTES : nb * 8192u);
-            const CUtensorMap* map_b = big || b_mn ? &p.tmap_b : &p.tmap_b32;
-            const uint32_t bytes = C::A_BYTES + b_bytes;
-            const int ksteps = (w.klen + 127) / 128;
-            if (t == x.cl && !gate()) r.ok = false;
-            for (int ks = 0; r.ok && ks < ksteps; ++ks) {
-                if (!mbar_wait_short(x.empty0 + 8u * r.stage, r.phase ^ 1u, x.abort_flag, p.status, p.timeout_ns)) {
-                    r.ok = false;
-                    break;
-                }
-                if (p.test_stall == 1 && r.armed == 0) {
-                    r.ok = false;  // test only: the MMA warp's bounded wait must expire
-                    break;
-                }
-                const uint32_t fb = x.full0 + 8u * r.stage;
-                // a ragged tail lands on each CTA's own barrier, for the zeroing
-                const bool tail = FORM == RG_WGRAD && ks == ksteps - 1 && (w.klen & 15) != 0;
-                uint32_t bar;
+        // As in the MMA warp, the whole warp walks the stages and one lane issues.
+        const int rows_b = w.n_mma / CG;  // column rows of this CTA
+        const int b_row = w.b_row + static_cast<int>(x.rank) * rows_b;
+        const int za = p.a_z ? w.group : 0, zb = p.b_z ? w.group : 0;
+        const bool a_mn = p.a_mn, b_mn = p.b_mn, a_k4 = p.a_k4, b_k4 = p.b_k4;
+        // K-major columns: whole-tile boxes, or 32-row boxes where those are fewer bytes
+        const bool big = !b_mn && 4 * rows_b > 3 * C::B_ROWS;
+        const int nb = b_mn ? rows_b / 64 : (big ? 1 : (rows_b + 31) / 32);
+        const uint32_t b_bytes = b_mn ? nb * 16384u : (big ? C::B_BYTES : nb * 8192u);
+        const CUtensorMap* map_b = big || b_mn ? &p.tmap_b : &p.tmap_b32;
+        const uint32_t bytes = C::A_BYTES + b_bytes;
+        const int ksteps = (w.klen + 127) / 128;
+        if (t == x.cl) {
+            int open = 1;
+            if (x.lane == 0) open = gate() ? 1 : 0;
+            r.ok = __shfl_sync(0xffffffffu, open, 0) != 0;
+        }
+        for (int ks = 0; r.ok && ks < ksteps; ++ks) {
+            r.ok = mbar_wait_short(x.empty0 + 8u * r.stage, r.phase ^ 1u, x.abort_flag, p.status,
+                                   p.timeout_ns);
+            if (p.test_stall == 1 && r.armed == 0)
+                r.ok = false;  // test only: the MMA warp's bounded wait must expire
+            if (!r.ok) break;
+            const uint32_t fb = x.full0 + 8u * r.stage;
+            const uint32_t tb = x.tail0 + 8u * r.stage;
+            // a ragged tail lands on each CTA's own barrier, for the zeroing
+            const bool tail = FORM == RG_WGRAD && ks == ksteps - 1 && (w.klen & 15) != 0;
+            const uint32_t bar = tail ? tb : (CG == 1 || x.leader ? fb : mapa_shared(fb, 0u));
+            const uint32_t a_dst = x.sA0 + r.stage * C::A_BYTES;
+            const uint32_t b_dst = x.sB0 + r.stage * C::B_BYTES;
+            const int k = w.k0 + ks * 128;
+            if (x.lane == 0) {
                 if (tail) {
-                    mbar_arrive_expect_tx(x.tail0 + 8u * r.stage, bytes);
+                    mbar_arrive_expect_tx(tb, bytes);
                     if (x.leader) mbar_arrive(fb);
-                    bar = x.tail0 + 8u * r.stage;
-                    r.tail_used |= 1u << r.stage;
-                    r.tail_odd ^= 1u << r.stage;
-                } else {
-                    if (x.leader) mbar_arrive_expect_tx(fb, CG * bytes);
-                    bar = CG == 1 || x.leader ? fb : mapa_shared(fb, 0u);
+                } else if (x.leader) {
+                    mbar_arrive_expect_tx(fb, CG * bytes);
                 }
-                auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y, int z) {
+                auto load = [&](uint32_t dst, const CUtensorMap* map, int cx, int cy, int cz) {
                     if constexpr (CG == 2)
-                        tma_load_3d_pair(dst, map, bar, x, y, z, pol);
+                        tma_load_3d_pair(dst, map, bar, cx, cy, cz, pol);
                     else
-                        tma_load_3d(dst, map, bar, x, y, z, pol);
+                        tma_load_3d(dst, map, bar, cx, cy, cz, pol);
                 };
-                const uint32_t a_dst = x.sA0 + r.stage * C::A_BYTES;
-                const uint32_t b_dst = x.sB0 + r.stage * C::B_BYTES;
-                const int k = w.k0 + ks * 128;
                 // K-major: the second block's rows follow the first's; MN-major:
                 // 64-wide atom columns of 128 K rows (16 KB)
                 if (a_k4) {
@@ -649,14 +648,18 @@ __device__ __forceinline__ void rg_produce(const RgParams& p, const RgCta& x, Rg
                         load(b_dst + C::B_BYTES / 2 + 4096u * h, map_b, k + 64, b_row + 32 * h, zb);
                     }
                 }
-                ++r.armed;
-                if (++r.stage == C::STAGES) {
-                    r.stage = 0;
-                    r.phase ^= 1u;
-                }
+            }
+            if (tail) {
+                r.tail_used |= 1u << r.stage;
+                r.tail_odd ^= 1u << r.stage;
+            }
+            ++r.armed;
+            if (++r.stage == C::STAGES) {
+                r.stage = 0;
+                r.phase ^= 1u;
             }
         }
-        r.ok = __shfl_sync(0xffffffffu, r.ok ? 1 : 0, 0) != 0;
+        r.ok = __all_sync(0xffffffffu, r.ok) != 0;
     }
 }
 
