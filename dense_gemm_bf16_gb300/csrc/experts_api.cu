@@ -178,7 +178,11 @@ gemm_status_t rg_fill(const RgProblem& q, const DeviceInfo& d, int cg, int bt, R
         auto mn_major = [&](CUtensorMap* map, const RgOperand& o, int64_t z) {
             return encode_map16(map, q.dt, o.ptr, o.rows, o.k, z, o.ld * 2, o.stride * 2, 64, 128);
         };
+        auto tails = [&](CUtensorMap* map, const RgOperand& o) {
+            return encode_map16(map, q.dt, o.ptr, o.rows, o.k, 1, o.ld * 2, 0, 64, 16);
+        };
         const bool ok =
+            (q.form != RG_WGRAD || (tails(&p.tmap_a16, q.a) && tails(&p.tmap_b32, q.b))) &&
             (q.a.mn ? mn_major(&p.tmap_a, q.a, az) : k_major(&p.tmap_a, q.a, az, p.a_k4, 128)) &&
             (q.b.mn ? mn_major(&p.tmap_b, q.b, bz)
                     : k_major(&p.tmap_b, q.b, bz, p.b_k4, bt / cg) &&

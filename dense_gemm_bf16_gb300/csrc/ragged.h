@@ -27,7 +27,9 @@ struct RgDiv {
 struct RgParams {
     CUtensorMap tmap_a;      // lane operand, (inner, outer, z: group or 0)
     CUtensorMap tmap_b;      // column operand, whole-tile boxes
-    CUtensorMap tmap_b32;    // column operand, K-major: (K, rows, z), boxes of 64 x 32
+    CUtensorMap tmap_b32;    // column operand, K-major: (K, rows, z), boxes of 64 x 32;
+                             // RG_WGRAD: boxes of 64 x 16 rows of the contraction
+    CUtensorMap tmap_a16;    // RG_WGRAD: the lane operand's
     const int32_t* offsets;  // [groups + 1] on the device, or null: equal groups
     int32_t groups;
     int32_t rows;            // T: rows that the offsets index (RG_ROWS, RG_WGRAD)

@@ -16,14 +16,15 @@
 //             decoding step has to read.
 //   RG_WGRAD  dw_e[m, n] = sum_{t in group e} x[t, m] d[t, n].  Lanes are n,
 //             columns m; the contraction is ragged.  Both operands are
-//             MN-major; a group's last K = 16 step may end inside the next
-//             group, whose rows (finite or not) are overwritten with zeros in
-//             shared memory before the MMA reads them.
+//             MN-major.  A group's last K = 16 step may end inside the next
+//             group: its 16 rows are loaded apart, at the start of the tile, the
+//             rows past the group's end (finite or not) are overwritten with
+//             zeros in shared memory, and the tile's last MMA takes them.
 //   RG_SYM    S = X X^T (or X^T X), and b S + c S S: only tiles on or below
 //             the diagonal are computed, and each is written to both places.
 //
-// Warps: 0 TMA producer, 1 MMA issuer (and the zeroing of ragged tails),
-// 2-9 epilogue, two per tensor-memory lane quarter taking 32-column chunks in
+// Warps: 0 TMA producer, 1 MMA issuer, 10 (RG_WGRAD) ragged tails, 2-9 epilogue,
+// two per tensor-memory lane quarter taking 32-column chunks in
 // turn.  Two accumulators let a tile's epilogue overlap the next main loop.
 // The output's contiguous dimension runs along the lanes.  A 16-bit chunk is
 // read from tensor memory in the MMA-fragment layout, turned by transposing
@@ -63,7 +64,8 @@ struct RgCfg {
     static constexpr uint32_t B_BYTES = 2 * B_ROWS * 128;
     static constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int EPI_WARPS = 8;
-    static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+    // (RG_WGRAD has one warp more, for the ragged tails)
+    static constexpr int threads(int form) { return 64 + 32 * EPI_WARPS + (form == RG_WGRAD ? 32 : 0); }
     static constexpr uint32_t EPI_WARP = 2 * 2048;  // two tiles of 32 x 32 16-bit elements
     static constexpr uint32_t EPI_SMEM = EPI_WARPS * EPI_WARP;
     static constexpr uint32_t BAR_BYTES = 512;
@@ -73,7 +75,13 @@ struct RgCfg {
     static constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE_BYTES + EPI_SMEM + BAR_BYTES;
     static_assert(BT % 32 == 0 && BT <= 256 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "tile width");
     static_assert(CG == 1 || BT == 256, "pairs take 256-column tiles (two 64-wide atoms per CTA)");
-    static_assert((4 * STAGES + 6) * 8 + 8 <= BAR_BYTES, "barrier area too small");
+    // RG_WGRAD: half of the staging (one tile a warp), and two buffers of 16 rows of
+    // both operands for the ragged ends of groups
+    static constexpr uint32_t TAIL_A = 2 * 16 * 128, TAIL_B = (B_ROWS / 64) * 16 * 128;
+    static constexpr uint32_t TAIL_AT = EPI_SMEM / 2, TAIL_BYTES = 8192;
+    static_assert(B_ROWS < 64 || 2 * TAIL_BYTES <= EPI_SMEM / 2, "tail buffers");
+    static_assert(TAIL_A + TAIL_B <= TAIL_BYTES, "tail buffer");
+    static_assert((2 * STAGES + 12) * 8 + 8 <= BAR_BYTES, "barrier area too small");
 };
 
 struct RgTile {
@@ -353,7 +361,9 @@ __device__ __forceinline__ void rg_out16(const RgParams& p, const RgTile& w, uin
     const bool beta = p.beta != 0.0f;
     const int pcol = lane >> 2, part = lane & 3;  // this lane's 16 bytes of a staged tile
     const int nn = p.n_lane - nl0 - 8 * part;     // of which this many columns exist
-    const uint32_t s_out = smem_u32(buf), s_in = s_out + 2048u;
+    // (RG_WGRAD has one staged tile, which Cin and the output share)
+    constexpr uint32_t IN = FORM == RG_WGRAD ? 0u : 2048u;
+    const uint32_t s_out = smem_u32(buf), s_in = s_out + IN;
     const uint32_t mat = rg_at(lane & 7, lane >> 3);  // this lane's row of a transposed store
     float bias[4];
 #pragma unroll
@@ -395,7 +405,7 @@ __device__ __forceinline__ void rg_out16(const RgParams& p, const RgTile& w, uin
         if (ready()) release();
         return;
     }
-    if (FORM != RG_SYM && !beta) {
+    if (FORM == RG_ROWS && !beta) {
         // two chunks at a time, one in each staged tile
         if (!ready()) return;
 #pragma unroll 1
@@ -444,7 +454,7 @@ __device__ __forceinline__ void rg_out16(const RgParams& p, const RgTile& w, uin
         if (beta) {
 #pragma unroll
             for (int it = 0; it < 4; ++it)
-                *reinterpret_cast<uint4*>(buf + 2048 + rg_at(8 * it + pcol, part)) = cin[it];
+                *reinterpret_cast<uint4*>(buf + IN + rg_at(8 * it + pcol, part)) = cin[it];
             if (more) load_in(c0 + 64);
             __syncwarp();
 #pragma unroll
@@ -459,7 +469,7 @@ __device__ __forceinline__ void rg_out16(const RgParams& p, const RgTile& w, uin
                     x[1] = fmaf(p.beta, f.y, x[1]);
                 }
             }
-            if (FORM == RG_SYM) __syncwarp();  // (the mirrored tile takes Cin's place)
+            if (FORM != RG_ROWS) __syncwarp();  // (Cin's place is written again)
         }
         if (ACT) rg_act(v, p.act);
         rg_pack16(p.c_dtype, v, pk);
@@ -546,7 +556,7 @@ __device__ __forceinline__ void rg_out32(const RgParams& p, const RgTile& w, uin
 struct RgCta {
     uint8_t* smem;
     uint32_t sA0, sB0;
-    uint32_t full0, empty0, tail0, peer_tail0, tfull0, tempty0, drain_bar, gate_bar;
+    uint32_t full0, empty0, tail0, tfull0, tempty0, drain_bar, gate_bar;
     uint32_t tmem_base;
     volatile int* abort_flag;
     uint32_t rank;   // CTA of the pair
@@ -560,8 +570,7 @@ struct RgRole {
     int stage = 0;
     uint32_t phase = 0;
     uint32_t armed = 0;                    // producer: stages filled
-    uint32_t tail_used = 0, tail_odd = 0;  // ... per stage: tails armed; an odd number of them
-    uint32_t tail_phase = 0;               // MMA warp: one bit per stage
+    uint32_t tails = 0;                    // ragged ends so far
     int abuf = 0;
     uint32_t aphase = 0;
     bool issued = false, ok = true;
@@ -582,12 +591,14 @@ __device__ __forceinline__ void rg_produce(const RgParams& p, const RgCta& x, Rg
         const int za = p.a_z ? w.group : 0, zb = p.b_z ? w.group : 0;
         const bool a_mn = p.a_mn, b_mn = p.b_mn, a_k4 = p.a_k4, b_k4 = p.b_k4;
         // K-major columns: whole-tile boxes, or 32-row boxes where those are fewer bytes
-        const bool big = !b_mn && 4 * rows_b > 3 * C::B_ROWS;
+        // (one load a block costs as much issue time as bytes: half a tile suffices there)
+        const bool big = !b_mn && (b_k4 ? 4 * rows_b > 3 * C::B_ROWS : 2 * rows_b > C::B_ROWS);
         const int nb = b_mn ? rows_b / 64 : (big ? 1 : (rows_b + 31) / 32);
         const uint32_t b_bytes = b_mn ? nb * 16384u : (big ? C::B_BYTES : nb * 8192u);
         const CUtensorMap* map_b = big || b_mn ? &p.tmap_b : &p.tmap_b32;
         const uint32_t bytes = C::A_BYTES + b_bytes;
-        const int ksteps = (w.klen + 127) / 128;
+        // (RG_WGRAD: whole K = 16 steps; the tail warp loads the rest)
+        const int ksteps = ((FORM == RG_WGRAD ? w.klen & ~15 : w.klen) + 127) / 128;
         if (t == x.cl) {
             int open = 1;
             if (x.lane == 0) open = gate() ? 1 : 0;
@@ -600,20 +611,12 @@ __device__ __forceinline__ void rg_produce(const RgParams& p, const RgCta& x, Rg
                 r.ok = false;  // test only: the MMA warp's bounded wait must expire
             if (!r.ok) break;
             const uint32_t fb = x.full0 + 8u * r.stage;
-            const uint32_t tb = x.tail0 + 8u * r.stage;
-            // a ragged tail lands on each CTA's own barrier, for the zeroing
-            const bool tail = FORM == RG_WGRAD && ks == ksteps - 1 && (w.klen & 15) != 0;
-            const uint32_t bar = tail ? tb : (CG == 1 || x.leader ? fb : mapa_shared(fb, 0u));
+            const uint32_t bar = CG == 1 || x.leader ? fb : mapa_shared(fb, 0u);
             const uint32_t a_dst = x.sA0 + r.stage * C::A_BYTES;
             const uint32_t b_dst = x.sB0 + r.stage * C::B_BYTES;
             const int k = w.k0 + ks * 128;
             if (x.lane == 0) {
-                if (tail) {
-                    mbar_arrive_expect_tx(tb, bytes);
-                    if (x.leader) mbar_arrive(fb);
-                } else if (x.leader) {
-                    mbar_arrive_expect_tx(fb, CG * bytes);
-                }
+                if (x.leader) mbar_arrive_expect_tx(fb, CG * bytes);
                 auto load = [&](uint32_t dst, const CUtensorMap* map, int cx, int cy, int cz) {
                     if constexpr (CG == 2)
                         tma_load_3d_pair(dst, map, bar, cx, cy, cz, pol);
@@ -649,10 +652,6 @@ __device__ __forceinline__ void rg_produce(const RgParams& p, const RgCta& x, Rg
                     }
                 }
             }
-            if (tail) {
-                r.tail_used |= 1u << r.stage;
-                r.tail_odd ^= 1u << r.stage;
-            }
             ++r.armed;
             if (++r.stage == C::STAGES) {
                 r.stage = 0;
@@ -671,9 +670,6 @@ template <int CG, int BT>
 __device__ __forceinline__ void rg_produce_end(const RgParams& p, const RgCta& x, const RgRole& r) {
     using C = RgCfg<CG, BT>;
     if (x.lane != 0) return;
-    for (int s = 0; s < C::STAGES; ++s)
-        if (r.tail_used >> s & 1u)  // an odd count: its last phase has parity 0
-            rg_drain(x.tail0 + 8u * s, (r.tail_odd >> s & 1u) ^ 1u, p.timeout_ns);
     if (CG == 2 && !x.leader) {
         if (!r.ok) {
             const uint64_t t0 = globaltimer_ns();
@@ -689,7 +685,7 @@ __device__ __forceinline__ void rg_produce_end(const RgParams& p, const RgCta& x
 }
 
 // ------------------------------------------------ MMA issuer (a warp)
-// The pair's peer walks the same tiles for the tails only.
+// (nothing to do in the pair's peer)
 template <int CG, int BT, int FORM>
 __device__ __forceinline__ void rg_issue(const RgParams& p, const RgCta& x, RgRole& r) {
     using C = RgCfg<CG, BT>;
@@ -701,15 +697,14 @@ __device__ __forceinline__ void rg_issue(const RgParams& p, const RgCta& x, RgRo
     const uint64_t b_desc0 = smem_desc_sw128(x.sB0, b_mn ? 16384u : 16u, 1024u);
     const uint32_t a_step = a_mn ? 128u : 2u, b_step = b_mn ? 128u : 2u;
     const uint32_t a_block = a_mn ? 512u : C::A_BYTES >> 5, b_block = b_mn ? 512u : C::B_BYTES >> 5;
-    const bool issuer = CG == 1 || x.leader;
+    if (CG == 2 && !x.leader) return;
     RgWalk walk = rg_begin<FORM>(p, x.lane);
     RgTile w;
     for (int t = x.cl; r.ok && rg_tile<CG, BT, FORM>(p, walk, t, x.lane, x.rank, w); t += x.ncl) {
-        const int ksteps = (w.klen + 127) / 128;
-        if (ksteps == 0) continue;  // no rows: the epilogue writes zeros
-        if (!issuer && FORM != RG_WGRAD) continue;
+        if (w.klen == 0) continue;  // no rows: the epilogue writes zeros
         const bool tail = FORM == RG_WGRAD && (w.klen & 15) != 0;
-        const int whole = ksteps - (tail ? 1 : 0);  // stages the MMA reads as they are
+        const int klen = FORM == RG_WGRAD ? w.klen & ~15 : w.klen;
+        const int ksteps = (klen + 127) / 128;
         const uint32_t d_tmem = x.tmem_base + static_cast<uint32_t>(r.abuf * BT);
         const uint32_t idesc = p.idesc | (static_cast<uint32_t>(w.n_mma >> 3) << 17);
         auto issue = [&](int ks, int steps) {
@@ -733,7 +728,7 @@ __device__ __forceinline__ void rg_issue(const RgParams& p, const RgCta& x, RgRo
                     umma_commit_mc_cg<CG>(empty, kPair);
                 else
                     umma_commit_cg<CG>(empty);
-                if (ks == ksteps - 1) {
+                if (!tail && ks == ksteps - 1) {
                     if constexpr (CG > 1)
                         umma_commit_mc_cg<CG>(x.tfull0 + 8u * r.abuf, kPair);
                     else
@@ -741,81 +736,113 @@ __device__ __forceinline__ void rg_issue(const RgParams& p, const RgCta& x, RgRo
                 }
             }
         };
-        if (!issuer) {
-            r.stage += whole;  // (the peer only counts them)
-            while (r.stage >= C::STAGES) r.stage -= C::STAGES;
-        } else {
-            // The whole warp walks the stages and one lane issues, so that the
-            // stage's addresses stay in uniform registers.
-            r.ok = mbar_wait_short(x.tempty0 + 8u * r.abuf, r.aphase ^ 1u, x.abort_flag, p.status,
+        // The whole warp walks the stages and one lane issues, so that the stage's
+        // addresses stay in uniform registers (16384 x 4096 x 2048: 174 -> 154 us; one
+        // lane alone took as long to issue eight MMAs as they take to run).
+        r.ok = mbar_wait_short(x.tempty0 + 8u * r.abuf, r.aphase ^ 1u, x.abort_flag, p.status,
+                               p.timeout_ns);
+        if (r.ok) tc_fence_after_sync();
+        for (int ks = 0; r.ok && ks < ksteps; ++ks) {
+            r.ok = mbar_wait_short(x.full0 + 8u * r.stage, r.phase, x.abort_flag, p.status,
                                    p.timeout_ns);
-            if (r.ok) tc_fence_after_sync();
-            for (int ks = 0; r.ok && ks < whole; ++ks) {
-                r.ok = mbar_wait_short(x.full0 + 8u * r.stage, r.phase, x.abort_flag, p.status,
-                                       p.timeout_ns);
-                if (!r.ok) break;
-                tc_fence_after_sync();
-                const int left = w.klen - ks * 128;
-                issue(ks, left >= 128 ? 8 : (left + 15) / 16);
-                r.issued = true;
-                if (++r.stage == C::STAGES) {
-                    r.stage = 0;
-                    r.phase ^= 1u;
-                }
-            }
-            __syncwarp();
-            if (FORM == RG_WGRAD) {
-                r.ok = __all_sync(0xffffffffu, r.ok) != 0;
-                if (!r.ok) break;
-            }
-        }
-        if (FORM == RG_WGRAD && tail) {
-            if (!rg_warp_wait(x.tail0 + 8u * r.stage, r.tail_phase >> r.stage & 1u, x.lane, x.abort_flag, p)) {
-                r.ok = false;
-                break;
-            }
-            __syncwarp();
-            // rows klen % 128 .. up to the end of the last K = 16 step: one row is
-            // 128 bytes of every 64-wide atom column (whole rows, so the swizzle
-            // inside them does not matter)
-            const int v = w.klen - whole * 128;
-            const int nz = ((v + 15) & ~15) - v;
-            const int acols = 2 + w.n_mma / CG / 64;
-            for (int col = 0; col < acols; ++col) {
-                const uint32_t base =
-                    col < 2 ? r.stage * C::A_BYTES + col * 16384u
-                            : C::STAGES * C::A_BYTES + r.stage * C::B_BYTES + (col - 2) * 16384u;
-                for (int row = x.lane >> 3; row < nz; row += 4)
-                    *reinterpret_cast<uint4*>(x.smem + base + (v + row) * 128 + (x.lane & 7) * 16) =
-                        make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (!issuer) {
-                if (x.lane == 0) mbar_arrive_remote(mapa_shared(x.peer_tail0 + 8u * r.stage, 0u));
-            } else {
-                if (!rg_warp_wait(x.full0 + 8u * r.stage, r.phase, x.lane, x.abort_flag, p) ||
-                    (CG == 2 && !rg_warp_wait(x.peer_tail0 + 8u * r.stage, r.tail_phase >> r.stage & 1u,
-                                              x.lane, x.abort_flag, p))) {
-                    r.ok = false;
-                    break;
-                }
-                fence_proxy_async_smem();
-                tc_fence_after_sync();
-                issue(whole, (v + 15) / 16);
-                r.issued = true;
-            }
-            r.tail_phase ^= 1u << r.stage;
+            if (!r.ok) break;
+            tc_fence_after_sync();
+            const int left = klen - ks * 128;
+            issue(ks, left >= 128 ? 8 : (left + 15) / 16);
+            r.issued = true;
             if (++r.stage == C::STAGES) {
                 r.stage = 0;
                 r.phase ^= 1u;
+            }
+        }
+        if (FORM == RG_WGRAD && tail && r.ok) {
+            const uint32_t b = r.tails & 1u;
+            r.ok = mbar_wait_short(x.tail0 + 16u + 8u * b, r.tails >> 1 & 1u, x.abort_flag,
+                                   p.status, p.timeout_ns);
+            ++r.tails;
+            if (r.ok) {
+                fence_proxy_async_smem();
+                tc_fence_after_sync();
+                // 64-wide atom columns of 16 rows (2 KB)
+                const uint32_t at = x.sA0 + C::STAGES * C::STAGE_BYTES + C::TAIL_AT + b * C::TAIL_BYTES;
+                const uint64_t ad = smem_desc_sw128(at, 2048u, 1024u);
+                const uint64_t bd = smem_desc_sw128(at + C::TAIL_A, 2048u, 1024u);
+                if (x.lane == 0) {
+                    umma_f16_cg<CG>(d_tmem, ad, bd, idesc, ksteps > 0 ? 1u : 0u);
+                    if constexpr (CG > 1) {
+                        umma_commit_mc_cg<CG>(x.tail0 + 32u + 8u * b, kPair);
+                        umma_commit_mc_cg<CG>(x.tfull0 + 8u * r.abuf, kPair);
+                    } else {
+                        umma_commit_cg<CG>(x.tail0 + 32u + 8u * b);
+                        umma_commit_cg<CG>(x.tfull0 + 8u * r.abuf);
+                    }
+                }
+                r.issued = true;
             }
         }
         if (++r.abuf == 2) {
             r.abuf = 0;
             r.aphase ^= 1u;
         }
-        r.ok = __shfl_sync(0xffffffffu, r.ok ? 1 : 0, 0) != 0;
+        r.ok = __all_sync(0xffffffffu, r.ok) != 0;
+    }
+}
+
+// ------------------------------------------------ ragged tails (a warp, RG_WGRAD)
+// Loads the 16 rows that a group's last, partial K = 16 step reads into one of two
+// buffers, overwrites the rows past the group's end with zeros, and hands them to
+// the MMA warp of the leader, up to two tiles ahead.  (Zeroing inside the ring's
+// last stage made every ragged tile wait for its own loads: 247 us against 197 for
+// 16 groups of 1021 and of 1024 rows.)
+template <int CG, int BT>
+__device__ __forceinline__ void rg_tails(const RgParams& p, const RgCta& x, RgRole& r) {
+    using C = RgCfg<CG, BT>;
+    const uint64_t pol = l2_policy_evict_normal();
+    RgWalk walk = rg_begin<RG_WGRAD>(p, x.lane);
+    RgTile w;
+    for (int t = x.cl; rg_tile<CG, BT, RG_WGRAD>(p, walk, t, x.lane, x.rank, w); t += x.ncl) {
+        const int v = w.klen & 15;  // valid rows
+        if (v == 0) continue;
+        const uint32_t b = r.tails & 1u, turn = r.tails >> 1 & 1u;
+        ++r.tails;
+        const uint32_t loaded = x.tail0 + 8u * b, ready = x.tail0 + 16u + 8u * b;
+        if (!rg_warp_wait(x.tail0 + 32u + 8u * b, turn ^ 1u, x.lane, x.abort_flag, p)) return;
+        uint8_t* buf = x.smem + C::STAGES * C::STAGE_BYTES + C::TAIL_AT + b * C::TAIL_BYTES;
+        const uint32_t dst = smem_u32(buf);
+        const int rows_b = w.n_mma / CG, nb = rows_b / 64;
+        const int b_row = w.b_row + static_cast<int>(x.rank) * rows_b;
+        if (x.lane == 0) {
+            const int k = w.k0 + (w.klen & ~15);
+            mbar_arrive_expect_tx(loaded, (2 + nb) * 2048u);
+            tma_load_3d(dst, &p.tmap_a16, loaded, w.lane0, k, 0, pol);
+            tma_load_3d(dst + 2048u, &p.tmap_a16, loaded, w.lane0 + 64, k, 0, pol);
+            for (int h = 0; h < nb; ++h)
+                tma_load_3d(dst + C::TAIL_A + 2048u * h, &p.tmap_b32, loaded, b_row + 64 * h, k, 0,
+                            pol);
+        }
+        __syncwarp();
+        // (gives up only after its copies have had their time to land)
+        if (!rg_warp_wait(loaded, turn, x.lane, x.abort_flag, p)) {
+            if (x.lane == 0) rg_drain(loaded, turn, p.timeout_ns);
+            return;
+        }
+        __syncwarp();
+        // rows v .. 15: one row is 128 bytes of every 64-wide atom column (whole
+        // rows, so the swizzle inside them does not matter)
+        for (int i = x.lane; i < (2 + nb) * 128; i += 32) {
+            const int row = i >> 3 & 15;
+            if (row >= v)
+                *reinterpret_cast<uint4*>(buf + (i >> 7) * 2048 + row * 128 + (i & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (x.lane == 0) {
+            if (CG == 2 && !x.leader)
+                mbar_arrive_remote(mapa_shared(ready, 0u));
+            else
+                mbar_arrive(ready);
+        }
     }
 }
 
@@ -889,27 +916,27 @@ __device__ __forceinline__ RgCta rg_setup(const RgParams& p, uint8_t* smem_raw) 
     x.sA0 = smem_u32(x.smem);
     x.sB0 = x.sA0 + C::STAGES * C::A_BYTES;
     uint64_t* bars = reinterpret_cast<uint64_t*>(x.smem + C::STAGES * C::STAGE_BYTES + C::EPI_SMEM);
-    // full[STAGES], empty[STAGES], tail[STAGES], peer_tail[STAGES], tmem_full[2],
-    // tmem_empty[2], drain, gate
+    // full[STAGES], empty[STAGES], tail_full[2], tail_ready[2], tail_empty[2],
+    // tmem_full[2], tmem_empty[2], drain, gate
     x.full0 = smem_u32(bars);
     x.empty0 = x.full0 + 8u * C::STAGES;
     x.tail0 = x.full0 + 16u * C::STAGES;
-    x.peer_tail0 = x.full0 + 24u * C::STAGES;
-    x.tfull0 = x.full0 + 32u * C::STAGES;
+    x.tfull0 = x.tail0 + 48u;
     x.tempty0 = x.tfull0 + 16u;
     x.drain_bar = x.tempty0 + 16u;
     x.gate_bar = x.drain_bar + 8u;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 4 * C::STAGES + 6);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * C::STAGES + 12);
     x.abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(x.full0 + 8u * s, 1);
             mbar_init(x.empty0 + 8u * s, 1);
-            mbar_init(x.tail0 + 8u * s, 1);
-            mbar_init(x.peer_tail0 + 8u * s, 1);
         }
         for (int b = 0; b < 2; ++b) {
+            mbar_init(x.tail0 + 8u * b, 1);        // loaded (own bytes)
+            mbar_init(x.tail0 + 16u + 8u * b, CG);  // zeroed, by every CTA of the pair
+            mbar_init(x.tail0 + 32u + 8u * b, 1);  // read by the MMA
             mbar_init(x.tfull0 + 8u * b, 1);
             mbar_init(x.tempty0 + 8u * b, CG * C::EPI_WARPS);
         }
@@ -949,7 +976,7 @@ __device__ __forceinline__ void rg_teardown(const RgCta& x) {
 }
 
 template <int CG, int BT, int FORM>
-__global__ void __launch_bounds__(RgCfg<CG, BT>::THREADS, 1)
+__global__ void __launch_bounds__(RgCfg<CG, BT>::threads(FORM), 1)
     ragged_kernel(const __grid_constant__ RgParams p) {
     using C = RgCfg<CG, BT>;
     extern __shared__ uint8_t smem_raw[];
@@ -962,9 +989,13 @@ __global__ void __launch_bounds__(RgCfg<CG, BT>::THREADS, 1)
     } else if (warp == 1) {
         rg_issue<CG, BT, FORM>(p, x, r);
         rg_issue_end<CG>(p, x, r);
+    } else if (FORM == RG_WGRAD && warp == 2 + C::EPI_WARPS) {
+        rg_tails<CG, BT>(p, x, r);
     } else {
         rg_epilogue<CG, BT, FORM, FORM == RG_ROWS>(
-            p, x, r, warp, x.smem + C::STAGES * C::STAGE_BYTES + (warp - 2) * C::EPI_WARP,
+            p, x, r, warp,
+            x.smem + C::STAGES * C::STAGE_BYTES +
+                (warp - 2) * (FORM == RG_WGRAD ? C::EPI_WARP / 2 : C::EPI_WARP),
             [] { return true; });
     }
     rg_teardown<CG, BT>(x);
@@ -974,7 +1005,7 @@ template <int CG, int BT, int FORM>
 cudaError_t rg_launch(const RgParams& p, int grid, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(RgCfg<CG, BT>::THREADS);
+    cfg.blockDim = dim3(RgCfg<CG, BT>::threads(FORM));
     cfg.dynamicSmemBytes = RgCfg<CG, BT>::SMEM;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

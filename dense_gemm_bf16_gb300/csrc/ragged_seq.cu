@@ -39,7 +39,7 @@ __device__ __forceinline__ int seq_phase(const RgSeq& q, int step, int k) {
 }
 
 template <int CG, int BT>
-__global__ void __launch_bounds__(RgCfg<CG, BT>::THREADS, 1)
+__global__ void __launch_bounds__(RgCfg<CG, BT>::threads(RG_SYM), 1)
     ragged_seq_kernel(const __grid_constant__ RgSeq q) {
     using C = RgCfg<CG, BT>;
     extern __shared__ uint8_t smem_raw[];
@@ -122,7 +122,7 @@ template <int CG, int BT>
 cudaError_t launch_seq(const RgSeq& q, int grid, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(RgCfg<CG, BT>::THREADS);
+    cfg.blockDim = dim3(RgCfg<CG, BT>::threads(RG_SYM));
     cfg.dynamicSmemBytes = RgCfg<CG, BT>::SMEM;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];

@@ -31,16 +31,12 @@ def _fn(name):
 _fns: dict = {}
 
 
-def _device(first, *others):
-    """The CUDA device of `first`, on which every other buffer has to be: the
-    kernels read device pointers.  Buffers come as (name, tensor or None)."""
-    dev = first[1].device
-    if dev.type != "cuda":
-        raise ValueError(f"{first[0]} must be a CUDA tensor on one CUDA device (it is on {dev})")
-    for name, t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} must be a CUDA tensor on {dev} (it is on {t.device})")
-    return dev
+def _wrong_device(dev, **tensors):
+    """Every buffer has to be on one CUDA device: the kernels read device pointers."""
+    for name, t in tensors.items():
+        if t is not None and (not t.is_cuda or t.get_device() != dev):
+            where = f"cuda:{dev}" if dev >= 0 else "one CUDA device"
+            raise ValueError(f"{name} must be a CUDA tensor on {where} (it is on {t.device})")
 
 
 def _ld(name, t):
@@ -55,11 +51,10 @@ def _ld(name, t):
 
 
 def _offsets(offsets, groups):
-    if offsets.dtype != torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous():
-        raise ValueError("offsets must be a contiguous int32 vector")
-    if offsets.shape[0] != groups + 1:
-        raise ValueError(f"offsets must hold groups + 1 = {groups + 1} values "
-                         f"(it holds {offsets.shape[0]})")
+    if offsets.dtype is not torch.int32 or offsets.shape != (groups + 1,) or \
+            not offsets.is_contiguous():
+        raise ValueError(f"offsets must be a contiguous int32 vector of groups + 1 = {groups + 1} "
+                         f"values (it is {offsets.dtype} of shape {tuple(offsets.shape)})")
     return offsets.data_ptr()
 
 
@@ -86,14 +81,14 @@ def _epilogue(epilogue, bias, groups, N):
     return epi, bias.data_ptr(), bias.stride(0) if bias.dim() == 2 and groups > 1 else 0
 
 
-def _out(name, out, shape, dtype, device, types):
+def _out(name, out, shape, dtype, like, types):
     if out is None:
         if dtype is None:
             dtype = types[0]
         elif dtype not in types:
             raise TypeError(f"{name} must be one of {', '.join(str(t) for t in types)}")
-        return torch.empty(shape, dtype=dtype, device=device)
-    if tuple(out.shape) != tuple(shape):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if out.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)} (it has {tuple(out.shape)})")
     if out.dtype not in types or (dtype is not None and out.dtype != dtype):
         raise TypeError(f"{name} must be one of {', '.join(str(t) for t in types)}")
@@ -107,21 +102,18 @@ def _code16(A, B, names="A and B"):
     return code
 
 
-def _scratch(workspace, need, device):
+def _scratch(workspace, need, like):
     """(workspace kept alive, pointer, bytes)."""
     if workspace is None:
         if need == 0:
             return None, 0, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _stream(stream, device):
-    if stream is not None:
-        return stream
-    if _raw_stream is not None and device.index is not None:
-        return _raw_stream(device.index)
-    return torch.cuda.current_stream(device).cuda_stream
+if _raw_stream is None:
+    def _raw_stream(dev):
+        return torch.cuda.current_stream(dev).cuda_stream
 
 
 def grouped_gemm(A: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor,
@@ -139,13 +131,15 @@ def grouped_gemm(A: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor,
     dt = _code16(A, B)
     if A.dim() != 2 or B.dim() != 3 or A.shape[1] != B.shape[1]:
         raise ValueError(f"shape mismatch: A{tuple(A.shape)} B{tuple(B.shape)}")
-    dev = _device(("A", A), ("B", B), ("offsets", offsets), ("C", C), ("bias", bias),
-                  ("workspace", workspace))
+    dev = A.get_device()
+    if not dev == B.get_device() == offsets.get_device() or dev < 0 or C is not None or \
+            bias is not None or workspace is not None:
+        _wrong_device(dev, A=A, B=B, offsets=offsets, C=C, bias=bias, workspace=workspace)
     T, K = A.shape
     groups, _, N = B.shape
     if C is None and beta != 0.0:
         raise ValueError("beta != 0 needs an input C")
-    C = _out("C", C, (T, N), out_dtype, dev, (A.dtype, torch.float32))
+    C = _out("C", C, (T, N), out_dtype, A, (A.dtype, torch.float32))
     epi, bias_ptr, stride_bias = _epilogue(epilogue, bias, groups, N)
     lda, ldc = _ld("A", A), _ld("C", C)
     sb, s1, s2 = B.stride()
@@ -163,10 +157,10 @@ def grouped_gemm(A: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor,
     need = 0
     if workspace is None and (pa | pb | (lda | ldb | sb) * 2) & 15:
         need = _abi.gemm_grouped_workspace_size(dt, groups, T, N, K, pa, lda, pb, ldb, lb, sb)
-    workspace, ws, ws_bytes = _scratch(workspace, need, dev)
+    workspace, ws, ws_bytes = _scratch(workspace, need, A)
     st = _fn("gemm_grouped")(dt, groups, T, N, K, pa, lda, pb, ldb, lb, sb, C.data_ptr(), ldc,
                              _CODE[C.dtype], off, alpha, beta, bias_ptr, stride_bias, epi, ws,
-                             ws_bytes, _stream(stream, dev))
+                             ws_bytes, _raw_stream(dev) if stream is None else stream)
     if st:
         check(st)
     return C
@@ -181,7 +175,8 @@ def grouped_gemm_wgrad(A: torch.Tensor, D: torch.Tensor, offsets: torch.Tensor,
     dt = _code16(A, D, "A and D")
     if A.dim() != 2 or D.dim() != 2 or A.shape[0] != D.shape[0]:
         raise ValueError(f"shape mismatch: A{tuple(A.shape)} D{tuple(D.shape)}")
-    dev = _device(("A", A), ("D", D), ("offsets", offsets), ("C", C), ("workspace", workspace))
+    dev = A.get_device()
+    _wrong_device(dev, A=A, D=D, offsets=offsets, C=C, workspace=workspace)
     T, M = A.shape
     N = D.shape[1]
     groups = offsets.numel() - 1
@@ -189,17 +184,17 @@ def grouped_gemm_wgrad(A: torch.Tensor, D: torch.Tensor, offsets: torch.Tensor,
         raise ValueError("offsets must hold groups + 1 values")
     if C is None and beta != 0.0:
         raise ValueError("beta != 0 needs an input C")
-    C = _out("C", C, (groups, M, N), out_dtype, dev, (A.dtype, torch.float32))
+    C = _out("C", C, (groups, M, N), out_dtype, A, (A.dtype, torch.float32))
     lda, ldd, ldc = _ld("A", A), _ld("D", D), _ld("C", C)
     off = _offsets(offsets, groups)
     pa, pd = A.data_ptr(), D.data_ptr()
     need = 0
     if workspace is None and (pa | pd | (lda | ldd) * 2) & 15:
         need = _abi.gemm_grouped_wgrad_workspace_size(dt, groups, T, M, N, pa, lda, pd, ldd)
-    workspace, ws, ws_bytes = _scratch(workspace, need, dev)
+    workspace, ws, ws_bytes = _scratch(workspace, need, A)
     st = _fn("gemm_grouped_wgrad")(dt, groups, T, M, N, pa, lda, pd, ldd, C.data_ptr(), ldc,
                                    C.stride(0) if groups > 1 else 0, _CODE[C.dtype], off, alpha,
-                                   beta, ws, ws_bytes, _stream(stream, dev))
+                                   beta, ws, ws_bytes, _raw_stream(dev) if stream is None else stream)
     if st:
         check(st)
     return C
@@ -217,18 +212,19 @@ def newton_schulz(G: torch.Tensor, out: torch.Tensor | None = None, *, steps=5,
         raise ValueError("G must be a 2-D or 3-D tensor")
     if len(coefficients) != 3:
         raise ValueError("coefficients must be three numbers")
-    dev = _device(("G", G), ("out", out), ("workspace", workspace))
-    out = _out("out", out, G.shape, out_dtype, dev, (torch.bfloat16, torch.float16))
+    dev = G.get_device()
+    _wrong_device(dev, G=G, out=out, workspace=workspace)
+    out = _out("out", out, G.shape, out_dtype, G, (torch.bfloat16, torch.float16))
     batch = G.shape[0] if G.dim() == 3 else 1
     M, N = G.shape[-2:]
     ldg, ldo = _ld("G", G), _ld("out", out)
     sg, so = (G.stride(0), out.stride(0)) if batch > 1 else (0, 0)
     need = _abi.gemm_newton_schulz_workspace_size(batch, M, N) if workspace is None else 0
-    workspace, ws, ws_bytes = _scratch(workspace, need, dev)
+    workspace, ws, ws_bytes = _scratch(workspace, need, G)
     a, b, c = coefficients
     st = _fn("gemm_newton_schulz")(_CODE[G.dtype], batch, M, N, G.data_ptr(), ldg, sg,
                                    out.data_ptr(), ldo, so, _CODE[out.dtype], steps, a, b, c, eps,
-                                   ws, ws_bytes, _stream(stream, dev))
+                                   ws, ws_bytes, _raw_stream(dev) if stream is None else stream)
     if st:
         check(st)
     return out
@@ -251,8 +247,11 @@ def w4_gemm(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, *, zeros=Non
     if x.dim() != 2 or q.dim() != lead or scales.dim() != lead:
         raise ValueError(f"x must be 2-D, q and scales {lead}-D "
                          f"({'with' if lead == 3 else 'without'} offsets)")
-    dev = _device(("x", x), ("q", q), ("scales", scales), ("zeros", zeros), ("offsets", offsets),
-                  ("out", out), ("bias", bias), ("workspace", workspace))
+    dev = x.get_device()
+    if not dev == q.get_device() == scales.get_device() or dev < 0 or zeros is not None or \
+            offsets is not None or out is not None or bias is not None or workspace is not None:
+        _wrong_device(dev, x=x, q=q, scales=scales, zeros=zeros, offsets=offsets, out=out,
+                      bias=bias, workspace=workspace)
     T, K = x.shape
     groups = q.shape[0] if lead == 3 else 1
     N = q.shape[-2]
@@ -264,10 +263,10 @@ def w4_gemm(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, *, zeros=Non
         raise ValueError(f"scales {tuple(scales.shape)} do not fit q {tuple(q.shape)}")
     if zeros is not None and (zeros.dtype != torch.uint8 or zeros.shape != scales.shape):
         raise ValueError("zeros must be uint8 of the shape of scales")
-    for name, t in (("q", q), ("scales", scales), ("zeros", zeros)):
-        if t is not None and not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    out = _out("out", out, (T, N), out_dtype, dev, (x.dtype, torch.float32))
+    if not (q.is_contiguous() and scales.is_contiguous() and
+            (zeros is None or zeros.is_contiguous())):
+        raise ValueError("q, scales and zeros must be contiguous")
+    out = _out("out", out, (T, N), out_dtype, x, (x.dtype, torch.float32))
     epi, bias_ptr, stride_bias = _epilogue(epilogue, bias, groups, N)
     ldx, ldo = _ld("x", x), _ld("out", out)
     off = _offsets(offsets, groups) if offsets is not None else 0
@@ -275,11 +274,11 @@ def w4_gemm(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, *, zeros=Non
     need = 0
     if workspace is None and ((px | ldx * 2) & 15 or T > groups):
         need = _abi.gemm_w4_workspace_size(dt, groups, T, N, K, px, ldx, odt)
-    workspace, ws, ws_bytes = _scratch(workspace, need, dev)
+    workspace, ws, ws_bytes = _scratch(workspace, need, x)
     st = _fn("gemm_w4")(dt, groups, T, N, K, px, ldx, q.data_ptr(), scales.data_ptr(),
                         0 if zeros is None else zeros.data_ptr(), K // n_groups, out.data_ptr(),
                         ldo, odt, off, bias_ptr, stride_bias, epi, ws, ws_bytes,
-                        _stream(stream, dev))
+                        _raw_stream(dev) if stream is None else stream)
     if st:
         check(st)
     return out
