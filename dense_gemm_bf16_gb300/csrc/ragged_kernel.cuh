@@ -232,6 +232,17 @@ __device__ __forceinline__ bool rg_tile(const RgParams& p, RgWalk& w, int t, int
     return true;
 }
 
+// A value that all lanes hold, in a register that the compiler knows to be uniform:
+// the tensor-core and TMA instructions take their operands from uniform registers.
+__device__ __forceinline__ int rg_uniform(int v) { return __reduce_max_sync(0xffffffffu, v); }
+
+// Bounded wait of a whole warp (all lanes poll, and agree on the result).
+__device__ __forceinline__ bool rg_all_wait(uint32_t bar, uint32_t parity, const RgParams& p,
+                                            volatile int* abort_flag) {
+    const bool ok = mbar_wait_short(bar, parity, abort_flag, p.status, p.timeout_ns);
+    return __all_sync(0xffffffffu, ok) != 0;
+}
+
 // Bounded wait of a whole warp (one lane polls).
 __device__ __forceinline__ bool rg_warp_wait(uint32_t bar, uint32_t parity, int lane,
                                              volatile int* abort_flag, const RgParams& p) {
@@ -586,6 +597,12 @@ __device__ __forceinline__ void rg_produce(const RgParams& p, const RgCta& x, Rg
     RgTile w;
     for (int t = x.cl; r.ok && rg_tile<CG, BT, FORM>(p, walk, t, x.lane, x.rank, w); t += x.ncl) {
         // As in the MMA warp, the whole warp walks the stages and one lane issues.
+        w.group = rg_uniform(w.group);
+        w.lane0 = rg_uniform(w.lane0);
+        w.n_mma = rg_uniform(w.n_mma);
+        w.b_row = rg_uniform(w.b_row);
+        w.k0 = rg_uniform(w.k0);
+        w.klen = rg_uniform(w.klen);
         const int rows_b = w.n_mma / CG;  // column rows of this CTA
         const int b_row = w.b_row + static_cast<int>(x.rank) * rows_b;
         const int za = p.a_z ? w.group : 0, zb = p.b_z ? w.group : 0;
@@ -602,11 +619,10 @@ __device__ __forceinline__ void rg_produce(const RgParams& p, const RgCta& x, Rg
         if (t == x.cl) {
             int open = 1;
             if (x.lane == 0) open = gate() ? 1 : 0;
-            r.ok = __shfl_sync(0xffffffffu, open, 0) != 0;
+            r.ok = __any_sync(0xffffffffu, x.lane == 0 && open) != 0;
         }
         for (int ks = 0; r.ok && ks < ksteps; ++ks) {
-            r.ok = mbar_wait_short(x.empty0 + 8u * r.stage, r.phase ^ 1u, x.abort_flag, p.status,
-                                   p.timeout_ns);
+            r.ok = rg_all_wait(x.empty0 + 8u * r.stage, r.phase ^ 1u, p, x.abort_flag);
             if (p.test_stall == 1 && r.armed == 0)
                 r.ok = false;  // test only: the MMA warp's bounded wait must expire
             if (!r.ok) break;
@@ -702,10 +718,13 @@ __device__ __forceinline__ void rg_issue(const RgParams& p, const RgCta& x, RgRo
     RgTile w;
     for (int t = x.cl; r.ok && rg_tile<CG, BT, FORM>(p, walk, t, x.lane, x.rank, w); t += x.ncl) {
         if (w.klen == 0) continue;  // no rows: the epilogue writes zeros
+        w.klen = rg_uniform(w.klen);
+        w.n_mma = rg_uniform(w.n_mma);
         const bool tail = FORM == RG_WGRAD && (w.klen & 15) != 0;
         const int klen = FORM == RG_WGRAD ? w.klen & ~15 : w.klen;
         const int ksteps = (klen + 127) / 128;
-        const uint32_t d_tmem = x.tmem_base + static_cast<uint32_t>(r.abuf * BT);
+        const uint32_t d_tmem = static_cast<uint32_t>(rg_uniform(static_cast<int>(x.tmem_base))) +
+                                static_cast<uint32_t>(r.abuf * BT);
         const uint32_t idesc = p.idesc | (static_cast<uint32_t>(w.n_mma >> 3) << 17);
         auto issue = [&](int ks, int steps) {
             const uint64_t ad = a_desc0 + static_cast<uint32_t>(r.stage) * (C::A_BYTES >> 4);
@@ -739,12 +758,10 @@ __device__ __forceinline__ void rg_issue(const RgParams& p, const RgCta& x, RgRo
         // The whole warp walks the stages and one lane issues, so that the stage's
         // addresses stay in uniform registers (16384 x 4096 x 2048: 174 -> 154 us; one
         // lane alone took as long to issue eight MMAs as they take to run).
-        r.ok = mbar_wait_short(x.tempty0 + 8u * r.abuf, r.aphase ^ 1u, x.abort_flag, p.status,
-                               p.timeout_ns);
+        r.ok = rg_all_wait(x.tempty0 + 8u * r.abuf, r.aphase ^ 1u, p, x.abort_flag);
         if (r.ok) tc_fence_after_sync();
         for (int ks = 0; r.ok && ks < ksteps; ++ks) {
-            r.ok = mbar_wait_short(x.full0 + 8u * r.stage, r.phase, x.abort_flag, p.status,
-                                   p.timeout_ns);
+            r.ok = rg_all_wait(x.full0 + 8u * r.stage, r.phase, p, x.abort_flag);
             if (!r.ok) break;
             tc_fence_after_sync();
             const int left = klen - ks * 128;
@@ -757,8 +774,7 @@ __device__ __forceinline__ void rg_issue(const RgParams& p, const RgCta& x, RgRo
         }
         if (FORM == RG_WGRAD && tail && r.ok) {
             const uint32_t b = r.tails & 1u;
-            r.ok = mbar_wait_short(x.tail0 + 16u + 8u * b, r.tails >> 1 & 1u, x.abort_flag,
-                                   p.status, p.timeout_ns);
+            r.ok = rg_all_wait(x.tail0 + 16u + 8u * b, r.tails >> 1 & 1u, p, x.abort_flag);
             ++r.tails;
             if (r.ok) {
                 fence_proxy_async_smem();
