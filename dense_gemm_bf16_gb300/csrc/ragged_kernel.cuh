@@ -325,16 +325,19 @@ __device__ __forceinline__ void rg_act(float (&v)[32], int act) {
 
 // Elements off .. off + 7 of Cin, of which `n` exist (16-bit types); through L2: in
 // a sequence of products other SMs wrote Cin in the same launch.
+// PAD: rows are padded to whole 16 bytes on 16-byte boundaries (RG_SYM's buffers).
+template <bool PAD>
 __device__ __forceinline__ uint4 rg_load8(const RgParams& p, int64_t off, int n) {
     const char* src = static_cast<const char*>(p.Cin) + off * 2;
-    if (p.c_vec && n >= 8) return __ldcg(reinterpret_cast<const uint4*>(src));
+    if (PAD || (p.c_vec && n >= 8)) return __ldcg(reinterpret_cast<const uint4*>(src));
     return rg_load8_slow(src, n);
 }
 
+template <bool PAD>
 __device__ __forceinline__ void rg_store8(const RgParams& p, int64_t off, int n, uint4 v) {
     if (!rg_span_ok(p, off, n < 8 ? n : 8)) return;
     char* dst = static_cast<char*>(p.C) + off * 2;
-    if (p.c_vec && n >= 8)
+    if (PAD || (p.c_vec && n >= 8))
         *reinterpret_cast<uint4*>(dst) = v;
     else
         rg_store8_slow(dst, n, v);
@@ -388,7 +391,7 @@ __device__ __forceinline__ void rg_out16(const RgParams& p, const RgTile& w, uin
         for (int it = 0; it < 4; ++it) {
             const int c = c0 + 8 * it + pcol;
             cin[it] = c < w.ncols && nn > 0
-                          ? rg_load8(p, in_base + (w.out_row + c) * p.ldcin + 8 * part, nn)
+                          ? rg_load8<FORM == RG_SYM>(p, in_base + (w.out_row + c) * p.ldcin + 8 * part, nn)
                           : make_uint4(0, 0, 0, 0);
         }
     };
@@ -407,7 +410,7 @@ __device__ __forceinline__ void rg_out16(const RgParams& p, const RgTile& w, uin
         for (int it = 0; it < 4; ++it) {
             const int c = c0 + 8 * it + pcol;
             if (c < w.ncols && nn > 0)
-                rg_store8(p, c_base + (w.out_row + c) * p.ldc + 8 * part, nn,
+                rg_store8<FORM == RG_SYM>(p, c_base + (w.out_row + c) * p.ldc + 8 * part, nn,
                           *reinterpret_cast<const uint4*>(buf + tile + rg_at(8 * it + pcol, part)));
         }
     };
@@ -497,7 +500,7 @@ __device__ __forceinline__ void rg_out16(const RgParams& p, const RgTile& w, uin
 #pragma unroll
             for (int it = 0; it < 4; ++it)
                 if (nl0 + 8 * it + pcol < p.n_lane)
-                    rg_store8(p, w.group * p.stride_c + (nl0 + 8 * it + pcol) * p.ldc + w.col0 +
+                    rg_store8<FORM == RG_SYM>(p, w.group * p.stride_c + (nl0 + 8 * it + pcol) * p.ldc + w.col0 +
                                      c0 + 8 * part,
                               8, *reinterpret_cast<const uint4*>(buf + 2048 +
                                                                  rg_at(8 * it + pcol, part)));
