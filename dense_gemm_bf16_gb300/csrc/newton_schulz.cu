@@ -4,8 +4,9 @@
 //
 // The norm sums squares in fp32 with a fixed order (threads, then blocks), so
 // results repeat.  Squares of large or small entries would leave fp32's range,
-// so entries are summed in three ranges (Blue's method): above 2^60 as
-// (2^-64 x)^2, below 2^-60 as (2^64 x)^2, and the rest as they are.
+// so entries are summed in three ranges (Blue's method): above 2^40 as
+// (2^-88 x)^2, below 2^-40 as (2^88 x)^2, and the rest as they are: every square
+// lies in 2^-122 .. 2^96, so that 2^31 of them still fit.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -16,10 +17,10 @@ namespace dg {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr float kBig = 1.152921504606846976e18f;       // 2^60
-constexpr float kSmall = 8.673617379884035472e-19f;    // 2^-60
-constexpr float kDown = 5.421010862427522170e-20f;     // 2^-64
-constexpr float kUp = 1.8446744073709551616e19f;       // 2^64
+constexpr float kBig = 1.099511627776e12f;             // 2^40
+constexpr float kSmall = 9.094947017729282379e-13f;    // 2^-40
+constexpr float kDown = 3.231174267785264355e-27f;     // 2^-88
+constexpr float kUp = 3.094850098213450687e26f;        // 2^88
 
 struct Sum3 {
     float big, mid, small;
@@ -101,7 +102,7 @@ template <int GDT>
 __global__ void __launch_bounds__(kThreads) ns_scale_kernel(const NsParams p) {
     const int64_t b = blockIdx.x / p.parts;
     const int part = static_cast<int>(blockIdx.x - b * p.parts);
-    __shared__ float factor;
+    __shared__ float factor[2];
     if (threadIdx.x < 32) {
         // every block adds its matrix's partial sums in the same order
         float s[3] = {0.0f, 0.0f, 0.0f};
@@ -112,15 +113,20 @@ __global__ void __launch_bounds__(kThreads) ns_scale_kernel(const NsParams p) {
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) s[k] += __shfl_xor_sync(0xffffffffu, s[k], d);
         if (threadIdx.x == 0) {
-            constexpr double down = 5.421010862427522170e-20;  // 2^-64
-            const double sq = static_cast<double>(s[0]) / (down * down) + s[1] +
+            constexpr double up = kUp, down = kDown;
+            const double sq = static_cast<double>(s[0]) * (up * up) + s[1] +
                               static_cast<double>(s[2]) * (down * down);
-            factor = static_cast<float>(p.scale / (sqrt(sq) + static_cast<double>(p.eps)));
+            // the factor itself may leave fp32's range: its first part is a power of
+            // two that brings the entries near 1
+            const double f = static_cast<double>(p.scale) / (sqrt(sq) + static_cast<double>(p.eps));
+            const double pre = f > up ? up : f < down ? down : 1.0;
+            factor[0] = static_cast<float>(pre);
+            factor[1] = static_cast<float>(f / pre);
         }
     }
     if (blockIdx.x == 0 && threadIdx.x == 32) *p.arrived = 0u;
     __syncthreads();
-    const float f = factor;
+    const float f0 = factor[0], f1 = factor[1];
     __half* X = static_cast<__half*>(p.X) + b * p.M * p.ldx;
     for (int r = part; r < p.M; r += p.parts)
         for (int c = threadIdx.x * 8; c < p.N; c += kThreads * 8) {
@@ -129,7 +135,7 @@ __global__ void __launch_bounds__(kThreads) ns_scale_kernel(const NsParams p) {
             uint32_t w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const __half2 h = __floats2half2_rn(v[2 * i] * f, v[2 * i + 1] * f);
+                const __half2 h = __floats2half2_rn(v[2 * i] * f0 * f1, v[2 * i + 1] * f0 * f1);
                 w[i] = *reinterpret_cast<const uint32_t*>(&h);
             }
             // rows of X are padded to 8 elements, so the last store stays in its row
