@@ -268,10 +268,11 @@ __device__ __forceinline__ void w4_fetch(const W4Params& p, int64_t row, int gi,
     for (int k = 0; k < (NG + 3) / 4; ++k) v.z[i][k] = 0u;
 #pragma unroll
     for (int k = 0; k < NG; ++k) {
-        // (groups past K read the last one: they multiply zeros)
-        const int g = gi + k < kg ? gi + k : kg - 1;
-        v.s[i][k / 2] |= static_cast<uint32_t>(__ldg(s + g)) << (16 * (k & 1));
-        if (p.zeros) v.z[i][k / 4] |= static_cast<uint32_t>(__ldg(z + g)) << (8 * (k & 3));
+        // (groups past K: zero times zero)
+        if (gi + k < kg) {
+            v.s[i][k / 2] |= static_cast<uint32_t>(__ldg(s + gi + k)) << (16 * (k & 1));
+            if (p.zeros) v.z[i][k / 4] |= static_cast<uint32_t>(__ldg(z + gi + k)) << (8 * (k & 3));
+        }
     }
 }
 
@@ -323,8 +324,9 @@ __global__ void __launch_bounds__(W4Cfg<MT, GROUP>::THREADS, 1) w4_kernel(const 
         int stage = 0;
         uint32_t phase = 0, armed = 0;
         bool ok = true;
-        for (int u = u0; ok && w4_unit<MT>(p, walk, u, lane, w); u += nu) {
-            if (lane == 0) {
+        // (after a failed wait the units' cluster barriers still run)
+        for (int u = u0; (ok || p.splits > 1) && w4_unit<MT>(p, walk, u, lane, w); u += nu) {
+            if (ok && lane == 0) {
                 const uint64_t pol_q = l2_policy_evict_first();
                 const uint64_t pol_x = l2_policy_evict_last();
                 const int n = st1 - st0;
@@ -370,7 +372,6 @@ __global__ void __launch_bounds__(W4Cfg<MT, GROUP>::THREADS, 1) w4_kernel(const 
                 // the consumers' two cluster barriers of the unit
                 cluster_sync();
                 cluster_sync();
-                if (!ok) break;
             }
         }
         // every issued copy lands before the CTA exits

@@ -490,6 +490,19 @@ def test_w4_rows_do_not_mix():
         assert np.array_equal(got[keep], want[keep]) and np.isnan(got[3]).all()
 
 
+@pytest.mark.parametrize("group", [32, 128])
+def test_w4_infinite_scale_in_a_last_partial_stage(group):
+    """The row's output is infinite, and no other one changes."""
+    rng = np.random.default_rng(44)
+    x, q, s, z = w4_case(rng, 2, 20, 384, group, False)
+    s[7, -1] = float("inf")
+    x[:, -group:] = 1                        # (the last group's sum of q - 8, made positive)
+    q[7, -group // 2:] = 0x99
+    want = ref.w4(x, q, s, z)
+    got = ref.f64(w4_run(x, q, s, z, out_dtype=F32))
+    assert np.isposinf(want[:, 7]).all() and np.array_equal(got, want)
+
+
 def test_w4_repeats():
     g = torch.Generator(device=DEV).manual_seed(4)
     x = torch.randn((3, 4096), generator=g, device=DEV).to(BF)
