@@ -2,6 +2,7 @@
 // copies, tensor maps and launches.  No device memory is allocated here.
 #include <stdint.h>
 
+#include <cmath>
 #include <cstring>
 #include <new>
 
@@ -204,6 +205,7 @@ gemm_status_t rg_fill(const RgProblem& q, const DeviceInfo& d, int cg, int bt, R
                                   q.stride_cin * es % 16 == 0));
     p.alpha = q.alpha;
     p.beta = q.beta;
+    p.diag = q.diag;
     p.bias = q.bias;
     p.stride_bias = q.stride_bias;
     p.act = q.act;
@@ -448,7 +450,8 @@ bool ns_layout(int64_t batch, int64_t M, int64_t N, NsLayout* l) {
     l->x_bytes = static_cast<size_t>(round_up(batch * M * l->ldx * 2, 256));
     l->s_bytes = static_cast<size_t>(round_up(batch * l->side * l->lds * 2, 256));
     l->part_bytes = static_cast<size_t>(round_up(batch * parts * 12, 256));
-    l->total = 2 * l->x_bytes + 2 * l->s_bytes + l->part_bytes + 256;
+    l->total = 2 * l->x_bytes + 2 * l->s_bytes + l->part_bytes +
+               static_cast<size_t>(round_up(batch * 4, 256));
     return true;
 }
 
@@ -505,6 +508,12 @@ gemm_status_t gemm_newton_schulz(gemm_dtype_t g_dtype, int64_t batch, int64_t M,
     n.eps = eps;
     n.scale = kNsX;
     n.arrived = reinterpret_cast<unsigned int*>(P + l.s_bytes + l.part_bytes);
+    // a X + b S X + c S S X = P X, with P from a square completed, so that no product
+    // reads its own kind of matrix back: with Y = S + b / (2 c),
+    //   P = a + b S + c S S = c Y Y + (a - b b / (4 c)).
+    // Where b / (2 c) would cost Y its bits (or c is zero), Y is S and P adds b S.
+    const bool squared = std::fabs(b) <= 4.0f * std::fabs(c) && c != 0.0f;
+    const float shift = squared ? b / (2.0f * c) : 0.0f;
     const bool wide = M <= N;
     const int64_t xs = batch > 1 ? M * l.ldx : 0, ss = batch > 1 ? l.side * l.lds : 0;
     int cg = 0, bt = 0;
@@ -526,7 +535,7 @@ gemm_status_t gemm_newton_schulz(gemm_dtype_t g_dtype, int64_t batch, int64_t M,
     seq->arrived = n.arrived;
     for (int odd = 0; odd < 2 && st == GEMM_OK; ++odd) {
         const void* X = x[odd];
-        // S = X X^T (K-major) or X^T X (MN-major), times kNsS
+        // Y = X X^T (K-major) or X^T X (MN-major), shifted, times kNsS
         RgProblem q{};
         q.form = RG_SYM;
         q.dt = DT_F16;
@@ -539,16 +548,18 @@ gemm_status_t gemm_newton_schulz(gemm_dtype_t g_dtype, int64_t batch, int64_t M,
         q.stride_c = q.stride_cin = ss;
         q.c_dtype = q.cin_dtype = DT_F16;
         q.alpha = kNsS / (kNsX * kNsX);
+        q.diag = shift * kNsS;
         st = add(q, &seq->ph[3 * odd]);
-        // P = b S + c S S, times kNsS
+        // P = c Y Y + beta Y + constant, times kNsS
         q.K = l.side;
         q.a = q.b = RgOperand{S, l.lds, ss, false, l.side, l.side};
         q.C = P;
         q.Cin = S;
         q.alpha = c / kNsS;
-        q.beta = b;
+        q.beta = squared ? 0.0f : b;
+        q.diag = (squared ? static_cast<float>(a - 0.25 * b * (static_cast<double>(b) / c)) : a) * kNsS;
         if (st == GEMM_OK) st = add(q, &seq->ph[3 * odd + 1]);
-        // X <- a X + P X, or a X + X P
+        // X <- P X, or X P
         RgProblem u{};
         u.form = RG_ROWS;
         u.dt = DT_F16;
@@ -559,11 +570,7 @@ gemm_status_t gemm_newton_schulz(gemm_dtype_t g_dtype, int64_t batch, int64_t M,
         const RgOperand sym{P, l.lds, ss, false, l.side, l.side};
         u.a = wide ? RgOperand{X, l.ldx, xs, true, N, M} : sym;
         u.b = wide ? sym : RgOperand{X, l.ldx, xs, false, M, N};
-        u.Cin = X;
-        u.ldcin = l.ldx;
-        u.stride_cin = xs;
         u.alpha = 1.0f / kNsS;
-        u.beta = a;
         u.c_dtype = u.cin_dtype = DT_F16;
         u.C = x[1 - odd];
         u.ldc = l.ldx;
@@ -571,7 +578,6 @@ gemm_status_t gemm_newton_schulz(gemm_dtype_t g_dtype, int64_t batch, int64_t M,
         if (st == GEMM_OK) st = add(u, &seq->ph[3 * odd + 2]);
         if (((steps - 1) & 1) == odd) {
             u.alpha /= kNsX;
-            u.beta /= kNsX;
             u.C = O;
             u.ldc = ldo;
             u.stride_c = batch > 1 ? stride_o : 0;

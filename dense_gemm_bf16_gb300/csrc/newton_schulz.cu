@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kThreads) ns_scale_kernel(const NsParams p) {
             factor[1] = static_cast<float>(f / pre);
         }
     }
-    if (blockIdx.x == 0 && threadIdx.x == 32) *p.arrived = 0u;
+    if (part == 0 && threadIdx.x == 32) p.arrived[b] = 0u;
     __syncthreads();
     const float f0 = factor[0], f1 = factor[1];
     __half* X = static_cast<__half*>(p.X) + b * p.M * p.ldx;

@@ -54,6 +54,7 @@ struct RgParams {
     int32_t c_dtype, cin_dtype;  // types of one size
     int32_t c_vec;           // C (and Cin) rows start on 16-byte boundaries
     float alpha, beta;
+    float diag;              // RG_SYM: added on the diagonal
     const float* bias;       // [groups][n_lane] with stride_bias, or null
     int64_t stride_bias;
     int32_t act;
@@ -72,14 +73,15 @@ cudaError_t rg_launch_wgrad(int cg, int bt, const RgParams& p, int grid, cudaStr
 cudaError_t rg_prepare_rows();   // kernel attributes (once per device)
 cudaError_t rg_prepare_wgrad();
 
-// A sequence of products in one cooperative launch, with a barrier over the grid
-// between them: `steps` times the three products of a Newton-Schulz step.  ph[0..2]
+// A sequence of products in one cooperative launch, each waiting for the one before
+// matrix by matrix: `steps` times the three products of a Newton-Schulz step.  ph[0..2]
 // serve even steps, ph[3..5] odd ones (the state alternates between two buffers),
 // ph[6] is the last step's third product.
 struct RgSeq {
     RgParams ph[7];
     int32_t steps;
-    unsigned int* arrived;   // one word, zero at the start: CTAs that finished a product
+    unsigned int* arrived;   // a word per matrix, zero at the start: epilogue warps that
+                             // finished a tile of it
 };
 cudaError_t rg_launch_seq(int cg, int bt, const RgSeq& q, int grid, cudaStream_t stream);
 cudaError_t rg_prepare_seq();
@@ -132,6 +134,7 @@ struct RgProblem {
     int64_t ldc, stride_c, ldcin, stride_cin;
     int c_dtype, cin_dtype;  // cin_dtype: read where beta != 0, of c_dtype's size
     float alpha, beta;
+    float diag;              // RG_SYM: added on the diagonal
     const float* bias;
     int64_t stride_bias;
     int act;
@@ -192,7 +195,7 @@ struct NsParams {
     void* X;                 // fp16, [batch][M][ldx]
     int64_t ldx;
     float eps, scale;
-    unsigned int* arrived;   // zeroed for the sequence that follows
+    unsigned int* arrived;   // [batch], zeroed for the sequence that follows
 };
 cudaError_t ns_norm_launch(const NsParams& p, cudaStream_t stream);
 cudaError_t ns_scale_launch(const NsParams& p, cudaStream_t stream);

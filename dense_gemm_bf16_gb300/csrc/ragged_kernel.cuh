@@ -20,8 +20,9 @@
 //             group: its 16 rows are loaded apart, at the start of the tile, the
 //             rows past the group's end (finite or not) are overwritten with
 //             zeros in shared memory, and the tile's last MMA takes them.
-//   RG_SYM    S = X X^T (or X^T X), and b S + c S S: only tiles on or below
-//             the diagonal are computed, and each is written to both places.
+//   RG_SYM    X X^T (or X^T X), plus beta Cin and a multiple of the unit matrix:
+//             only tiles on or below the diagonal are computed, and each is
+//             written to both places.
 //
 // Warps: 0 TMA producer, 1 MMA issuer, 10 (RG_WGRAD) ragged tails, 2-9 epilogue,
 // two per tensor-memory lane quarter taking 32-column chunks in
@@ -45,6 +46,8 @@
 // drains its copies and MMAs, frees tensor memory and returns.
 #pragma once
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "epilogue.cuh"
 #include "ptx.cuh"
@@ -81,7 +84,7 @@ struct RgCfg {
     static constexpr uint32_t TAIL_AT = EPI_SMEM / 2, TAIL_BYTES = 8192;
     static_assert(B_ROWS < 64 || 2 * TAIL_BYTES <= EPI_SMEM / 2, "tail buffers");
     static_assert(TAIL_A + TAIL_B <= TAIL_BYTES, "tail buffer");
-    static_assert((2 * STAGES + 12) * 8 + 8 <= BAR_BYTES, "barrier area too small");
+    static_assert((2 * STAGES + 11) * 8 + 8 <= BAR_BYTES, "barrier area too small");
 };
 
 struct RgTile {
@@ -453,8 +456,10 @@ __device__ __forceinline__ void rg_out16(const RgParams& p, const RgTile& w, uin
         }
         return;
     }
+    // (RG_SYM: Cin comes from the product before, which is known to be complete only here)
+    if (FORM == RG_SYM && !ready()) return;
     if (beta) load_in(first);
-    if (!ready()) return;
+    if (FORM != RG_SYM && !ready()) return;
 #pragma unroll 1
     for (int c0 = first; c0 < w.ncols; c0 += 64) {
         uint32_t r[32], pk[4][4];
@@ -484,6 +489,13 @@ __device__ __forceinline__ void rg_out16(const RgParams& p, const RgTile& w, uin
                 }
             }
             if (FORM != RG_ROWS) __syncwarp();  // (Cin's place is written again)
+        }
+        if (FORM == RG_SYM && w.diag && w.col0 + c0 == nl0) {
+            // a 32 x 32 block on the diagonal: lane 16 h + 8 g + pcol, column 8 b + 2 part + k
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (((i >> 2) & 3) == 2 * (i >> 4) + ((i >> 1) & 1) && 2 * part + (i & 1) == pcol)
+                    v[i] += p.diag;
         }
         if (ACT) rg_act(v, p.act);
         rg_pack16(p.c_dtype, v, pk);
@@ -566,11 +578,16 @@ __device__ __forceinline__ void rg_out32(const RgParams& p, const RgTile& w, uin
     }
 }
 
+// Products that stand alone wait for nothing and tell no one.
+struct RgAlone {
+    __device__ bool operator()(int) const { return true; }
+};
+
 // What the roles of a CTA share.
 struct RgCta {
     uint8_t* smem;
     uint32_t sA0, sB0;
-    uint32_t full0, empty0, tail0, tfull0, tempty0, drain_bar, gate_bar;
+    uint32_t full0, empty0, tail0, tfull0, tempty0, drain_bar;
     uint32_t tmem_base;
     volatile int* abort_flag;
     uint32_t rank;   // CTA of the pair
@@ -591,14 +608,16 @@ struct RgRole {
 };
 
 // ------------------------------------------------ TMA producer (a warp)
-// `gate` runs before the first load (false: gave up), once the first tile is known.
+// Tiles first, first + clusters, ...  gate(group) runs in lane 0 before a tile's loads
+// (false: gave up).
 template <int CG, int BT, int FORM, typename Gate>
-__device__ __forceinline__ void rg_produce(const RgParams& p, const RgCta& x, RgRole& r, Gate gate) {
+__device__ __forceinline__ void rg_produce(const RgParams& p, const RgCta& x, RgRole& r, int first,
+                                           Gate gate) {
     using C = RgCfg<CG, BT>;
     const uint64_t pol = l2_policy_evict_normal();
     RgWalk walk = rg_begin<FORM>(p, x.lane);
     RgTile w;
-    for (int t = x.cl; r.ok && rg_tile<CG, BT, FORM>(p, walk, t, x.lane, x.rank, w); t += x.ncl) {
+    for (int t = first; r.ok && rg_tile<CG, BT, FORM>(p, walk, t, x.lane, x.rank, w); t += x.ncl) {
         // As in the MMA warp, the whole warp walks the stages and one lane issues.
         w.group = rg_uniform(w.group);
         w.lane0 = rg_uniform(w.lane0);
@@ -619,10 +638,10 @@ __device__ __forceinline__ void rg_produce(const RgParams& p, const RgCta& x, Rg
         const uint32_t bytes = C::A_BYTES + b_bytes;
         // (RG_WGRAD: whole K = 16 steps; the tail warp loads the rest)
         const int ksteps = ((FORM == RG_WGRAD ? w.klen & ~15 : w.klen) + 127) / 128;
-        if (t == x.cl) {
+        if constexpr (!std::is_same<Gate, RgAlone>::value) {
             int open = 1;
-            if (x.lane == 0) open = gate() ? 1 : 0;
-            r.ok = __any_sync(0xffffffffu, x.lane == 0 && open) != 0;
+            if (x.lane == 0) open = gate(w.group) ? 1 : 0;
+            r.ok = __all_sync(0xffffffffu, open) != 0;
         }
         for (int ks = 0; r.ok && ks < ksteps; ++ks) {
             r.ok = rg_all_wait(x.empty0 + 8u * r.stage, r.phase ^ 1u, p, x.abort_flag);
@@ -706,7 +725,7 @@ __device__ __forceinline__ void rg_produce_end(const RgParams& p, const RgCta& x
 // ------------------------------------------------ MMA issuer (a warp)
 // (nothing to do in the pair's peer)
 template <int CG, int BT, int FORM>
-__device__ __forceinline__ void rg_issue(const RgParams& p, const RgCta& x, RgRole& r) {
+__device__ __forceinline__ void rg_issue(const RgParams& p, const RgCta& x, RgRole& r, int first) {
     using C = RgCfg<CG, BT>;
     constexpr uint16_t kPair = 3u;
     const bool a_mn = p.a_mn != 0, b_mn = p.b_mn != 0;
@@ -719,7 +738,7 @@ __device__ __forceinline__ void rg_issue(const RgParams& p, const RgCta& x, RgRo
     if (CG == 2 && !x.leader) return;
     RgWalk walk = rg_begin<FORM>(p, x.lane);
     RgTile w;
-    for (int t = x.cl; r.ok && rg_tile<CG, BT, FORM>(p, walk, t, x.lane, x.rank, w); t += x.ncl) {
+    for (int t = first; r.ok && rg_tile<CG, BT, FORM>(p, walk, t, x.lane, x.rank, w); t += x.ncl) {
         if (w.klen == 0) continue;  // no rows: the epilogue writes zeros
         w.klen = rg_uniform(w.klen);
         w.n_mma = rg_uniform(w.n_mma);
@@ -876,20 +895,17 @@ __device__ __forceinline__ void rg_issue_end(const RgParams& p, const RgCta& x, 
 }
 
 // ------------------------------------------------ epilogue (a warp of eight)
-template <int CG, int BT, int FORM, bool ACT, typename Gate>
-__device__ __forceinline__ void rg_epilogue(const RgParams& p, const RgCta& x, RgRole& r, int warp,
-                                            uint8_t* buf, Gate gate) {
-    // (gate: before the first tile's Cin is read; r.ok goes false, and stays so, when a wait gave up)
+// told(group) runs in the whole warp after its part of a tile has been stored; r.ok goes
+// false when a wait gave up.
+template <int CG, int BT, int FORM, bool ACT, typename Told>
+__device__ __forceinline__ void rg_epilogue(const RgParams& p, const RgCta& x, RgRole& r, int first,
+                                            int warp, uint8_t* buf, Told told) {
     const int q = warp & 3;            // tensor-memory lane quarter of this warp
     const int half = (warp - 2) >> 2;  // which 32-column chunks it takes
     const uint32_t lane_field = static_cast<uint32_t>(q * 32) << 16;
     RgWalk walk = rg_begin<FORM>(p, x.lane);
     RgTile w;
-    for (int t = x.cl; rg_tile<CG, BT, FORM>(p, walk, t, x.lane, x.rank, w); t += x.ncl) {
-        if (t == x.cl && !gate()) {
-            r.ok = false;
-            break;
-        }
+    for (int t = first; rg_tile<CG, BT, FORM>(p, walk, t, x.lane, x.rank, w); t += x.ncl) {
         const bool empty = w.klen == 0;
         const int nl0 = w.lane0 + q * 32;  // first output column of this warp
         auto ready = [&]() {
@@ -912,6 +928,7 @@ __device__ __forceinline__ void rg_epilogue(const RgParams& p, const RgCta& x, R
         else
             rg_out16<FORM, ACT>(p, w, tmem_row, nl0, half, x.lane, buf, empty, ready, release);
         if (!r.ok) break;
+        told(w.group);
         if (!empty && ++r.abuf == 2) {
             r.abuf = 0;
             r.aphase ^= 1u;
@@ -936,15 +953,14 @@ __device__ __forceinline__ RgCta rg_setup(const RgParams& p, uint8_t* smem_raw) 
     x.sB0 = x.sA0 + C::STAGES * C::A_BYTES;
     uint64_t* bars = reinterpret_cast<uint64_t*>(x.smem + C::STAGES * C::STAGE_BYTES + C::EPI_SMEM);
     // full[STAGES], empty[STAGES], tail_full[2], tail_ready[2], tail_empty[2],
-    // tmem_full[2], tmem_empty[2], drain, gate
+    // tmem_full[2], tmem_empty[2], drain
     x.full0 = smem_u32(bars);
     x.empty0 = x.full0 + 8u * C::STAGES;
     x.tail0 = x.full0 + 16u * C::STAGES;
     x.tfull0 = x.tail0 + 48u;
     x.tempty0 = x.tfull0 + 16u;
     x.drain_bar = x.tempty0 + 16u;
-    x.gate_bar = x.drain_bar + 8u;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * C::STAGES + 12);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * C::STAGES + 11);
     x.abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
@@ -960,7 +976,6 @@ __device__ __forceinline__ RgCta rg_setup(const RgParams& p, uint8_t* smem_raw) 
             mbar_init(x.tempty0 + 8u * b, CG * C::EPI_WARPS);
         }
         mbar_init(x.drain_bar, 1);
-        mbar_init(x.gate_bar, 1);  // a sequence's producer has seen the product before
         *x.abort_flag = 0;
         fence_mbar_init();
         if (p.maps) {
@@ -1003,19 +1018,19 @@ __global__ void __launch_bounds__(RgCfg<CG, BT>::threads(FORM), 1)
     const int warp = threadIdx.x >> 5;
     RgRole r;
     if (warp == 0) {
-        rg_produce<CG, BT, FORM>(p, x, r, [] { return true; });
+        rg_produce<CG, BT, FORM>(p, x, r, x.cl, RgAlone());
         rg_produce_end<CG, BT>(p, x, r);
     } else if (warp == 1) {
-        rg_issue<CG, BT, FORM>(p, x, r);
+        rg_issue<CG, BT, FORM>(p, x, r, x.cl);
         rg_issue_end<CG>(p, x, r);
     } else if (FORM == RG_WGRAD && warp == 2 + C::EPI_WARPS) {
         rg_tails<CG, BT>(p, x, r);
     } else {
         rg_epilogue<CG, BT, FORM, FORM == RG_ROWS>(
-            p, x, r, warp,
+            p, x, r, x.cl, warp,
             x.smem + C::STAGES * C::STAGE_BYTES +
                 (warp - 2) * (FORM == RG_WGRAD ? C::EPI_WARP / 2 : C::EPI_WARP),
-            [] { return true; });
+            RgAlone());
     }
     rg_teardown<CG, BT>(x);
 }

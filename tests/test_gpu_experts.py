@@ -351,6 +351,32 @@ def test_newton_schulz_pairs_and_steps():
         assert err <= ns_bound(steps) + 2.0 ** -12, (steps, err)
 
 
+@pytest.mark.parametrize("coefficients,steps", [((1.5, -0.5, 0.0), 6), ((1.875, -1.25, 0.375), 4),
+                                                ((2.0, -1.5, 0.3), 3), ((1.0, 0.0, -0.25), 2),
+                                                ((0.5, 0.0, 0.0), 2)])
+@pytest.mark.parametrize("shape", [(200, 136), (9, 130, 300)])
+def test_newton_schulz_other_coefficients(shape, coefficients, steps):
+    """Polynomials whose square is completed, and such (c zero or small) whose is not."""
+    rng = np.random.default_rng(36)
+    G = torch.from_numpy(rng.standard_normal(shape).astype(np.float32))
+    got = dg.newton_schulz(G.to(DEV), steps=steps, coefficients=coefficients, out_dtype=HF)
+    want = ref.newton_schulz(G, steps, coefficients)
+    err = np.linalg.norm(ref.f64(got) - want) / np.linalg.norm(want)
+    assert err <= ns_bound(steps) + 2.0 ** -12, err
+
+
+def test_newton_schulz_matrices_of_a_batch_do_not_depend_on_each_other():
+    """Each matrix of a batch comes out as it does alone (which may take another tile
+    shape, so to the output's rounding), and repeats bit for bit."""
+    G = torch.randn((37, 256, 384), generator=torch.Generator(device=DEV).manual_seed(2), device=DEV)
+    for _ in range(5):
+        got = dg.newton_schulz(G)
+        for i in (0, 17, 36):
+            alone = dg.newton_schulz(G[i]).float()
+            assert float((got[i].float() - alone).norm()) <= 2.0 ** -8 * float(alone.norm())
+        assert torch.equal(got, dg.newton_schulz(G))
+
+
 def test_newton_schulz_singular_values():
     rng = np.random.default_rng(32)
     G = torch.from_numpy(rng.standard_normal((96, 384)).astype(np.float32))
