@@ -203,6 +203,9 @@ gemm_status_t rg_fill(const RgProblem& q, const DeviceInfo& d, int cg, int bt, R
     p.c_vec = aligned(q.C, 16) && q.ldc * es % 16 == 0 && q.stride_c * es % 16 == 0 &&
               (q.beta == 0.0f || (aligned(q.Cin, 16) && q.ldcin * es % 16 == 0 &&
                                   q.stride_cin * es % 16 == 0));
+    p.c_tma = q.form == RG_WGRAD && p.c_vec &&
+              encode_map_out(&p.tmap_c, q.c_dtype, q.C, q.n_lane, q.n_col, q.groups, q.ldc * es,
+                             q.stride_c * es);
     p.alpha = q.alpha;
     p.beta = q.beta;
     p.diag = q.diag;

@@ -1100,6 +1100,26 @@ bool encode_map16(CUtensorMap* map, int dt, const void* ptr, int64_t inner, int6
                       ptr, inner, outer, depth, outer_stride, depth_stride, box_inner, box_outer);
 }
 
+bool encode_map_out(CUtensorMap* map, int dt, const void* ptr, int64_t cols, int64_t rows,
+                    int64_t depth, int64_t row_stride, int64_t depth_stride) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    if (depth == 1) depth_stride = row_stride;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                          static_cast<cuuint64_t>(depth)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_stride),
+                             static_cast<cuuint64_t>(depth_stride)};
+    cuuint32_t box[3] = {32u, dt == DT_F32 ? 16u : 32u, 1u};
+    cuuint32_t estr[3] = {1u, 1u, 1u};
+    return fn(map,
+              dt == DT_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                           : (dt == DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                            : CU_TENSOR_MAP_DATA_TYPE_FLOAT16),
+              3u, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              dt == DT_F32 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool encode_map16_k4(CUtensorMap* map, int dt, const void* ptr, int64_t k, int64_t rows,
                      int64_t depth, int64_t row_stride, int64_t depth_stride, uint32_t box_rows) {
     auto fn = encode_fn();

@@ -30,6 +30,7 @@ struct RgParams {
     CUtensorMap tmap_b32;    // column operand, K-major: (K, rows, z), boxes of 64 x 32;
                              // RG_WGRAD: boxes of 64 x 16 rows of the contraction
     CUtensorMap tmap_a16;    // RG_WGRAD: the lane operand's
+    CUtensorMap tmap_c;      // RG_WGRAD: output, where c_tma
     const int32_t* offsets;  // [groups + 1] on the device, or null: equal groups
     int32_t groups;
     int32_t rows;            // T: rows that the offsets index (RG_ROWS, RG_WGRAD)
@@ -52,6 +53,7 @@ struct RgParams {
     const void* Cin;         // beta's input, same type and shape as C
     int64_t ldc, stride_c, ldcin, stride_cin;
     int32_t c_dtype, cin_dtype;  // types of one size
+    int32_t c_tma;           // RG_WGRAD: C leaves by TMA (its base and strides allow)
     int32_t c_vec;           // C (and Cin) rows start on 16-byte boundaries
     float alpha, beta;
     float diag;              // RG_SYM: added on the diagonal
@@ -101,6 +103,10 @@ int take_test_stall();
 bool encode_map16(CUtensorMap* map, int dt, const void* ptr, int64_t inner, int64_t outer,
                   int64_t depth, int64_t outer_stride, int64_t depth_stride, uint32_t box_inner,
                   uint32_t box_outer);
+// Output of 32-column boxes: 32 rows of 64 bytes, swizzled by 64 bytes, or 16 rows of
+// fp32.
+bool encode_map_out(CUtensorMap* map, int dt, const void* ptr, int64_t cols, int64_t rows,
+                    int64_t depth, int64_t row_stride, int64_t depth_stride);
 // K-major matrix with a whole number of 64-wide K blocks as (64, rows, K blocks,
 // depth), in boxes of 64 x box_rows x 2 blocks.
 bool encode_map16_k4(CUtensorMap* map, int dt, const void* ptr, int64_t k, int64_t rows,

@@ -36,7 +36,10 @@
 // 128 contiguous bytes.  Rows of another group are masked per column.  (A
 // first form that turned fp32 values through padded rows with 4-byte stores
 // took 10.6 thousand cycles for a CTA's 128 x 256 tile, more than the main
-// loop of K = 1024.)
+// loop of K = 1024.)  RG_WGRAD's tiles end with their matrix, so its staged tiles
+// leave as TMA boxes that end there too (16 groups, 16384 rows, 2048 x 4096, fp32:
+// 209 -> 198 us).  For the other forms, whose whole boxes could do the same, it gave
+// nothing (187 -> 191 us for the forward product of that size).
 //
 // Work: tiles are dealt round robin to CTAs (pairs).  Where group sizes are on
 // the device, each warp finds its tile by a 32-group window of prefix sums held
@@ -417,6 +420,7 @@ __device__ __forceinline__ void rg_out16(const RgParams& p, const RgTile& w, uin
                           *reinterpret_cast<const uint4*>(buf + tile + rg_at(8 * it + pcol, part)));
         }
     };
+    const bool tma = FORM == RG_WGRAD && p.c_tma;
     const int first = half * 32;
     if (first >= w.ncols || nl0 >= p.n_lane) {
         if (ready()) release();
@@ -469,7 +473,9 @@ __device__ __forceinline__ void rg_out16(const RgParams& p, const RgTile& w, uin
         const bool more = c0 + 64 < w.ncols;
         if (!more) release();
         rg_values(p, r, bias, v);
-        __syncwarp();  // the previous chunk has left the staged tiles
+        // the previous chunk has left the staged tiles
+        if (tma && lane == 0) bulk_wait_group_read<0>();
+        __syncwarp();
         if (beta) {
 #pragma unroll
             for (int it = 0; it < 4; ++it)
@@ -506,6 +512,15 @@ __device__ __forceinline__ void rg_out16(const RgParams& p, const RgTile& w, uin
             if (FORM == RG_SYM && !w.diag)
                 stmatrix_x4(s_in + rg_at(lane, i), pk[i][0], pk[i][1], pk[i][2], pk[i][3]);
         }
+        if (tma) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                tma_store_3d(&p.tmap_c, s_out, nl0, w.out_row + c0, w.group, l2_policy_evict_normal());
+                bulk_commit_group();
+            }
+            continue;
+        }
         __syncwarp();
         store_tile(c0, 0u);
         if (FORM == RG_SYM && !w.diag) {
@@ -521,11 +536,11 @@ __device__ __forceinline__ void rg_out16(const RgParams& p, const RgTile& w, uin
 }
 
 // The same for an fp32 C: one lane (output column) per thread, stores of 32
-// neighbouring columns of one row.
-template <bool ACT, typename Ready, typename Release>
+// neighbouring columns of one row (RG_WGRAD: TMA boxes of 16 rows by 32 columns).
+template <int FORM, bool ACT, typename Ready, typename Release>
 __device__ __forceinline__ void rg_out32(const RgParams& p, const RgTile& w, uint32_t tmem_row,
-                                         int nl0, int half, int lane, bool empty, Ready ready,
-                                         Release release) {
+                                         int nl0, int half, int lane, uint8_t* buf, bool empty,
+                                         Ready ready, Release release) {
     if (!ready()) return;
     const int n = nl0 + lane;
     const int first = half * 32;
@@ -562,6 +577,25 @@ __device__ __forceinline__ void rg_out32(const RgParams& p, const RgTile& w, uin
             for (int i = 0; i < 32; ++i) v[i] = fmaf(p.beta, f[i], v[i]);
         }
         if (ACT) rg_act(v, p.act);
+        if (FORM == RG_WGRAD && p.c_tma) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (c0 + 16 * h >= w.ncols) break;
+                if (lane == 0) bulk_wait_group_read<0>();
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    *reinterpret_cast<float*>(buf + i * 128 + lane * 4) = v[16 * h + i];
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_3d(&p.tmap_c, smem_u32(buf), nl0, w.out_row + c0 + 16 * h, w.group,
+                                 l2_policy_evict_normal());
+                    bulk_commit_group();
+                }
+            }
+            continue;
+        }
         if (!in) continue;
         const int64_t off = w.group * p.stride_c + row * p.ldc + n;
         float* dst = static_cast<float*>(p.C) + off;
@@ -631,7 +665,7 @@ __device__ __forceinline__ void rg_produce(const RgParams& p, const RgCta& x, Rg
         const bool a_mn = p.a_mn, b_mn = p.b_mn, a_k4 = p.a_k4, b_k4 = p.b_k4;
         // K-major columns: whole-tile boxes, or 32-row boxes where those are fewer bytes
         // (one load a block costs as much issue time as bytes: half a tile suffices there)
-        const bool big = !b_mn && (b_k4 ? 4 * rows_b > 3 * C::B_ROWS : 2 * rows_b > C::B_ROWS);
+        const bool big = !b_mn && 4 * rows_b > 3 * C::B_ROWS;
         const int nb = b_mn ? rows_b / 64 : (big ? 1 : (rows_b + 31) / 32);
         const uint32_t b_bytes = b_mn ? nb * 16384u : (big ? C::B_BYTES : nb * 8192u);
         const CUtensorMap* map_b = big || b_mn ? &p.tmap_b : &p.tmap_b32;
@@ -924,7 +958,7 @@ __device__ __forceinline__ void rg_epilogue(const RgParams& p, const RgCta& x, R
                 mbar_arrive_relaxed(mapa_shared(x.tempty0 + 8u * r.abuf, 0u));
         };
         if (p.c_dtype == DT_F32)
-            rg_out32<ACT>(p, w, tmem_row, nl0, half, x.lane, empty, ready, release);
+            rg_out32<FORM, ACT>(p, w, tmem_row, nl0, half, x.lane, buf, empty, ready, release);
         else
             rg_out16<FORM, ACT>(p, w, tmem_row, nl0, half, x.lane, buf, empty, ready, release);
         if (!r.ok) break;
@@ -934,6 +968,7 @@ __device__ __forceinline__ void rg_epilogue(const RgParams& p, const RgCta& x, R
             r.aphase ^= 1u;
         }
     }
+    if (FORM == RG_WGRAD && x.lane == 0) bulk_wait_group_all();  // the staged tiles have been read
     __syncwarp();
 }
 
@@ -981,6 +1016,7 @@ __device__ __forceinline__ RgCta rg_setup(const RgParams& p, uint8_t* smem_raw) 
         if (p.maps) {
             prefetch_tmap(&p.tmap_a);
             prefetch_tmap(&p.tmap_b);
+            if (p.c_tma) prefetch_tmap(&p.tmap_c);
             if (!p.b_mn) prefetch_tmap(&p.tmap_b32);
         }
     }
