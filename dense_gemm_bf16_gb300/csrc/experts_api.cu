@@ -223,7 +223,73 @@ gemm_status_t rg_fill(const RgProblem& q, const DeviceInfo& d, int cg, int bt, R
     return GEMM_OK;
 }
 
+constexpr int64_t kFewRows = 16;
+
+// Few rows (RG_ROWS with offsets): the kernel of w4.cu, with 16-bit weights.
+static bool few_rows(const RgProblem& q, const DeviceInfo& d) {
+    return q.form == RG_ROWS && q.offsets && q.K > 0 && q.T <= kFewRows && true;
+}
+
+static gemm_status_t few_run(const RgProblem& q, const DeviceInfo& d, cudaStream_t stream) {
+    const int64_t avg = cdiv(q.T, q.groups);
+    const int tokens = (q.T < 2 * avg ? q.T : 2 * avg) <= 8 ? 8 : 16;
+    const W4Shape shape = w4_shape(tokens, 0);
+    W4Params p;
+    std::memset(&p, 0, sizeof(p));
+    const int64_t z = q.a.stride != 0 ? q.groups : 1;
+    p.w_mn = q.a.mn;
+    p.w_z = z > 1;
+    p.q4 = !q.a.mn && q.K % 64 == 0;
+    p.x4 = q.K % 64 == 0;
+    const bool ok =
+        (q.a.mn ? encode_map16(&p.tmap_q, q.dt, q.a.ptr, q.n_lane, q.K, z, q.a.ld * 2, q.a.stride * 2,
+                               static_cast<uint32_t>(shape.rows), static_cast<uint32_t>(shape.step))
+         : p.q4 ? encode_map16_k4(&p.tmap_q, q.dt, q.a.ptr, q.K, q.n_lane, z, q.a.ld * 2,
+                                  q.a.stride * 2, static_cast<uint32_t>(shape.rows))
+                : encode_map16(&p.tmap_q, q.dt, q.a.ptr, q.K, q.n_lane, z, q.a.ld * 2,
+                               q.a.stride * 2, 64, static_cast<uint32_t>(shape.rows))) &&
+        (p.x4 ? encode_map16_blocks(&p.tmap_x, q.dt, q.b.ptr, q.K, q.T, q.b.ld * 2,
+                                    static_cast<uint32_t>(tokens),
+                                    static_cast<uint32_t>(shape.step / 64))
+              : encode_map16(&p.tmap_x, q.dt, q.b.ptr, q.K, q.T, 1, q.b.ld * 2, 0, 64,
+                             static_cast<uint32_t>(tokens)));
+    if (!ok) return GEMM_ERR_CUDA;
+    p.offsets = q.offsets;
+    p.groups = static_cast<int32_t>(q.groups);
+    p.T = static_cast<int32_t>(q.T);
+    p.N = static_cast<int32_t>(q.n_lane);
+    p.K = static_cast<int32_t>(q.K);
+    const int64_t n_tiles = cdiv(q.n_lane, shape.rows), steps = cdiv(q.K, shape.step);
+    const int64_t units = n_tiles * (q.T / tokens + (q.groups < q.T ? q.groups : q.T));
+    if (units > kLim) return GEMM_ERR_UNSUPPORTED;
+    int splits = 1;
+    while (splits < 4 && units * splits * 2 <= d.sm_count && steps >= splits * 8) splits *= 2;
+    p.n_tiles = static_cast<int32_t>(n_tiles);
+    p.splits = splits;
+    p.grid = static_cast<int32_t>(units < d.sm_count ? units : d.sm_count);
+    p.C = q.C;
+    p.ldc = q.ldc;
+    p.c_dtype = q.c_dtype;
+    p.alpha = q.alpha;
+    p.beta = q.beta;
+    p.bias = q.bias;
+    p.stride_bias = q.stride_bias;
+    p.act = q.act;
+    p.test_stall = take_test_stall();
+    p.status = d.status;
+    p.timeout_ns = option_timeout_ns();
+#if DG_DEBUG
+    p.dbg_c_elems = (q.T - 1) * q.ldc + q.n_lane;
+#endif
+    if (w4_launch(q.dt, tokens, p, stream) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_CUDA;
+    }
+    return GEMM_OK;
+}
+
 gemm_status_t rg_run(const RgProblem& q, const DeviceInfo& d, cudaStream_t stream) {
+    if (few_rows(q, d)) return few_run(q, d, stream);
     int cg, bt;
     rg_variant(q, d, &cg, &bt);
     RgParams p;
@@ -706,10 +772,10 @@ gemm_status_t gemm_w4(gemm_dtype_t ab_dtype, int64_t groups, int64_t T, int64_t 
     p.q4 = K % 256 == 0;
     p.x4 = K % 64 == 0;
     if (!encode_map8(&p.tmap_q, Q, K / 2, N, groups, static_cast<uint32_t>(shape.rows),
-                     p.q4 ? static_cast<uint32_t>(shape.blocks) : 0u) ||
+                     p.q4 ? static_cast<uint32_t>(shape.step / 256) : 0u) ||
         !(p.x4 ? encode_map16_blocks(&p.tmap_x, ab_dtype, a.ptr, K, T, a.ld * 2,
                                      static_cast<uint32_t>(tokens),
-                                     static_cast<uint32_t>(4 * shape.blocks))
+                                     static_cast<uint32_t>(shape.step / 64))
                : encode_map16(&p.tmap_x, ab_dtype, a.ptr, K, T, 1, a.ld * 2, 0, 64,
                               static_cast<uint32_t>(tokens))))
         return GEMM_ERR_CUDA;
@@ -722,7 +788,7 @@ gemm_status_t gemm_w4(gemm_dtype_t ab_dtype, int64_t groups, int64_t T, int64_t 
     p.N = static_cast<int32_t>(N);
     p.K = static_cast<int32_t>(K);
     p.group = group;
-    const int stage_k = 256 * shape.blocks;
+    const int stage_k = shape.step;
     p.vec = K % stage_k == 0 && aligned(scales, 16) && (!zeros || aligned(zeros, 8));
     const int64_t n_tiles = cdiv(N, shape.rows), steps = cdiv(K, stage_k);
     // units there may be: full token tiles and one more for each non-empty group
@@ -743,9 +809,11 @@ gemm_status_t gemm_w4(gemm_dtype_t ab_dtype, int64_t groups, int64_t T, int64_t 
     p.C = C;
     p.ldc = ldc;
     p.c_dtype = c_dtype;
+    p.alpha = 1.0f;
     p.bias = (epi & 1) ? bias : nullptr;
     p.stride_bias = stride_bias;
     p.act = act;
+    p.test_stall = take_test_stall();
     p.status = d.status;
     p.timeout_ns = option_timeout_ns();
 #if DG_DEBUG

@@ -152,15 +152,19 @@ gemm_status_t rg_fill(const RgProblem& q, const DeviceInfo& d, int cg, int bt, R
                       int64_t* tiles);
 gemm_status_t rg_run(const RgProblem& q, const DeviceInfo& d, cudaStream_t stream);
 
-// ---- 4-bit weights (w4.cu)
+// ---- few rows: 4-bit weights, and 16-bit ones for decoding steps (w4.cu)
 struct W4Params {
-    CUtensorMap tmap_q;      // [groups][N][K / 2] bytes, boxes of 128 bytes x rows (x blocks)
+    CUtensorMap tmap_q;      // [groups][N][K / 2] bytes, boxes of 128 bytes x rows (x blocks);
+                             // 16-bit weights: 64 x rows x 2 blocks, or 64 columns x 128 k
     CUtensorMap tmap_x;      // [T][K], boxes of 64 x the tokens of a tile (x blocks)
     const uint8_t* q;
     const void* scales;
     const uint8_t* zeros;
     const int32_t* offsets;  // or null
-    int32_t groups, T, N, K, group;
+    int32_t groups, T, N, K;
+    int32_t group;           // weights per scale; 0: 16-bit weights
+    int32_t w_mn;            // 16-bit weights: 1: stored with N contiguous
+    int32_t w_z;             // 16-bit weights: 1: the map's z coordinate is the group
     int32_t vec;             // 1: scales and zeros of a stage load as vectors
     int32_t q4, x4;          // 1: the map has blocks as a dimension, a stage is one load
     int32_t n_tiles, splits; // row tiles; CTAs (K slices) of a cluster
@@ -168,19 +172,21 @@ struct W4Params {
     void* C;
     int64_t ldc;
     int32_t c_dtype;
+    float alpha, beta;
     const float* bias;
     int64_t stride_bias;
     int32_t act;
+    int32_t test_stall;      // test only: leave one stage unfilled
     int* status;
     uint64_t timeout_ns;
 #if DG_DEBUG
     int64_t dbg_c_elems;
 #endif
 };
-// Shape of the kernel for `tokens` token columns and a scale per `group` weights: weight rows of a unit, and
-// 256-weight blocks of a stage.
+// Shape of the kernel for `tokens` token columns and a scale per `group` weights (0: 16-bit
+// weights): weight rows of a unit, and weights of a row per stage.
 struct W4Shape {
-    int rows, blocks;
+    int rows, step;
 };
 W4Shape w4_shape(int tokens, int group);
 cudaError_t w4_launch(int dt, int tokens, const W4Params& p, cudaStream_t stream);

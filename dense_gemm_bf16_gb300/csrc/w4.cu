@@ -45,17 +45,19 @@ struct W4Cfg {
     // 256-weight blocks of a stage (one where many tokens' or groups' values take
     // the registers)
     static constexpr int BLK = MT <= 16 && GROUP > 32 ? 2 : 1;
-    static constexpr int STEP = 256 * BLK;           // weights of a row per stage
-    static constexpr uint32_t Q_BYTES = RT * 128;    // of a block
+    static constexpr int STEP = GROUP == 0 ? 128 : 256 * BLK;  // weights of a row per stage
+    static constexpr uint32_t Q_BYTES = RT * 128;    // of a block of 4-bit weights
+    static constexpr uint32_t W_BYTES = GROUP == 0 ? RT * STEP * 2 : BLK * Q_BYTES;
     static constexpr uint32_t X_BOX = MT * 128;      // 64 values of MT tokens
-    static constexpr uint32_t STAGE = BLK * (Q_BYTES + 4 * X_BOX);
+    static constexpr int X_BOXES = STEP / 64;
+    static constexpr uint32_t STAGE = W_BYTES + X_BOXES * X_BOX;
     static constexpr int R_LD = RT + 4;
     static constexpr uint32_t R_BYTES = SG * MT * R_LD * 4;
     static constexpr int FIT = (232448 - 1024 - 512 - R_BYTES) / STAGE;
     static constexpr int STAGES = FIT > 16 ? 16 : FIT;
     static constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE + R_BYTES + 512;
     static_assert(STAGES >= 3 && (2 * STAGES + 1) * 8 <= 512, "ring");
-    static_assert(Q_BYTES % 1024 == 0 && X_BOX % 1024 == 0, "swizzle atoms");
+    static_assert(W_BYTES % 1024 == 0 && X_BOX % 1024 == 0, "swizzle atoms");
 };
 
 template <int DT>
@@ -276,13 +278,62 @@ __device__ __forceinline__ void w4_fetch(const W4Params& p, int64_t row, int gi,
     }
 }
 
+// A warp's 16 rows of a stage of 16-bit weights (128 of each row): K-major as two
+// 64-wide blocks of 64 rows, or with the rows contiguous as 128 k of 64 rows.
+template <int DT, int NT, uint32_t X_BOX>
+__device__ __forceinline__ void w16_stage(const uint8_t* ws, const uint8_t* xs, int rg, int lane,
+                                          bool mn, float (&total)[NT][4]) {
+    // ldmatrix: lane l gives a row of matrix l >> 3; the matrices are (rows 0-7, k 0-7),
+    // (rows 8-15, k 0-7), (rows 0-7, k 8-15), (rows 8-15, k 8-15) of 16 rows x 16 k
+    const int l = lane & 7, m = lane >> 3;
+    const uint32_t w0 = smem_u32(ws), x0 = smem_u32(xs);
+    const int row = rg * 16 + (m & 1) * 8 + l;       // K-major: a row's 8 k
+    const int col = rg * 2 + (m & 1);                // rows contiguous: 8 rows of one k
+    float acc[NT][4];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {  // 32 k
+        uint32_t a[2][4];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int kk = 2 * h + s;                // 16 k
+            if (mn) {
+                const int k = kk * 16 + (m >> 1) * 8 + l;
+                ldmatrix_x4_trans(w0 + k * 128 + ((col ^ (k & 7)) << 4), a[s][0], a[s][1], a[s][2],
+                                  a[s][3]);
+            } else {
+                const int part = (kk & 3) * 2 + (m >> 1);
+                ldmatrix_x4(w0 + (kk >> 2) * 8192 + row * 128 + ((part ^ (row & 7)) << 4), a[s][0],
+                            a[s][1], a[s][2], a[s][3]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            uint32_t b[4];                           // k 0-7, 8-15, 16-23, 24-31 of 8 tokens
+            const int part = (h & 1) * 4 + m;
+            ldmatrix_x4(x0 + (h >> 1) * X_BOX + (8 * j + l) * 128 + ((part ^ l) << 4), b[0], b[1],
+                        b[2], b[3]);
+            mma16816<DT>(total[j], a[0], b[0], b[1]);
+            mma16816<DT>(acc[j], a[1], b[2], b[3]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) total[j][i] += acc[j][i];
+}
+
 template <int DT, int MT, int GROUP>
 __global__ void __launch_bounds__(W4Cfg<MT, GROUP>::THREADS, 1) w4_kernel(const __grid_constant__ W4Params p) {
     using C = W4Cfg<MT, GROUP>;
     constexpr int NT = MT / 8;
-    constexpr int CPG = GROUP / 32;        // 16-byte chunks per group
-    constexpr int NG = C::STEP / GROUP;    // groups of a row per stage
-    constexpr int NGB = 256 / GROUP;       // ... per block
+    constexpr int GR = GROUP == 0 ? 128 : GROUP;  // (16-bit weights have no scales)
+    constexpr int CPG = GR / 32;           // 16-byte chunks per group
+    constexpr int NG = GROUP == 0 ? 2 : C::STEP / GR;  // groups of a row per stage
+    constexpr int NGB = 256 / GR;          // ... per block
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -340,10 +391,26 @@ __global__ void __launch_bounds__(W4Cfg<MT, GROUP>::THREADS, 1) w4_kernel(const 
                             break;
                         }
                         const uint32_t fb = full0 + 8u * stage;
+                        if (p.test_stall == 1 && armed == 0) {
+                            ok = false;  // test only: the consumers' bounded waits must expire
+                            break;
+                        }
                         mbar_arrive_expect_tx(fb, C::STAGE);
                         const uint32_t dst = smem_u32(smem) + stage * C::STAGE;
-                        const uint32_t xdst = dst + C::BLK * C::Q_BYTES;
-                        if (p.q4) {
+                        const uint32_t xdst = dst + C::W_BYTES;
+                        if constexpr (GROUP == 0) {
+                            const int k0 = st * C::STEP, wz = p.w_z ? w.group : 0;
+                            if (p.w_mn) {
+                                tma_load_3d(dst, &p.tmap_q, fb, w.n0, k0, wz, pol_q);
+                            } else if (p.q4) {
+                                tma_load_4d_cg<1>(dst, &p.tmap_q, fb, 0, w.n0, k0 / 64, w.group,
+                                                  pol_q);
+                            } else {
+                                tma_load_3d(dst, &p.tmap_q, fb, k0, w.n0, w.group, pol_q);
+                                tma_load_3d(dst + C::W_BYTES / 2, &p.tmap_q, fb, k0 + 64, w.n0,
+                                            w.group, pol_q);
+                            }
+                        } else if (p.q4) {
                             tma_load_4d_cg<1>(dst, &p.tmap_q, fb, 0, w.n0, st * C::BLK, w.group, pol_q);
                         } else {
 #pragma unroll
@@ -352,10 +419,10 @@ __global__ void __launch_bounds__(W4Cfg<MT, GROUP>::THREADS, 1) w4_kernel(const 
                                             (st * C::BLK + j) * 128, w.n0, w.group, pol_q);
                         }
                         if (p.x4) {
-                            tma_load_3d(xdst, &p.tmap_x, fb, 0, w.row0, st * C::BLK * 4, pol_x);
+                            tma_load_3d(xdst, &p.tmap_x, fb, 0, w.row0, st * C::X_BOXES, pol_x);
                         } else {
 #pragma unroll
-                            for (int j = 0; j < 4 * C::BLK; ++j)
+                            for (int j = 0; j < C::X_BOXES; ++j)
                                 tma_load_3d(xdst + j * C::X_BOX, &p.tmap_x, fb,
                                             st * C::STEP + 64 * j, w.row0, 0, pol_x);
                         }
@@ -388,7 +455,7 @@ __global__ void __launch_bounds__(W4Cfg<MT, GROUP>::THREADS, 1) w4_kernel(const 
         const int cw = warp - 1, gr = lane >> 2, t = lane & 3;
         const int rg = cw % C::RG, sg = cw / C::RG;
         const int r = rg * 16 + gr;  // rows r and r + 8 of the unit
-        const int kg = p.K / GROUP;
+        const int kg = p.K / GR;
         // word t of chunk c of row r of a stage: the chunk is swizzled by the row
         const uint32_t q_at = static_cast<uint32_t>(r * 128 + t * 4);
         const W4Bits bits = w4_bits<DT>();
@@ -412,6 +479,7 @@ __global__ void __launch_bounds__(W4Cfg<MT, GROUP>::THREADS, 1) w4_kernel(const 
             row_hi = static_cast<int64_t>(v.group) * p.N + n_hi;
         };
         auto fetch = [&](int st) {
+            if (GROUP == 0) return;
             w4_fetch<NG>(p, row_lo, st * NG, kg, 0, nxt);
             w4_fetch<NG>(p, row_hi, st * NG, kg, 1, nxt);
         };
@@ -442,9 +510,11 @@ __global__ void __launch_bounds__(W4Cfg<MT, GROUP>::THREADS, 1) w4_kernel(const 
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 const uint8_t* qs = smem + stage * C::STAGE;
-                const uint8_t* xs = qs + C::BLK * C::Q_BYTES;
+                const uint8_t* xs = qs + C::W_BYTES;
+                if constexpr (GROUP == 0)
+                    w16_stage<DT, NT, C::X_BOX>(qs, xs, rg, lane, p.w_mn != 0, total);
 #pragma unroll 1
-                for (int blk = 0; blk < C::BLK; ++blk, qs += C::Q_BYTES, xs += 4 * C::X_BOX) {
+                for (int blk = 0; GROUP != 0 && blk < C::BLK; ++blk, qs += C::Q_BYTES, xs += 4 * C::X_BOX) {
 #pragma unroll
                 for (int gg = 0; gg < NGB; ++gg) {
                     // (two chains of sums where neither tokens nor a short group give
@@ -562,14 +632,18 @@ __global__ void __launch_bounds__(W4Cfg<MT, GROUP>::THREADS, 1) w4_kernel(const 
 #pragma unroll
                         for (int m = 0; m < C::SG; ++m) v += src[m * MT * C::R_LD];
                     }
-                    if (p.bias) v += __ldg(p.bias + done.group * p.stride_bias + n);
-                    v = apply_act(v, p.act);
                     const int64_t off = static_cast<int64_t>(done.row0 + tok) * p.ldc + n;
 #if DG_DEBUG
                     if (!DG_CHECK(off >= 0 && off < p.dbg_c_elems, p.status, STATUS_CHECK_BOUNDS))
                         continue;
 #endif
-                    store_elem(static_cast<char*>(p.C) + off * dt_size(p.c_dtype), p.c_dtype, v);
+                    char* dst = static_cast<char*>(p.C) + off * dt_size(p.c_dtype);
+                    if (GROUP == 0) {
+                        v *= p.alpha;
+                        if (p.beta != 0.0f) v = fmaf(p.beta, load_elem(dst, p.c_dtype), v);
+                    }
+                    if (p.bias) v += __ldg(p.bias + done.group * p.stride_bias + n);
+                    store_elem(dst, p.c_dtype, apply_act(v, p.act));
                 }
             }
             // the sums are read before the next unit's (or the exit) replace them;
@@ -598,6 +672,8 @@ cudaError_t launch_one(const W4Params& p, cudaStream_t stream) {
 
 template <int DT, int MT>
 cudaError_t launch_group(const W4Params& p, cudaStream_t stream) {
+    if constexpr (MT <= 16)
+        if (p.group == 0) return launch_one<DT, MT, 0>(p, stream);
     if (p.group == 32) return launch_one<DT, MT, 32>(p, stream);
     if (p.group == 64) return launch_one<DT, MT, 64>(p, stream);
     return launch_one<DT, MT, 128>(p, stream);
@@ -621,6 +697,8 @@ cudaError_t prepare_one() {
 template <int DT, int MT>
 cudaError_t prepare_group() {
     cudaError_t e = prepare_one<DT, MT, 32>();
+    if constexpr (MT <= 16)
+        if (e == cudaSuccess) e = prepare_one<DT, MT, 0>();
     if (e == cudaSuccess) e = prepare_one<DT, MT, 64>();
     if (e == cudaSuccess) e = prepare_one<DT, MT, 128>();
     return e;
@@ -668,8 +746,9 @@ __global__ void __launch_bounds__(256) w4_dequantise_kernel(const uint32_t* q, c
 }  // namespace
 
 W4Shape w4_shape(int tokens, int group) {
-    if (tokens > 16) return W4Shape{W4Cfg<64, 128>::RT, W4Cfg<64, 128>::BLK};
-    return W4Shape{W4Cfg<16, 128>::RT, group > 32 ? W4Cfg<16, 128>::BLK : W4Cfg<16, 32>::BLK};
+    if (tokens > 16) return W4Shape{W4Cfg<64, 128>::RT, W4Cfg<64, 128>::STEP};
+    return W4Shape{W4Cfg<16, 128>::RT, group == 0 ? W4Cfg<16, 0>::STEP
+                                                  : (group > 32 ? W4Cfg<16, 128>::STEP : W4Cfg<16, 32>::STEP)};
 }
 
 cudaError_t w4_launch(int dt, int tokens, const W4Params& p, cudaStream_t stream) {
