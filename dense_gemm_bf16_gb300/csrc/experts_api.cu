@@ -223,11 +223,15 @@ gemm_status_t rg_fill(const RgProblem& q, const DeviceInfo& d, int cg, int bt, R
     return GEMM_OK;
 }
 
-constexpr int64_t kFewRows = 16;
+// Few rows (RG_ROWS with offsets): the kernel of w4.cu, with 16-bit weights.  Against
+// the ragged kernel, K = 2048 (us): 8 rows, 8 experts of N = 1024 10.5 : 15.3, of
+// N = 4096 28.0 : 43.5; 32 rows, 32 experts of N = 1024 28.4 : 28.8, of N = 4096
+// 88.1 : 85.6; 64 rows, 64 experts of N = 1024 46.4 : 51.1; one expert with 64 rows
+// 9.8 : 13.5; but 192 rows over 64 experts of N = 2048 90.3 : 83.6.
+constexpr int64_t kFewRows = 64;
 
-// Few rows (RG_ROWS with offsets): the kernel of w4.cu, with 16-bit weights.
 static bool few_rows(const RgProblem& q, const DeviceInfo& d) {
-    return q.form == RG_ROWS && q.offsets && q.K > 0 && q.T <= kFewRows && true;
+    return q.form == RG_ROWS && q.offsets && q.K > 0 && q.T <= kFewRows;
 }
 
 static gemm_status_t few_run(const RgProblem& q, const DeviceInfo& d, cudaStream_t stream) {
