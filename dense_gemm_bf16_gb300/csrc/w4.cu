@@ -147,6 +147,20 @@ __device__ __forceinline__ float w4_float(uint16_t u) {
     return __half2float(__ushort_as_half(u));
 }
 
+// (volatile: in order with the waits around them)
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+
+__device__ __forceinline__ uint4 ld_shared_u128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
@@ -281,12 +295,11 @@ __device__ __forceinline__ void w4_fetch(const W4Params& p, int64_t row, int gi,
 // A warp's 16 rows of a stage of 16-bit weights (128 of each row): K-major as two
 // 64-wide blocks of 64 rows, or with the rows contiguous as 128 k of 64 rows.
 template <int DT, int NT, uint32_t X_BOX>
-__device__ __forceinline__ void w16_stage(const uint8_t* ws, const uint8_t* xs, int rg, int lane,
+__device__ __forceinline__ void w16_stage(uint32_t w0, uint32_t x0, int rg, int lane,
                                           bool mn, float (&total)[NT][4]) {
     // ldmatrix: lane l gives a row of matrix l >> 3; the matrices are (rows 0-7, k 0-7),
     // (rows 8-15, k 0-7), (rows 0-7, k 8-15), (rows 8-15, k 8-15) of 16 rows x 16 k
     const int l = lane & 7, m = lane >> 3;
-    const uint32_t w0 = smem_u32(ws), x0 = smem_u32(xs);
     const int row = rg * 16 + (m & 1) * 8 + l;       // K-major: a row's 8 k
     const int col = rg * 2 + (m & 1);                // rows contiguous: 8 rows of one k
     float acc[NT][4];
@@ -457,7 +470,7 @@ __global__ void __launch_bounds__(W4Cfg<MT, GROUP>::THREADS, 1) w4_kernel(const 
         const int r = rg * 16 + gr;  // rows r and r + 8 of the unit
         const int kg = p.K / GR;
         // word t of chunk c of row r of a stage: the chunk is swizzled by the row
-        const uint32_t q_at = static_cast<uint32_t>(r * 128 + t * 4);
+        const uint32_t q_at = static_cast<uint32_t>(r * 128 + t * 4) | static_cast<uint32_t>(gr << 4);
         const W4Bits bits = w4_bits<DT>();
         bool ok = true;
         uint32_t it0 = 0;  // stages of the units before
@@ -498,6 +511,7 @@ __global__ void __launch_bounds__(W4Cfg<MT, GROUP>::THREADS, 1) w4_kernel(const 
             // one's values along with its lane; a column of the product has only its
             // own token)
             const int xr = NT > 1 || gr < w.tokens ? gr : 0;
+            const uint32_t x_at = static_cast<uint32_t>(xr * 128 + ((t ^ xr) << 4));
             for (int st = a0; ok && st < a1; ++st) {
                 const int round = st - a0;
                 const uint32_t it = it0 + static_cast<uint32_t>(
@@ -509,12 +523,14 @@ __global__ void __launch_bounds__(W4Cfg<MT, GROUP>::THREADS, 1) w4_kernel(const 
                 ok = mbar_wait_short(full0 + 8u * stage, turn & 1u, abort_flag, p.status, p.timeout_ns);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                const uint8_t* qs = smem + stage * C::STAGE;
-                const uint8_t* xs = qs + C::W_BYTES;
+                const uint32_t ws = smem_u32(smem) + stage * C::STAGE;
                 if constexpr (GROUP == 0)
-                    w16_stage<DT, NT, C::X_BOX>(qs, xs, rg, lane, p.w_mn != 0, total);
+                    w16_stage<DT, NT, C::X_BOX>(ws, ws + C::W_BYTES, rg, lane, p.w_mn != 0, total);
+                // (stages are aligned, so that the swizzle is an exclusive or of addresses)
+                uint32_t qs = ws + q_at, xs = ws + C::W_BYTES + x_at;
 #pragma unroll 1
                 for (int blk = 0; GROUP != 0 && blk < C::BLK; ++blk, qs += C::Q_BYTES, xs += 4 * C::X_BOX) {
+                const uint32_t xs2 = xs ^ 64u;
 #pragma unroll
                 for (int gg = 0; gg < NGB; ++gg) {
                     // (two chains of sums where neither tokens nor a short group give
@@ -529,9 +545,8 @@ __global__ void __launch_bounds__(W4Cfg<MT, GROUP>::THREADS, 1) w4_kernel(const 
 #pragma unroll
                     for (int cc = 0; cc < CPG; ++cc) {
                         const int c = gg * CPG + cc;
-                        const uint8_t* src = qs + (q_at + static_cast<uint32_t>((c ^ gr) << 4));
-                        const uint32_t lo = *reinterpret_cast<const uint32_t*>(src);
-                        const uint32_t hi = *reinterpret_cast<const uint32_t*>(src + 1024);
+                        const uint32_t src = qs ^ static_cast<uint32_t>(c << 4);
+                        const uint32_t lo = ld_shared_u32(src), hi = ld_shared_u32(src + 1024u);
                         const uint32_t lo4 = lo >> 4, hi4 = hi >> 4;
                         const uint32_t a1[4] = {w4_pair<DT, 0>(lo, lo4, sub_lo, bits),
                                                 w4_pair<DT, 0>(hi, hi4, sub_hi, bits),
@@ -541,11 +556,10 @@ __global__ void __launch_bounds__(W4Cfg<MT, GROUP>::THREADS, 1) w4_kernel(const 
                                                 w4_pair<DT, 2>(hi, hi4, sub_hi, bits),
                                                 w4_pair<DT, 3>(lo, lo4, sub_lo, bits),
                                                 w4_pair<DT, 3>(hi, hi4, sub_hi, bits)};
-                        const uint8_t* xsrc = xs + (c >> 1) * C::X_BOX + xr * 128 +
-                                              ((((c & 1) * 4 + t) ^ xr) << 4);
+                        const uint32_t xsrc = ((c & 1) ? xs2 : xs) + (c >> 1) * C::X_BOX;
 #pragma unroll
                         for (int j = 0; j < NT; ++j) {
-                            const uint4 x = *reinterpret_cast<const uint4*>(xsrc + 1024 * j);
+                            const uint4 x = ld_shared_u128(xsrc + 1024u * j);
                             if (cc == 0)
                                 mma16816_first<DT>(acc[j], a1, x.x, x.y);
                             else
