@@ -1,30 +1,40 @@
-// Products with 4-bit weights and group scales (gemm_w4's direct form) and the
-// dequantising pass of its other form.
+// Products of few rows, which are bound by reading the weights: 4-bit weights with group
+// scales (gemm_w4's direct form, and the dequantising pass of its other form),
 //
 //   y[t, n] = sum_G s[n, G] * sum_{k in G} x[t, k] (q[n, k] - z[n, G])
 //
-// With few tokens the call is bound by the N K / 2 bytes of weights.  One CTA per
-// SM streams 64 (128 for more than 16 tokens) rows of them through a ring of TMA
-// boxes (128 bytes = 256 weights of a row, with the same 256 columns of the
-// tokens), filled by one producer warp that runs ahead over the CTA's units.
-// Of its sixteen (eight) consumer warps, each set of RT / 16 takes a range of the
-// stages of its own, a warp 16 rows by a whole stage (512 or 256 weights).  The
-// arithmetic stays near the loads by going through mma.sync m16n8k16 with the
-// weights on its M side: a 4-bit integer is an exact bf16 (fp16) number, made by
-// a byte permute, one masking and one packed subtraction for every two weights,
-// and the tokens are the 8 columns.  The products x (q - z) are summed in fp32
-// and scaled by s once per group, so nothing is rounded but the output.  What
-// bounds it is issue slots: about 34 instructions for 16 rows x 32 weights.
+// and 16-bit weights (gemm_grouped with up to 64 rows).
 //
-// The sum over k may be taken in any order, so lane t of a quad takes the 8
-// weights of 32-bit word t of a 16-byte chunk (32 weights) and 8 values of its
-// token.  The boxes are 128-byte swizzled, which makes the word reads of 8 rows
-// x 4 words conflict-free.
+// One CTA per SM streams units of 64 (128 for more than 16 tokens) weight rows through a
+// ring of 128-byte-swizzled TMA boxes, with the tokens' values of the same columns,
+// filled by one producer warp that runs ahead over the CTA's units.  Of its sixteen
+// (eight) consumer warps, each set of RT / 16 takes a range of the stages of its own, a
+// warp 16 rows by a whole stage.  The arithmetic stays near the loads by going through
+// mma.sync m16n8k16 with the weights on its M side and 8 tokens as its columns.
+// (tcgen05.mma would need the 4-bit weights written back to shared memory as 16 bits; and
+// for 16-bit ones its tiles of 128 weight rows leave most SMs idle in a decoding step:
+// 8 experts with a row each, 2048 x 1024, were 64 tiles of half a megabyte, loaded at the
+// 55 bytes a clock that an SM takes and multiplied at 115 clocks an instruction, 15.3 us;
+// here 128 units take 10.5 us, of which 4.5 are what any one unit takes, against 5.0 us
+// for reading the 34 MB.)
 //
-// Units (group, 64 rows, tokens of a tile) are dealt round robin; where they are
-// fewer than half of the SMs, K is cut over the CTAs of a cluster (at most 8),
-// whose fp32 sums meet in distributed shared memory and are added in rank order,
-// so results repeat.  All waits are bounded, as in the other kernels.
+// 4-bit integers are exact bf16 (fp16) numbers, made by a byte permute, one masking and
+// one packed subtraction for every two weights.  The products x (q - z) are summed in
+// fp32 and scaled by s once per group, so nothing is rounded but the output.  The sum
+// over k may be taken in any order, so lane t of a quad takes the 8 weights of 32-bit
+// word t of a 16-byte chunk (32 weights) and 8 values of its token; the swizzle makes the
+// word reads of 8 rows x 4 words conflict-free.  What bounds it: 34 instructions for 16
+// rows x 32 weights, more with short groups (with groups of 32 the schedulers issue in
+// 53 % of the cycles, the integer pipe is 47 % busy, and warps wait in equal parts for
+// that pipe, fixed latencies and the unit's barriers), and where there is less than one
+// unit a CTA, start-up.  Measured: one token, 8192 x 8192, groups of 128, 13.6 us
+// (2.5 TB/s); 32 rows over 32 experts of 2048 x 4096, groups of 32 and zero points,
+// 48.1 us (2.3 TB/s).
+//
+// Units (group, 64 rows, tokens of a tile) are dealt round robin; where they are fewer
+// than half of the SMs, K is cut over the CTAs of a cluster (at most 4), whose fp32 sums
+// meet in distributed shared memory and are added in rank order, so results repeat.  All
+// waits are bounded, as in the other kernels.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -81,13 +81,22 @@ def _epilogue(epilogue, bias, groups, N):
     return epi, bias.data_ptr(), bias.stride(0) if bias.dim() == 2 and groups > 1 else 0
 
 
-def _out(name, out, shape, dtype, like, types):
+def _empty(shape, dtype, like, stream):
+    """New memory that belongs to the stream the kernels run on: a block of another
+    stream's pool may still be in use there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=like.device)):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _out(name, out, shape, dtype, like, types, stream):
     if out is None:
         if dtype is None:
             dtype = types[0]
         elif dtype not in types:
             raise TypeError(f"{name} must be one of {', '.join(str(t) for t in types)}")
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return _empty(shape, dtype, like, stream)
     if out.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)} (it has {tuple(out.shape)})")
     if out.dtype not in types or (dtype is not None and out.dtype != dtype):
@@ -102,12 +111,12 @@ def _code16(A, B, names="A and B"):
     return code
 
 
-def _scratch(workspace, need, like):
+def _scratch(workspace, need, like, stream):
     """(workspace kept alive, pointer, bytes)."""
     if workspace is None:
         if need == 0:
             return None, 0, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+        workspace = _empty(need, torch.uint8, like, stream)
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -139,7 +148,7 @@ def grouped_gemm(A: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor,
     groups, _, N = B.shape
     if C is None and beta != 0.0:
         raise ValueError("beta != 0 needs an input C")
-    C = _out("C", C, (T, N), out_dtype, A, (A.dtype, torch.float32))
+    C = _out("C", C, (T, N), out_dtype, A, (A.dtype, torch.float32), stream)
     epi, bias_ptr, stride_bias = _epilogue(epilogue, bias, groups, N)
     lda, ldc = _ld("A", A), _ld("C", C)
     sb, s1, s2 = B.stride()
@@ -157,7 +166,7 @@ def grouped_gemm(A: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor,
     need = 0
     if workspace is None and (pa | pb | (lda | ldb | sb) * 2) & 15:
         need = _abi.gemm_grouped_workspace_size(dt, groups, T, N, K, pa, lda, pb, ldb, lb, sb)
-    workspace, ws, ws_bytes = _scratch(workspace, need, A)
+    workspace, ws, ws_bytes = _scratch(workspace, need, A, stream)
     st = _fn("gemm_grouped")(dt, groups, T, N, K, pa, lda, pb, ldb, lb, sb, C.data_ptr(), ldc,
                              _CODE[C.dtype], off, alpha, beta, bias_ptr, stride_bias, epi, ws,
                              ws_bytes, _raw_stream(dev) if stream is None else stream)
@@ -184,14 +193,14 @@ def grouped_gemm_wgrad(A: torch.Tensor, D: torch.Tensor, offsets: torch.Tensor,
         raise ValueError("offsets must hold groups + 1 values")
     if C is None and beta != 0.0:
         raise ValueError("beta != 0 needs an input C")
-    C = _out("C", C, (groups, M, N), out_dtype, A, (A.dtype, torch.float32))
+    C = _out("C", C, (groups, M, N), out_dtype, A, (A.dtype, torch.float32), stream)
     lda, ldd, ldc = _ld("A", A), _ld("D", D), _ld("C", C)
     off = _offsets(offsets, groups)
     pa, pd = A.data_ptr(), D.data_ptr()
     need = 0
     if workspace is None and (pa | pd | (lda | ldd) * 2) & 15:
         need = _abi.gemm_grouped_wgrad_workspace_size(dt, groups, T, M, N, pa, lda, pd, ldd)
-    workspace, ws, ws_bytes = _scratch(workspace, need, A)
+    workspace, ws, ws_bytes = _scratch(workspace, need, A, stream)
     st = _fn("gemm_grouped_wgrad")(dt, groups, T, M, N, pa, lda, pd, ldd, C.data_ptr(), ldc,
                                    C.stride(0) if groups > 1 else 0, _CODE[C.dtype], off, alpha,
                                    beta, ws, ws_bytes, _raw_stream(dev) if stream is None else stream)
@@ -214,13 +223,13 @@ def newton_schulz(G: torch.Tensor, out: torch.Tensor | None = None, *, steps=5,
         raise ValueError("coefficients must be three numbers")
     dev = G.get_device()
     _wrong_device(dev, G=G, out=out, workspace=workspace)
-    out = _out("out", out, G.shape, out_dtype, G, (torch.bfloat16, torch.float16))
+    out = _out("out", out, G.shape, out_dtype, G, (torch.bfloat16, torch.float16), stream)
     batch = G.shape[0] if G.dim() == 3 else 1
     M, N = G.shape[-2:]
     ldg, ldo = _ld("G", G), _ld("out", out)
     sg, so = (G.stride(0), out.stride(0)) if batch > 1 else (0, 0)
     need = _abi.gemm_newton_schulz_workspace_size(batch, M, N) if workspace is None else 0
-    workspace, ws, ws_bytes = _scratch(workspace, need, G)
+    workspace, ws, ws_bytes = _scratch(workspace, need, G, stream)
     a, b, c = coefficients
     st = _fn("gemm_newton_schulz")(_CODE[G.dtype], batch, M, N, G.data_ptr(), ldg, sg,
                                    out.data_ptr(), ldo, so, _CODE[out.dtype], steps, a, b, c, eps,
@@ -266,7 +275,7 @@ def w4_gemm(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, *, zeros=Non
     if not (q.is_contiguous() and scales.is_contiguous() and
             (zeros is None or zeros.is_contiguous())):
         raise ValueError("q, scales and zeros must be contiguous")
-    out = _out("out", out, (T, N), out_dtype, x, (x.dtype, torch.float32))
+    out = _out("out", out, (T, N), out_dtype, x, (x.dtype, torch.float32), stream)
     epi, bias_ptr, stride_bias = _epilogue(epilogue, bias, groups, N)
     ldx, ldo = _ld("x", x), _ld("out", out)
     off = _offsets(offsets, groups) if offsets is not None else 0
@@ -274,7 +283,7 @@ def w4_gemm(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, *, zeros=Non
     need = 0
     if workspace is None and ((px | ldx * 2) & 15 or T > groups):
         need = _abi.gemm_w4_workspace_size(dt, groups, T, N, K, px, ldx, odt)
-    workspace, ws, ws_bytes = _scratch(workspace, need, x)
+    workspace, ws, ws_bytes = _scratch(workspace, need, x, stream)
     st = _fn("gemm_w4")(dt, groups, T, N, K, px, ldx, q.data_ptr(), scales.data_ptr(),
                         0 if zeros is None else zeros.data_ptr(), K // n_groups, out.data_ptr(),
                         ldo, odt, off, bias_ptr, stride_bias, epi, ws, ws_bytes,

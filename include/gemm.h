@@ -248,7 +248,9 @@ const char* gemm_status_string(gemm_status_t status);
  * current device's error word, which a kernel sets when one of its bounded
  * waits expires (or, in the debug build, when a device-side check fails).
  * Returns GEMM_ERR_DEVICE_CHECK if a check failed, else GEMM_ERR_TIMEOUT if a
- * wait expired, GEMM_ERR_CUDA if the synchronisation failed, else GEMM_OK.
+ * wait expired, GEMM_ERR_INVALID_ARG if a kernel found group offsets that
+ * descend or leave the rows (gemm_experts.h), GEMM_ERR_CUDA if the
+ * synchronisation failed, else GEMM_OK.
  * For tests and debugging; it blocks.
  */
 gemm_status_t gemm_check_device_status(gemm_stream_t stream);

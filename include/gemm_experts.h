@@ -106,11 +106,11 @@ size_t gemm_grouped_wgrad_workspace_size(gemm_dtype_t ab_dtype, int64_t groups, 
  *   steps        1 to 64.     eps   >= 0 (0 gives NaN for a zero matrix).
  *   workspace    gemm_newton_schulz_workspace_size() bytes, 256-byte aligned.
  *
- * The norm and every product accumulate in fp32.  X, S and b S + c S S are held
- * between products in fp16 times a power of two (eight times finer than bf16);
- * coefficients must keep singular values below 4 and b S + c S S below 8 in
- * norm, which the values above do.  Both symmetric products compute the tiles
- * on and below the diagonal only.
+ * The norm and every product accumulate in fp32.  Between products X and the
+ * symmetric matrices S + b / (2 c) and a + b S + c S S are held in fp16 times a
+ * power of two (eight times finer than bf16); coefficients must keep singular
+ * values below 4 and both matrices below 8 in norm, which the values above do.
+ * Both symmetric products compute the tiles on and below the diagonal only.
  */
 gemm_status_t gemm_newton_schulz(gemm_dtype_t g_dtype, int64_t batch, int64_t M, int64_t N,
                                  const void* G, int64_t ldg, int64_t stride_g,

@@ -562,6 +562,27 @@ def test_side_stream_and_caller_workspace():
     assert e.value.status == dg.Status.ERR_WORKSPACE
 
 
+def test_explicit_stream():
+    """Outputs and copies of operands are allocated for the stream that is named."""
+    rng = np.random.default_rng(55)
+    b = bounds_of([40, 90])
+    A, B, o = ints(rng, (130, 131)).to(DEV), ints(rng, (2, 131, 70)).to(DEV), offs(b)
+    G = torch.randn((70, 90), device=DEV)
+    x, q, s, z = (t.to(DEV) for t in w4_case(rng, 5, 70, 320, 64, True))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    y = dg.grouped_gemm(A, B, o, out_dtype=F32, stream=side.cuda_stream)
+    w = dg.grouped_gemm_wgrad(A, A, o, out_dtype=F32, stream=side.cuda_stream)
+    n = dg.newton_schulz(G, stream=side.cuda_stream)
+    v = dg.w4_gemm(x, q, s, zeros=z, out_dtype=F32, stream=side.cuda_stream)
+    side.synchronize()
+    equal(y, ref.grouped(A, B, b), F32)
+    equal(w, ref.wgrad(A, A, b), F32)
+    equal(v, ref.w4(x, q, s, z), F32)
+    want = ref.newton_schulz(G)
+    assert np.linalg.norm(ref.f64(n) - want) <= (ns_bound(5) + 2.0 ** -9) * np.linalg.norm(want)
+
+
 def test_graph_replays_read_offsets_and_inputs_anew():
     rng = np.random.default_rng(52)
     K, N, E, T = 256, 192, 3, 60
@@ -596,7 +617,30 @@ def test_graph_replays_read_offsets_and_inputs_anew():
         assert np.linalg.norm(ref.f64(n) - want) <= (ns_bound(5) + 2.0 ** -9) * np.linalg.norm(want)
 
 
-@pytest.mark.parametrize("rows", [8, 200, 3000])
+@pytest.mark.parametrize("counts", [[1] * 8, [0, 5, 0, 40], [64], [3, 0, 13], [2] * 32])
+@pytest.mark.parametrize("layout", ["row", "col"])
+@pytest.mark.parametrize("K,N", [(64, 40), (200, 72), (2048, 1000), (72, 4096)])
+def test_few_rows(counts, layout, K, N):
+    """Up to 64 rows: K split over clusters, tiles of 8 and 16 tokens, both layouts."""
+    rng = np.random.default_rng(K + N + len(counts))
+    b = bounds_of(counts)
+    E = len(counts)
+    A = ints(rng, (b[-1], K), -2, 2)
+    B = ints(rng, (E, K, N) if layout == "row" else (E, N, K), -2, 2)
+    B = B if layout == "row" else B.transpose(1, 2)
+    bias = ints(rng, (E, N), dtype=F32)
+    C0 = ints(rng, (b[-1], N), dtype=F32)
+    got = dg.grouped_gemm(A.to(DEV), B.to(DEV), offs(b), C0.to(DEV), alpha=0.5, beta=2.0,
+                          bias=bias.to(DEV), epilogue="bias_relu")
+    equal(got, ref.grouped(A, B, b, C0, 0.5, 2.0, bias, "bias_relu"), F32)
+    equal(dg.grouped_gemm(A.to(DEV), B.to(DEV), offs(b)), ref.grouped(A, B, b), BF)
+    W = B[:1].to(DEV).expand(E, K, N)
+    equal(dg.grouped_gemm(A.to(DEV), W, offs(b), out_dtype=F32),
+          ref.grouped(A, B[:1].expand(E, K, N), b), F32)
+    assert status() == 0
+
+
+@pytest.mark.parametrize("rows", [8, 70, 200, 3000])
 def test_a_stalled_pipeline_reports_a_timeout_and_recovers(rows):
     """One stage is left unfilled (a flag that nothing sets), in each tile shape."""
     rng = np.random.default_rng(53)
