@@ -426,12 +426,12 @@ __global__ void __launch_bounds__(W4Cfg<MT, GROUP>::THREADS, 1) w4_kernel(const 
                             if (p.w_mn) {
                                 tma_load_3d(dst, &p.tmap_q, fb, w.n0, k0, wz, pol_q);
                             } else if (p.q4) {
-                                tma_load_4d_cg<1>(dst, &p.tmap_q, fb, 0, w.n0, k0 / 64, w.group,
+                                tma_load_4d_cg<1>(dst, &p.tmap_q, fb, 0, w.n0, k0 / 64, wz,
                                                   pol_q);
                             } else {
-                                tma_load_3d(dst, &p.tmap_q, fb, k0, w.n0, w.group, pol_q);
+                                tma_load_3d(dst, &p.tmap_q, fb, k0, w.n0, wz, pol_q);
                                 tma_load_3d(dst + C::W_BYTES / 2, &p.tmap_q, fb, k0 + 64, w.n0,
-                                            w.group, pol_q);
+                                            wz, pol_q);
                             }
                         } else if (p.q4) {
                             tma_load_4d_cg<1>(dst, &p.tmap_q, fb, 0, w.n0, st * C::BLK, w.group, pol_q);

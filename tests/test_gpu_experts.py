@@ -640,6 +640,35 @@ def test_few_rows(counts, layout, K, N):
     assert status() == 0
 
 
+@pytest.mark.parametrize("layout", ["row", "col"])
+def test_few_rows_do_not_mix(layout):
+    """NaN and infinite rows stay in their rows, NaN weights in their group, and what lies
+    beside the operands in padded rows stays out."""
+    rng = np.random.default_rng(17)
+    b = bounds_of([20, 1, 0, 30, 3], 1)
+    K, N, E = 136, 72, 5
+    A = ints(rng, (b[-1] + 2, K))
+    B = ints(rng, (E, K, N))
+    want = ref.grouped(A, B, b)
+    Ap = torch.full((b[-1] + 2, K + 8), float("nan"), dtype=BF, device=DEV)
+    Ap[:, :K] = A.to(DEV)
+    Ap[8], Ap[30] = float("nan"), float("inf")
+    if layout == "row":
+        Bp = torch.full((E, K, N + 8), float("nan"), dtype=BF, device=DEV)
+        Bp[:, :, :N] = B.to(DEV)
+        Bd = Bp[:, :, :N]
+    else:
+        Bp = torch.full((E, N, K + 8), float("nan"), dtype=BF, device=DEV)
+        Bp[:, :, :K] = B.transpose(1, 2).to(DEV)
+        Bd = Bp[:, :, :K].transpose(1, 2)
+    Bd[4] = float("nan")
+    got = ref.f64(dg.grouped_gemm(Ap[:, :K], Bd, offs(b), out_dtype=F32))
+    keep = [i for i in range(b[0], b[4]) if i not in (8, 30)]
+    assert np.array_equal(got[keep], want[keep])
+    assert np.isnan(got[8]).all() and np.isnan(got[b[4]:b[5]]).all()
+    assert not np.isfinite(got[30]).any()
+
+
 @pytest.mark.parametrize("rows", [8, 70, 200, 3000])
 def test_a_stalled_pipeline_reports_a_timeout_and_recovers(rows):
     """One stage is left unfilled (a flag that nothing sets), in each tile shape."""
@@ -671,6 +700,11 @@ def test_debug_build_trips_no_check():
     C = torch.full((T, N), float("nan"), dtype=F32, device=DEV)
     assert D.gemm_grouped(0, E, T, N, K, A.data_ptr(), K, B.data_ptr(), N, 0, K * N, C.data_ptr(), N,
                           2, o.data_ptr(), 1.0, 0.0, 0, 0, 0, 0, 0, st) == 0
+    few = [0, 3, 20, 20, 33]
+    of = offs(few)
+    C2 = torch.full((33, N), float("nan"), dtype=BF, device=DEV)
+    assert D.gemm_grouped(0, E, 33, N, K, A.data_ptr(), K, B.data_ptr(), N, 0, K * N, C2.data_ptr(),
+                          N, 0, of.data_ptr(), 1.0, 0.0, 0, 0, 0, 0, 0, st) == 0
     W = torch.empty((E, K, N), dtype=BF, device=DEV)
     assert D.gemm_grouped_wgrad(0, E, T, K, N, A.data_ptr(), K, X.data_ptr(), N, W.data_ptr(), N,
                                 K * N, 0, o.data_ptr(), 1.0, 0.0, 0, 0, st) == 0
@@ -686,6 +720,7 @@ def test_debug_build_trips_no_check():
                      64, Y.data_ptr(), 70, 2, 0, 0, 0, 0, 0, 0, st) == 0
     assert D.gemm_check_device_status(st) == 0
     equal(C, ref.grouped(A, B, b), F32)
+    equal(C2, ref.grouped(A[:33], B, few), BF)
     equal(W, ref.wgrad(A, X, b), BF)
     equal(Y, ref.w4(x, q, s, z), F32)
     want = ref.newton_schulz(G)
