@@ -204,11 +204,14 @@ __device__ __forceinline__ bool rg_tile(const RgParams& p, RgWalk& w, int t, int
         o.group = rg_div(t, p.div_group);
         const int r = t - o.group * p.per_group;
         if (FORM == RG_SYM) {
-            int i = static_cast<int>((sqrtf(8.0f * static_cast<float>(r) + 1.0f) - 1.0f) * 0.5f);
-            while (i * (i + 1) / 2 > r) --i;
-            while ((i + 1) * (i + 2) / 2 <= r) ++i;
-            const int j = r - i * (i + 1) / 2;
-            o.diag = i == j;
+            // F column tiles to a lane tile; those on the diagonal are computed whole
+            constexpr int F = LANES / BT;
+            const int q = r / F;
+            int i = static_cast<int>((sqrtf(8.0f * static_cast<float>(q) + 1.0f) - 1.0f) * 0.5f);
+            while (i * (i + 1) / 2 > q) --i;
+            while ((i + 1) * (i + 2) / 2 <= q) ++i;
+            const int j = r - F * (i * (i + 1) / 2);
+            o.diag = j >= F * i;
             o.lane0 = i * LANES + static_cast<int>(rank) * 128;
             o.col0 = j * p.col_tile;
         } else {

@@ -142,12 +142,15 @@ cudaError_t prepare_seq() {
 cudaError_t rg_launch_seq(int cg, int bt, const RgSeq& q, int grid, cudaStream_t stream) {
     if (cg == 2 && bt == 256) return launch_seq<2, 256>(q, grid, stream);
     if (cg == 1 && bt == 128) return launch_seq<1, 128>(q, grid, stream);
+    if (cg == 1 && bt == 64) return launch_seq<1, 64>(q, grid, stream);
     return cudaErrorInvalidValue;
 }
 
 cudaError_t rg_prepare_seq() {
-    const cudaError_t e = prepare_seq<2, 256>();
-    return e != cudaSuccess ? e : prepare_seq<1, 128>();
+    cudaError_t e = prepare_seq<2, 256>();
+    if (e == cudaSuccess) e = prepare_seq<1, 128>();
+    if (e == cudaSuccess) e = prepare_seq<1, 64>();
+    return e;
 }
 
 }  // namespace dg
