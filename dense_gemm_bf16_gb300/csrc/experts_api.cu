@@ -217,6 +217,7 @@ gemm_status_t rg_fill(const RgProblem& q, const DeviceInfo& d, int cg, int bt, R
     p.status = d.status;
     p.timeout_ns = option_timeout_ns();
     p.test_stall = take_test_stall();
+    p.pdl = q.pdl;
 #if DG_DEBUG
     const int64_t out_rows = q.form == RG_ROWS && q.offsets ? q.T : q.n_col;
     p.dbg_c_elems = (q.offsets && q.form == RG_ROWS ? 0 : (q.groups - 1) * q.stride_c) +
@@ -400,6 +401,7 @@ gemm_status_t gemm_grouped(gemm_dtype_t ab_dtype, int64_t groups, int64_t T, int
     q.bias = (epi & 1) ? bias : nullptr;
     q.stride_bias = stride_bias;
     q.act = act;
+    q.pdl = a.ptr != A || b.ptr != B;
     return rg_run(q, d, s);
 }
 
@@ -482,6 +484,7 @@ gemm_status_t gemm_grouped_wgrad(gemm_dtype_t ab_dtype, int64_t groups, int64_t 
     q.c_dtype = q.cin_dtype = c_dtype;
     q.alpha = alpha;
     q.beta = beta;
+    q.pdl = a.ptr != A || b.ptr != D;
     return rg_run(q, d, s);
 }
 
@@ -770,6 +773,7 @@ gemm_status_t gemm_w4(gemm_dtype_t ab_dtype, int64_t groups, int64_t T, int64_t 
         q.bias = (epi & 1) ? bias : nullptr;
         q.stride_bias = stride_bias;
         q.act = act;
+        q.pdl = true;
         return rg_run(q, d, s);
     }
     // tokens of a tile: the rows a group is expected to have

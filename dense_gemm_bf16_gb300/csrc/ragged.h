@@ -61,6 +61,9 @@ struct RgParams {
     int64_t stride_bias;
     int32_t act;
     int32_t test_stall;      // test only: leave one stage unfilled
+    // 1: launched as the programmatic dependent of the kernel that prepares an operand
+    // (a copy, or weights made from 4-bit ones): set up while it runs, then wait for it
+    int32_t pdl;
     int* status;
     uint64_t timeout_ns;
 #if DG_DEBUG
@@ -144,6 +147,7 @@ struct RgProblem {
     const float* bias;
     int64_t stride_bias;
     int act;
+    bool pdl;          // the kernel enqueued just before prepares an operand
 };
 // The kernel variant a problem takes (CTAs per tile, columns), its parameters, and
 // a bound on its tiles.

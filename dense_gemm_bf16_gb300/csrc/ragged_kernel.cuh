@@ -655,6 +655,7 @@ __device__ __forceinline__ void rg_produce(const RgParams& p, const RgCta& x, Rg
     const uint64_t pol = l2_policy_evict_normal();
     RgWalk walk = rg_begin<FORM>(p, x.lane);
     RgTile w;
+    if (p.pdl) griddep_wait();
     for (int t = first; r.ok && rg_tile<CG, BT, FORM>(p, walk, t, x.lane, x.rank, w); t += x.ncl) {
         // As in the MMA warp, the whole warp walks the stages and one lane issues.
         w.group = rg_uniform(w.group);
@@ -876,6 +877,7 @@ __device__ __forceinline__ void rg_tails(const RgParams& p, const RgCta& x, RgRo
     const uint64_t pol = l2_policy_evict_normal();
     RgWalk walk = rg_begin<RG_WGRAD>(p, x.lane);
     RgTile w;
+    if (p.pdl) griddep_wait();
     for (int t = x.cl; rg_tile<CG, BT, RG_WGRAD>(p, walk, t, x.lane, x.rank, w); t += x.ncl) {
         const int v = w.klen & 15;  // valid rows
         if (v == 0) continue;
@@ -1082,8 +1084,13 @@ cudaError_t rg_launch(const RgParams& p, int grid, cudaStream_t stream) {
     cfg.blockDim = dim3(RgCfg<CG, BT>::threads(FORM));
     cfg.dynamicSmemBytes = RgCfg<CG, BT>::SMEM;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     unsigned n = 0;
+    if (p.pdl) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
     if (CG > 1) {
         attr[n].id = cudaLaunchAttributeClusterDimension;
         attr[n].val.clusterDim.x = CG;

@@ -742,6 +742,7 @@ template <int DT>
 __global__ void __launch_bounds__(256) w4_dequantise_kernel(const uint32_t* q, const uint16_t* scales,
                                                             const uint8_t* zeros, int64_t words,
                                                             int shift, uint4* out) {
+    griddep_launch_dependents();  // the product sets itself up meanwhile
     const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
 #pragma unroll 4
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < words;
