@@ -8,8 +8,9 @@
 // epilogue warp adds to it (release) after storing its part of a tile, and before
 // a tile's loads the producer waits (acquire) for all tiles of the matrix's
 // products before.  With several matrices the products overlap and their last,
-// partly filled rounds of tiles with them (16 matrices of 1024 x 2048: 510 us
-// against 663 us with a barrier over the grid after every product).  The launch is
+// partly filled rounds of tiles with them (16 matrices of 1024 x 2048: 510 us,
+// against 663 with a barrier over the grid after every product and with a X and b S
+// read back in the epilogues instead of the constants on the diagonals).  The launch is
 // cooperative, so every CTA is resident, and a tile waits only for tiles that come
 // before it in that order; the wait is bounded like all others.
 #include "ragged_kernel.cuh"
