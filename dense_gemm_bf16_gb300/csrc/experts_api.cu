@@ -684,11 +684,15 @@ gemm_status_t gemm_newton_schulz(gemm_dtype_t g_dtype, int64_t batch, int64_t M,
 
 namespace {
 
-// Rows up to which the 4-bit integers are multiplied directly.
-constexpr int64_t kW4DirectRows = 64;
+// Rows (of a group, on average) up to which the 4-bit integers are multiplied directly.
+// Against 16-bit weights in the workspace, K x N = 4096 x 4096 (us): 64 rows 19.7 (29
+// from 65 rows on), 96 rows 32 : 29; 32 experts of 2048 x 4096: 16 rows each on average
+// 133 : 215, 25 rows 207 : 221, 37 rows 223 : 214 unevenly and 192 : 215 evenly spread,
+// 50 rows 261 : 221 and 203 : 215; 8 experts: 37 rows 62.1 : 62.6, 50 rows 85 : 63.
+constexpr int64_t kW4DirectRows = 64, kW4DirectGroupRows = 40;
 
 bool w4_direct(int64_t groups, int64_t T, int c_dtype) {
-    return c_dtype == DT_F32 || T <= kW4DirectRows * groups;
+    return c_dtype == DT_F32 || T <= (groups > 1 ? kW4DirectGroupRows * groups : kW4DirectRows);
 }
 
 size_t w4_need(int64_t groups, int64_t T, int64_t N, int64_t K, const void* A, int64_t lda,
