@@ -18,6 +18,7 @@ _CODE = {dt: int(v) for dt, v in _DT.items()}
 _CODE16 = {dt: v for dt, v in _CODE.items() if dt != torch.float32}
 _EPI_CODE = {name: int(v) for name, v in _EPI.items()}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _fn(name):
@@ -37,6 +38,14 @@ def _wrong_device(dev, **tensors):
         if t is not None and (not t.is_cuda or t.get_device() != dev):
             where = f"cuda:{dev}" if dev >= 0 else "one CUDA device"
             raise ValueError(f"{name} must be a CUDA tensor on {where} (it is on {t.device})")
+
+
+def _require_current(dev):
+    """The library launches on the current device, with that device's error word; the
+    stream is the tensors' device's.  On another device both would meet foreign pointers."""
+    if dev != _current_device():
+        raise ValueError(f"the tensors are on cuda:{dev}, but cuda:{_current_device()} is the "
+                         "current device: make theirs current (torch.cuda.device)")
 
 
 def _ld(name, t):
@@ -129,7 +138,7 @@ def grouped_gemm(A: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor,
                  C: torch.Tensor | None = None, *, alpha=1.0, beta=0.0, bias=None, epilogue=None,
                  out_dtype=None, workspace=None, stream=None) -> torch.Tensor:
     """C[t] <- act(alpha * A[t] @ B[e] + beta * C[t] + bias[e]) for the rows t
-    of every group e, rows offsets[e] .. offsets[e + 1] - 1.
+    of every group e, rows offsets[e] .. offsets[e + 1] - 1, on the current CUDA device.
 
     A: [T, K] row-major; B: [groups, K, N], row- or column-major matrices (a
     ``transpose(1, 2)`` gives the gradient of A); offsets: int32 [groups + 1] on
@@ -144,6 +153,7 @@ def grouped_gemm(A: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor,
     if not dev == B.get_device() == offsets.get_device() or dev < 0 or C is not None or \
             bias is not None or workspace is not None:
         _wrong_device(dev, A=A, B=B, offsets=offsets, C=C, bias=bias, workspace=workspace)
+    _require_current(dev)
     T, K = A.shape
     groups, _, N = B.shape
     if C is None and beta != 0.0:
@@ -179,13 +189,14 @@ def grouped_gemm_wgrad(A: torch.Tensor, D: torch.Tensor, offsets: torch.Tensor,
                        C: torch.Tensor | None = None, *, alpha=1.0, beta=0.0, out_dtype=None,
                        workspace=None, stream=None) -> torch.Tensor:
     """C[e] <- alpha * A_e^T @ D_e + beta * C[e], the weights' gradient of
-    ``grouped_gemm``: A [T, M] and D [T, N] row-major, C [groups, M, N] (a group
-    without rows gives beta * C[e])."""
+    ``grouped_gemm``, on the current CUDA device: A [T, M] and D [T, N] row-major,
+    C [groups, M, N] (a group without rows gives beta * C[e])."""
     dt = _code16(A, D, "A and D")
     if A.dim() != 2 or D.dim() != 2 or A.shape[0] != D.shape[0]:
         raise ValueError(f"shape mismatch: A{tuple(A.shape)} D{tuple(D.shape)}")
     dev = A.get_device()
     _wrong_device(dev, A=A, D=D, offsets=offsets, C=C, workspace=workspace)
+    _require_current(dev)
     T, M = A.shape
     N = D.shape[1]
     groups = offsets.numel() - 1
@@ -214,7 +225,8 @@ def newton_schulz(G: torch.Tensor, out: torch.Tensor | None = None, *, steps=5,
                   workspace=None, stream=None) -> torch.Tensor:
     """The orthogonalised form of G ([M, N], or [batch, M, N] matrix by matrix):
     X = G / (||G||_F + eps), then ``steps`` times X = a X + (b S + c S S) X with
-    S = X X^T.  G is fp32, bf16 or fp16; the result bf16 (default) or fp16."""
+    S = X X^T.  G is fp32, bf16 or fp16; the result bf16 (default) or fp16.  Runs on
+    the current CUDA device."""
     if G.dtype not in _CODE:
         raise TypeError("G must be bfloat16, float16 or float32")
     if G.dim() not in (2, 3):
@@ -223,6 +235,7 @@ def newton_schulz(G: torch.Tensor, out: torch.Tensor | None = None, *, steps=5,
         raise ValueError("coefficients must be three numbers")
     dev = G.get_device()
     _wrong_device(dev, G=G, out=out, workspace=workspace)
+    _require_current(dev)
     out = _out("out", out, G.shape, out_dtype, G, (torch.bfloat16, torch.float16), stream)
     batch = G.shape[0] if G.dim() == 3 else 1
     M, N = G.shape[-2:]
@@ -244,7 +257,7 @@ def w4_gemm(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, *, zeros=Non
             stream=None) -> torch.Tensor:
     """act(x @ W^T + bias) with 4-bit weights W[n, k] = (q[n, k] - z) * s, one
     scale (and zero point, 8 without ``zeros``) per group of K // scales.shape[-1]
-    neighbours along k.
+    neighbours along k, on the current CUDA device.
 
     x: [T, K] row-major; q: uint8 [N, K // 2], the low half of byte j holding
     k = 2 j; scales: [N, K // group] in x's dtype; zeros: uint8 of that shape.
@@ -261,6 +274,7 @@ def w4_gemm(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, *, zeros=Non
             offsets is not None or out is not None or bias is not None or workspace is not None:
         _wrong_device(dev, x=x, q=q, scales=scales, zeros=zeros, offsets=offsets, out=out,
                       bias=bias, workspace=workspace)
+    _require_current(dev)
     T, K = x.shape
     groups = q.shape[0] if lead == 3 else 1
     N = q.shape[-2]

@@ -165,6 +165,30 @@ def test_tensor_level_refusals():
         dg.w4_gemm(x, q[None], s)
 
 
+def test_tensors_of_another_device_than_the_current_one_are_refused(monkeypatch):
+    """The library launches on the current device, so tensors of another one would be
+    foreign pointers there: refused before the library is called."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+
+    from dense_gemm_bf16_gb300 import experts
+    called = []
+    monkeypatch.setattr(experts, "_fn", lambda name: called.append(name))
+    monkeypatch.setattr(experts, "_current_device", lambda: 0, raising=False)
+    with FakeTensorMode():
+        A = torch.empty((4, 64), dtype=torch.bfloat16, device="cuda:1")
+        B = torch.empty((2, 64, 16), dtype=torch.bfloat16, device="cuda:1")
+        o = torch.empty(3, dtype=torch.int32, device="cuda:1")
+        q = torch.empty((6, 32), dtype=torch.uint8, device="cuda:1")
+        s = torch.empty((6, 2), dtype=torch.bfloat16, device="cuda:1")
+        for call in (lambda: dg.grouped_gemm(A, B, o, stream=0),
+                     lambda: dg.grouped_gemm_wgrad(A, A, o, stream=0),
+                     lambda: dg.newton_schulz(A, stream=0),
+                     lambda: dg.w4_gemm(A, q, s, stream=0)):
+            with pytest.raises(ValueError, match="current"):
+                call()
+    assert called == []
+
+
 def test_references_agree_with_closed_forms():
     """The references themselves: identity weights, a transposed product, an orthogonal
     matrix's fixed scaling, and packed weights written out by hand."""
