@@ -21,7 +21,17 @@ inline bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintpt
 inline int dt_bytes(int dt) { return dt == DT_F32 ? 4 : 2; }
 constexpr int64_t kLim = 0x7FFFFFFF;
 
+// The kernels walk extents in 32 bits, by up to 2048 at a time, and round them up to
+// whole tiles: an extent this close to 2^31 would wrap.
+constexpr int64_t kMaxExtent = kLim - 4095;
+
 inline bool size_ok(int64_t v) { return v >= 0 && v <= kLim; }
+gemm_status_t extents(int64_t a, int64_t b, int64_t c, int64_t d) {
+    if (!size_ok(a) || !size_ok(b) || !size_ok(c) || !size_ok(d)) return GEMM_ERR_INVALID_ARG;
+    return a > kMaxExtent || b > kMaxExtent || c > kMaxExtent || d > kMaxExtent
+               ? GEMM_ERR_UNSUPPORTED
+               : GEMM_OK;
+}
 inline bool is16(int dt) { return dt == DT_BF16 || dt == DT_F16; }
 inline bool is_dt(int dt) { return is16(dt) || dt == DT_F32; }
 
@@ -321,7 +331,8 @@ gemm_status_t check_grouped(int ab, int64_t groups, int64_t T, int64_t N, int64_
                             int64_t lda, const void* B, int64_t ldb, int lb, int64_t stride_b) {
     if (!is_dt(ab)) return GEMM_ERR_INVALID_ARG;
     if (lb != GEMM_ROW_MAJOR && lb != GEMM_COL_MAJOR) return GEMM_ERR_INVALID_ARG;
-    if (!size_ok(groups) || !size_ok(T) || !size_ok(N) || !size_ok(K)) return GEMM_ERR_INVALID_ARG;
+    const gemm_status_t st = extents(groups, T, N, K);
+    if (st != GEMM_OK) return st;
     if (ab == DT_F32) return GEMM_ERR_UNSUPPORTED;
     if (groups == 0 || T == 0 || N == 0 || K == 0) return GEMM_OK;
     if (!A || !B || !aligned(A, 2) || !aligned(B, 2)) return GEMM_ERR_INVALID_ARG;
@@ -422,7 +433,8 @@ size_t gemm_grouped_workspace_size(gemm_dtype_t ab_dtype, int64_t groups, int64_
 static gemm_status_t check_wgrad(int ab, int64_t groups, int64_t T, int64_t M, int64_t N,
                                  const void* A, int64_t lda, const void* D, int64_t ldd) {
     if (!is_dt(ab)) return GEMM_ERR_INVALID_ARG;
-    if (!size_ok(groups) || !size_ok(T) || !size_ok(N) || !size_ok(M)) return GEMM_ERR_INVALID_ARG;
+    const gemm_status_t st = extents(groups, T, N, M);
+    if (st != GEMM_OK) return st;
     if (ab == DT_F32) return GEMM_ERR_UNSUPPORTED;
     if (groups == 0 || T == 0 || N == 0 || M == 0) return GEMM_OK;
     if (!A || !D || !aligned(A, 2) || !aligned(D, 2)) return GEMM_ERR_INVALID_ARG;
@@ -547,7 +559,8 @@ gemm_status_t gemm_newton_schulz(gemm_dtype_t g_dtype, int64_t batch, int64_t M,
                                  float a, float b, float c, float eps, void* workspace,
                                  size_t workspace_bytes, gemm_stream_t stream) {
     if (!is_dt(g_dtype) || !is_dt(o_dtype)) return GEMM_ERR_INVALID_ARG;
-    if (!size_ok(batch) || !size_ok(M) || !size_ok(N)) return GEMM_ERR_INVALID_ARG;
+    gemm_status_t st = extents(batch, M, N, 0);
+    if (st != GEMM_OK) return st;
     if (steps < 1 || steps > 64 || !(eps >= 0.0f)) return GEMM_ERR_INVALID_ARG;
     if (o_dtype == GEMM_DT_F32) return GEMM_ERR_UNSUPPORTED;
     if (batch == 0 || M == 0 || N == 0) return GEMM_OK;
@@ -561,7 +574,7 @@ gemm_status_t gemm_newton_schulz(gemm_dtype_t g_dtype, int64_t batch, int64_t M,
     if (!workspace || workspace_bytes < l.total) return GEMM_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return GEMM_ERR_INVALID_ARG;
     DeviceInfo d;
-    gemm_status_t st = device_info(&d);
+    st = device_info(&d);
     if (st != GEMM_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
@@ -721,13 +734,14 @@ gemm_status_t gemm_w4(gemm_dtype_t ab_dtype, int64_t groups, int64_t T, int64_t 
                       gemm_epilogue_t epi, void* workspace, size_t workspace_bytes,
                       gemm_stream_t stream) {
     if (!is_dt(ab_dtype) || !is_dt(c_dtype)) return GEMM_ERR_INVALID_ARG;
-    if (!size_ok(groups) || !size_ok(T) || !size_ok(N) || !size_ok(K)) return GEMM_ERR_INVALID_ARG;
+    gemm_status_t st = extents(groups, T, N, K);
+    if (st != GEMM_OK) return st;
     if (group != 32 && group != 64 && group != 128) return GEMM_ERR_INVALID_ARG;
     if (K % group != 0) return GEMM_ERR_INVALID_ARG;
     if (ab_dtype == GEMM_DT_F32 || (c_dtype != ab_dtype && c_dtype != GEMM_DT_F32))
         return GEMM_ERR_UNSUPPORTED;
     int act = ACT_NONE;
-    gemm_status_t st = epilogue_of(epi, bias, stride_bias, N, groups, &act);
+    st = epilogue_of(epi, bias, stride_bias, N, groups, &act);
     if (st != GEMM_OK) return st;
     if (groups == 0 || T == 0 || N == 0) return GEMM_OK;
     if (offsets ? !aligned(offsets, 4) : groups != 1) return GEMM_ERR_INVALID_ARG;

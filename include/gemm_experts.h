@@ -5,7 +5,8 @@
  * update of the weights (Newton-Schulz products), and products with 4-bit
  * weights.  The conventions of gemm.h hold: device pointers, caller-owned
  * buffers and workspaces, work enqueued on `stream`, argument errors by return
- * code before anything is enqueued, no allocation.
+ * code before anything is enqueued, no allocation.  An extent above 2^31 - 4096
+ * is GEMM_ERR_UNSUPPORTED: the kernels walk extents in 32 bits, tile by tile.
  *
  * Group offsets.  `offsets` is a device array of groups + 1 ascending int32
  * values: group e owns the rows offsets[e] .. offsets[e+1] - 1 of the row

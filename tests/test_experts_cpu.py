@@ -101,6 +101,22 @@ def test_w4_refusals(kw, want):
     assert w4(**kw) == want
 
 
+@pytest.mark.parametrize("call,dims", [
+    (grouped, dict(groups="stride_b", T="", N="ldb ldc", K="lda")),
+    (wgrad, dict(groups="stride_c", T="", M="lda", N="ldd ldc")),
+    (ns, dict(batch="", M="", N="ldg ldo")),
+    (w4, dict(groups="", T="", N="ldc", K="lda")),
+])
+def test_extents_that_would_wrap_in_32_bits_are_refused(call, dims):
+    """The kernels step past an extent by up to 2048 and round it up to a tile."""
+    big = (1 << 31) - 32                     # (a multiple of the 4-bit weights' group)
+    for dim, pitches in dims.items():
+        kw = {p: big if p[0] == "l" else 0 for p in pitches.split()}
+        if dim == "N" and call is grouped:
+            kw["stride_b"] = 0
+        assert call(**{dim: big, **kw}) == UNSUP, dim
+
+
 def test_empty_calls_are_noops():
     assert grouped(T=0, A=None, C=None, offsets=None) == 0
     assert grouped(groups=0, offsets=None) == 0 and grouped(N=0, C=None) == 0
