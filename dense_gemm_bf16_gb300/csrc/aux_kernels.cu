@@ -205,18 +205,24 @@ int grid_for(int64_t total) {
 cudaError_t pack16_launch(const void* src, int64_t ld, int64_t stride, int64_t rows, int64_t cols,
                           int64_t batch, void* dst, int64_t ld_dst, cudaStream_t stream) {
     if (batch <= 0 || rows <= 0 || cols <= 0) return cudaSuccess;
-    if (batch > 65535) return cudaErrorInvalidValue;
     if ((ld_dst & 7) != 0 || (reinterpret_cast<uintptr_t>(dst) & 15) != 0)
         return cudaErrorInvalidValue;  // the 16-byte stores need an aligned destination
     const int64_t gx = ((cols + 7) / 8 + kThreads - 1) / kThreads;
     const int64_t groups = (rows + 3) / 4;
     const int64_t gy = groups < 4096 ? groups : 4096;
     if (gx > 0x7FFFFFFF) return cudaErrorInvalidValue;
-    pack16_kernel<<<dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy),
-                         static_cast<unsigned>(batch)),
-                    kThreads, 0, stream>>>(static_cast<const uint16_t*>(src), ld, stride, rows,
-                                           cols, static_cast<uint16_t*>(dst), ld_dst);
-    return cudaGetLastError();
+    const uint16_t* from = static_cast<const uint16_t*>(src);
+    uint16_t* to = static_cast<uint16_t*>(dst);
+    for (int64_t b = 0; b < batch; b += 65535) {  // (what a grid's z holds)
+        const int64_t n = batch - b < 65535 ? batch - b : 65535;
+        pack16_kernel<<<dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy),
+                             static_cast<unsigned>(n)),
+                        kThreads, 0, stream>>>(from + b * stride, ld, stride, rows, cols,
+                                               to + b * rows * ld_dst, ld_dst);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 cudaError_t splitk_epilogue_launch(const float* partials, int splits, int64_t batch, int64_t M,

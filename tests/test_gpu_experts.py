@@ -738,3 +738,23 @@ def test_example_runs():
     first, last, gap = mod.main(tokens=512, width=256, hidden=512, experts=8, top=2, steps=12,
                                 quiet=True)
     assert last < 0.9 * first and gap < 0.2
+
+
+def test_more_groups_than_a_grid_holds_are_copied():
+    """65537 matrices that TMA cannot address (5 columns), and as many groups in place."""
+    rng = np.random.default_rng(61)
+    E, K, N = 65537, 3, 5
+    rows = [0, 1, 65534, 65535, 65536]
+    counts = np.zeros(E, dtype=np.int64)
+    counts[rows] = [2, 1, 3, 30, 40]
+    b = bounds_of(counts)
+    A, B = ints(rng, (b[-1], K)), ints(rng, (E, K, N))
+    got = dg.grouped_gemm(A.to(DEV), B.to(DEV), offs(b), out_dtype=F32)
+    want = np.concatenate([ref.f64(A[b[e]:b[e + 1]]) @ ref.f64(B[e]) for e in rows])
+    equal(got, want, F32)
+    W = ints(rng, (E, 8, 8)).to(DEV)
+    A = ints(rng, (b[-1], 8))
+    got = dg.grouped_gemm(A.to(DEV), W, offs(b), out_dtype=F32)
+    want = np.concatenate([ref.f64(A[b[e]:b[e + 1]]) @ ref.f64(W[e]) for e in rows])
+    equal(got, want, F32)
+    assert status() == 0
