@@ -32,6 +32,22 @@ gemm_status_t extents(int64_t a, int64_t b, int64_t c, int64_t d) {
                ? GEMM_ERR_UNSUPPORTED
                : GEMM_OK;
 }
+// Tiles are dealt in 32 bits, with the grid's size to spare.  The bounds below count the
+// smallest tiles there are, so that a call is refused before an operand's copy is
+// enqueued, whichever tile the device's size then chooses.
+constexpr int64_t kMaxTiles = kLim - 65535;
+
+// Row products, with a last tile for every group that has rows: 128 lanes by 32 columns,
+// or 64 lanes by 8 rows in the kernel for few rows (`few`).
+bool row_tiles_ok(int64_t groups, int64_t T, int64_t N, bool few) {
+    const int64_t active = groups < T ? groups : T;
+    return cdiv(N, few ? 64 : 128) <= kMaxTiles / (cdiv(T, few ? 8 : 32) + active);
+}
+
+bool wgrad_tiles_ok(int64_t groups, int64_t M, int64_t N) {
+    return cdiv(N, 128) * cdiv(M, 128) <= kMaxTiles / groups;
+}
+
 inline bool is16(int dt) { return dt == DT_BF16 || dt == DT_F16; }
 inline bool is_dt(int dt) { return is16(dt) || dt == DT_F32; }
 
@@ -157,8 +173,9 @@ gemm_status_t rg_fill(const RgProblem& q, const DeviceInfo& d, int cg, int bt, R
         }
         total = bound = q.groups * lane_tiles * cdiv(q.n_col, p.col_tile);
     }
-    // (the triangle's index arithmetic takes up to 32767 tile rows)
-    if (bound > kLim || (q.form == RG_SYM && lane_tiles > 32767)) return GEMM_ERR_UNSUPPORTED;
+    // (the triangle's index arithmetic takes up to 32767 tile rows; the sequence of
+    // products fills its parameters before it enqueues anything)
+    if (bound > kMaxTiles || (q.form == RG_SYM && lane_tiles > 32767)) return GEMM_ERR_UNSUPPORTED;
     *tiles = bound;
     p.total_tiles = static_cast<int32_t>(total);
     p.per_group = static_cast<int32_t>(q.groups > 0 ? total / q.groups : 0);
@@ -278,7 +295,6 @@ static gemm_status_t few_run(const RgProblem& q, const DeviceInfo& d, cudaStream
     p.K = static_cast<int32_t>(q.K);
     const int64_t n_tiles = cdiv(q.n_lane, shape.rows), steps = cdiv(q.K, shape.step);
     const int64_t units = n_tiles * (q.T / tokens + (q.groups < q.T ? q.groups : q.T));
-    if (units > kLim) return GEMM_ERR_UNSUPPORTED;
     int splits = 1;
     while (splits < 4 && units * splits * 2 <= d.sm_count && steps >= splits * 8) splits *= 2;
     p.n_tiles = static_cast<int32_t>(n_tiles);
@@ -372,6 +388,7 @@ gemm_status_t gemm_grouped(gemm_dtype_t ab_dtype, int64_t groups, int64_t T, int
     if (groups == 0 || T == 0 || N == 0) return GEMM_OK;
     if (!offsets || !aligned(offsets, 4)) return GEMM_ERR_INVALID_ARG;
     if (!c_ok(C, T, N, ldc, 1, 0, c_dtype)) return GEMM_ERR_INVALID_ARG;
+    if (!row_tiles_ok(groups, T, N, T <= kFewRows)) return GEMM_ERR_UNSUPPORTED;
     const bool b_mn = lb == GEMM_ROW_MAJOR;
     Stored a{A, lda, 0}, b{B, ldb, groups > 1 ? stride_b : 0};
     DeviceInfo d;
@@ -460,6 +477,7 @@ gemm_status_t gemm_grouped_wgrad(gemm_dtype_t ab_dtype, int64_t groups, int64_t 
     if (!c_ok(C, M, N, ldc, groups, groups > 1 ? stride_c : 0, c_dtype)) return GEMM_ERR_INVALID_ARG;
     if (groups > 1 && stride_c < (M - 1) * ldc + N) return GEMM_ERR_INVALID_ARG;
     if (Tc > 0 && (!offsets || !aligned(offsets, 4))) return GEMM_ERR_INVALID_ARG;
+    if (!wgrad_tiles_ok(groups, M, N)) return GEMM_ERR_UNSUPPORTED;
     DeviceInfo d;
     st = device_info(&d);
     if (st != GEMM_OK) return st;
@@ -756,6 +774,7 @@ gemm_status_t gemm_w4(gemm_dtype_t ab_dtype, int64_t groups, int64_t T, int64_t 
     if (!A || !aligned(A, 2) || lda < K || !Q || !aligned(Q, 16) || !scales || !aligned(scales, 2))
         return GEMM_ERR_INVALID_ARG;
     if (!strided_span_ok(T, K, lda, 1, 1, 0) || !count_ok(groups, N, K)) return GEMM_ERR_INVALID_ARG;
+    if (!row_tiles_ok(groups, T, N, w4_direct(groups, T, c_dtype))) return GEMM_ERR_UNSUPPORTED;
     const size_t need = w4_need(groups, T, N, K, A, lda, c_dtype);
     if (need > 0 && (!workspace || workspace_bytes < need)) return GEMM_ERR_WORKSPACE;
     if (need > 0 && !aligned(workspace, 256)) return GEMM_ERR_INVALID_ARG;
@@ -825,7 +844,6 @@ gemm_status_t gemm_w4(gemm_dtype_t ab_dtype, int64_t groups, int64_t T, int64_t 
     const int64_t n_tiles = cdiv(N, shape.rows), steps = cdiv(K, stage_k);
     // units there may be: full token tiles and one more for each non-empty group
     const int64_t units = n_tiles * (T / tokens + (groups < T ? groups : T));
-    if (units > kLim) return GEMM_ERR_UNSUPPORTED;
     // K slices (a cluster per unit) where the units would leave SMs idle, each of
     // at least one stage for every set of consumer warps.  (Clusters of 8 do not all
     // fit at once: N = 1024, K = 8192 took 11.9 us in 8 slices.)

@@ -117,6 +117,26 @@ def test_extents_that_would_wrap_in_32_bits_are_refused(call, dims):
         assert call(**{dim: big, **kw}) == UNSUP, dim
 
 
+WIDE = (1 << 31) - 4096
+
+
+@pytest.mark.parametrize("kw", [
+    # more than 2^31 tiles of at least 64 outputs each, with an operand to be copied first
+    dict(call=grouped, groups=64, T=64, N=WIDE, K=1, lda=1, ldb=WIDE, stride_b=0, ldc=WIDE),
+    dict(call=grouped, groups=1 << 17, T=1 << 17, N=1 << 30, K=1, lda=1, ldb=1 << 30, stride_b=0,
+         ldc=1 << 30),
+    dict(call=wgrad, groups=1 << 30, T=1, M=129, N=129, lda=129, ldd=129, ldc=129,
+         stride_c=129 * 129),
+    dict(call=w4, groups=64, T=64, N=WIDE, K=32, lda=33, ldc=WIDE, offsets=64),
+    dict(call=w4, groups=1, T=1 << 28, N=1 << 20, K=32, lda=32, ldc=1 << 20),
+])
+def test_more_tiles_than_32_bits_are_refused_before_anything_else(kw):
+    """Before a device is looked for, so before a copy or a pass over the weights is
+    enqueued."""
+    kw = dict(kw, workspace=256, workspace_bytes=1 << 50)
+    assert kw.pop("call")(**kw) == UNSUP
+
+
 def test_empty_calls_are_noops():
     assert grouped(T=0, A=None, C=None, offsets=None) == 0
     assert grouped(groups=0, offsets=None) == 0 and grouped(N=0, C=None) == 0
