@@ -60,6 +60,8 @@ struct DevState {
     int cc = 0;
     int* status = nullptr;
     int max_pairs[3][3] = {};  // co-resident two-CTA clusters [mode][BN 128, 256, 512] (mode 2)
+    std::once_flag experts_once;  // kernels of the expert-layer entry points
+    cudaError_t experts_err = cudaSuccess;
 };
 DevState g_dev[kMaxDevices];
 
@@ -99,10 +101,6 @@ gemm_status_t device_state(DevState** out) {
             for (int bn : kBlockN)
                 if (e == cudaSuccess) e = tc_prepare(bn);
             if (e == cudaSuccess) e = sgemm_prepare();
-            if (e == cudaSuccess) e = rg_prepare_rows();
-            if (e == cudaSuccess) e = rg_prepare_wgrad();
-            if (e == cudaSuccess) e = rg_prepare_seq();
-            if (e == cudaSuccess) e = w4_prepare();
             if (e == cudaSuccess) {
                 d.max_pairs[2][0] = tc_max_pairs(128, 2);
                 d.max_pairs[2][1] = tc_max_pairs(256, 2);
@@ -1052,19 +1050,25 @@ Call make_call(int ab, int64_t batch, int64_t M, int64_t N, int64_t K, const voi
 
 // ---------------------------------------------------------------- shared with the expert-layer entry points
 
-namespace {
-void fill_info(const DevState& d, DeviceInfo* out) {
-    out->sm_count = d.sm_count;
-    out->max_pairs = d.max_pairs[2][1] > 0 ? d.max_pairs[2][1] : d.sm_count / 2;
-    out->status = d.status;
-}
-}  // namespace
-
+// (their kernels are prepared by the first call that may launch one: a program of
+// dense products alone does not load them, 2 ms and 2 MB)
 gemm_status_t device_info(DeviceInfo* out) {
     DevState* d = nullptr;
     const gemm_status_t st = device_state(&d);
-    if (st == GEMM_OK) fill_info(*d, out);
-    return st;
+    if (st != GEMM_OK) return st;
+    std::call_once(d->experts_once, [d] {
+        cudaError_t e = rg_prepare_rows();
+        if (e == cudaSuccess) e = rg_prepare_wgrad();
+        if (e == cudaSuccess) e = rg_prepare_seq();
+        if (e == cudaSuccess) e = w4_prepare();
+        d->experts_err = e;
+        if (e != cudaSuccess) cudaGetLastError();
+    });
+    if (d->experts_err != cudaSuccess) return GEMM_ERR_CUDA;
+    out->sm_count = d->sm_count;
+    out->max_pairs = d->max_pairs[2][1] > 0 ? d->max_pairs[2][1] : d->sm_count / 2;
+    out->status = d->status;
+    return GEMM_OK;
 }
 
 uint64_t option_timeout_ns() { return static_cast<uint64_t>(g_opt_timeout_us.load()) * 1000ull; }

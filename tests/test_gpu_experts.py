@@ -758,3 +758,47 @@ def test_more_groups_than_a_grid_holds_are_copied():
     want = np.concatenate([ref.f64(A[b[e]:b[e + 1]]) @ ref.f64(W[e]) for e in rows])
     equal(got, want, F32)
     assert status() == 0
+
+
+FIRST_CALLS = """
+import torch
+import dense_gemm_bf16_gb300 as dg
+A = torch.ones((256, 256), dtype=torch.bfloat16, device="cuda:0")
+B = torch.ones((2, 256, 256), dtype=torch.bfloat16, device="cuda:0")
+o = torch.tensor([0, 100, 256], dtype=torch.int32, device="cuda:0")
+C, Y = torch.empty_like(A), torch.empty_like(A)
+from dense_gemm_bf16_gb300 import api, experts
+
+def free():
+    torch.cuda.synchronize()
+    return torch.cuda.mem_get_info()[0]
+
+at_first = free()
+dg.gemm(A, A, C)
+dense = free()
+if {capture}:
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        dg.grouped_gemm(A, B, o, Y)
+    g.replay()
+else:
+    dg.grouped_gemm(A, B, o, Y)
+with_experts = free()
+assert bool((Y == 256).all()) and dg.gemm_check_device_status(0) == 0
+assert dense < at_first
+assert {capture} or with_experts < dense, "the dense product loaded the expert kernels"
+"""
+
+
+@pytest.mark.parametrize("capture", [False, True])
+def test_a_dense_product_does_not_load_the_expert_kernels(capture):
+    """In a process of its own: kernels take device memory when they are prepared, the
+    dense ones at the first dense call and the others at the first call of theirs, which
+    may be a captured one."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS.format(capture=capture)], cwd=root,
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
