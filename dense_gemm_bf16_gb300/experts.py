@@ -145,6 +145,10 @@ def grouped_gemm(A: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor,
     the device; C: [T, N] row-major (allocated when None, in ``out_dtype`` or
     A's dtype; rows of no group are not written); bias: fp32 [N] or [groups, N].
     ``epilogue`` is a name as in ``gemm``.
+
+    Calls repeat bit for bit.  T and the number of groups choose the kernel, and with
+    it the order of a row's sum; at equal ones a group's results do not depend on the
+    other groups.
     """
     dt = _code16(A, B)
     if A.dim() != 2 or B.dim() != 3 or A.shape[1] != B.shape[1]:

@@ -46,8 +46,11 @@ extern "C" {
  *                a multiple of 16 bytes), which is copied first.
  *                gemm_grouped_workspace_size() always suffices.
  *
- * Products accumulate in fp32 and are rounded once.  Results do not depend on
- * the other groups, and repeat bit for bit.
+ * Products accumulate in fp32 and are rounded once.  Calls repeat bit for bit.
+ * T, groups, N and the operands' layout choose the kernel and its tiles, and with
+ * them the order of a row's sum; where they are equal, a group's results do not
+ * depend on the other groups' rows, weights or sizes, bit for bit.  (One more row,
+ * of any group, may change the last bits of all.)
  */
 gemm_status_t gemm_grouped(gemm_dtype_t ab_dtype, int64_t groups, int64_t T, int64_t N, int64_t K,
                            const void* A, int64_t lda,

@@ -802,3 +802,56 @@ def test_a_dense_product_does_not_load_the_expert_kernels(capture):
     r = subprocess.run([sys.executable, "-c", FIRST_CALLS.format(capture=capture)], cwd=root,
                        capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+# rows in all, experts, N: few rows, and the ragged kernel in tiles of 32 columns, of 128,
+# and in pairs (at least 38 tiles of 256 x 256)
+VARIANTS = {"few": (60, 4, 256), "t32": (110, 4, 256), "t128": (700, 4, 256),
+            "pairs": (3000, 4, 1000)}
+
+
+@pytest.mark.parametrize("case", sorted(VARIANTS))
+@pytest.mark.parametrize("layout", ["row", "col"])
+def test_grouped_results_do_not_depend_on_the_other_groups(case, layout):
+    """At equal T and number of groups the others' rows, weights and sizes change, and the
+    one group's place with them; its fp32 sums stay equal bit for bit."""
+    T, E, N = VARIANTS[case]
+    K, n = 520, T // 3
+    g = torch.Generator(device=DEV).manual_seed(5)
+
+    def rand(*shape):
+        return torch.randn(shape, generator=g, device=DEV).to(BF)
+
+    rows, weights = rand(n, K), rand(K, N) if layout == "row" else rand(N, K).t()
+    got = []
+    for sizes, e in (([n // 2, n, T - n - n // 2, 0], 1), ([0, T - n, n, 0], 2),
+                     ([n, 1, T - n - 5, 4], 0), ([T - n, 0, 0, n], 3)):
+        b = bounds_of(sizes)
+        assert b[-1] == T
+        A, B = rand(T, K) * 100, rand(E, K, N) if layout == "row" else rand(E, N, K).transpose(1, 2)
+        A[b[e]:b[e + 1]], B[e] = rows, weights
+        got.append(dg.grouped_gemm(A, B, offs(b), out_dtype=F32)[b[e]:b[e + 1]])
+    assert float(got[0].abs().max()) > 1.0
+    for other in got[1:]:
+        assert torch.equal(got[0], other)
+    assert status() == 0
+
+
+@pytest.mark.parametrize("T,out", [(30, BF), (30, F32), (150, F32), (200, BF)])
+def test_w4_results_do_not_depend_on_the_other_experts(T, out):
+    """The same for 4-bit experts: the integers themselves, and 16-bit weights (200 rows)."""
+    E, K, N, n = 4, 512, 200, T // 3
+    g = torch.Generator(device=DEV).manual_seed(6)
+    q0 = torch.randint(0, 256, (N, K // 2), generator=g, device=DEV, dtype=torch.uint8)
+    s0 = torch.rand((N, K // 64), generator=g, device=DEV).to(BF)
+    rows = torch.randn((n, K), generator=g, device=DEV).to(BF)
+    got = []
+    for sizes, e in (([n // 2, n, T - n - n // 2, 0], 1), ([0, T - n, n, 0], 2), ([T - n, 0, 0, n], 3)):
+        b = bounds_of(sizes)
+        x = torch.randn((T, K), generator=g, device=DEV).to(BF)
+        q = torch.randint(0, 256, (E, N, K // 2), generator=g, device=DEV, dtype=torch.uint8)
+        s = torch.rand((E, N, K // 64), generator=g, device=DEV).to(BF)
+        x[b[e]:b[e + 1]], q[e], s[e] = rows, q0, s0
+        got.append(dg.w4_gemm(x, q, s, offsets=offs(b), out_dtype=out)[b[e]:b[e + 1]])
+    for other in got[1:]:
+        assert torch.equal(got[0], other)
