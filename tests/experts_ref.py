@@ -77,6 +77,30 @@ def newton_schulz(G, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7):
     return X[0] if single else X
 
 
+def newton_schulz_fp16(G, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7):
+    """The same with what the kernels hold between products rounded to fp16: X times
+    2^13, Y = S + b / (2 c) and P = c Y Y + a - b b / (4 c) times 2^12, the result as it
+    is; all products in 64 bits, S on the smaller side."""
+    a, b, c = coefficients
+
+    def fp16(x, scale=1.0):
+        return (x * scale).astype(np.float16).astype(np.float64) / scale
+
+    def one(x):
+        X = fp16(x / (np.sqrt((x * x).sum()) + eps), 2.0 ** 13)
+        wide = X.shape[0] <= X.shape[1]
+        eye = np.eye(min(X.shape))
+        for step in range(steps):
+            Y = fp16((X @ X.T if wide else X.T @ X) + b / (2 * c) * eye, 2.0 ** 12)
+            P = fp16(c * (Y @ Y) + (a - b * b / (4 * c)) * eye, 2.0 ** 12)
+            X = P @ X if wide else X @ P
+            X = fp16(X, 1.0 if step == steps - 1 else 2.0 ** 13)
+        return X
+
+    G = f64(G)
+    return one(G) if G.ndim == 2 else np.stack([one(x) for x in G])
+
+
 def w4_weights(q, scales, zeros):
     """[..., N, K] weights of packed q [..., N, K / 2]."""
     q = q.cpu().numpy().astype(np.int64)

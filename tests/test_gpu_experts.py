@@ -855,3 +855,327 @@ def test_w4_results_do_not_depend_on_the_other_experts(T, out):
         got.append(dg.w4_gemm(x, q, s, offsets=offs(b), out_dtype=out)[b[e]:b[e + 1]])
     for other in got[1:]:
         assert torch.equal(got[0], other)
+
+
+# ---------------------------------------------------------------- CTA pairs
+# Row products and the 16-bit route of 4-bit ones take pairs of CTAs (tiles of 256 x 256)
+# from half as many tiles on as pairs fit the GPU (38 of 76): groups * ceil(N / 256) *
+# ceil(rows of a group on average / 256) of them, and more than 128 rows and columns.
+
+PAIR_COUNTS = [300, 0, 513, 700, 31, 257]               # 1801 rows, 301 on average: 2 x 6 x
+                                                        # ceil(N / 256) >= 48 tiles
+
+
+def on_pairs(E, T, N):
+    avg = -(-T // E)
+    return avg > 128 and N > 128 and E * -(-N // 256) * -(-avg // 256) >= 38
+
+
+@pytest.mark.parametrize("dtype,out", [(BF, BF), (BF, F32), (HF, HF), (HF, F32)])
+@pytest.mark.parametrize("layout", ["row", "col"])
+@pytest.mark.parametrize("K,N", [(320, 1000), (200, 1032), (64, 1001), (136, 1288)])
+def test_grouped_pairs_exact(K, N, layout, dtype, out):
+    """Both layouts (two K blocks a load where K is a multiple of 64), widths in steps of
+    32, and rows of C that start on odd addresses (N = 1001)."""
+    rng = np.random.default_rng(K + N)
+    b = bounds_of(PAIR_COUNTS, 2)
+    T, E = b[-1] + 1, len(PAIR_COUNTS)
+    assert on_pairs(E, T, N)
+    A = ints(rng, (T, K), dtype=dtype)
+    B = ints(rng, (E, K, N) if layout == "row" else (E, N, K), dtype=dtype)
+    B = B if layout == "row" else B.transpose(1, 2)
+    C = torch.full((T, N), float("nan"), dtype=out, device=DEV)
+    dg.grouped_gemm(A.to(DEV), B.to(DEV), offs(b), C)
+    equal(C, ref.grouped(A, B, b), out)
+    assert status() == 0
+
+
+@pytest.mark.parametrize("layout", ["row", "col"])
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("N", [1000, 1001])
+def test_grouped_pairs_beta_bias_relu(N, out, layout):
+    rng = np.random.default_rng(71)
+    b = bounds_of(PAIR_COUNTS, 1)
+    T, K, E = b[-1] + 2, 200, len(PAIR_COUNTS)
+    assert on_pairs(E, T, N)
+    A, bias, C0 = ints(rng, (T, K)), ints(rng, (E, N), dtype=F32), ints(rng, (T, N), dtype=out)
+    B = ints(rng, (E, K, N)) if layout == "row" else ints(rng, (E, N, K)).transpose(1, 2)
+    got = dg.grouped_gemm(A.to(DEV), B.to(DEV), offs(b), C0.to(DEV), alpha=2.0, beta=-0.5,
+                          bias=bias.to(DEV), epilogue="bias_relu")
+    equal(got, ref.grouped(A, B, b, C0, 2.0, -0.5, bias, "bias_relu"), out)
+
+
+@pytest.mark.parametrize("copied", ["A", "B", "both"])
+def test_grouped_pairs_with_copied_operands(copied):
+    """Operands of odd pitch: the product is launched while their copy runs."""
+    rng = np.random.default_rng(72)
+    b = bounds_of(PAIR_COUNTS)
+    T, K, N, E = b[-1], 192, 1000, len(PAIR_COUNTS)
+    assert on_pairs(E, T, N)
+    A = ints(rng, (T, K + (copied != "B"))).to(DEV)[:, :K]
+    B = ints(rng, (E, K, N + (copied != "A"))).to(DEV)[:, :, :N]
+    for _ in range(3):
+        equal(dg.grouped_gemm(A, B, offs(b), out_dtype=F32), ref.grouped(A, B, b), F32)
+    assert status() == 0
+
+
+@pytest.mark.parametrize("epilogue", ["bias_gelu_tanh", "gelu_erf"])
+def test_grouped_pairs_gelu(epilogue):
+    """The bound of test_grouped_gelu, for a 16-bit output with its own rounding (2^-8)."""
+    rng = np.random.default_rng(73)
+    b = bounds_of(PAIR_COUNTS)
+    T, K, N, E = b[-1], 320, 1000, len(PAIR_COUNTS)
+    assert on_pairs(E, T, N)
+    A = torch.from_numpy(rng.standard_normal((T, K)).astype(np.float32)).to(BF)
+    B = torch.from_numpy(rng.standard_normal((E, N, K)).astype(np.float32) / 18).to(BF).transpose(1, 2)
+    bias = torch.from_numpy(rng.standard_normal((E, N)).astype(np.float32))
+    use = bias if epilogue.startswith("bias") else None
+    want = ref.grouped(A, B, b, bias=use, epilogue=epilogue)
+    size = ref.grouped(A.abs(), B.abs(), b, bias=None if use is None else use.abs())
+    for out in (F32, BF):
+        got = dg.grouped_gemm(A.to(DEV), B.to(DEV), offs(b), out_dtype=out, epilogue=epilogue,
+                              bias=None if use is None else use.to(DEV))
+        bound = 1.13 * K * 2.0 ** -23 * size + 2.0 ** -20 * (size + np.abs(want))
+        if out == BF:
+            bound = bound + 2.0 ** -8 * np.abs(want)
+        assert np.all(np.abs(ref.f64(got) - want) <= bound)
+
+
+def test_grouped_pairs_do_not_mix_rows():
+    rng = np.random.default_rng(74)
+    b = bounds_of(PAIR_COUNTS)
+    T, K, N, E = b[-1], 136, 1000, len(PAIR_COUNTS)
+    A, B = ints(rng, (T, K)), ints(rng, (E, K, N))
+    want = ref.grouped(A, B, b)
+    A[7], A[900], B[5] = float("nan"), float("inf"), float("nan")
+    got = ref.f64(dg.grouped_gemm(A.to(DEV), B.to(DEV), offs(b), out_dtype=F32))
+    keep = [i for i in range(b[5]) if i not in (7, 900)]
+    assert np.array_equal(got[keep], want[keep])
+    assert np.isnan(got[7]).all() and np.isnan(got[b[5]:]).all()
+
+
+def test_grouped_pairs_replayed_from_a_graph():
+    rng = np.random.default_rng(75)
+    b = bounds_of(PAIR_COUNTS)
+    T, K, N, E = b[-1], 128, 1000, len(PAIR_COUNTS)
+    A, B, o = ints(rng, (T, K)).to(DEV), ints(rng, (E, K, N)).to(DEV), offs(b)
+    odd = ints(rng, (E, K, N + 1)).to(DEV)[:, :, :N]       # copied in every replay
+    y, z = (torch.empty((T, N), dtype=F32, device=DEV) for _ in range(2))
+    dg.grouped_gemm(A, odd, o, z)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        dg.grouped_gemm(A, B, o, y)
+        dg.grouped_gemm(A, odd, o, z)
+    for counts in (PAIR_COUNTS, PAIR_COUNTS[::-1], [0, 0, T, 0, 0, 0]):
+        b = bounds_of(counts)
+        o.copy_(offs(b))
+        A.copy_(ints(rng, (T, K)))
+        y.zero_(), z.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        equal(y, ref.grouped(A, B, b), F32)
+        equal(z, ref.grouped(A, odd, b), F32)
+    assert status() == 0
+
+
+@pytest.mark.parametrize("out", [F32, BF])
+@pytest.mark.parametrize("odd", [0, 1])
+def test_wgrad_pairs_accumulate(odd, out):
+    """beta on the pair tiles; odd: copied operands, and a C of odd rows (no TMA stores)."""
+    rng = np.random.default_rng(76)
+    b = bounds_of([300, 0, 77, 130, 16, 1000], 1)
+    M, N, T = 1000 + odd, 1032 + odd, b[-1] + 1
+    A, D = ints(rng, (T, M), -2, 2), ints(rng, (T, N), -2, 2)
+    C0 = ints(rng, (6, M, N), dtype=out)
+    got = dg.grouped_gemm_wgrad(A.to(DEV), D.to(DEV), offs(b), C0.to(DEV), alpha=0.5, beta=2.0)
+    equal(got, ref.wgrad(A, D, b, C0, 0.5, 2.0), out)
+    assert status() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("experts", [0, 4])
+def test_w4_pairs(experts, dtype):
+    """The 16-bit route on pair tiles: one matrix (equal widths), and experts."""
+    rng = np.random.default_rng(77 + experts)
+    counts = [900, 0, 513, 700] if experts else [2000]
+    b = bounds_of(counts)
+    T, N, K = b[-1], 1032, 320
+    assert on_pairs(len(counts), T, N)
+    x, q, s, z = w4_case(rng, T, N, K, 64, True, dtype, experts)
+    bias = ints(rng, (N,), dtype=F32)
+    got = w4_run(x, q, s, z, bias=bias.to(DEV), epilogue="bias_relu",
+                 offsets=offs(b) if experts else None)
+    equal(got, ref.w4(x, q, s, z, b if experts else None, bias, "bias_relu"), dtype)
+    assert status() == 0
+
+
+# ---------------------------------------------------------------- K over four CTAs
+# Few rows and the direct 4-bit form cut K over a cluster of four where the units (tiles
+# of 64 rows by the tokens of a tile) are at most 38 (a quarter of the SMs) and K has
+# 16 stages: of 128 with 16-bit weights, of 256 (groups of 32, more than 16 tokens) or 512.
+
+@pytest.mark.parametrize("group,K", [(32, 8192), (64, 16384), (128, 16384), (128, 16512), (32, 8224)])
+@pytest.mark.parametrize("T,N", [(1, 200), (9, 130), (33, 70)])
+def test_w4_split_over_four(T, N, group, K):
+    rng = np.random.default_rng(T + K)
+    x, q, s, z = w4_case(rng, T, N, K, group, True)
+    x = x.clamp(-1, 1)                                     # sums below 2^24 quarters
+    bias = ints(rng, (N,), dtype=F32)
+    for out in (F32, BF):
+        equal(w4_run(x, q, s, z, out_dtype=out, bias=bias.to(DEV), epilogue="bias_relu"),
+              ref.w4(x, q, s, z, bias=bias, epilogue="bias_relu"), out)
+    assert status() == 0
+
+
+@pytest.mark.parametrize("layout", ["row", "col"])
+@pytest.mark.parametrize("counts", [[1], [1, 0, 1], [5, 0, 9], [30]])
+@pytest.mark.parametrize("K,N", [(4096, 200), (4104, 130), (5000, 72)])
+def test_few_rows_split_over_four(K, N, counts, layout):
+    rng = np.random.default_rng(K + N)
+    b = bounds_of(counts, 1)
+    E, T = len(counts), b[-1] + 1
+    A, bias = ints(rng, (T, K), -2, 2), ints(rng, (E, N), dtype=F32)
+    B = ints(rng, (E, K, N), -2, 2) if layout == "row" else \
+        ints(rng, (E, N, K), -2, 2).transpose(1, 2)
+    C0 = ints(rng, (T, N), dtype=F32)
+    got = dg.grouped_gemm(A.to(DEV), B.to(DEV), offs(b), C0.to(DEV), alpha=0.5, beta=2.0,
+                          bias=bias.to(DEV), epilogue="bias_relu")
+    equal(got, ref.grouped(A, B, b, C0, 0.5, 2.0, bias, "bias_relu"), F32)
+    assert status() == 0
+
+
+# ---------------------------------------------------------------- fp32 sums of other numbers
+
+def prefix_norms(A, D, step=16):
+    """sum over the MMA steps j of |P_j|_F, P_j the exact sum after j steps of 16."""
+    P, total = np.zeros((A.shape[1], D.shape[1])), 0.0
+    for k in range(0, A.shape[0], step):
+        P += A[k:k + step].T @ D[k:k + step]
+        total += np.linalg.norm(P)
+    return P, total
+
+
+@pytest.mark.parametrize("counts,M,N", [([900, 77, 1500], 120, 136), ([513, 0, 1000, 300, 700, 31], 1000, 1032)])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_wgrad_fp32_sums(counts, M, N, dtype):
+    """Normal inputs: the accumulator holds 24 bits and each step of 16 may lose one unit
+    in the last place of it, so the error's norm is at most 2^-23 times the sum of the
+    norms of the partial sums."""
+    rng = np.random.default_rng(81)
+    b = bounds_of(counts)
+    A = torch.from_numpy(rng.standard_normal((b[-1], M)).astype(np.float32)).to(dtype)
+    D = torch.from_numpy(rng.standard_normal((b[-1], N)).astype(np.float32)).to(dtype)
+    got = ref.f64(dg.grouped_gemm_wgrad(A.to(DEV), D.to(DEV), offs(b), out_dtype=F32))
+    a, d = ref.f64(A), ref.f64(D)
+    for e in range(len(counts)):
+        want, size = prefix_norms(a[b[e]:b[e + 1]], d[b[e]:b[e + 1]])
+        assert np.linalg.norm(got[e] - want) <= 2.0 ** -23 * size
+
+
+@pytest.mark.parametrize("counts,K,N", [([20, 3, 30], 1000, 136), ([40, 30, 60], 2000, 136),
+                                        ([300, 0, 513, 700, 31, 257], 1500, 1000)])
+def test_grouped_fp32_sums(counts, K, N):
+    """The same for the row products, by group: few rows, single CTAs, pairs.  (Few rows:
+    slices of K are summed apart, which only shortens the partial sums' paths.)"""
+    rng = np.random.default_rng(82)
+    b = bounds_of(counts)
+    A = torch.from_numpy(rng.standard_normal((b[-1], K)).astype(np.float32)).to(BF)
+    B = torch.from_numpy(rng.standard_normal((len(counts), K, N)).astype(np.float32)).to(BF)
+    got = ref.f64(dg.grouped_gemm(A.to(DEV), B.to(DEV), offs(b), out_dtype=F32))
+    for e in range(len(counts)):
+        if b[e] < b[e + 1]:
+            want, size = prefix_norms(ref.f64(A[b[e]:b[e + 1]]).T, ref.f64(B[e]))
+            assert np.linalg.norm(got[b[e]:b[e + 1]] - want) <= 2.0 ** -23 * size
+
+
+# ---------------------------------------------------------------- Newton-Schulz, block by block
+
+@pytest.mark.parametrize("shape", [(64, 64), (129, 257), (300, 200), (96, 1000), (3, 200, 264),
+                                   (6, 257, 130),                               # 64-column tiles
+                                   (15, 257, 300), (15, 300, 257), (40, 100, 300),  # 128 columns
+                                   (10, 520, 600), (20, 512, 640), (10, 600, 520),  # pairs
+                                   (2100, 2304), (2310, 2100)])
+@pytest.mark.parametrize("steps", [1, 5])
+def test_newton_schulz_block_by_block(shape, steps):
+    """Against the 64-bit result, the error may be 1.5 times that of the same steps with X,
+    Y and the polynomial rounded to fp16 between exact products (fp32 sums and roundings
+    that fall the other way add little to it): over every matrix, over its worst 32 x 32
+    block, and twice that for its worst entry.  One wrong 8 x 8 part of a block is two
+    hundred times its error."""
+    rng = np.random.default_rng(sum(shape) + steps)
+    G = torch.from_numpy(rng.standard_normal(shape).astype(np.float32))
+    got = ref.f64(dg.newton_schulz(G.to(DEV), steps=steps, out_dtype=HF))
+    assert status() == 0
+    want, near = ref.newton_schulz(G, steps), ref.newton_schulz_fp16(G, steps)
+    if len(shape) == 2:
+        got, want, near = got[None], want[None], near[None]
+    for g, w, n in zip(got, want, near):
+        for size in (w.shape, (32, 32), (1, 1)):
+            allowed = max(blocks(n - w, size)) * (1.5 if size != (1, 1) else 2.0)
+            assert max(blocks(g - w, size)) <= allowed, size
+
+
+def blocks(x, size):
+    """Root mean squares of the blocks of x."""
+    if size == (1, 1):
+        return [np.abs(x).max()]
+    return [np.sqrt((x[i:i + size[0], j:j + size[1]] ** 2).mean())
+            for i in range(0, x.shape[0], size[0]) for j in range(0, x.shape[1], size[1])
+            if x[i:i + size[0], j:j + size[1]].size >= 256]   # (slivers: by entries)
+
+
+# ---------------------------------------------------------------- waits that run out
+
+def stalled(call):
+    """`call` with one stage left unfilled and a short limit: its status."""
+    dg.gemm_set_option(dg.Option.TIMEOUT_US, 20000)
+    try:
+        dg.gemm_set_option(dg.Option.TEST_STALL, 1)
+        call()
+        return status()
+    finally:
+        dg.gemm_set_option(dg.Option.TEST_STALL, 0)
+        dg.gemm_set_option(dg.Option.TIMEOUT_US, 1000000)
+
+
+@pytest.mark.parametrize("M,N", [(72, 136), (1000, 1032)])
+@pytest.mark.parametrize("out", [F32, BF])
+def test_a_stalled_weight_gradient_recovers(M, N, out):
+    """Ragged groups, so that the tail warp waits too; single CTAs and pairs."""
+    rng = np.random.default_rng(91)
+    b = bounds_of([300, 0, 77, 130, 17, 401])
+    A, D = ints(rng, (b[-1], M), -2, 2).to(DEV), ints(rng, (b[-1], N), -2, 2).to(DEV)
+    assert stalled(lambda: dg.grouped_gemm_wgrad(A, D, offs(b), out_dtype=out)) == \
+        dg.Status.ERR_TIMEOUT
+    equal(dg.grouped_gemm_wgrad(A, D, offs(b), out_dtype=out), ref.wgrad(A, D, b), out)
+    assert status() == 0
+
+
+@pytest.mark.parametrize("shape", [(100, 140), (15, 257, 300), (20, 512, 640), (10, 600, 520)])
+def test_a_stalled_newton_schulz_recovers(shape):
+    """CTAs whose own pipeline does not stall wait for a matrix's counter in vain."""
+    G = torch.randn(shape, generator=torch.Generator(device=DEV).manual_seed(7), device=DEV)
+    want = dg.newton_schulz(G)
+    assert status() == 0
+    assert stalled(lambda: dg.newton_schulz(G)) == dg.Status.ERR_TIMEOUT
+    assert torch.equal(dg.newton_schulz(G), want)
+    assert status() == 0
+
+
+@pytest.mark.parametrize("T,N,K,experts", [(1, 200, 16384, 0), (2, 2500, 4096, 0), (40, 300, 512, 0),
+                                           (12, 136, 320, 4)])
+def test_a_stalled_4_bit_product_recovers(T, N, K, experts):
+    """Four and two CTAs of a cluster, whose barriers go on after the failed wait; single
+    CTAs with one and with several units."""
+    rng = np.random.default_rng(92)
+    x, q, s, z = (t.to(DEV) for t in w4_case(rng, T, N, K, 64, True, BF, experts))
+    x = x.clamp(-1, 1)
+    b = bounds_of([3, 0, 8, 1]) if experts else None
+
+    def call():
+        return dg.w4_gemm(x, q, s, zeros=z, offsets=offs(b) if b else None, out_dtype=F32)
+
+    assert stalled(call) == dg.Status.ERR_TIMEOUT
+    equal(call(), ref.w4(x, q, s, z, b), F32)
+    assert status() == 0
