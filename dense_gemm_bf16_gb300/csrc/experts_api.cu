@@ -137,7 +137,7 @@ void rg_variant(const RgProblem& q, const DeviceInfo& d, int* cg, int* bt) {
     } else {
         const int64_t tiles = q.groups * cdiv(q.n_lane, 256) *
                               (q.form == RG_SYM ? (cdiv(cols, 256) + 1) / 2 : cdiv(cols, 256));
-        if (tiles < d.max_pairs / 2) *cg = 1, *bt = 128;
+        if (d.max_pairs == 0 || tiles < d.max_pairs / 2) *cg = 1, *bt = 128;
     }
 }
 

@@ -1067,6 +1067,11 @@ gemm_status_t device_info(DeviceInfo* out) {
     if (d->experts_err != cudaSuccess) return GEMM_ERR_CUDA;
     out->sm_count = d->sm_count;
     out->max_pairs = d->max_pairs[2][1] > 0 ? d->max_pairs[2][1] : d->sm_count / 2;
+    const int64_t cap = g_opt_max_ctas.load();
+    if (cap > 0 && cap < out->sm_count) {
+        out->sm_count = static_cast<int>(cap);
+        if (cap / 2 < out->max_pairs) out->max_pairs = static_cast<int>(cap / 2);
+    }
     out->status = d->status;
     return GEMM_OK;
 }

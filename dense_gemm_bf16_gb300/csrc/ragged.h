@@ -93,8 +93,8 @@ cudaError_t rg_prepare_seq();
 
 // ---- host helpers (gemm_api.cu)
 struct DeviceInfo {
-    int sm_count;
-    int max_pairs;     // two-CTA clusters resident at once
+    int sm_count;      // CTAs a launch may have: one per SM, or the cap of GEMM_OPT_MAX_CTAS
+    int max_pairs;     // two-CTA clusters resident at once, under the cap (0: none)
     int* status;       // device error word
 };
 gemm_status_t device_info(DeviceInfo* out);   // the current device

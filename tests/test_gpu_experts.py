@@ -1179,3 +1179,51 @@ def test_a_stalled_4_bit_product_recovers(T, N, K, experts):
     assert stalled(call) == dg.Status.ERR_TIMEOUT
     equal(call(), ref.w4(x, q, s, z, b), F32)
     assert status() == 0
+
+
+# ---------------------------------------------------------------- process-wide options
+
+def elapsed(call):
+    """The shortest of five calls, in ms."""
+    times = []
+    for _ in range(5):
+        start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        start.record()
+        call()
+        end.record()
+        end.synchronize()
+        times.append(start.elapsed_time(end))
+    return min(times)
+
+
+@pytest.mark.parametrize("cap", [1, 4, 7])
+def test_the_cap_on_ctas_holds(cap):
+    """GEMM_OPT_MAX_CTAS leaves the other SMs to other work: the same results, in at least
+    four times the time of the whole GPU for products that fill it."""
+    rng = np.random.default_rng(95)
+    b = bounds_of([700, 0, 1300, 1096, 500, 500])
+    T, K, N, E = b[-1], 2048, 2048, 6
+    A, B, D = ints(rng, (T, K)).to(DEV), ints(rng, (E, K, N)).to(DEV), ints(rng, (T, N)).to(DEV)
+    x, q, s, z = (t.to(DEV) for t in w4_case(rng, 6, 32768, 4096, 64, True))
+    G, o = torch.randn((24, 512, 640), device=DEV), offs(b)
+    few = offs([0, 3, 3, 5, 6, 6, 6])
+    calls = (lambda: dg.grouped_gemm(A, B, o, out_dtype=F32),
+             lambda: dg.grouped_gemm_wgrad(A, D, o, out_dtype=F32),
+             lambda: dg.w4_gemm(x, q, s, zeros=z, out_dtype=F32),
+             lambda: dg.grouped_gemm(x[:, :K], B, few, out_dtype=F32),
+             lambda: dg.newton_schulz(G))
+    free = [c() for c in calls]
+    fast = [elapsed(c) for c in calls]
+    dg.gemm_set_option(dg.Option.MAX_CTAS, cap)
+    try:
+        capped = [c() for c in calls]
+        slow = [elapsed(c) for c in calls]
+    finally:
+        dg.gemm_set_option(dg.Option.MAX_CTAS, 0)
+    for u, v in zip(free[:4], capped[:4]):
+        assert torch.equal(u, v)                       # (exact)
+    assert float((free[4].float() - capped[4].float()).norm()) <= \
+        2.0 ** -8 * float(free[4].float().norm())
+    for i in (0, 1, 2, 4):
+        assert slow[i] > 4 * fast[i], (i, slow[i], fast[i])
+    assert status() == 0
