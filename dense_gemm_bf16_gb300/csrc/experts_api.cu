@@ -244,7 +244,7 @@ gemm_status_t rg_fill(const RgProblem& q, const DeviceInfo& d, int cg, int bt, R
     p.status = d.status;
     p.timeout_ns = option_timeout_ns();
     p.test_stall = take_test_stall();
-    p.pdl = q.pdl;
+    p.pdl = q.pdl && option_overlap_copy();
 #if DG_DEBUG
     const int64_t out_rows = q.form == RG_ROWS && q.offsets ? q.T : q.n_col;
     p.dbg_c_elems = (q.offsets && q.form == RG_ROWS ? 0 : (q.groups - 1) * q.stride_c) +

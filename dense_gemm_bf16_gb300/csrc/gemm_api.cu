@@ -1078,6 +1078,8 @@ gemm_status_t device_info(DeviceInfo* out) {
 
 uint64_t option_timeout_ns() { return static_cast<uint64_t>(g_opt_timeout_us.load()) * 1000ull; }
 
+bool option_overlap_copy() { return g_opt_overlap_copy.load() == 0; }
+
 int take_test_stall() { return static_cast<int>(g_opt_test_stall.exchange(0)); }
 
 namespace {

@@ -99,6 +99,7 @@ struct DeviceInfo {
 };
 gemm_status_t device_info(DeviceInfo* out);   // the current device
 uint64_t option_timeout_ns();
+bool option_overlap_copy();   // a product may start while its operand is prepared
 int take_test_stall();
 
 // Three-dimensional tensor map of 16-bit elements (inner, outer, depth), 128-byte

@@ -278,7 +278,8 @@ int32_t gemm_build_flags(void);
  * (the caller's batch entry, row and column, whatever C's layout), so that a
  * correct call leaves exactly 1 in each of its batch * M * N counters.  Split-K
  * partials and stream-K partial tiles are not final values and are not
- * counted; gemm_strided's scatter of a dense result is not counted either.
+ * counted; gemm_strided's scatter of a dense result is not counted either, nor
+ * are the calls of gemm_experts.h.
  * Calls whose batch * M * N exceeds count_elems return GEMM_ERR_INVALID_ARG
  * while the mode is on.  NULL turns the mode off.  The caller owns `counts`.
  * Returns GEMM_ERR_UNSUPPORTED in the product library.

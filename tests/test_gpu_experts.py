@@ -1227,3 +1227,24 @@ def test_the_cap_on_ctas_holds(cap):
     for i in (0, 1, 2, 4):
         assert slow[i] > 4 * fast[i], (i, slow[i], fast[i])
     assert status() == 0
+
+
+@pytest.mark.parametrize("overlap", [0, 1])
+def test_copied_operands_with_and_without_overlap(overlap):
+    """GEMM_OPT_OVERLAP_COPY: the product starts while its operand is prepared, or after."""
+    rng = np.random.default_rng(96)
+    b = bounds_of(PAIR_COUNTS)
+    T, K, N, E = b[-1], 201, 1000, len(PAIR_COUNTS)
+    A, B, D = ints(rng, (T, K)), ints(rng, (E, K, N)), ints(rng, (T, N))
+    x, q, s, z = w4_case(rng, 300, 1032, 320, 64, True)
+    dg.gemm_set_option(dg.Option.OVERLAP_COPY, overlap)
+    try:
+        for _ in range(3):
+            equal(dg.grouped_gemm(A.to(DEV), B.to(DEV), offs(b), out_dtype=F32),
+                  ref.grouped(A, B, b), F32)
+            equal(dg.grouped_gemm_wgrad(A.to(DEV), D.to(DEV), offs(b), out_dtype=F32),
+                  ref.wgrad(A, D, b), F32)
+            equal(w4_run(x, q, s, z), ref.w4(x, q, s, z), BF)
+    finally:
+        dg.gemm_set_option(dg.Option.OVERLAP_COPY, 0)
+    assert status() == 0
