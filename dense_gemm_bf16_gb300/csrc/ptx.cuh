@@ -350,6 +350,17 @@ __device__ __forceinline__ void umma_commit_mc(uint32_t bar, uint16_t mask) {
         : "memory");
 }
 
+// Registers a thread of this warpgroup may hold from here on (all its warps).
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // 32 lanes x 32 bits, 32 consecutive columns: thread t of the warp receives
 // lane (taddr.lane + t), columns taddr.col .. taddr.col+31.
 __device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32]) {

@@ -27,7 +27,8 @@
 //
 // Warps: 0 TMA producer, 1 MMA issuer, 10 (RG_WGRAD) ragged tails, 2-9 epilogue,
 // two per tensor-memory lane quarter taking 32-column chunks in
-// turn.  Two accumulators let a tile's epilogue overlap the next main loop.
+// turn (fp32 outputs: 2 tails, 4-11 epilogue).  Two accumulators let a tile's epilogue
+// overlap the next main loop.
 // The output's contiguous dimension runs along the lanes.  A 16-bit chunk is
 // read from tensor memory in the MMA-fragment layout, turned by transposing
 // 8 x 8 matrix stores into a shared-memory tile of 32 columns by 32 lanes (rows
@@ -71,8 +72,11 @@ struct RgCfg {
     static constexpr uint32_t B_BYTES = 2 * B_ROWS * 128;
     static constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int EPI_WARPS = 8;
-    // (RG_WGRAD has one warp more, for the ragged tails)
-    static constexpr int threads(int form) { return 64 + 32 * EPI_WARPS + (form == RG_WGRAD ? 32 : 0); }
+    // (RG_WGRAD has one warp more, for the ragged tails; fp32 outputs take four warps
+    // before the epilogue's, so that registers move between whole warpgroups)
+    static constexpr int threads(int form, bool sum = false) {
+        return sum ? 128 + 32 * EPI_WARPS : 64 + 32 * EPI_WARPS + (form == RG_WGRAD ? 32 : 0);
+    }
     static constexpr uint32_t EPI_WARP = 2 * 2048;  // two tiles of 32 x 32 16-bit elements
     static constexpr uint32_t EPI_SMEM = EPI_WARPS * EPI_WARP;
     static constexpr uint32_t BAR_BYTES = 512;
@@ -558,81 +562,77 @@ __device__ __forceinline__ void rg_out16(const RgParams& p, const RgTile& w, uin
     }
 }
 
-// The same for an fp32 C: one lane (output column) per thread, stores of 32
-// neighbouring columns of one row (RG_WGRAD: TMA boxes of 16 rows by 32 columns).
-template <int FORM, bool ACT, typename Ready, typename Release>
-__device__ __forceinline__ void rg_out32(const RgParams& p, const RgTile& w, uint32_t tmem_row,
-                                         int nl0, int half, int lane, uint8_t* buf, bool empty,
-                                         Ready ready, Release release) {
-    if (!ready()) return;
+// Columns c0 .. c0 + 31 of an fp32 C from their sums v: one lane (output column) per
+// thread, stores of 32 neighbouring columns of one row (RG_WGRAD: TMA boxes of 16 rows by
+// 32 columns).  MORE: with beta * C or an activation.
+template <int FORM, bool MORE>
+__device__ __forceinline__ void rg_out32(const RgParams& p, const RgTile& w, int nl0, int c0,
+                                         float bias, int lane, uint8_t* buf,
+                                         const uint32_t (&v)[32]) {
     const int n = nl0 + lane;
-    const int first = half * 32;
-    if (first >= w.ncols || nl0 >= p.n_lane) {
-        release();
+    const bool in = n < p.n_lane;
+    float o[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] = fmaf(p.alpha, __uint_as_float(v[i]), bias);
+    const int64_t row = w.out_row + c0;
+    if (MORE && p.beta != 0.0f && in) {
+        const float* src = static_cast<const float*>(p.Cin) + w.group * p.stride_cin +
+                           row * p.ldcin + n;
+        float f[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) f[i] = c0 + i < w.ncols ? src[i * p.ldcin] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = fmaf(p.beta, f[i], o[i]);
+    }
+    if (MORE && FORM == RG_ROWS) rg_act(o, p.act);
+    if (FORM == RG_WGRAD && p.c_tma) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (c0 + 16 * h >= w.ncols) break;
+            if (lane == 0) bulk_wait_group_read<0>();
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                *reinterpret_cast<float*>(buf + i * 128 + lane * 4) = o[16 * h + i];
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                tma_store_3d(&p.tmap_c, smem_u32(buf), nl0, w.out_row + c0 + 16 * h, w.group,
+                             l2_policy_evict_normal());
+                bulk_commit_group();
+            }
+        }
         return;
     }
-    const bool in = n < p.n_lane;
-    const float bias = p.bias && in ? __ldg(p.bias + w.group * p.stride_bias + n) : 0.0f;
-    const bool beta = p.beta != 0.0f;
-    uint32_t r[32];
-#pragma unroll 1
-    for (int c0 = first; c0 < w.ncols; c0 += 64) {
-        if (empty) {
+    if (!in) return;
+    const int64_t off = w.group * p.stride_c + row * p.ldc + n;
+    float* dst = static_cast<float*>(p.C) + off;
+    const int left = w.ncols - c0;
+    if (left >= 32) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) r[i] = 0u;
-        } else {
-            tmem_ld_x32(tmem_row + static_cast<uint32_t>(c0), r);
-            tmem_ld_wait(r);
-        }
-        float v[32];
+        for (int i = 0; i < 32; ++i)
+            if (rg_span_ok(p, off + i * p.ldc, 1)) dst[i * p.ldc] = o[i];
+    } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = fmaf(p.alpha, __uint_as_float(r[i]), bias);
-        const bool more = c0 + 64 < w.ncols;
-        if (!more && !empty) release();
-        const int64_t row = w.out_row + c0;
-        if (beta && in) {
-            const float* src = static_cast<const float*>(p.Cin) + w.group * p.stride_cin +
-                               row * p.ldcin + n;
-            float f[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) f[i] = c0 + i < w.ncols ? src[i * p.ldcin] : 0.0f;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = fmaf(p.beta, f[i], v[i]);
-        }
-        if (ACT) rg_act(v, p.act);
-        if (FORM == RG_WGRAD && p.c_tma) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (c0 + 16 * h >= w.ncols) break;
-                if (lane == 0) bulk_wait_group_read<0>();
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    *reinterpret_cast<float*>(buf + i * 128 + lane * 4) = v[16 * h + i];
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    tma_store_3d(&p.tmap_c, smem_u32(buf), nl0, w.out_row + c0 + 16 * h, w.group,
-                                 l2_policy_evict_normal());
-                    bulk_commit_group();
-                }
-            }
-            continue;
-        }
-        if (!in) continue;
-        const int64_t off = w.group * p.stride_c + row * p.ldc + n;
-        float* dst = static_cast<float*>(p.C) + off;
-        const int left = w.ncols - c0;
-        if (left >= 32) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (rg_span_ok(p, off + i * p.ldc, 1)) dst[i * p.ldc] = v[i];
-        } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (i < left && rg_span_ok(p, off + i * p.ldc, 1)) dst[i * p.ldc] = v[i];
-        }
+        for (int i = 0; i < 32; ++i)
+            if (i < left && rg_span_ok(p, off + i * p.ldc, 1)) dst[i * p.ldc] = o[i];
     }
+}
+
+// Stages of 128 of a tile's contraction (RG_WGRAD: of its whole K = 16 steps), and for an
+// fp32 output the sums that it is cut into: RG_SUM stages each, the last one the rest
+// and the ragged tail.
+constexpr int RG_SUM = 6;
+
+template <int FORM>
+__device__ __forceinline__ int rg_stages(int klen) {
+    return ((FORM == RG_WGRAD ? klen & ~15 : klen) + 127) / 128;
+}
+
+template <int FORM>
+__device__ __forceinline__ int rg_sums(int klen) {
+    const int stages = rg_stages<FORM>(klen);
+    return klen == 0 ? 0 : stages <= RG_SUM ? 1 : (stages + RG_SUM - 1) / RG_SUM;
 }
 
 // Products that stand alone wait for nothing and tell no one.
@@ -695,7 +695,7 @@ __device__ __forceinline__ void rg_produce(const RgParams& p, const RgCta& x, Rg
         const CUtensorMap* map_b = big || b_mn ? &p.tmap_b : &p.tmap_b32;
         const uint32_t bytes = C::A_BYTES + b_bytes;
         // (RG_WGRAD: whole K = 16 steps; the tail warp loads the rest)
-        const int ksteps = ((FORM == RG_WGRAD ? w.klen & ~15 : w.klen) + 127) / 128;
+        const int ksteps = rg_stages<FORM>(w.klen);
         if constexpr (!std::is_same<Gate, RgAlone>::value) {
             int open = 1;
             if (x.lane == 0) open = gate(w.group) ? 1 : 0;
@@ -782,7 +782,7 @@ __device__ __forceinline__ void rg_produce_end(const RgParams& p, const RgCta& x
 
 // ------------------------------------------------ MMA issuer (a warp)
 // (nothing to do in the pair's peer)
-template <int CG, int BT, int FORM>
+template <int CG, int BT, int FORM, bool SUM = false>
 __device__ __forceinline__ void rg_issue(const RgParams& p, const RgCta& x, RgRole& r, int first) {
     using C = RgCfg<CG, BT>;
     constexpr uint16_t kPair = 3u;
@@ -802,11 +802,12 @@ __device__ __forceinline__ void rg_issue(const RgParams& p, const RgCta& x, RgRo
         w.n_mma = rg_uniform(w.n_mma);
         const bool tail = FORM == RG_WGRAD && (w.klen & 15) != 0;
         const int klen = FORM == RG_WGRAD ? w.klen & ~15 : w.klen;
-        const int ksteps = (klen + 127) / 128;
-        const uint32_t d_tmem = static_cast<uint32_t>(rg_uniform(static_cast<int>(x.tmem_base))) +
-                                static_cast<uint32_t>(r.abuf * BT);
+        const int ksteps = rg_stages<FORM>(w.klen);
+        const uint32_t tmem0 = static_cast<uint32_t>(rg_uniform(static_cast<int>(x.tmem_base)));
+        uint32_t d_tmem = 0;
         const uint32_t idesc = p.idesc | (static_cast<uint32_t>(w.n_mma >> 3) << 17);
-        auto issue = [&](int ks, int steps) {
+        // `fresh`: the first stage of a sum; `last`: the accumulator goes to the epilogue
+        auto issue = [&](bool fresh, bool last, int steps) {
             const uint64_t ad = a_desc0 + static_cast<uint32_t>(r.stage) * (C::A_BYTES >> 4);
             const uint64_t bd = b_desc0 + static_cast<uint32_t>(r.stage) * (C::B_BYTES >> 4);
             const uint32_t empty = x.empty0 + 8u * r.stage;
@@ -816,18 +817,18 @@ __device__ __forceinline__ void rg_issue(const RgParams& p, const RgCta& x, RgRo
                     for (int k = 0; k < 8; ++k)
                         umma_f16_cg<CG>(d_tmem, ad + (k >> 2) * a_block + (k & 3) * a_step,
                                         bd + (k >> 2) * b_block + (k & 3) * b_step, idesc,
-                                        (ks > 0 || k > 0) ? 1u : 0u);
+                                        (!fresh || k > 0) ? 1u : 0u);
                 } else {
                     for (int k = 0; k < steps; ++k)
                         umma_f16_cg<CG>(d_tmem, ad + (k >> 2) * a_block + (k & 3) * a_step,
                                         bd + (k >> 2) * b_block + (k & 3) * b_step, idesc,
-                                        (ks > 0 || k > 0) ? 1u : 0u);
+                                        (!fresh || k > 0) ? 1u : 0u);
                 }
                 if constexpr (CG > 1)
                     umma_commit_mc_cg<CG>(empty, kPair);
                 else
                     umma_commit_cg<CG>(empty);
-                if (!tail && ks == ksteps - 1) {
+                if (last) {
                     if constexpr (CG > 1)
                         umma_commit_mc_cg<CG>(x.tfull0 + 8u * r.abuf, kPair);
                     else
@@ -838,14 +839,31 @@ __device__ __forceinline__ void rg_issue(const RgParams& p, const RgCta& x, RgRo
         // The whole warp walks the stages and one lane issues, so that the stage's
         // addresses stay in uniform registers (16384 x 4096 x 2048: 174 -> 154 us; one
         // lane alone took as long to issue eight MMAs as they take to run).
-        r.ok = rg_all_wait(x.tempty0 + 8u * r.abuf, r.aphase ^ 1u, p, x.abort_flag);
-        if (r.ok) tc_fence_after_sync();
+        auto open = [&]() {
+            d_tmem = tmem0 + static_cast<uint32_t>(r.abuf * BT);
+            r.ok = rg_all_wait(x.tempty0 + 8u * r.abuf, r.aphase ^ 1u, p, x.abort_flag);
+            if (r.ok) tc_fence_after_sync();
+        };
+        auto close = [&]() {
+            if (++r.abuf == 2) {
+                r.abuf = 0;
+                r.aphase ^= 1u;
+            }
+        };
+        open();
         for (int ks = 0; r.ok && ks < ksteps; ++ks) {
+            const bool fresh = SUM ? ks % RG_SUM == 0 : ks == 0;
+            if (SUM && fresh && ks > 0) {
+                close();
+                open();
+                if (!r.ok) break;
+            }
             r.ok = rg_all_wait(x.full0 + 8u * r.stage, r.phase, p, x.abort_flag);
             if (!r.ok) break;
             tc_fence_after_sync();
             const int left = klen - ks * 128;
-            issue(ks, left >= 128 ? 8 : (left + 15) / 16);
+            issue(fresh, ks == ksteps - 1 ? !tail : SUM && ks % RG_SUM == RG_SUM - 1,
+                  left >= 128 ? 8 : (left + 15) / 16);
             r.issued = true;
             if (++r.stage == C::STAGES) {
                 r.stage = 0;
@@ -876,10 +894,7 @@ __device__ __forceinline__ void rg_issue(const RgParams& p, const RgCta& x, RgRo
                 r.issued = true;
             }
         }
-        if (++r.abuf == 2) {
-            r.abuf = 0;
-            r.aphase ^= 1u;
-        }
+        close();
         r.ok = __all_sync(0xffffffffu, r.ok) != 0;
     }
 }
@@ -982,16 +997,104 @@ __device__ __forceinline__ void rg_epilogue(const RgParams& p, const RgCta& x, R
             if (x.lane == 0)
                 mbar_arrive_relaxed(mapa_shared(x.tempty0 + 8u * r.abuf, 0u));
         };
-        if (p.c_dtype == DT_F32)
-            rg_out32<FORM, ACT>(p, w, tmem_row, nl0, half, x.lane, buf, empty, ready, release);
-        else
-            rg_out16<FORM, ACT>(p, w, tmem_row, nl0, half, x.lane, buf, empty, ready, release);
+        rg_out16<FORM, ACT>(p, w, tmem_row, nl0, half, x.lane, buf, empty, ready, release);
         if (!r.ok) break;
         told(w.group);
         if (!empty && ++r.abuf == 2) {
             r.abuf = 0;
             r.aphase ^= 1u;
         }
+    }
+    if (FORM == RG_WGRAD && x.lane == 0) bulk_wait_group_all();  // the staged tiles have been read
+    __syncwarp();
+}
+
+// The same for an fp32 output (warps 4 to 11).  The tensor core cuts off what an addition
+// leaves below its accumulator's 24 bits, always towards zero, so that the error grows
+// with the length of the sum (2.1e-6 of the result for 2048 products, 1.9e-5 for 16384).
+// Here an accumulator takes RG_SUM stages (768 products) and the epilogue adds it to sums
+// in its registers, rounding to nearest, while the MMAs go on in the other one: 7e-7 at
+// any length.  It costs 192 -> 197 us for the weight gradient of 16384 rows over 16
+// groups, 2048 x 4096, and nothing measurable for row products; stages of 4 (4.7e-7) and
+// 8 (1.0e-6) took 199 and 195 us.
+template <int CG, int BT, int FORM>
+__device__ __forceinline__ void rg_epilogue_sum(const RgParams& p, const RgCta& x, RgRole& r,
+                                                int first, int warp, uint8_t* buf) {
+    constexpr int NC = BT < 64 ? 1 : BT / 64;  // 32-column chunks of a warp
+    const int q = warp & 3;                    // tensor-memory lane quarter of this warp
+    const int c_first = ((warp - 4) >> 2) * 32;
+    const uint32_t tmem_row = x.tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                              static_cast<uint32_t>(c_first);
+    RgWalk walk = rg_begin<FORM>(p, x.lane);
+    RgTile w;
+    for (int t = first; rg_tile<CG, BT, FORM>(p, walk, t, x.lane, x.rank, w); t += x.ncl) {
+        const int nl0 = w.lane0 + q * 32;  // first output column of this warp
+        const bool mine = c_first < w.ncols && nl0 < p.n_lane;
+        const int sums = rg_sums<FORM>(w.klen);
+        uint32_t v[NC][32];                // (bits of the fp32 sums)
+        if (sums == 0) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[c][i] = 0u;
+        }
+#pragma unroll 1
+        for (int s = 0; s < sums; ++s) {
+            r.ok = rg_warp_wait(x.tfull0 + 8u * r.abuf, r.aphase, x.lane, x.abort_flag, p);
+            if (!r.ok) break;
+            tc_fence_after_sync();
+            const uint32_t from = tmem_row + static_cast<uint32_t>(r.abuf * BT);
+            if (mine && s == 0) {
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+                    if (c_first + 64 * c < w.ncols) tmem_ld_x32(from + 64u * c, v[c]);
+#pragma unroll
+                for (int c = 0; c < NC; ++c) tmem_ld_wait(v[c]);
+            } else if (mine) {
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    if (c_first + 64 * c < w.ncols) {
+                        uint32_t u[32];
+                        tmem_ld_x32(from + 64u * c, u);
+                        tmem_ld_wait(u);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            v[c][i] = __float_as_uint(__uint_as_float(v[c][i]) + __uint_as_float(u[i]));
+                    }
+                }
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (x.lane == 0) mbar_arrive_relaxed(mapa_shared(x.tempty0 + 8u * r.abuf, 0u));
+            if (++r.abuf == 2) {
+                r.abuf = 0;
+                r.aphase ^= 1u;
+            }
+        }
+        if (!r.ok) break;
+        if (mine) {
+            const int n = nl0 + x.lane;
+            const float bias =
+                p.bias && n < p.n_lane ? __ldg(p.bias + w.group * p.stride_bias + n) : 0.0f;
+            if (p.beta != 0.0f || p.act != ACT_NONE) {
+                // (one copy of this code, which takes registers of its own: the next chunk
+                // moves to the front)
+#pragma unroll 1
+                for (int c0 = c_first; c0 < w.ncols; c0 += 64) {
+                    rg_out32<FORM, true>(p, w, nl0, c0, bias, x.lane, buf, v[0]);
+#pragma unroll
+                    for (int c = 0; c + 1 < NC; ++c)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[c][i] = v[c + 1][i];
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+                    if (c_first + 64 * c < w.ncols)
+                        rg_out32<FORM, false>(p, w, nl0, c_first + 64 * c, bias, x.lane, buf, v[c]);
+            }
+        }
+        __syncwarp();
     }
     if (FORM == RG_WGRAD && x.lane == 0) bulk_wait_group_all();  // the staged tiles have been read
     __syncwarp();
@@ -1070,37 +1173,51 @@ __device__ __forceinline__ void rg_teardown(const RgCta& x) {
     }
 }
 
-template <int CG, int BT, int FORM>
-__global__ void __launch_bounds__(RgCfg<CG, BT>::threads(FORM), 1)
+// Registers of an fp32 kernel: 128 sums a thread of the epilogue's two warpgroups, for
+// which the first one (producer, MMA issuer, tails) gives some of its own up.  384 threads
+// are launched with at least 160 (rg_prepare checks it): 128 x 80 + 256 x 200 fit.
+constexpr int RG_LAUNCH_REGS = 160, RG_FEW_REGS = 80, RG_SUM_REGS = 200;
+static_assert(128 * RG_FEW_REGS + 256 * RG_SUM_REGS <= 384 * RG_LAUNCH_REGS, "register split");
+
+// SUM: an fp32 output, with its sums cut (see rg_epilogue_sum).
+template <int CG, int BT, int FORM, bool SUM>
+__global__ void __launch_bounds__(RgCfg<CG, BT>::threads(FORM, SUM), 1)
     ragged_kernel(const __grid_constant__ RgParams p) {
     using C = RgCfg<CG, BT>;
     extern __shared__ uint8_t smem_raw[];
     const RgCta x = rg_setup<CG, BT>(p, smem_raw);
     const int warp = threadIdx.x >> 5;
+    constexpr int EPI0 = SUM ? 4 : 2;                           // the epilogue's first warp
+    constexpr int TAILS = SUM ? 2 : 2 + C::EPI_WARPS;           // RG_WGRAD
+    uint8_t* buf = x.smem + C::STAGES * C::STAGE_BYTES +
+                   (warp - EPI0) * (FORM == RG_WGRAD ? C::EPI_WARP / 2 : C::EPI_WARP);
     RgRole r;
+    if (SUM && warp >= EPI0) {
+        if (BT == 256) reg_inc<RG_SUM_REGS>();
+        rg_epilogue_sum<CG, BT, FORM>(p, x, r, x.cl, warp, buf);
+        rg_teardown<CG, BT>(x);
+        return;
+    }
+    if (SUM && BT == 256) reg_dec<RG_FEW_REGS>();
     if (warp == 0) {
         rg_produce<CG, BT, FORM>(p, x, r, x.cl, RgAlone());
         rg_produce_end<CG, BT>(p, x, r);
     } else if (warp == 1) {
-        rg_issue<CG, BT, FORM>(p, x, r, x.cl);
+        rg_issue<CG, BT, FORM, SUM>(p, x, r, x.cl);
         rg_issue_end<CG>(p, x, r);
-    } else if (FORM == RG_WGRAD && warp == 2 + C::EPI_WARPS) {
+    } else if (FORM == RG_WGRAD && warp == TAILS) {
         rg_tails<CG, BT>(p, x, r);
-    } else {
-        rg_epilogue<CG, BT, FORM, FORM == RG_ROWS>(
-            p, x, r, x.cl, warp,
-            x.smem + C::STAGES * C::STAGE_BYTES +
-                (warp - 2) * (FORM == RG_WGRAD ? C::EPI_WARP / 2 : C::EPI_WARP),
-            RgAlone());
+    } else if (!SUM) {
+        rg_epilogue<CG, BT, FORM, FORM == RG_ROWS>(p, x, r, x.cl, warp, buf, RgAlone());
     }
     rg_teardown<CG, BT>(x);
 }
 
-template <int CG, int BT, int FORM>
-cudaError_t rg_launch(const RgParams& p, int grid, cudaStream_t stream) {
+template <int CG, int BT, int FORM, bool SUM>
+cudaError_t rg_launch_as(const RgParams& p, int grid, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(RgCfg<CG, BT>::threads(FORM));
+    cfg.blockDim = dim3(RgCfg<CG, BT>::threads(FORM, SUM));
     cfg.dynamicSmemBytes = RgCfg<CG, BT>::SMEM;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -1119,14 +1236,28 @@ cudaError_t rg_launch(const RgParams& p, int grid, cudaStream_t stream) {
     }
     cfg.attrs = attr;
     cfg.numAttrs = n;
-    return cudaLaunchKernelEx(&cfg, ragged_kernel<CG, BT, FORM>, p);
+    return cudaLaunchKernelEx(&cfg, ragged_kernel<CG, BT, FORM, SUM>, p);
+}
+
+template <int CG, int BT, int FORM>
+cudaError_t rg_launch(const RgParams& p, int grid, cudaStream_t stream) {
+    return p.c_dtype == DT_F32 ? rg_launch_as<CG, BT, FORM, true>(p, grid, stream)
+                               : rg_launch_as<CG, BT, FORM, false>(p, grid, stream);
 }
 
 template <int CG, int BT, int FORM>
 cudaError_t rg_prepare() {
-    return cudaFuncSetAttribute(ragged_kernel<CG, BT, FORM>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(RgCfg<CG, BT>::SMEM));
+    const int smem = static_cast<int>(RgCfg<CG, BT>::SMEM);
+    cudaError_t e = cudaFuncSetAttribute(ragged_kernel<CG, BT, FORM, false>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(ragged_kernel<CG, BT, FORM, true>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // (a wait for registers that the launch does not have would never end)
+    cudaFuncAttributes a;
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, ragged_kernel<CG, BT, FORM, true>);
+    if (e == cudaSuccess && BT == 256 && a.numRegs < RG_LAUNCH_REGS) e = cudaErrorInvalidConfiguration;
+    return e;
 }
 
 }  // namespace

@@ -1248,3 +1248,54 @@ def test_copied_operands_with_and_without_overlap(overlap):
     finally:
         dg.gemm_set_option(dg.Option.OVERLAP_COPY, 0)
     assert status() == 0
+
+
+# ---------------------------------------------------------------- fp32 sums of any length
+
+def segment_bound(A, D, length=768, step=128):
+    """(exact A^T D, bound on the norm of an fp32 result's error).  Each step of 16 may lose
+    one unit in the last place of its accumulator (2^-23 of the partial sum's norm, taken
+    at the nearer end of a block of eight steps); accumulators of `length` products err
+    independently (normal inputs), so their errors add in squares; adding them up rounds
+    to nearest, 2^-24 of the running sum each time."""
+    total, squares = np.zeros((A.shape[1], D.shape[1])), 0.0
+    for s in range(0, A.shape[0], length):
+        P, before, size = np.zeros_like(total), 0.0, 0.0
+        for k in range(s, min(s + length, A.shape[0]), step):
+            e = min(k + step, s + length)
+            P += A[k:e].T @ D[k:e]
+            after = np.linalg.norm(P)
+            size += step / 16 * max(before, after)
+            before = after
+        total += P
+        squares += (2.0 ** -23 * size) ** 2 + (2.0 ** -24 * np.linalg.norm(total)) ** 2
+    return total, np.sqrt(squares)
+
+
+@pytest.mark.parametrize("M,N", [(120, 136), (1600, 1608)])
+@pytest.mark.parametrize("odd", [0, 9])
+def test_wgrad_fp32_sums_do_not_lose_with_their_length(M, N, odd):
+    """16384 rows in one group (and nine more, a ragged tail): single CTAs and pairs."""
+    rng = np.random.default_rng(97)
+    T = 16384 + odd
+    A = torch.from_numpy(rng.standard_normal((T, M)).astype(np.float32)).to(BF)
+    D = torch.from_numpy(rng.standard_normal((T, N)).astype(np.float32)).to(BF)
+    got = ref.f64(dg.grouped_gemm_wgrad(A.to(DEV), D.to(DEV), offs([0, T]), out_dtype=F32))[0]
+    want, bound = segment_bound(ref.f64(A), ref.f64(D))
+    assert np.linalg.norm(got - want) <= bound
+    assert status() == 0
+
+
+@pytest.mark.parametrize("T,N", [(90, 200), (300, 200), (1600, 1608)])
+@pytest.mark.parametrize("K", [16384, 16394])
+def test_grouped_fp32_sums_do_not_lose_with_their_length(T, N, K):
+    """Tiles of 32 columns, of 128, and pairs; K in whole stages and not."""
+    rng = np.random.default_rng(98)
+    A = torch.from_numpy(rng.standard_normal((T, K)).astype(np.float32)).to(BF)
+    B = torch.from_numpy(rng.standard_normal((1, K, N)).astype(np.float32)).to(BF)
+    E = 4 if T == 90 else 1
+    b = bounds_of([T // E] * (E - 1) + [T - T // E * (E - 1)])
+    got = ref.f64(dg.grouped_gemm(A.to(DEV), B.to(DEV).expand(E, K, N), offs(b), out_dtype=F32))
+    want, bound = segment_bound(ref.f64(A).T, ref.f64(B[0]))
+    assert np.linalg.norm(got - want) <= bound
+    assert status() == 0
