@@ -312,11 +312,9 @@ __device__ __forceinline__ void w16_stage(uint32_t w0, uint32_t x0, int rg, int 
     const int l = lane & 7, m = lane >> 3;
     const int row = rg * 16 + (m & 1) * 8 + l;       // K-major: a row's 8 k
     const int col = rg * 2 + (m & 1);                // rows contiguous: 8 rows of one k
-    float acc[NT][4];
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
+    // (two chains of a stage's sums, added to the total to nearest: a matrix instruction
+    // cuts its sum off towards zero, which over a long row would add up)
+    float acc[2][NT][4];
 #pragma unroll
     for (int h = 0; h < 4; ++h) {  // 32 k
         uint32_t a[2][4];
@@ -339,14 +337,19 @@ __device__ __forceinline__ void w16_stage(uint32_t w0, uint32_t x0, int rg, int 
             const int part = (h & 1) * 4 + m;
             ldmatrix_x4(x0 + (h >> 1) * X_BOX + (8 * j + l) * 128 + ((part ^ l) << 4), b[0], b[1],
                         b[2], b[3]);
-            mma16816<DT>(total[j], a[0], b[0], b[1]);
-            mma16816<DT>(acc[j], a[1], b[2], b[3]);
+            if (h == 0) {
+                mma16816_first<DT>(acc[0][j], a[0], b[0], b[1]);
+                mma16816_first<DT>(acc[1][j], a[1], b[2], b[3]);
+            } else {
+                mma16816<DT>(acc[0][j], a[0], b[0], b[1]);
+                mma16816<DT>(acc[1][j], a[1], b[2], b[3]);
+            }
         }
     }
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) total[j][i] += acc[j][i];
+        for (int i = 0; i < 4; ++i) total[j][i] += acc[0][j][i] + acc[1][j][i];
 }
 
 template <int DT, int MT, int GROUP>

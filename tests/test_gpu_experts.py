@@ -1299,3 +1299,18 @@ def test_grouped_fp32_sums_do_not_lose_with_their_length(T, N, K):
     want, bound = segment_bound(ref.f64(A).T, ref.f64(B[0]))
     assert np.linalg.norm(got - want) <= bound
     assert status() == 0
+
+
+@pytest.mark.parametrize("T", [4, 30])
+@pytest.mark.parametrize("layout", ["row", "col"])
+def test_few_rows_fp32_sums_do_not_lose_with_their_length(T, layout):
+    """131072 products, 128 of them in a matrix instruction's accumulator at a time."""
+    rng = np.random.default_rng(99)
+    K, N = 131072, 200
+    A = torch.from_numpy(rng.standard_normal((T, K)).astype(np.float32)).to(BF)
+    B = torch.from_numpy(rng.standard_normal((K, N)).astype(np.float32)).to(BF)
+    Bd = B.to(DEV) if layout == "row" else B.t().contiguous().to(DEV).t()
+    got = ref.f64(dg.grouped_gemm(A.to(DEV), Bd[None], offs([0, T]), out_dtype=F32))
+    want, bound = segment_bound(ref.f64(A).T, ref.f64(B), 128, 16)
+    assert np.linalg.norm(got - want) <= bound
+    assert status() == 0
