@@ -260,7 +260,7 @@ gemm_status_t rg_fill(const RgProblem& q, const DeviceInfo& d, int cg, int bt, R
 // 9.8 : 13.5; but 192 rows over 64 experts of N = 2048 90.3 : 83.6.
 constexpr int64_t kFewRows = 64;
 
-static bool few_rows(const RgProblem& q, const DeviceInfo& d) {
+static bool few_rows(const RgProblem& q) {
     return q.form == RG_ROWS && q.offsets && q.K > 0 && q.T <= kFewRows;
 }
 
@@ -322,7 +322,7 @@ static gemm_status_t few_run(const RgProblem& q, const DeviceInfo& d, cudaStream
 }
 
 gemm_status_t rg_run(const RgProblem& q, const DeviceInfo& d, cudaStream_t stream) {
-    if (few_rows(q, d)) return few_run(q, d, stream);
+    if (few_rows(q)) return few_run(q, d, stream);
     int cg, bt;
     rg_variant(q, d, &cg, &bt);
     RgParams p;
@@ -715,11 +715,15 @@ gemm_status_t gemm_newton_schulz(gemm_dtype_t g_dtype, int64_t batch, int64_t M,
 
 namespace {
 
-// Rows (of a group, on average) up to which the 4-bit integers are multiplied directly.
-// Against 16-bit weights in the workspace, K x N = 4096 x 4096 (us): 64 rows 19.7 (29
-// from 65 rows on), 96 rows 32 : 29; 32 experts of 2048 x 4096: 16 rows each on average
-// 133 : 215, 25 rows 207 : 221, 37 rows 223 : 214 unevenly and 192 : 215 evenly spread,
-// 50 rows 261 : 221 and 203 : 215; 8 experts: 37 rows 62.1 : 62.6, 50 rows 85 : 63.
+// Rows (of a group, on average) up to which the 4-bit integers are multiplied directly;
+// more rows multiply 16-bit weights in the workspace, rounded once more (bf16 output: 2.2e-3
+// of the result against 1.7e-3).  Direct : 16-bit (us), K x N = 4096 x 4096, one matrix:
+// 64 rows 19.7 : 29, 96 rows 32 : 29.  Experts of 2048 x 4096, where the host knows the
+// average alone: 32 of them with 16 rows each 133 : 215, 25 rows 207 : 221, 37 rows
+// 223 : 214 unevenly and 192 : 215 evenly spread, 50 rows 261 : 221 and 203 : 215;
+// 8 of them with 37 rows 62.1 : 62.6, 50 rows 85 : 63.  So past 40 rows, evenly spread
+// rows over many experts lose up to a tenth of their time, and uneven ones or few experts
+// win more.
 constexpr int64_t kW4DirectRows = 64, kW4DirectGroupRows = 40;
 
 bool w4_direct(int64_t groups, int64_t T, int c_dtype) {
@@ -830,7 +834,6 @@ gemm_status_t gemm_w4(gemm_dtype_t ab_dtype, int64_t groups, int64_t T, int64_t 
                : encode_map16(&p.tmap_x, ab_dtype, a.ptr, K, T, 1, a.ld * 2, 0, 64,
                               static_cast<uint32_t>(tokens))))
         return GEMM_ERR_CUDA;
-    p.q = Q;
     p.scales = scales;
     p.zeros = zeros;
     p.offsets = offsets;

@@ -162,7 +162,6 @@ struct W4Params {
     CUtensorMap tmap_q;      // [groups][N][K / 2] bytes, boxes of 128 bytes x rows (x blocks);
                              // 16-bit weights: 64 x rows x 2 blocks, or 64 columns x 128 k
     CUtensorMap tmap_x;      // [T][K], boxes of 64 x the tokens of a tile (x blocks)
-    const uint8_t* q;
     const void* scales;
     const uint8_t* zeros;
     const int32_t* offsets;  // or null

@@ -23,11 +23,11 @@
 // fp32 and scaled by s once per group, so nothing is rounded but the output.  The sum
 // over k may be taken in any order, so lane t of a quad takes the 8 weights of 32-bit
 // word t of a 16-byte chunk (32 weights) and 8 values of its token; the swizzle makes the
-// word reads of 8 rows x 4 words conflict-free.  What bounds it: 34 instructions for 16
-// rows x 32 weights, more with short groups (with groups of 32 the schedulers issue in
-// 53 % of the cycles, the integer pipe is 47 % busy, and warps wait in equal parts for
-// that pipe, fixed latencies and the unit's barriers), and where there is less than one
-// unit a CTA, start-up.  Measured: one token, 8192 x 8192, groups of 128, 13.6 us
+// word reads of 8 rows x 4 words conflict-free.  What bounds it: instructions and their
+// latencies, 34 for 16 rows x 32 weights and 78 with groups of 32, where the schedulers
+// issue in 53 % of the cycles, no pipe is busy for more than 47 %, and warps wait in
+// about equal parts for fixed latencies, the integer pipe, loads and the unit's barriers;
+// and where there is less than one unit a CTA, start-up.  Measured: one token, 8192 x 8192, groups of 128, 13.6 us
 // (2.5 TB/s); 32 rows over 32 experts of 2048 x 4096, groups of 32 and zero points,
 // 48.1 us (2.3 TB/s).
 //
@@ -49,6 +49,8 @@ template <int MT, int GROUP>
 struct W4Cfg {
     static constexpr int WARPS = MT <= 16 ? 16 : 8;  // consumer warps
     static constexpr int THREADS = 32 * (WARPS + 1); // and the producer, warp 0
+    // (registers come to four warps at once: 9 warps have 168 each, 17 have 96; 64 tokens
+    // spill 28 to 64 bytes a thread there, 16 and 32 with groups of 64 spill 4)
     static constexpr int RT = MT <= 16 ? 64 : 128;   // weight rows (outputs) of a unit
     static constexpr int RG = RT / 16;               // row groups of a stage
     static constexpr int SG = WARPS / RG;            // stages in work at once

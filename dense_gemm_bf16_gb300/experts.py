@@ -266,7 +266,13 @@ def w4_gemm(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, *, zeros=Non
     x: [T, K] row-major; q: uint8 [N, K // 2], the low half of byte j holding
     k = 2 j; scales: [N, K // group] in x's dtype; zeros: uint8 of that shape.
     With ``offsets`` (int32 [experts + 1]) q, scales and zeros carry a leading
-    expert dimension and rows offsets[e] .. offsets[e + 1] - 1 use expert e.
+    expert dimension and rows offsets[e] .. offsets[e + 1] - 1 use expert e
+    (rows of no expert are not written).
+
+    An fp32 result (``out_dtype``, ``out``) and 16-bit results of up to 64 rows, or of
+    40 rows an expert on average, round nothing before the output; more rows multiply
+    weights that were rounded to x's dtype, so a row's last bits may depend on how many
+    rows the call has.
     """
     dt = _code16(x, scales, "x and scales")
     lead = 3 if offsets is not None else 2

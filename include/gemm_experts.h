@@ -46,7 +46,9 @@ extern "C" {
  *                a multiple of 16 bytes), which is copied first.
  *                gemm_grouped_workspace_size() always suffices.
  *
- * Products accumulate in fp32 and are rounded once.  Calls repeat bit for bit.
+ * Products accumulate in fp32 (an fp32 C: 768 of them in the tensor core's
+ * accumulator, which cuts off towards zero, then added to nearest) and are rounded
+ * once.  Calls repeat bit for bit.
  * T, groups, N and the operands' layout choose the kernel and its tiles, and with
  * them the order of a row's sum; where they are equal, a group's results do not
  * depend on the other groups' rows, weights or sizes, bit for bit.  (One more row,
@@ -148,7 +150,8 @@ size_t gemm_newton_schulz_workspace_size(int64_t batch, int64_t M, int64_t N);
  * Few rows (a 16-bit C with T <= 64, or T <= 40 * groups for several groups, or
  * any fp32 C) multiply the 4-bit integers themselves and scale fp32 sums once
  * per group, so nothing is rounded before the output.  More rows with a 16-bit
- * C multiply weights that were rounded to ab_dtype in the workspace.
+ * C multiply weights that were rounded to ab_dtype in the workspace.  A row's
+ * last bits may so depend on how many rows the call has.
  */
 gemm_status_t gemm_w4(gemm_dtype_t ab_dtype, int64_t groups, int64_t T, int64_t N, int64_t K,
                       const void* A, int64_t lda, const uint8_t* Q, const void* scales,
