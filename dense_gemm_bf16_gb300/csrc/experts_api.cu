@@ -238,6 +238,9 @@ gemm_status_t rg_fill(const RgProblem& q, const DeviceInfo& d, int cg, int bt, R
     p.alpha = q.alpha;
     p.beta = q.beta;
     p.diag = q.diag;
+    p.resid = q.resid;
+    p.stride_resid = q.stride_resid;
+    p.resid_in = q.resid_in;
     p.bias = q.bias;
     p.stride_bias = q.stride_bias;
     p.act = q.act;
@@ -621,6 +624,11 @@ gemm_status_t gemm_newton_schulz(gemm_dtype_t g_dtype, int64_t batch, int64_t M,
     // reads its own kind of matrix back: with Y = S + b / (2 c),
     //   P = a + b S + c S S = c Y Y + (a - b b / (4 c)).
     // Where b / (2 c) would cost Y its bits (or c is zero), Y is S and P adds b S.
+    // The shift would cost Y's diagonal bits of S too (fp16 steps of 2^-11 near 1.2): what
+    // an entry Y_ii loses, r_i, comes back as the 2 c r_i Y_ii that P_ii lacks for it.  The
+    // products lie in the buffer of the next X, which is not in use between the two.  (The
+    // result's error before its own rounding: 128 x 2048 1.6e-3 -> 8.5e-4, 64 x 64 1.9e-3
+    // -> 1.5e-3; rounding the products c (r_i + r_j) Y_ij beside the diagonal is left.)
     const bool squared = std::fabs(b) <= 4.0f * std::fabs(c) && c != 0.0f;
     const float shift = squared ? b / (2.0f * c) : 0.0f;
     const bool wide = M <= N;
@@ -662,10 +670,15 @@ gemm_status_t gemm_newton_schulz(gemm_dtype_t g_dtype, int64_t batch, int64_t M,
         q.c_dtype = q.cin_dtype = DT_F16;
         q.alpha = kNsS / (kNsX * kNsX);
         q.diag = shift * kNsS;
+        if (squared) {
+            q.resid = reinterpret_cast<float*>(x[1 - odd]);
+            q.stride_resid = xs / 2;
+        }
         st = add(q, &seq->ph[3 * odd]);
         // P = c Y Y + beta Y + constant, times kNsS
         q.K = l.side;
         q.a = q.b = RgOperand{S, l.lds, ss, false, l.side, l.side};
+        q.resid_in = 1;
         q.C = P;
         q.Cin = S;
         q.alpha = c / kNsS;

@@ -57,6 +57,12 @@ struct RgParams {
     int32_t c_vec;           // C (and Cin) rows start on 16-byte boundaries
     float alpha, beta;
     float diag;              // RG_SYM: added on the diagonal
+    // RG_SYM, where set: n_col floats a group, stride_resid apart.  resid_in 0: what the
+    // diagonal lost by its rounding, times twice the rounded value, goes there; 1: alpha
+    // times that is added on the diagonal.
+    float* resid;
+    int64_t stride_resid;
+    int32_t resid_in;
     const float* bias;       // [groups][n_lane] with stride_bias, or null
     int64_t stride_bias;
     int32_t act;
@@ -145,6 +151,9 @@ struct RgProblem {
     int c_dtype, cin_dtype;  // cin_dtype: read where beta != 0, of c_dtype's size
     float alpha, beta;
     float diag;              // RG_SYM: added on the diagonal
+    float* resid;            // RG_SYM: see RgParams
+    int64_t stride_resid;
+    int resid_in;
     const float* bias;
     int64_t stride_bias;
     int act;

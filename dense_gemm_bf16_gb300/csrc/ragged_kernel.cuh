@@ -489,6 +489,15 @@ __device__ __forceinline__ void rg_out16(const RgParams& p, const RgTile& w, uin
     }
     // (RG_SYM: Cin comes from the product before, which is known to be complete only here)
     if (FORM == RG_SYM && !ready()) return;
+    // RG_SYM: the chunk of this warp on the diagonal, if any, and what its rounding lost
+    const int c_diag = FORM == RG_SYM && w.diag ? nl0 - w.col0 : -1;
+    float* resid = FORM == RG_SYM && p.resid ? p.resid + w.group * p.stride_resid + nl0 + pcol : nullptr;
+    float lost[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (FORM == RG_SYM && p.resid_in && resid && w.diag) {
+#pragma unroll
+        for (int hg = 0; hg < 4; ++hg)
+            if (nl0 + 8 * hg + pcol < p.n_lane) lost[hg] = __ldcg(resid + 8 * hg);
+    }
     if (beta) load_in(first);
     if (FORM != RG_SYM && !ready()) return;
 #pragma unroll 1
@@ -523,12 +532,20 @@ __device__ __forceinline__ void rg_out16(const RgParams& p, const RgTile& w, uin
             }
             if (FORM != RG_ROWS) __syncwarp();  // (Cin's place is written again)
         }
-        if (FORM == RG_SYM && w.diag && w.col0 + c0 == nl0) {
+        if (FORM == RG_SYM && c0 == c_diag && pcol >> 1 == part) {
             // a 32 x 32 block on the diagonal: lane 16 h + 8 g + pcol, column 8 b + 2 part + k
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (((i >> 2) & 3) == 2 * (i >> 4) + ((i >> 1) & 1) && 2 * part + (i & 1) == pcol)
-                    v[i] += p.diag;
+            for (int hg = 0; hg < 4; ++hg) {
+                const int i = 16 * (hg >> 1) + 4 * hg + 2 * (hg & 1);
+                float y = (pcol & 1 ? v[i + 1] : v[i]) + p.diag;
+                if (p.resid_in) y = fmaf(p.alpha, lost[hg], y);
+                v[i] = pcol & 1 ? v[i] : y;
+                v[i + 1] = pcol & 1 ? y : v[i + 1];
+                if (resid && !p.resid_in && nl0 + 8 * hg + pcol < p.n_lane) {
+                    const float h = __half2float(__float2half_rn(y));
+                    resid[8 * hg] = 2.0f * h * (y - h);
+                }
+            }
         }
         if (ACT) rg_act(v, p.act);
         rg_pack16(p.c_dtype, v, pk);

@@ -114,7 +114,8 @@ size_t gemm_grouped_wgrad_workspace_size(gemm_dtype_t ab_dtype, int64_t groups, 
  *
  * The norm and every product accumulate in fp32.  Between products X and the
  * symmetric matrices S + b / (2 c) and a + b S + c S S are held in fp16 times a
- * power of two (eight times finer than bf16); coefficients must keep singular
+ * power of two (eight times finer than bf16), with what the first one's diagonal
+ * loses carried on in fp32; coefficients must keep singular
  * values below 4 and both matrices below 8 in norm, which the values above do.
  * Both symmetric products compute the tiles on and below the diagonal only.
  */

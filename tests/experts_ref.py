@@ -80,7 +80,8 @@ def newton_schulz(G, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7):
 def newton_schulz_fp16(G, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7):
     """The same with what the kernels hold between products rounded to fp16: X times
     2^13, Y = S + b / (2 c) and P = c Y Y + a - b b / (4 c) times 2^12, the result as it
-    is; all products in 64 bits, S on the smaller side."""
+    is; all products in 64 bits, S on the smaller side.  What Y's diagonal loses, r_i, comes
+    back in P's as 2 c r_i Y_ii."""
     a, b, c = coefficients
 
     def fp16(x, scale=1.0):
@@ -91,8 +92,10 @@ def newton_schulz_fp16(G, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1
         wide = X.shape[0] <= X.shape[1]
         eye = np.eye(min(X.shape))
         for step in range(steps):
-            Y = fp16((X @ X.T if wide else X.T @ X) + b / (2 * c) * eye, 2.0 ** 12)
-            P = fp16(c * (Y @ Y) + (a - b * b / (4 * c)) * eye, 2.0 ** 12)
+            exact = (X @ X.T if wide else X.T @ X) + b / (2 * c) * eye
+            Y = fp16(exact, 2.0 ** 12)
+            lost = np.diag(2 * c * np.diag(exact - Y) * np.diag(Y))
+            P = fp16(c * (Y @ Y) + (a - b * b / (4 * c)) * eye + lost, 2.0 ** 12)
             X = P @ X if wide else X @ P
             X = fp16(X, 1.0 if step == steps - 1 else 2.0 ** 13)
         return X

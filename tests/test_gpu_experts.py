@@ -1092,7 +1092,7 @@ def test_grouped_fp32_sums(counts, K, N):
 # ---------------------------------------------------------------- Newton-Schulz, block by block
 
 @pytest.mark.parametrize("shape", [(64, 64), (129, 257), (300, 200), (96, 1000), (3, 200, 264),
-                                   (6, 257, 130),                               # 64-column tiles
+                                   (128, 2048), (6, 257, 130),                            # 64-column tiles
                                    (15, 257, 300), (15, 300, 257), (40, 100, 300),  # 128 columns
                                    (10, 520, 600), (20, 512, 640), (10, 600, 520),  # pairs
                                    (2100, 2304), (2310, 2100)])
