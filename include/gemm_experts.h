@@ -46,7 +46,7 @@ extern "C" {
  *                a multiple of 16 bytes), which is copied first.
  *                gemm_grouped_workspace_size() always suffices.
  *
- * Products accumulate in fp32 (an fp32 C: 768 of them in the tensor core's
+ * Products accumulate in fp32 (an fp32 C: at most 768 in the tensor core's
  * accumulator, which cuts off towards zero, then added to nearest) and are rounded
  * once.  Calls repeat bit for bit.
  * T, groups, N and the operands' layout choose the kernel and its tiles, and with
