@@ -73,6 +73,7 @@ class Option(enum.IntEnum):
     TEST_DEBUG_BOUND = 16
     OVERLAP_COPY = 17
     EPILOGUE_WARPS = 18
+    W4_EXACT = 19
 
 
 class Plan(ctypes.Structure):

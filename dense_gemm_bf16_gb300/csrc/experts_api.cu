@@ -740,14 +740,14 @@ namespace {
 constexpr int64_t kW4DirectRows = 64, kW4DirectGroupRows = 40;
 
 bool w4_direct(int64_t groups, int64_t T, int c_dtype) {
-    return c_dtype == DT_F32 || T <= (groups > 1 ? kW4DirectGroupRows * groups : kW4DirectRows);
+    return c_dtype == DT_F32 || option_w4_exact() || T <= (groups > 1 ? kW4DirectGroupRows * groups : kW4DirectRows);
 }
 
-size_t w4_need(int64_t groups, int64_t T, int64_t N, int64_t K, const void* A, int64_t lda,
-               int c_dtype) {
+size_t w4_need(bool direct, int64_t groups, int64_t T, int64_t N, int64_t K, const void* A,
+               int64_t lda) {
     size_t need = 0;
     if (!in_place(A, lda, 1, 0)) need += copy_bytes(T, K, 1);
-    if (!w4_direct(groups, T, c_dtype)) need += copy_bytes(N, K, groups);
+    if (!direct) need += copy_bytes(N, K, groups);
     return need;
 }
 
@@ -759,7 +759,7 @@ size_t gemm_w4_workspace_size(gemm_dtype_t ab_dtype, int64_t groups, int64_t T, 
         !size_ok(K) || groups == 0 || T == 0 || N == 0 || K == 0 || !count_ok(groups, N, K) ||
         !count_ok(1, T, K + 8))
         return 0;
-    return w4_need(groups, T, N, K, A, lda, c_dtype);
+    return w4_need(w4_direct(groups, T, c_dtype), groups, T, N, K, A, lda);
 }
 
 gemm_status_t gemm_w4(gemm_dtype_t ab_dtype, int64_t groups, int64_t T, int64_t N, int64_t K,
@@ -791,8 +791,10 @@ gemm_status_t gemm_w4(gemm_dtype_t ab_dtype, int64_t groups, int64_t T, int64_t 
     if (!A || !aligned(A, 2) || lda < K || !Q || !aligned(Q, 16) || !scales || !aligned(scales, 2))
         return GEMM_ERR_INVALID_ARG;
     if (!strided_span_ok(T, K, lda, 1, 1, 0) || !count_ok(groups, N, K)) return GEMM_ERR_INVALID_ARG;
-    if (!row_tiles_ok(groups, T, N, w4_direct(groups, T, c_dtype))) return GEMM_ERR_UNSUPPORTED;
-    const size_t need = w4_need(groups, T, N, K, A, lda, c_dtype);
+    // (once: the option may change meanwhile)
+    const bool direct = w4_direct(groups, T, c_dtype);
+    if (!row_tiles_ok(groups, T, N, direct)) return GEMM_ERR_UNSUPPORTED;
+    const size_t need = w4_need(direct, groups, T, N, K, A, lda);
     if (need > 0 && (!workspace || workspace_bytes < need)) return GEMM_ERR_WORKSPACE;
     if (need > 0 && !aligned(workspace, 256)) return GEMM_ERR_INVALID_ARG;
     DeviceInfo d;
@@ -804,7 +806,7 @@ gemm_status_t gemm_w4(gemm_dtype_t ab_dtype, int64_t groups, int64_t T, int64_t 
     Stored a{A, lda, 0};
     st = place(&a, T, K, 1, ws, workspace_bytes, &off, true, s);
     if (st != GEMM_OK) return st;
-    if (!w4_direct(groups, T, c_dtype)) {
+    if (!direct) {
         if (w4_dequantise(ab_dtype, Q, scales, zeros, groups * N, K, group, ws + off, s) !=
             cudaSuccess)
             return GEMM_ERR_CUDA;

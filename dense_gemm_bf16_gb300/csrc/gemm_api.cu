@@ -32,6 +32,7 @@ std::atomic<int64_t> g_opt_swap_ab{0};
 std::atomic<int64_t> g_opt_l2_hints{0};
 std::atomic<int64_t> g_opt_overlap_copy{0};
 std::atomic<int64_t> g_opt_epilogue_warps{0};
+std::atomic<int64_t> g_opt_w4_exact{0};
 std::atomic<int64_t> g_opt_stream_k{0};
 std::atomic<int64_t> g_opt_fast_epilogue{0};
 std::atomic<int64_t> g_opt_sgemm_kernel{0};
@@ -1078,6 +1079,8 @@ gemm_status_t device_info(DeviceInfo* out) {
 
 uint64_t option_timeout_ns() { return static_cast<uint64_t>(g_opt_timeout_us.load()) * 1000ull; }
 
+bool option_w4_exact() { return g_opt_w4_exact.load() != 0; }
+
 bool option_overlap_copy() { return g_opt_overlap_copy.load() == 0; }
 
 int take_test_stall() { return static_cast<int>(g_opt_test_stall.exchange(0)); }
@@ -1443,6 +1446,10 @@ gemm_status_t gemm_set_option(gemm_option_t option, int64_t value) {
             if (value != 0 && value != 4) return GEMM_ERR_INVALID_ARG;
             g_opt_epilogue_warps.store(value);
             return GEMM_OK;
+        case GEMM_OPT_W4_EXACT:
+            if (value < 0 || value > 1) return GEMM_ERR_INVALID_ARG;
+            g_opt_w4_exact.store(value);
+            return GEMM_OK;
     }
     return GEMM_ERR_INVALID_ARG;
 }
@@ -1467,6 +1474,7 @@ int64_t gemm_get_option(gemm_option_t option) {
         case GEMM_OPT_TEST_DEBUG_BOUND: return g_opt_test_debug_bound.load();
         case GEMM_OPT_OVERLAP_COPY: return g_opt_overlap_copy.load();
         case GEMM_OPT_EPILOGUE_WARPS: return g_opt_epilogue_warps.load();
+        case GEMM_OPT_W4_EXACT: return g_opt_w4_exact.load();
     }
     return -1;
 }

@@ -105,6 +105,7 @@ struct DeviceInfo {
 };
 gemm_status_t device_info(DeviceInfo* out);   // the current device
 uint64_t option_timeout_ns();
+bool option_w4_exact();       // no 16-bit weights
 bool option_overlap_copy();   // a product may start while its operand is prepared
 int take_test_stall();
 

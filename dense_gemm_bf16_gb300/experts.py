@@ -271,8 +271,8 @@ def w4_gemm(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, *, zeros=Non
 
     An fp32 result (``out_dtype``, ``out``) and 16-bit results of up to 64 rows, or of
     40 rows an expert on average, round nothing before the output; more rows multiply
-    weights that were rounded to x's dtype, so a row's last bits may depend on how many
-    rows the call has.
+    weights that were rounded to x's dtype (unless ``Option.W4_EXACT`` is set), so a
+    row's last bits may depend on how many rows the call has.
     """
     dt = _code16(x, scales, "x and scales")
     lead = 3 if offsets is not None else 2

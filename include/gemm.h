@@ -440,6 +440,12 @@ gemm_status_t gemm_strided_plan_query(gemm_dtype_t ab_dtype, int64_t batch,
  *                         column-major C; plan fast_epilogue 3) or when beta * C
  *                         is read by TMA loads and K is at most 32 blocks of 64
  *                         (plan fast_epilogue 4); 4: four warps always.
+ *   GEMM_OPT_W4_EXACT     gemm_w4 (gemm_experts.h) with a 16-bit C: 0 (default): many
+ *                         rows multiply weights rounded to 16 bits; 1: every call
+ *                         multiplies the 4-bit integers themselves, so that nothing
+ *                         is rounded before the output, in one pass over the weights
+ *                         for every 64 rows (4096 x 4096, 1500 rows: 297 us against
+ *                         50).
  *   GEMM_OPT_TEST_SIM_SMS test only: n > 0 makes gemm_plan_query and
  *                         gemm_workspace_size plan for a simulated sm_103 device of n
  *                         SMs whose CTA pairs of every tile width fit n / 2 at once,
@@ -479,7 +485,8 @@ typedef enum {
     GEMM_OPT_TEST_SIM_SMS = 15,
     GEMM_OPT_TEST_DEBUG_BOUND = 16,
     GEMM_OPT_OVERLAP_COPY = 17,
-    GEMM_OPT_EPILOGUE_WARPS = 18
+    GEMM_OPT_EPILOGUE_WARPS = 18,
+    GEMM_OPT_W4_EXACT = 19
 } gemm_option_t;
 
 gemm_status_t gemm_set_option(gemm_option_t option, int64_t value);

@@ -151,8 +151,9 @@ size_t gemm_newton_schulz_workspace_size(int64_t batch, int64_t M, int64_t N);
  * Few rows (a 16-bit C with T <= 64, or T <= 40 * groups for several groups, or
  * any fp32 C) multiply the 4-bit integers themselves and scale fp32 sums once
  * per group, so nothing is rounded before the output.  More rows with a 16-bit
- * C multiply weights that were rounded to ab_dtype in the workspace.  A row's
- * last bits may so depend on how many rows the call has.
+ * C multiply weights that were rounded to ab_dtype in the workspace, unless
+ * GEMM_OPT_W4_EXACT is set.  A row's last bits may so depend on how many rows the
+ * call has.
  */
 gemm_status_t gemm_w4(gemm_dtype_t ab_dtype, int64_t groups, int64_t T, int64_t N, int64_t K,
                       const void* A, int64_t lda, const uint8_t* Q, const void* scales,

@@ -168,6 +168,20 @@ def test_workspace_sizes():
     assert dg.gemm_w4_workspace_size(0, 1, 2, 16, 64, 64, 65, 0) == 256
 
 
+def test_exact_4_bit_products_need_no_weights_in_the_workspace():
+    opt = dg.Option.W4_EXACT
+    assert dg.gemm_get_option(opt) == 0
+    assert dg.gemm_set_option(opt, 2) == BAD and dg.gemm_set_option(opt, -1) == BAD
+    assert dg.gemm_set_option(opt, 1) == 0 and dg.gemm_get_option(opt) == 1
+    try:
+        assert dg.gemm_w4_workspace_size(0, 1, 300, 16, 64, 64, 64, 0) == 0
+        assert dg.gemm_w4_workspace_size(0, 3, 300, 16, 64, 64, 65, 0) == \
+            dg.gemm_w4_workspace_size(0, 3, 300, 16, 64, 64, 65, 2) > 0
+    finally:
+        assert dg.gemm_set_option(opt, 0) == 0
+    assert dg.gemm_w4_workspace_size(0, 1, 300, 16, 64, 64, 64, 0) == 2048
+
+
 def test_tensor_level_refusals():
     A, B = torch.zeros((4, 8), dtype=torch.bfloat16), torch.zeros((2, 8, 16), dtype=torch.bfloat16)
     o = torch.tensor([0, 1, 4], dtype=torch.int32)

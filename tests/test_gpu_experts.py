@@ -1314,3 +1314,28 @@ def test_few_rows_fp32_sums_do_not_lose_with_their_length(T, layout):
     want, bound = segment_bound(ref.f64(A).T, ref.f64(B), 128, 16)
     assert np.linalg.norm(got - want) <= bound
     assert status() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("counts", [None, [200, 0, 160, 3]])
+def test_w4_exact_option_rounds_once(counts, dtype):
+    """Many rows with a 16-bit output, as the caller asks: the fp32 result (of the integers
+    themselves), rounded once.  By default the weights' own rounding is in it too."""
+    rng = np.random.default_rng(100)
+    E, N, K = (len(counts) if counts else 0), 264, 512
+    b = bounds_of(counts) if counts else None
+    T = b[-1] if counts else 300
+    x, q, s, z = w4_case(rng, T, N, K, 64, True, dtype, E)
+    x = torch.from_numpy(rng.standard_normal((T, K)).astype(np.float32)).to(dtype)
+    s = torch.from_numpy(rng.uniform(0.01, 0.02, s.shape).astype(np.float32)).to(dtype)
+    kw = dict(offsets=offs(b)) if counts else {}
+    once = w4_run(x, q, s, z, out_dtype=F32, **kw).to(dtype)
+    default = w4_run(x, q, s, z, **kw)
+    dg.gemm_set_option(dg.Option.W4_EXACT, 1)
+    try:
+        got = w4_run(x, q, s, z, **kw)
+    finally:
+        dg.gemm_set_option(dg.Option.W4_EXACT, 0)
+    assert torch.equal(got, once)
+    assert not torch.equal(default, once)
+    assert status() == 0
