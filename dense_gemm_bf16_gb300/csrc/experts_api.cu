@@ -70,9 +70,11 @@ gemm_status_t epilogue_of(int epi, const float* bias, int64_t stride_bias, int64
     return GEMM_OK;
 }
 
-// Can TMA address this 16-bit matrix (`depth` of them, `stride` apart)?
+// Can TMA address this 16-bit matrix (`depth` of them, `stride` apart)?  Matrices side by
+// side, whose stride is less than a row's, are copied: a map's strides ascend.
 bool in_place(const void* ptr, int64_t ld, int64_t depth, int64_t stride) {
-    return aligned(ptr, 16) && ld % 8 == 0 && (depth <= 1 || stride == 0 || stride % 8 == 0);
+    return aligned(ptr, 16) && ld % 8 == 0 &&
+           (depth <= 1 || stride == 0 || (stride % 8 == 0 && stride >= ld));
 }
 
 // Workspace bytes of the dense copy of an outer x inner matrix, `depth` times.
@@ -101,6 +103,13 @@ gemm_status_t place(Stored* m, int64_t outer, int64_t inner, int64_t depth, char
     m->stride = n > 1 ? outer * ld : 0;
     *off += need;
     return GEMM_OK;
+}
+
+// Do the matrices of a batch stay clear of each other: one after another, or side by side
+// (the rows of one between those of the others, as column blocks of one wide matrix)?
+bool apart(int64_t outer, int64_t inner, int64_t ld, int64_t depth, int64_t stride) {
+    return depth <= 1 || stride >= (outer - 1) * ld + inner ||
+           (stride >= inner && (ld - inner) / stride >= depth - 1);
 }
 
 bool c_ok(const void* C, int64_t rows, int64_t cols, int64_t ld, int64_t depth, int64_t stride,
@@ -232,7 +241,7 @@ gemm_status_t rg_fill(const RgProblem& q, const DeviceInfo& d, int cg, int bt, R
     p.c_vec = aligned(q.C, 16) && q.ldc * es % 16 == 0 && q.stride_c * es % 16 == 0 &&
               (q.beta == 0.0f || (aligned(q.Cin, 16) && q.ldcin * es % 16 == 0 &&
                                   q.stride_cin * es % 16 == 0));
-    p.c_tma = q.form == RG_WGRAD && p.c_vec &&
+    p.c_tma = q.form == RG_WGRAD && p.c_vec && (q.groups <= 1 || q.stride_c >= q.ldc) &&
               encode_map_out(&p.tmap_c, q.c_dtype, q.C, q.n_lane, q.n_col, q.groups, q.ldc * es,
                              q.stride_c * es);
     p.alpha = q.alpha;
@@ -357,11 +366,10 @@ gemm_status_t check_grouped(int ab, int64_t groups, int64_t T, int64_t N, int64_
     if (!A || !B || !aligned(A, 2) || !aligned(B, 2)) return GEMM_ERR_INVALID_ARG;
     const int64_t inner = lb == GEMM_ROW_MAJOR ? N : K, outer = lb == GEMM_ROW_MAJOR ? K : N;
     if (lda < K || ldb < inner || stride_b < 0) return GEMM_ERR_INVALID_ARG;
-    if (groups > 1 && stride_b != 0 && stride_b < (outer - 1) * ldb + inner)
-        return GEMM_ERR_INVALID_ARG;
     if (!strided_span_ok(T, K, lda, 1, 1, 0) || !count_ok(1, T, K) ||
         !strided_span_ok(outer, inner, ldb, 1, groups, stride_b) || !count_ok(groups, K, N))
         return GEMM_ERR_INVALID_ARG;
+    if (stride_b != 0 && !apart(outer, inner, ldb, groups, stride_b)) return GEMM_ERR_INVALID_ARG;
     return GEMM_OK;
 }
 
@@ -478,7 +486,7 @@ gemm_status_t gemm_grouped_wgrad(gemm_dtype_t ab_dtype, int64_t groups, int64_t 
     if (c_dtype != ab_dtype && c_dtype != GEMM_DT_F32) return GEMM_ERR_UNSUPPORTED;
     if (groups == 0 || M == 0 || N == 0) return GEMM_OK;
     if (!c_ok(C, M, N, ldc, groups, groups > 1 ? stride_c : 0, c_dtype)) return GEMM_ERR_INVALID_ARG;
-    if (groups > 1 && stride_c < (M - 1) * ldc + N) return GEMM_ERR_INVALID_ARG;
+    if (!apart(M, N, ldc, groups, stride_c)) return GEMM_ERR_INVALID_ARG;
     if (Tc > 0 && (!offsets || !aligned(offsets, 4))) return GEMM_ERR_INVALID_ARG;
     if (!wgrad_tiles_ok(groups, M, N)) return GEMM_ERR_UNSUPPORTED;
     DeviceInfo d;
@@ -589,7 +597,7 @@ gemm_status_t gemm_newton_schulz(gemm_dtype_t g_dtype, int64_t batch, int64_t M,
         return GEMM_ERR_INVALID_ARG;
     if (!strided_span_ok(M, N, ldg, 1, batch, batch > 1 ? stride_g : 0)) return GEMM_ERR_INVALID_ARG;
     if (!c_ok(O, M, N, ldo, batch, batch > 1 ? stride_o : 0, o_dtype)) return GEMM_ERR_INVALID_ARG;
-    if (batch > 1 && stride_o < (M - 1) * ldo + N) return GEMM_ERR_INVALID_ARG;
+    if (!apart(M, N, ldo, batch, stride_o)) return GEMM_ERR_INVALID_ARG;
     NsLayout l;
     if (!ns_layout(batch, M, N, &l)) return GEMM_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < l.total) return GEMM_ERR_WORKSPACE;

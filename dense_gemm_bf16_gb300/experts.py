@@ -178,7 +178,7 @@ def grouped_gemm(A: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor,
     off = _offsets(offsets, groups)
     pa, pb = A.data_ptr(), B.data_ptr()
     need = 0
-    if workspace is None and (pa | pb | (lda | ldb | sb) * 2) & 15:
+    if workspace is None and ((pa | pb | (lda | ldb | sb) * 2) & 15 or 0 < sb < ldb):
         need = _abi.gemm_grouped_workspace_size(dt, groups, T, N, K, pa, lda, pb, ldb, lb, sb)
     workspace, ws, ws_bytes = _scratch(workspace, need, A, stream)
     st = _fn("gemm_grouped")(dt, groups, T, N, K, pa, lda, pb, ldb, lb, sb, C.data_ptr(), ldc,

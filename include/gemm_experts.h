@@ -35,7 +35,9 @@ extern "C" {
  *   groups, T    number of groups; rows of A and C.
  *   A, lda       T x K, row-major.
  *   B, ldb, lb, stride_b   one K x N matrix per group, stride_b elements apart
- *                (0: the same matrix for all), row- or column-major.  The
+ *                (0: the same matrix for all), row- or column-major: one after
+ *                another, or side by side (column blocks of one wide matrix:
+ *                ldb >= (groups - 1) * stride_b + a row), which are copied.  The
  *                gradient of A is the same call with the other layout of B.
  *   C, ldc       T x N, row-major, c_dtype ab_dtype or GEMM_DT_F32.
  *   bias, stride_bias  fp32, N values per group, stride_bias elements apart
@@ -43,7 +45,8 @@ extern "C" {
  *                row-bias epilogues are GEMM_ERR_UNSUPPORTED.
  *   workspace    256-byte aligned; needed only for an A or B that TMA cannot
  *                address (a base, leading dimension or group stride that is not
- *                a multiple of 16 bytes), which is copied first.
+ *                a multiple of 16 bytes, or matrices side by side), which is
+ *                copied first.
  *                gemm_grouped_workspace_size() always suffices.
  *
  * Products accumulate in fp32 (an fp32 C: at most 768 in the tensor core's
@@ -79,7 +82,8 @@ size_t gemm_grouped_workspace_size(gemm_dtype_t ab_dtype, int64_t groups, int64_
  *
  *   A, lda       T x M, row-major.     D, ldd   T x N, row-major.
  *   C, ldc, stride_c   one M x N row-major matrix per group, c_dtype ab_dtype
- *                or GEMM_DT_F32; stride_c must keep them apart.
+ *                or GEMM_DT_F32; stride_c must keep them apart (one after
+ *                another, or side by side as B of gemm_grouped).
  *   Other arguments as gemm_grouped.
  */
 gemm_status_t gemm_grouped_wgrad(gemm_dtype_t ab_dtype, int64_t groups, int64_t T, int64_t M,

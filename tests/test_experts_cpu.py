@@ -182,6 +182,20 @@ def test_exact_4_bit_products_need_no_weights_in_the_workspace():
     assert dg.gemm_w4_workspace_size(0, 1, 300, 16, 64, 64, 64, 0) == 2048
 
 
+def test_matrices_side_by_side_are_no_overlap():
+    """Column blocks of one wide matrix stay clear of each other; blocks that are not as wide
+    as their stride says do not."""
+    ok = NODEV if NO_GPU else None
+    assert dg.gemm_grouped_workspace_size(0, 3, 10, 16, 8, 64, 8, 64, 48, 0, 16) == 512 + 256
+    assert grouped(ldb=40, stride_b=16) == BAD and grouped(ldb=48, stride_b=8) == BAD
+    assert wgrad(ldc=40, stride_c=16) == BAD and wgrad(ldc=48, stride_c=8) == BAD
+    assert ns(batch=3, stride_g=16, ldg=48, ldo=40, stride_o=16) == BAD
+    if ok is not None:
+        assert grouped(ldb=48, stride_b=16, workspace=256, workspace_bytes=768) == ok
+        assert wgrad(ldc=48, stride_c=16) == ok
+        assert ns(batch=3, stride_g=16, ldg=48, ldo=48, stride_o=16) == ok
+
+
 def test_tensor_level_refusals():
     A, B = torch.zeros((4, 8), dtype=torch.bfloat16), torch.zeros((2, 8, 16), dtype=torch.bfloat16)
     o = torch.tensor([0, 1, 4], dtype=torch.int32)

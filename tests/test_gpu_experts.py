@@ -1339,3 +1339,36 @@ def test_w4_exact_option_rounds_once(counts, dtype):
     assert torch.equal(got, once)
     assert not torch.equal(default, once)
     assert status() == 0
+
+
+@pytest.mark.parametrize("layout", ["row", "col"])
+@pytest.mark.parametrize("counts", [[5, 0, 20], [300, 77, 900]])
+def test_weights_side_by_side(counts, layout):
+    """The experts' weights as column (row) blocks of one wide matrix, and their gradients
+    into such blocks: neighbours' columns stay what they were."""
+    rng = np.random.default_rng(101)
+    b, E, K, N = bounds_of(counts), len(counts), 264, 136
+    T = b[-1]
+    A, D = ints(rng, (T, K), -2, 2), ints(rng, (T, N), -2, 2)
+    wide = ints(rng, (K, E * N)) if layout == "row" else ints(rng, (N, E * K))
+    B = wide.view(K, E, N).transpose(0, 1) if layout == "row" else \
+        wide.view(N, E, K).permute(1, 2, 0)
+    Bd = wide.to(DEV)
+    Bd = Bd.view(K, E, N).transpose(0, 1) if layout == "row" else Bd.view(N, E, K).permute(1, 2, 0)
+    assert Bd.stride() == B.stride() and Bd.shape == (E, K, N)
+    equal(dg.grouped_gemm(A.to(DEV), Bd, offs(b), out_dtype=F32), ref.grouped(A, B, b), F32)
+    for out in (F32, BF):
+        C = torch.full((K, E * N + 8), 3.0, dtype=out, device=DEV)
+        blocks = C.as_strided((E, K, N), (N, E * N + 8, 1))
+        dg.grouped_gemm_wgrad(A.to(DEV), D.to(DEV), offs(b), blocks, beta=1.0)
+        equal(blocks, ref.wgrad(A, D, b, torch.full((E, K, N), 3.0), beta=1.0), out)
+        assert bool((C[:, E * N:] == 3).all())
+    assert status() == 0
+
+
+def test_newton_schulz_results_side_by_side():
+    G = torch.randn((3, 40, 56), generator=torch.Generator(device=DEV).manual_seed(8), device=DEV)
+    wide = torch.full((40, 3 * 56 + 4), 2.0, dtype=BF, device=DEV)
+    out = wide.as_strided((3, 40, 56), (56, 3 * 56 + 4, 1))
+    dg.newton_schulz(G, out)
+    assert torch.equal(out, dg.newton_schulz(G)) and bool((wide[:, 168:] == 2).all())
