@@ -327,7 +327,8 @@ def run(state):
                                   out_scales=s.get("rows_scales"))
     if c["op"] == "combine":
         return dg.expert_combine(s["ys"], s["slots"], s["weights"], out_dtype=_DT[c["out"]])
-    return dg.expert_combine_grad(s["dy"], s["slots"], s["weights"], ys=s["ys"], out=s["d_rows"])
+    return dg.expert_combine_grad(s["dy"], s["slots"], s["weights"], rows=s["ys"],
+                                  out=s["d_rows"])
 
 
 def exact(case, seed):
