@@ -37,6 +37,7 @@ class DType(enum.IntEnum):
     BF16 = 0
     F16 = 1
     F32 = 2
+    I8 = 3
 
 
 class Epi(enum.IntEnum):
@@ -144,6 +145,17 @@ _SIGNATURES = {
     "gemm_w4": ([_i32, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i32, _vp, _i64, _i32,
                  _vp, _vp, _i64, _i32, _vp, _sz, _vp], _i32),
     "gemm_w4_workspace_size": ([_i32, _i64, _i64, _i64, _i64, _vp, _i64, _i32], _sz),
+    "gemm_expert_dispatch": ([_i32, _i64, _i64, _vp, _i64, _vp, _i32, _vp, _i64, _i64, _i64, _vp,
+                              _i64, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
+    "gemm_expert_dispatch_workspace_size": ([_i64, _i64, _i64], _sz),
+    "gemm_expert_combine": ([_i32, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i32, _i64, _vp,
+                             _i64, _i32, _vp], _i32),
+    "gemm_expert_combine_grad": ([_i32, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i32, _i64, _vp,
+                                  _i64, _i64, _vp, _i64, _vp, _i32, _i64, _vp], _i32),
+    "gemm_i8_quantize": ([_i32, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp], _i32),
+    "gemm_i8": ([_i32, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _i64, _vp,
+                 _i64, _i32, _vp, _vp, _i64, _i32, _vp, _sz, _vp], _i32),
+    "gemm_i8_workspace_size": ([_i32, _i64, _i64, _i64, _i64, _vp, _i64, _i64], _sz),
     "gemm_debug_count_writes": ([_vp, _i64], _i32),
 }
 # size of the library-owned scratch array used by gemm_bf16_static_workspace
@@ -321,6 +333,48 @@ def gemm_w4(ab_dtype, groups, T, N, K, A, lda, Q, scales, zeros, group, C, ldc, 
 
 def gemm_w4_workspace_size(ab_dtype, groups, T, N, K, A, lda, c_dtype) -> int:
     return lib().gemm_w4_workspace_size(ab_dtype, groups, T, N, K, A, lda, c_dtype)
+
+
+def gemm_expert_dispatch(elem_bytes, T, K, X, ldx, scales, id_bytes, ids, ld_ids, top, groups, rows,
+                         ld_rows, row_scales, offsets, slots, workspace, workspace_bytes,
+                         stream) -> int:
+    return lib().gemm_expert_dispatch(elem_bytes, T, K, X, ldx, scales, id_bytes, ids, ld_ids, top,
+                                      groups, rows, ld_rows, row_scales, offsets, slots, workspace,
+                                      workspace_bytes, stream)
+
+
+def gemm_expert_dispatch_workspace_size(T, top, groups) -> int:
+    return lib().gemm_expert_dispatch_workspace_size(T, top, groups)
+
+
+def gemm_expert_combine(dtype, T, K, top, rows, R, ld_rows, slots, weights, w_dtype, ld_weights, Y,
+                        ldy, y_dtype, stream) -> int:
+    return lib().gemm_expert_combine(dtype, T, K, top, rows, R, ld_rows, slots, weights, w_dtype,
+                                     ld_weights, Y, ldy, y_dtype, stream)
+
+
+def gemm_expert_combine_grad(dtype, T, K, top, DY, lddy, slots, weights, w_dtype, ld_weights, rows,
+                             R, ld_rows, d_rows, ld_drows, d_weights, dw_dtype, ld_dweights,
+                             stream) -> int:
+    return lib().gemm_expert_combine_grad(dtype, T, K, top, DY, lddy, slots, weights, w_dtype,
+                                          ld_weights, rows, R, ld_rows, d_rows, ld_drows, d_weights,
+                                          dw_dtype, ld_dweights, stream)
+
+
+def gemm_i8_quantize(dtype, T, K, X, ldx, Q, ldq, scales, stream) -> int:
+    return lib().gemm_i8_quantize(dtype, T, K, X, ldx, Q, ldq, scales, stream)
+
+
+def gemm_i8(x_dtype, groups, T, N, K, X, ldx, x_scales, Q, ldq, stride_q, w_scales, stride_ws, C,
+            ldc, c_dtype, offsets, bias, stride_bias, epi, workspace, workspace_bytes,
+            stream) -> int:
+    return lib().gemm_i8(x_dtype, groups, T, N, K, X, ldx, x_scales, Q, ldq, stride_q, w_scales,
+                         stride_ws, C, ldc, c_dtype, offsets, bias, stride_bias, epi, workspace,
+                         workspace_bytes, stream)
+
+
+def gemm_i8_workspace_size(x_dtype, groups, T, N, K, Q, ldq, stride_q) -> int:
+    return lib().gemm_i8_workspace_size(x_dtype, groups, T, N, K, Q, ldq, stride_q)
 
 
 def gemm_build_flags() -> int:

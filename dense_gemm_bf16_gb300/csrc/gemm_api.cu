@@ -10,6 +10,7 @@
 #include <mutex>
 
 #include "gemm.h"
+#include "i8.h"
 #include "internal.h"
 #include "ptx.cuh"
 #include "ragged.h"
@@ -1062,6 +1063,7 @@ gemm_status_t device_info(DeviceInfo* out) {
         if (e == cudaSuccess) e = rg_prepare_wgrad();
         if (e == cudaSuccess) e = rg_prepare_seq();
         if (e == cudaSuccess) e = w4_prepare();
+        if (e == cudaSuccess) e = i8_prepare();
         d->experts_err = e;
         if (e != cudaSuccess) cudaGetLastError();
     });
@@ -1167,6 +1169,12 @@ bool encode_map8(CUtensorMap* map, const void* ptr, int64_t inner, int64_t rows,
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4u, const_cast<void*>(ptr), dims, strides, box,
               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_map8_rows(CUtensorMap* map, const void* ptr, int64_t inner, int64_t rows, int64_t depth,
+                      int64_t ld, int64_t stride, uint32_t box_rows) {
+    return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, ptr, inner, rows, depth, ld, stride, 128,
+                      box_rows);
 }
 
 bool encode_map16_blocks(CUtensorMap* map, int dt, const void* ptr, int64_t k, int64_t rows,

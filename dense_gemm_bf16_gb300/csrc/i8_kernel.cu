@@ -1,0 +1,654 @@
+// Products of 8-bit integers with a scale for each token and each output channel:
+//
+//   y[t, n] = act( (sum_k x[t, k] q_e[n, k]) * sx[t] * sw_e[n] + bias_e[n] )
+//
+// for the rows t of group e.  The tensor cores of sm_103a multiply no 8-bit integers at a
+// useful rate, but an int8 is an exact fp16 number, a product of two at most 2^14, and 1024
+// of them sum to at most 2^24, which the fp32 accumulator holds exactly.  So the kernel
+// multiplies fp16 (at the 16-bit rate), takes at most 1024 products into an accumulator and
+// adds that to 32-bit integers in registers: the sum is the integer sum, whatever the
+// tiles, splits and order, and a row's result does not depend on the call's other rows.
+//
+// What it saves against 16-bit weights is bytes, so the weights stay bytes up to the SM:
+//
+//   warp 2       loads 128 weight rows x 128 bytes by TMA (128-byte swizzle);
+//   warps 4-7    read their lane's row, make fp16 pairs by byte permutes (b ^ 128 under the
+//                exponent of 1024 is 1152 + b; one packed subtraction) and store them to
+//                tensor memory, 64 columns a stage;
+//   warp 0       loads the tokens' fp16 rows by TMA (made once per call in the workspace);
+//   warp 1       issues tcgen05.mma with its A operand in tensor memory;
+//   warps 8-15   add accumulators up and write the result.
+//
+// Weights in tensor memory rather than back in shared memory: a stage then moves 16 KB in
+// and out of shared memory for the weights and 24 KB in and out for the tokens in 768
+// clocks of MMAs, 107 of the 128 bytes a clock; with fp16 weights stored to shared memory
+// and read from there it would be 150.  Tiles have the weights on the MMA's M side (128 rows
+// a CTA, 256 a pair) and the tokens on its N side, which is ragged in steps of 16: as in
+// ragged_kernel.cuh, whose tiles, walk and bounded waits this kernel shares.  A pair's tile
+// has 192 columns, so that two accumulators (384 columns) and two stages of weights (128)
+// fill tensor memory: with 256 columns and one accumulator the MMAs would wait for every
+// one of its hand-overs.
+//
+// Few tokens leave one tile per 128 weight rows; where those do not fill half of the SMs,
+// the CTAs of a cluster share a tile's contraction and send their integer sums to the first
+// one's shared memory.
+#include "i8.h"
+#include "ragged_kernel.cuh"
+
+namespace dg {
+namespace {
+
+constexpr int kI8Threads = 512;
+constexpr int kI8Sum = 8;        // stages of 128 that an accumulator takes
+constexpr int kI8MaxSplits = 4;
+
+template <int CG, int BT, bool SPLIT>
+struct I8Cfg {
+    static constexpr int B_ROWS = BT / CG;                  // token rows a CTA holds
+    static constexpr uint32_t A_BYTES = 128 * 128;          // int8
+    static constexpr uint32_t B_BYTES = 2 * B_ROWS * 128;   // two 64-deep blocks of fp16
+    static constexpr int NC = BT < 64 ? 1 : BT / 64;        // 32-column chunks of an epilogue warp
+    static constexpr uint32_t D_COLS = 2 * BT;              // two accumulators
+    static constexpr int TA = (512 - D_COLS) / 64 < 4 ? (512 - D_COLS) / 64 : 4;
+    static constexpr uint32_t RED_BYTES = SPLIT ? (kI8MaxSplits - 1) * BT * 128 * 4 : 0;
+    static constexpr uint32_t BAR_BYTES = 512;
+    // stages of tokens, and of weights with what is left
+    static constexpr int SB = BT >= 128 ? (CG == 2 ? 4 : 3) : 6;
+    static constexpr int FIT = (kRgMaxSmem - 1024 - BAR_BYTES - RED_BYTES - SB * B_BYTES) / A_BYTES;
+    static constexpr int SA = FIT > 10 ? 10 : FIT;
+    static constexpr size_t SMEM = 1024 + size_t(SA) * A_BYTES + SB * B_BYTES + RED_BYTES + BAR_BYTES;
+    static_assert(TA >= 2 && SA >= 3, "rings");
+    static_assert(B_BYTES % 2048 == 0, "both blocks start on swizzle atoms");
+    static_assert((2 * (SA + SB + TA) + 6) * 8 + 8 <= BAR_BYTES, "barrier area too small");
+    static_assert(!SPLIT || CG == 1, "a tile is shared by single CTAs");
+};
+
+// What the roles of a CTA share.
+struct I8Cta {
+    uint32_t sA0, sB0;
+    int* red;
+    uint32_t afull, aempty;    // weights in shared memory
+    uint32_t wfull, wempty;    // weights in tensor memory
+    uint32_t bfull, bempty;    // tokens
+    uint32_t tfull, tempty;    // accumulators
+    uint32_t drain_bar, red_bar;
+    uint32_t tmem;
+    volatile int* abort_flag;
+    uint32_t rank;             // CTA of the pair, or of the split
+    bool leader;
+    int cl, ncl;               // this cluster, clusters of the grid
+    int lane;
+};
+
+// D += A B with A in tensor memory (a row per lane, two fp16 of it per column).
+template <int CG>
+__device__ __forceinline__ void umma_f16_tmem_a(uint32_t d, uint32_t a, uint64_t b_desc,
+                                                uint32_t idesc, uint32_t accumulate) {
+    if constexpr (CG == 2)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+            ::"r"(d), "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+            ::"r"(d), "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+
+// Four int8 as two pairs of fp16.
+__device__ __forceinline__ void i8_halves(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const uint32_t u = w ^ 0x80808080u;
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const uint32_t bias = 0x64806480u;  // 1152
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&bias));
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), *reinterpret_cast<const __half2*>(&bias));
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+}
+
+__device__ __forceinline__ uint4 i8_ld_shared(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+
+__device__ __forceinline__ void i8_st_cluster(uint32_t addr, int v) {
+    asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// Acquires what the CTAs of the cluster wrote before they arrived.
+__device__ __forceinline__ bool i8_try_wait_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// Stages of a tile's contraction that this CTA takes.
+template <bool SPLIT>
+__device__ __forceinline__ void i8_range(const I8Params& p, const I8Cta& x, int klen, int& s0, int& s1) {
+    const int steps = (klen + 127) / 128;
+    s0 = SPLIT ? static_cast<int>(static_cast<int64_t>(steps) * x.rank / p.splits) : 0;
+    s1 = SPLIT ? static_cast<int>(static_cast<int64_t>(steps) * (x.rank + 1) / p.splits) : steps;
+}
+
+// Where a role stands in a ring.
+template <int N>
+struct I8Ring {
+    int at = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++at == N) {
+            at = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
+// Every copy armed on a ring's barriers lands before the CTA exits.
+template <int N>
+__device__ __forceinline__ void i8_drain(uint32_t full, uint32_t armed, uint64_t timeout_ns) {
+    for (int s = 0; s < N && static_cast<uint32_t>(s) < armed; ++s) {
+        const uint32_t fills = (armed - 1u - s) / N + 1u;
+        rg_drain(full + 8u * s, (fills - 1u) & 1u, timeout_ns);
+    }
+}
+
+// ------------------------------------------------ weights, by TMA (a warp)
+template <int CG, int BT, bool SPLIT>
+__device__ __forceinline__ void i8_load_weights(const I8Params& p, const I8Cta& x) {
+    using C = I8Cfg<CG, BT, SPLIT>;
+    // (few tokens read a weight once; many read it for every tile of tokens)
+    const uint64_t pol = BT <= 32 ? l2_policy_evict_first() : l2_policy_evict_normal();
+    RgWalk walk = rg_begin<RG_ROWS>(p.g, x.lane);
+    RgTile w;
+    I8Ring<C::SA> ring;
+    uint32_t armed = 0;
+    bool ok = true;
+    for (int t = x.cl; ok && rg_tile<CG, BT, RG_ROWS>(p.g, walk, t, x.lane, SPLIT ? 0u : x.rank, w); t += x.ncl) {
+        int s0, s1;
+        i8_range<SPLIT>(p, x, w.klen, s0, s1);
+        for (int s = s0; s < s1; ++s) {
+            ok = rg_all_wait(x.aempty + 8u * ring.at, ring.phase ^ 1u, p.g, x.abort_flag);
+            if (p.g.test_stall == 1 && armed == 0) ok = false;  // test only: the others' bounded waits must expire
+            if (!ok) break;
+            if (x.lane == 0) {
+                const uint32_t bar = x.afull + 8u * ring.at;
+                mbar_arrive_expect_tx(bar, C::A_BYTES);
+                tma_load_3d(x.sA0 + ring.at * C::A_BYTES, &p.g.tmap_a, bar, s * 128, w.lane0,
+                            p.g.a_z ? w.group : 0, pol);
+            }
+            ++armed;
+            ring.next();
+        }
+    }
+    if (x.lane == 0) i8_drain<C::SA>(x.afull, armed, p.g.timeout_ns);
+    __syncwarp();
+}
+
+// ------------------------------------------------ tokens, by TMA (a warp)
+template <int CG, int BT, bool SPLIT>
+__device__ __forceinline__ void i8_load_tokens(const I8Params& p, const I8Cta& x) {
+    using C = I8Cfg<CG, BT, SPLIT>;
+    const uint64_t pol = l2_policy_evict_last();
+    RgWalk walk = rg_begin<RG_ROWS>(p.g, x.lane);
+    RgTile w;
+    I8Ring<C::SB> ring;
+    uint32_t armed = 0;
+    bool ok = true;
+    if (p.g.pdl) griddep_wait();
+    for (int t = x.cl; ok && rg_tile<CG, BT, RG_ROWS>(p.g, walk, t, x.lane, SPLIT ? 0u : x.rank, w); t += x.ncl) {
+        const int n_mma = rg_uniform(w.n_mma);
+        const int rows_b = n_mma / CG;
+        const int b_row = rg_uniform(w.b_row) + (CG == 2 ? static_cast<int>(x.rank) * rows_b : 0);
+        // whole-tile boxes, or 32-row boxes where those are fewer bytes
+        const bool big = 4 * rows_b > 3 * C::B_ROWS;
+        const int nb = big ? 1 : (rows_b + 31) / 32;
+        const uint32_t bytes = big ? C::B_BYTES : nb * 8192u;
+        int s0, s1;
+        i8_range<SPLIT>(p, x, w.klen, s0, s1);
+        for (int s = s0; s < s1; ++s) {
+            ok = rg_all_wait(x.bempty + 8u * ring.at, ring.phase ^ 1u, p.g, x.abort_flag);
+            if (!ok) break;
+            if (x.lane == 0) {
+                const uint32_t fb = x.bfull + 8u * ring.at;
+                const uint32_t bar = CG == 1 || x.leader ? fb : mapa_shared(fb, 0u);
+                const uint32_t dst = x.sB0 + ring.at * C::B_BYTES;
+                if (CG == 1 || x.leader) mbar_arrive_expect_tx(fb, CG * bytes);
+                if (big) {
+                    tma_load_4d_cg<CG>(dst, &p.g.tmap_b, bar, 0, b_row, 2 * s, 0, pol);
+                } else {
+                    for (int h = 0; h < nb; ++h)
+                        for (int blk = 0; blk < 2; ++blk) {
+                            const uint32_t to = dst + blk * (C::B_BYTES / 2) + 4096u * h;
+                            if constexpr (CG == 2)
+                                tma_load_3d_pair(to, &p.g.tmap_b32, bar, s * 128 + 64 * blk,
+                                                 b_row + 32 * h, 0, pol);
+                            else
+                                tma_load_3d(to, &p.g.tmap_b32, bar, s * 128 + 64 * blk,
+                                            b_row + 32 * h, 0, pol);
+                        }
+                }
+            }
+            ++armed;
+            ring.next();
+        }
+    }
+    if (x.lane == 0) {
+        if (CG == 2 && !x.leader) {
+            // (its copies complete on the leader's barriers: after an abort they get a
+            // fixed time, otherwise the leader has consumed them before the last barrier)
+            if (!ok) {
+                const uint64_t t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 200000ull) {
+                }
+            }
+        } else {
+            i8_drain<C::SB>(x.bfull, armed, p.g.timeout_ns);
+        }
+    }
+    __syncwarp();
+}
+
+// ------------------------------------------------ weights to tensor memory (four warps)
+template <int CG, int BT, bool SPLIT>
+__device__ __forceinline__ void i8_convert(const I8Params& p, const I8Cta& x, int warp) {
+    using C = I8Cfg<CG, BT, SPLIT>;
+    const int q = warp & 3, row = q * 32 + x.lane;
+    const uint32_t a_row = x.sA0 + row * 128, swz = static_cast<uint32_t>(row & 7) << 4;
+    const uint32_t to = x.tmem + (static_cast<uint32_t>(q * 32) << 16) + C::D_COLS;
+    RgWalk walk = rg_begin<RG_ROWS>(p.g, x.lane);
+    RgTile w;
+    I8Ring<C::SA> in;
+    I8Ring<C::TA> out;
+    bool ok = true;
+    for (int t = x.cl; ok && rg_tile<CG, BT, RG_ROWS>(p.g, walk, t, x.lane, SPLIT ? 0u : x.rank, w); t += x.ncl) {
+        int s0, s1;
+        i8_range<SPLIT>(p, x, w.klen, s0, s1);
+        for (int s = s0; s < s1; ++s) {
+            ok = rg_all_wait(x.afull + 8u * in.at, in.phase, p.g, x.abort_flag);
+            if (!ok) break;
+            const uint32_t src = a_row + in.at * C::A_BYTES;
+            uint4 v[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) v[c] = i8_ld_shared(src + ((c << 4) ^ swz));
+            __syncwarp();
+            if (x.lane == 0) mbar_arrive(x.aempty + 8u * in.at);
+            in.next();
+            ok = rg_all_wait(x.wempty + 8u * out.at, out.phase ^ 1u, p.g, x.abort_flag);
+            if (!ok) break;
+            tc_fence_after_sync();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t r[32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    i8_halves(v[4 * h + c].x, r[8 * c], r[8 * c + 1]);
+                    i8_halves(v[4 * h + c].y, r[8 * c + 2], r[8 * c + 3]);
+                    i8_halves(v[4 * h + c].z, r[8 * c + 4], r[8 * c + 5]);
+                    i8_halves(v[4 * h + c].w, r[8 * c + 6], r[8 * c + 7]);
+                }
+                tmem_st_x32(to + out.at * 64 + 32 * h, r);
+            }
+            tmem_st_wait();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (x.lane == 0) {
+                const uint32_t bar = x.wfull + 8u * out.at;
+                if (CG == 2)
+                    mbar_arrive_remote(mapa_shared(bar, 0u));
+                else
+                    mbar_arrive(bar);
+            }
+            out.next();
+        }
+    }
+}
+
+// ------------------------------------------------ MMA issuer (a warp; of the pair's leader)
+template <int CG, int BT, bool SPLIT>
+__device__ __forceinline__ void i8_issue(const I8Params& p, const I8Cta& x) {
+    using C = I8Cfg<CG, BT, SPLIT>;
+    constexpr uint16_t kPair = 3u;
+    if (CG == 2 && !x.leader) return;
+    const uint64_t b_desc0 = smem_desc_sw128(x.sB0, 16u, 1024u);
+    const uint32_t tmem = static_cast<uint32_t>(rg_uniform(static_cast<int>(x.tmem)));
+    RgWalk walk = rg_begin<RG_ROWS>(p.g, x.lane);
+    RgTile w;
+    I8Ring<C::TA> wr;
+    I8Ring<C::SB> br;
+    I8Ring<2> acc;
+    bool ok = true, issued = false;
+    auto commit = [&](uint32_t bar) {
+        if constexpr (CG == 2)
+            umma_commit_mc_cg<CG>(bar, kPair);
+        else
+            umma_commit_cg<CG>(bar);
+    };
+    for (int t = x.cl; ok && rg_tile<CG, BT, RG_ROWS>(p.g, walk, t, x.lane, SPLIT ? 0u : x.rank, w); t += x.ncl) {
+        int s0, s1;
+        i8_range<SPLIT>(p, x, w.klen, s0, s1);
+        const uint32_t idesc = p.g.idesc | (static_cast<uint32_t>(rg_uniform(w.n_mma) >> 3) << 17);
+        for (int s = s0; s < s1; ++s) {
+            const bool fresh = (s - s0) % kI8Sum == 0;
+            const bool last = s + 1 == s1 || (s - s0) % kI8Sum == kI8Sum - 1;
+            if (fresh) {
+                ok = rg_all_wait(x.tempty + 8u * acc.at, acc.phase ^ 1u, p.g, x.abort_flag);
+                if (!ok) break;
+            }
+            ok = rg_all_wait(x.bfull + 8u * br.at, br.phase, p.g, x.abort_flag) &&
+                 rg_all_wait(x.wfull + 8u * wr.at, wr.phase, p.g, x.abort_flag);
+            if (!ok) break;
+            tc_fence_after_sync();
+            const uint32_t d = tmem + static_cast<uint32_t>(acc.at * BT);
+            const uint32_t a = tmem + C::D_COLS + static_cast<uint32_t>(wr.at * 64);
+            const uint64_t b = b_desc0 + static_cast<uint32_t>(br.at) * (C::B_BYTES >> 4);
+            if (x.lane == 0) {
+                // (past K both operands are zeros)
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    umma_f16_tmem_a<CG>(d, a + 8 * k, b + (k >> 2) * (C::B_BYTES >> 5) + (k & 3) * 2,
+                                        idesc, (!fresh || k > 0) ? 1u : 0u);
+                commit(x.wempty + 8u * wr.at);
+                commit(x.bempty + 8u * br.at);
+                if (last) commit(x.tfull + 8u * acc.at);
+            }
+            issued = true;
+            wr.next();
+            br.next();
+            if (last) acc.next();
+        }
+    }
+    // all MMAs complete before tensor memory is released
+    if (issued && x.lane == 0) {
+        umma_commit_cg<CG>(x.drain_bar);
+        rg_drain(x.drain_bar, 0u, p.g.timeout_ns);
+    }
+    __syncwarp();
+}
+
+// ------------------------------------------------ epilogue (a warp of eight)
+// One output column per thread, its tile's tokens in the registers.
+template <int CG, int BT, bool SPLIT>
+__device__ __forceinline__ void i8_epilogue(const I8Params& p, const I8Cta& x, int warp) {
+    using C = I8Cfg<CG, BT, SPLIT>;
+    const int q = warp & 3;  // tensor-memory lane quarter of this warp
+    const int c_first = ((warp - 8) >> 2) * 32;
+    const uint32_t row = x.tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(c_first);
+    RgWalk walk = rg_begin<RG_ROWS>(p.g, x.lane);
+    RgTile w;
+    I8Ring<2> acc;
+    if (p.g.pdl) griddep_wait();  // (the tokens' scales)
+    for (int t = x.cl; rg_tile<CG, BT, RG_ROWS>(p.g, walk, t, x.lane, SPLIT ? 0u : x.rank, w); t += x.ncl) {
+        int s0, s1;
+        i8_range<SPLIT>(p, x, w.klen, s0, s1);
+        const int n = w.lane0 + q * 32 + x.lane;
+        const bool mine = c_first < w.ncols && n - x.lane < p.g.n_lane;
+        int v[C::NC][32];
+#pragma unroll
+        for (int c = 0; c < C::NC; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[c][i] = 0;
+        bool ok = true;
+#pragma unroll 1
+        for (int s = s0; s < s1; s += kI8Sum) {
+            ok = rg_warp_wait(x.tfull + 8u * acc.at, acc.phase, x.lane, x.abort_flag, p.g);
+            if (!ok) break;
+            tc_fence_after_sync();
+            if (mine) {
+                const uint32_t from = row + static_cast<uint32_t>(acc.at * BT);
+#pragma unroll
+                for (int c = 0; c < C::NC; ++c) {
+                    if (c_first + 64 * c < w.ncols) {
+                        uint32_t u[32];
+                        tmem_ld_x32(from + 64u * c, u);
+                        tmem_ld_wait(u);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[c][i] += __float2int_rn(__uint_as_float(u[i]));
+                    }
+                }
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (x.lane == 0)
+                mbar_arrive_relaxed(mapa_shared(x.tempty + 8u * acc.at, CG == 2 ? 0u : x.rank));
+            acc.next();
+        }
+        if (!ok) return;
+        if (SPLIT) {
+            // (one tile a cluster) the other CTAs' sums go to the first one
+            if (x.rank != 0) {
+                if (mine) {
+                    const uint32_t at = mapa_shared(smem_u32(x.red), 0u) +
+                                        ((x.rank - 1) * BT * 128 + q * 32 + x.lane) * 4u;
+#pragma unroll
+                    for (int c = 0; c < C::NC; ++c)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            i8_st_cluster(at + (c_first + 64 * c + i) * 512u, v[c][i]);
+                }
+                __syncwarp();
+                if (x.lane == 0) mbar_arrive_remote(mapa_shared(x.red_bar, 0u));
+                return;
+            }
+            const uint64_t begin = globaltimer_ns();
+            while (!i8_try_wait_cluster(x.red_bar, 0u)) {
+                if (*x.abort_flag) return;
+                if (globaltimer_ns() - begin > p.g.timeout_ns) {
+                    *x.abort_flag = 1;
+                    if (p.g.status) DG_SET_TIMEOUT(p.g.status);
+                    return;
+                }
+            }
+            __syncwarp();
+            if (mine)
+                for (int r = 1; r < p.splits; ++r) {
+                    const int* from = x.red + (r - 1) * BT * 128 + q * 32 + x.lane;
+#pragma unroll
+                    for (int c = 0; c < C::NC; ++c)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[c][i] += from[(c_first + 64 * c + i) * 128];
+                }
+        }
+        if (!mine || n >= p.g.n_lane) continue;
+        const float sw = __ldg(p.w_scales + w.group * p.stride_ws + n);
+        const float bias = p.g.bias ? __ldg(p.g.bias + w.group * p.g.stride_bias + n) : 0.0f;
+#pragma unroll
+        for (int c = 0; c < C::NC; ++c) {
+            const int c0 = c_first + 64 * c;
+            if (c0 >= w.ncols) break;
+            const int left = w.ncols - c0;
+            const float* sx = p.x_scales + w.out_row + c0;
+            float o[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const float s = i < left ? __ldcg(sx + i) : 0.0f;
+                o[i] = fmaf(__int2float_rn(v[c][i]) * s, sw, bias);
+            }
+            rg_act(o, p.g.act);
+            const int64_t off = static_cast<int64_t>(w.out_row + c0) * p.g.ldc + n;
+            if (p.g.c_dtype == DT_F32) {
+                float* dst = static_cast<float*>(p.g.C) + off;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (i < left && rg_span_ok(p.g, off + i * p.g.ldc, 1)) dst[i * p.g.ldc] = o[i];
+            } else {
+                uint16_t* dst = static_cast<uint16_t*>(p.g.C) + off;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (i < left && rg_span_ok(p.g, off + i * p.g.ldc, 1))
+                        dst[i * p.g.ldc] = static_cast<uint16_t>(rg_pack(p.g.c_dtype, o[i], o[i]));
+            }
+        }
+    }
+}
+
+// Registers of the pair form: 96 sums a thread of the epilogue's two warpgroups.  512
+// threads are launched with 128 (i8_prepare checks it): 72 + 96 + 2 x 168 fit 4 x 128.
+constexpr int I8_LAUNCH_REGS = 128, I8_ISSUE_REGS = 72, I8_CONVERT_REGS = 96, I8_SUM_REGS = 168;
+static_assert(I8_ISSUE_REGS + I8_CONVERT_REGS + 2 * I8_SUM_REGS <= 4 * I8_LAUNCH_REGS, "register split");
+
+template <int CG, int BT, bool SPLIT>
+__global__ void __launch_bounds__(kI8Threads, 1) i8_kernel(const __grid_constant__ I8Params p) {
+    using C = I8Cfg<CG, BT, SPLIT>;
+    constexpr bool MOVE = BT > 128;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    const int warp = threadIdx.x >> 5;
+    const int per_tile = SPLIT ? p.splits : CG;
+    I8Cta x;
+    x.rank = CG > 1 || SPLIT ? cluster_ctarank() : 0u;
+    x.leader = x.rank == 0;
+    x.cl = static_cast<int>(blockIdx.x) / per_tile;
+    x.ncl = static_cast<int>(gridDim.x) / per_tile;
+    x.lane = threadIdx.x & 31;
+    x.sA0 = smem_u32(smem);
+    x.sB0 = x.sA0 + C::SA * C::A_BYTES;
+    x.red = reinterpret_cast<int*>(smem + C::SA * C::A_BYTES + C::SB * C::B_BYTES);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(x.red) + C::RED_BYTES);
+    x.afull = smem_u32(bars);
+    x.aempty = x.afull + 8u * C::SA;
+    x.bfull = x.aempty + 8u * C::SA;
+    x.bempty = x.bfull + 8u * C::SB;
+    x.wfull = x.bempty + 8u * C::SB;
+    x.wempty = x.wfull + 8u * C::TA;
+    x.tfull = x.wempty + 8u * C::TA;
+    x.tempty = x.tfull + 16u;
+    x.drain_bar = x.tempty + 16u;
+    x.red_bar = x.drain_bar + 8u;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * (C::SA + C::SB + C::TA) + 6);
+    x.abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::SA; ++s) {
+            mbar_init(x.afull + 8u * s, 1);
+            mbar_init(x.aempty + 8u * s, 4);
+        }
+        for (int s = 0; s < C::SB; ++s) {
+            mbar_init(x.bfull + 8u * s, 1);
+            mbar_init(x.bempty + 8u * s, 1);
+        }
+        for (int s = 0; s < C::TA; ++s) {
+            mbar_init(x.wfull + 8u * s, 4 * CG);
+            mbar_init(x.wempty + 8u * s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(x.tfull + 8u * b, 1);
+            mbar_init(x.tempty + 8u * b, 8 * CG);
+        }
+        mbar_init(x.drain_bar, 1);
+        mbar_init(x.red_bar, SPLIT ? 8 * (p.splits - 1) : 1);
+        *x.abort_flag = 0;
+        fence_mbar_init();
+        if (p.g.maps) {
+            prefetch_tmap(&p.g.tmap_a);
+            prefetch_tmap(&p.g.tmap_b);
+            prefetch_tmap(&p.g.tmap_b32);
+        }
+    }
+    if (warp == 1) {
+        tmem_alloc_cg<CG>(smem_u32(tmem_slot), 512u);
+        tmem_relinquish_cg<CG>();
+    }
+    tc_fence_before_sync();
+    if constexpr (CG > 1 || SPLIT)
+        cluster_sync();
+    else
+        __syncthreads();
+    tc_fence_after_sync();
+    x.tmem = *tmem_slot;
+
+    if (warp >= 8) {
+        if (MOVE) reg_inc<I8_SUM_REGS>();
+        i8_epilogue<CG, BT, SPLIT>(p, x, warp);
+    } else if (warp >= 4) {
+        if (MOVE) reg_dec<I8_CONVERT_REGS>();
+        i8_convert<CG, BT, SPLIT>(p, x, warp);
+    } else {
+        if (MOVE) reg_dec<I8_ISSUE_REGS>();
+        if (warp == 0)
+            i8_load_tokens<CG, BT, SPLIT>(p, x);
+        else if (warp == 1)
+            i8_issue<CG, BT, SPLIT>(p, x);
+        else if (warp == 2)
+            i8_load_weights<CG, BT, SPLIT>(p, x);
+    }
+    __syncwarp();
+    tc_fence_before_sync();
+    __syncthreads();
+    if constexpr (CG > 1 || SPLIT) cluster_sync();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc_cg<CG>(x.tmem, 512u);
+    }
+}
+
+template <int CG, int BT, bool SPLIT>
+cudaError_t launch_form(const I8Params& p, int grid, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(kI8Threads);
+    cfg.dynamicSmemBytes = I8Cfg<CG, BT, SPLIT>::SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    unsigned n = 0;
+    if (p.g.pdl) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
+    if (CG > 1 || SPLIT) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = SPLIT ? static_cast<unsigned>(p.splits) : CG;
+        attr[n].val.clusterDim.y = 1;
+        attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    return cudaLaunchKernelEx(&cfg, i8_kernel<CG, BT, SPLIT>, p);
+}
+
+template <int CG, int BT, bool SPLIT>
+cudaError_t prepare_form() {
+    cudaError_t e = cudaFuncSetAttribute(i8_kernel<CG, BT, SPLIT>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(I8Cfg<CG, BT, SPLIT>::SMEM));
+    // (a wait for registers that the launch does not have would never end)
+    cudaFuncAttributes a;
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, i8_kernel<CG, BT, SPLIT>);
+    if (e == cudaSuccess && BT > 128 && a.numRegs < I8_LAUNCH_REGS) e = cudaErrorInvalidConfiguration;
+    return e;
+}
+
+}  // namespace
+
+cudaError_t i8_launch(int cg, int bt, const I8Params& p, int grid, cudaStream_t stream) {
+    if (p.splits > 1) return launch_form<1, 32, true>(p, grid, stream);
+    if (cg == 2) return launch_form<2, 192, false>(p, grid, stream);
+    if (bt == 128) return launch_form<1, 128, false>(p, grid, stream);
+    if (bt == 64) return launch_form<1, 64, false>(p, grid, stream);
+    return launch_form<1, 32, false>(p, grid, stream);
+}
+
+cudaError_t i8_prepare() {
+    cudaError_t e = prepare_form<1, 32, true>();
+    if (e == cudaSuccess) e = prepare_form<1, 32, false>();
+    if (e == cudaSuccess) e = prepare_form<1, 64, false>();
+    if (e == cudaSuccess) e = prepare_form<1, 128, false>();
+    if (e == cudaSuccess) e = prepare_form<2, 192, false>();
+    return e;
+}
+
+}  // namespace dg

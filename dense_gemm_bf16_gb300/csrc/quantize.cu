@@ -1,0 +1,318 @@
+// Rows to 8-bit integers with a scale each, and 8-bit operands in the forms that the
+// product of i8_kernel.cu reads.
+//
+//   s = max |x| / 127,   q = 127 x / max |x| to the nearest integer (ties to even)
+//
+// The quotient is decided exactly: fp32 gives y = x (127 / max |x|) to within 2^-23 of
+// itself, at most 1.6e-5; where y lies within 2^-14 of a border between two integers, the
+// two products 254 |x| and (2 n + 1) max |x| (at most 32 bits each, exact in fp64) are
+// compared instead.  So q does not depend on the reciprocal's rounding, and a result
+// computed in 64 bits is the same integer.
+//
+// One pass over the data: the threads of a row (a warp's worth at least, a block's at
+// most) keep its elements in registers between the maximum and the quotients, up to 32
+// each; longer rows are read again, from L2.  Bound by the bytes.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "experts_host.h"
+#include "gemm_experts.h"
+#include "i8.h"
+#include "ptx.cuh"
+
+namespace dg {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kKeep = 32;  // elements of a row that a thread keeps
+
+struct QuantParams {
+    const void* x;
+    int64_t ld_x;
+    int32_t T, K;
+    void* q;            // int8, or fp16 (the integers' values, padded with zeros to `pad`)
+    int64_t ld_q;       // elements
+    int32_t pad;
+    float* scales;
+    int32_t tpr_log2;   // threads of a row
+};
+
+template <int BYTES>
+struct Raw {
+    using V = std::conditional_t<BYTES == 16, uint4,
+                                 std::conditional_t<BYTES == 8, uint2,
+                                                    std::conditional_t<BYTES == 4, uint32_t,
+                                                                       std::conditional_t<BYTES == 2, uint16_t, uint8_t>>>>;
+};
+
+// N elements of type DT as fp32 (exact).
+template <int DT, int N, typename V>
+__device__ __forceinline__ void widen(const V& v, float (&f)[N]) {
+    if constexpr (DT == DT_F32) {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
+#pragma unroll
+        for (int i = 0; i < N; ++i) f[i] = __uint_as_float(w[i]);
+    } else {
+        const uint16_t* h = reinterpret_cast<const uint16_t*>(&v);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            f[i] = DT == DT_BF16 ? __uint_as_float(static_cast<uint32_t>(h[i]) << 16)
+                                 : __half2float(__ushort_as_half(h[i]));
+    }
+}
+
+// 127 x / top to the nearest integer; r = 127 / top rounded.
+__device__ __forceinline__ float quotient(float x, float top, float r) {
+    const float y = x * r;
+    float n = rintf(y);
+    if (fabsf(y - n) > 0.5f - 6.103515625e-5f) {
+        const float lo = floorf(fabsf(y));
+        const double a = 254.0 * static_cast<double>(fabsf(x));
+        const double b = (2.0 * static_cast<double>(lo) + 1.0) * static_cast<double>(top);
+        const bool odd = (static_cast<int>(lo) & 1) != 0;
+        n = copysignf(a > b || (a == b && odd) ? lo + 1.0f : lo, x);
+    }
+    return n;
+}
+
+// WIDE: fp16 integers, padded; else int8.
+template <int DT, int N, bool WIDE>
+__global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantParams p) {
+    constexpr int ES = DT == DT_F32 ? 4 : 2;
+    constexpr int R = kKeep / N;
+    using V = typename Raw<N * ES>::V;
+    using O = typename Raw<N * (WIDE ? 2 : 1)>::V;
+    __shared__ uint32_t tops[kThreads / 32];
+    if (WIDE) griddep_launch_dependents();
+    const int tpr = 1 << p.tpr_log2, in = threadIdx.x & (tpr - 1);
+    const int per_block = kThreads >> p.tpr_log2;
+    const int warp = threadIdx.x >> 5, warps = tpr >> 5, lane = threadIdx.x & 31;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * per_block;
+    // (whole blocks walk together: the maximum's barriers are the block's)
+    for (int64_t rb = static_cast<int64_t>(blockIdx.x) * per_block; rb < p.T; rb += step) {
+        const int64_t row = rb + (threadIdx.x >> p.tpr_log2);
+        const bool live = row < p.T;
+        const char* src = static_cast<const char*>(p.x) + row * p.ld_x * ES;
+        V keep[R];
+        // (magnitudes order as integers, infinities above all numbers and NaN above those)
+        uint32_t top = 0;
+        auto take = [&](const V& v) {
+            float f[N];
+            widen<DT, N>(v, f);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const uint32_t m = __float_as_uint(f[i]) & 0x7fffffffu;
+                top = m > top ? m : top;
+            }
+        };
+        if (live) {
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                const int c = (k * tpr + in) * N;
+                if (c < p.K) keep[k] = __ldg(reinterpret_cast<const V*>(src + static_cast<int64_t>(c) * ES));
+            }
+#pragma unroll
+            for (int k = 0; k < R; ++k)
+                if ((k * tpr + in) * N < p.K) take(keep[k]);
+            for (int64_t c = (static_cast<int64_t>(R) * tpr + in) * N; c < p.K; c += tpr * N)
+                take(__ldg(reinterpret_cast<const V*>(src + c * ES)));
+        }
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (warps > 1) {
+            __syncthreads();  // (the row before has been read)
+            if (lane == 0) tops[warp] = top;
+            __syncthreads();
+            const int first = warp & ~(warps - 1);
+            for (int i = 0; i < warps; ++i) top = tops[first + i] > top ? tops[first + i] : top;
+        }
+        if (!live) continue;
+        // (a row with an infinity or a NaN has no integers: a NaN scale says so)
+        const bool finite = top < 0x7f800000u;
+        const float size = __uint_as_float(top);
+        if (in == 0) p.scales[row] = finite ? __fdiv_rn(size, 127.0f) : __uint_as_float(0x7fffffffu);
+        // (a power of two keeps 127 / size and x 127 inside fp32; where it rounds an
+        // element, that element's integer is zero)
+        const float even = size < 0x1p-40f ? 0x1p100f : (size > 0x1p100f ? 0x1p-100f : 1.0f);
+        const float big = size * even;
+        const bool some = finite && top != 0;
+        const float r = some ? __fdiv_rn(127.0f, big) : 0.0f;
+        char* dst = static_cast<char*>(p.q) + row * p.ld_q * (WIDE ? 2 : 1);
+        auto put = [&](const V& v, int64_t c) {
+            float f[N];
+            widen<DT, N>(v, f);
+            O o;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float n = some ? quotient(f[i] * even, big, r) : 0.0f;
+                if constexpr (WIDE)
+                    reinterpret_cast<uint16_t*>(&o)[i] = __half_as_ushort(__float2half_rn(n));
+                else
+                    reinterpret_cast<int8_t*>(&o)[i] = static_cast<int8_t>(__float2int_rn(n));
+            }
+            *reinterpret_cast<O*>(dst + c * (WIDE ? 2 : 1)) = o;
+        };
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int c = (k * tpr + in) * N;
+            if (c < p.K) put(keep[k], c);
+        }
+        for (int64_t c = (static_cast<int64_t>(R) * tpr + in) * N; c < p.K; c += tpr * N)
+            put(__ldg(reinterpret_cast<const V*>(src + c * ES)), c);
+        if (WIDE)
+            for (int c = p.K + in; c < p.pad; c += tpr) reinterpret_cast<uint16_t*>(dst)[c] = 0;
+    }
+}
+
+int row_threads(int64_t units) {
+    int log2 = 5;
+    while (log2 < 8 && (int64_t(1) << log2) < units) ++log2;
+    return log2;
+}
+
+template <int DT, int N, bool WIDE>
+cudaError_t quantize_launch(QuantParams p, int sms, cudaStream_t stream) {
+    // a thread takes two units or more where the row has them: fewer barriers
+    p.tpr_log2 = row_threads((static_cast<int64_t>(p.K) + 2 * N - 1) / (2 * N));
+    int64_t blocks = cdiv(p.T, kThreads >> p.tpr_log2);
+    if (blocks > int64_t(sms) * 8) blocks = int64_t(sms) * 8;
+    quantize_kernel<DT, N, WIDE><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <int DT, bool WIDE>
+cudaError_t quantize_width(const QuantParams& p, int sms, cudaStream_t stream) {
+    constexpr int ES = DT == DT_F32 ? 4 : 2, FULL = 16 / ES;
+    auto fits = [&](int n) {
+        return p.K % n == 0 && aligned(p.x, n * ES) && p.ld_x % n == 0 &&
+               aligned(p.q, n * (WIDE ? 2 : 1)) && p.ld_q % n == 0;
+    };
+    if (fits(FULL)) return quantize_launch<DT, FULL, WIDE>(p, sms, stream);
+    if (fits(2)) return quantize_launch<DT, 2, WIDE>(p, sms, stream);
+    return quantize_launch<DT, 1, WIDE>(p, sms, stream);
+}
+
+template <bool WIDE>
+cudaError_t quantize_type(int dt, const QuantParams& p, int sms, cudaStream_t stream) {
+    return dt == DT_BF16  ? quantize_width<DT_BF16, WIDE>(p, sms, stream)
+           : dt == DT_F16 ? quantize_width<DT_F16, WIDE>(p, sms, stream)
+                          : quantize_width<DT_F32, WIDE>(p, sms, stream);
+}
+
+// int8 rows to fp16 ones, padded with zeros to `pad` (a multiple of 64): a thread takes 8
+// neighbouring elements.  VEC: the source's rows start on 8-byte boundaries and K is a
+// multiple of 8.
+template <bool VEC>
+__global__ void __launch_bounds__(kThreads) widen_kernel(const int8_t* x, int64_t ld, int T, int K,
+                                                         int pad, uint16_t* out) {
+    griddep_launch_dependents();
+    const int units = pad / 8;
+    const int64_t n = static_cast<int64_t>(T) * units;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n; i += stride) {
+        const int64_t row = i / units;
+        const int c = static_cast<int>(i - row * units) * 8;
+        const int8_t* src = x + row * ld + c;
+        int8_t b[8];
+        if (VEC) {
+            uint2 v = make_uint2(0, 0);
+            if (c < K) v = __ldg(reinterpret_cast<const uint2*>(src));
+            *reinterpret_cast<uint2*>(b) = v;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) b[k] = c + k < K ? __ldg(src + k) : int8_t(0);
+        }
+        uint4 o;
+        uint16_t* h = reinterpret_cast<uint16_t*>(&o);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) h[k] = __half_as_ushort(__short2half_rn(b[k]));
+        *reinterpret_cast<uint4*>(out + row * pad + c) = o;
+    }
+}
+
+// Bytes to rows of `ld_dst` (a multiple of 16), for weights that TMA cannot address.
+__global__ void __launch_bounds__(kThreads) pack8_kernel(const uint8_t* src, int64_t ld,
+                                                         int64_t stride, int64_t rows, int32_t cols,
+                                                         int64_t depth, uint8_t* dst, int64_t ld_dst) {
+    const int64_t n = rows * depth, step = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
+    for (int64_t r = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); r < n; r += step) {
+        const int64_t z = r / rows;
+        const uint8_t* from = src + z * stride + (r - z * rows) * ld;
+        uint8_t* to = dst + r * ld_dst;
+        for (int c = threadIdx.x & 31; c < cols; c += 32) to[c] = __ldg(from + c);
+    }
+}
+
+}  // namespace
+
+cudaError_t i8_widen_quantized(int dt, const void* x, int64_t ld, int64_t T, int64_t K, int64_t pad,
+                               void* out, float* scales, int sms, cudaStream_t stream) {
+    QuantParams p{};
+    p.x = x;
+    p.ld_x = ld;
+    p.T = static_cast<int32_t>(T);
+    p.K = static_cast<int32_t>(K);
+    p.q = out;
+    p.ld_q = pad;
+    p.pad = static_cast<int32_t>(pad);
+    p.scales = scales;
+    return quantize_type<true>(dt, p, sms, stream);
+}
+
+cudaError_t i8_widen(const void* x, int64_t ld, int64_t T, int64_t K, int64_t pad, void* out, int sms,
+                     cudaStream_t stream) {
+    const int64_t units = T * (pad / 8);
+    int64_t blocks = cdiv(units, kThreads);
+    if (blocks > int64_t(sms) * 16) blocks = int64_t(sms) * 16;
+    const dim3 g(static_cast<unsigned>(blocks));
+    const int8_t* src = static_cast<const int8_t*>(x);
+    const int t = static_cast<int>(T), k = static_cast<int>(K), n = static_cast<int>(pad);
+    if (aligned(x, 8) && ld % 8 == 0 && K % 8 == 0)
+        widen_kernel<true><<<g, kThreads, 0, stream>>>(src, ld, t, k, n, static_cast<uint16_t*>(out));
+    else
+        widen_kernel<false><<<g, kThreads, 0, stream>>>(src, ld, t, k, n, static_cast<uint16_t*>(out));
+    return cudaGetLastError();
+}
+
+cudaError_t i8_pack(const void* src, int64_t ld, int64_t stride, int64_t rows, int64_t cols,
+                    int64_t depth, void* dst, int64_t ld_dst, int sms, cudaStream_t stream) {
+    int64_t blocks = cdiv(rows * depth, kThreads / 32);
+    if (blocks > int64_t(sms) * 8) blocks = int64_t(sms) * 8;
+    pack8_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(
+        static_cast<const uint8_t*>(src), ld, stride, rows, static_cast<int32_t>(cols), depth,
+        static_cast<uint8_t*>(dst), ld_dst);
+    return cudaGetLastError();
+}
+
+}  // namespace dg
+
+using namespace dg;
+
+extern "C" gemm_status_t gemm_i8_quantize(gemm_dtype_t dtype, int64_t T, int64_t K, const void* X,
+                                          int64_t ldx, int8_t* Q, int64_t ldq, float* scales,
+                                          gemm_stream_t stream) {
+    if (!is_dt(dtype)) return GEMM_ERR_INVALID_ARG;
+    gemm_status_t st = extents(T, K, 0, 0);
+    if (st != GEMM_OK) return st;
+    if (T == 0) return GEMM_OK;
+    if (!scales || !aligned(scales, 4)) return GEMM_ERR_INVALID_ARG;
+    if (K > 0 && (!X || !aligned(X, dt_bytes(dtype)) || !Q || ldx < K || ldq < K ||
+                  !strided_span_ok(T, K, ldx, 1, 1, 0) || !strided_span_ok(T, K, ldq, 1, 1, 0) ||
+                  !count_ok(1, T, K)))
+        return GEMM_ERR_INVALID_ARG;
+    DeviceInfo d;
+    st = device_info(&d);
+    if (st != GEMM_OK) return st;
+    QuantParams p{};
+    p.x = X;
+    p.ld_x = ldx;
+    p.T = static_cast<int32_t>(T);
+    p.K = static_cast<int32_t>(K);
+    p.q = Q;
+    p.ld_q = ldq;
+    p.scales = scales;
+    if (quantize_type<false>(dtype, p, d.sm_count, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_CUDA;
+    }
+    return GEMM_OK;
+}

@@ -126,6 +126,9 @@ bool encode_map16_k4(CUtensorMap* map, int dt, const void* ptr, int64_t k, int64
 // blocks, or (bytes, rows, depth) with box_blocks == 0.
 bool encode_map8(CUtensorMap* map, const void* ptr, int64_t inner, int64_t rows, int64_t depth,
                  uint32_t box_rows, uint32_t box_blocks);
+// int8 matrices in boxes of 128 bytes x box_rows; ld and stride in bytes.
+bool encode_map8_rows(CUtensorMap* map, const void* ptr, int64_t inner, int64_t rows, int64_t depth,
+                      int64_t ld, int64_t stride, uint32_t box_rows);
 // 16-bit rows in 64-wide blocks: (64, rows, blocks) in boxes of `box_blocks` blocks.
 bool encode_map16_blocks(CUtensorMap* map, int dt, const void* ptr, int64_t k, int64_t rows,
                          int64_t row_stride, uint32_t box_rows, uint32_t box_blocks);
@@ -159,6 +162,7 @@ struct RgProblem {
     int64_t stride_bias;
     int act;
     bool pdl;          // the kernel enqueued just before prepares an operand
+    bool a8;           // the lane operand is int8, K-major, ld and stride in bytes
 };
 // The kernel variant a problem takes (CTAs per tile, columns), its parameters, and
 // a bound on its tiles.

@@ -315,3 +315,265 @@ def w4_gemm(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, *, zeros=Non
     if st:
         check(st)
     return out
+
+
+def _ids(ids):
+    """(pointer, bytes, row pitch) of a [T, top] matrix of expert ids."""
+    if ids.dim() != 2 or ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError("ids must be a [T, top] matrix of int32 or int64 "
+                        f"(it is {ids.dtype} of shape {tuple(ids.shape)})")
+    return ids.data_ptr(), 4 if ids.dtype is torch.int32 else 8, _ld("ids", ids)
+
+
+def _slots(slots, T):
+    if slots.dim() != 2 or slots.shape[0] != T or slots.dtype is not torch.int32 or \
+            not slots.is_contiguous():
+        raise ValueError(f"slots must be a contiguous int32 matrix of {T} rows (it is {slots.dtype} "
+                         f"of shape {tuple(slots.shape)})")
+    return slots.data_ptr()
+
+
+def _pair_weights(weights, slots):
+    """(pointer, dtype code, row pitch) of the weights of all pairs."""
+    if weights is None:
+        return 0, 0, 0
+    if weights.dtype not in _CODE:
+        raise TypeError("weights must be bfloat16, float16 or float32")
+    if weights.shape != slots.shape:
+        raise ValueError(f"weights must have the shape of slots, {tuple(slots.shape)} (they have "
+                         f"{tuple(weights.shape)})")
+    return weights.data_ptr(), _CODE[weights.dtype], _ld("weights", weights)
+
+
+_COPIED = (torch.bfloat16, torch.float16, torch.float32, torch.int8)
+
+
+def expert_dispatch(x: torch.Tensor, ids: torch.Tensor, experts: int, *, scales=None, out=None,
+                    out_scales=None, workspace=None, stream=None):
+    """Tokens to the rows of their experts, on the current CUDA device: the pairs (t, j)
+    that have an expert get the rows 0, 1, ... in the order of (expert, t, j).  Returns
+    (rows, offsets, slots): rows[slots[t, j]] = x[t], expert e owns the rows offsets[e] ..
+    offsets[e + 1] - 1, and slots[t, j] is -1 for a pair without a row.  With ``scales``
+    (fp32 [T], of int8 rows) the rows' scales come fourth.
+
+    x: [T, K] row-major, bf16, fp16, fp32 or int8; ids: int32 or int64 [T, top], the experts
+    that each token chose, negative for none (ids past the last expert are reported by
+    ``gemm_check_device_status`` and get no row).  ``out`` [T * top, K] and ``out_scales``
+    [T * top] are allocated when None; rows past the last expert's are not written.
+
+    The gradient of x is ``expert_combine(d_rows, slots)``.
+    """
+    if x.dtype not in _COPIED:
+        raise TypeError("x must be bfloat16, float16, float32 or int8")
+    if x.dim() != 2 or ids.dim() != 2 or ids.shape[0] != x.shape[0]:
+        raise ValueError(f"shape mismatch: x{tuple(x.shape)} ids{tuple(ids.shape)}")
+    if experts < 0:
+        raise ValueError("the number of experts must not be negative")
+    dev = x.get_device()
+    _wrong_device(dev, x=x, ids=ids, scales=scales, out=out, out_scales=out_scales,
+                  workspace=workspace)
+    _require_current(dev)
+    T, K = x.shape
+    top = ids.shape[1]
+    pi, id_bytes, ld_ids = _ids(ids)
+    ps = po = 0
+    if scales is not None:
+        if scales.dtype != torch.float32 or scales.shape != (T,) or not scales.is_contiguous():
+            raise ValueError(f"scales must be a contiguous fp32 vector of {T} values")
+        ps = scales.data_ptr()
+        out_scales = _out("out_scales", out_scales, (T * top,), None, x, (torch.float32,), stream)
+        if not out_scales.is_contiguous():
+            raise ValueError("out_scales must be contiguous")
+        po = out_scales.data_ptr()
+    elif out_scales is not None:
+        raise ValueError("out_scales needs scales")
+    out = _out("out", out, (T * top, K), None, x, (x.dtype,), stream)
+    offsets = _empty((experts + 1,), torch.int32, x, stream)
+    slots = _empty((T, top), torch.int32, x, stream)
+    ldx, ldo = _ld("x", x), _ld("out", out)
+    need = _fn("gemm_expert_dispatch_workspace_size")(T, top, experts) if workspace is None else 0
+    workspace, ws, ws_bytes = _scratch(workspace, need, x, stream)
+    st = _fn("gemm_expert_dispatch")(x.element_size(), T, K, x.data_ptr(), ldx, ps, id_bytes, pi,
+                                     ld_ids, top, experts, out.data_ptr(), ldo, po,
+                                     offsets.data_ptr(), slots.data_ptr(), ws, ws_bytes,
+                                     _raw_stream(dev) if stream is None else stream)
+    if st:
+        check(st)
+    return (out, offsets, slots) if scales is None else (out, offsets, slots, out_scales)
+
+
+def expert_combine(rows: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | None = None, *,
+                   out=None, out_dtype=None, stream=None) -> torch.Tensor:
+    """y[t] = sum_j weights[t, j] * rows[slots[t, j]], the experts' rows added up per token
+    (in fp32, j ascending, rounded once), on the current CUDA device.
+
+    rows: [R, K] row-major, bf16, fp16 or fp32; slots: int32 [T, top] of ``expert_dispatch``
+    (negative: no row, adds nothing); weights: [T, top] of any of the three types, or None:
+    ones.  The result is [T, K] in rows' dtype or fp32."""
+    code = _CODE.get(rows.dtype)
+    if code is None:
+        raise TypeError("rows must be bfloat16, float16 or float32")
+    if rows.dim() != 2 or slots.dim() != 2:
+        raise ValueError(f"shape mismatch: rows{tuple(rows.shape)} slots{tuple(slots.shape)}")
+    dev = rows.get_device()
+    _wrong_device(dev, rows=rows, slots=slots, weights=weights, out=out)
+    _require_current(dev)
+    R, K = rows.shape
+    T, top = slots.shape
+    psl = _slots(slots, T)
+    pw, w_dt, ldw = _pair_weights(weights, slots)
+    out = _out("out", out, (T, K), out_dtype, rows, (rows.dtype, torch.float32), stream)
+    st = _fn("gemm_expert_combine")(code, T, K, top, rows.data_ptr(), R, _ld("rows", rows), psl, pw,
+                                    w_dt, ldw, out.data_ptr(), _ld("out", out), _CODE[out.dtype],
+                                    _raw_stream(dev) if stream is None else stream)
+    if st:
+        check(st)
+    return out
+
+
+def expert_combine_grad(dy: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | None = None,
+                        *, rows=None, out=None, stream=None):
+    """The gradient of ``expert_combine``, in one pass over dy, on the current CUDA device:
+    (d_rows, d_weights) with d_rows[slots[t, j]] = weights[t, j] * dy[t] and d_weights[t, j] =
+    <dy[t], rows[slots[t, j]]>.
+
+    dy: [T, K] row-major, bf16, fp16 or fp32; slots and weights as in the forward call;
+    rows: the forward call's rows, or None: no gradient of the weights (None is returned for
+    it).  ``out`` is [R, K] in dy's dtype (allocated with T * top rows, or as many as
+    ``rows`` has, when None); rows that no pair names are not written.  d_weights has weights'
+    dtype (fp32 without weights)."""
+    code = _CODE.get(dy.dtype)
+    if code is None:
+        raise TypeError("dy must be bfloat16, float16 or float32")
+    if dy.dim() != 2 or slots.dim() != 2:
+        raise ValueError(f"shape mismatch: dy{tuple(dy.shape)} slots{tuple(slots.shape)}")
+    dev = dy.get_device()
+    _wrong_device(dev, dy=dy, slots=slots, weights=weights, rows=rows, out=out)
+    _require_current(dev)
+    T, K = dy.shape
+    psl = _slots(slots, T)
+    top = slots.shape[1]
+    pw, w_dt, ldw = _pair_weights(weights, slots)
+    if rows is not None:
+        if rows.dtype != dy.dtype:
+            raise TypeError("rows and dy must share one dtype")
+        if rows.dim() != 2 or rows.shape[1] != K:
+            raise ValueError(f"shape mismatch: dy{tuple(dy.shape)} rows{tuple(rows.shape)}")
+    R = rows.shape[0] if rows is not None else (T * top if out is None else out.shape[0])
+    out = _out("out", out, (R, K), None, dy, (dy.dtype,), stream)
+    d_weights, pr, ldr, pdw, dw_dt = None, 0, 0, 0, 0
+    if rows is not None:
+        d_weights = _empty((T, top), torch.float32 if weights is None else weights.dtype, dy, stream)
+        pr, ldr, pdw, dw_dt = rows.data_ptr(), _ld("rows", rows), d_weights.data_ptr(), \
+            _CODE[d_weights.dtype]
+    st = _fn("gemm_expert_combine_grad")(code, T, K, top, dy.data_ptr(), _ld("dy", dy), psl, pw,
+                                         w_dt, ldw, pr, R, ldr, out.data_ptr(), _ld("out", out),
+                                         pdw, dw_dt, max(top, 1),
+                                         _raw_stream(dev) if stream is None else stream)
+    if st:
+        check(st)
+    return out, d_weights
+
+
+def i8_quantize(x: torch.Tensor, *, out=None, out_scales=None, stream=None):
+    """(q, scales) with q = 127 x / max|x| to the nearest integer (ties to even) and scales =
+    max|x| / 127, row by row over the last dimension, on the current CUDA device: tokens
+    [T, K] over their features, weights [..., N, K] over the inputs of an output channel.
+
+    x: bf16, fp16 or fp32, its rows one after another at one distance.  A row of zeros has the
+    scale 0; a row with an infinity or a NaN has a NaN scale."""
+    code = _CODE.get(x.dtype)
+    if code is None:
+        raise TypeError("x must be bfloat16, float16 or float32")
+    if x.dim() < 2:
+        raise ValueError("x must have at least two dimensions")
+    dev = x.get_device()
+    _wrong_device(dev, x=x, out=out, out_scales=out_scales)
+    _require_current(dev)
+    out = _out("out", out, x.shape, None, x, (torch.int8,), stream)
+    out_scales = _out("out_scales", out_scales, x.shape[:-1], None, x, (torch.float32,), stream)
+    if not out_scales.is_contiguous():
+        raise ValueError("out_scales must be contiguous")
+    st = _fn("gemm_i8_quantize")(code, out_scales.numel(), x.shape[-1], x.data_ptr(),
+                                 _row_pitch("x", x), out.data_ptr(), _row_pitch("out", out),
+                                 out_scales.data_ptr(), _raw_stream(dev) if stream is None else stream)
+    if st:
+        check(st)
+    return out, out_scales
+
+
+def _row_pitch(name, t):
+    """Distance of neighbouring rows over all leading dimensions."""
+    ld = _ld(name, t)
+    if t.dim() == 2 or t.is_contiguous():
+        return ld
+    rows, step = t.shape[-2], ld * t.shape[-2]
+    if rows == 1:                           # (the rows are those of the dimension before)
+        ld = step = t.stride(-3) if t.shape[-3] > 1 else ld
+    for i in range(t.dim() - 3, -1, -1):
+        if t.shape[i] > 1 and t.stride(i) != step:
+            raise ValueError(f"{name}'s rows must lie at one distance (shape {tuple(t.shape)}, "
+                             f"strides {tuple(t.stride())})")
+        step *= t.shape[i]
+    return ld
+
+
+def i8_gemm(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, *, x_scales=None, offsets=None,
+            out=None, bias=None, epilogue=None, out_dtype=None, workspace=None,
+            stream=None) -> torch.Tensor:
+    """act((x @ q^T) * x_scales[:, None] * scales + bias) with 8-bit integers x and q and a
+    scale for each token and each output channel, on the current CUDA device.
+
+    x: [T, K] row-major, int8 with x_scales (fp32 [T]), or bf16, fp16 or fp32, which is
+    quantised row by row on the way as by ``i8_quantize``; q: int8 [N, K]; scales: fp32 [N].
+    With ``offsets`` (int32 [experts + 1]) q and scales carry a leading expert dimension and
+    rows offsets[e] .. offsets[e + 1] - 1 use expert e (rows of no expert are not written).
+    The result is bf16 (default for int8 x, else x's dtype), fp16 or fp32.
+
+    Sums are exact integers and the result is rounded once: a row's bits do not depend on the
+    call's other rows.  Rows of q on 16-byte boundaries are used in place, others copied."""
+    given = x.dtype is torch.int8
+    if not given and x.dtype not in _CODE:
+        raise TypeError("x must be int8, bfloat16, float16 or float32")
+    if given != (x_scales is not None):
+        raise ValueError("int8 x needs x_scales" if given else "x_scales belong to int8 x")
+    if q.dtype is not torch.int8 or scales.dtype is not torch.float32:
+        raise TypeError("q must be int8 and scales float32")
+    lead = 3 if offsets is not None else 2
+    if x.dim() != 2 or q.dim() != lead or q.shape[-1] != x.shape[1] or scales.shape != q.shape[:-1]:
+        raise ValueError(f"shape mismatch: x{tuple(x.shape)} q{tuple(q.shape)} "
+                         f"scales{tuple(scales.shape)} "
+                         f"({'with' if lead == 3 else 'without'} offsets)")
+    dev = x.get_device()
+    _wrong_device(dev, x=x, q=q, scales=scales, x_scales=x_scales, offsets=offsets, out=out,
+                  bias=bias, workspace=workspace)
+    _require_current(dev)
+    T, K = x.shape
+    groups = q.shape[0] if lead == 3 else 1
+    N = q.shape[-2]
+    if given and (x_scales.dtype is not torch.float32 or x_scales.shape != (T,) or
+                  not x_scales.is_contiguous()):
+        raise ValueError(f"x_scales must be a contiguous fp32 vector of {T} values")
+    if N > 1 and scales.stride(-1) != 1:
+        raise ValueError("scales must have unit inner stride")
+    kinds = (torch.bfloat16, torch.float16, torch.float32)
+    if out is None and out_dtype is None and not given:
+        out_dtype = x.dtype
+    out = _out("out", out, (T, N), out_dtype, x, kinds, stream)
+    epi, bias_ptr, stride_bias = _epilogue(epilogue, bias, groups, N)
+    off = _offsets(offsets, groups) if offsets is not None else 0
+    ldx, ldq, ldo = _ld("x", x), _ld("q", q), _ld("out", out)
+    stride_q, stride_s = (q.stride(0), scales.stride(0)) if groups > 1 else (0, 0)
+    dt = 3 if given else _CODE[x.dtype]
+    pq = q.data_ptr()
+    need = 0
+    if workspace is None:
+        need = _fn("gemm_i8_workspace_size")(dt, groups, T, N, K, pq, ldq, stride_q)
+    workspace, ws, ws_bytes = _scratch(workspace, need, x, stream)
+    st = _fn("gemm_i8")(dt, groups, T, N, K, x.data_ptr(), ldx, x_scales.data_ptr() if given else 0,
+                        pq, ldq, stride_q, scales.data_ptr(), stride_s, out.data_ptr(), ldo,
+                        _CODE[out.dtype], off, bias_ptr, stride_bias, epi, ws, ws_bytes,
+                        _raw_stream(dev) if stream is None else stream)
+    if st:
+        check(st)
+    return out

@@ -70,7 +70,8 @@ typedef void* gemm_stream_t;
 
 typedef enum { GEMM_ROW_MAJOR = 0, GEMM_COL_MAJOR = 1 } gemm_layout_t;
 
-typedef enum { GEMM_DT_BF16 = 0, GEMM_DT_F16 = 1, GEMM_DT_F32 = 2 } gemm_dtype_t;
+/* GEMM_DT_I8 is an operand of gemm_i8 (gemm_experts.h); the products here refuse it. */
+typedef enum { GEMM_DT_BF16 = 0, GEMM_DT_F16 = 1, GEMM_DT_F32 = 2, GEMM_DT_I8 = 3 } gemm_dtype_t;
 
 /*
  * Epilogue: C = act(alpha*A@B + beta*C + bias), applied once after the K loop

@@ -1,0 +1,407 @@
+"""Rows quantised to 8 bits and products of 8-bit integers on the GPU, against plain 64-bit
+references: the integers and the sums exactly, results without bias bit for bit."""
+import numpy as np
+import pytest
+import torch
+
+import dense_gemm_bf16_gb300 as dg
+import experts_ref
+import routing_ref as ref
+from routing_ref import HALF_STEP, TINIEST
+
+pytestmark = pytest.mark.gpu
+
+BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
+DEV = "cuda:0"
+
+
+def status():
+    return dg.gemm_check_device_status(torch.cuda.current_stream().cuda_stream)
+
+
+def offs(bounds):
+    return torch.tensor(bounds, dtype=torch.int32, device=DEV)
+
+
+def bounds_of(counts, start=0):
+    return [start + int(v) for v in np.concatenate(([0], np.cumsum(counts)))]
+
+
+# ---------------------------------------------------------------- quantise
+
+def quantized_exactly(x, q, s):
+    want, scales = ref.quantize(x)
+    assert np.array_equal(q.cpu().numpy(), want)
+    got = experts_ref.f64(s)
+    assert np.array_equal(np.isnan(got), np.isnan(scales))
+    ok = ~np.isnan(scales)
+    assert np.array_equal(got[ok], scales[ok].astype(np.float32).astype(np.float64))
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+@pytest.mark.parametrize("T,K", [(1, 1), (3, 7), (5, 64), (64, 255), (33, 1024), (9, 4096), (1001, 130),
+                                 (2, 8192), (3, 8200), (2, 40001), (700, 2048), (4, 16384)])
+def test_quantize(T, K, dtype):
+    rng = np.random.default_rng(T * 31 + K)
+    x = rng.standard_normal((T, K)) * np.exp(2 * rng.standard_normal((T, 1)))
+    x = torch.from_numpy(x.astype(np.float32)).to(dtype)
+    q, s = dg.i8_quantize(x.to(DEV))
+    quantized_exactly(x, q, s)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+def test_quantize_borders_and_ties(dtype):
+    """Rows whose largest magnitude is 127 times a power of two, with every half integer and
+    its neighbours among the elements, both signs."""
+    half = torch.arange(0, 127, dtype=torch.float64) + 0.5
+    rows = []
+    for e in (-8, -1, 0, 3):
+        v = half.to(dtype)
+        bits = v.view(torch.int32 if dtype == F32 else torch.int16)
+        near = [v, (bits + 1).view(dtype), (bits - 1).view(dtype)]
+        v = torch.cat(near + [-n for n in near] + [torch.full((2,), 127.0, dtype=dtype)])
+        rows.append((v.double() * 2.0 ** e).to(dtype))
+    x = torch.stack(rows)
+    q, s = dg.i8_quantize(x.to(DEV))
+    quantized_exactly(x, q, s)
+
+
+@pytest.mark.parametrize("top", [3.3895e38, 1e37, 1e-10, 1e-30, 1.1e-38, 3e-42, 1.4e-45])
+def test_quantize_extreme_rows(top):
+    rng = np.random.default_rng(1)
+    x = rng.uniform(-1, 1, (4, 300))
+    x[:, 0] = 1.0
+    with np.errstate(over="ignore"):
+        x = torch.from_numpy((x * top).astype(np.float32))
+    for dtype in (F32, BF):
+        v = x.to(dtype)
+        q, s = dg.i8_quantize(v.to(DEV))
+        quantized_exactly(v, q, s)
+
+
+def test_quantize_zero_nan_and_infinite_rows():
+    x = torch.randn((6, 500))
+    x[1], x[2, 7], x[3, 499], x[4, 0] = 0.0, float("nan"), float("inf"), -float("inf")
+    for dtype in (BF, HF, F32):
+        q, s = dg.i8_quantize(x.to(dtype).to(DEV))
+        quantized_exactly(x.to(dtype), q, s)
+        assert s[1] == 0 and torch.isnan(s[2:5]).all() and not torch.isnan(s[[0, 1, 5]]).any()
+
+
+def test_quantize_views_and_leading_dimensions():
+    rng = np.random.default_rng(2)
+    w = torch.from_numpy(rng.standard_normal((3, 5, 48)).astype(np.float32))
+    q, s = dg.i8_quantize(w.to(DEV))
+    assert q.shape == (3, 5, 48) and s.shape == (3, 5)
+    quantized_exactly(w, q, s)
+    wide = w.to(DEV).to(BF)
+    for view in (wide[:, :, 3:40], wide[:, 1:2], wide[:, :1, 5:6]):
+        q, s = dg.i8_quantize(view)
+        quantized_exactly(view.cpu(), q, s)
+    with pytest.raises(ValueError, match="distance"):
+        dg.i8_quantize(wide[:, :3])
+    out = torch.full((5, 60), 9, dtype=torch.int8, device=DEV)
+    dg.i8_quantize(wide[0], out=out[:, 7:55])
+    quantized_exactly(wide[0].cpu(), out[:, 7:55], dg.i8_quantize(wide[0])[1])
+    assert bool((out[:, :7] == 9).all()) and bool((out[:, 55:] == 9).all())
+    assert dg.i8_quantize(wide[0, :0])[0].shape == (0, 48)
+    assert dg.i8_quantize(wide[0, :, :0])[1].tolist() == [0.0] * 5
+
+
+# ---------------------------------------------------------------- products
+
+def case(rng, T, N, K, experts=0, full=False):
+    lead = (experts,) if experts else ()
+    if full:                                     # the largest magnitudes there are
+        x = rng.choice([-128, 127], (T, K)).astype(np.int8)
+        q = rng.choice([-128, 127], lead + (N, K)).astype(np.int8)
+    else:
+        x = rng.integers(-128, 128, (T, K)).astype(np.int8)
+        q = rng.integers(-128, 128, lead + (N, K)).astype(np.int8)
+    sx = rng.uniform(0.5, 1.5, T).astype(np.float32) * 0.01
+    sw = rng.uniform(0.5, 1.5, lead + (N,)).astype(np.float32) * 0.01
+    return x, q, sx, sw
+
+
+def run(x, q, sx, sw, **kw):
+    to = lambda v: torch.from_numpy(v).to(DEV)  # noqa: E731
+    return dg.i8_gemm(to(x), to(q), to(sw), x_scales=to(sx), **kw)
+
+
+def equal_bits(got, x, q, sx, sw, offsets=None):
+    want = ref.i8_bits(ref.integer_sums(x, q, offsets), sx, sw, got.dtype, offsets)
+    rows = slice(0, x.shape[0]) if offsets is None else slice(offsets[0], offsets[-1])
+    assert torch.equal(got.cpu()[rows], want[rows])
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 128, 128), (1, 1, 16), (2, 130, 48), (16, 128, 128), (17, 300, 256),
+                                   (32, 128, 1024), (33, 129, 1040), (64, 256, 2048), (1, 1000, 4096),
+                                   (5, 72, 8192), (65, 136, 640), (100, 1000, 272), (129, 128, 1152)])
+@pytest.mark.parametrize("out", [BF, HF, F32])
+def test_products(T, N, K, out):
+    rng = np.random.default_rng(T * 1000 + N + K)
+    c = case(rng, T, N, K)
+    equal_bits(run(*c, out_dtype=out), *c)
+    assert status() == 0
+
+
+@pytest.mark.parametrize("T,N,K", [(200, 2000, 300), (700, 3000, 1100), (1500, 1016, 2064), (385, 5003, 160)])
+def test_products_on_pairs(T, N, K):
+    rng = np.random.default_rng(T)
+    c = case(rng, T, N, K)
+    equal_bits(run(*c, out_dtype=F32), *c)
+    assert status() == 0
+
+
+@pytest.mark.parametrize("T,N", [(3, 200), (70, 200), (260, 5000)])
+@pytest.mark.parametrize("K", [1024, 1025, 2048, 4096, 16400])
+def test_sums_are_exact_at_full_magnitude(T, N, K):
+    """Sums past what fp32 holds: all products +-2^14 or near, some rows with one sign."""
+    rng = np.random.default_rng(K + T)
+    x, q, sx, sw = case(rng, T, N, K, full=True)
+    x[0], q[0], q[1] = -128, -128, 127
+    x[1] = 127
+    x[2, ::2], x[2, 1::2] = 127, -128
+    sx[:], sw[:] = 1.0, 1.0
+    got = run(x, q, sx, sw, out_dtype=F32)
+    equal_bits(got, x, q, sx, sw)
+
+
+def test_the_longest_contraction():
+    rng = np.random.default_rng(9)
+    K = 131071
+    x, q, sx, sw = case(rng, 3, 5, K, full=True)
+    x[0], q[0] = -128, -128                     # 2^31 - 2^14
+    sx[:], sw[:] = 1.0, 1.0
+    equal_bits(run(x, q, sx, sw, out_dtype=F32), x, q, sx, sw)
+    with pytest.raises(dg.GemmError):
+        run(np.zeros((1, K + 1), np.int8), np.zeros((1, K + 1), np.int8), sx[:1], sw[:1])
+
+
+COUNTS = [[1], [1, 0, 1, 1, 0, 0, 1], [3, 0, 31, 32, 33, 1], [0, 100, 129, 64, 127, 128, 0],
+          [255, 256, 257, 0, 513, 40], [(7 * i) % 5 for i in range(100)], [0, 0, 0], [2] * 40, [64, 0, 300]]
+
+
+@pytest.mark.parametrize("i", range(len(COUNTS)))
+@pytest.mark.parametrize("K,N", [(200, 264), (1296, 136)])
+def test_experts(i, K, N):
+    rng = np.random.default_rng(i * 10 + K)
+    counts = COUNTS[i]
+    b = bounds_of(counts, 2)                    # rows of no expert before and after
+    T = b[-1] + 3
+    x, q, sx, sw = case(rng, T, N, K, len(counts))
+    out = torch.full((T, N), 7.0, dtype=F32, device=DEV)
+    got = run(x, q, sx, sw, offsets=offs(b), out=out)
+    assert got is out
+    equal_bits(got, x, q, sx, sw, b)
+    assert bool((out[:2] == 7).all()) and bool((out[b[-1]:] == 7).all())
+    assert status() == 0
+
+
+@pytest.mark.parametrize("counts,N", [([700, 0, 900, 1000], 3000), ([300] * 8, 1000), ([2500, 3], 2056)])
+@pytest.mark.parametrize("out", [BF, F32])
+def test_experts_on_pairs(counts, N, out):
+    rng = np.random.default_rng(N)
+    b = bounds_of(counts)
+    c = case(rng, b[-1], N, 272, len(counts))
+    equal_bits(run(*c, offsets=offs(b), out_dtype=out), *c, b)
+
+
+@pytest.mark.parametrize("K", [1, 3, 15, 17, 63, 65, 127, 130, 1001])
+@pytest.mark.parametrize("experts", [0, 3])
+def test_odd_contractions(K, experts):
+    """Rows of weights that no 16-byte boundary divides are copied."""
+    rng = np.random.default_rng(K)
+    b = bounds_of([20, 0, 30]) if experts else None
+    c = case(rng, 50, 70, K, experts)
+    equal_bits(run(*c, out_dtype=F32, offsets=None if b is None else offs(b)), *c, b)
+
+
+def test_strides_and_broadcast():
+    rng = np.random.default_rng(5)
+    b = bounds_of([30, 90, 0, 7])
+    T, K, N = b[-1], 100, 80
+    x, q, sx, sw = case(rng, T, N, K, 4)
+    to = lambda v: torch.from_numpy(v).to(DEV)  # noqa: E731
+    xp = to(np.pad(x, ((0, 0), (3, 5))))[:, 3:3 + K]
+    outs = []
+    for left, right in ((0, 12), (16, 12), (1, 0)):  # in place, in place, copied
+        qp = to(np.pad(q, ((0, 0), (0, 0), (left, right))))[:, :, left:left + K]
+        sp = to(np.pad(sw, ((0, 0), (2, 1))))[:, 2:2 + N]
+        C = torch.full((T, N + 5), 3.0, dtype=HF, device=DEV)
+        dg.i8_gemm(xp, qp, sp, x_scales=to(sx), offsets=offs(b), out=C[:, 2:2 + N])
+        equal_bits(C[:, 2:2 + N], x, q, sx, sw, b)
+        assert bool((C[:, :2] == 3).all()) and bool((C[:, 2 + N:] == 3).all())
+        outs.append(C)
+    q1, s1 = to(q[0]), to(sw[0])
+    got = dg.i8_gemm(xp, q1.expand(4, N, K), s1.expand(4, N), x_scales=to(sx), offsets=offs(b))
+    equal_bits(got, x, np.broadcast_to(q[0], q.shape), sx, np.broadcast_to(sw[0], sw.shape), b)
+
+
+@pytest.mark.parametrize("epilogue", ["bias", "gelu_tanh", "bias_gelu_tanh", "bias_relu", "bias_gelu_erf"])
+@pytest.mark.parametrize("per_expert", [False, True])
+@pytest.mark.parametrize("T,N", [(40, 72), (900, 1500)])
+def test_epilogues(epilogue, per_expert, T, N):
+    """Before the activation the value is within 2^-22 of its parts' magnitudes (four fp32
+    roundings: sum, two scales, bias); GELU's slope is below 1.13 and its own evaluation
+    within 2^-20 of the value and its argument."""
+    rng = np.random.default_rng(T)
+    b = bounds_of([T // 4, 0, T - T // 4])
+    x, q, sx, sw = case(rng, T, N, 160, 3)
+    sw *= 0.05
+    bias = rng.standard_normal((3, N) if per_expert else (N,)).astype(np.float32)
+    use = bias if epilogue.startswith("bias") else None
+    got = run(x, q, sx, sw, offsets=offs(b), out_dtype=F32, epilogue=epilogue,
+              bias=None if use is None else torch.from_numpy(use).to(DEV))
+    want, size = ref.i8(ref.integer_sums(x, q, b), sx, sw, b, use, epilogue)
+    assert np.all(np.abs(experts_ref.f64(got) - want) <=
+                  1.13 * 2.0 ** -22 * size + 2.0 ** -20 * (size + np.abs(want)))
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+@pytest.mark.parametrize("T,N,K", [(1, 300, 2048), (20, 130, 1001), (500, 1500, 320), (3, 64, 9000)])
+def test_tokens_quantised_on_the_way(T, N, K, dtype):
+    """The same bits as i8_quantize and the product of its integers."""
+    rng = np.random.default_rng(K)
+    x = torch.from_numpy((rng.standard_normal((T, K)) * 3).astype(np.float32)).to(dtype).to(DEV)
+    _, q, _, sw = case(rng, 1, N, K)
+    q, sw = torch.from_numpy(q).to(DEV), torch.from_numpy(sw).to(DEV)
+    xi, sx = dg.i8_quantize(x)
+    got = dg.i8_gemm(x, q, sw)
+    assert got.dtype == dtype
+    assert torch.equal(got, dg.i8_gemm(xi, q, sw, x_scales=sx, out_dtype=dtype))
+    equal_bits(got, xi.cpu().numpy(), q.cpu().numpy(), sx.cpu().numpy(), sw.cpu().numpy())
+
+
+def test_rows_do_not_mix_and_do_not_depend_on_their_number():
+    """A NaN scale stays in its row (or channel); a row's bits are the same alone, in every
+    form of the kernel, as an expert's row and in a batch."""
+    rng = np.random.default_rng(6)
+    T, N, K = 900, 1400, 2320
+    x, q, sx, sw = case(rng, T, N, K)
+    full = run(x, q, sx, sw, out_dtype=F32)
+    for n in (1, 20, 50, 100, 300):
+        assert torch.equal(run(x[:n], q, sx[:n], sw, out_dtype=F32), full[:n])
+    lone = run(x[7:8], q[:100], sx[7:8], sw[:100], out_dtype=F32)
+    assert torch.equal(lone, full[7:8, :100])
+    b = [0, 5, 300, 300, 900]
+    assert torch.equal(run(x, np.stack([q] * 4), sx, np.stack([sw] * 4), offsets=offs(b), out_dtype=F32), full)
+    sx2, sw2 = sx.copy(), sw.copy()
+    sx2[13], sw2[21] = np.nan, np.inf
+    got = run(x, q, sx2, sw2, out_dtype=F32)
+    keep = [i for i in range(T) if i != 13]
+    cols = [i for i in range(N) if i != 21]
+    assert torch.equal(got[keep][:, cols], full[keep][:, cols]) and torch.isnan(got[13]).all()
+
+
+def test_empty():
+    q, sw = torch.zeros((24, 64), dtype=torch.int8, device=DEV), torch.ones(24, device=DEV)
+    x = torch.ones((5, 64), dtype=BF, device=DEV)
+    assert dg.i8_gemm(x[:0], q, sw).shape == (0, 24)
+    assert dg.i8_gemm(x, q[:0], sw[:0]).shape == (5, 0)
+    bias = torch.randn(24, device=DEV)
+    got = dg.i8_gemm(x[:, :0], q[:, :0], sw, bias=bias, out_dtype=F32)
+    assert torch.equal(got, bias.expand(5, 24))
+    C = torch.full((5, 24), 7.0, dtype=BF, device=DEV)
+    dg.i8_gemm(x, q[None][:0], sw[None][:0], offsets=offs([0]), out=C)
+    assert bool((C == 7).all())
+
+
+@pytest.mark.parametrize("bad", [[0, 5, 3, 10], [0, 5, 8, 11], [-1, 5, 8, 10], [4, 3, 2, 1]])
+def test_bad_offsets_are_reported_and_touch_nothing_else(bad):
+    rng = np.random.default_rng(10)
+    x, q, sx, sw = case(rng, 10, 40, 64, 3)
+    C = torch.full((12, 40), 5.0, dtype=F32, device=DEV)
+    run(x, q, sx, sw, offsets=offs(bad), out=C[:10])
+    assert status() == dg.Status.ERR_INVALID_ARG
+    assert status() == 0
+    assert bool((C[10:] == 5).all())
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 300, 8192), (20, 3000, 1024), (50, 3000, 512), (100, 8000, 512),
+                                   (700, 3000, 1100)])
+def test_a_stalled_pipeline_reports_a_timeout_and_recovers(T, N, K):
+    rng = np.random.default_rng(11)
+    c = case(rng, T, N, K)
+    good = run(*c, out_dtype=F32)
+    dg.gemm_set_option(dg.Option.TIMEOUT_US, 2000)
+    dg.gemm_set_option(dg.Option.TEST_STALL, 1)
+    try:
+        run(*c, out_dtype=F32)
+        assert status() == dg.Status.ERR_TIMEOUT
+    finally:
+        dg.gemm_set_option(dg.Option.TEST_STALL, 0)
+        dg.gemm_set_option(dg.Option.TIMEOUT_US, 2000000)
+    assert status() == 0
+    assert torch.equal(run(*c, out_dtype=F32), good)
+
+
+@pytest.mark.parametrize("cap", [1, 5])
+def test_the_cap_on_ctas(cap):
+    rng = np.random.default_rng(13)
+    for T, N, K in ((1, 1000, 4096), (600, 2000, 300)):
+        c = case(rng, T, N, K)
+        free = run(*c, out_dtype=F32)
+        dg.gemm_set_option(dg.Option.MAX_CTAS, cap)
+        try:
+            assert torch.equal(run(*c, out_dtype=F32), free)
+        finally:
+            dg.gemm_set_option(dg.Option.MAX_CTAS, 0)
+
+
+def test_graph_replay_side_stream_and_workspace():
+    rng = np.random.default_rng(14)
+    x, q, sx, sw = case(rng, 90, 200, 700)
+    xd = torch.randn((90, 700), device=DEV).to(BF)
+    qd, sd = torch.from_numpy(q).to(DEV), torch.from_numpy(sw).to(DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        y = dg.i8_gemm(xd, qd, sd)
+    side.synchronize()
+    assert torch.equal(y, dg.i8_gemm(xd, qd, sd))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = dg.i8_gemm(xd, qd, sd)
+    for _ in range(3):
+        xd.normal_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, dg.i8_gemm(xd, qd, sd))
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device=DEV)
+    assert torch.equal(y, dg.i8_gemm(xd, qd, sd, workspace=ws))
+    with pytest.raises(dg.GemmError):
+        dg.i8_gemm(xd, qd, sd, workspace=ws[:1024])
+
+
+def test_the_operators_together():
+    """An expert layer in 8 bits: quantise, dispatch the integers, two products, combine;
+    against the definition in 64 bits on the same integers."""
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    T, D, H, E, top = 70, 192, 320, 12, 3
+    x = torch.randn((T, D), generator=gen, device=DEV).to(BF)
+    w1 = torch.randn((E, H, D), generator=gen, device=DEV) * D ** -0.5
+    w2 = torch.randn((E, D, H), generator=gen, device=DEV) * H ** -0.5
+    q1, s1 = dg.i8_quantize(w1)
+    q2, s2 = dg.i8_quantize(w2.to(BF))
+    share, ids = torch.softmax(torch.randn((T, E), generator=gen, device=DEV), -1).topk(top)
+    xi, xs = dg.i8_quantize(x)
+    rows, offsets, slots, rs = dg.expert_dispatch(xi, ids, E, scales=xs)
+    h = dg.i8_gemm(rows, q1, s1, x_scales=rs, offsets=offsets, epilogue="gelu_tanh")
+    y2 = dg.i8_gemm(h, q2, s2, offsets=offsets)
+    y = dg.expert_combine(y2, slots, share, out_dtype=F32)
+    hi, hs = dg.i8_quantize(h)
+    want = np.zeros((T, D))
+    f = experts_ref.f64
+    for t in range(T):
+        for j in range(top):
+            e, s = int(ids[t, j]), int(slots[t, j])
+            a = (f(q1[e]) @ f(xi[t])) * f(xs[t]) * f(s1[e])
+            g = experts_ref.gelu_tanh(a)
+            assert np.all(np.abs(f(h[s]) - g) <= 2.0 ** -8 * np.abs(g) + 2.0 ** -19 * (np.abs(a) + np.abs(g)))
+            b = (f(q2[e]) @ f(hi[s])) * f(hs[s]) * f(s2[e])
+            assert np.all(np.abs(f(y2[s]) - b) <= (2.0 ** -8 + 2.0 ** -22) * np.abs(b))
+            want[t] += f(share[t, j]) * f(y2[s])
+    size = ref.combine(y2, slots.cpu().numpy(), share)[1]
+    assert np.all(np.abs(f(y) - want) <= (top + 2) * 2.0 ** -24 * size)
+    assert status() == 0
