@@ -283,9 +283,6 @@ __device__ __forceinline__ void i8_convert(const I8Params& p, const I8Cta& x, in
             uint4 v[8];
 #pragma unroll
             for (int c = 0; c < 8; ++c) v[c] = i8_ld_shared(src + ((c << 4) ^ swz));
-            __syncwarp();
-            if (x.lane == 0) mbar_arrive(x.aempty + 8u * in.at);
-            in.next();
             ok = rg_all_wait(x.wempty + 8u * out.at, out.phase ^ 1u, p.g, x.abort_flag);
             if (!ok) break;
             tc_fence_after_sync();
@@ -304,6 +301,11 @@ __device__ __forceinline__ void i8_convert(const I8Params& p, const I8Cta& x, in
             tmem_st_wait();
             tc_fence_before_sync();
             __syncwarp();
+            // (the stage goes back only now that its values have been used: an arrival right
+            // behind the loads overtook them where the epilogue's stores held them up, and
+            // the next copy overwrote what single lanes had still to read)
+            if (x.lane == 0) mbar_arrive(x.aempty + 8u * in.at);
+            in.next();
             if (x.lane == 0) {
                 const uint32_t bar = x.wfull + 8u * out.at;
                 if (CG == 2)

@@ -178,6 +178,20 @@ def test_the_longest_contraction():
         run(np.zeros((1, K + 1), np.int8), np.zeros((1, K + 1), np.int8), sx[:1], sw[:1])
 
 
+@pytest.mark.parametrize("T,N,K", [(1500, 4096, 4096), (900, 8192, 2048), (2000, 8192, 1024), (100, 30000, 2048),
+                                   (20, 40000, 4096)])
+def test_many_tiles_a_cta(T, N, K):
+    """Tiles whose output leaves while the next one's weights are on their way: the stages
+    come round many times under load.  (Sums below 2^53 are exact in 64 bits.)"""
+    gen = torch.Generator(device=DEV).manual_seed(K)
+    x = torch.randint(-128, 128, (T, K), generator=gen, device=DEV, dtype=torch.int8)
+    q = torch.randint(-128, 128, (N, K), generator=gen, device=DEV, dtype=torch.int8)
+    want = (x.double() @ q.double().T).float()
+    for _ in range(4):
+        assert torch.equal(dg.i8_gemm(x, q, torch.ones(N, device=DEV), x_scales=torch.ones(T, device=DEV),
+                                      out_dtype=F32), want)
+
+
 COUNTS = [[1], [1, 0, 1, 1, 0, 0, 1], [3, 0, 31, 32, 33, 1], [0, 100, 129, 64, 127, 128, 0],
           [255, 256, 257, 0, 513, 40], [(7 * i) % 5 for i in range(100)], [0, 0, 0], [2] * 40, [64, 0, 300]]
 
