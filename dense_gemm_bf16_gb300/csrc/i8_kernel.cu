@@ -135,10 +135,37 @@ __device__ __forceinline__ bool i8_try_wait_cluster(uint32_t bar, uint32_t parit
     return ok != 0;
 }
 
+// Has the phase completed?  (Does not wait; the result is used later, so that the answer is
+// on its way while other work is issued.)  One lane asks, the others say yes.
+__device__ __forceinline__ bool i8_peek(uint32_t bar, uint32_t parity, int lane) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.eq.s32 q, %3, 0;\n\t"
+        "setp.eq.s32 p, 0, 0;\n\t"
+        "@q mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(lane)
+        : "memory");
+    return ok != 0;
+}
+
+// Bounded wait of a whole warp, of which `seen` says that it may have ended already.  One
+// lane polls; the result comes from votes, so that the compiler knows it to be the same in
+// all lanes (see i8_issue).
+__device__ __forceinline__ bool i8_wait(bool seen, uint32_t bar, uint32_t parity, const I8Params& p,
+                                        const I8Cta& x) {
+    if (__all_sync(0xffffffffu, seen)) return true;
+    bool ok = true;
+    if (x.lane == 0) ok = mbar_wait_short(bar, parity, x.abort_flag, p.g.status, p.g.timeout_ns);
+    return __all_sync(0xffffffffu, ok) != 0;
+}
+
 // Stages of a tile's contraction that this CTA takes.
 template <bool SPLIT>
-__device__ __forceinline__ void i8_range(const I8Params& p, const I8Cta& x, int klen, int& s0, int& s1) {
-    const int steps = (klen + 127) / 128;
+__device__ __forceinline__ void i8_range(const I8Params& p, const I8Cta& x, int& s0, int& s1) {
+    const int steps = (p.g.K + 127) / 128;
     s0 = SPLIT ? static_cast<int>(static_cast<int64_t>(steps) * x.rank / p.splits) : 0;
     s1 = SPLIT ? static_cast<int>(static_cast<int64_t>(steps) * (x.rank + 1) / p.splits) : steps;
 }
@@ -178,9 +205,9 @@ __device__ __forceinline__ void i8_load_weights(const I8Params& p, const I8Cta& 
     bool ok = true;
     for (int t = x.cl; ok && rg_tile<CG, BT, RG_ROWS>(p.g, walk, t, x.lane, SPLIT ? 0u : x.rank, w); t += x.ncl) {
         int s0, s1;
-        i8_range<SPLIT>(p, x, w.klen, s0, s1);
+        i8_range<SPLIT>(p, x, s0, s1);
         for (int s = s0; s < s1; ++s) {
-            ok = rg_all_wait(x.aempty + 8u * ring.at, ring.phase ^ 1u, p.g, x.abort_flag);
+            ok = rg_warp_wait(x.aempty + 8u * ring.at, ring.phase ^ 1u, x.lane, x.abort_flag, p.g);
             if (p.g.test_stall == 1 && armed == 0) ok = false;  // test only: the others' bounded waits must expire
             if (!ok) break;
             if (x.lane == 0) {
@@ -217,9 +244,9 @@ __device__ __forceinline__ void i8_load_tokens(const I8Params& p, const I8Cta& x
         const int nb = big ? 1 : (rows_b + 31) / 32;
         const uint32_t bytes = big ? C::B_BYTES : nb * 8192u;
         int s0, s1;
-        i8_range<SPLIT>(p, x, w.klen, s0, s1);
+        i8_range<SPLIT>(p, x, s0, s1);
         for (int s = s0; s < s1; ++s) {
-            ok = rg_all_wait(x.bempty + 8u * ring.at, ring.phase ^ 1u, p.g, x.abort_flag);
+            ok = rg_warp_wait(x.bempty + 8u * ring.at, ring.phase ^ 1u, x.lane, x.abort_flag, p.g);
             if (!ok) break;
             if (x.lane == 0) {
                 const uint32_t fb = x.bfull + 8u * ring.at;
@@ -272,18 +299,19 @@ __device__ __forceinline__ void i8_convert(const I8Params& p, const I8Cta& x, in
     RgTile w;
     I8Ring<C::SA> in;
     I8Ring<C::TA> out;
-    bool ok = true;
+    bool ok = true, seen_a = false;
     for (int t = x.cl; ok && rg_tile<CG, BT, RG_ROWS>(p.g, walk, t, x.lane, SPLIT ? 0u : x.rank, w); t += x.ncl) {
         int s0, s1;
-        i8_range<SPLIT>(p, x, w.klen, s0, s1);
+        i8_range<SPLIT>(p, x, s0, s1);
         for (int s = s0; s < s1; ++s) {
-            ok = rg_all_wait(x.afull + 8u * in.at, in.phase, p.g, x.abort_flag);
+            const bool seen_w = i8_peek(x.wempty + 8u * out.at, out.phase ^ 1u, x.lane);
+            ok = i8_wait(seen_a, x.afull + 8u * in.at, in.phase, p, x);
             if (!ok) break;
             const uint32_t src = a_row + in.at * C::A_BYTES;
             uint4 v[8];
 #pragma unroll
             for (int c = 0; c < 8; ++c) v[c] = i8_ld_shared(src + ((c << 4) ^ swz));
-            ok = rg_all_wait(x.wempty + 8u * out.at, out.phase ^ 1u, p.g, x.abort_flag);
+            ok = i8_wait(seen_w, x.wempty + 8u * out.at, out.phase ^ 1u, p, x);
             if (!ok) break;
             tc_fence_after_sync();
 #pragma unroll
@@ -304,21 +332,28 @@ __device__ __forceinline__ void i8_convert(const I8Params& p, const I8Cta& x, in
             // (the stage goes back only now that its values have been used: an arrival right
             // behind the loads overtook them where the epilogue's stores held them up, and
             // the next copy overwrote what single lanes had still to read)
-            if (x.lane == 0) mbar_arrive(x.aempty + 8u * in.at);
-            in.next();
             if (x.lane == 0) {
                 const uint32_t bar = x.wfull + 8u * out.at;
+                // (nothing but tensor memory is handed over, which the fence above orders: a
+                // release at cluster scope took 500 to 1500 clocks here)
                 if (CG == 2)
-                    mbar_arrive_remote(mapa_shared(bar, 0u));
+                    mbar_arrive_relaxed(mapa_shared(bar, 0u));
                 else
                     mbar_arrive(bar);
+                mbar_arrive(x.aempty + 8u * in.at);
             }
+            in.next();
             out.next();
+            seen_a = i8_peek(x.afull + 8u * in.at, in.phase, x.lane);
         }
     }
 }
 
 // ------------------------------------------------ MMA issuer (a warp; of the pair's leader)
+// The whole warp walks tiles and stages, every branch decided by a vote and every position
+// made uniform, and one lane issues: operands of the tensor-core instructions are then in
+// uniform registers.  (With branches that the compiler took for divergent, an MMA took 67
+// clocks to issue, whatever its size, a commit 100, and a stage 1200 in all.)
 template <int CG, int BT, bool SPLIT>
 __device__ __forceinline__ void i8_issue(const I8Params& p, const I8Cta& x) {
     using C = I8Cfg<CG, BT, SPLIT>;
@@ -331,45 +366,53 @@ __device__ __forceinline__ void i8_issue(const I8Params& p, const I8Cta& x) {
     I8Ring<C::TA> wr;
     I8Ring<C::SB> br;
     I8Ring<2> acc;
-    bool ok = true, issued = false;
+    bool ok = true, issued = false, seen_b = false, seen_w = false;
     auto commit = [&](uint32_t bar) {
         if constexpr (CG == 2)
             umma_commit_mc_cg<CG>(bar, kPair);
         else
             umma_commit_cg<CG>(bar);
     };
-    for (int t = x.cl; ok && rg_tile<CG, BT, RG_ROWS>(p.g, walk, t, x.lane, SPLIT ? 0u : x.rank, w); t += x.ncl) {
-        int s0, s1;
-        i8_range<SPLIT>(p, x, w.klen, s0, s1);
+    int s0, s1;
+    i8_range<SPLIT>(p, x, s0, s1);
+    const int steps = rg_uniform(s1 - s0);
+    for (int t = x.cl; ok; t += x.ncl) {
+        const bool more = rg_tile<CG, BT, RG_ROWS>(p.g, walk, t, x.lane, SPLIT ? 0u : x.rank, w);
+        if (!__all_sync(0xffffffffu, more)) break;
         const uint32_t idesc = p.g.idesc | (static_cast<uint32_t>(rg_uniform(w.n_mma) >> 3) << 17);
-        for (int s = s0; s < s1; ++s) {
-            const bool fresh = (s - s0) % kI8Sum == 0;
-            const bool last = s + 1 == s1 || (s - s0) % kI8Sum == kI8Sum - 1;
+        for (int s = 0; s < steps; ++s) {
+            const bool fresh = s % kI8Sum == 0;
+            const bool last = s + 1 == steps || s % kI8Sum == kI8Sum - 1;
             if (fresh) {
-                ok = rg_all_wait(x.tempty + 8u * acc.at, acc.phase ^ 1u, p.g, x.abort_flag);
+                ok = i8_wait(false, x.tempty + 8u * acc.at, acc.phase ^ 1u, p, x);
                 if (!ok) break;
             }
-            ok = rg_all_wait(x.bfull + 8u * br.at, br.phase, p.g, x.abort_flag) &&
-                 rg_all_wait(x.wfull + 8u * wr.at, wr.phase, p.g, x.abort_flag);
+            ok = i8_wait(seen_b, x.bfull + 8u * br.at, br.phase, p, x) &&
+                 i8_wait(seen_w, x.wfull + 8u * wr.at, wr.phase, p, x);
             if (!ok) break;
             tc_fence_after_sync();
             const uint32_t d = tmem + static_cast<uint32_t>(acc.at * BT);
             const uint32_t a = tmem + C::D_COLS + static_cast<uint32_t>(wr.at * 64);
             const uint64_t b = b_desc0 + static_cast<uint32_t>(br.at) * (C::B_BYTES >> 4);
+            const uint32_t wdone = x.wempty + 8u * wr.at, bdone = x.bempty + 8u * br.at;
+            const uint32_t tdone = x.tfull + 8u * acc.at;
             if (x.lane == 0) {
                 // (past K both operands are zeros)
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     umma_f16_tmem_a<CG>(d, a + 8 * k, b + (k >> 2) * (C::B_BYTES >> 5) + (k & 3) * 2,
                                         idesc, (!fresh || k > 0) ? 1u : 0u);
-                commit(x.wempty + 8u * wr.at);
-                commit(x.bempty + 8u * br.at);
-                if (last) commit(x.tfull + 8u * acc.at);
+                commit(wdone);
+                commit(bdone);
+                if (last) commit(tdone);
             }
             issued = true;
             wr.next();
             br.next();
             if (last) acc.next();
+            // (the next stage's waits, asked for while its MMAs' predecessors run)
+            seen_b = i8_peek(x.bfull + 8u * br.at, br.phase, x.lane);
+            seen_w = i8_peek(x.wfull + 8u * wr.at, wr.phase, x.lane);
         }
     }
     // all MMAs complete before tensor memory is released
@@ -394,7 +437,7 @@ __device__ __forceinline__ void i8_epilogue(const I8Params& p, const I8Cta& x, i
     if (p.g.pdl) griddep_wait();  // (the tokens' scales)
     for (int t = x.cl; rg_tile<CG, BT, RG_ROWS>(p.g, walk, t, x.lane, SPLIT ? 0u : x.rank, w); t += x.ncl) {
         int s0, s1;
-        i8_range<SPLIT>(p, x, w.klen, s0, s1);
+        i8_range<SPLIT>(p, x, s0, s1);
         const int n = w.lane0 + q * 32 + x.lane;
         const bool mine = c_first < w.ncols && n - x.lane < p.g.n_lane;
         int v[C::NC][32];
@@ -463,19 +506,27 @@ __device__ __forceinline__ void i8_epilogue(const I8Params& p, const I8Cta& x, i
                         for (int i = 0; i < 32; ++i) v[c][i] += from[(c_first + 64 * c + i) * 128];
                 }
         }
-        if (!mine || n >= p.g.n_lane) continue;
-        const float sw = __ldg(p.w_scales + w.group * p.stride_ws + n);
-        const float bias = p.g.bias ? __ldg(p.g.bias + w.group * p.g.stride_bias + n) : 0.0f;
+        if (!mine) continue;
+        const bool in = n < p.g.n_lane;
+        const float sw = in ? __ldg(p.w_scales + w.group * p.stride_ws + n) : 0.0f;
+        const float bias = in && p.g.bias ? __ldg(p.g.bias + w.group * p.g.stride_bias + n) : 0.0f;
+        // (a lane's token scale of each chunk, handed round: 32 loads of one value each
+        // waited for L2 one after another, 20 us a tile of 128 columns)
+        float sx[C::NC];
+#pragma unroll
+        for (int c = 0; c < C::NC; ++c) {
+            const int at = c_first + 64 * c + x.lane;
+            sx[c] = at < w.ncols ? __ldcg(p.x_scales + w.out_row + at) : 0.0f;
+        }
 #pragma unroll
         for (int c = 0; c < C::NC; ++c) {
             const int c0 = c_first + 64 * c;
             if (c0 >= w.ncols) break;
-            const int left = w.ncols - c0;
-            const float* sx = p.x_scales + w.out_row + c0;
+            const int left = in ? w.ncols - c0 : 0;
             float o[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-                const float s = i < left ? __ldcg(sx + i) : 0.0f;
+                const float s = __shfl_sync(0xffffffffu, sx[c], i);
                 o[i] = fmaf(__int2float_rn(v[c][i]) * s, sw, bias);
             }
             rg_act(o, p.g.act);
