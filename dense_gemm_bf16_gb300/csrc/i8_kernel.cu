@@ -12,12 +12,12 @@
 // What it saves against 16-bit weights is bytes, so the weights stay bytes up to the SM:
 //
 //   warp 2       loads 128 weight rows x 128 bytes by TMA (128-byte swizzle);
-//   warps 4-7    read their lane's row, make fp16 pairs by byte permutes (b ^ 128 under the
+//   warps 4-11   read their lane's row, make fp16 pairs by byte permutes (b ^ 128 under the
 //                exponent of 1024 is 1152 + b; one packed subtraction) and store them to
 //                tensor memory, 64 columns a stage;
 //   warp 0       loads the tokens' fp16 rows by TMA (made once per call in the workspace);
 //   warp 1       issues tcgen05.mma with its A operand in tensor memory;
-//   warps 8-15   add accumulators up and write the result.
+//   warps 12-19  add accumulators up and write the result.
 //
 // Weights in tensor memory rather than back in shared memory: a stage then moves 16 KB in
 // and out of shared memory for the weights and 24 KB in and out for the tokens in 768
@@ -38,7 +38,9 @@
 namespace dg {
 namespace {
 
-constexpr int kI8Threads = 512;
+constexpr int kI8Convert = 8;    // warps that make fp16 weights
+constexpr int kI8Epilogue = 4 + kI8Convert;  // the epilogue's first warp
+constexpr int kI8Threads = 32 * (kI8Epilogue + 8);
 constexpr int kI8Sum = 8;        // stages of 128 that an accumulator takes
 constexpr int kI8MaxSplits = 4;
 
@@ -111,11 +113,36 @@ __device__ __forceinline__ void i8_halves(uint32_t w, uint32_t& lo, uint32_t& hi
     hi = *reinterpret_cast<const uint32_t*>(&y);
 }
 
+// One lane of a converged warp.  (elect.sync, not a comparison of the lane: the compiler then
+// keeps the operands of tensor-core and copy instructions in uniform registers.)
+__device__ __forceinline__ bool i8_elect() {
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
+}
+
 __device__ __forceinline__ uint4 i8_ld_shared(uint32_t addr) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
     return v;
+}
+
+// 32 lanes x 16 columns of tensor memory, complete on return.
+__device__ __forceinline__ void i8_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
 }
 
 __device__ __forceinline__ void i8_st_cluster(uint32_t addr, int v) {
@@ -135,28 +162,11 @@ __device__ __forceinline__ bool i8_try_wait_cluster(uint32_t bar, uint32_t parit
     return ok != 0;
 }
 
-// Has the phase completed?  (Does not wait; the result is used later, so that the answer is
-// on its way while other work is issued.)  One lane asks, the others say yes.
-__device__ __forceinline__ bool i8_peek(uint32_t bar, uint32_t parity, int lane) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.eq.s32 q, %3, 0;\n\t"
-        "setp.eq.s32 p, 0, 0;\n\t"
-        "@q mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.b32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(lane)
-        : "memory");
-    return ok != 0;
-}
-
-// Bounded wait of a whole warp, of which `seen` says that it may have ended already.  One
-// lane polls; the result comes from votes, so that the compiler knows it to be the same in
-// all lanes (see i8_issue).
-__device__ __forceinline__ bool i8_wait(bool seen, uint32_t bar, uint32_t parity, const I8Params& p,
-                                        const I8Cta& x) {
-    if (__all_sync(0xffffffffu, seen)) return true;
+// Bounded wait of a whole warp.  Every lane asks once, which costs least where the phase has
+// completed; otherwise one lane polls.  The result comes from votes, so that the compiler
+// knows it to be the same in all lanes (see i8_issue).
+__device__ __forceinline__ bool i8_wait(uint32_t bar, uint32_t parity, const I8Params& p, const I8Cta& x) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     bool ok = true;
     if (x.lane == 0) ok = mbar_wait_short(bar, parity, x.abort_flag, p.g.status, p.g.timeout_ns);
     return __all_sync(0xffffffffu, ok) != 0;
@@ -210,7 +220,7 @@ __device__ __forceinline__ void i8_load_weights(const I8Params& p, const I8Cta& 
             ok = rg_warp_wait(x.aempty + 8u * ring.at, ring.phase ^ 1u, x.lane, x.abort_flag, p.g);
             if (p.g.test_stall == 1 && armed == 0) ok = false;  // test only: the others' bounded waits must expire
             if (!ok) break;
-            if (x.lane == 0) {
+            if (i8_elect()) {
                 const uint32_t bar = x.afull + 8u * ring.at;
                 mbar_arrive_expect_tx(bar, C::A_BYTES);
                 tma_load_3d(x.sA0 + ring.at * C::A_BYTES, &p.g.tmap_a, bar, s * 128, w.lane0,
@@ -248,7 +258,7 @@ __device__ __forceinline__ void i8_load_tokens(const I8Params& p, const I8Cta& x
         for (int s = s0; s < s1; ++s) {
             ok = rg_warp_wait(x.bempty + 8u * ring.at, ring.phase ^ 1u, x.lane, x.abort_flag, p.g);
             if (!ok) break;
-            if (x.lane == 0) {
+            if (i8_elect()) {
                 const uint32_t fb = x.bfull + 8u * ring.at;
                 const uint32_t bar = CG == 1 || x.leader ? fb : mapa_shared(fb, 0u);
                 const uint32_t dst = x.sB0 + ring.at * C::B_BYTES;
@@ -288,72 +298,71 @@ __device__ __forceinline__ void i8_load_tokens(const I8Params& p, const I8Cta& x
     __syncwarp();
 }
 
-// ------------------------------------------------ weights to tensor memory (four warps)
+// ------------------------------------------------ weights to tensor memory (eight warps)
+// Two warps per tensor-memory lane quarter, each for 64 of a stage's 128 weights a row.  They
+// are converted before the wait for their place in tensor memory: a pair's two stages there
+// leave 768 clocks from one MMA's end to the next one's start, of which the hand-over takes
+// 600 (the commit's arrival 300, the weights' 250).
 template <int CG, int BT, bool SPLIT>
 __device__ __forceinline__ void i8_convert(const I8Params& p, const I8Cta& x, int warp) {
     using C = I8Cfg<CG, BT, SPLIT>;
-    const int q = warp & 3, row = q * 32 + x.lane;
-    const uint32_t a_row = x.sA0 + row * 128, swz = static_cast<uint32_t>(row & 7) << 4;
-    const uint32_t to = x.tmem + (static_cast<uint32_t>(q * 32) << 16) + C::D_COLS;
+    const int q = warp & 3, row = q * 32 + x.lane, half = (warp - 4) >> 2;
+    // (16-byte part 4 half + c of the row, swizzled by the row)
+    const uint32_t a_row = x.sA0 + row * 128 + ((half << 6) ^ ((row & 4) << 4)), swz = (row & 3) << 4;
+    const uint32_t to = x.tmem + (static_cast<uint32_t>(q * 32) << 16) + C::D_COLS + half * 32;
     RgWalk walk = rg_begin<RG_ROWS>(p.g, x.lane);
     RgTile w;
     I8Ring<C::SA> in;
     I8Ring<C::TA> out;
-    bool ok = true, seen_a = false;
-    for (int t = x.cl; ok && rg_tile<CG, BT, RG_ROWS>(p.g, walk, t, x.lane, SPLIT ? 0u : x.rank, w); t += x.ncl) {
-        int s0, s1;
-        i8_range<SPLIT>(p, x, s0, s1);
+    bool ok = true;
+    int s0, s1;
+    i8_range<SPLIT>(p, x, s0, s1);
+    for (int t = x.cl; ok; t += x.ncl) {
+        const bool more = rg_tile<CG, BT, RG_ROWS>(p.g, walk, t, x.lane, SPLIT ? 0u : x.rank, w);
+        if (!__all_sync(0xffffffffu, more)) break;
         for (int s = s0; s < s1; ++s) {
-            const bool seen_w = i8_peek(x.wempty + 8u * out.at, out.phase ^ 1u, x.lane);
-            ok = i8_wait(seen_a, x.afull + 8u * in.at, in.phase, p, x);
+            ok = i8_wait(x.afull + 8u * in.at, in.phase, p, x);
             if (!ok) break;
             const uint32_t src = a_row + in.at * C::A_BYTES;
-            uint4 v[8];
+            uint32_t r[32];
 #pragma unroll
-            for (int c = 0; c < 8; ++c) v[c] = i8_ld_shared(src + ((c << 4) ^ swz));
-            ok = i8_wait(seen_w, x.wempty + 8u * out.at, out.phase ^ 1u, p, x);
+            for (int c = 0; c < 4; ++c) {
+                const uint4 v = i8_ld_shared(src + ((c << 4) ^ swz));
+                i8_halves(v.x, r[8 * c], r[8 * c + 1]);
+                i8_halves(v.y, r[8 * c + 2], r[8 * c + 3]);
+                i8_halves(v.z, r[8 * c + 4], r[8 * c + 5]);
+                i8_halves(v.w, r[8 * c + 6], r[8 * c + 7]);
+            }
+            ok = i8_wait(x.wempty + 8u * out.at, out.phase ^ 1u, p, x);
             if (!ok) break;
             tc_fence_after_sync();
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t r[32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    i8_halves(v[4 * h + c].x, r[8 * c], r[8 * c + 1]);
-                    i8_halves(v[4 * h + c].y, r[8 * c + 2], r[8 * c + 3]);
-                    i8_halves(v[4 * h + c].z, r[8 * c + 4], r[8 * c + 5]);
-                    i8_halves(v[4 * h + c].w, r[8 * c + 6], r[8 * c + 7]);
-                }
-                tmem_st_x32(to + out.at * 64 + 32 * h, r);
-            }
+            tmem_st_x32(to + out.at * 64, r);
             tmem_st_wait();
             tc_fence_before_sync();
             __syncwarp();
-            // (the stage goes back only now that its values have been used: an arrival right
-            // behind the loads overtook them where the epilogue's stores held them up, and
-            // the next copy overwrote what single lanes had still to read)
             if (x.lane == 0) {
-                const uint32_t bar = x.wfull + 8u * out.at;
                 // (nothing but tensor memory is handed over, which the fence above orders: a
                 // release at cluster scope took 500 to 1500 clocks here)
+                const uint32_t bar = x.wfull + 8u * out.at;
                 if (CG == 2)
                     mbar_arrive_relaxed(mapa_shared(bar, 0u));
                 else
                     mbar_arrive(bar);
+                // (the stage goes back only now that its values have been used: an arrival
+                // right behind the loads overtook them where the epilogue's stores held them
+                // up, and the next copy overwrote what single lanes had still to read)
                 mbar_arrive(x.aempty + 8u * in.at);
             }
             in.next();
             out.next();
-            seen_a = i8_peek(x.afull + 8u * in.at, in.phase, x.lane);
         }
     }
 }
 
 // ------------------------------------------------ MMA issuer (a warp; of the pair's leader)
-// The whole warp walks tiles and stages, every branch decided by a vote and every position
-// made uniform, and one lane issues: operands of the tensor-core instructions are then in
-// uniform registers.  (With branches that the compiler took for divergent, an MMA took 67
-// clocks to issue, whatever its size, a commit 100, and a stage 1200 in all.)
+// The whole warp walks tiles and stages, every branch decided by a vote, and an elected lane
+// issues.  (Chosen by its number, that lane took 67 clocks to issue an MMA of any size and 100
+// for a commit, 1200 a stage in all; 20 tokens, 19456 x 8192: 47 -> 34 us.)
 template <int CG, int BT, bool SPLIT>
 __device__ __forceinline__ void i8_issue(const I8Params& p, const I8Cta& x) {
     using C = I8Cfg<CG, BT, SPLIT>;
@@ -366,7 +375,7 @@ __device__ __forceinline__ void i8_issue(const I8Params& p, const I8Cta& x) {
     I8Ring<C::TA> wr;
     I8Ring<C::SB> br;
     I8Ring<2> acc;
-    bool ok = true, issued = false, seen_b = false, seen_w = false;
+    bool ok = true, issued = false;
     auto commit = [&](uint32_t bar) {
         if constexpr (CG == 2)
             umma_commit_mc_cg<CG>(bar, kPair);
@@ -384,11 +393,13 @@ __device__ __forceinline__ void i8_issue(const I8Params& p, const I8Cta& x) {
             const bool fresh = s % kI8Sum == 0;
             const bool last = s + 1 == steps || s % kI8Sum == kI8Sum - 1;
             if (fresh) {
-                ok = i8_wait(false, x.tempty + 8u * acc.at, acc.phase ^ 1u, p, x);
+                ok = i8_wait(x.tempty + 8u * acc.at, acc.phase ^ 1u, p, x);
                 if (!ok) break;
             }
-            ok = i8_wait(seen_b, x.bfull + 8u * br.at, br.phase, p, x) &&
-                 i8_wait(seen_w, x.wfull + 8u * wr.at, wr.phase, p, x);
+            const uint32_t bbar = x.bfull + 8u * br.at, wbar = x.wfull + 8u * wr.at;
+            const bool b_in = mbar_try_wait(bbar, br.phase), w_in = mbar_try_wait(wbar, wr.phase);
+            if (!__all_sync(0xffffffffu, b_in && w_in))
+                ok = i8_wait(bbar, br.phase, p, x) && i8_wait(wbar, wr.phase, p, x);
             if (!ok) break;
             tc_fence_after_sync();
             const uint32_t d = tmem + static_cast<uint32_t>(acc.at * BT);
@@ -396,7 +407,7 @@ __device__ __forceinline__ void i8_issue(const I8Params& p, const I8Cta& x) {
             const uint64_t b = b_desc0 + static_cast<uint32_t>(br.at) * (C::B_BYTES >> 4);
             const uint32_t wdone = x.wempty + 8u * wr.at, bdone = x.bempty + 8u * br.at;
             const uint32_t tdone = x.tfull + 8u * acc.at;
-            if (x.lane == 0) {
+            if (i8_elect()) {
                 // (past K both operands are zeros)
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
@@ -410,9 +421,6 @@ __device__ __forceinline__ void i8_issue(const I8Params& p, const I8Cta& x) {
             wr.next();
             br.next();
             if (last) acc.next();
-            // (the next stage's waits, asked for while its MMAs' predecessors run)
-            seen_b = i8_peek(x.bfull + 8u * br.at, br.phase, x.lane);
-            seen_w = i8_peek(x.wfull + 8u * wr.at, wr.phase, x.lane);
         }
     }
     // all MMAs complete before tensor memory is released
@@ -429,7 +437,7 @@ template <int CG, int BT, bool SPLIT>
 __device__ __forceinline__ void i8_epilogue(const I8Params& p, const I8Cta& x, int warp) {
     using C = I8Cfg<CG, BT, SPLIT>;
     const int q = warp & 3;  // tensor-memory lane quarter of this warp
-    const int c_first = ((warp - 8) >> 2) * 32;
+    const int c_first = ((warp - kI8Epilogue) >> 2) * 32;
     const uint32_t row = x.tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(c_first);
     RgWalk walk = rg_begin<RG_ROWS>(p.g, x.lane);
     RgTile w;
@@ -456,11 +464,14 @@ __device__ __forceinline__ void i8_epilogue(const I8Params& p, const I8Cta& x, i
 #pragma unroll
                 for (int c = 0; c < C::NC; ++c) {
                     if (c_first + 64 * c < w.ncols) {
-                        uint32_t u[32];
-                        tmem_ld_x32(from + 64u * c, u);
-                        tmem_ld_wait(u);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[c][i] += __float2int_rn(__uint_as_float(u[i]));
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t u[16];
+                            i8_ld16(from + 64u * c + 16u * h, u);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                v[c][16 * h + i] += __float2int_rn(__uint_as_float(u[i]));
+                        }
                     }
                 }
             }
@@ -547,15 +558,15 @@ __device__ __forceinline__ void i8_epilogue(const I8Params& p, const I8Cta& x, i
     }
 }
 
-// Registers of the pair form: 96 sums a thread of the epilogue's two warpgroups.  512
-// threads are launched with 128 (i8_prepare checks it): 72 + 96 + 2 x 168 fit 4 x 128.
-constexpr int I8_LAUNCH_REGS = 128, I8_ISSUE_REGS = 72, I8_CONVERT_REGS = 96, I8_SUM_REGS = 168;
-static_assert(I8_ISSUE_REGS + I8_CONVERT_REGS + 2 * I8_SUM_REGS <= 4 * I8_LAUNCH_REGS, "register split");
+// Registers: up to 96 sums a thread of the epilogue's two warpgroups.  640 threads are
+// launched with 96 (i8_prepare checks it): 64 + 2 x 72 + 2 x 136 fit 5 x 96.
+constexpr int I8_LAUNCH_REGS = 96, I8_ISSUE_REGS = 64, I8_CONVERT_REGS = 72, I8_SUM_REGS = 136;
+static_assert(I8_ISSUE_REGS + 2 * I8_CONVERT_REGS + 2 * I8_SUM_REGS <= 5 * I8_LAUNCH_REGS, "register split");
 
 template <int CG, int BT, bool SPLIT>
 __global__ void __launch_bounds__(kI8Threads, 1) i8_kernel(const __grid_constant__ I8Params p) {
     using C = I8Cfg<CG, BT, SPLIT>;
-    constexpr bool MOVE = BT > 128;
+    constexpr bool MOVE = BT > 64;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
@@ -586,14 +597,14 @@ __global__ void __launch_bounds__(kI8Threads, 1) i8_kernel(const __grid_constant
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::SA; ++s) {
             mbar_init(x.afull + 8u * s, 1);
-            mbar_init(x.aempty + 8u * s, 4);
+            mbar_init(x.aempty + 8u * s, kI8Convert);
         }
         for (int s = 0; s < C::SB; ++s) {
             mbar_init(x.bfull + 8u * s, 1);
             mbar_init(x.bempty + 8u * s, 1);
         }
         for (int s = 0; s < C::TA; ++s) {
-            mbar_init(x.wfull + 8u * s, 4 * CG);
+            mbar_init(x.wfull + 8u * s, kI8Convert * CG);
             mbar_init(x.wempty + 8u * s, 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -622,7 +633,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) i8_kernel(const __grid_constant
     tc_fence_after_sync();
     x.tmem = *tmem_slot;
 
-    if (warp >= 8) {
+    if (warp >= kI8Epilogue) {
         if (MOVE) reg_inc<I8_SUM_REGS>();
         i8_epilogue<CG, BT, SPLIT>(p, x, warp);
     } else if (warp >= 4) {
@@ -681,7 +692,7 @@ cudaError_t prepare_form() {
     // (a wait for registers that the launch does not have would never end)
     cudaFuncAttributes a;
     if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, i8_kernel<CG, BT, SPLIT>);
-    if (e == cudaSuccess && BT > 128 && a.numRegs < I8_LAUNCH_REGS) e = cudaErrorInvalidConfiguration;
+    if (e == cudaSuccess && BT > 64 && a.numRegs < I8_LAUNCH_REGS) e = cudaErrorInvalidConfiguration;
     return e;
 }
 
