@@ -56,8 +56,8 @@ void i8_variant(const RgProblem& q, const DeviceInfo& d, int* cg, int* bt) {
         return cdiv(q.n_lane, lanes) * (q.offsets ? q.groups : 1) * cdiv(cols, w);
     };
     *cg = 1;
-    if (cols > 128 && q.n_lane > 128 && d.max_pairs > 0 && tiles(256, 192) >= d.max_pairs / 2) {
-        *cg = 2, *bt = 192;
+    if (cols > 128 && q.n_lane > 128 && d.max_pairs > 0 && tiles(256, kI8PairCols) >= d.max_pairs / 2) {
+        *cg = 2, *bt = kI8PairCols;
         return;
     }
     *bt = cols <= 32 ? 32 : (cols <= 64 ? 64 : 128);

@@ -49,16 +49,17 @@ struct I8Cfg {
     static constexpr int B_ROWS = BT / CG;                  // token rows a CTA holds
     static constexpr uint32_t A_BYTES = 128 * 128;          // int8
     static constexpr uint32_t B_BYTES = 2 * B_ROWS * 128;   // two 64-deep blocks of fp16
-    static constexpr int NC = BT < 64 ? 1 : BT / 64;        // 32-column chunks of an epilogue warp
+    static constexpr int NC = (BT + 63) / 64;        // 32-column chunks of an epilogue warp
     static constexpr uint32_t D_COLS = 2 * BT;              // two accumulators
     static constexpr int TA = (512 - D_COLS) / 64 < 4 ? (512 - D_COLS) / 64 : 4;
     static constexpr uint32_t RED_BYTES = SPLIT ? (kI8MaxSplits - 1) * BT * 128 * 4 : 0;
     static constexpr uint32_t BAR_BYTES = 512;
+    static constexpr uint32_t EPI_WARP = 2048;  // a staged tile of 32 x 32 16-bit elements
     // stages of tokens, and of weights with what is left
     static constexpr int SB = BT >= 128 ? (CG == 2 ? 4 : 3) : 6;
-    static constexpr int FIT = (kRgMaxSmem - 1024 - BAR_BYTES - RED_BYTES - SB * B_BYTES) / A_BYTES;
+    static constexpr int FIT = (kRgMaxSmem - 1024 - BAR_BYTES - RED_BYTES - 8 * EPI_WARP - SB * B_BYTES) / A_BYTES;
     static constexpr int SA = FIT > 10 ? 10 : FIT;
-    static constexpr size_t SMEM = 1024 + size_t(SA) * A_BYTES + SB * B_BYTES + RED_BYTES + BAR_BYTES;
+    static constexpr size_t SMEM = 1024 + size_t(SA) * A_BYTES + SB * B_BYTES + RED_BYTES + 8 * EPI_WARP + BAR_BYTES;
     static_assert(TA >= 2 && SA >= 3, "rings");
     static_assert(B_BYTES % 2048 == 0, "both blocks start on swizzle atoms");
     static_assert((2 * (SA + SB + TA) + 6) * 8 + 8 <= BAR_BYTES, "barrier area too small");
@@ -132,10 +133,11 @@ __device__ __forceinline__ uint4 i8_ld_shared(uint32_t addr) {
     return v;
 }
 
-// 32 lanes x 16 columns of tensor memory, complete on return.
+// 16 lanes x 32 columns of tensor memory in the layout of tmem_ld_16x256_x4, complete on
+// return.
 __device__ __forceinline__ void i8_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
@@ -162,14 +164,45 @@ __device__ __forceinline__ bool i8_try_wait_cluster(uint32_t bar, uint32_t parit
     return ok != 0;
 }
 
-// Bounded wait of a whole warp.  Every lane asks once, which costs least where the phase has
-// completed; otherwise one lane polls.  The result comes from votes, so that the compiler
-// knows it to be the same in all lanes (see i8_issue).
+// Bounded wait of a whole warp for one phase, or for two.  All lanes poll and
+// vote, which costs least where the phases have completed, and the compiler knows a vote to
+// be the same in all lanes (see i8_issue).
+__device__ __forceinline__ bool i8_wait2(uint32_t bar_a, uint32_t parity_a, uint32_t bar_b,
+                                         uint32_t parity_b, const I8Params& p, const I8Cta& x) {
+    uint64_t t0 = 0;
+    bool a = false, b = false;
+    for (uint32_t it = 1;; ++it) {
+        a = a || mbar_try_wait(bar_a, parity_a);
+        b = b || mbar_try_wait(bar_b, parity_b);
+        if (__all_sync(0xffffffffu, a && b)) return true;
+        if ((it & 63u) == 0) {
+            const uint64_t now = globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            const bool late = now - t0 > p.g.timeout_ns;
+            if (late) {
+                *x.abort_flag = 1;
+                if (p.g.status) DG_SET_TIMEOUT(p.g.status);
+            }
+            if (__any_sync(0xffffffffu, late || *x.abort_flag != 0)) return false;
+        }
+    }
+}
+
 __device__ __forceinline__ bool i8_wait(uint32_t bar, uint32_t parity, const I8Params& p, const I8Cta& x) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    bool ok = true;
-    if (x.lane == 0) ok = mbar_wait_short(bar, parity, x.abort_flag, p.g.status, p.g.timeout_ns);
-    return __all_sync(0xffffffffu, ok) != 0;
+    uint64_t t0 = 0;
+    for (uint32_t it = 1;; ++it) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if ((it & 63u) == 0) {
+            const uint64_t now = globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            const bool late = now - t0 > p.g.timeout_ns;
+            if (late) {
+                *x.abort_flag = 1;
+                if (p.g.status) DG_SET_TIMEOUT(p.g.status);
+            }
+            if (__any_sync(0xffffffffu, late || *x.abort_flag != 0)) return false;
+        }
+    }
 }
 
 // Stages of a tile's contraction that this CTA takes.
@@ -344,7 +377,7 @@ __device__ __forceinline__ void i8_convert(const I8Params& p, const I8Cta& x, in
                 // (nothing but tensor memory is handed over, which the fence above orders: a
                 // release at cluster scope took 500 to 1500 clocks here)
                 const uint32_t bar = x.wfull + 8u * out.at;
-                if (CG == 2)
+                if (CG == 2 && !x.leader)
                     mbar_arrive_relaxed(mapa_shared(bar, 0u));
                 else
                     mbar_arrive(bar);
@@ -397,9 +430,7 @@ __device__ __forceinline__ void i8_issue(const I8Params& p, const I8Cta& x) {
                 if (!ok) break;
             }
             const uint32_t bbar = x.bfull + 8u * br.at, wbar = x.wfull + 8u * wr.at;
-            const bool b_in = mbar_try_wait(bbar, br.phase), w_in = mbar_try_wait(wbar, wr.phase);
-            if (!__all_sync(0xffffffffu, b_in && w_in))
-                ok = i8_wait(bbar, br.phase, p, x) && i8_wait(wbar, wr.phase, p, x);
+            ok = i8_wait2(bbar, br.phase, wbar, wr.phase, p, x);
             if (!ok) break;
             tc_fence_after_sync();
             const uint32_t d = tmem + static_cast<uint32_t>(acc.at * BT);
@@ -432,12 +463,18 @@ __device__ __forceinline__ void i8_issue(const I8Params& p, const I8Cta& x) {
 }
 
 // ------------------------------------------------ epilogue (a warp of eight)
-// One output column per thread, its tile's tokens in the registers.
+// Sums stay in the registers in the layout of the matrix loads: of a chunk of 32 tokens, value
+// i is output column 8 (2 (i / 16) + (i / 2) % 2) + lane / 4 and token 8 ((i / 4) % 4) +
+// 2 (lane % 4) + i % 2 of the warp's.  16-bit results go through a staged tile, as
+// in rg_out16, and leave 16 bytes at a time.  (One output column per thread, a shuffle for
+// each token's scale and a two-byte store for each result took 4.5 us a tile: 1500 x 4096 x
+// 4096 46 us.)
 template <int CG, int BT, bool SPLIT>
-__device__ __forceinline__ void i8_epilogue(const I8Params& p, const I8Cta& x, int warp) {
+__device__ __forceinline__ void i8_epilogue(const I8Params& p, const I8Cta& x, int warp, uint8_t* buf) {
     using C = I8Cfg<CG, BT, SPLIT>;
     const int q = warp & 3;  // tensor-memory lane quarter of this warp
     const int c_first = ((warp - kI8Epilogue) >> 2) * 32;
+    const int pcol = x.lane >> 2, part = x.lane & 3;
     const uint32_t row = x.tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(c_first);
     RgWalk walk = rg_begin<RG_ROWS>(p.g, x.lane);
     RgTile w;
@@ -446,8 +483,8 @@ __device__ __forceinline__ void i8_epilogue(const I8Params& p, const I8Cta& x, i
     for (int t = x.cl; rg_tile<CG, BT, RG_ROWS>(p.g, walk, t, x.lane, SPLIT ? 0u : x.rank, w); t += x.ncl) {
         int s0, s1;
         i8_range<SPLIT>(p, x, s0, s1);
-        const int n = w.lane0 + q * 32 + x.lane;
-        const bool mine = c_first < w.ncols && n - x.lane < p.g.n_lane;
+        const int nl0 = w.lane0 + q * 32;  // first output column of this warp
+        const bool mine = c_first < w.ncols && nl0 < p.g.n_lane;
         int v[C::NC][32];
 #pragma unroll
         for (int c = 0; c < C::NC; ++c)
@@ -467,7 +504,7 @@ __device__ __forceinline__ void i8_epilogue(const I8Params& p, const I8Cta& x, i
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             uint32_t u[16];
-                            i8_ld16(from + 64u * c + 16u * h, u);
+                            i8_ld16(from + 64u * c + (static_cast<uint32_t>(h) << 20), u);
 #pragma unroll
                             for (int i = 0; i < 16; ++i)
                                 v[c][16 * h + i] += __float2int_rn(__uint_as_float(u[i]));
@@ -486,6 +523,7 @@ __device__ __forceinline__ void i8_epilogue(const I8Params& p, const I8Cta& x, i
             // (one tile a cluster) the other CTAs' sums go to the first one
             if (x.rank != 0) {
                 if (mine) {
+                    // (value by value, 32 lanes side by side)
                     const uint32_t at = mapa_shared(smem_u32(x.red), 0u) +
                                         ((x.rank - 1) * BT * 128 + q * 32 + x.lane) * 4u;
 #pragma unroll
@@ -518,12 +556,15 @@ __device__ __forceinline__ void i8_epilogue(const I8Params& p, const I8Cta& x, i
                 }
         }
         if (!mine) continue;
-        const bool in = n < p.g.n_lane;
-        const float sw = in ? __ldg(p.w_scales + w.group * p.stride_ws + n) : 0.0f;
-        const float bias = in && p.g.bias ? __ldg(p.g.bias + w.group * p.g.stride_bias + n) : 0.0f;
-        // (a lane's token scale of each chunk, handed round: 32 loads of one value each
-        // waited for L2 one after another, 20 us a tile of 128 columns)
-        float sx[C::NC];
+        // this lane's four output columns and, of each chunk, one token
+        float sw[4], bias[4], sx[C::NC];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int n = nl0 + 8 * i + pcol;
+            const bool in = n < p.g.n_lane;
+            sw[i] = in ? __ldg(p.w_scales + w.group * p.stride_ws + n) : 0.0f;
+            bias[i] = in && p.g.bias ? __ldg(p.g.bias + w.group * p.g.stride_bias + n) : 0.0f;
+        }
 #pragma unroll
         for (int c = 0; c < C::NC; ++c) {
             const int at = c_first + 64 * c + x.lane;
@@ -533,26 +574,49 @@ __device__ __forceinline__ void i8_epilogue(const I8Params& p, const I8Cta& x, i
         for (int c = 0; c < C::NC; ++c) {
             const int c0 = c_first + 64 * c;
             if (c0 >= w.ncols) break;
-            const int left = in ? w.ncols - c0 : 0;
             float o[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const float s = __shfl_sync(0xffffffffu, sx[c], i);
-                o[i] = fmaf(__int2float_rn(v[c][i]) * s, sw, bias);
+            for (int k = 0; k < 8; ++k) {
+                const float s = __shfl_sync(0xffffffffu, sx[c], 8 * (k >> 1) + 2 * part + (k & 1));
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const int i = 16 * (h >> 1) + 4 * (k >> 1) + 2 * (h & 1) + (k & 1);
+                    o[i] = fmaf(__int2float_rn(v[c][i]) * s, sw[h], bias[h]);
+                }
             }
             rg_act(o, p.g.act);
-            const int64_t off = static_cast<int64_t>(w.out_row + c0) * p.g.ldc + n;
             if (p.g.c_dtype == DT_F32) {
-                float* dst = static_cast<float*>(p.g.C) + off;
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (i < left && rg_span_ok(p.g, off + i * p.g.ldc, 1)) dst[i * p.g.ldc] = o[i];
-            } else {
-                uint16_t* dst = static_cast<uint16_t*>(p.g.C) + off;
+                for (int i = 0; i < 32; ++i) {
+                    const int n = nl0 + 8 * (2 * (i >> 4) + ((i >> 1) & 1)) + pcol;
+                    const int col = c0 + 8 * ((i >> 2) & 3) + 2 * part + (i & 1);
+                    const int64_t off = (w.out_row + col) * p.g.ldc + n;
+                    if (n < p.g.n_lane && col < w.ncols && rg_span_ok(p.g, off, 1))
+                        static_cast<float*>(p.g.C)[off] = o[i];
+                }
+                continue;
+            }
+            uint32_t pk[4][4];
+            rg_pack16(p.g.c_dtype, o, pk);
+            __syncwarp();  // (the chunk before has left the staged tile)
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (i < left && rg_span_ok(p.g, off + i * p.g.ldc, 1))
-                        dst[i * p.g.ldc] = static_cast<uint16_t>(rg_pack(p.g.c_dtype, o[i], o[i]));
+            for (int i = 0; i < 4; ++i)
+                stmatrix_x4_trans(smem_u32(buf) + rg_at(x.lane & 7, x.lane >> 3) + 512u * i, pk[i][0],
+                                  pk[i][1], pk[i][2], pk[i][3]);
+            __syncwarp();
+            const int64_t base = (w.out_row + c0) * p.g.ldc + nl0;
+            if (!p.g.c_vec) {
+                rg_put_rows(p.g, buf, base, w.ncols - c0 < 32 ? w.ncols - c0 : 32, p.g.n_lane - nl0,
+                            x.lane);
+                continue;
+            }
+            const int nn = p.g.n_lane - nl0 - 8 * part;
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
+                const int row = 8 * it + pcol;
+                if (c0 + row < w.ncols && nn > 0)
+                    rg_store8<false>(p.g, base + row * p.g.ldc + 8 * part, nn,
+                                     *reinterpret_cast<const uint4*>(buf + rg_at(row, part)));
             }
         }
     }
@@ -581,7 +645,8 @@ __global__ void __launch_bounds__(kI8Threads, 1) i8_kernel(const __grid_constant
     x.sA0 = smem_u32(smem);
     x.sB0 = x.sA0 + C::SA * C::A_BYTES;
     x.red = reinterpret_cast<int*>(smem + C::SA * C::A_BYTES + C::SB * C::B_BYTES);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(x.red) + C::RED_BYTES);
+    uint8_t* staged = reinterpret_cast<uint8_t*>(x.red) + C::RED_BYTES;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(staged + 8 * C::EPI_WARP);
     x.afull = smem_u32(bars);
     x.aempty = x.afull + 8u * C::SA;
     x.bfull = x.aempty + 8u * C::SA;
@@ -635,7 +700,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) i8_kernel(const __grid_constant
 
     if (warp >= kI8Epilogue) {
         if (MOVE) reg_inc<I8_SUM_REGS>();
-        i8_epilogue<CG, BT, SPLIT>(p, x, warp);
+        i8_epilogue<CG, BT, SPLIT>(p, x, warp, staged + (warp - kI8Epilogue) * C::EPI_WARP);
     } else if (warp >= 4) {
         if (MOVE) reg_dec<I8_CONVERT_REGS>();
         i8_convert<CG, BT, SPLIT>(p, x, warp);
@@ -700,7 +765,7 @@ cudaError_t prepare_form() {
 
 cudaError_t i8_launch(int cg, int bt, const I8Params& p, int grid, cudaStream_t stream) {
     if (p.splits > 1) return launch_form<1, 32, true>(p, grid, stream);
-    if (cg == 2) return launch_form<2, 192, false>(p, grid, stream);
+    if (cg == 2) return launch_form<2, kI8PairCols, false>(p, grid, stream);
     if (bt == 128) return launch_form<1, 128, false>(p, grid, stream);
     if (bt == 64) return launch_form<1, 64, false>(p, grid, stream);
     return launch_form<1, 32, false>(p, grid, stream);
@@ -711,7 +776,7 @@ cudaError_t i8_prepare() {
     if (e == cudaSuccess) e = prepare_form<1, 32, false>();
     if (e == cudaSuccess) e = prepare_form<1, 64, false>();
     if (e == cudaSuccess) e = prepare_form<1, 128, false>();
-    if (e == cudaSuccess) e = prepare_form<2, 192, false>();
+    if (e == cudaSuccess) e = prepare_form<2, kI8PairCols, false>();
     return e;
 }
 
