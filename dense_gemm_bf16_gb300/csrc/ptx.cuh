@@ -293,6 +293,12 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
         : "memory");
 }
 
+// `bytes` (a multiple of 16, from a 16-byte boundary on) towards L2.
+__device__ __forceinline__ void l2_prefetch(const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;"
+                 ::"l"(reinterpret_cast<uint64_t>(src)), "r"(bytes) : "memory");
+}
+
 // Relaxed (strong, unordered) load at GPU scope: the polling half of a
 // release / fence-acquire pattern.
 __device__ __forceinline__ unsigned long long ld_relaxed_u64(const unsigned long long* ptr) {

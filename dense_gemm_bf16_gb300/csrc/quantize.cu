@@ -11,7 +11,8 @@
 //
 // One pass over the data: the threads of a row (a warp's worth at least, a block's at
 // most) keep its elements in registers between the maximum and the quotients, up to 32
-// each; longer rows are read again, from L2.  Bound by the bytes.
+// each (16 of fp32, and where rows are not aligned), and load the next row's meanwhile;
+// what a row has beyond is read again, from L2.  Bound by the bytes.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -24,7 +25,11 @@ namespace dg {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kKeep = 32;  // elements of a row that a thread keeps
+// Elements of a row that a thread keeps (16 registers; the next row's take 16 more).
+template <int DT>
+__host__ __device__ constexpr int quant_keep(int n) {
+    return DT == DT_F32 || n == 1 ? 16 : 32;
+}
 
 struct QuantParams {
     const void* x;
@@ -36,6 +41,8 @@ struct QuantParams {
     float* scales;
     int32_t tpr_log2;   // threads of a row
 };
+
+constexpr int kQuantBlocksPerSm = 4;  // all resident at once
 
 template <int BYTES>
 struct Raw {
@@ -61,62 +68,136 @@ __device__ __forceinline__ void widen(const V& v, float (&f)[N]) {
     }
 }
 
-// 127 x / top to the nearest integer; r = 127 / top rounded.
-__device__ __forceinline__ float quotient(float x, float top, float r) {
-    const float y = x * r;
-    float n = rintf(y);
-    if (fabsf(y - n) > 0.5f - 6.103515625e-5f) {
-        const float lo = floorf(fabsf(y));
-        const double a = 254.0 * static_cast<double>(fabsf(x));
-        const double b = (2.0 * static_cast<double>(lo) + 1.0) * static_cast<double>(top);
-        const bool odd = (static_cast<int>(lo) & 1) != 0;
-        n = copysignf(a > b || (a == b && odd) ? lo + 1.0f : lo, x);
+// The larger magnitudes of a unit's elements and `top`, as bit patterns, which order as
+// integers: infinities above all numbers, NaN above those.  (16-bit pairs two at a time.)
+template <int DT, int N, typename V>
+__device__ __forceinline__ uint32_t larger(const V& v, uint32_t top) {
+    if constexpr (DT == DT_F32) {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
+#pragma unroll
+        for (int i = 0; i < N; ++i) top = max(top, w[i] & 0x7fffffffu);
+    } else if constexpr (N == 1) {
+        top = max(top, static_cast<uint32_t>(v) & 0x7fffu);
+    } else {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
     }
-    return n;
+    return top;
+}
+
+// ... of a thread, as fp32 bits.
+template <int DT, int N>
+__device__ __forceinline__ uint32_t magnitude(uint32_t top) {
+    if constexpr (DT == DT_F32) return top;
+    const uint32_t h = N == 1 ? top : max(top & 0xffffu, top >> 16);
+    return DT == DT_BF16 ? h << 16
+                         : __float_as_uint(__half2float(__ushort_as_half(static_cast<uint16_t>(h))));
+}
+
+// Adding and subtracting this rounds an fp32 number of at most 2^22 to the nearest integer,
+// ties to even; the sum's low bits are the integer.
+constexpr float kToInt = 12582912.0f;  // 1.5 * 2^23
+
+// 127 x / top decided exactly, where fp32's y may lie on the wrong side of a border.
+__device__ __noinline__ float quotient_exact(float x, float y, float top) {
+    const float lo = floorf(fabsf(y));
+    const double a = 254.0 * static_cast<double>(fabsf(x));
+    const double b = (2.0 * static_cast<double>(lo) + 1.0) * static_cast<double>(top);
+    const bool odd = (static_cast<int>(lo) & 1) != 0;
+    return copysignf(a > b || (a == b && odd) ? lo + 1.0f : lo, x);
+}
+
+// N quotients 127 x / top as rounded integers + kToInt; r = 127 / top rounded.
+template <int N>
+__device__ __forceinline__ void quotients(const float (&x)[N], float top, float r, float (&t)[N]) {
+    float far = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float y = x[i] * r;
+        t[i] = y + kToInt;
+        far = fmaxf(far, fabsf(y - (t[i] - kToInt)));
+    }
+    if (far > 0.5f - 6.103515625e-5f) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float y = x[i] * r;
+            if (fabsf(y - (t[i] - kToInt)) > 0.5f - 6.103515625e-5f)
+                t[i] = quotient_exact(x[i], y, top) + kToInt;
+        }
+    }
+}
+
+// N rounded integers + kToInt as int8 or fp16.
+template <int N, bool WIDE>
+__device__ __forceinline__ void store_integers(char* dst, const float (&t)[N]) {
+    if constexpr (N == 1) {
+        if constexpr (WIDE)
+            *reinterpret_cast<__half*>(dst) = __float2half_rn(t[0] - kToInt);
+        else
+            *reinterpret_cast<uint8_t*>(dst) = static_cast<uint8_t>(__float_as_uint(t[0]));
+    } else if constexpr (WIDE) {
+        typename Raw<N * 2>::V o;
+        __half2* h = reinterpret_cast<__half2*>(&o);
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) h[i] = __floats2half2_rn(t[2 * i] - kToInt, t[2 * i + 1] - kToInt);
+        *reinterpret_cast<typename Raw<N * 2>::V*>(dst) = o;
+    } else if constexpr (N == 2) {
+        *reinterpret_cast<uint16_t*>(dst) =
+            static_cast<uint16_t>(__byte_perm(__float_as_uint(t[0]), __float_as_uint(t[1]), 0x0040));
+    } else {
+        typename Raw<N>::V o;
+        uint32_t* w = reinterpret_cast<uint32_t*>(&o);
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i)
+            w[i] = __byte_perm(__byte_perm(__float_as_uint(t[4 * i]), __float_as_uint(t[4 * i + 1]), 0x0040),
+                               __byte_perm(__float_as_uint(t[4 * i + 2]), __float_as_uint(t[4 * i + 3]), 0x0040),
+                               0x5410);
+        *reinterpret_cast<typename Raw<N>::V*>(dst) = o;
+    }
 }
 
 // WIDE: fp16 integers, padded; else int8.
 template <int DT, int N, bool WIDE>
-__global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantParams p) {
+__global__ void __launch_bounds__(kThreads, kQuantBlocksPerSm) quantize_kernel(const QuantParams p) {
     constexpr int ES = DT == DT_F32 ? 4 : 2;
-    constexpr int R = kKeep / N;
+    constexpr int R = quant_keep<DT>(N) / N;
     using V = typename Raw<N * ES>::V;
-    using O = typename Raw<N * (WIDE ? 2 : 1)>::V;
     __shared__ uint32_t tops[kThreads / 32];
     if (WIDE) griddep_launch_dependents();
     const int tpr = 1 << p.tpr_log2, in = threadIdx.x & (tpr - 1);
     const int per_block = kThreads >> p.tpr_log2;
     const int warp = threadIdx.x >> 5, warps = tpr >> 5, lane = threadIdx.x & 31;
     const int64_t step = static_cast<int64_t>(gridDim.x) * per_block;
+    V next[R];
+    auto fetch = [&](int64_t row) {
+        if (row >= p.T) return;
+        const char* src = static_cast<const char*>(p.x) + row * p.ld_x * ES;
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int c = (k * tpr + in) * N;
+            if (c < p.K) next[k] = __ldg(reinterpret_cast<const V*>(src + static_cast<int64_t>(c) * ES));
+        }
+    };
+    fetch(static_cast<int64_t>(blockIdx.x) * per_block + (threadIdx.x >> p.tpr_log2));
     // (whole blocks walk together: the maximum's barriers are the block's)
     for (int64_t rb = static_cast<int64_t>(blockIdx.x) * per_block; rb < p.T; rb += step) {
         const int64_t row = rb + (threadIdx.x >> p.tpr_log2);
         const bool live = row < p.T;
         const char* src = static_cast<const char*>(p.x) + row * p.ld_x * ES;
         V keep[R];
-        // (magnitudes order as integers, infinities above all numbers and NaN above those)
-        uint32_t top = 0;
-        auto take = [&](const V& v) {
-            float f[N];
-            widen<DT, N>(v, f);
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const uint32_t m = __float_as_uint(f[i]) & 0x7fffffffu;
-                top = m > top ? m : top;
-            }
-        };
+        for (int k = 0; k < R; ++k) keep[k] = next[k];
+        fetch(row + step);
+        uint32_t top = 0;
         if (live) {
 #pragma unroll
-            for (int k = 0; k < R; ++k) {
-                const int c = (k * tpr + in) * N;
-                if (c < p.K) keep[k] = __ldg(reinterpret_cast<const V*>(src + static_cast<int64_t>(c) * ES));
-            }
-#pragma unroll
             for (int k = 0; k < R; ++k)
-                if ((k * tpr + in) * N < p.K) take(keep[k]);
+                if ((k * tpr + in) * N < p.K) top = larger<DT, N>(keep[k], top);
             for (int64_t c = (static_cast<int64_t>(R) * tpr + in) * N; c < p.K; c += tpr * N)
-                take(__ldg(reinterpret_cast<const V*>(src + c * ES)));
+                top = larger<DT, N>(__ldg(reinterpret_cast<const V*>(src + c * ES)), top);
         }
+        top = magnitude<DT, N>(top);
         top = __reduce_max_sync(0xffffffffu, top);
         if (warps > 1) {
             __syncthreads();  // (the row before has been read)
@@ -138,26 +219,30 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantParams p)
         const float r = some ? __fdiv_rn(127.0f, big) : 0.0f;
         char* dst = static_cast<char*>(p.q) + row * p.ld_q * (WIDE ? 2 : 1);
         auto put = [&](const V& v, int64_t c) {
-            float f[N];
+            float f[N], t[N];
             widen<DT, N>(v, f);
-            O o;
+            if (even != 1.0f) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const float n = some ? quotient(f[i] * even, big, r) : 0.0f;
-                if constexpr (WIDE)
-                    reinterpret_cast<uint16_t*>(&o)[i] = __half_as_ushort(__float2half_rn(n));
-                else
-                    reinterpret_cast<int8_t*>(&o)[i] = static_cast<int8_t>(__float2int_rn(n));
+                for (int i = 0; i < N; ++i) f[i] *= even;
             }
-            *reinterpret_cast<O*>(dst + c * (WIDE ? 2 : 1)) = o;
+            quotients<N>(f, big, r, t);
+            store_integers<N, WIDE>(dst + c * (WIDE ? 2 : 1), t);
         };
+        if (some) {
 #pragma unroll
-        for (int k = 0; k < R; ++k) {
-            const int c = (k * tpr + in) * N;
-            if (c < p.K) put(keep[k], c);
+            for (int k = 0; k < R; ++k) {
+                const int c = (k * tpr + in) * N;
+                if (c < p.K) put(keep[k], c);
+            }
+            for (int64_t c = (static_cast<int64_t>(R) * tpr + in) * N; c < p.K; c += tpr * N)
+                put(__ldg(reinterpret_cast<const V*>(src + c * ES)), c);
+        } else {
+            float zero[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) zero[i] = kToInt;
+            for (int64_t c = in * N; c < p.K; c += tpr * N)
+                store_integers<N, WIDE>(dst + c * (WIDE ? 2 : 1), zero);
         }
-        for (int64_t c = (static_cast<int64_t>(R) * tpr + in) * N; c < p.K; c += tpr * N)
-            put(__ldg(reinterpret_cast<const V*>(src + c * ES)), c);
         if (WIDE)
             for (int c = p.K + in; c < p.pad; c += tpr) reinterpret_cast<uint16_t*>(dst)[c] = 0;
     }
@@ -174,7 +259,7 @@ cudaError_t quantize_launch(QuantParams p, int sms, cudaStream_t stream) {
     // a thread takes two units or more where the row has them: fewer barriers
     p.tpr_log2 = row_threads((static_cast<int64_t>(p.K) + 2 * N - 1) / (2 * N));
     int64_t blocks = cdiv(p.T, kThreads >> p.tpr_log2);
-    if (blocks > int64_t(sms) * 8) blocks = int64_t(sms) * 8;
+    if (blocks > int64_t(sms) * kQuantBlocksPerSm) blocks = int64_t(sms) * kQuantBlocksPerSm;
     quantize_kernel<DT, N, WIDE><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }

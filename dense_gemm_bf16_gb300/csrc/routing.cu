@@ -53,6 +53,7 @@ struct DispatchParams {
     int32_t vecs;           // units of the copy in a row
     int32_t tpt_log2;       // threads that share a token's row
     int32_t warps;          // segments of a block's range
+    int32_t ahead;          // tokens of a range that are prefetched
     int* status;
 };
 
@@ -89,7 +90,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_count_kernel(const Dispat
 // Offsets, slots and rows.  V: the copy's unit, which divides the rows' size, pitches and
 // addresses.
 template <typename ID, typename V>
-__global__ void __launch_bounds__(kRouteThreads) dispatch_kernel(const DispatchParams p) {
+__global__ void __launch_bounds__(kRouteThreads, 1) dispatch_kernel(const DispatchParams p) {
     extern __shared__ int smem[];
     int* before = smem;                  // [groups] first the pairs before this range
     int* total = smem + p.groups;        // [groups] all pairs, then the experts' offsets
@@ -99,6 +100,10 @@ __global__ void __launch_bounds__(kRouteThreads) dispatch_kernel(const DispatchP
     const int64_t t0 = route_first(p, b, blocks), t1 = route_first(p, b + 1, blocks);
     const int64_t i0 = t0 * p.top, i1 = t1 * p.top;
     for (int i = tid; i < (2 + p.warps) * E; i += kRouteThreads) smem[i] = 0;
+    // this range's tokens are on their way to L2 while their rows are found
+    if (sizeof(V) == 16)
+        for (int64_t t = t0 + tid; t < t1 && t < t0 + p.ahead; t += kRouteThreads)
+            l2_prefetch(p.x + t * p.x_pitch, static_cast<uint32_t>(p.vecs) * 16u);
     __syncthreads();
     if (p.hist) {
         griddep_wait();
@@ -236,7 +241,8 @@ cudaError_t dispatch_unit(int unit, const DispatchParams& p, int blocks, cudaStr
 // ---------------------------------------------------------------- combine and its gradient
 
 constexpr int kSumThreads = 256;
-constexpr int kSumBlocksPerSm = 8;
+constexpr int kSumBlocksPerSm = 4;      // all resident at once: no second, partial wave
+constexpr int kGradBlocksPerSm = 8;
 
 struct CombineParams {
     const int32_t* slots;    // [T][top]
@@ -332,58 +338,112 @@ __device__ __forceinline__ float combine_weight(const CombineParams& p, int64_t 
                      p.w_dtype);
 }
 
-// A thread takes N neighbouring columns of a token and adds its rows in the order of j, in
-// fp32: four rows' loads are in flight at once.
+// A pair as the block's threads read it: its row (bytes from the first one, negative: none)
+// and weight.
+struct alignas(16) CombinePair {
+    int64_t row;
+    float w;
+};
+constexpr int kSumPairs = 512;  // pairs that a block holds at once, and choices of a token at most
+
+// The pairs of `n` tokens from t on, by all threads of the block.
+__device__ __forceinline__ void combine_pairs(const CombineParams& p, int64_t t, int n, int64_t pitch,
+                                              CombinePair* pairs) {
+    __syncthreads();  // (the ones before have been read)
+    for (int i = threadIdx.x; i < n * p.top; i += kSumThreads) {
+        const int64_t tok = t + i / p.top;
+        const int j = i % p.top, s = combine_slot(p, tok, j);
+        pairs[i].row = s < 0 ? -1 : s * pitch;
+        pairs[i].w = s < 0 ? 0.0f : combine_weight(p, tok, j);
+    }
+    __syncthreads();
+}
+
+// N results from element `off` of y on.
 template <int DT, int N>
-__global__ void __launch_bounds__(kSumThreads) combine_kernel(const CombineParams p) {
+__device__ __forceinline__ void combine_store(const CombineParams& p, int64_t off, const float (&sum)[N]) {
+    if (DT != DT_F32 && p.y_dtype == DT_F32) {
+        float* dst = static_cast<float*>(p.y) + off;
+        if constexpr (N % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < N; i += 4)
+                *reinterpret_cast<float4*>(dst + i) =
+                    make_float4(sum[i], sum[i + 1], sum[i + 2], sum[i + 3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) dst[i] = sum[i];
+        }
+    } else {
+        using V = typename Pack<DT, N>::V;
+        *reinterpret_cast<V*>(static_cast<char*>(p.y) + off * (DT == DT_F32 ? 4 : 2)) = pack<DT, N>(sum);
+    }
+}
+
+// A block owns a range of tokens and reads their slots and weights once, some hundred pairs at
+// a time (every thread for itself, they were most of the instructions: 16384 tokens x 4 of
+// 2048, bf16, 70 us).  A thread takes N neighbouring columns of a token and adds its rows in the
+// order of j, in fp32; the next four rows, of this token or the next, are loaded meanwhile.
+template <int DT, int N>
+__global__ void __launch_bounds__(kSumThreads, kSumBlocksPerSm) combine_kernel(const CombineParams p) {
     using V = typename Pack<DT, N>::V;
-    const int tpt = 1 << p.tpt_log2, in = threadIdx.x & (tpt - 1);
+    constexpr int ES = DT == DT_F32 ? 4 : 2;
+    __shared__ CombinePair pairs[kSumPairs];
+    const int tpt = 1 << p.tpt_log2, in = threadIdx.x & (tpt - 1), mine = threadIdx.x >> p.tpt_log2;
     const int per_block = kSumThreads >> p.tpt_log2;
     const char* rows = static_cast<const char*>(p.rows);
-    constexpr int ES = DT == DT_F32 ? 4 : 2;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * per_block + (threadIdx.x >> p.tpt_log2);
-         t < p.T; t += static_cast<int64_t>(gridDim.x) * per_block) {
-        for (int c = in * N; c < p.K; c += tpt * N) {
-            float sum[N];
+    const int64_t t1 = static_cast<int64_t>(p.T) * (blockIdx.x + 1) / gridDim.x;
+    const int batch = kSumPairs / (p.top > 0 ? p.top : 1);
+    for (int64_t tb = static_cast<int64_t>(p.T) * blockIdx.x / gridDim.x; tb < t1; tb += batch) {
+        const int n = static_cast<int>(t1 - tb < batch ? t1 - tb : batch);
+        combine_pairs(p, tb, n, p.ld_rows * ES, pairs);
+        // (tokens mine, mine + per_block, ...; of each the columns in * N, ...; of those the
+        // pairs by fours)
+        int tok = mine, c = in * N, j0 = 0;
+        V next[4];
+        auto load = [&]() {
 #pragma unroll
-            for (int i = 0; i < N; ++i) sum[i] = 0.0f;
-            for (int j0 = 0; j0 < p.top; j0 += 4) {
-                V v[4];
-                float w[4];
-                bool has[4];
+            for (int k = 0; k < 4; ++k) {
+                if (j0 + k >= p.top) break;
+                const int64_t row = pairs[tok * p.top + j0 + k].row;
+                if (row >= 0) next[k] = __ldg(reinterpret_cast<const V*>(rows + row + static_cast<int64_t>(c) * ES));
+            }
+        };
+        bool more = tok < n && c < p.K;
+        if (more) load();
+        float sum[N];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    has[k] = false;
-                    if (j0 + k >= p.top) continue;
-                    const int s = combine_slot(p, t, j0 + k);
-                    has[k] = s >= 0;
-                    if (!has[k]) continue;
-                    v[k] = __ldg(reinterpret_cast<const V*>(rows + (s * p.ld_rows + c) * ES));
-                    w[k] = combine_weight(p, t, j0 + k);
-                }
+        for (int i = 0; i < N; ++i) sum[i] = 0.0f;
+        while (more) {
+            const int at = tok * p.top + j0, left = p.top - j0;
+            const int64_t off = (tb + tok) * p.ld_y + c;
+            V v[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (!has[k]) continue;
-                    float f[N];
-                    unpack<DT, N>(v[k], f);
-#pragma unroll
-                    for (int i = 0; i < N; ++i) sum[i] = fmaf(w[k], f[i], sum[i]);
+            for (int k = 0; k < 4; ++k) v[k] = next[k];
+            j0 += 4;
+            if (j0 >= p.top) {
+                j0 = 0;
+                c += tpt * N;
+                if (c >= p.K) {
+                    c = in * N;
+                    tok += per_block;
+                    more = tok < n;
                 }
             }
-            const int64_t off = t * p.ld_y + c;
-            if (DT != DT_F32 && p.y_dtype == DT_F32) {
-                float* dst = static_cast<float*>(p.y) + off;
-                if constexpr (N % 4 == 0) {
+            if (more) load();
 #pragma unroll
-                    for (int i = 0; i < N; i += 4)
-                        *reinterpret_cast<float4*>(dst + i) =
-                            make_float4(sum[i], sum[i + 1], sum[i + 2], sum[i + 3]);
-                } else {
+            for (int k = 0; k < 4; ++k) {
+                if (k >= left) break;
+                const CombinePair pair = pairs[at + k];
+                if (pair.row < 0) continue;
+                float f[N];
+                unpack<DT, N>(v[k], f);
 #pragma unroll
-                    for (int i = 0; i < N; ++i) dst[i] = sum[i];
-                }
-            } else {
-                *reinterpret_cast<V*>(static_cast<char*>(p.y) + off * ES) = pack<DT, N>(sum);
+                for (int i = 0; i < N; ++i) sum[i] = fmaf(pair.w, f[i], sum[i]);
+            }
+            if (left <= 4) {
+                combine_store<DT, N>(p, off, sum);
+#pragma unroll
+                for (int i = 0; i < N; ++i) sum[i] = 0.0f;
             }
         }
     }
@@ -395,79 +455,87 @@ template <int DT, int N, int J>
 __global__ void __launch_bounds__(kSumThreads) combine_grad_kernel(const CombineParams p) {
     using V = typename Pack<DT, N>::V;
     constexpr int ES = DT == DT_F32 ? 4 : 2;
+    __shared__ CombinePair pairs[kSumPairs];
     __shared__ float part[kSumThreads / 32][J];
-    const int tpt = 1 << p.tpt_log2, in = threadIdx.x & (tpt - 1);
+    const int tpt = 1 << p.tpt_log2, in = threadIdx.x & (tpt - 1), mine = threadIdx.x >> p.tpt_log2;
     const int per_block = kSumThreads >> p.tpt_log2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = tpt >> 5;
     const char* dy = static_cast<const char*>(p.y);
     const char* rows = static_cast<const char*>(p.rows);
     char* d_rows = static_cast<char*>(p.d_rows);
-    const int64_t step = static_cast<int64_t>(gridDim.x) * per_block;
-    // (whole blocks walk together: the sums' barriers are the block's)
-    for (int64_t tb = static_cast<int64_t>(blockIdx.x) * per_block; tb < p.T; tb += step) {
-        const int64_t t = tb + (threadIdx.x >> p.tpt_log2);
-        const bool live = t < p.T;
-        for (int j0 = 0; j0 < p.top; j0 += J) {
-            int s[J];
-            float w[J], dot[J];
+    const int64_t t1 = static_cast<int64_t>(p.T) * (blockIdx.x + 1) / gridDim.x;
+    const int batch = kSumPairs / p.top;
+    for (int64_t tb = static_cast<int64_t>(p.T) * blockIdx.x / gridDim.x; tb < t1; tb += batch) {
+        const int n = static_cast<int>(t1 - tb < batch ? t1 - tb : batch);
+        combine_pairs(p, tb, n, 1, pairs);  // (row numbers: two pitches)
+        // (whole blocks walk together: the sums' barriers are the block's)
+        for (int t0 = 0; t0 < n; t0 += per_block) {
+            const int tok = t0 + mine;
+            const int64_t t = tb + tok;
+            const bool live = tok < n;
+            for (int j0 = 0; j0 < p.top; j0 += J) {
+                int64_t s[J];
+                float w[J], dot[J];
 #pragma unroll
-            for (int k = 0; k < J; ++k) {
-                s[k] = live && j0 + k < p.top ? combine_slot(p, t, j0 + k) : -1;
-                w[k] = s[k] >= 0 ? combine_weight(p, t, j0 + k) : 0.0f;
-                dot[k] = 0.0f;
-            }
-            if (live)
-                for (int c = in * N; c < p.K; c += tpt * N) {
-                    V r[J];
-                    const V v = *reinterpret_cast<const V*>(dy + (t * p.ld_y + c) * ES);
-                    if (p.d_weights) {
-#pragma unroll
-                        for (int k = 0; k < J; ++k)
-                            if (s[k] >= 0)
-                                r[k] = *reinterpret_cast<const V*>(rows + (s[k] * p.ld_rows + c) * ES);
-                    }
-                    float g[N];
-                    unpack<DT, N>(v, g);
-#pragma unroll
-                    for (int k = 0; k < J; ++k) {
-                        if (s[k] < 0) continue;
-                        float o[N];
+                for (int k = 0; k < J; ++k) {
+                    const bool in_range = live && j0 + k < p.top;
+                    s[k] = in_range ? pairs[tok * p.top + j0 + k].row : -1;
+                    w[k] = in_range ? pairs[tok * p.top + j0 + k].w : 0.0f;
+                    dot[k] = 0.0f;
+                }
+                if (live)
+                    for (int c = in * N; c < p.K; c += tpt * N) {
+                        V r[J];
+                        const V v = *reinterpret_cast<const V*>(dy + (t * p.ld_y + c) * ES);
                         if (p.d_weights) {
-                            unpack<DT, N>(r[k], o);
 #pragma unroll
-                            for (int i = 0; i < N; ++i) dot[k] = fmaf(g[i], o[i], dot[k]);
+                            for (int k = 0; k < J; ++k)
+                                if (s[k] >= 0)
+                                    r[k] = *reinterpret_cast<const V*>(rows + (s[k] * p.ld_rows + c) * ES);
                         }
+                        float g[N];
+                        unpack<DT, N>(v, g);
 #pragma unroll
-                        for (int i = 0; i < N; ++i) o[i] = w[k] * g[i];
-                        *reinterpret_cast<V*>(d_rows + (s[k] * p.ld_drows + c) * ES) = pack<DT, N>(o);
+                        for (int k = 0; k < J; ++k) {
+                            if (s[k] < 0) continue;
+                            float o[N];
+                            if (p.d_weights) {
+                                unpack<DT, N>(r[k], o);
+#pragma unroll
+                                for (int i = 0; i < N; ++i) dot[k] = fmaf(g[i], o[i], dot[k]);
+                            }
+#pragma unroll
+                            for (int i = 0; i < N; ++i) o[i] = w[k] * g[i];
+                            *reinterpret_cast<V*>(d_rows + (s[k] * p.ld_drows + c) * ES) = pack<DT, N>(o);
+                        }
                     }
+                if (!p.d_weights) continue;
+#pragma unroll
+                for (int k = 0; k < J; ++k)
+#pragma unroll
+                    for (int d = 16; d > 0; d >>= 1) dot[k] += __shfl_xor_sync(0xffffffffu, dot[k], d);
+                if (warps > 1) {
+                    __syncthreads();  // (the pairs before have been read)
+                    if (lane == 0) {
+#pragma unroll
+                        for (int k = 0; k < J; ++k) part[warp][k] = dot[k];
+                    }
+                    __syncthreads();
+                    if (in < J) {
+                        float sum = 0.0f;
+                        for (int i = 0; i < warps; ++i) sum += part[warp + i][in];
+                        dot[0] = sum;
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 1; k < J; ++k)
+                        if (lane == k) dot[0] = dot[k];
                 }
-            if (!p.d_weights) continue;
-#pragma unroll
-            for (int k = 0; k < J; ++k)
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1) dot[k] += __shfl_xor_sync(0xffffffffu, dot[k], d);
-            if (warps > 1) {
-                __syncthreads();  // (the pairs before have been read)
-                if (lane == 0) {
-#pragma unroll
-                    for (int k = 0; k < J; ++k) part[warp][k] = dot[k];
-                }
-                __syncthreads();
-                if (in < J) {
-                    float sum = 0.0f;
-                    for (int i = 0; i < warps; ++i) sum += part[warp + i][in];
-                    dot[0] = sum;
-                }
-            } else {
-#pragma unroll
-                for (int k = 1; k < J; ++k)
-                    if (lane == k) dot[0] = dot[k];
+                if (live && in < J && j0 + in < p.top)
+                    store_elem(static_cast<char*>(p.d_weights) +
+                                   (t * p.ld_dw + j0 + in) * dt_size(p.dw_dtype),
+                               p.dw_dtype, dot[0]);
             }
-            if (live && in < J && j0 + in < p.top)
-                store_elem(static_cast<char*>(p.d_weights) +
-                               (t * p.ld_dw + j0 + in) * dt_size(p.dw_dtype),
-                           p.dw_dtype, dot[0]);
         }
     }
 }
@@ -525,7 +593,8 @@ gemm_status_t combine_run(CombineParams& p, int dt, bool grad, cudaStream_t stre
     while (log2 < 8 && (int64_t(1) << log2) < units) ++log2;
     p.tpt_log2 = log2;
     int64_t blocks = cdiv(p.T, kSumThreads >> log2);
-    if (blocks > int64_t(d.sm_count) * kSumBlocksPerSm) blocks = int64_t(d.sm_count) * kSumBlocksPerSm;
+    const int64_t fit = int64_t(d.sm_count) * (grad ? kGradBlocksPerSm : kSumBlocksPerSm);
+    if (blocks > fit) blocks = fit;
     const int n = static_cast<int>(blocks);
     const cudaError_t e = dt == DT_BF16  ? combine_width<DT_BF16>(w.n, p, grad, n, stream)
                           : dt == DT_F16 ? combine_width<DT_F16>(w.n, p, grad, n, stream)
@@ -619,6 +688,8 @@ gemm_status_t gemm_expert_dispatch(int elem_bytes, int64_t T, int64_t K, const v
     p.warps = static_cast<int32_t>(fit < 32 ? fit : 32);
     int64_t blocks = route_blocks(p.T);
     if (blocks > d.sm_count) blocks = d.sm_count;
+    // (96 MB in all: what L2 holds beside the rows on their way out)
+    p.ahead = bytes > 0 && bytes <= 65536 ? static_cast<int32_t>((int64_t(96) << 20) / (bytes * blocks)) : 0;
     const cudaError_t e =
         id_bytes == 8
             ? dispatch_unit<int64_t>(unit, p, static_cast<int>(blocks), static_cast<cudaStream_t>(stream))
@@ -638,7 +709,7 @@ gemm_status_t gemm_expert_combine(gemm_dtype_t dtype, int64_t T, int64_t K, int6
     if (!is_dt(dtype) || !is_dt(y_dtype) || (weights && !is_dt(w_dtype))) return GEMM_ERR_INVALID_ARG;
     const gemm_status_t st = extents(T, K, top, R);
     if (st != GEMM_OK) return st;
-    if (y_dtype != dtype && y_dtype != GEMM_DT_F32) return GEMM_ERR_UNSUPPORTED;
+    if ((y_dtype != dtype && y_dtype != GEMM_DT_F32) || top > kSumPairs) return GEMM_ERR_UNSUPPORTED;
     if (T == 0 || K == 0) return GEMM_OK;
     if (!matrix_ok(Y, T, K, ldy, dt_bytes(y_dtype))) return GEMM_ERR_INVALID_ARG;
     if (top > 0 && (!slots || !aligned(slots, 4))) return GEMM_ERR_INVALID_ARG;
@@ -676,6 +747,7 @@ gemm_status_t gemm_expert_combine_grad(gemm_dtype_t dtype, int64_t T, int64_t K,
         return GEMM_ERR_INVALID_ARG;
     const gemm_status_t st = extents(T, K, top, R);
     if (st != GEMM_OK) return st;
+    if (top > kSumPairs) return GEMM_ERR_UNSUPPORTED;
     if (T == 0 || top == 0) return GEMM_OK;
     if (!slots || !aligned(slots, 4)) return GEMM_ERR_INVALID_ARG;
     if (K > 0 && !matrix_ok(DY, T, K, lddy, dt_bytes(dtype))) return GEMM_ERR_INVALID_ARG;
