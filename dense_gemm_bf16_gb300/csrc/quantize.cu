@@ -3,10 +3,11 @@
 //
 //   s = max |x| / 127,   q = 127 x / max |x| to the nearest integer (ties to even)
 //
-// The quotient is decided exactly: fp32 gives y = x (127 / max |x|) to within 2^-23 of
-// itself, at most 1.6e-5; where y lies within 2^-14 of a border between two integers, the
-// two products 254 |x| and (2 n + 1) max |x| (at most 32 bits each, exact in fp64) are
-// compared instead.  So q does not depend on the reciprocal's rounding, and a result
+// The quotient is decided exactly: fp32 gives y = x (127 / max |x|) to within 2.5 * 2^-23 of
+// itself, at most 3.8e-5; where y lies within 2^-14 of a border between two integers, 254 |x|
+// and (2 n + 1) max |x| are compared exactly instead (in fp32: 16-bit rows whose maximum is
+// 127 times a power of two have half of their larger elements on a border, and took 64-bit
+// products for all of them, alone on an SM; 4096 x 4096: 20 us).  So q does not depend on the reciprocal's rounding, and a result
 // computed in 64 bits is the same integer.
 //
 // One pass over the data: the threads of a row (a warp's worth at least, a block's at
@@ -68,29 +69,35 @@ __device__ __forceinline__ void widen(const V& v, float (&f)[N]) {
     }
 }
 
-// The larger magnitudes of a unit's elements and `top`, as bit patterns, which order as
-// integers: infinities above all numbers, NaN above those.  (16-bit pairs two at a time.)
+// The larger magnitudes of a unit's elements and `top`: 16-bit elements two at a time and as
+// they are (a NaN stays), fp32 as bit patterns, which order as integers, infinities above all
+// numbers and NaN above those.
 template <int DT, int N, typename V>
 __device__ __forceinline__ uint32_t larger(const V& v, uint32_t top) {
-    if constexpr (DT == DT_F32) {
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
+    const uint32_t one = N == 1 ? static_cast<uint32_t>(*reinterpret_cast<const typename Raw<DT == DT_F32 ? 4 : 2>::V*>(&v)) : 0u;
+    const uint32_t* w = N == 1 ? &one : reinterpret_cast<const uint32_t*>(&v);
 #pragma unroll
-        for (int i = 0; i < N; ++i) top = max(top, w[i] & 0x7fffffffu);
-    } else if constexpr (N == 1) {
-        top = max(top, static_cast<uint32_t>(v) & 0x7fffu);
-    } else {
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
+    for (int i = 0; i < (DT == DT_F32 ? N : (N + 1) / 2); ++i) {
+        if constexpr (DT == DT_F32) {
+            top = max(top, w[i] & 0x7fffffffu);
+        } else if constexpr (DT == DT_BF16) {
+            const __nv_bfloat162 m = __hmax2_nan(__habs2(*reinterpret_cast<const __nv_bfloat162*>(w + i)),
+                                                 *reinterpret_cast<const __nv_bfloat162*>(&top));
+            top = *reinterpret_cast<const uint32_t*>(&m);
+        } else {
+            const __half2 m = __hmax2_nan(__habs2(*reinterpret_cast<const __half2*>(w + i)),
+                                          *reinterpret_cast<const __half2*>(&top));
+            top = *reinterpret_cast<const uint32_t*>(&m);
+        }
     }
     return top;
 }
 
 // ... of a thread, as fp32 bits.
-template <int DT, int N>
+template <int DT>
 __device__ __forceinline__ uint32_t magnitude(uint32_t top) {
     if constexpr (DT == DT_F32) return top;
-    const uint32_t h = N == 1 ? top : max(top & 0xffffu, top >> 16);
+    const uint32_t h = max(top & 0x7fffu, (top >> 16) & 0x7fffu);
     return DT == DT_BF16 ? h << 16
                          : __float_as_uint(__half2float(__ushort_as_half(static_cast<uint16_t>(h))));
 }
@@ -99,16 +106,18 @@ __device__ __forceinline__ uint32_t magnitude(uint32_t top) {
 // ties to even; the sum's low bits are the integer.
 constexpr float kToInt = 12582912.0f;  // 1.5 * 2^23
 
-// 127 x / top decided exactly, where fp32's y may lie on the wrong side of a border.
-__device__ __noinline__ float quotient_exact(float x, float y, float top) {
-    const float lo = floorf(fabsf(y));
-    const double a = 254.0 * static_cast<double>(fabsf(x));
-    const double b = (2.0 * static_cast<double>(lo) + 1.0) * static_cast<double>(top);
-    const bool odd = (static_cast<int>(lo) & 1) != 0;
-    return copysignf(a > b || (a == b && odd) ? lo + 1.0f : lo, x);
+// 127 x / top decided exactly, where fp32's y may lie on the wrong side of the border
+// lo + 1/2: 254 |x| is compared with (2 lo + 1) top, each as its difference from q, the second
+// one's rounded value.  Both differences are exact: the second is a product's rounding error,
+// and the first is below 2^-13 of q and a multiple of the last place of 254 |x|, 32 bits down.
+__device__ __forceinline__ float quotient_exact(float x, float y, float top) {
+    const float lo = floorf(fabsf(y)), odd = 2.0f * lo + 1.0f;
+    const float q = odd * top, b = fmaf(odd, top, -q), a = fmaf(254.0f, fabsf(x), -q);
+    const bool up = a > b || (a == b && (static_cast<int>(lo) & 1) != 0);
+    return copysignf(up ? lo + 1.0f : lo, x);
 }
 
-// N quotients 127 x / top as rounded integers + kToInt; r = 127 / top rounded.
+// N quotients 127 x / top as rounded integers + kToInt; r = 127 / top within 2 ulp.
 template <int N>
 __device__ __forceinline__ void quotients(const float (&x)[N], float top, float r, float (&t)[N]) {
     float far = 0.0f;
@@ -197,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, kQuantBlocksPerSm) quantize_kernel(c
             for (int64_t c = (static_cast<int64_t>(R) * tpr + in) * N; c < p.K; c += tpr * N)
                 top = larger<DT, N>(__ldg(reinterpret_cast<const V*>(src + c * ES)), top);
         }
-        top = magnitude<DT, N>(top);
+        top = magnitude<DT>(top);
         top = __reduce_max_sync(0xffffffffu, top);
         if (warps > 1) {
             __syncthreads();  // (the row before has been read)
@@ -216,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, kQuantBlocksPerSm) quantize_kernel(c
         const float even = size < 0x1p-40f ? 0x1p100f : (size > 0x1p100f ? 0x1p-100f : 1.0f);
         const float big = size * even;
         const bool some = finite && top != 0;
-        const float r = some ? __fdiv_rn(127.0f, big) : 0.0f;
+        const float r = some ? __fdividef(127.0f, big) : 0.0f;  // (within 2 ulp)
         char* dst = static_cast<char*>(p.q) + row * p.ld_q * (WIDE ? 2 : 1);
         auto put = [&](const V& v, int64_t c) {
             float f[N], t[N];
@@ -256,8 +265,11 @@ int row_threads(int64_t units) {
 
 template <int DT, int N, bool WIDE>
 cudaError_t quantize_launch(QuantParams p, int sms, cudaStream_t stream) {
-    // a thread takes two units or more where the row has them: fewer barriers
-    p.tpr_log2 = row_threads((static_cast<int64_t>(p.K) + 2 * N - 1) / (2 * N));
+    // as few threads a row as keep it, but enough rows' worth of threads to fill the GPU: what
+    // a thread does once a row costs as much as eight elements
+    constexpr int keep = quant_keep<DT>(N);
+    p.tpr_log2 = row_threads((static_cast<int64_t>(p.K) + keep - 1) / keep);
+    while (p.tpr_log2 < 8 && (int64_t(p.T) << p.tpr_log2) < int64_t(sms) * kThreads) ++p.tpr_log2;
     int64_t blocks = cdiv(p.T, kThreads >> p.tpr_log2);
     if (blocks > int64_t(sms) * kQuantBlocksPerSm) blocks = int64_t(sms) * kQuantBlocksPerSm;
     quantize_kernel<DT, N, WIDE><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p);

@@ -242,7 +242,6 @@ cudaError_t dispatch_unit(int unit, const DispatchParams& p, int blocks, cudaStr
 
 constexpr int kSumThreads = 256;
 constexpr int kSumBlocksPerSm = 4;      // all resident at once: no second, partial wave
-constexpr int kGradBlocksPerSm = 8;
 
 struct CombineParams {
     const int32_t* slots;    // [T][top]
@@ -593,7 +592,8 @@ gemm_status_t combine_run(CombineParams& p, int dt, bool grad, cudaStream_t stre
     while (log2 < 8 && (int64_t(1) << log2) < units) ++log2;
     p.tpt_log2 = log2;
     int64_t blocks = cdiv(p.T, kSumThreads >> log2);
-    const int64_t fit = int64_t(d.sm_count) * (grad ? kGradBlocksPerSm : kSumBlocksPerSm);
+    // (eight pairs at once of whole 16 bytes take 114 registers: two blocks)
+    const int64_t fit = int64_t(d.sm_count) * (grad && p.top > 4 && w.n == full ? 2 : kSumBlocksPerSm);
     if (blocks > fit) blocks = fit;
     const int n = static_cast<int>(blocks);
     const cudaError_t e = dt == DT_BF16  ? combine_width<DT_BF16>(w.n, p, grad, n, stream)
