@@ -317,17 +317,18 @@ def w4_gemm(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, *, zeros=Non
     return out
 
 
-def _ids(ids):
-    """(pointer, bytes, row pitch) of a [T, top] matrix of expert ids."""
-    if ids.dim() != 2 or ids.dtype not in (torch.int32, torch.int64):
-        raise TypeError("ids must be a [T, top] matrix of int32 or int64 "
-                        f"(it is {ids.dtype} of shape {tuple(ids.shape)})")
-    return ids.data_ptr(), 4 if ids.dtype is torch.int32 else 8, _ld("ids", ids)
+def _elsewhere(dev, *tensors):
+    """Is one of them not on CUDA device `dev`?  (_wrong_device then says which.)"""
+    if dev < 0:
+        return True
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            return True
+    return False
 
 
 def _slots(slots, T):
-    if slots.dim() != 2 or slots.shape[0] != T or slots.dtype is not torch.int32 or \
-            not slots.is_contiguous():
+    if slots.dtype is not torch.int32 or slots.shape[0] != T or not slots.is_contiguous():
         raise ValueError(f"slots must be a contiguous int32 matrix of {T} rows (it is {slots.dtype} "
                          f"of shape {tuple(slots.shape)})")
     return slots.data_ptr()
@@ -345,7 +346,10 @@ def _pair_weights(weights, slots):
     return weights.data_ptr(), _CODE[weights.dtype], _ld("weights", weights)
 
 
-_COPIED = (torch.bfloat16, torch.float16, torch.float32, torch.int8)
+_COPIED = {torch.bfloat16: 2, torch.float16: 2, torch.float32: 4, torch.int8: 1}
+_ID_BYTES = {torch.int32: 4, torch.int64: 8}
+# Pairs up to which a dispatch needs no workspace (the library refuses a call that does).
+_ONE_PASS = 4096
 
 
 def expert_dispatch(x: torch.Tensor, ids: torch.Tensor, experts: int, *, scales=None, out=None,
@@ -363,19 +367,20 @@ def expert_dispatch(x: torch.Tensor, ids: torch.Tensor, experts: int, *, scales=
 
     The gradient of x is ``expert_combine(d_rows, slots)``.
     """
-    if x.dtype not in _COPIED:
-        raise TypeError("x must be bfloat16, float16, float32 or int8")
+    elem_bytes, id_bytes = _COPIED.get(x.dtype), _ID_BYTES.get(ids.dtype)
+    if elem_bytes is None or id_bytes is None:
+        raise TypeError("x must be bfloat16, float16, float32 or int8, ids int32 or int64")
     if x.dim() != 2 or ids.dim() != 2 or ids.shape[0] != x.shape[0]:
         raise ValueError(f"shape mismatch: x{tuple(x.shape)} ids{tuple(ids.shape)}")
     if experts < 0:
         raise ValueError("the number of experts must not be negative")
     dev = x.get_device()
-    _wrong_device(dev, x=x, ids=ids, scales=scales, out=out, out_scales=out_scales,
-                  workspace=workspace)
+    if _elsewhere(dev, ids, scales, out, out_scales, workspace):
+        _wrong_device(dev, x=x, ids=ids, scales=scales, out=out, out_scales=out_scales,
+                      workspace=workspace)
     _require_current(dev)
     T, K = x.shape
     top = ids.shape[1]
-    pi, id_bytes, ld_ids = _ids(ids)
     ps = po = 0
     if scales is not None:
         if scales.dtype != torch.float32 or scales.shape != (T,) or not scales.is_contiguous():
@@ -390,13 +395,14 @@ def expert_dispatch(x: torch.Tensor, ids: torch.Tensor, experts: int, *, scales=
     out = _out("out", out, (T * top, K), None, x, (x.dtype,), stream)
     offsets = _empty((experts + 1,), torch.int32, x, stream)
     slots = _empty((T, top), torch.int32, x, stream)
-    ldx, ldo = _ld("x", x), _ld("out", out)
-    need = _fn("gemm_expert_dispatch_workspace_size")(T, top, experts) if workspace is None else 0
+    need = 0
+    if workspace is None and T * top > _ONE_PASS:
+        need = _fn("gemm_expert_dispatch_workspace_size")(T, top, experts)
     workspace, ws, ws_bytes = _scratch(workspace, need, x, stream)
-    st = _fn("gemm_expert_dispatch")(x.element_size(), T, K, x.data_ptr(), ldx, ps, id_bytes, pi,
-                                     ld_ids, top, experts, out.data_ptr(), ldo, po,
-                                     offsets.data_ptr(), slots.data_ptr(), ws, ws_bytes,
-                                     _raw_stream(dev) if stream is None else stream)
+    st = _fn("gemm_expert_dispatch")(elem_bytes, T, K, x.data_ptr(), _ld("x", x), ps, id_bytes,
+                                     ids.data_ptr(), _ld("ids", ids), top, experts, out.data_ptr(),
+                                     _ld("out", out), po, offsets.data_ptr(), slots.data_ptr(), ws,
+                                     ws_bytes, _raw_stream(dev) if stream is None else stream)
     if st:
         check(st)
     return (out, offsets, slots) if scales is None else (out, offsets, slots, out_scales)
@@ -416,7 +422,8 @@ def expert_combine(rows: torch.Tensor, slots: torch.Tensor, weights: torch.Tenso
     if rows.dim() != 2 or slots.dim() != 2:
         raise ValueError(f"shape mismatch: rows{tuple(rows.shape)} slots{tuple(slots.shape)}")
     dev = rows.get_device()
-    _wrong_device(dev, rows=rows, slots=slots, weights=weights, out=out)
+    if _elsewhere(dev, slots, weights, out):
+        _wrong_device(dev, rows=rows, slots=slots, weights=weights, out=out)
     _require_current(dev)
     R, K = rows.shape
     T, top = slots.shape
@@ -448,7 +455,8 @@ def expert_combine_grad(dy: torch.Tensor, slots: torch.Tensor, weights: torch.Te
     if dy.dim() != 2 or slots.dim() != 2:
         raise ValueError(f"shape mismatch: dy{tuple(dy.shape)} slots{tuple(slots.shape)}")
     dev = dy.get_device()
-    _wrong_device(dev, dy=dy, slots=slots, weights=weights, rows=rows, out=out)
+    if _elsewhere(dev, slots, weights, rows, out):
+        _wrong_device(dev, dy=dy, slots=slots, weights=weights, rows=rows, out=out)
     _require_current(dev)
     T, K = dy.shape
     psl = _slots(slots, T)
@@ -488,7 +496,8 @@ def i8_quantize(x: torch.Tensor, *, out=None, out_scales=None, stream=None):
     if x.dim() < 2:
         raise ValueError("x must have at least two dimensions")
     dev = x.get_device()
-    _wrong_device(dev, x=x, out=out, out_scales=out_scales)
+    if _elsewhere(dev, out, out_scales):
+        _wrong_device(dev, x=x, out=out, out_scales=out_scales)
     _require_current(dev)
     out = _out("out", out, x.shape, None, x, (torch.int8,), stream)
     out_scales = _out("out_scales", out_scales, x.shape[:-1], None, x, (torch.float32,), stream)
@@ -518,6 +527,9 @@ def _row_pitch(name, t):
     return ld
 
 
+_RESULTS = (torch.bfloat16, torch.float16, torch.float32)
+
+
 def i8_gemm(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, *, x_scales=None, offsets=None,
             out=None, bias=None, epilogue=None, out_dtype=None, workspace=None,
             stream=None) -> torch.Tensor:
@@ -545,8 +557,9 @@ def i8_gemm(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, *, x_scales=
                          f"scales{tuple(scales.shape)} "
                          f"({'with' if lead == 3 else 'without'} offsets)")
     dev = x.get_device()
-    _wrong_device(dev, x=x, q=q, scales=scales, x_scales=x_scales, offsets=offsets, out=out,
-                  bias=bias, workspace=workspace)
+    if _elsewhere(dev, q, scales, x_scales, offsets, out, bias, workspace):
+        _wrong_device(dev, x=x, q=q, scales=scales, x_scales=x_scales, offsets=offsets, out=out,
+                      bias=bias, workspace=workspace)
     _require_current(dev)
     T, K = x.shape
     groups = q.shape[0] if lead == 3 else 1
@@ -556,13 +569,12 @@ def i8_gemm(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, *, x_scales=
         raise ValueError(f"x_scales must be a contiguous fp32 vector of {T} values")
     if N > 1 and scales.stride(-1) != 1:
         raise ValueError("scales must have unit inner stride")
-    kinds = (torch.bfloat16, torch.float16, torch.float32)
     if out is None and out_dtype is None and not given:
         out_dtype = x.dtype
-    out = _out("out", out, (T, N), out_dtype, x, kinds, stream)
+    out = _out("out", out, (T, N), out_dtype, x, _RESULTS, stream)
     epi, bias_ptr, stride_bias = _epilogue(epilogue, bias, groups, N)
     off = _offsets(offsets, groups) if offsets is not None else 0
-    ldx, ldq, ldo = _ld("x", x), _ld("q", q), _ld("out", out)
+    ldq = _ld("q", q)
     stride_q, stride_s = (q.stride(0), scales.stride(0)) if groups > 1 else (0, 0)
     dt = 3 if given else _CODE[x.dtype]
     pq = q.data_ptr()
@@ -570,9 +582,9 @@ def i8_gemm(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, *, x_scales=
     if workspace is None:
         need = _fn("gemm_i8_workspace_size")(dt, groups, T, N, K, pq, ldq, stride_q)
     workspace, ws, ws_bytes = _scratch(workspace, need, x, stream)
-    st = _fn("gemm_i8")(dt, groups, T, N, K, x.data_ptr(), ldx, x_scales.data_ptr() if given else 0,
-                        pq, ldq, stride_q, scales.data_ptr(), stride_s, out.data_ptr(), ldo,
-                        _CODE[out.dtype], off, bias_ptr, stride_bias, epi, ws, ws_bytes,
+    st = _fn("gemm_i8")(dt, groups, T, N, K, x.data_ptr(), _ld("x", x), x_scales.data_ptr() if given else 0,
+                        pq, ldq, stride_q, scales.data_ptr(), stride_s, out.data_ptr(),
+                        _ld("out", out), _CODE[out.dtype], off, bias_ptr, stride_bias, epi, ws, ws_bytes,
                         _raw_stream(dev) if stream is None else stream)
     if st:
         check(st)
