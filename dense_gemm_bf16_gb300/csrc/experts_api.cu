@@ -121,7 +121,7 @@ gemm_status_t rg_fill(const RgProblem& q, const DeviceInfo& d, int cg, int bt, R
                       : k_major(&p.tmap_a, q.a, az, p.a_k4, 128)) &&
             (q.b.mn ? mn_major(&p.tmap_b, q.b, bz)
                     : k_major(&p.tmap_b, q.b, bz, p.b_k4, bt / cg) &&
-                          k_major(&p.tmap_b32, q.b, bz, false, 32));
+                          k_major(&p.tmap_b32, q.b, bz, false, q.a8 && bt == 32 ? 16 : 32));
         if (!ok) return GEMM_ERR_CUDA;
     }
     p.idesc = make_idesc_f16(q.dt == DT_BF16, q.a.mn, q.b.mn, 128 * cg, 0);

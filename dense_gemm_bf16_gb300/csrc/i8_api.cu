@@ -156,7 +156,7 @@ gemm_status_t gemm_i8(gemm_dtype_t x_dtype, int64_t groups, int64_t T, int64_t N
     // idle, each with four stages at least
     p.splits = 1;
     if (cg == 1 && bt == 32)
-        while (p.splits < 4 && tiles * p.splits * 2 <= d.sm_count && cdiv(K, 128) >= p.splits * 8)
+        while (p.splits < 4 && tiles * p.splits * 2 <= d.sm_count && cdiv(K, 256) >= p.splits * 4)
             p.splits *= 2;
     int64_t grid = cg == 2 ? d.max_pairs : d.sm_count;
     if (tiles < grid) grid = tiles;

@@ -41,27 +41,36 @@ namespace {
 constexpr int kI8Convert = 8;    // warps that make fp16 weights
 constexpr int kI8Epilogue = 4 + kI8Convert;  // the epilogue's first warp
 constexpr int kI8Threads = 32 * (kI8Epilogue + 8);
-constexpr int kI8Sum = 8;        // stages of 128 that an accumulator takes
+constexpr int kI8Sum = 8;        // 128-deep blocks that an accumulator takes
 constexpr int kI8MaxSplits = 4;
 
 template <int CG, int BT, bool SPLIT>
 struct I8Cfg {
-    static constexpr int B_ROWS = BT / CG;                  // token rows a CTA holds
-    static constexpr uint32_t A_BYTES = 128 * 128;          // int8
-    static constexpr uint32_t B_BYTES = 2 * B_ROWS * 128;   // two 64-deep blocks of fp16
+    static constexpr int B_ROWS = BT / CG;                       // token rows a CTA holds
+    // 128-deep blocks of a stage: a stage costs its roles 500 clocks beside its work, which
+    // narrow tiles, bound by the weights' bytes, do not hide (192 rows over 64 experts, 2048 x
+    // 2048: 59 us with one block)
+    static constexpr int KS = BT <= 64 ? 2 : 1;
+    static constexpr uint32_t A_BLOCK = 128 * 128;               // int8
+    static constexpr uint32_t A_BYTES = KS * A_BLOCK;
+    static constexpr uint32_t B_BLOCK = B_ROWS * 128;            // 64 deep, fp16
+    static constexpr uint32_t B_BYTES = 2 * KS * B_BLOCK;
+    static constexpr int A_COLS = 64 * KS;                       // of a stage in tensor memory
+    static constexpr int SUM = kI8Sum / KS;                      // stages that an accumulator takes
+    static constexpr int SMALL = BT == 32 ? 16 : 32;             // rows of the smaller token boxes
     static constexpr int NC = (BT + 63) / 64;        // 32-column chunks of an epilogue warp
     static constexpr uint32_t D_COLS = 2 * BT;              // two accumulators
-    static constexpr int TA = (512 - D_COLS) / 64 < 4 ? (512 - D_COLS) / 64 : 4;
+    static constexpr int TA = (512 - D_COLS) / A_COLS < 4 ? (512 - D_COLS) / A_COLS : 4;
     static constexpr uint32_t RED_BYTES = SPLIT ? (kI8MaxSplits - 1) * BT * 128 * 4 : 0;
     static constexpr uint32_t BAR_BYTES = 512;
     static constexpr uint32_t EPI_WARP = 2048;  // a staged tile of 32 x 32 16-bit elements
     // stages of tokens, and of weights with what is left
-    static constexpr int SB = BT >= 128 ? (CG == 2 ? 4 : 3) : 6;
+    static constexpr int SB = CG == 2 ? 4 : 3;
     static constexpr int FIT = (kRgMaxSmem - 1024 - BAR_BYTES - RED_BYTES - 8 * EPI_WARP - SB * B_BYTES) / A_BYTES;
     static constexpr int SA = FIT > 10 ? 10 : FIT;
     static constexpr size_t SMEM = 1024 + size_t(SA) * A_BYTES + SB * B_BYTES + RED_BYTES + 8 * EPI_WARP + BAR_BYTES;
     static_assert(TA >= 2 && SA >= 3, "rings");
-    static_assert(B_BYTES % 2048 == 0, "both blocks start on swizzle atoms");
+    static_assert(B_BLOCK % 1024 == 0, "blocks start on swizzle atoms");
     static_assert((2 * (SA + SB + TA) + 6) * 8 + 8 <= BAR_BYTES, "barrier area too small");
     static_assert(!SPLIT || CG == 1, "a tile is shared by single CTAs");
 };
@@ -206,9 +215,9 @@ __device__ __forceinline__ bool i8_wait(uint32_t bar, uint32_t parity, const I8P
 }
 
 // Stages of a tile's contraction that this CTA takes.
-template <bool SPLIT>
+template <bool SPLIT, int KS>
 __device__ __forceinline__ void i8_range(const I8Params& p, const I8Cta& x, int& s0, int& s1) {
-    const int steps = (p.g.K + 127) / 128;
+    const int steps = (p.g.K + 128 * KS - 1) / (128 * KS);
     s0 = SPLIT ? static_cast<int>(static_cast<int64_t>(steps) * x.rank / p.splits) : 0;
     s1 = SPLIT ? static_cast<int>(static_cast<int64_t>(steps) * (x.rank + 1) / p.splits) : steps;
 }
@@ -248,7 +257,7 @@ __device__ __forceinline__ void i8_load_weights(const I8Params& p, const I8Cta& 
     bool ok = true;
     for (int t = x.cl; ok && rg_tile<CG, BT, RG_ROWS>(p.g, walk, t, x.lane, SPLIT ? 0u : x.rank, w); t += x.ncl) {
         int s0, s1;
-        i8_range<SPLIT>(p, x, s0, s1);
+        i8_range<SPLIT, C::KS>(p, x, s0, s1);
         for (int s = s0; s < s1; ++s) {
             ok = rg_warp_wait(x.aempty + 8u * ring.at, ring.phase ^ 1u, x.lane, x.abort_flag, p.g);
             if (p.g.test_stall == 1 && armed == 0) ok = false;  // test only: the others' bounded waits must expire
@@ -256,8 +265,10 @@ __device__ __forceinline__ void i8_load_weights(const I8Params& p, const I8Cta& 
             if (i8_elect()) {
                 const uint32_t bar = x.afull + 8u * ring.at;
                 mbar_arrive_expect_tx(bar, C::A_BYTES);
-                tma_load_3d(x.sA0 + ring.at * C::A_BYTES, &p.g.tmap_a, bar, s * 128, w.lane0,
-                            p.g.a_z ? w.group : 0, pol);
+#pragma unroll
+                for (int j = 0; j < C::KS; ++j)
+                    tma_load_3d(x.sA0 + ring.at * C::A_BYTES + j * C::A_BLOCK, &p.g.tmap_a, bar,
+                                (s * C::KS + j) * 128, w.lane0, p.g.a_z ? w.group : 0, pol);
             }
             ++armed;
             ring.next();
@@ -282,12 +293,12 @@ __device__ __forceinline__ void i8_load_tokens(const I8Params& p, const I8Cta& x
         const int n_mma = rg_uniform(w.n_mma);
         const int rows_b = n_mma / CG;
         const int b_row = rg_uniform(w.b_row) + (CG == 2 ? static_cast<int>(x.rank) * rows_b : 0);
-        // whole-tile boxes, or 32-row boxes where those are fewer bytes
+        // whole-tile boxes, or smaller ones where those are fewer bytes
         const bool big = 4 * rows_b > 3 * C::B_ROWS;
-        const int nb = big ? 1 : (rows_b + 31) / 32;
-        const uint32_t bytes = big ? C::B_BYTES : nb * 8192u;
+        const int nb = big ? 1 : (rows_b + C::SMALL - 1) / C::SMALL;
+        const uint32_t bytes = big ? C::B_BYTES : nb * (C::SMALL * 256u * C::KS);
         int s0, s1;
-        i8_range<SPLIT>(p, x, s0, s1);
+        i8_range<SPLIT, C::KS>(p, x, s0, s1);
         for (int s = s0; s < s1; ++s) {
             ok = rg_warp_wait(x.bempty + 8u * ring.at, ring.phase ^ 1u, x.lane, x.abort_flag, p.g);
             if (!ok) break;
@@ -297,17 +308,20 @@ __device__ __forceinline__ void i8_load_tokens(const I8Params& p, const I8Cta& x
                 const uint32_t dst = x.sB0 + ring.at * C::B_BYTES;
                 if (CG == 1 || x.leader) mbar_arrive_expect_tx(fb, CG * bytes);
                 if (big) {
-                    tma_load_4d_cg<CG>(dst, &p.g.tmap_b, bar, 0, b_row, 2 * s, 0, pol);
+#pragma unroll
+                    for (int j = 0; j < C::KS; ++j)
+                        tma_load_4d_cg<CG>(dst + 2 * j * C::B_BLOCK, &p.g.tmap_b, bar, 0, b_row,
+                                           2 * (s * C::KS + j), 0, pol);
                 } else {
                     for (int h = 0; h < nb; ++h)
-                        for (int blk = 0; blk < 2; ++blk) {
-                            const uint32_t to = dst + blk * (C::B_BYTES / 2) + 4096u * h;
+#pragma unroll
+                        for (int blk = 0; blk < 2 * C::KS; ++blk) {
+                            const uint32_t to = dst + blk * C::B_BLOCK + C::SMALL * 128u * h;
+                            const int k = (2 * C::KS * s + blk) * 64, row = b_row + C::SMALL * h;
                             if constexpr (CG == 2)
-                                tma_load_3d_pair(to, &p.g.tmap_b32, bar, s * 128 + 64 * blk,
-                                                 b_row + 32 * h, 0, pol);
+                                tma_load_3d_pair(to, &p.g.tmap_b32, bar, k, row, 0, pol);
                             else
-                                tma_load_3d(to, &p.g.tmap_b32, bar, s * 128 + 64 * blk,
-                                            b_row + 32 * h, 0, pol);
+                                tma_load_3d(to, &p.g.tmap_b32, bar, k, row, 0, pol);
                         }
                 }
             }
@@ -349,7 +363,7 @@ __device__ __forceinline__ void i8_convert(const I8Params& p, const I8Cta& x, in
     I8Ring<C::TA> out;
     bool ok = true;
     int s0, s1;
-    i8_range<SPLIT>(p, x, s0, s1);
+    i8_range<SPLIT, C::KS>(p, x, s0, s1);
     for (int t = x.cl; ok; t += x.ncl) {
         const bool more = rg_tile<CG, BT, RG_ROWS>(p.g, walk, t, x.lane, SPLIT ? 0u : x.rank, w);
         if (!__all_sync(0xffffffffu, more)) break;
@@ -357,19 +371,25 @@ __device__ __forceinline__ void i8_convert(const I8Params& p, const I8Cta& x, in
             ok = i8_wait(x.afull + 8u * in.at, in.phase, p, x);
             if (!ok) break;
             const uint32_t src = a_row + in.at * C::A_BYTES;
-            uint32_t r[32];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const uint4 v = i8_ld_shared(src + ((c << 4) ^ swz));
-                i8_halves(v.x, r[8 * c], r[8 * c + 1]);
-                i8_halves(v.y, r[8 * c + 2], r[8 * c + 3]);
-                i8_halves(v.z, r[8 * c + 4], r[8 * c + 5]);
-                i8_halves(v.w, r[8 * c + 6], r[8 * c + 7]);
+            for (int j = 0; j < C::KS; ++j) {
+                uint32_t r[32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint4 v = i8_ld_shared(src + j * C::A_BLOCK + ((c << 4) ^ swz));
+                    i8_halves(v.x, r[8 * c], r[8 * c + 1]);
+                    i8_halves(v.y, r[8 * c + 2], r[8 * c + 3]);
+                    i8_halves(v.z, r[8 * c + 4], r[8 * c + 5]);
+                    i8_halves(v.w, r[8 * c + 6], r[8 * c + 7]);
+                }
+                if (j == 0) {
+                    ok = i8_wait(x.wempty + 8u * out.at, out.phase ^ 1u, p, x);
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                }
+                tmem_st_x32(to + out.at * C::A_COLS + j * 64, r);
             }
-            ok = i8_wait(x.wempty + 8u * out.at, out.phase ^ 1u, p, x);
             if (!ok) break;
-            tc_fence_after_sync();
-            tmem_st_x32(to + out.at * 64, r);
             tmem_st_wait();
             tc_fence_before_sync();
             __syncwarp();
@@ -416,15 +436,15 @@ __device__ __forceinline__ void i8_issue(const I8Params& p, const I8Cta& x) {
             umma_commit_cg<CG>(bar);
     };
     int s0, s1;
-    i8_range<SPLIT>(p, x, s0, s1);
+    i8_range<SPLIT, C::KS>(p, x, s0, s1);
     const int steps = rg_uniform(s1 - s0);
     for (int t = x.cl; ok; t += x.ncl) {
         const bool more = rg_tile<CG, BT, RG_ROWS>(p.g, walk, t, x.lane, SPLIT ? 0u : x.rank, w);
         if (!__all_sync(0xffffffffu, more)) break;
         const uint32_t idesc = p.g.idesc | (static_cast<uint32_t>(rg_uniform(w.n_mma) >> 3) << 17);
         for (int s = 0; s < steps; ++s) {
-            const bool fresh = s % kI8Sum == 0;
-            const bool last = s + 1 == steps || s % kI8Sum == kI8Sum - 1;
+            const bool fresh = s % C::SUM == 0;
+            const bool last = s + 1 == steps || s % C::SUM == C::SUM - 1;
             if (fresh) {
                 ok = i8_wait(x.tempty + 8u * acc.at, acc.phase ^ 1u, p, x);
                 if (!ok) break;
@@ -434,15 +454,15 @@ __device__ __forceinline__ void i8_issue(const I8Params& p, const I8Cta& x) {
             if (!ok) break;
             tc_fence_after_sync();
             const uint32_t d = tmem + static_cast<uint32_t>(acc.at * BT);
-            const uint32_t a = tmem + C::D_COLS + static_cast<uint32_t>(wr.at * 64);
+            const uint32_t a = tmem + C::D_COLS + static_cast<uint32_t>(wr.at * C::A_COLS);
             const uint64_t b = b_desc0 + static_cast<uint32_t>(br.at) * (C::B_BYTES >> 4);
             const uint32_t wdone = x.wempty + 8u * wr.at, bdone = x.bempty + 8u * br.at;
             const uint32_t tdone = x.tfull + 8u * acc.at;
             if (i8_elect()) {
                 // (past K both operands are zeros)
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    umma_f16_tmem_a<CG>(d, a + 8 * k, b + (k >> 2) * (C::B_BYTES >> 5) + (k & 3) * 2,
+                for (int k = 0; k < 8 * C::KS; ++k)
+                    umma_f16_tmem_a<CG>(d, a + 8 * k, b + (k >> 2) * (C::B_BLOCK >> 4) + (k & 3) * 2,
                                         idesc, (!fresh || k > 0) ? 1u : 0u);
                 commit(wdone);
                 commit(bdone);
@@ -482,7 +502,7 @@ __device__ __forceinline__ void i8_epilogue(const I8Params& p, const I8Cta& x, i
     if (p.g.pdl) griddep_wait();  // (the tokens' scales)
     for (int t = x.cl; rg_tile<CG, BT, RG_ROWS>(p.g, walk, t, x.lane, SPLIT ? 0u : x.rank, w); t += x.ncl) {
         int s0, s1;
-        i8_range<SPLIT>(p, x, s0, s1);
+        i8_range<SPLIT, C::KS>(p, x, s0, s1);
         const int nl0 = w.lane0 + q * 32;  // first output column of this warp
         const bool mine = c_first < w.ncols && nl0 < p.g.n_lane;
         int v[C::NC][32];
@@ -492,7 +512,7 @@ __device__ __forceinline__ void i8_epilogue(const I8Params& p, const I8Cta& x, i
             for (int i = 0; i < 32; ++i) v[c][i] = 0;
         bool ok = true;
 #pragma unroll 1
-        for (int s = s0; s < s1; s += kI8Sum) {
+        for (int s = s0; s < s1; s += C::SUM) {
             ok = rg_warp_wait(x.tfull + 8u * acc.at, acc.phase, x.lane, x.abort_flag, p.g);
             if (!ok) break;
             tc_fence_after_sync();
