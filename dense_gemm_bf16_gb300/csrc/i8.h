@@ -15,7 +15,7 @@ struct I8Params {
     int64_t stride_ws;
     int32_t splits;          // CTAs of a cluster that share a tile's contraction
 };
-constexpr int kI8PairCols = 160;  // columns of a pair's tile at most
+constexpr int kI8PairCols = 192;  // columns of a pair's tile at most
 // CTAs per tile (1, or 2 with cta_group::2 MMAs) and columns of a tile at most.
 cudaError_t i8_launch(int cg, int bt, const I8Params& p, int grid, cudaStream_t stream);
 cudaError_t i8_prepare();  // kernel attributes (once per device)

@@ -173,35 +173,17 @@ __device__ __forceinline__ bool i8_try_wait_cluster(uint32_t bar, uint32_t parit
     return ok != 0;
 }
 
-// Bounded wait of a whole warp for one phase, or for two.  All lanes poll and
-// vote, which costs least where the phases have completed, and the compiler knows a vote to
-// be the same in all lanes (see i8_issue).
-__device__ __forceinline__ bool i8_wait2(uint32_t bar_a, uint32_t parity_a, uint32_t bar_b,
-                                         uint32_t parity_b, const I8Params& p, const I8Cta& x) {
-    uint64_t t0 = 0;
-    bool a = false, b = false;
-    for (uint32_t it = 1;; ++it) {
-        a = a || mbar_try_wait(bar_a, parity_a);
-        b = b || mbar_try_wait(bar_b, parity_b);
-        if (__all_sync(0xffffffffu, a && b)) return true;
-        if ((it & 63u) == 0) {
-            const uint64_t now = globaltimer_ns();
-            if (t0 == 0) t0 = now;
-            const bool late = now - t0 > p.g.timeout_ns;
-            if (late) {
-                *x.abort_flag = 1;
-                if (p.g.status) DG_SET_TIMEOUT(p.g.status);
-            }
-            if (__any_sync(0xffffffffu, late || *x.abort_flag != 0)) return false;
-        }
-    }
-}
+// Bounded wait of a whole warp.  All lanes ask and vote, which costs least where the phase has
+// completed, and the compiler knows a vote to be the same in all lanes (see i8_issue).  A
+// warp that has to wait is suspended: polling, it took issue slots from the epilogue, which
+// shares its scheduler.
+constexpr uint32_t kI8Suspend = 20000;  // ns
 
 __device__ __forceinline__ bool i8_wait(uint32_t bar, uint32_t parity, const I8Params& p, const I8Cta& x) {
     uint64_t t0 = 0;
     for (uint32_t it = 1;; ++it) {
-        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-        if ((it & 63u) == 0) {
+        if (__all_sync(0xffffffffu, mbar_try_wait_ns(bar, parity, kI8Suspend))) return true;
+        if ((it & 7u) == 0) {
             const uint64_t now = globaltimer_ns();
             if (t0 == 0) t0 = now;
             const bool late = now - t0 > p.g.timeout_ns;
@@ -259,7 +241,7 @@ __device__ __forceinline__ void i8_load_weights(const I8Params& p, const I8Cta& 
         int s0, s1;
         i8_range<SPLIT, C::KS>(p, x, s0, s1);
         for (int s = s0; s < s1; ++s) {
-            ok = rg_warp_wait(x.aempty + 8u * ring.at, ring.phase ^ 1u, x.lane, x.abort_flag, p.g);
+            ok = i8_wait(x.aempty + 8u * ring.at, ring.phase ^ 1u, p, x);
             if (p.g.test_stall == 1 && armed == 0) ok = false;  // test only: the others' bounded waits must expire
             if (!ok) break;
             if (i8_elect()) {
@@ -300,7 +282,7 @@ __device__ __forceinline__ void i8_load_tokens(const I8Params& p, const I8Cta& x
         int s0, s1;
         i8_range<SPLIT, C::KS>(p, x, s0, s1);
         for (int s = s0; s < s1; ++s) {
-            ok = rg_warp_wait(x.bempty + 8u * ring.at, ring.phase ^ 1u, x.lane, x.abort_flag, p.g);
+            ok = i8_wait(x.bempty + 8u * ring.at, ring.phase ^ 1u, p, x);
             if (!ok) break;
             if (i8_elect()) {
                 const uint32_t fb = x.bfull + 8u * ring.at;
@@ -450,7 +432,7 @@ __device__ __forceinline__ void i8_issue(const I8Params& p, const I8Cta& x) {
                 if (!ok) break;
             }
             const uint32_t bbar = x.bfull + 8u * br.at, wbar = x.wfull + 8u * wr.at;
-            ok = i8_wait2(bbar, br.phase, wbar, wr.phase, p, x);
+            ok = i8_wait(bbar, br.phase, p, x) && i8_wait(wbar, wr.phase, p, x);
             if (!ok) break;
             tc_fence_after_sync();
             const uint32_t d = tmem + static_cast<uint32_t>(acc.at * BT);
@@ -482,6 +464,79 @@ __device__ __forceinline__ void i8_issue(const I8Params& p, const I8Cta& x) {
     __syncwarp();
 }
 
+// A chunk's results (`cols` of its tokens and `lanes` of its output columns exist) from
+// element `base` of C on: 16-bit ones through a staged tile, 16 bytes at a time.
+__device__ __forceinline__ void i8_store16(const RgParams& p, int64_t base, int cols, int lanes,
+                                           int lane, uint8_t* buf, const float (&o)[32]) {
+    const int row = lane >> 2, part = lane & 3;
+    uint32_t pk[4][4];
+    rg_pack16(p.c_dtype, o, pk);
+    __syncwarp();  // (the chunk before has left the staged tile)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        stmatrix_x4_trans(smem_u32(buf) + rg_at(lane & 7, lane >> 3) + 512u * i, pk[i][0], pk[i][1],
+                          pk[i][2], pk[i][3]);
+    __syncwarp();
+    if (!p.c_vec) {
+        rg_put_rows(p, buf, base, cols < 32 ? cols : 32, lanes, lane);
+        return;
+    }
+    uint16_t* dst = static_cast<uint16_t*>(p.C) + base + row * p.ldc + 8 * part;
+    if (cols >= 32 && lanes >= 32) {
+        const int64_t step = 8 * p.ldc;
+#pragma unroll
+        for (int it = 0; it < 4; ++it)
+            if (rg_span_ok(p, base + (8 * it + row) * p.ldc + 8 * part, 8))
+                *reinterpret_cast<uint4*>(dst + it * step) =
+                    *reinterpret_cast<const uint4*>(buf + rg_at(8 * it + row, part));
+        return;
+    }
+    const int n = lanes - 8 * part;
+#pragma unroll 1
+    for (int it = 0; it < 4; ++it)
+        if (8 * it + row < cols && n > 0)
+            rg_store8<false>(p, base + (8 * it + row) * p.ldc + 8 * part, n,
+                             *reinterpret_cast<const uint4*>(buf + rg_at(8 * it + row, part)));
+}
+
+// fp32 ones: whole chunks through the staged tile, 16 tokens of 128 bytes at a time (16-byte
+// parts swizzled by the token, conflict-free both ways), others directly: a store of 32 lanes is
+// then 32 bytes in each of four rows.
+__device__ __forceinline__ void i8_store32(const RgParams& p, int64_t base, int cols, int lanes,
+                                           int lane, uint8_t* buf, const float (&o)[32]) {
+    const int pcol = lane >> 2, part = lane & 3;
+    if (p.c_vec && cols >= 32 && lanes >= 32) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            __syncwarp();  // (the tokens before have left the staged tile)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                if (((i >> 3) & 1) != h) continue;
+                const int tok = 8 * ((i >> 2) & 1) + 2 * part + (i & 1);
+                const int n = 8 * (2 * (i >> 4) + ((i >> 1) & 1)) + pcol;
+                *reinterpret_cast<float*>(buf + tok * 128 + (((n >> 2) ^ (2 * part)) << 4) + (n & 3) * 4) = o[i];
+            }
+            __syncwarp();
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
+                const int tok = 4 * it + (lane >> 3), unit = lane & 7;
+                const int64_t off = base + (16 * h + tok) * p.ldc + 4 * unit;
+                if (rg_span_ok(p, off, 4))
+                    *reinterpret_cast<uint4*>(static_cast<float*>(p.C) + off) =
+                        *reinterpret_cast<const uint4*>(buf + tok * 128 + ((unit ^ (((tok >> 1) & 3) * 2)) << 4));
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        const int n = 8 * (2 * (i >> 4) + ((i >> 1) & 1)) + pcol;
+        const int col = 8 * ((i >> 2) & 3) + 2 * part + (i & 1);
+        const int64_t off = base + col * p.ldc + n;
+        if (n < lanes && col < cols && rg_span_ok(p, off, 1)) static_cast<float*>(p.C)[off] = o[i];
+    }
+}
+
 // ------------------------------------------------ epilogue (a warp of eight)
 // Sums stay in the registers in the layout of the matrix loads: of a chunk of 32 tokens, value
 // i is output column 8 (2 (i / 16) + (i / 2) % 2) + lane / 4 and token 8 ((i / 4) % 4) +
@@ -505,33 +560,54 @@ __device__ __forceinline__ void i8_epilogue(const I8Params& p, const I8Cta& x, i
         i8_range<SPLIT, C::KS>(p, x, s0, s1);
         const int nl0 = w.lane0 + q * 32;  // first output column of this warp
         const bool mine = c_first < w.ncols && nl0 < p.g.n_lane;
+        // the scale and bias of one output column and, of each chunk, one token's scale (on
+        // their way before the sums: they took 1000 clocks in front of every tile's output)
+        const bool in = mine && nl0 + x.lane < p.g.n_lane;
+        const float sw_lane = in ? __ldg(p.w_scales + w.group * p.stride_ws + nl0 + x.lane) : 0.0f;
+        const float bias_lane =
+            in && p.g.bias ? __ldg(p.g.bias + w.group * p.g.stride_bias + nl0 + x.lane) : 0.0f;
+        float sx[C::NC];
+#pragma unroll
+        for (int c = 0; c < C::NC; ++c) {
+            const int at = c_first + 64 * c + x.lane;
+            sx[c] = at < w.ncols ? __ldcg(p.x_scales + w.out_row + at) : 0.0f;
+        }
         int v[C::NC][32];
-#pragma unroll
-        for (int c = 0; c < C::NC; ++c)
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[c][i] = 0;
         bool ok = true;
-#pragma unroll 1
-        for (int s = s0; s < s1; s += C::SUM) {
-            ok = rg_warp_wait(x.tfull + 8u * acc.at, acc.phase, x.lane, x.abort_flag, p.g);
-            if (!ok) break;
-            tc_fence_after_sync();
-            if (mine) {
-                const uint32_t from = row + static_cast<uint32_t>(acc.at * BT);
+        // an accumulator to the sums (the first one replaces them)
+        auto add = [&](auto first) {
+            const uint32_t from = row + static_cast<uint32_t>(acc.at * BT);
 #pragma unroll
-                for (int c = 0; c < C::NC; ++c) {
-                    if (c_first + 64 * c < w.ncols) {
+            for (int c = 0; c < C::NC; ++c) {
+                if (c_first + 64 * c < w.ncols) {
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t u[16];
-                            i8_ld16(from + 64u * c + (static_cast<uint32_t>(h) << 20), u);
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t u[16];
+                        i8_ld16(from + 64u * c + (static_cast<uint32_t>(h) << 20), u);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                v[c][16 * h + i] += __float2int_rn(__uint_as_float(u[i]));
+                        for (int i = 0; i < 16; ++i) {
+                            const int n = __float2int_rn(__uint_as_float(u[i]));
+                            v[c][16 * h + i] = decltype(first)::value ? n : v[c][16 * h + i] + n;
                         }
                     }
                 }
             }
+        };
+        if (s0 == s1) {
+#pragma unroll
+            for (int c = 0; c < C::NC; ++c)
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[c][i] = 0;
+        }
+#pragma unroll 1
+        for (int s = s0; s < s1; s += C::SUM) {
+            ok = i8_wait(x.tfull + 8u * acc.at, acc.phase, p, x);
+            if (!ok) break;
+            tc_fence_after_sync();
+            if (mine && s == s0)
+                add(std::true_type());
+            else if (mine)
+                add(std::false_type());
             tc_fence_before_sync();
             __syncwarp();
             if (x.lane == 0)
@@ -576,75 +652,46 @@ __device__ __forceinline__ void i8_epilogue(const I8Params& p, const I8Cta& x, i
                 }
         }
         if (!mine) continue;
-        // this lane's four output columns and, of each chunk, one token
-        float sw[4], bias[4], sx[C::NC];
+        float sw[4], bias[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int n = nl0 + 8 * i + pcol;
-            const bool in = n < p.g.n_lane;
-            sw[i] = in ? __ldg(p.w_scales + w.group * p.stride_ws + n) : 0.0f;
-            bias[i] = in && p.g.bias ? __ldg(p.g.bias + w.group * p.g.stride_bias + n) : 0.0f;
+            sw[i] = __shfl_sync(0xffffffffu, sw_lane, 8 * i + pcol);
+            bias[i] = __shfl_sync(0xffffffffu, bias_lane, 8 * i + pcol);
         }
-#pragma unroll
-        for (int c = 0; c < C::NC; ++c) {
-            const int at = c_first + 64 * c + x.lane;
-            sx[c] = at < w.ncols ? __ldcg(p.x_scales + w.out_row + at) : 0.0f;
-        }
-#pragma unroll
-        for (int c = 0; c < C::NC; ++c) {
-            const int c0 = c_first + 64 * c;
-            if (c0 >= w.ncols) break;
+        // (one copy of the code, the next chunk's sums move to the front: unrolled, it did not
+        // stay in the instruction cache beside the other roles')
+#pragma unroll 1
+        for (int c0 = c_first; c0 < w.ncols; c0 += 64) {
             float o[32];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                const float s = __shfl_sync(0xffffffffu, sx[c], 8 * (k >> 1) + 2 * part + (k & 1));
+                const float s = __shfl_sync(0xffffffffu, sx[0], 8 * (k >> 1) + 2 * part + (k & 1));
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
                     const int i = 16 * (h >> 1) + 4 * (k >> 1) + 2 * (h & 1) + (k & 1);
-                    o[i] = fmaf(__int2float_rn(v[c][i]) * s, sw[h], bias[h]);
+                    o[i] = fmaf(__int2float_rn(v[0][i]) * s, sw[h], bias[h]);
                 }
+            }
+#pragma unroll
+            for (int c = 0; c + 1 < C::NC; ++c) {
+                sx[c] = sx[c + 1];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[c][i] = v[c + 1][i];
             }
             rg_act(o, p.g.act);
-            if (p.g.c_dtype == DT_F32) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const int n = nl0 + 8 * (2 * (i >> 4) + ((i >> 1) & 1)) + pcol;
-                    const int col = c0 + 8 * ((i >> 2) & 3) + 2 * part + (i & 1);
-                    const int64_t off = (w.out_row + col) * p.g.ldc + n;
-                    if (n < p.g.n_lane && col < w.ncols && rg_span_ok(p.g, off, 1))
-                        static_cast<float*>(p.g.C)[off] = o[i];
-                }
-                continue;
-            }
-            uint32_t pk[4][4];
-            rg_pack16(p.g.c_dtype, o, pk);
-            __syncwarp();  // (the chunk before has left the staged tile)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                stmatrix_x4_trans(smem_u32(buf) + rg_at(x.lane & 7, x.lane >> 3) + 512u * i, pk[i][0],
-                                  pk[i][1], pk[i][2], pk[i][3]);
-            __syncwarp();
+            const int left = w.ncols - c0;
             const int64_t base = (w.out_row + c0) * p.g.ldc + nl0;
-            if (!p.g.c_vec) {
-                rg_put_rows(p.g, buf, base, w.ncols - c0 < 32 ? w.ncols - c0 : 32, p.g.n_lane - nl0,
-                            x.lane);
-                continue;
-            }
-            const int nn = p.g.n_lane - nl0 - 8 * part;
-#pragma unroll
-            for (int it = 0; it < 4; ++it) {
-                const int row = 8 * it + pcol;
-                if (c0 + row < w.ncols && nn > 0)
-                    rg_store8<false>(p.g, base + row * p.g.ldc + 8 * part, nn,
-                                     *reinterpret_cast<const uint4*>(buf + rg_at(row, part)));
-            }
+            if (p.g.c_dtype == DT_F32)
+                i8_store32(p.g, base, left, p.g.n_lane - nl0, x.lane, buf, o);
+            else
+                i8_store16(p.g, base, left, p.g.n_lane - nl0, x.lane, buf, o);
         }
     }
 }
 
 // Registers: up to 96 sums a thread of the epilogue's two warpgroups.  640 threads are
-// launched with 96 (i8_prepare checks it): 64 + 2 x 72 + 2 x 136 fit 5 x 96.
-constexpr int I8_LAUNCH_REGS = 96, I8_ISSUE_REGS = 64, I8_CONVERT_REGS = 72, I8_SUM_REGS = 136;
+// launched with 96 (i8_prepare checks it): 48 + 2 x 56 + 2 x 160 fit 5 x 96.
+constexpr int I8_LAUNCH_REGS = 96, I8_ISSUE_REGS = 48, I8_CONVERT_REGS = 56, I8_SUM_REGS = 160;
 static_assert(I8_ISSUE_REGS + 2 * I8_CONVERT_REGS + 2 * I8_SUM_REGS <= 5 * I8_LAUNCH_REGS, "register split");
 
 template <int CG, int BT, bool SPLIT>
