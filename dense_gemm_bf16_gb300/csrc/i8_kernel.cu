@@ -697,7 +697,6 @@ static_assert(I8_ISSUE_REGS + 2 * I8_CONVERT_REGS + 2 * I8_SUM_REGS <= 5 * I8_LA
 template <int CG, int BT, bool SPLIT>
 __global__ void __launch_bounds__(kI8Threads, 1) i8_kernel(const __grid_constant__ I8Params p) {
     using C = I8Cfg<CG, BT, SPLIT>;
-    constexpr bool MOVE = BT > 64;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
@@ -766,13 +765,13 @@ __global__ void __launch_bounds__(kI8Threads, 1) i8_kernel(const __grid_constant
     x.tmem = *tmem_slot;
 
     if (warp >= kI8Epilogue) {
-        if (MOVE) reg_inc<I8_SUM_REGS>();
+        reg_inc<I8_SUM_REGS>();
         i8_epilogue<CG, BT, SPLIT>(p, x, warp, staged + (warp - kI8Epilogue) * C::EPI_WARP);
     } else if (warp >= 4) {
-        if (MOVE) reg_dec<I8_CONVERT_REGS>();
+        reg_dec<I8_CONVERT_REGS>();
         i8_convert<CG, BT, SPLIT>(p, x, warp);
     } else {
-        if (MOVE) reg_dec<I8_ISSUE_REGS>();
+        reg_dec<I8_ISSUE_REGS>();
         if (warp == 0)
             i8_load_tokens<CG, BT, SPLIT>(p, x);
         else if (warp == 1)
@@ -824,7 +823,7 @@ cudaError_t prepare_form() {
     // (a wait for registers that the launch does not have would never end)
     cudaFuncAttributes a;
     if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, i8_kernel<CG, BT, SPLIT>);
-    if (e == cudaSuccess && BT > 64 && a.numRegs < I8_LAUNCH_REGS) e = cudaErrorInvalidConfiguration;
+    if (e == cudaSuccess && a.numRegs < I8_LAUNCH_REGS) e = cudaErrorInvalidConfiguration;
     return e;
 }
 
