@@ -3,12 +3,13 @@
 A layer of experts y = W2_e gelu(W1_e x), each token sent to `top` of them, learns
 to reproduce the outputs of a fixed random layer:
 
-  forward   grouped_gemm, twice
-  backward  grouped_gemm with transposed weights, grouped_gemm_wgrad
+  forward   expert_dispatch (tokens to their experts' rows), grouped_gemm twice, expert_combine
+  backward  expert_combine_grad, grouped_gemm with transposed weights, grouped_gemm_wgrad
   update    newton_schulz of the momentum, one batch over the experts
-  answer    w4_gemm on the weights quantised to 4 bits, token by token
+  answer    w4_gemm on the weights quantised to 4 bits, token by token, and i8_gemm on
+            weights and activations in 8 bits
 
-PyTorch routes the tokens (top-k, sort) and does the element-wise parts.
+PyTorch chooses the experts (softmax, top-k) and does the element-wise parts.
 
     python examples/expert_layer.py
 """
@@ -23,15 +24,9 @@ import dense_gemm_bf16_gb300 as dg  # noqa: E402
 
 
 def route(x, gate, top):
-    """Rows of x in the order of their experts: (token of each row, its share,
-    offsets of the experts' rows)."""
+    """(experts of every token, their shares)."""
     share, expert = torch.softmax(x.float() @ gate, dim=-1).topk(top, dim=-1)
-    share = (share / share.sum(dim=-1, keepdim=True)).reshape(-1)
-    order = torch.argsort(expert.reshape(-1), stable=True)
-    counts = torch.bincount(expert.reshape(-1), minlength=gate.shape[1])
-    offsets = torch.zeros(gate.shape[1] + 1, dtype=torch.int32, device=x.device)
-    offsets[1:] = torch.cumsum(counts, 0)
-    return order // top, share[order], offsets
+    return expert, share / share.sum(dim=-1, keepdim=True)
 
 
 def gelu(h):
@@ -47,24 +42,35 @@ def gelu_grad(h, g):
 
 def layer(x, w1, w2, plan):
     """Outputs per token, and what the backward pass needs."""
-    token, share, offsets = plan
-    rows = x[token]
+    expert, share = plan
+    rows, offsets, slots = dg.expert_dispatch(x, expert, w1.shape[0])
     h = dg.grouped_gemm(rows, w1, offsets)
     z = gelu(h)
     y = dg.grouped_gemm(z, w2, offsets)
-    out = torch.zeros(x.shape, dtype=torch.float32, device=x.device)
-    out.index_add_(0, token, y.float() * share[:, None])
-    return out, (rows, h, z)
+    out = dg.expert_combine(y, slots, share, out_dtype=torch.float32)
+    return out, (rows, h, z, offsets, slots)
 
 
 def gradients(d_out, saved, w2, plan):
-    token, share, offsets = plan
-    rows, h, z = saved
-    d_y = (d_out[token] * share[:, None]).to(rows.dtype)
+    rows, h, z, offsets, slots = saved
+    d_y, _ = dg.expert_combine_grad(d_out, slots, plan[1])
+    d_y = d_y.to(rows.dtype)
     d_w2 = dg.grouped_gemm_wgrad(z, d_y, offsets, out_dtype=torch.float32)
     d_h = gelu_grad(h, dg.grouped_gemm(d_y, w2.transpose(1, 2), offsets))
     d_w1 = dg.grouped_gemm_wgrad(rows, d_h, offsets, out_dtype=torch.float32)
     return d_w1, d_w2
+
+
+def answer_in_8_bits(x, w1, w2, plan):
+    """The layer with 8-bit weights (q [experts, N, K], scales) and activations: a token is
+    quantised once and its bytes go to its experts' rows."""
+    (q1, s1), (q2, s2) = w1, w2
+    expert, share = plan
+    xq, xs = dg.i8_quantize(x)
+    rows, offsets, slots, rows_scales = dg.expert_dispatch(xq, expert, q1.shape[0], scales=xs)
+    h = dg.i8_gemm(rows, q1, s1, x_scales=rows_scales, offsets=offsets, epilogue="gelu_tanh")
+    y = dg.i8_gemm(h, q2, s2, offsets=offsets)
+    return dg.expert_combine(y, slots, share, out_dtype=torch.float32)
 
 
 def quantise(w, group=64):
@@ -111,19 +117,24 @@ def main(tokens=4096, width=1024, hidden=2048, experts=16, top=2, steps=30, quie
             print(f"step {step:3d}  loss {losses[-1]:.5f}")
     w1, w2 = (w.bfloat16() for w in master)
     (q1, s1, z1), (q2, s2, z2) = quantise(w1), quantise(w2)
-    far = size = 0.0
+    in_8_bits = [dg.i8_quantize(w.transpose(1, 2).contiguous()) for w in (w1, w2)]
+    far = far8 = size = 0.0
     for _ in range(4):
         x = normal(1, width).bfloat16()
-        token, share, offsets = route(x, gate, top)
-        full, _ = layer(x, w1, w2, (token, share, offsets))
-        h = dg.w4_gemm(x[token], q1, s1, zeros=z1, offsets=offsets, epilogue="gelu_tanh")
+        expert, share = route(x, gate, top)
+        full, _ = layer(x, w1, w2, (expert, share))
+        rows, offsets, slots = dg.expert_dispatch(x, expert, experts)
+        h = dg.w4_gemm(rows, q1, s1, zeros=z1, offsets=offsets, epilogue="gelu_tanh")
         y = dg.w4_gemm(h, q2, s2, zeros=z2, offsets=offsets)
-        four = torch.zeros_like(full).index_add_(0, token, y.float() * share[:, None])
+        four = dg.expert_combine(y, slots, share, out_dtype=torch.float32)
+        eight = answer_in_8_bits(x, *in_8_bits, (expert, share))
         far += float((four - full).square().sum())
+        far8 += float((eight - full).square().sum())
         size += float(full.square().sum())
     gap = (far / size) ** 0.5
     if not quiet:
-        print(f"4-bit answers differ from the 16-bit ones by {gap:.3f} of their size")
+        print(f"4-bit answers differ from the 16-bit ones by {gap:.3f} of their size, 8-bit ones "
+              f"by {(far8 / size) ** 0.5:.3f}")
     return losses[0], losses[-1], gap
 
 

@@ -72,7 +72,8 @@ size_t gemm_expert_dispatch_workspace_size(int64_t T, int64_t top, int64_t group
  * (GEMM_ERR_INVALID_ARG of gemm_check_device_status) and adds nothing.
  *
  *   dtype        GEMM_DT_BF16, GEMM_DT_F16 or GEMM_DT_F32.
- *   rows, R, ld_rows   R x K, row-major.      slots   T x top, dense.
+ *   rows, R, ld_rows   R x K, row-major.      slots   T x top, dense; top at most 512
+ *                (more: GEMM_ERR_UNSUPPORTED).
  *   weights, w_dtype, ld_weights   T x top, of any of the three types, or NULL: ones.
  *   Y, ldy       T x K, row-major, y_dtype dtype or GEMM_DT_F32; not over an input.
  */

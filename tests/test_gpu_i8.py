@@ -419,3 +419,68 @@ def test_the_operators_together():
     size = ref.combine(y2, slots.cpu().numpy(), share)[1]
     assert np.all(np.abs(f(y) - want) <= (top + 2) * 2.0 ** -24 * size)
     assert status() == 0
+
+
+def test_debug_build_trips_no_check():
+    """The same sources with device-side bounds checks, in every form of the kernel."""
+    D = dg.debug_lib()
+    rng = np.random.default_rng(21)
+    st = torch.cuda.current_stream().cuda_stream
+    for T, N, K, E in ((3, 200, 8192, 0), (20, 136, 272, 3), (60, 3000, 256, 0), (120, 8200, 256, 2),
+                       (700, 3001, 272, 0), (900, 2056, 272, 3)):
+        x, q, sx, sw = case(rng, T, N, K, E)
+        b = bounds_of([T // 3, 0, T - T // 3 - 1][:E], 1) if E else None
+        if E == 2:
+            b = [1, T // 3, T]
+        xd, qd, sxd, swd = (torch.from_numpy(v).to(DEV) for v in (x, q, sx, sw))
+        o = offs(b) if E else None
+        need = D.gemm_i8_workspace_size(3, max(E, 1), T, N, K, qd.data_ptr(), K, N * K)
+        ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+        for out, code in ((BF, 0), (F32, 2)):
+            C = torch.full((T, N), 7.0, dtype=out, device=DEV)
+            assert D.gemm_i8(3, max(E, 1), T, N, K, xd.data_ptr(), K, sxd.data_ptr(), qd.data_ptr(), K,
+                             N * K, swd.data_ptr(), N, C.data_ptr(), N, code,
+                             o.data_ptr() if E else 0, 0, 0, 0, ws.data_ptr(), need, st) == 0
+            assert D.gemm_check_device_status(st) == 0
+            equal_bits(C, x, q, sx, sw, b)
+
+
+@pytest.mark.parametrize("overlap", [0, 1])
+def test_with_and_without_overlap(overlap):
+    """GEMM_OPT_OVERLAP_COPY: the product starts while its tokens are prepared, or after; weights
+    that are copied are waited for either way."""
+    rng = np.random.default_rng(22)
+    dg.gemm_set_option(dg.Option.OVERLAP_COPY, overlap)
+    try:
+        for T, N, K in ((40, 300, 1001), (900, 1500, 320)):
+            c = case(rng, T, N, K)
+            for _ in range(3):
+                equal_bits(run(*c, out_dtype=F32), *c)
+        x = torch.randn((3000, 64), device=DEV).to(BF)
+        ids = torch.randint(0, 30, (3000, 3), device=DEV)
+        rows, offsets, slots = dg.expert_dispatch(x, ids, 30)
+        assert torch.equal(rows[slots.long()], x[:, None].expand(3000, 3, 64))
+    finally:
+        dg.gemm_set_option(dg.Option.OVERLAP_COPY, 0)
+
+
+def test_two_streams_at_once():
+    """Two products and two dispatches in flight together, each with its own workspace."""
+    gen = torch.Generator(device=DEV).manual_seed(8)
+    x = torch.randn((900, 1024), generator=gen, device=DEV).to(BF)
+    q = torch.randint(-127, 128, (3000, 1024), generator=gen, device=DEV, dtype=torch.int8)
+    s = torch.rand(3000, generator=gen, device=DEV)
+    ids = torch.randint(0, 50, (900, 6), generator=gen, device=DEV)
+    want, (rows, offsets, slots) = dg.i8_gemm(x, q, s), dg.expert_dispatch(x, ids, 50)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(10):
+        for st in streams:
+            with torch.cuda.stream(st):
+                got.append((dg.i8_gemm(x, q, s), *dg.expert_dispatch(x, ids, 50)))
+    torch.cuda.synchronize()
+    for y, r, o, sl in got:
+        assert torch.equal(y, want) and torch.equal(r, rows) and torch.equal(o, offsets)
+        assert torch.equal(sl, slots)
+    assert status() == 0

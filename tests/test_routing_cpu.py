@@ -81,6 +81,7 @@ def test_dispatch_refusals(kw, want):
     (dict(rows=None), BAD), (dict(rows=65), BAD), (dict(ld_rows=7), BAD), (dict(slots=None), BAD),
     (dict(slots=66), BAD), (dict(weights=66), BAD), (dict(ld_weights=1), BAD), (dict(Y=None), BAD),
     (dict(Y=65), BAD), (dict(ldy=7), BAD), (dict(Y=66, y_dtype=DType.F32), BAD), (dict(ldy=1 << 60), BAD),
+    (dict(top=513, ld_weights=513), UNSUP),
 ])
 def test_combine_refusals(kw, want):
     assert combine(**kw) == want
@@ -91,7 +92,7 @@ def test_combine_refusals(kw, want):
     (dict(R=BIG), UNSUP), (dict(DY=None), BAD), (dict(DY=65), BAD), (dict(lddy=7), BAD),
     (dict(slots=None), BAD), (dict(weights=66), BAD), (dict(ld_weights=1), BAD), (dict(rows=None), BAD),
     (dict(ld_rows=7), BAD), (dict(d_rows=None), BAD), (dict(d_rows=65), BAD), (dict(ld_drows=7), BAD),
-    (dict(d_weights=66), BAD), (dict(ld_dweights=1), BAD),
+    (dict(d_weights=66), BAD), (dict(ld_dweights=1), BAD), (dict(top=513, ld_weights=513, ld_dweights=513), UNSUP),
 ])
 def test_combine_grad_refusals(kw, want):
     assert grad(**kw) == want
