@@ -317,6 +317,13 @@ def w4_gemm(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, *, zeros=Non
     return out
 
 
+def _rows(name, t):
+    """_ld of a matrix that is usually contiguous or has padded rows."""
+    s0, s1 = t.stride()
+    r, c = t.shape
+    return s0 if s1 == 1 and s0 >= c and r > 1 else _ld(name, t)
+
+
 def _elsewhere(dev, *tensors):
     """Is one of them not on CUDA device `dev`?  (_wrong_device then says which.)"""
     if dev < 0:
@@ -343,7 +350,7 @@ def _pair_weights(weights, slots):
     if weights.shape != slots.shape:
         raise ValueError(f"weights must have the shape of slots, {tuple(slots.shape)} (they have "
                          f"{tuple(weights.shape)})")
-    return weights.data_ptr(), _CODE[weights.dtype], _ld("weights", weights)
+    return weights.data_ptr(), _CODE[weights.dtype], _rows("weights", weights)
 
 
 _COPIED = {torch.bfloat16: 2, torch.float16: 2, torch.float32: 4, torch.int8: 1}
@@ -392,16 +399,20 @@ def expert_dispatch(x: torch.Tensor, ids: torch.Tensor, experts: int, *, scales=
         po = out_scales.data_ptr()
     elif out_scales is not None:
         raise ValueError("out_scales needs scales")
-    out = _out("out", out, (T * top, K), None, x, (x.dtype,), stream)
+    if out is None:
+        out, ldo = _empty((T * top, K), x.dtype, x, stream), max(K, 1)
+    else:
+        out = _out("out", out, (T * top, K), None, x, (x.dtype,), stream)
+        ldo = _rows("out", out)
     offsets = _empty((experts + 1,), torch.int32, x, stream)
     slots = _empty((T, top), torch.int32, x, stream)
     need = 0
     if workspace is None and T * top > _ONE_PASS:
         need = _fn("gemm_expert_dispatch_workspace_size")(T, top, experts)
     workspace, ws, ws_bytes = _scratch(workspace, need, x, stream)
-    st = _fn("gemm_expert_dispatch")(elem_bytes, T, K, x.data_ptr(), _ld("x", x), ps, id_bytes,
-                                     ids.data_ptr(), _ld("ids", ids), top, experts, out.data_ptr(),
-                                     _ld("out", out), po, offsets.data_ptr(), slots.data_ptr(), ws,
+    st = _fn("gemm_expert_dispatch")(elem_bytes, T, K, x.data_ptr(), _rows("x", x), ps, id_bytes,
+                                     ids.data_ptr(), _rows("ids", ids), top, experts,
+                                     out.data_ptr(), ldo, po, offsets.data_ptr(), slots.data_ptr(), ws,
                                      ws_bytes, _raw_stream(dev) if stream is None else stream)
     if st:
         check(st)
@@ -429,9 +440,13 @@ def expert_combine(rows: torch.Tensor, slots: torch.Tensor, weights: torch.Tenso
     T, top = slots.shape
     psl = _slots(slots, T)
     pw, w_dt, ldw = _pair_weights(weights, slots)
-    out = _out("out", out, (T, K), out_dtype, rows, (rows.dtype, torch.float32), stream)
-    st = _fn("gemm_expert_combine")(code, T, K, top, rows.data_ptr(), R, _ld("rows", rows), psl, pw,
-                                    w_dt, ldw, out.data_ptr(), _ld("out", out), _CODE[out.dtype],
+    if out is None and (out_dtype is None or out_dtype is rows.dtype):
+        out, ldo = _empty((T, K), rows.dtype, rows, stream), max(K, 1)
+    else:
+        out = _out("out", out, (T, K), out_dtype, rows, (rows.dtype, torch.float32), stream)
+        ldo = _rows("out", out)
+    st = _fn("gemm_expert_combine")(code, T, K, top, rows.data_ptr(), R, _rows("rows", rows), psl,
+                                    pw, w_dt, ldw, out.data_ptr(), ldo, _CODE[out.dtype],
                                     _raw_stream(dev) if stream is None else stream)
     if st:
         check(st)
@@ -472,10 +487,10 @@ def expert_combine_grad(dy: torch.Tensor, slots: torch.Tensor, weights: torch.Te
     d_weights, pr, ldr, pdw, dw_dt = None, 0, 0, 0, 0
     if rows is not None:
         d_weights = _empty((T, top), torch.float32 if weights is None else weights.dtype, dy, stream)
-        pr, ldr, pdw, dw_dt = rows.data_ptr(), _ld("rows", rows), d_weights.data_ptr(), \
+        pr, ldr, pdw, dw_dt = rows.data_ptr(), _rows("rows", rows), d_weights.data_ptr(), \
             _CODE[d_weights.dtype]
-    st = _fn("gemm_expert_combine_grad")(code, T, K, top, dy.data_ptr(), _ld("dy", dy), psl, pw,
-                                         w_dt, ldw, pr, R, ldr, out.data_ptr(), _ld("out", out),
+    st = _fn("gemm_expert_combine_grad")(code, T, K, top, dy.data_ptr(), _rows("dy", dy), psl, pw,
+                                         w_dt, ldw, pr, R, ldr, out.data_ptr(), _rows("out", out),
                                          pdw, dw_dt, max(top, 1),
                                          _raw_stream(dev) if stream is None else stream)
     if st:
@@ -499,13 +514,21 @@ def i8_quantize(x: torch.Tensor, *, out=None, out_scales=None, stream=None):
     if _elsewhere(dev, out, out_scales):
         _wrong_device(dev, x=x, out=out, out_scales=out_scales)
     _require_current(dev)
-    out = _out("out", out, x.shape, None, x, (torch.int8,), stream)
-    out_scales = _out("out_scales", out_scales, x.shape[:-1], None, x, (torch.float32,), stream)
-    if not out_scales.is_contiguous():
-        raise ValueError("out_scales must be contiguous")
-    st = _fn("gemm_i8_quantize")(code, out_scales.numel(), x.shape[-1], x.data_ptr(),
-                                 _row_pitch("x", x), out.data_ptr(), _row_pitch("out", out),
-                                 out_scales.data_ptr(), _raw_stream(dev) if stream is None else stream)
+    shape = x.shape
+    if out is None:
+        out, ldo = _empty(shape, torch.int8, x, stream), max(shape[-1], 1)
+    else:
+        out = _out("out", out, shape, None, x, (torch.int8,), stream)
+        ldo = _row_pitch("out", out)
+    if out_scales is None:
+        out_scales = _empty(shape[:-1], torch.float32, x, stream)
+    else:
+        out_scales = _out("out_scales", out_scales, shape[:-1], None, x, (torch.float32,), stream)
+        if not out_scales.is_contiguous():
+            raise ValueError("out_scales must be contiguous")
+    st = _fn("gemm_i8_quantize")(code, out_scales.numel(), shape[-1], x.data_ptr(),
+                                 _row_pitch("x", x), out.data_ptr(), ldo, out_scales.data_ptr(),
+                                 _raw_stream(dev) if stream is None else stream)
     if st:
         check(st)
     return out, out_scales
@@ -513,8 +536,10 @@ def i8_quantize(x: torch.Tensor, *, out=None, out_scales=None, stream=None):
 
 def _row_pitch(name, t):
     """Distance of neighbouring rows over all leading dimensions."""
+    if t.dim() == 2:
+        return _rows(name, t)
     ld = _ld(name, t)
-    if t.dim() == 2 or t.is_contiguous():
+    if t.is_contiguous():
         return ld
     rows, step = t.shape[-2], ld * t.shape[-2]
     if rows == 1:                           # (the rows are those of the dimension before)
@@ -552,8 +577,9 @@ def i8_gemm(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, *, x_scales=
     if q.dtype is not torch.int8 or scales.dtype is not torch.float32:
         raise TypeError("q must be int8 and scales float32")
     lead = 3 if offsets is not None else 2
-    if x.dim() != 2 or q.dim() != lead or q.shape[-1] != x.shape[1] or scales.shape != q.shape[:-1]:
-        raise ValueError(f"shape mismatch: x{tuple(x.shape)} q{tuple(q.shape)} "
+    shape = q.shape
+    if x.dim() != 2 or len(shape) != lead or shape[-1] != x.shape[1] or scales.shape != shape[:-1]:
+        raise ValueError(f"shape mismatch: x{tuple(x.shape)} q{tuple(shape)} "
                          f"scales{tuple(scales.shape)} "
                          f"({'with' if lead == 3 else 'without'} offsets)")
     dev = x.get_device()
@@ -562,29 +588,39 @@ def i8_gemm(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, *, x_scales=
                       bias=bias, workspace=workspace)
     _require_current(dev)
     T, K = x.shape
-    groups = q.shape[0] if lead == 3 else 1
-    N = q.shape[-2]
+    groups = shape[0] if lead == 3 else 1
+    N = shape[-2]
     if given and (x_scales.dtype is not torch.float32 or x_scales.shape != (T,) or
                   not x_scales.is_contiguous()):
         raise ValueError(f"x_scales must be a contiguous fp32 vector of {T} values")
     if N > 1 and scales.stride(-1) != 1:
         raise ValueError("scales must have unit inner stride")
-    if out is None and out_dtype is None and not given:
-        out_dtype = x.dtype
-    out = _out("out", out, (T, N), out_dtype, x, _RESULTS, stream)
+    if out is None:
+        if out_dtype is None:
+            out_dtype = torch.bfloat16 if given else x.dtype
+        code = _CODE.get(out_dtype)
+        if code is None:
+            raise TypeError("out must be bfloat16, float16 or float32")
+        out, ldo = _empty((T, N), out_dtype, x, stream), max(N, 1)
+    else:
+        out = _out("out", out, (T, N), out_dtype, x, _RESULTS, stream)
+        code, ldo = _CODE[out.dtype], _rows("out", out)
     epi, bias_ptr, stride_bias = _epilogue(epilogue, bias, groups, N)
     off = _offsets(offsets, groups) if offsets is not None else 0
-    ldq = _ld("q", q)
+    ldq = _rows("q", q) if lead == 2 else _ld("q", q)
     stride_q, stride_s = (q.stride(0), scales.stride(0)) if groups > 1 else (0, 0)
     dt = 3 if given else _CODE[x.dtype]
     pq = q.data_ptr()
     need = 0
     if workspace is None:
-        need = _fn("gemm_i8_workspace_size")(dt, groups, T, N, K, pq, ldq, stride_q)
+        if (pq | ldq | stride_q) & 15 or 0 < stride_q < ldq:  # (the weights are copied)
+            need = _fn("gemm_i8_workspace_size")(dt, groups, T, N, K, pq, ldq, stride_q)
+        else:                               # tokens as 16-bit integers, and their scales
+            need = (T * (K + 63 & -64) * 2 + 255 & -256) + (0 if given else T * 4 + 255 & -256)
     workspace, ws, ws_bytes = _scratch(workspace, need, x, stream)
-    st = _fn("gemm_i8")(dt, groups, T, N, K, x.data_ptr(), _ld("x", x), x_scales.data_ptr() if given else 0,
-                        pq, ldq, stride_q, scales.data_ptr(), stride_s, out.data_ptr(),
-                        _ld("out", out), _CODE[out.dtype], off, bias_ptr, stride_bias, epi, ws, ws_bytes,
+    st = _fn("gemm_i8")(dt, groups, T, N, K, x.data_ptr(), _rows("x", x), x_scales.data_ptr() if given else 0,
+                        pq, ldq, stride_q, scales.data_ptr(), stride_s, out.data_ptr(), ldo, code,
+                        off, bias_ptr, stride_bias, epi, ws, ws_bytes,
                         _raw_stream(dev) if stream is None else stream)
     if st:
         check(st)
