@@ -166,8 +166,21 @@ __device__ __forceinline__ void store_integers(char* dst, const float (&t)[N]) {
     }
 }
 
-// WIDE: fp16 integers, padded; else int8.
-template <int DT, int N, bool WIDE>
+// A unit of a row that lies partly outside it, zeros there.
+template <int ES, int N, typename V>
+__device__ __noinline__ V quant_edge(const char* src, int64_t c, int K) {
+    using E = typename Raw<ES>::V;
+    V v{};
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (c + i >= 0 && c + i < K)
+            reinterpret_cast<E*>(&v)[i] = __ldg(reinterpret_cast<const E*>(src + (c + i) * ES));
+    return v;
+}
+
+// WIDE: fp16 integers, padded; else int8.  EDGE: units may lie partly outside their row (the
+// checks cost 4096 x 4096 bf16 1.3 us of 15).
+template <int DT, int N, bool WIDE, bool EDGE>
 __global__ void __launch_bounds__(kThreads, kQuantBlocksPerSm) quantize_kernel(const QuantParams p) {
     constexpr int ES = DT == DT_F32 ? 4 : 2;
     constexpr int R = quant_keep<DT>(N) / N;
@@ -178,14 +191,24 @@ __global__ void __launch_bounds__(kThreads, kQuantBlocksPerSm) quantize_kernel(c
     const int per_block = kThreads >> p.tpr_log2;
     const int warp = threadIdx.x >> 5, warps = tpr >> 5, lane = threadIdx.x & 31;
     const int64_t step = static_cast<int64_t>(gridDim.x) * per_block;
+    // A row's units start on the boundaries of N elements in memory, so its first and last one
+    // may lie partly outside: `off` elements before the row the first one starts.
+    auto before = [&](const char* src) {
+        return EDGE ? static_cast<int>(reinterpret_cast<uintptr_t>(src) / ES % N) : 0;
+    };
+    auto load = [&](const char* src, int64_t c) {
+        if (!EDGE || (c >= 0 && c + N <= p.K)) return __ldg(reinterpret_cast<const V*>(src + c * ES));
+        return quant_edge<ES, N, V>(src, c, p.K);
+    };
     V next[R];
     auto fetch = [&](int64_t row) {
         if (row >= p.T) return;
         const char* src = static_cast<const char*>(p.x) + row * p.ld_x * ES;
+        const int off = before(src);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            const int c = (k * tpr + in) * N;
-            if (c < p.K) next[k] = __ldg(reinterpret_cast<const V*>(src + static_cast<int64_t>(c) * ES));
+            const int c = (k * tpr + in) * N - off;
+            if (c < p.K) next[k] = load(src, c);
         }
     };
     fetch(static_cast<int64_t>(blockIdx.x) * per_block + (threadIdx.x >> p.tpr_log2));
@@ -194,6 +217,7 @@ __global__ void __launch_bounds__(kThreads, kQuantBlocksPerSm) quantize_kernel(c
         const int64_t row = rb + (threadIdx.x >> p.tpr_log2);
         const bool live = row < p.T;
         const char* src = static_cast<const char*>(p.x) + row * p.ld_x * ES;
+        const int off = before(src);
         V keep[R];
 #pragma unroll
         for (int k = 0; k < R; ++k) keep[k] = next[k];
@@ -202,9 +226,9 @@ __global__ void __launch_bounds__(kThreads, kQuantBlocksPerSm) quantize_kernel(c
         if (live) {
 #pragma unroll
             for (int k = 0; k < R; ++k)
-                if ((k * tpr + in) * N < p.K) top = larger<DT, N>(keep[k], top);
-            for (int64_t c = (static_cast<int64_t>(R) * tpr + in) * N; c < p.K; c += tpr * N)
-                top = larger<DT, N>(__ldg(reinterpret_cast<const V*>(src + c * ES)), top);
+                if ((k * tpr + in) * N - off < p.K) top = larger<DT, N>(keep[k], top);
+            for (int64_t c = (static_cast<int64_t>(R) * tpr + in) * N - off; c < p.K; c += tpr * N)
+                top = larger<DT, N>(load(src, c), top);
         }
         top = magnitude<DT>(top);
         top = __reduce_max_sync(0xffffffffu, top);
@@ -227,6 +251,17 @@ __global__ void __launch_bounds__(kThreads, kQuantBlocksPerSm) quantize_kernel(c
         const bool some = finite && top != 0;
         const float r = some ? __fdividef(127.0f, big) : 0.0f;  // (within 2 ulp)
         char* dst = static_cast<char*>(p.q) + row * p.ld_q * (WIDE ? 2 : 1);
+        auto put_integers = [&](int64_t c, const float (&t)[N]) {
+            if (!EDGE || (c >= 0 && c + N <= p.K)) {
+                store_integers<N, WIDE>(dst + c * (WIDE ? 2 : 1), t);
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const float one[1] = {t[i]};
+                    if (c + i >= 0 && c + i < p.K) store_integers<1, WIDE>(dst + (c + i) * (WIDE ? 2 : 1), one);
+                }
+            }
+        };
         auto put = [&](const V& v, int64_t c) {
             float f[N], t[N];
             widen<DT, N>(v, f);
@@ -235,22 +270,21 @@ __global__ void __launch_bounds__(kThreads, kQuantBlocksPerSm) quantize_kernel(c
                 for (int i = 0; i < N; ++i) f[i] *= even;
             }
             quotients<N>(f, big, r, t);
-            store_integers<N, WIDE>(dst + c * (WIDE ? 2 : 1), t);
+            put_integers(c, t);
         };
         if (some) {
 #pragma unroll
             for (int k = 0; k < R; ++k) {
-                const int c = (k * tpr + in) * N;
+                const int c = (k * tpr + in) * N - off;
                 if (c < p.K) put(keep[k], c);
             }
-            for (int64_t c = (static_cast<int64_t>(R) * tpr + in) * N; c < p.K; c += tpr * N)
-                put(__ldg(reinterpret_cast<const V*>(src + c * ES)), c);
+            for (int64_t c = (static_cast<int64_t>(R) * tpr + in) * N - off; c < p.K; c += tpr * N)
+                put(load(src, c), c);
         } else {
             float zero[N];
 #pragma unroll
             for (int i = 0; i < N; ++i) zero[i] = kToInt;
-            for (int64_t c = in * N; c < p.K; c += tpr * N)
-                store_integers<N, WIDE>(dst + c * (WIDE ? 2 : 1), zero);
+            for (int64_t c = in * N - off; c < p.K; c += tpr * N) put_integers(c, zero);
         }
         if (WIDE)
             for (int c = p.K + in; c < p.pad; c += tpr) reinterpret_cast<uint16_t*>(dst)[c] = 0;
@@ -263,29 +297,34 @@ int row_threads(int64_t units) {
     return log2;
 }
 
-template <int DT, int N, bool WIDE>
+template <int DT, int N, bool WIDE, bool EDGE>
 cudaError_t quantize_launch(QuantParams p, int sms, cudaStream_t stream) {
     // as few threads a row as keep it, but enough rows' worth of threads to fill the GPU: what
     // a thread does once a row costs as much as eight elements
     constexpr int keep = quant_keep<DT>(N);
-    p.tpr_log2 = row_threads((static_cast<int64_t>(p.K) + keep - 1) / keep);
+    // (rows that start inside a unit have one more)
+    p.tpr_log2 = row_threads((static_cast<int64_t>(p.K) + (EDGE ? N - 1 : 0) + keep - 1) / keep);
     while (p.tpr_log2 < 8 && (int64_t(p.T) << p.tpr_log2) < int64_t(sms) * kThreads) ++p.tpr_log2;
     int64_t blocks = cdiv(p.T, kThreads >> p.tpr_log2);
     if (blocks > int64_t(sms) * kQuantBlocksPerSm) blocks = int64_t(sms) * kQuantBlocksPerSm;
-    quantize_kernel<DT, N, WIDE><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p);
+    quantize_kernel<DT, N, WIDE, EDGE><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
 template <int DT, bool WIDE>
 cudaError_t quantize_width(const QuantParams& p, int sms, cudaStream_t stream) {
     constexpr int ES = DT == DT_F32 ? 4 : 2, FULL = 16 / ES;
+    // units of n elements, where an element's place in its unit is the same in X and in Q
     auto fits = [&](int n) {
-        return p.K % n == 0 && aligned(p.x, n * ES) && p.ld_x % n == 0 &&
-               aligned(p.q, n * (WIDE ? 2 : 1)) && p.ld_q % n == 0;
+        return reinterpret_cast<uintptr_t>(p.x) / ES % n ==
+                   reinterpret_cast<uintptr_t>(p.q) / (WIDE ? 2 : 1) % n &&
+               p.ld_x % n == p.ld_q % n;
     };
-    if (fits(FULL)) return quantize_launch<DT, FULL, WIDE>(p, sms, stream);
-    if (fits(2)) return quantize_launch<DT, 2, WIDE>(p, sms, stream);
-    return quantize_launch<DT, 1, WIDE>(p, sms, stream);
+    if (fits(FULL) && p.K % FULL == 0 && p.ld_x % FULL == 0 && aligned(p.x, 16))
+        return quantize_launch<DT, FULL, WIDE, false>(p, sms, stream);
+    if (fits(FULL)) return quantize_launch<DT, FULL, WIDE, true>(p, sms, stream);
+    if (fits(2)) return quantize_launch<DT, 2, WIDE, true>(p, sms, stream);
+    return quantize_launch<DT, 1, WIDE, false>(p, sms, stream);
 }
 
 template <bool WIDE>

@@ -108,6 +108,24 @@ def test_quantize_views_and_leading_dimensions():
     assert dg.i8_quantize(wide[0, :, :0])[1].tolist() == [0.0] * 5
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("K", [5, 37, 96, 1030])
+@pytest.mark.parametrize("x_off,x_pad,q_off,q_pad", [(0, 0, 0, 0), (1, 0, 1, 0), (3, 5, 3, 13), (1, 7, 2, 6),
+                                                     (8, 0, 8, 0), (2, 2, 4, 2), (5, 0, 0, 3)])
+def test_quantize_strides(dtype, K, x_off, x_pad, q_off, q_pad):
+    """Rows that start anywhere in their units, where X's and Q's places agree and where not;
+    what lies around them is neither read as theirs nor written."""
+    rng = np.random.default_rng(K)
+    T = 19
+    wide = torch.full((T, x_off + K + x_pad), float("nan"), dtype=dtype)
+    wide[:, x_off:x_off + K] = torch.from_numpy(rng.standard_normal((T, K)).astype(np.float32)).to(dtype)
+    x = wide.to(DEV)[:, x_off:x_off + K]
+    out = torch.full((T, q_off + K + q_pad), 77, dtype=torch.int8, device=DEV)
+    q, s = dg.i8_quantize(x, out=out[:, q_off:q_off + K])
+    quantized_exactly(x.cpu(), q, s)
+    assert bool((out[:, :q_off] == 77).all()) and bool((out[:, q_off + K:] == 77).all())
+
+
 # ---------------------------------------------------------------- products
 
 def case(rng, T, N, K, experts=0, full=False):
