@@ -241,6 +241,9 @@ __device__ __forceinline__ void i8_load_weights(const I8Params& p, const I8Cta& 
         int s0, s1;
         i8_range<SPLIT, C::KS>(p, x, s0, s1);
         for (int s = s0; s < s1; ++s) {
+            // (from here on it waits for the MMAs, which wait for the tokens' pass: that pass's
+            // time is not the bounded wait's)
+            if (p.g.pdl && armed == C::SA) griddep_wait();
             ok = i8_wait(x.aempty + 8u * ring.at, ring.phase ^ 1u, p, x);
             if (p.g.test_stall == 1 && armed == 0) ok = false;  // test only: the others' bounded waits must expire
             if (!ok) break;
@@ -344,6 +347,7 @@ __device__ __forceinline__ void i8_convert(const I8Params& p, const I8Cta& x, in
     I8Ring<C::SA> in;
     I8Ring<C::TA> out;
     bool ok = true;
+    uint32_t done = 0;  // stages, while the tokens' pass may still run
     int s0, s1;
     i8_range<SPLIT, C::KS>(p, x, s0, s1);
     for (int t = x.cl; ok; t += x.ncl) {
@@ -365,6 +369,7 @@ __device__ __forceinline__ void i8_convert(const I8Params& p, const I8Cta& x, in
                     i8_halves(v.w, r[8 * c + 6], r[8 * c + 7]);
                 }
                 if (j == 0) {
+                    if (p.g.pdl && done++ == C::TA) griddep_wait();
                     ok = i8_wait(x.wempty + 8u * out.at, out.phase ^ 1u, p, x);
                     if (!ok) break;
                     tc_fence_after_sync();
@@ -403,6 +408,7 @@ __device__ __forceinline__ void i8_issue(const I8Params& p, const I8Cta& x) {
     using C = I8Cfg<CG, BT, SPLIT>;
     constexpr uint16_t kPair = 3u;
     if (CG == 2 && !x.leader) return;
+    if (p.g.pdl) griddep_wait();
     const uint64_t b_desc0 = smem_desc_sw128(x.sB0, 16u, 1024u);
     const uint32_t tmem = static_cast<uint32_t>(rg_uniform(static_cast<int>(x.tmem)));
     RgWalk walk = rg_begin<RG_ROWS>(p.g, x.lane);

@@ -363,7 +363,7 @@ def test_a_stalled_pipeline_reports_a_timeout_and_recovers(T, N, K):
         assert status() == dg.Status.ERR_TIMEOUT
     finally:
         dg.gemm_set_option(dg.Option.TEST_STALL, 0)
-        dg.gemm_set_option(dg.Option.TIMEOUT_US, 2000000)
+        dg.gemm_set_option(dg.Option.TIMEOUT_US, 1000000)
     assert status() == 0
     assert torch.equal(run(*c, out_dtype=F32), good)
 
@@ -502,3 +502,18 @@ def test_two_streams_at_once():
         assert torch.equal(y, want) and torch.equal(r, rows) and torch.equal(o, offsets)
         assert torch.equal(sl, slots)
     assert status() == 0
+
+
+def test_the_tokens_pass_does_not_count_as_a_wait():
+    """A short bound on waits inside the product, and tokens whose preparation takes longer."""
+    T, N, K = 400000, 128, 1024
+    x = torch.ones((T, K), dtype=F32, device=DEV)
+    q, s = torch.ones((N, K), dtype=torch.int8, device=DEV), torch.ones(N, device=DEV)
+    dg.gemm_set_option(dg.Option.TIMEOUT_US, 100)
+    try:
+        for _ in range(3):
+            y = dg.i8_gemm(x, q, s, out_dtype=BF)
+            assert status() == 0
+    finally:
+        dg.gemm_set_option(dg.Option.TIMEOUT_US, 1000000)
+    assert bool((y == 1024).all())
