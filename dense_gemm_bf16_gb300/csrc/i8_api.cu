@@ -139,9 +139,9 @@ gemm_status_t gemm_i8(gemm_dtype_t x_dtype, int64_t groups, int64_t T, int64_t N
     q.bias = (epi & 1) ? bias : nullptr;
     q.stride_bias = stride_bias;
     q.act = act;
-    // (copied weights are complete before the tokens' pass, but the kernel reads weights
-    // before it waits for that pass)
-    q.pdl = l.q_bytes == 0;
+    // (the product overlaps the tokens' pass, but reads offsets and weights before it waits for
+    // it: weights must not be copied in front of the pass, and there must be a pass)
+    q.pdl = l.q_bytes == 0 && K > 0;
     int cg, bt;
     i8_variant(q, d, &cg, &bt);
     I8Params p;

@@ -12,17 +12,17 @@
 // What it saves against 16-bit weights is bytes, so the weights stay bytes up to the SM:
 //
 //   warp 2       loads 128 weight rows x 128 bytes by TMA (128-byte swizzle);
-//   warps 4-11   read their lane's row, make fp16 pairs by byte permutes (b ^ 128 under the
+//   warps 4-11   read half of their lane's row, make fp16 pairs by byte permutes (b ^ 128 under the
 //                exponent of 1024 is 1152 + b; one packed subtraction) and store them to
 //                tensor memory, 64 columns a stage;
 //   warp 0       loads the tokens' fp16 rows by TMA (made once per call in the workspace);
 //   warp 1       issues tcgen05.mma with its A operand in tensor memory;
 //   warps 12-19  add accumulators up and write the result.
 //
-// Weights in tensor memory rather than back in shared memory: a stage then moves 16 KB in
-// and out of shared memory for the weights and 24 KB in and out for the tokens in 768
+// Weights in tensor memory rather than back in shared memory: a pair's stage then moves 16 KB
+// in and out of shared memory for the weights and 24 KB in and out for the tokens in 768
 // clocks of MMAs, 107 of the 128 bytes a clock; with fp16 weights stored to shared memory
-// and read from there it would be 150.  Tiles have the weights on the MMA's M side (128 rows
+// and read from there it would be 192.  Tiles have the weights on the MMA's M side (128 rows
 // a CTA, 256 a pair) and the tokens on its N side, which is ragged in steps of 16: as in
 // ragged_kernel.cuh, whose tiles, walk and bounded waits this kernel shares.  A pair's tile
 // has 192 columns, so that two accumulators (384 columns) and two stages of weights (128)
@@ -32,6 +32,14 @@
 // Few tokens leave one tile per 128 weight rows; where those do not fill half of the SMs,
 // the CTAs of a cluster share a tile's contraction and send their integer sums to the first
 // one's shared memory.
+//
+// Bounds and times (graph replay, with the tokens' pass).  One token of 8192 x 8192: 20 us
+// (16 without the quantisation), the bytes take 10: start-up, and 128 of the 152 SMs have a
+// tile.  192 rows over 64 experts of 2048 x 2048: 47 us, the bytes 40.  1500 tokens of 4096 x
+// 4096: 44 us, the bytes of the weights 2.5 and the products 26: two rounds of 128 tiles on 76
+// pairs, and the pass.  16384 rows over 16 experts, 2048 to 4096, GELU: 209 us, the products
+// 143: the MMA pipe is busy 62 % of the time; the issue slots are too (62 %), most of them
+// taken by integer sums, scales, GELU and the conversion of the weights.
 #include "i8.h"
 #include "ragged_kernel.cuh"
 
@@ -49,7 +57,7 @@ struct I8Cfg {
     static constexpr int B_ROWS = BT / CG;                       // token rows a CTA holds
     // 128-deep blocks of a stage: a stage costs its roles 500 clocks beside its work, which
     // narrow tiles, bound by the weights' bytes, do not hide (192 rows over 64 experts, 2048 x
-    // 2048: 59 us with one block)
+    // 2048: 59 us with one block, 47 with two)
     static constexpr int KS = BT <= 64 ? 2 : 1;
     static constexpr uint32_t A_BLOCK = 128 * 128;               // int8
     static constexpr uint32_t A_BYTES = KS * A_BLOCK;
@@ -402,7 +410,7 @@ __device__ __forceinline__ void i8_convert(const I8Params& p, const I8Cta& x, in
 // ------------------------------------------------ MMA issuer (a warp; of the pair's leader)
 // The whole warp walks tiles and stages, every branch decided by a vote, and an elected lane
 // issues.  (Chosen by its number, that lane took 67 clocks to issue an MMA of any size and 100
-// for a commit, 1200 a stage in all; 20 tokens, 19456 x 8192: 47 -> 34 us.)
+// for a commit, 1200 a stage in all: 4096 tokens, 4096 x 4096, 166 us against 129.)
 template <int CG, int BT, bool SPLIT>
 __device__ __forceinline__ void i8_issue(const I8Params& p, const I8Cta& x) {
     using C = I8Cfg<CG, BT, SPLIT>;
@@ -548,8 +556,8 @@ __device__ __forceinline__ void i8_store32(const RgParams& p, int64_t base, int 
 // i is output column 8 (2 (i / 16) + (i / 2) % 2) + lane / 4 and token 8 ((i / 4) % 4) +
 // 2 (lane % 4) + i % 2 of the warp's.  16-bit results go through a staged tile, as
 // in rg_out16, and leave 16 bytes at a time.  (One output column per thread, a shuffle for
-// each token's scale and a two-byte store for each result took 4.5 us a tile: 1500 x 4096 x
-// 4096 46 us.)
+// each token's scale and a two-byte store for each result took 4.5 us a tile: 1500 tokens of
+// 4096 x 4096 46 us, then 42.)
 template <int CG, int BT, bool SPLIT>
 __device__ __forceinline__ void i8_epilogue(const I8Params& p, const I8Cta& x, int warp, uint8_t* buf) {
     using C = I8Cfg<CG, BT, SPLIT>;

@@ -6,16 +6,21 @@
 // The quotient is decided exactly: fp32 gives y = x (127 / max |x|) to within 2.5 * 2^-23 of
 // itself, at most 3.8e-5; where y lies within 2^-14 of a border between two integers, 254 |x|
 // and (2 n + 1) max |x| are compared exactly instead (in fp32: 16-bit rows whose maximum is
-// 127 times a power of two have half of their larger elements on a border, and took 64-bit
-// products for all of them, alone on an SM; 4096 x 4096: 20 us).  So q does not depend on the reciprocal's rounding, and a result
-// computed in 64 bits is the same integer.
+// 127 times a power of two have half of their larger elements on a border; with 64-bit products
+// for those, 4096 x 4096 took 20 us).  So q does not depend on the reciprocal's rounding, and a
+// result computed in 64 bits is the same integer.
 //
 // One pass over the data: the threads of a row (a warp's worth at least, a block's at
 // most) keep its elements in registers between the maximum and the quotients, up to 32
 // each (16 of fp32, and where rows are not aligned), and load the next row's meanwhile;
-// what a row has beyond is read again, from L2.  Bound by the bytes.
+// what a row has beyond is read again, from L2.  4096 x 4096 bf16: 14.5 us, 3.5 TB/s by graph
+// replay, where the copy rate would take 7.4; 1001 x 7001 fp32, rows that start anywhere: 13.4
+// against 5.2.  The instructions bound it (about six an element), then the load of few rows a
+// block (4096 rows on 608 blocks: 6.7 each).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "experts_host.h"
 #include "gemm_experts.h"
@@ -47,10 +52,9 @@ constexpr int kQuantBlocksPerSm = 4;  // all resident at once
 
 template <int BYTES>
 struct Raw {
-    using V = std::conditional_t<BYTES == 16, uint4,
-                                 std::conditional_t<BYTES == 8, uint2,
-                                                    std::conditional_t<BYTES == 4, uint32_t,
-                                                                       std::conditional_t<BYTES == 2, uint16_t, uint8_t>>>>;
+    using Small = std::conditional_t<BYTES == 2, uint16_t, uint8_t>;
+    using Half = std::conditional_t<BYTES == 8, uint2, std::conditional_t<BYTES == 4, uint32_t, Small>>;
+    using V = std::conditional_t<BYTES == 16, uint4, Half>;
 };
 
 // N elements of type DT as fp32 (exact).
@@ -74,7 +78,8 @@ __device__ __forceinline__ void widen(const V& v, float (&f)[N]) {
 // numbers and NaN above those.
 template <int DT, int N, typename V>
 __device__ __forceinline__ uint32_t larger(const V& v, uint32_t top) {
-    const uint32_t one = N == 1 ? static_cast<uint32_t>(*reinterpret_cast<const typename Raw<DT == DT_F32 ? 4 : 2>::V*>(&v)) : 0u;
+    using E = typename Raw<DT == DT_F32 ? 4 : 2>::V;
+    const uint32_t one = N == 1 ? static_cast<uint32_t>(*reinterpret_cast<const E*>(&v)) : 0u;
     const uint32_t* w = N == 1 ? &one : reinterpret_cast<const uint32_t*>(&v);
 #pragma unroll
     for (int i = 0; i < (DT == DT_F32 ? N : (N + 1) / 2); ++i) {

@@ -20,6 +20,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "epilogue.cuh"
 #include "experts_host.h"
 #include "gemm_experts.h"

@@ -618,10 +618,10 @@ def i8_gemm(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, *, x_scales=
         else:                               # tokens as 16-bit integers, and their scales
             need = (T * (K + 63 & -64) * 2 + 255 & -256) + (0 if given else T * 4 + 255 & -256)
     workspace, ws, ws_bytes = _scratch(workspace, need, x, stream)
-    st = _fn("gemm_i8")(dt, groups, T, N, K, x.data_ptr(), _rows("x", x), x_scales.data_ptr() if given else 0,
-                        pq, ldq, stride_q, scales.data_ptr(), stride_s, out.data_ptr(), ldo, code,
-                        off, bias_ptr, stride_bias, epi, ws, ws_bytes,
-                        _raw_stream(dev) if stream is None else stream)
+    st = _fn("gemm_i8")(dt, groups, T, N, K, x.data_ptr(), _rows("x", x),
+                        x_scales.data_ptr() if given else 0, pq, ldq, stride_q, scales.data_ptr(),
+                        stride_s, out.data_ptr(), ldo, code, off, bias_ptr, stride_bias, epi, ws,
+                        ws_bytes, _raw_stream(dev) if stream is None else stream)
     if st:
         check(st)
     return out
