@@ -3,20 +3,23 @@
 //
 //   s = max |x| / 127,   q = 127 x / max |x| to the nearest integer (ties to even)
 //
-// The quotient is decided exactly: fp32 gives y = x (127 / max |x|) to within 2.5 * 2^-23 of
-// itself, at most 3.8e-5; where y lies within 2^-14 of a border between two integers, 254 |x|
-// and (2 n + 1) max |x| are compared exactly instead (in fp32: 16-bit rows whose maximum is
-// 127 times a power of two have half of their larger elements on a border; with 64-bit products
-// for those, 4096 x 4096 took 20 us).  So q does not depend on the reciprocal's rounding, and a
-// result computed in 64 bits is the same integer.
+// The quotient is decided exactly, so q does not depend on the reciprocal's rounding and a
+// result computed in 64 bits is the same integer.  Of fp32 rows, y = x (127 / max |x|) is
+// within 3.2e-5; where it lies within 2^-14 of a border between two integers, 254 |x| and
+// (2 n + 1) max |x| are compared exactly instead.  16-bit rows are often on a border (every
+// element of half the maximum; half of all elements where the maximum is 127 times a power of
+// two), but never very close to one otherwise, so cutting y's last bits off decides them
+// (see quotients; with comparisons 4096 x 4096 took 17.4 us, without 10.7).
 //
 // One pass over the data: the threads of a row (a warp's worth at least, a block's at
 // most) keep its elements in registers between the maximum and the quotients, up to 32
-// each (16 of fp32, and where rows are not aligned), and load the next row's meanwhile;
-// what a row has beyond is read again, from L2.  4096 x 4096 bf16: 14.5 us, 3.5 TB/s by graph
-// replay, where the copy rate would take 7.4; 1001 x 7001 fp32, rows that start anywhere: 13.4
-// against 5.2.  The instructions bound it (about six an element), then the load of few rows a
-// block (4096 rows on 608 blocks: 6.7 each).
+// each (16 where rows are not aligned), and load the next row's meanwhile; what a row has
+// beyond is read again, from L2.  Units that need more care (a border, a scale outside fp32's
+// middle) are read again element by element in one copy of the code: unrolled beside the
+// others it did not stay in the instruction cache (4096 x 4095 fp32: 36 us against 17.6).
+//
+// 4096 x 4096 bf16: 9.7 us by graph replay, 5.2 TB/s, where the copy rate would take 7.4;
+// 1001 x 7001 fp32, rows that start anywhere: 9.7 against 5.2 (3.3 rows for each block).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -31,11 +34,13 @@ namespace dg {
 namespace {
 
 constexpr int kThreads = 256;
-// Elements of a row that a thread keeps (16 registers; the next row's take 16 more).
+// Quantising blocks on an SM, all resident at once.
 template <int DT>
-__host__ __device__ constexpr int quant_keep(int n) {
-    return DT == DT_F32 || n == 1 ? 16 : 32;
-}
+constexpr int kQuantBlocksPerSm = DT == DT_F32 ? 2 : 3;
+// Elements of a row that a thread keeps (16 or 32 registers; the next row's take as many more).
+// fp32 rows of up to 8192 stay on the SM: with 16 elements and twice the blocks, 1001 x 7001
+// took 12 us against 9.7, and 16-bit ones with four blocks 10.7 against 9.7 (4096 x 4096).
+__host__ __device__ constexpr int quant_keep(int n) { return n == 1 ? 16 : 32; }
 
 struct QuantParams {
     const void* x;
@@ -47,8 +52,6 @@ struct QuantParams {
     float* scales;
     int32_t tpr_log2;   // threads of a row
 };
-
-constexpr int kQuantBlocksPerSm = 4;  // all resident at once
 
 template <int BYTES>
 struct Raw {
@@ -107,9 +110,11 @@ __device__ __forceinline__ uint32_t magnitude(uint32_t top) {
                          : __float_as_uint(__half2float(__ushort_as_half(static_cast<uint16_t>(h))));
 }
 
-// Adding and subtracting this rounds an fp32 number of at most 2^22 to the nearest integer,
-// ties to even; the sum's low bits are the integer.
-constexpr float kToInt = 12582912.0f;  // 1.5 * 2^23
+// An fp32 number of at most 2^22 plus this is rounded to the nearest integer n, ties to even,
+// whose bits are the sum's low ones.  For fp16 results (WIDE) the low 16 bits are 0x6480 + n
+// instead, the fp16 number 1152 + n.
+template <bool WIDE>
+constexpr float kToInt = WIDE ? 12582912.0f + 0x6480 : 12582912.0f;  // 1.5 * 2^23
 
 // 127 x / top decided exactly, where fp32's y may lie on the wrong side of the border
 // lo + 1/2: 254 |x| is compared with (2 lo + 1) top, each as its difference from q, the second
@@ -122,23 +127,31 @@ __device__ __forceinline__ float quotient_exact(float x, float y, float top) {
     return copysignf(up ? lo + 1.0f : lo, x);
 }
 
-// N quotients 127 x / top as rounded integers + kToInt; r = 127 / top within 2 ulp.
-template <int N>
-__device__ __forceinline__ void quotients(const float (&x)[N], float top, float r, float (&t)[N]) {
-    float far = 0.0f;
+// N quotients 127 x / top as rounded integers + kToInt.
+//
+// fp32: r = 127 / top within 2 ulp (2^-22); what lies close to a border is decided exactly.
+//
+// 16-bit: 127 x / top is on a border or, m_x below 2^11 being x's significand, at least
+// 1 / (254 m_x) > 2^-19 of itself away from one.  r is 127 / top times 1 + 2^-21, within 2 ulp
+// again, so that x r exceeds the quotient by 2^-23 to 2^-20.2 of itself, and cutting x r off
+// after 20 bits leaves a quotient on a border (8 bits) there and all others on their side of it.
+// True: one of them may be wrong (fp32).
+template <int DT, bool WIDE, int N>
+__device__ __forceinline__ bool quotients(const float (&x)[N], float r, float (&t)[N]) {
+    constexpr float C = kToInt<WIDE>;
+    if constexpr (DT != DT_F32) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const float y = x[i] * r;
-        t[i] = y + kToInt;
-        far = fmaxf(far, fabsf(y - (t[i] - kToInt)));
-    }
-    if (far > 0.5f - 6.103515625e-5f) {
+        for (int i = 0; i < N; ++i)
+            t[i] = __uint_as_float(__float_as_uint(x[i] * r) & 0xfffffff0u) + C;
+        return false;
+    } else {
+        float far = 0.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const float y = x[i] * r;
-            if (fabsf(y - (t[i] - kToInt)) > 0.5f - 6.103515625e-5f)
-                t[i] = quotient_exact(x[i], y, top) + kToInt;
+            t[i] = fmaf(x[i], r, C);
+            far = fmaxf(far, fabsf(fmaf(x[i], r, C - t[i])));
         }
+        return far > 0.5f - 6.103515625e-5f;
     }
 }
 
@@ -147,14 +160,18 @@ template <int N, bool WIDE>
 __device__ __forceinline__ void store_integers(char* dst, const float (&t)[N]) {
     if constexpr (N == 1) {
         if constexpr (WIDE)
-            *reinterpret_cast<__half*>(dst) = __float2half_rn(t[0] - kToInt);
+            *reinterpret_cast<__half*>(dst) = __float2half_rn(t[0] - kToInt<WIDE>);
         else
             *reinterpret_cast<uint8_t*>(dst) = static_cast<uint8_t>(__float_as_uint(t[0]));
     } else if constexpr (WIDE) {
         typename Raw<N * 2>::V o;
         __half2* h = reinterpret_cast<__half2*>(&o);
 #pragma unroll
-        for (int i = 0; i < N / 2; ++i) h[i] = __floats2half2_rn(t[2 * i] - kToInt, t[2 * i + 1] - kToInt);
+        for (int i = 0; i < N / 2; ++i) {
+            const uint32_t w =
+                __byte_perm(__float_as_uint(t[2 * i]), __float_as_uint(t[2 * i + 1]), 0x5410);
+            h[i] = __hsub2(*reinterpret_cast<const __half2*>(&w), __float2half2_rn(1152.0f));
+        }
         *reinterpret_cast<typename Raw<N * 2>::V*>(dst) = o;
     } else if constexpr (N == 2) {
         *reinterpret_cast<uint16_t*>(dst) =
@@ -163,57 +180,57 @@ __device__ __forceinline__ void store_integers(char* dst, const float (&t)[N]) {
         typename Raw<N>::V o;
         uint32_t* w = reinterpret_cast<uint32_t*>(&o);
 #pragma unroll
-        for (int i = 0; i < N / 4; ++i)
-            w[i] = __byte_perm(__byte_perm(__float_as_uint(t[4 * i]), __float_as_uint(t[4 * i + 1]), 0x0040),
-                               __byte_perm(__float_as_uint(t[4 * i + 2]), __float_as_uint(t[4 * i + 3]), 0x0040),
-                               0x5410);
+        for (int i = 0; i < N / 4; ++i) {
+            const uint32_t lo = __byte_perm(__float_as_uint(t[4 * i]), __float_as_uint(t[4 * i + 1]), 0x0040);
+            const uint32_t hi = __byte_perm(__float_as_uint(t[4 * i + 2]), __float_as_uint(t[4 * i + 3]), 0x0040);
+            w[i] = __byte_perm(lo, hi, 0x5410);
+        }
         *reinterpret_cast<typename Raw<N>::V*>(dst) = o;
     }
 }
 
-// A unit of a row that lies partly outside it, zeros there.
-template <int ES, int N, typename V>
-__device__ __noinline__ V quant_edge(const char* src, int64_t c, int K) {
-    using E = typename Raw<ES>::V;
-    V v{};
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        if (c + i >= 0 && c + i < K)
-            reinterpret_cast<E*>(&v)[i] = __ldg(reinterpret_cast<const E*>(src + (c + i) * ES));
-    return v;
-}
-
-// WIDE: fp16 integers, padded; else int8.  EDGE: units may lie partly outside their row (the
-// checks cost 4096 x 4096 bf16 1.3 us of 15).
+// WIDE: fp16 integers, padded; else int8.  A row's units start on the boundaries of N elements
+// in memory; EDGE: what it has before its first and behind its last whole unit, up to 2 (N - 1)
+// elements, goes to one thread each.
 template <int DT, int N, bool WIDE, bool EDGE>
-__global__ void __launch_bounds__(kThreads, kQuantBlocksPerSm) quantize_kernel(const QuantParams p) {
-    constexpr int ES = DT == DT_F32 ? 4 : 2;
-    constexpr int R = quant_keep<DT>(N) / N;
+__global__ void __launch_bounds__(kThreads, kQuantBlocksPerSm<DT>)
+quantize_kernel(const QuantParams p) {
+    constexpr int ES = DT == DT_F32 ? 4 : 2, QS = WIDE ? 2 : 1;
+    constexpr int R = quant_keep(N) / N;
     using V = typename Raw<N * ES>::V;
+    using E = typename Raw<ES>::V;
     __shared__ uint32_t tops[kThreads / 32];
     if (WIDE) griddep_launch_dependents();
     const int tpr = 1 << p.tpr_log2, in = threadIdx.x & (tpr - 1);
     const int per_block = kThreads >> p.tpr_log2;
     const int warp = threadIdx.x >> 5, warps = tpr >> 5, lane = threadIdx.x & 31;
     const int64_t step = static_cast<int64_t>(gridDim.x) * per_block;
-    // A row's units start on the boundaries of N elements in memory, so its first and last one
-    // may lie partly outside: `off` elements before the row the first one starts.
-    auto before = [&](const char* src) {
-        return EDGE ? static_cast<int>(reinterpret_cast<uintptr_t>(src) / ES % N) : 0;
+    // elements before a row's first whole unit; the end of its whole units
+    auto head_of = [&](const char* src) {
+        if (!EDGE) return 0;
+        const int h = static_cast<int>((0 - reinterpret_cast<uintptr_t>(src) / ES) % N);
+        return h < p.K ? h : p.K;
     };
-    auto load = [&](const char* src, int64_t c) {
-        if (!EDGE || (c >= 0 && c + N <= p.K)) return __ldg(reinterpret_cast<const V*>(src + c * ES));
-        return quant_edge<ES, N, V>(src, c, p.K);
+    auto end_of = [&](int head) { return EDGE ? p.K - (p.K - head) % N : p.K; };
+    // the element beside the units that is this thread's, or K
+    auto edge_of = [&](int head, int end) {
+        return in < head ? in : (in - head < p.K - end ? end + in - head : p.K);
     };
+    auto load = [&](const char* src, int64_t c) { return __ldg(reinterpret_cast<const V*>(src + c * ES)); };
     V next[R];
+    E next_edge = 0;
     auto fetch = [&](int64_t row) {
         if (row >= p.T) return;
         const char* src = static_cast<const char*>(p.x) + row * p.ld_x * ES;
-        const int off = before(src);
+        const int head = head_of(src), end = end_of(head);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            const int c = (k * tpr + in) * N - off;
-            if (c < p.K) next[k] = load(src, c);
+            const int c = (k * tpr + in) * N + head;
+            if (c < end) next[k] = load(src, c);
+        }
+        if (EDGE) {
+            const int c = edge_of(head, end);
+            if (c < p.K) next_edge = __ldg(reinterpret_cast<const E*>(src) + c);
         }
     };
     fetch(static_cast<int64_t>(blockIdx.x) * per_block + (threadIdx.x >> p.tpr_log2));
@@ -222,18 +239,20 @@ __global__ void __launch_bounds__(kThreads, kQuantBlocksPerSm) quantize_kernel(c
         const int64_t row = rb + (threadIdx.x >> p.tpr_log2);
         const bool live = row < p.T;
         const char* src = static_cast<const char*>(p.x) + row * p.ld_x * ES;
-        const int off = before(src);
+        const int head = head_of(src), end = end_of(head), edge = EDGE ? edge_of(head, end) : p.K;
+        const int64_t more = static_cast<int64_t>(R * tpr + in) * N + head;  // units not kept
         V keep[R];
 #pragma unroll
         for (int k = 0; k < R; ++k) keep[k] = next[k];
+        const E keep_edge = next_edge;
         fetch(row + step);
         uint32_t top = 0;
         if (live) {
 #pragma unroll
             for (int k = 0; k < R; ++k)
-                if ((k * tpr + in) * N - off < p.K) top = larger<DT, N>(keep[k], top);
-            for (int64_t c = (static_cast<int64_t>(R) * tpr + in) * N - off; c < p.K; c += tpr * N)
-                top = larger<DT, N>(load(src, c), top);
+                if ((k * tpr + in) * N + head < end) top = larger<DT, N>(keep[k], top);
+            for (int64_t c = more; c < end; c += tpr * N) top = larger<DT, N>(load(src, c), top);
+            if (EDGE && edge < p.K) top = larger<DT, 1>(keep_edge, top);
         }
         top = magnitude<DT>(top);
         top = __reduce_max_sync(0xffffffffu, top);
@@ -246,72 +265,73 @@ __global__ void __launch_bounds__(kThreads, kQuantBlocksPerSm) quantize_kernel(c
         }
         if (!live) continue;
         // (a row with an infinity or a NaN has no integers: a NaN scale says so)
-        const bool finite = top < 0x7f800000u;
+        const bool finite = top < 0x7f800000u, some = finite && top != 0;
         const float size = __uint_as_float(top);
         if (in == 0) p.scales[row] = finite ? __fdiv_rn(size, 127.0f) : __uint_as_float(0x7fffffffu);
         // (a power of two keeps 127 / size and x 127 inside fp32; where it rounds an
         // element, that element's integer is zero)
         const float even = size < 0x1p-40f ? 0x1p100f : (size > 0x1p100f ? 0x1p-100f : 1.0f);
-        const float big = size * even;
-        const bool some = finite && top != 0;
-        const float r = some ? __fdividef(127.0f, big) : 0.0f;  // (within 2 ulp)
-        char* dst = static_cast<char*>(p.q) + row * p.ld_q * (WIDE ? 2 : 1);
-        auto put_integers = [&](int64_t c, const float (&t)[N]) {
-            if (!EDGE || (c >= 0 && c + N <= p.K)) {
-                store_integers<N, WIDE>(dst + c * (WIDE ? 2 : 1), t);
-            } else {
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const float one[1] = {t[i]};
-                    if (c + i >= 0 && c + i < p.K) store_integers<1, WIDE>(dst + (c + i) * (WIDE ? 2 : 1), one);
-                }
-            }
-        };
+        // (within 2 ulp; see quotients)
+        constexpr float above = DT == DT_F32 ? 1.0f : 1.0f + 0x1p-21f;
+        const float r = some ? __fdividef(127.0f, size * even) * above : 0.0f;
+        char* dst = static_cast<char*>(p.q) + row * p.ld_q * QS;
         auto put = [&](const V& v, int64_t c) {
             float f[N], t[N];
             widen<DT, N>(v, f);
-            if (even != 1.0f) {
-#pragma unroll
-                for (int i = 0; i < N; ++i) f[i] *= even;
-            }
-            quotients<N>(f, big, r, t);
-            put_integers(c, t);
+            const bool again = quotients<DT, WIDE>(f, r, t);
+            store_integers<N, WIDE>(dst + c * QS, t);
+            return again;
         };
-        if (some) {
+        auto put_one = [&](E v, int64_t c) {
+            float f[1], t[1];
+            widen<DT, 1>(v, f);
+            f[0] *= even;
+            if (quotients<DT, WIDE>(f, r, t))
+                t[0] = quotient_exact(f[0], f[0] * r, size * even) + kToInt<WIDE>;
+            if (!some) t[0] = kToInt<WIDE>;
+            store_integers<1, WIDE>(dst + c * QS, t);
+        };
+        // units that need more care are read again, element by element, in one copy of the code
+        const bool plain = some && even == 1.0f;
+        uint32_t again = 0;
 #pragma unroll
-            for (int k = 0; k < R; ++k) {
-                const int c = (k * tpr + in) * N - off;
-                if (c < p.K) put(keep[k], c);
-            }
-            for (int64_t c = (static_cast<int64_t>(R) * tpr + in) * N - off; c < p.K; c += tpr * N)
-                put(load(src, c), c);
-        } else {
-            float zero[N];
-#pragma unroll
-            for (int i = 0; i < N; ++i) zero[i] = kToInt;
-            for (int64_t c = in * N - off; c < p.K; c += tpr * N) put_integers(c, zero);
+        for (int k = 0; k < R; ++k) {
+            const int c = (k * tpr + in) * N + head;
+            if (c < end && (!plain || put(keep[k], c))) again |= 1u << k;
         }
+        int64_t c = more;
+        for (;;) {
+            int64_t redo;
+            if (again) {
+                redo = (int64_t(__ffs(again) - 1) * tpr + in) * N + head;
+                again &= again - 1;
+            } else {
+                if (c >= end) break;
+                redo = c;
+                c += tpr * N;
+                if (plain && !put(load(src, redo), redo)) continue;
+            }
+#pragma unroll 1
+            for (int i = 0; i < N; ++i)
+                put_one(__ldg(reinterpret_cast<const E*>(src) + redo + i), redo + i);
+        }
+        if (EDGE && edge < p.K) put_one(keep_edge, edge);
         if (WIDE)
-            for (int c = p.K + in; c < p.pad; c += tpr) reinterpret_cast<uint16_t*>(dst)[c] = 0;
+            for (int k = p.K + in; k < p.pad; k += tpr) reinterpret_cast<uint16_t*>(dst)[k] = 0;
     }
-}
-
-int row_threads(int64_t units) {
-    int log2 = 5;
-    while (log2 < 8 && (int64_t(1) << log2) < units) ++log2;
-    return log2;
 }
 
 template <int DT, int N, bool WIDE, bool EDGE>
 cudaError_t quantize_launch(QuantParams p, int sms, cudaStream_t stream) {
     // as few threads a row as keep it, but enough rows' worth of threads to fill the GPU: what
     // a thread does once a row costs as much as eight elements
-    constexpr int keep = quant_keep<DT>(N);
-    // (rows that start inside a unit have one more)
-    p.tpr_log2 = row_threads((static_cast<int64_t>(p.K) + (EDGE ? N - 1 : 0) + keep - 1) / keep);
-    while (p.tpr_log2 < 8 && (int64_t(p.T) << p.tpr_log2) < int64_t(sms) * kThreads) ++p.tpr_log2;
+    constexpr int keep = quant_keep(N);
+    p.tpr_log2 = 5;
+    while ((1 << p.tpr_log2) < kThreads && (p.K > int64_t(keep) << p.tpr_log2 ||
+                                      (int64_t(p.T) << p.tpr_log2) < int64_t(sms) * 256))
+        ++p.tpr_log2;
     int64_t blocks = cdiv(p.T, kThreads >> p.tpr_log2);
-    if (blocks > int64_t(sms) * kQuantBlocksPerSm) blocks = int64_t(sms) * kQuantBlocksPerSm;
+    if (blocks > int64_t(sms) * kQuantBlocksPerSm<DT>) blocks = int64_t(sms) * kQuantBlocksPerSm<DT>;
     quantize_kernel<DT, N, WIDE, EDGE><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }

@@ -66,6 +66,31 @@ def test_quantize_borders_and_ties(dtype):
     quantized_exactly(x, q, s)
 
 
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_quantize_every_pair_of_significands(dtype):
+    """Each row's largest element has another significand, and the row holds all significands
+    from there down to quotients below one half: 16-bit quotients are decided by their distance
+    from a border, which no pair may come below."""
+    ones = 128 if dtype == BF else 1024          # the lowest significand, as an integer
+    tops = torch.arange(ones, 2 * ones, device=DEV)[:, None]
+    halvings = 10
+    m = torch.arange(ones, 2 * ones, device=DEV).repeat(halvings)
+    down = torch.arange(halvings, device=DEV).repeat_interleave(ones)
+    num, den = 127 * m[None], tops * 2 ** down[None]              # 127 x / max |x|
+    over = (down[None] == 0) & (m[None] > tops)                   # (they would be the maximum)
+    num, den = torch.where(over, 127, num), torch.where(over, 1, den)
+    q = num // den
+    twice = 2 * (num - q * den)
+    want = q + ((twice > den) | ((twice == den) & (q % 2 == 1))).long()
+    x = torch.where(over, tops.double(), m[None].double() / 2.0 ** down[None].double())
+    sign = torch.where((m + down) % 2 == 0, 1, -1)[None]
+    x = torch.cat([x * sign, tops.double()], 1).to(dtype)
+    assert bool((x.double().abs().amax(1) == tops[:, 0]).all())
+    got, scales = dg.i8_quantize(x)
+    assert bool((got[:, :-1].long() == want * sign).all()) and bool((got[:, -1] == 127).all())
+    assert bool((scales == (tops[:, 0].double() / 127).float()).all())
+
+
 @pytest.mark.parametrize("top", [3.3895e38, 1e37, 1e-10, 1e-30, 1.1e-38, 3e-42, 1.4e-45])
 def test_quantize_extreme_rows(top):
     rng = np.random.default_rng(1)
