@@ -244,6 +244,7 @@ cudaError_t dispatch_unit(int unit, const DispatchParams& p, int blocks, cudaStr
 
 constexpr int kSumThreads = 256;
 constexpr int kSumBlocksPerSm = 4;      // all resident at once: no second, partial wave
+constexpr int kSumApart = 4;            // pieces of a thread's columns where rows are not aligned
 
 struct CombineParams {
     const int32_t* slots;    // [T][top]
@@ -384,7 +385,10 @@ __device__ __forceinline__ void combine_store(const CombineParams& p, int64_t of
 // a time (every thread for itself, they were most of the instructions: 16384 tokens x 4 of
 // 2048, bf16, 70 us).  A thread takes N neighbouring columns of a token and adds its rows in the
 // order of j, in fp32; the next four rows, of this token or the next, are loaded meanwhile.
-template <int DT, int N>
+// Where rows allow no 16 bytes at once it takes W times N columns, a token's threads apart
+// (3001 tokens x 6 of 1001, fp16: one column at a time 31 us, two at a time 21, four 17.4; 1002
+// columns, two neighbours each: 19 and 12).
+template <int DT, int N, int W>
 __global__ void __launch_bounds__(kSumThreads, kSumBlocksPerSm) combine_kernel(const CombineParams p) {
     using V = typename Pack<DT, N>::V;
     constexpr int ES = DT == DT_F32 ? 4 : 2;
@@ -400,30 +404,35 @@ __global__ void __launch_bounds__(kSumThreads, kSumBlocksPerSm) combine_kernel(c
         // (tokens mine, mine + per_block, ...; of each the columns in * N, ...; of those the
         // pairs by fours)
         int tok = mine, c = in * N, j0 = 0;
-        V next[4];
+        V next[4][W];
         auto load = [&]() {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 if (j0 + k >= p.top) break;
                 const int64_t row = pairs[tok * p.top + j0 + k].row;
-                if (row >= 0) next[k] = __ldg(reinterpret_cast<const V*>(rows + row + static_cast<int64_t>(c) * ES));
+                if (row < 0) continue;
+                const char* src = rows + row + static_cast<int64_t>(c) * ES;
+#pragma unroll
+                for (int w = 0; w < W; ++w)
+                    if (w == 0 || c + w * tpt * N < p.K)
+                        next[k][w] = __ldg(reinterpret_cast<const V*>(src + w * tpt * N * ES));
             }
         };
         bool more = tok < n && c < p.K;
         if (more) load();
-        float sum[N];
+        float sum[W][N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) sum[i] = 0.0f;
+        for (int i = 0; i < W * N; ++i) sum[i / N][i % N] = 0.0f;
         while (more) {
-            const int at = tok * p.top + j0, left = p.top - j0;
+            const int at = tok * p.top + j0, left = p.top - j0, col = c;
             const int64_t off = (tb + tok) * p.ld_y + c;
-            V v[4];
+            V v[4][W];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = next[k];
+            for (int k = 0; k < 4 * W; ++k) v[k / W][k % W] = next[k / W][k % W];
             j0 += 4;
             if (j0 >= p.top) {
                 j0 = 0;
-                c += tpt * N;
+                c += tpt * N * W;
                 if (c >= p.K) {
                     c = in * N;
                     tok += per_block;
@@ -436,18 +445,56 @@ __global__ void __launch_bounds__(kSumThreads, kSumBlocksPerSm) combine_kernel(c
                 if (k >= left) break;
                 const CombinePair pair = pairs[at + k];
                 if (pair.row < 0) continue;
-                float f[N];
-                unpack<DT, N>(v[k], f);
 #pragma unroll
-                for (int i = 0; i < N; ++i) sum[i] = fmaf(pair.w, f[i], sum[i]);
+                for (int w = 0; w < W; ++w) {
+                    float f[N];
+                    unpack<DT, N>(v[k][w], f);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) sum[w][i] = fmaf(pair.w, f[i], sum[w][i]);
+                }
             }
             if (left <= 4) {
-                combine_store<DT, N>(p, off, sum);
 #pragma unroll
-                for (int i = 0; i < N; ++i) sum[i] = 0.0f;
+                for (int w = 0; w < W; ++w) {
+                    if (w == 0 || col + w * tpt * N < p.K) combine_store<DT, N>(p, off + w * tpt * N, sum[w]);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) sum[w][i] = 0.0f;
+                }
             }
         }
     }
+}
+
+// The gradient's dot products of a token's pairs from j0 on, from its threads' parts.
+template <int J>
+__device__ __forceinline__ void combine_dots(const CombineParams& p, float (&dot)[J], float (*part)[J],
+                                             int64_t t, int j0, bool live) {
+    const int warps = 1 << p.tpt_log2 >> 5, in = threadIdx.x & ((1 << p.tpt_log2) - 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 0; k < J; ++k)
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) dot[k] += __shfl_xor_sync(0xffffffffu, dot[k], d);
+    if (warps > 1) {
+        __syncthreads();  // (the pairs before have been read)
+        if (lane == 0) {
+#pragma unroll
+            for (int k = 0; k < J; ++k) part[warp][k] = dot[k];
+        }
+        __syncthreads();
+        if (in < J) {
+            float sum = 0.0f;
+            for (int i = 0; i < warps; ++i) sum += part[warp + i][in];
+            dot[0] = sum;
+        }
+    } else {
+#pragma unroll
+        for (int k = 1; k < J; ++k)
+            if (lane == k) dot[0] = dot[k];
+    }
+    if (live && in < J && j0 + in < p.top)
+        store_elem(static_cast<char*>(p.d_weights) + (t * p.ld_dw + j0 + in) * dt_size(p.dw_dtype),
+                   p.dw_dtype, dot[0]);
 }
 
 // The threads of a token (a warp's worth at least, a block's at most) walk its columns once
@@ -460,7 +507,6 @@ __global__ void __launch_bounds__(kSumThreads) combine_grad_kernel(const Combine
     __shared__ float part[kSumThreads / 32][J];
     const int tpt = 1 << p.tpt_log2, in = threadIdx.x & (tpt - 1), mine = threadIdx.x >> p.tpt_log2;
     const int per_block = kSumThreads >> p.tpt_log2;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = tpt >> 5;
     const char* dy = static_cast<const char*>(p.y);
     const char* rows = static_cast<const char*>(p.rows);
     char* d_rows = static_cast<char*>(p.d_rows);
@@ -510,70 +556,165 @@ __global__ void __launch_bounds__(kSumThreads) combine_grad_kernel(const Combine
                             *reinterpret_cast<V*>(d_rows + (s[k] * p.ld_drows + c) * ES) = pack<DT, N>(o);
                         }
                     }
-                if (!p.d_weights) continue;
-#pragma unroll
-                for (int k = 0; k < J; ++k)
-#pragma unroll
-                    for (int d = 16; d > 0; d >>= 1) dot[k] += __shfl_xor_sync(0xffffffffu, dot[k], d);
-                if (warps > 1) {
-                    __syncthreads();  // (the pairs before have been read)
-                    if (lane == 0) {
-#pragma unroll
-                        for (int k = 0; k < J; ++k) part[warp][k] = dot[k];
-                    }
-                    __syncthreads();
-                    if (in < J) {
-                        float sum = 0.0f;
-                        for (int i = 0; i < warps; ++i) sum += part[warp + i][in];
-                        dot[0] = sum;
-                    }
-                } else {
-#pragma unroll
-                    for (int k = 1; k < J; ++k)
-                        if (lane == k) dot[0] = dot[k];
-                }
-                if (live && in < J && j0 + in < p.top)
-                    store_elem(static_cast<char*>(p.d_weights) +
-                                   (t * p.ld_dw + j0 + in) * dt_size(p.dw_dtype),
-                               p.dw_dtype, dot[0]);
+                if (p.d_weights) combine_dots<J>(p, dot, part, t, j0, live);
             }
         }
     }
 }
 
-template <int DT, int N>
-cudaError_t combine_launch(const CombineParams& p, bool grad, int blocks, cudaStream_t stream) {
+// The same for rows on any address.  Units of 16 bytes start where rows and d_rows (alike) have
+// their 16-byte boundaries, another column in every row; dy comes to them through shared memory,
+// in fp32, a word more for each unit so that neighbouring threads meet no bank twice.  What a row
+// has before its first and behind its last whole unit goes to one thread each.  (3001 tokens x 6 of
+// 1001, fp16: 23.7 us, 34 with one column at a time and as much with four of them apart; 16384 x
+// 4 of 2049, bf16: 147 and 235.  Three barriers and a load's latency for every token of a block's.)
+template <int DT, int J>
+__global__ void __launch_bounds__(kSumThreads, J > 4 ? 3 : kSumBlocksPerSm)
+combine_grad_any_kernel(const CombineParams p) {
+    constexpr int ES = DT == DT_F32 ? 4 : 2, N = 16 / ES;
+    using V = typename Pack<DT, N>::V;
+    using E = typename Pack<DT, 1>::V;
+    __shared__ CombinePair pairs[kSumPairs];
+    __shared__ float part[kSumThreads / 32][J];
+    __shared__ float staged[(kSumThreads + kSumThreads / 32) * (N + 1)];
+    const int tpt = 1 << p.tpt_log2, in = threadIdx.x & (tpt - 1), mine = threadIdx.x >> p.tpt_log2;
+    const int per_block = kSumThreads >> p.tpt_log2;
+    float* dy_at = staged + mine * (tpt + 1) * (N + 1);
+    const char* dy = static_cast<const char*>(p.y);
+    const char* rows = static_cast<const char*>(p.rows);
+    char* d_rows = static_cast<char*>(p.d_rows);
+    // columns of a row (K is 16 bytes or more) before its first whole unit
+    auto head_of = [&](int64_t row) {
+        return static_cast<int>((0 - (reinterpret_cast<uintptr_t>(d_rows) / ES + row * p.ld_drows)) % N);
+    };
+    const int64_t t1 = static_cast<int64_t>(p.T) * (blockIdx.x + 1) / gridDim.x;
+    const int batch = kSumPairs / p.top;
+    for (int64_t tb = static_cast<int64_t>(p.T) * blockIdx.x / gridDim.x; tb < t1; tb += batch) {
+        const int n = static_cast<int>(t1 - tb < batch ? t1 - tb : batch);
+        combine_pairs(p, tb, n, 1, pairs);  // (row numbers: two pitches)
+        // (whole blocks walk together: the barriers are the block's)
+        for (int t0 = 0; t0 < n; t0 += per_block) {
+            const int tok = t0 + mine;
+            const int64_t t = tb + tok;
+            const bool live = tok < n;
+            const char* g_row = dy + t * p.ld_y * ES;
+            auto edges = [&](int j0, float (&dot)[J]) {
+                for (int i = in; i < J * 2 * N; i += tpt) {
+                    const int k = i / (2 * N), at = i % (2 * N);
+                    if (!live || j0 + k >= p.top) continue;
+                    const CombinePair pair = pairs[tok * p.top + j0 + k];
+                    const int head = head_of(pair.row), tail = (p.K - head) % N;
+                    if (pair.row < 0 || at >= head + tail) continue;
+                    const int c = at < head ? at : p.K - tail + at - head;
+                    float g[1], o[1];
+                    unpack<DT, 1>(reinterpret_cast<const E*>(g_row)[c], g);
+                    if (p.d_weights) {
+                        unpack<DT, 1>(reinterpret_cast<const E*>(rows)[pair.row * p.ld_rows + c], o);
+#pragma unroll
+                        for (int l = 0; l < J; ++l)
+                            if (l == k) dot[l] = fmaf(g[0], o[0], dot[l]);
+                    }
+                    o[0] = pair.w * g[0];
+                    reinterpret_cast<E*>(d_rows)[pair.row * p.ld_drows + c] = pack<DT, 1>(o);
+                }
+            };
+            for (int j0 = 0; j0 < p.top; j0 += J) {
+                const CombinePair* pair = pairs + tok * p.top + j0;
+                const int count = live ? p.top - j0 : 0;
+                float dot[J];
+#pragma unroll
+                for (int k = 0; k < J; ++k) dot[k] = 0.0f;
+                for (int64_t c0 = 0; c0 + N <= p.K; c0 += tpt * N) {
+                    V r[J];
+                    if (p.d_weights) {
+#pragma unroll
+                        for (int k = 0; k < J; ++k) {
+                            if (k >= count) break;
+                            const int64_t row = pair[k].row, c = c0 + in * N + head_of(row);
+                            if (row >= 0 && c + N <= p.K)
+                                r[k] = *reinterpret_cast<const V*>(rows + (row * p.ld_rows + c) * ES);
+                        }
+                    }
+                    // (all of them on their way before the first is waited for)
+                    E e[N + 1];
+#pragma unroll
+                    for (int i = 0; i <= N; ++i) {
+                        const int64_t c = c0 + i * tpt + in;
+                        e[i] = 0;
+                        if (live && c < p.K && (i < N || in < N)) e[i] = reinterpret_cast<const E*>(g_row)[c];
+                    }
+                    if (c0 == 0) edges(j0, dot);
+                    __syncthreads();  // (the columns before have been read)
+#pragma unroll
+                    for (int i = 0; i <= N; ++i) {
+                        const int at = i * tpt + in;
+                        float g[1];
+                        unpack<DT, 1>(e[i], g);
+                        if (i < N || in < N) dy_at[at + at / N] = g[0];
+                    }
+                    __syncthreads();
+#pragma unroll
+                    for (int k = 0; k < J; ++k) {
+                        if (k >= count) break;
+                        const int64_t row = pair[k].row;
+                        const int head = head_of(row);
+                        const int64_t c = c0 + in * N + head;
+                        if (row < 0 || c + N > p.K) continue;
+                        const float w = pair[k].w;
+                        const float* lo = dy_at + in * (N + 1) + head;
+                        float g[N], o[N];
+#pragma unroll
+                        for (int i = 0; i < N; ++i) g[i] = lo[head + i >= N ? i + 1 : i];
+                        if (p.d_weights) {
+                            unpack<DT, N>(r[k], o);
+#pragma unroll
+                            for (int i = 0; i < N; ++i) dot[k] = fmaf(g[i], o[i], dot[k]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < N; ++i) o[i] = w * g[i];
+                        *reinterpret_cast<V*>(d_rows + (row * p.ld_drows + c) * ES) = pack<DT, N>(o);
+                    }
+                }
+                if (p.d_weights) combine_dots<J>(p, dot, part, t, j0, live);
+            }
+        }
+    }
+}
+
+// Neighbouring elements that a thread takes at once: 16 bytes' worth, two 16-bit ones, or one.
+template <int DT>
+cudaError_t combine_launch(int n, const CombineParams& p, int blocks, cudaStream_t stream) {
+    constexpr int FULL = DT == DT_F32 ? 4 : 8;
     const dim3 g(static_cast<unsigned>(blocks));
-    if (!grad)
-        combine_kernel<DT, N><<<g, kSumThreads, 0, stream>>>(p);
-    else if (p.top <= 4)
-        combine_grad_kernel<DT, N, 4><<<g, kSumThreads, 0, stream>>>(p);
+    if (n == FULL)
+        combine_kernel<DT, FULL, 1><<<g, kSumThreads, 0, stream>>>(p);
+    else if (DT != DT_F32 && n == 2)
+        combine_kernel<DT, DT == DT_F32 ? 1 : 2, kSumApart><<<g, kSumThreads, 0, stream>>>(p);
     else
-        combine_grad_kernel<DT, N, 8><<<g, kSumThreads, 0, stream>>>(p);
+        combine_kernel<DT, 1, kSumApart><<<g, kSumThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
+// The gradient: 16 bytes at a time, from aligned rows or from rows on any address, or one element.
 template <int DT>
-cudaError_t combine_width(int n, const CombineParams& p, bool grad, int blocks, cudaStream_t stream) {
+cudaError_t combine_grad_launch(int n, bool any, const CombineParams& p, int blocks, cudaStream_t stream) {
     constexpr int FULL = DT == DT_F32 ? 4 : 8;
-    if (n == FULL) return combine_launch<DT, FULL>(p, grad, blocks, stream);
-    if constexpr (DT != DT_F32)
-        if (n == 2) return combine_launch<DT, 2>(p, grad, blocks, stream);
-    return combine_launch<DT, 1>(p, grad, blocks, stream);
+    const dim3 g(static_cast<unsigned>(blocks));
+    auto run = [&](auto few) {
+        constexpr int J = decltype(few)::value ? 4 : 8;
+        if (any)
+            combine_grad_any_kernel<DT, J><<<g, kSumThreads, 0, stream>>>(p);
+        else if (n == FULL)
+            combine_grad_kernel<DT, FULL, J><<<g, kSumThreads, 0, stream>>>(p);
+        else
+            combine_grad_kernel<DT, 1, J><<<g, kSumThreads, 0, stream>>>(p);
+    };
+    if (p.top <= 4)
+        run(std::true_type());
+    else
+        run(std::false_type());
+    return cudaGetLastError();
 }
-
-// Elements that a thread may take at once: whole 16 bytes, a pair of 16-bit elements, or
-// one, whichever K and all addresses and pitches allow.
-struct Width {
-    int n;
-    void add(const void* ptr, int64_t ld, int es) {
-        while (n > 1) {
-            const int64_t a = n * es > 16 ? 16 : n * es;
-            if (reinterpret_cast<uintptr_t>(ptr) % a == 0 && ld * es % a == 0) break;
-            n = n > 2 ? (es == 2 ? 2 : 1) : 1;
-        }
-    }
-};
 
 // Runs combine or its gradient from checked arguments.
 gemm_status_t combine_run(CombineParams& p, int dt, bool grad, cudaStream_t stream) {
@@ -581,26 +722,42 @@ gemm_status_t combine_run(CombineParams& p, int dt, bool grad, cudaStream_t stre
     const gemm_status_t st = device_info(&d);
     if (st != GEMM_OK) return st;
     p.status = d.status;
-    const int es = dt_bytes(dt), full = 16 / es;
-    Width w{p.K % full == 0 ? full : (es == 2 && p.K % 2 == 0 ? 2 : 1)};
-    if (p.rows) w.add(p.rows, p.ld_rows, es);
-    if (grad) w.add(p.d_rows, p.ld_drows, es);
-    if (grad || p.y_dtype == dt)
-        w.add(p.y, p.ld_y, es);
-    else if (w.n == full && !(aligned(p.y, 16) && p.ld_y % 4 == 0))
-        w.n = 2;  // (an fp32 y beside 16-bit rows takes its 8 elements as two 16 bytes)
-    const int64_t units = cdiv(p.K, w.n);
+    const int es = dt_bytes(dt), ys = dt_bytes(p.y_dtype), full = 16 / es;
+    auto units = [](const void* ptr, int64_t ld, int bytes) {
+        return !ptr || (aligned(ptr, 16) && ld * bytes % 16 == 0);
+    };
+    auto pairs = [](const void* ptr, int64_t ld) { return !ptr || (aligned(ptr, 4) && ld % 2 == 0); };
+    int width = full;
+    if (p.K % full != 0 || !units(p.rows, p.ld_rows, es) || !units(p.y, p.ld_y, ys) ||
+        (grad && !units(p.d_rows, p.ld_drows, es)))
+        width = !grad && es == 2 && p.K % 2 == 0 && pairs(p.rows, p.ld_rows) &&
+                        pairs(p.y, p.ld_y) ? 2 : 1;
+    // (the gradient takes rows on any address if an element has the same place in its 16 bytes in
+    // both tensors)
+    auto place = [&](const void* ptr, int64_t ld, int64_t row) {
+        return (reinterpret_cast<uintptr_t>(ptr) + static_cast<uintptr_t>(row * ld * es)) % 16;
+    };
+    const bool any = grad && width != full && p.K >= full &&
+                     (!p.rows || (place(p.rows, p.ld_rows, 0) == place(p.d_rows, p.ld_drows, 0) &&
+                                  place(p.rows, p.ld_rows, 1) == place(p.d_rows, p.ld_drows, 1)));
+    const int64_t n = cdiv(p.K, width == full || any ? full : (grad ? 1 : width * kSumApart));
     int log2 = 5;
-    while (log2 < 8 && (int64_t(1) << log2) < units) ++log2;
+    while (log2 < 8 && (int64_t(1) << log2) < n) ++log2;
     p.tpt_log2 = log2;
     int64_t blocks = cdiv(p.T, kSumThreads >> log2);
-    // (eight pairs at once of whole 16 bytes take 114 registers: two blocks)
-    const int64_t fit = int64_t(d.sm_count) * (grad && p.top > 4 && w.n == full ? 2 : kSumBlocksPerSm);
-    if (blocks > fit) blocks = fit;
-    const int n = static_cast<int>(blocks);
-    const cudaError_t e = dt == DT_BF16  ? combine_width<DT_BF16>(w.n, p, grad, n, stream)
-                          : dt == DT_F16 ? combine_width<DT_F16>(w.n, p, grad, n, stream)
-                                         : combine_width<DT_F32>(w.n, p, grad, n, stream);
+    // (the gradient of eight pairs at once: 114 registers, or 80)
+    const int64_t fit = !grad || p.top <= 4 ? kSumBlocksPerSm : (any ? 3 : (width == full ? 2 : 4));
+    if (blocks > d.sm_count * fit) blocks = d.sm_count * fit;
+    const int g = static_cast<int>(blocks);
+    cudaError_t e;
+    if (grad)
+        e = dt == DT_BF16  ? combine_grad_launch<DT_BF16>(width, any, p, g, stream)
+            : dt == DT_F16 ? combine_grad_launch<DT_F16>(width, any, p, g, stream)
+                           : combine_grad_launch<DT_F32>(width, any, p, g, stream);
+    else
+        e = dt == DT_BF16  ? combine_launch<DT_BF16>(width, p, g, stream)
+            : dt == DT_F16 ? combine_launch<DT_F16>(width, p, g, stream)
+                           : combine_launch<DT_F32>(width, p, g, stream);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return GEMM_ERR_CUDA;

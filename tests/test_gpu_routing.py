@@ -259,6 +259,42 @@ def test_combine_grad_strides(shift):
     assert bool((out[:, :shift] == 5).all()) and bool((out[:, shift + K:] == 5).all())
 
 
+@pytest.mark.parametrize("dtype", [HF, F32])
+@pytest.mark.parametrize("T,top,K,shift", [(9, 3, 8, 1), (33, 6, 9, 0), (7, 9, 15, 3), (40, 2, 23, 5),
+                                           (300, 5, 130, 0), (5, 4, 2047, 1), (6, 8, 2049, 0),
+                                           (3, 2, 2056, 7), (4, 6, 4099, 2)])
+def test_rows_on_any_address(T, top, K, shift, dtype):
+    """Rows, results and gradients that start anywhere in their 16 bytes, the matrix's first and
+    last row included; what lies beside them is neither used nor written."""
+    rng = np.random.default_rng(K + shift)
+    _, slots = ref.places(route(rng, T, top, 12, 0.2), 12)
+    where = torch.from_numpy(slots).to(DEV, torch.int32)
+
+    def inside(rows, pitch):
+        wide = torch.full((rows, pitch), float("nan"), dtype=dtype, device=DEV)
+        view = wide.view(-1)[shift:shift + (rows - 1) * pitch + K].as_strided((rows, K), (pitch, 1))
+        view.copy_(experts_ref.ints(rng, (rows, K), dtype=dtype))
+        return view
+
+    rows, dy = inside(T * top, K + shift), inside(T, K + shift + 3)
+    w = experts_ref.ints(rng, (T, top), dtype=F32)
+    for kind in {dtype, F32}:
+        wide = torch.full((T, K + shift + 1), 5.0, dtype=kind, device=DEV)
+        dg.expert_combine(rows, where, w.to(DEV), out=wide[:, shift:shift + K])
+        want, _ = ref.combine(rows, slots, w)
+        assert np.array_equal(experts_ref.f64(wide[:, shift:shift + K]), want)
+        assert bool((wide[:, :shift] == 5).all()) and bool((wide[:, shift + K:] == 5).all())
+    for pitch in (K + shift, K + shift + 1):
+        wide = torch.full((T * top, pitch), 5.0, dtype=dtype, device=DEV)
+        d_rows, d_w = dg.expert_combine_grad(dy, where, w.to(DEV), rows=rows,
+                                             out=wide[:, shift:shift + K])
+        want, want_w, _ = ref.combine_grad(dy, slots, w, rows, torch.full((T * top, K), 5.0))
+        assert np.array_equal(experts_ref.f64(d_rows), want)
+        assert np.array_equal(experts_ref.f64(d_w), want_w)
+        assert bool((wide[:, :shift] == 5).all()) and bool((wide[:, shift + K:] == 5).all())
+    assert status() == 0
+
+
 def test_gradients_against_differences():
     """L = <g, combine(dispatch(x) * a, w)> is linear in x and in w: on small integers a
     difference quotient is its slope exactly."""
