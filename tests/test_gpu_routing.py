@@ -89,6 +89,31 @@ def test_dispatch_strides_types_and_scales(dtype, pad, shift):
     assert same(rows, want) and same(rs, ws)
 
 
+@pytest.mark.parametrize("dtype", [torch.int8, HF, F32])
+@pytest.mark.parametrize("T,top,K,x_shift,shift,pad", [
+    (40, 3, 3, 0, 0, 0), (6000, 2, 15, 1, 0, 0), (77, 4, 17, 0, 3, 5), (6000, 3, 33, 2, 1, 0),
+    (500, 2, 255, 0, 0, 0), (400, 3, 2047, 3, 0, 2), (300, 2, 2049, 0, 0, 0), (31, 40, 130, 1, 2, 3),
+    (400, 2, 20001, 1, 3, 0), (155, 2, 16390, 0, 2, 0), (90, 2, 1026, 0, 0, 0)])
+def test_dispatch_to_rows_on_any_address(T, top, K, x_shift, shift, pad, dtype):
+    """Tokens and rows that start anywhere in their 16 bytes, several rounds a block and several
+    rounds a row among them; what lies beside the rows stays."""
+    rng = np.random.default_rng(K + T)
+    ids = route(rng, T, top, 9, 0.1, twice=True)
+    offsets, slots = ref.places(ids, 9)
+    x = torch.from_numpy(rng.integers(-100, 100, (T, x_shift + K))).to(DEV, dtype)[:, x_shift:]
+    wide = torch.full((T * top, shift + K + pad), 101, dtype=dtype, device=DEV)
+    scales = values(rng, (T,), F32).to(DEV)
+    _, off, sl, rs = dg.expert_dispatch(x, torch.from_numpy(ids).to(DEV), 9, scales=scales,
+                                        out=wide[:, shift:shift + K])
+    assert np.array_equal(off.cpu().numpy(), offsets) and np.array_equal(sl.cpu().numpy(), slots)
+    t, j = (torch.from_numpy(v).to(DEV) for v in np.nonzero(slots >= 0))
+    want = torch.full((T * top, K), 101, dtype=dtype, device=DEV)
+    want[sl[t, j].long()] = x[t]
+    assert torch.equal(wide[:, shift:shift + K], want)
+    assert bool((wide[:, :shift] == 101).all()) and bool((wide[:, shift + K:] == 101).all())
+    assert torch.equal(rs[sl[t, j].long()], scales[t]) and status() == 0
+
+
 def test_dispatch_nothing_and_all_dropped():
     x = torch.zeros((0, 8), dtype=BF, device=DEV)
     rows, off, sl = dg.expert_dispatch(x, torch.zeros((0, 2), dtype=torch.int32, device=DEV), 5)
