@@ -18,8 +18,9 @@
 // middle) are read again element by element in one copy of the code: unrolled beside the
 // others it did not stay in the instruction cache (4096 x 4095 fp32: 36 us against 17.6).
 //
-// 4096 x 4096 bf16: 9.7 us by graph replay, 5.2 TB/s, where the copy rate would take 7.4;
-// 1001 x 7001 fp32, rows that start anywhere: 9.7 against 5.2 (3.3 rows for each block).
+// 4096 x 4096 bf16: 8.9 us by graph replay, 5.6 TB/s, where the copy rate would take 7.4 (the issue
+// slots are 70 % busy); 1001 x 7001 fp32, rows that start anywhere: 9.5 against 5.2 (3.3 rows for
+// each block).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -39,7 +40,7 @@ template <int DT>
 constexpr int kQuantBlocksPerSm = DT == DT_F32 ? 2 : 3;
 // Elements of a row that a thread keeps (16 or 32 registers; the next row's take as many more).
 // fp32 rows of up to 8192 stay on the SM: with 16 elements and twice the blocks, 1001 x 7001
-// took 12 us against 9.7, and 16-bit ones with four blocks 10.7 against 9.7 (4096 x 4096).
+// took 12 us against 9.5, and 16-bit ones with four blocks 10.7 against 9.7 (4096 x 4096).
 __host__ __device__ constexpr int quant_keep(int n) { return n == 1 ? 16 : 32; }
 
 struct QuantParams {
@@ -140,9 +141,20 @@ template <int DT, bool WIDE, int N>
 __device__ __forceinline__ bool quotients(const float (&x)[N], float r, float (&t)[N]) {
     constexpr float C = kToInt<WIDE>;
     if constexpr (DT != DT_F32) {
+        if constexpr (N == 1) {
+            t[0] = __uint_as_float(__float_as_uint(x[0] * r) & 0xfffffff0u) + C;
+        } else {
+            // (two at a time: packed fp32 operations)
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            t[i] = __uint_as_float(__float_as_uint(x[i] * r) & 0xfffffff0u) + C;
+            for (int i = 0; i < N; i += 2) {
+                float2 y = __fmul2_rn(make_float2(x[i], x[i + 1]), make_float2(r, r));
+                y.x = __uint_as_float(__float_as_uint(y.x) & 0xfffffff0u);
+                y.y = __uint_as_float(__float_as_uint(y.y) & 0xfffffff0u);
+                y = __fadd2_rn(y, make_float2(C, C));
+                t[i] = y.x;
+                t[i + 1] = y.y;
+            }
+        }
         return false;
     } else {
         float far = 0.0f;
@@ -199,7 +211,7 @@ quantize_kernel(const QuantParams p) {
     constexpr int R = quant_keep(N) / N;
     using V = typename Raw<N * ES>::V;
     using E = typename Raw<ES>::V;
-    __shared__ uint32_t tops[kThreads / 32];
+    __shared__ uint32_t tops[2][kThreads / 32];
     if (WIDE) griddep_launch_dependents();
     const int tpr = 1 << p.tpr_log2, in = threadIdx.x & (tpr - 1);
     const int per_block = kThreads >> p.tpr_log2;
@@ -234,6 +246,7 @@ quantize_kernel(const QuantParams p) {
         }
     };
     fetch(static_cast<int64_t>(blockIdx.x) * per_block + (threadIdx.x >> p.tpr_log2));
+    int turn = 0;
     // (whole blocks walk together: the maximum's barriers are the block's)
     for (int64_t rb = static_cast<int64_t>(blockIdx.x) * per_block; rb < p.T; rb += step) {
         const int64_t row = rb + (threadIdx.x >> p.tpr_log2);
@@ -257,11 +270,12 @@ quantize_kernel(const QuantParams p) {
         top = magnitude<DT>(top);
         top = __reduce_max_sync(0xffffffffu, top);
         if (warps > 1) {
-            __syncthreads();  // (the row before has been read)
-            if (lane == 0) tops[warp] = top;
+            // (two sets in turn: a warp is at most one row ahead of another's reading)
+            if (lane == 0) tops[turn][warp] = top;
             __syncthreads();
-            const int first = warp & ~(warps - 1);
-            for (int i = 0; i < warps; ++i) top = tops[first + i] > top ? tops[first + i] : top;
+            top = tops[turn][(warp & ~(warps - 1)) + (lane & (warps - 1))];
+            top = __reduce_max_sync(0xffffffffu, top);
+            turn ^= 1;
         }
         if (!live) continue;
         // (a row with an infinity or a NaN has no integers: a NaN scale says so)
