@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kRouteThreads, 1) dispatch_kernel(const Dispat
     for (int64_t t = t0 + (tid >> p.tpt_log2); t < t1; t += kRouteThreads >> p.tpt_log2) {
         const int32_t* slot = p.slots + t * p.top;
         const V* src = reinterpret_cast<const V*>(p.x + t * p.x_pitch);
-        for (int c = in; c < p.vecs; c += tpt * W) {
+        for (int64_t c = in; c < p.vecs; c += tpt * W) {
             V v[W];
 #pragma unroll
             for (int w = 0; w < W; ++w)

@@ -91,6 +91,17 @@ def test_quantize_every_pair_of_significands(dtype):
     assert bool((scales == (tops[:, 0].double() / 127).float()).all())
 
 
+def test_quantize_longest_row():
+    K = 2 ** 31 - 4097
+    x = torch.empty((1, K), dtype=BF, device=DEV).uniform_(-3, 3)
+    x[0, K // 2] = 5.0
+    q, s = dg.i8_quantize(x)
+    assert s.item() == np.float32(5.0 / 127)
+    for part in (slice(0, 10000), slice(K // 2 - 5000, K // 2 + 5000), slice(K - 10000, K)):
+        # (a quotient is on a border, which 64 bits hold, or 2^-16 of itself away from one)
+        assert torch.equal(q[0, part].double(), torch.round(127 * x[0, part].double() / 5.0))
+
+
 @pytest.mark.parametrize("top", [3.3895e38, 1e37, 1e-10, 1e-30, 1.1e-38, 3e-42, 1.4e-45])
 def test_quantize_extreme_rows(top):
     rng = np.random.default_rng(1)

@@ -114,6 +114,19 @@ def test_dispatch_to_rows_on_any_address(T, top, K, x_shift, shift, pad, dtype):
     assert torch.equal(rs[sl[t, j].long()], scales[t]) and status() == 0
 
 
+def test_longest_rows():
+    """Rows as long as extents may be, and odd: columns counted in steps come close to 2^31."""
+    K = 2 ** 31 - 4097
+    x = torch.randint(-100, 100, (1, K), dtype=torch.int8, device=DEV)
+    ids = torch.zeros((1, 1), dtype=torch.int32, device=DEV)
+    rows, off, slots = dg.expert_dispatch(x, ids, 1)
+    assert off.tolist() == [0, 1] and slots.tolist() == [[0]] and torch.equal(rows, x)
+    del x
+    wide = rows.to(HF)
+    assert torch.equal(dg.expert_combine(wide, slots), wide)
+    assert status() == 0
+
+
 def test_dispatch_nothing_and_all_dropped():
     x = torch.zeros((0, 8), dtype=BF, device=DEV)
     rows, off, sl = dg.expert_dispatch(x, torch.zeros((0, 2), dtype=torch.int32, device=DEV), 5)
