@@ -6,8 +6,9 @@
 // useful rate, but an int8 is an exact fp16 number, a product of two at most 2^14, and 1024
 // of them sum to at most 2^24, which the fp32 accumulator holds exactly.  So the kernel
 // multiplies fp16 (at the 16-bit rate), takes at most 1024 products into an accumulator and
-// adds that to 32-bit integers in registers: the sum is the integer sum, whatever the
-// tiles, splits and order, and a row's result does not depend on the call's other rows.
+// adds that to 32-bit integers in registers (or two of them in fp32, which rounds their sum as
+// the integer would be): the sum is the integer sum, whatever the tiles, splits and order, and
+// a row's result does not depend on the call's other rows.
 //
 // What it saves against 16-bit weights is bytes, so the weights stay bytes up to the SM:
 //
@@ -37,8 +38,8 @@
 // (16 without the quantisation), the bytes take 10: start-up, and 128 of the 152 SMs have a
 // tile.  192 rows over 64 experts of 2048 x 2048: 47 us, the bytes 40.  1500 tokens of 4096 x
 // 4096: 40 us, the products 26: two rounds of 128 tiles on 76 pairs, and the pass (5).  16384
-// rows over 16 experts, 2048 to 4096, GELU: 197 us, the products 143: issue slots, most of them
-// taken by integer sums, scales, GELU and the conversion of the weights, and the pass (17).
+// rows over 16 experts, 2048 to 4096, GELU: 190 us, the products 143: issue slots, most of them
+// taken by the sums, scales, GELU and the conversion of the weights, and the pass (17).
 #include "i8.h"
 #include "ragged_kernel.cuh"
 
@@ -552,8 +553,7 @@ __device__ __forceinline__ void i8_store32(const RgParams& p, int64_t base, int 
 
 // GELU's tanh form as x / (1 + exp(-2 y)), y = sqrt(2 / pi) (x + 0.044715 x^3): half the
 // instructions of 0.5 x (1 + tanh y), as the other kernels have it: their issue slots are free, this
-// one's are not (16384 rows over 16 experts, 2048 to 4096: 205 us against 221, 195 without an
-// activation).  The exponent is taken to base 2.
+// one's are not (16384 rows over 16 experts, 2048 to 4096: 205 us against 221).  The exponent is taken to base 2.
 __device__ __forceinline__ float i8_gelu_tanh(float x) {
     constexpr float k = -2.0f * 0.7978845608028654f * 1.4426950408889634f;
     float e;
@@ -607,8 +607,13 @@ __device__ __forceinline__ void i8_epilogue(const I8Params& p, const I8Cta& x, i
         }
         int v[C::NC][32];
         bool ok = true;
+        // Two accumulators' sum in fp32 is rounded as its integer would be for the scaling: with no
+        // more than two the sums stay fp32 numbers and save the conversions, whose rate
+        // is a fraction of an addition's (16384 rows over 16 experts, 2048 to 4096, GELU: 203 us with
+        // them, 197 without).
+        const bool two = !SPLIT && s1 - s0 <= 2 * C::SUM;
         // an accumulator to the sums (the first one replaces them)
-        auto add = [&](auto first) {
+        auto add = [&](auto first, auto exact) {
             const uint32_t from = row + static_cast<uint32_t>(acc.at * BT);
 #pragma unroll
             for (int c = 0; c < C::NC; ++c) {
@@ -619,8 +624,13 @@ __device__ __forceinline__ void i8_epilogue(const I8Params& p, const I8Cta& x, i
                         i8_ld16(from + 64u * c + (static_cast<uint32_t>(h) << 20), u);
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const int n = __float2int_rn(__uint_as_float(u[i]));
-                            v[c][16 * h + i] = decltype(first)::value ? n : v[c][16 * h + i] + n;
+                            int& sum = v[c][16 * h + i];
+                            const float f = __uint_as_float(u[i]);
+                            if (decltype(exact)::value)
+                                sum = decltype(first)::value ? __float_as_int(f)
+                                                             : __float_as_int(__int_as_float(sum) + f);
+                            else
+                                sum = decltype(first)::value ? __float2int_rn(f) : sum + __float2int_rn(f);
                         }
                     }
                 }
@@ -637,10 +647,17 @@ __device__ __forceinline__ void i8_epilogue(const I8Params& p, const I8Cta& x, i
             ok = i8_wait(x.tfull + 8u * acc.at, acc.phase, p, x);
             if (!ok) break;
             tc_fence_after_sync();
-            if (mine && s == s0)
-                add(std::true_type());
-            else if (mine)
-                add(std::false_type());
+            if (mine && two) {
+                if (s == s0)
+                    add(std::true_type(), std::true_type());
+                else
+                    add(std::false_type(), std::true_type());
+            } else if (mine) {
+                if (s == s0)
+                    add(std::true_type(), std::false_type());
+                else
+                    add(std::false_type(), std::false_type());
+            }
             tc_fence_before_sync();
             __syncwarp();
             if (x.lane == 0)
@@ -685,6 +702,12 @@ __device__ __forceinline__ void i8_epilogue(const I8Params& p, const I8Cta& x, i
                 }
         }
         if (!mine) continue;
+        if (!two) {
+#pragma unroll
+            for (int c = 0; c < C::NC; ++c)
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[c][i] = __float_as_int(__int2float_rn(v[c][i]));
+        }
         float sw[4], bias[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -702,7 +725,7 @@ __device__ __forceinline__ void i8_epilogue(const I8Params& p, const I8Cta& x, i
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
                     const int i = 16 * (h >> 1) + 4 * (k >> 1) + 2 * (h & 1) + (k & 1);
-                    o[i] = fmaf(__int2float_rn(v[0][i]) * s, sw[h], bias[h]);
+                    o[i] = fmaf(__int_as_float(v[0][i]) * s, sw[h], bias[h]);
                 }
             }
 #pragma unroll

@@ -208,7 +208,7 @@ def test_products_on_pairs(T, N, K):
 
 
 @pytest.mark.parametrize("T,N", [(3, 200), (70, 200), (260, 5000)])
-@pytest.mark.parametrize("K", [1024, 1025, 2048, 4096, 16400])
+@pytest.mark.parametrize("K", [1024, 1025, 2047, 2048, 2049, 4096, 16400])
 def test_sums_are_exact_at_full_magnitude(T, N, K):
     """Sums past what fp32 holds: all products +-2^14 or near, some rows with one sign."""
     rng = np.random.default_rng(K + T)
