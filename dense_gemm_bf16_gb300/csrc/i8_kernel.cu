@@ -168,29 +168,21 @@ __device__ __forceinline__ void i8_st_cluster(uint32_t addr, int v) {
     asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// Acquires what the CTAs of the cluster wrote before they arrived.
-__device__ __forceinline__ bool i8_try_wait_cluster(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.b32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
 // Bounded wait of a whole warp.  All lanes ask and vote, which costs least where the phase has
-// completed, and the compiler knows a vote to be the same in all lanes (see i8_issue).  A
-// warp that has to wait is suspended: polling, it took issue slots from the epilogue, which
-// shares its scheduler.
+// completed, and the compiler knows a vote to be the same in all lanes (see i8_issue).  A wait
+// that runs out is voted on too: a lane that gave up by its own clock would leave the others at
+// their next shuffle for ever.  A warp that has to wait is suspended: polling, it took issue
+// slots from the epilogue, which shares its scheduler.  CLUSTER: acquires what the CTAs of the
+// cluster wrote before they arrived.
 constexpr uint32_t kI8Suspend = 20000;  // ns
 
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool i8_wait(uint32_t bar, uint32_t parity, const I8Params& p, const I8Cta& x) {
     uint64_t t0 = 0;
     for (uint32_t it = 1;; ++it) {
-        if (__all_sync(0xffffffffu, mbar_try_wait_ns(bar, parity, kI8Suspend))) return true;
+        const bool done = CLUSTER ? mbar_try_wait_cluster_ns(bar, parity, kI8Suspend)
+                                  : mbar_try_wait_ns(bar, parity, kI8Suspend);
+        if (__all_sync(0xffffffffu, done)) return true;
         if ((it & 7u) == 0) {
             const uint64_t now = globaltimer_ns();
             if (t0 == 0) t0 = now;
@@ -679,19 +671,11 @@ __device__ __forceinline__ void i8_epilogue(const I8Params& p, const I8Cta& x, i
                             i8_st_cluster(at + (c_first + 64 * c + i) * 512u, v[c][i]);
                 }
                 __syncwarp();
-                if (x.lane == 0) mbar_arrive_remote(mapa_shared(x.red_bar, 0u));
+                // (test only: with test_stall 2 they never arrive, so the first CTA's wait expires)
+                if (x.lane == 0 && p.g.test_stall != 2) mbar_arrive_remote(mapa_shared(x.red_bar, 0u));
                 return;
             }
-            const uint64_t begin = globaltimer_ns();
-            while (!i8_try_wait_cluster(x.red_bar, 0u)) {
-                if (*x.abort_flag) return;
-                if (globaltimer_ns() - begin > p.g.timeout_ns) {
-                    *x.abort_flag = 1;
-                    if (p.g.status) DG_SET_TIMEOUT(p.g.status);
-                    return;
-                }
-            }
-            __syncwarp();
+            if (!i8_wait<true>(x.red_bar, 0u, p, x)) return;
             if (mine)
                 for (int r = 1; r < p.splits; ++r) {
                     const int* from = x.red + (r - 1) * BT * 128 + q * 32 + x.lane;

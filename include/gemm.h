@@ -458,7 +458,9 @@ gemm_status_t gemm_strided_plan_query(gemm_dtype_t ab_dtype, int64_t batch,
  *                         expires and the kernel reports GEMM_ERR_TIMEOUT; 2 makes
  *                         the first CTA of the next launch with stream-K pieces
  *                         leave its partial unpublished, so the waits of the
- *                         pieces that need it expire instead.  The knob resets
+ *                         pieces that need it expire instead (of gemm_i8, where
+ *                         CTAs share a tile's contraction: all of them but the first
+ *                         leave their sums unannounced).  The knob resets
  *                         itself after that launch.
  *   GEMM_OPT_TEST_DEBUG_BOUND  debug build, test only: the next tensor-core launch
  *                         gets one bound of its device-side checks set too small

@@ -553,3 +553,24 @@ def test_the_tokens_pass_does_not_count_as_a_wait():
     finally:
         dg.gemm_set_option(dg.Option.TIMEOUT_US, 1000000)
     assert bool((y == 1024).all())
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 300, 8192), (32, 1000, 1024)])
+def test_sums_that_never_arrive_report_a_timeout_and_recover(T, N, K):
+    """CTAs that share a tile's contraction: the first one's wait for the others' sums runs out
+    (four CTAs, then two)."""
+    rng = np.random.default_rng(12)
+    c = case(rng, T, N, K)
+    good = run(*c, out_dtype=F32)
+    dg.gemm_set_option(dg.Option.TIMEOUT_US, 2000)
+    try:
+        for _ in range(5):
+            dg.gemm_set_option(dg.Option.TEST_STALL, 2)
+            run(*c, out_dtype=F32)
+            assert status() == dg.Status.ERR_TIMEOUT
+    finally:
+        dg.gemm_set_option(dg.Option.TEST_STALL, 0)
+        dg.gemm_set_option(dg.Option.TIMEOUT_US, 1000000)
+    assert status() == 0
+    assert torch.equal(run(*c, out_dtype=F32), good)
+    assert status() == 0
