@@ -354,6 +354,11 @@ __device__ __forceinline__ void i8_convert(const I8Params& p, const I8Cta& x, in
         const bool more = rg_tile<CG, BT, RG_ROWS>(p.g, walk, t, x.lane, SPLIT ? 0u : x.rank, w);
         if (!__all_sync(0xffffffffu, more)) break;
         for (int s = s0; s < s1; ++s) {
+            // (the tokens' pass's time is not the bounded waits': it is waited for in front of the
+            // first of them that depends on it, which is for a stage that the loader fills behind
+            // the pass or, where shared memory has more stages than tensor memory, for a place
+            // there that an MMA gives back)
+            if (C::SA <= C::TA && p.g.pdl && done == C::SA) griddep_wait();
             ok = i8_wait(x.afull + 8u * in.at, in.phase, p, x);
             if (!ok) break;
             const uint32_t src = a_row + in.at * C::A_BYTES;
@@ -369,7 +374,8 @@ __device__ __forceinline__ void i8_convert(const I8Params& p, const I8Cta& x, in
                     i8_halves(v.w, r[8 * c + 6], r[8 * c + 7]);
                 }
                 if (j == 0) {
-                    if (p.g.pdl && done++ == C::TA) griddep_wait();
+                    if (C::SA > C::TA && p.g.pdl && done == C::TA) griddep_wait();
+                    ++done;
                     ok = i8_wait(x.wempty + 8u * out.at, out.phase ^ 1u, p, x);
                     if (!ok) break;
                     tc_fence_after_sync();

@@ -574,3 +574,26 @@ def test_sums_that_never_arrive_report_a_timeout_and_recover(T, N, K):
     assert status() == 0
     assert torch.equal(run(*c, out_dtype=F32), good)
     assert status() == 0
+
+
+@pytest.mark.parametrize("T,N,splits", [(32, 1024, 4), (32, 9000, 2), (20, 10240, 1), (64, 10240, 1),
+                                        (100, 10240, 1), (130, 10240, 1)])
+def test_a_long_pass_beside_few_tiles_does_not_count_as_a_wait(T, N, splits):
+    """Few long rows that start on odd elements: their quantisation takes some hundred
+    microseconds on as many SMs, while the product's CTAs wait on the others.  Every form: a
+    tile shared by four CTAs and by two, 32, 64 and 128 columns, pairs."""
+    K = 131056
+    gen = torch.Generator(device=DEV).manual_seed(T)
+    x = torch.randn((T, K + 2), generator=gen, device=DEV)[:, 1:-1]
+    q = torch.randint(-127, 128, (N, K), generator=gen, device=DEV, dtype=torch.int8)
+    s = torch.rand(N, generator=gen, device=DEV)
+    xi, sx = dg.i8_quantize(x)
+    want = dg.i8_gemm(xi, q, s, x_scales=sx, out_dtype=F32)
+    dg.gemm_set_option(dg.Option.TIMEOUT_US, 50)
+    try:
+        for _ in range(3):
+            y = dg.i8_gemm(x, q, s)
+            assert status() == 0
+            assert torch.equal(y, want)
+    finally:
+        dg.gemm_set_option(dg.Option.TIMEOUT_US, 1000000)
