@@ -559,10 +559,21 @@ __device__ __forceinline__ float i8_gelu_tanh(float x) {
     return __fdividef(x, 1.0f + e);
 }
 
+// max(x, 0) that keeps a NaN: a token with an infinity or a NaN has a NaN scale, which has to show
+// in its results (the other kernels' relu makes it 0).
+__device__ __forceinline__ float i8_relu(float x) {
+    float r;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 __device__ __forceinline__ void i8_act(float (&v)[32], int act) {
     if (act == ACT_GELU_TANH) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = i8_gelu_tanh(v[i]);
+    } else if (act == ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = i8_relu(v[i]);
     } else {
         rg_act(v, act);
     }

@@ -80,7 +80,7 @@ typedef enum { GEMM_DT_BF16 = 0, GEMM_DT_F16 = 1, GEMM_DT_F32 = 2, GEMM_DT_I8 = 
  *   bit 0     add the bias vector (fp32, device memory);
  *   bits 1-2  activation: 0 none, 1 GELU tanh form
  *             0.5x(1 + tanh(sqrt(2/pi)(x + 0.044715x^3))), 2 ReLU (x > 0 ? x : 0,
- *             NaN gives 0), 3 GELU erf form 0.5x(1 + erf(x/sqrt(2)));
+ *             NaN gives 0; gemm_i8 keeps a NaN), 3 GELU erf form 0.5x(1 + erf(x/sqrt(2)));
  *   bit 3     the bias runs along rows: bias[m], length M (requires bit 0);
  *             without it bias[n], length N.
  * The bias is added before the activation and is not scaled by alpha.

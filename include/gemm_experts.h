@@ -290,7 +290,8 @@ gemm_status_t gemm_i8_quantize(gemm_dtype_t dtype, int64_t T, int64_t K, const v
  *   C, ldc       T x N, row-major, GEMM_DT_BF16, GEMM_DT_F16 or GEMM_DT_F32.
  *   offsets      device group offsets as above, or NULL with groups == 1: one matrix for
  *                all rows.
- *   bias, stride_bias, epi   as gemm_grouped.
+ *   bias, stride_bias, epi   as gemm_grouped, but ReLU keeps a NaN, so that a token or a
+ *                channel with a NaN scale gives NaN through every epilogue.
  *   workspace    gemm_i8_workspace_size() bytes, 256-byte aligned: the tokens' integers as
  *                16-bit operands, and copies of weights that are not used in place.
  */

@@ -597,3 +597,26 @@ def test_a_long_pass_beside_few_tiles_does_not_count_as_a_wait(T, N, splits):
             assert torch.equal(y, want)
     finally:
         dg.gemm_set_option(dg.Option.TIMEOUT_US, 1000000)
+
+
+@pytest.mark.parametrize("epilogue", ["relu", "bias_relu", "gelu_tanh", "bias_gelu_erf"])
+@pytest.mark.parametrize("T,N,K", [(5, 130, 2048), (40, 300, 160), (100, 9001, 64), (700, 3000, 96)])
+def test_tokens_without_a_scale_are_nan_through_every_activation(epilogue, T, N, K):
+    """A token with a NaN or an infinity has a NaN scale, and so has a channel: neither may
+    come out as zeros.  All others are as in the call on their own."""
+    gen = torch.Generator(device=DEV).manual_seed(T)
+    x = torch.randn((T, K), generator=gen, device=DEV)
+    q = torch.randint(-127, 128, (N, K), generator=gen, device=DEV, dtype=torch.int8)
+    s = torch.rand(N, generator=gen, device=DEV) * 1e-3
+    bias = torch.randn(N, generator=gen, device=DEV) if epilogue.startswith("bias") else None
+    want = dg.i8_gemm(x, q, s, bias=bias, epilogue=epilogue)
+    assert not torch.isnan(want).any()
+    if epilogue.endswith("relu"):
+        plain = dg.i8_gemm(x, q, s, bias=bias)
+        assert torch.equal(want, plain.clamp(min=0)) and (plain < 0).any()
+    x[1, K // 2], x[3, 0], s[7] = float("nan"), -float("inf"), float("nan")
+    want[1], want[3], want[:, 7] = float("nan"), float("nan"), float("nan")
+    for out in (F32, BF):
+        got = dg.i8_gemm(x, q, s, bias=bias, epilogue=epilogue, out_dtype=out)
+        assert torch.equal(torch.isnan(got), torch.isnan(want))
+        assert torch.equal(got.nan_to_num(-9.0), want.to(out).nan_to_num(-9.0))
