@@ -64,6 +64,7 @@ struct DevState {
     int max_pairs[3][3] = {};  // co-resident two-CTA clusters [mode][BN 128, 256, 512] (mode 2)
     std::once_flag experts_once;  // kernels of the expert-layer entry points
     cudaError_t experts_err = cudaSuccess;
+    cudaError_t i8_err = cudaSuccess;  // ... of gemm_i8, which no other call depends on
 };
 DevState g_dev[kMaxDevices];
 
@@ -1063,9 +1064,9 @@ gemm_status_t device_info(DeviceInfo* out) {
         if (e == cudaSuccess) e = rg_prepare_wgrad();
         if (e == cudaSuccess) e = rg_prepare_seq();
         if (e == cudaSuccess) e = w4_prepare();
-        if (e == cudaSuccess) e = i8_prepare();
         d->experts_err = e;
-        if (e != cudaSuccess) cudaGetLastError();
+        d->i8_err = i8_prepare();
+        if (e != cudaSuccess || d->i8_err != cudaSuccess) cudaGetLastError();
     });
     if (d->experts_err != cudaSuccess) return GEMM_ERR_CUDA;
     out->sm_count = d->sm_count;
@@ -1076,6 +1077,7 @@ gemm_status_t device_info(DeviceInfo* out) {
         if (cap / 2 < out->max_pairs) out->max_pairs = static_cast<int>(cap / 2);
     }
     out->status = d->status;
+    out->i8 = d->i8_err == cudaSuccess;
     return GEMM_OK;
 }
 

@@ -111,6 +111,7 @@ gemm_status_t gemm_i8(gemm_dtype_t x_dtype, int64_t groups, int64_t T, int64_t N
     DeviceInfo d;
     st = device_info(&d);
     if (st != GEMM_OK) return st;
+    if (!d.i8) return GEMM_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
     float* made = reinterpret_cast<float*>(ws + l.x_bytes);

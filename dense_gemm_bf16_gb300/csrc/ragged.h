@@ -102,6 +102,7 @@ struct DeviceInfo {
     int sm_count;      // CTAs a launch may have: one per SM, or the cap of GEMM_OPT_MAX_CTAS
     int max_pairs;     // two-CTA clusters resident at once, under the cap (0: none)
     int* status;       // device error word
+    bool i8;           // gemm_i8's kernels are ready
 };
 gemm_status_t device_info(DeviceInfo* out);   // the current device
 uint64_t option_timeout_ns();
