@@ -541,14 +541,16 @@ def _row_pitch(name, t):
     ld = _ld(name, t)
     if t.is_contiguous():
         return ld
-    rows, step = t.shape[-2], ld * t.shape[-2]
-    if rows == 1:                           # (the rows are those of the dimension before)
-        ld = step = t.stride(-3) if t.shape[-3] > 1 else ld
-    for i in range(t.dim() - 3, -1, -1):
-        if t.shape[i] > 1 and t.stride(i) != step:
+    step = None                             # the rows' distance, times those seen so far
+    for n, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n == 1:
+            continue
+        if step is None:
+            ld = step = stride
+        if stride != step or stride < t.shape[-1]:
             raise ValueError(f"{name}'s rows must lie at one distance (shape {tuple(t.shape)}, "
                              f"strides {tuple(t.stride())})")
-        step *= t.shape[i]
+        step *= n
     return ld
 
 

@@ -235,3 +235,16 @@ def test_references():
     assert sums.tolist() == [[3], [30]]
     bits = ref.i8_bits(sums, [2.0, 0.5], [[4.0], [1.0]], torch.float32, [0, 1, 2])
     assert bits.tolist() == [[24.0], [15.0]]
+
+
+def test_rows_at_one_distance_over_any_leading_dimensions():
+    """i8_quantize takes rows that lie at one distance, whichever leading dimensions are one."""
+    from dense_gemm_bf16_gb300 import experts
+    for lead in ((5,), (4, 1), (1, 4), (4, 1, 1), (1, 4, 1), (4, 3, 1), (2, 1, 3), (4, 1, 3, 1), (1, 1, 1)):
+        for pad in (0, 3):
+            t = torch.empty(lead + (8 + pad,))[..., :8]
+            assert experts._row_pitch("x", t) == 8 + pad or t[..., 0].numel() == 1, (lead, pad)
+    for t in (torch.empty((4, 2, 8))[::2, :, :5], torch.empty((4, 1, 3, 8))[:, :, :2],
+              torch.empty((3, 8)).expand(2, 3, 8), torch.empty((1, 1, 8)).expand(4, 1, 8), torch.empty((4, 1, 1, 8))[..., ::2]):
+        with pytest.raises(ValueError):
+            experts._row_pitch("x", t)
