@@ -620,3 +620,63 @@ def test_tokens_without_a_scale_are_nan_through_every_activation(epilogue, T, N,
         got = dg.i8_gemm(x, q, s, bias=bias, epilogue=epilogue, out_dtype=out)
         assert torch.equal(torch.isnan(got), torch.isnan(want))
         assert torch.equal(got.nan_to_num(-9.0), want.to(out).nan_to_num(-9.0))
+
+
+def example():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "expert_layer.py")
+    spec = importlib.util.spec_from_file_location("expert_layer", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    return mod
+
+
+@pytest.mark.parametrize("T", [1, 33])
+def test_the_example_answers_in_8_bits(T):
+    """Against its own steps, token by token and expert by expert without a dispatch: products
+    have the same bits alone, and the sum of `top` terms is off by an fp32 rounding for each."""
+    mod = example()
+    gen = torch.Generator(device=DEV).manual_seed(T)
+    D, H, E, top = 256, 512, 8, 2
+    x = torch.randn((T, D), generator=gen, device=DEV).to(BF)
+    w1 = dg.i8_quantize(torch.randn((E, H, D), generator=gen, device=DEV) * D ** -0.5)
+    w2 = dg.i8_quantize(torch.randn((E, D, H), generator=gen, device=DEV) * H ** -0.5)
+    expert, share = mod.route(x, torch.randn((D, E), generator=gen, device=DEV), top)
+    got = mod.answer_in_8_bits(x, w1, w2, (expert, share))
+    assert got.dtype == F32 and got.shape == (T, D)
+    for t in range(T):
+        want, size = torch.zeros(D, dtype=torch.float64, device=DEV), 0.0
+        for j in range(top):
+            e = int(expert[t, j])
+            h = dg.i8_gemm(x[t:t + 1], w1[0][e], w1[1][e], epilogue="gelu_tanh")
+            y = dg.i8_gemm(h, w2[0][e], w2[1][e])[0].double() * share[t, j].double()
+            want, size = want + y, size + y.abs()
+        assert bool(((got[t].double() - want).abs() <= (top + 1) * 2.0 ** -24 * size).all())
+    assert status() == 0
+
+
+@pytest.mark.parametrize("T", [20, 2500])
+def test_a_layer_in_8_bits_captured_whole(T):
+    """Quantise, dispatch (one launch, then two), two products and combine in one graph, replayed
+    on new tokens and routes: the bits of the calls one by one."""
+    mod = example()
+    gen = torch.Generator(device=DEV).manual_seed(T)
+    D, H, E, top = 320, 640, 12, 3
+    x = torch.randn((T, D), generator=gen, device=DEV).to(BF)
+    w1 = dg.i8_quantize(torch.randn((E, H, D), generator=gen, device=DEV) * D ** -0.5)
+    w2 = dg.i8_quantize(torch.randn((E, D, H), generator=gen, device=DEV) * H ** -0.5)
+    expert, share = mod.route(x, torch.randn((D, E), generator=gen, device=DEV), top)
+    mod.answer_in_8_bits(x, w1, w2, (expert, share))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = mod.answer_in_8_bits(x, w1, w2, (expert, share))
+    for _ in range(3):
+        x.copy_(torch.randn((T, D), generator=gen, device=DEV))
+        expert.copy_(torch.randint(0, E, (T, top), generator=gen, device=DEV))
+        share.copy_(torch.rand((T, top), generator=gen, device=DEV))
+        for _ in range(3):
+            graph.replay()
+        assert torch.equal(y, mod.answer_in_8_bits(x, w1, w2, (expert, share)))
+    assert status() == 0
