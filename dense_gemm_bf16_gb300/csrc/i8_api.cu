@@ -140,8 +140,9 @@ gemm_status_t gemm_i8(gemm_dtype_t x_dtype, int64_t groups, int64_t T, int64_t N
     q.bias = (epi & 1) ? bias : nullptr;
     q.stride_bias = stride_bias;
     q.act = act;
-    // (the product overlaps the tokens' pass, but reads offsets and weights before it waits for
-    // it: weights must not be copied in front of the pass, and there must be a pass)
+    // (the product starts where the tokens' pass leaves an SM free, a CTA of it fits beside no
+    // block of the pass, and reads offsets and weights before it waits for the pass: weights must
+    // not be copied in front of it, and there must be a pass)
     q.pdl = l.q_bytes == 0 && K > 0;
     int cg, bt;
     i8_variant(q, d, &cg, &bt);
@@ -154,7 +155,7 @@ gemm_status_t gemm_i8(gemm_dtype_t x_dtype, int64_t groups, int64_t T, int64_t N
     p.w_scales = w_scales;
     p.stride_ws = groups > 1 ? stride_ws : 0;
     // CTAs of a cluster share a tile where all tiles there may be leave half of the SMs
-    // idle, each with four stages at least
+    // idle, each with two 256-deep stages at least
     p.splits = 1;
     if (cg == 1 && bt == 32)
         while (p.splits < 4 && tiles * p.splits * 2 <= d.sm_count && cdiv(K, 256) >= p.splits * 4)

@@ -15,7 +15,7 @@
 //   warp 2       loads 128 weight rows x 128 bytes by TMA (128-byte swizzle);
 //   warps 4-11   read half of their lane's row, make fp16 pairs by byte permutes (b ^ 128 under the
 //                exponent of 1024 is 1152 + b; one packed subtraction) and store them to
-//                tensor memory, 64 columns a stage;
+//                tensor memory, 64 columns for 128 of them;
 //   warp 0       loads the tokens' fp16 rows by TMA (made once per call in the workspace);
 //   warp 1       issues tcgen05.mma with its A operand in tensor memory;
 //   warps 12-19  add accumulators up and write the result.
@@ -34,12 +34,13 @@
 // the CTAs of a cluster share a tile's contraction and send their integer sums to the first
 // one's shared memory.
 //
-// Bounds and times (graph replay, with the tokens' pass).  One token of 8192 x 8192: 20 us
-// (16 without the quantisation), the bytes take 10: start-up, and 128 of the 152 SMs have a
-// tile.  192 rows over 64 experts of 2048 x 2048: 47 us, the bytes 40.  1500 tokens of 4096 x
-// 4096: 40 us, the products 26: two rounds of 128 tiles on 76 pairs, and the pass (5).  16384
-// rows over 16 experts, 2048 to 4096, GELU: 190 us, the products 143: issue slots, most of them
-// taken by the sums, scales, GELU and the conversion of the weights, and the pass (17).
+// Bounds and times (graph replay, with the tokens' pass, inputs in turn).  One token of 8192 x
+// 8192: 19 us (weights in L2: 16), the bytes take 10: start-up, the pass in front, and 128 of the
+// 152 SMs have a tile.  192 rows over 64 experts of 2048 x 2048: 47 us, the bytes 40.  1500 tokens
+// of 4096 x 4096: 40 us, the products 26: two rounds of 128 tiles on 76 pairs, and the pass (5).
+// 16384 rows over 16 experts, 2048 to 4096, GELU: 190 us (1024 rows each: 197), the products 143:
+// issue slots, most of them taken by the sums, scales, GELU and the conversion of the weights, and
+// the pass (17).
 #include "i8.h"
 #include "ragged_kernel.cuh"
 
@@ -551,7 +552,7 @@ __device__ __forceinline__ void i8_store32(const RgParams& p, int64_t base, int 
 
 // GELU's tanh form as x / (1 + exp(-2 y)), y = sqrt(2 / pi) (x + 0.044715 x^3): half the
 // instructions of 0.5 x (1 + tanh y), as the other kernels have it: their issue slots are free, this
-// one's are not (16384 rows over 16 experts, 2048 to 4096: 205 us against 221).  The exponent is taken to base 2.
+// one's are not (16384 rows over 16 experts, 2048 to 4096: 190 us against 204).  The exponent is taken to base 2.
 __device__ __forceinline__ float i8_gelu_tanh(float x) {
     constexpr float k = -2.0f * 0.7978845608028654f * 1.4426950408889634f;
     float e;
@@ -618,8 +619,8 @@ __device__ __forceinline__ void i8_epilogue(const I8Params& p, const I8Cta& x, i
         bool ok = true;
         // Two accumulators' sum in fp32 is rounded as its integer would be for the scaling: with no
         // more than two the sums stay fp32 numbers and save the conversions, whose rate
-        // is a fraction of an addition's (16384 rows over 16 experts, 2048 to 4096, GELU: 203 us with
-        // them, 197 without).
+        // is a fraction of an addition's (16384 rows over 16 experts, 2048 to 4096, GELU: 196 us with
+        // them, 190 without).
         const bool two = !SPLIT && s1 - s0 <= 2 * C::SUM;
         // an accumulator to the sums (the first one replaces them)
         auto add = [&](auto first, auto exact) {

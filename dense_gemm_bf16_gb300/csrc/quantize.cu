@@ -16,11 +16,11 @@
 // each (16 where rows are not aligned), and load the next row's meanwhile; what a row has
 // beyond is read again, from L2.  Units that need more care (a border, a scale outside fp32's
 // middle) are read again element by element in one copy of the code: unrolled beside the
-// others it did not stay in the instruction cache (4096 x 4095 fp32: 36 us against 17.6).
+// others it did not stay in the instruction cache (4096 x 4095 fp32: 36 us, now 16.7).
 //
-// 4096 x 4096 bf16: 8.9 us by graph replay, 5.6 TB/s, where the copy rate would take 7.4 (the issue
-// slots are 70 % busy); 1001 x 7001 fp32, rows that start anywhere: 9.5 against 5.2 (3.3 rows for
-// each block).
+// 4096 x 4096 bf16: 9.4 us by graph replay over six inputs in turn, 5.3 TB/s, where the copy rate
+// would take 7.4 (the issue slots are 67 % busy; one input again and again: 8.4); 1001 x 7001 fp32,
+// rows that start anywhere: 9.6 against 5.2 (3.3 rows for each block; one input: 8.3).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -570,7 +570,7 @@ def i8_gemm(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, *, x_scales=
     The result is bf16 (default for int8 x, else x's dtype), fp16 or fp32.
 
     Sums are exact integers and the result is rounded once: a row's bits do not depend on the
-    call's other rows.  Rows of q on 16-byte boundaries are used in place, others copied."""
+    call's other rows.  NaN scales give NaN, through ReLU too.  Rows of q on 16-byte boundaries are used in place, others copied."""
     given = x.dtype is torch.int8
     if not given and x.dtype not in _CODE:
         raise TypeError("x must be int8, bfloat16, float16 or float32")

@@ -433,7 +433,11 @@ gemm_status_t gemm_strided_plan_query(gemm_dtype_t ab_dtype, int64_t batch,
  *                         dependent (not for the cooperative stream-K forms): its
  *                         CTAs set up while the copy runs and wait for the copy's
  *                         completion before their first operand load; 1: the GEMM
- *                         starts after the copy in plain stream order.
+ *                         starts after the copy in plain stream order.  The same
+ *                         holds, in gemm_experts.h, for copies of the grouped
+ *                         products' operands and the 4-bit weights made 16-bit, for
+ *                         gemm_i8 behind its pass over the tokens and for
+ *                         gemm_expert_dispatch behind its count.
  *   GEMM_OPT_EPILOGUE_WARPS 0 (default): whole 256-wide CTA-pair tiles run their
  *                         epilogue on eight warps, each writing half of a lane
  *                         quarter's columns, when their output takes plain stores

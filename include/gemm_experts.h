@@ -96,8 +96,9 @@ gemm_status_t gemm_expert_combine(gemm_dtype_t dtype, int64_t T, int64_t K, int6
  *   rows         of the forward call; read only if d_weights is wanted.
  *   d_weights, dw_dtype, ld_dweights   T x top of any of the three types, summed in
  *                fp32, or NULL: not wanted.
- *   Other arguments as gemm_expert_combine.  Without weights and d_weights this
- *   copies tokens to rows that exist already (a second tensor's dispatch).
+ *   Other arguments as gemm_expert_combine; no output may overlap an input.  Without
+ *   weights and d_weights this copies tokens to rows that exist already (a second
+ *   tensor's dispatch).
  */
 gemm_status_t gemm_expert_combine_grad(gemm_dtype_t dtype, int64_t T, int64_t K, int64_t top,
                                        const void* DY, int64_t lddy, const int32_t* slots,
@@ -262,7 +263,7 @@ size_t gemm_w4_workspace_size(gemm_dtype_t ab_dtype, int64_t groups, int64_t T, 
  * [N][K] over the inputs of each output channel.
  *
  *   dtype        GEMM_DT_BF16, GEMM_DT_F16 or GEMM_DT_F32.   X, ldx   T x K, row-major.
- *   Q, ldq       T x K, row-major.      scales   T values.
+ *   Q, ldq       T x K, row-major, not over X.      scales   T values.
  */
 gemm_status_t gemm_i8_quantize(gemm_dtype_t dtype, int64_t T, int64_t K, const void* X, int64_t ldx,
                                int8_t* Q, int64_t ldq, float* scales, gemm_stream_t stream);
@@ -287,7 +288,8 @@ gemm_status_t gemm_i8_quantize(gemm_dtype_t dtype, int64_t T, int64_t K, const v
  *                same for all).  Matrices whose base, ldq and stride_q are multiples of 16
  *                bytes (stride_q at least ldq) are used in place, others copied first.
  *   w_scales, stride_ws   fp32, N values per group, stride_ws elements apart (0: the same).
- *   C, ldc       T x N, row-major, GEMM_DT_BF16, GEMM_DT_F16 or GEMM_DT_F32.
+ *   C, ldc       T x N, row-major, GEMM_DT_BF16, GEMM_DT_F16 or GEMM_DT_F32; not over an
+ *                input.
  *   offsets      device group offsets as above, or NULL with groups == 1: one matrix for
  *                all rows.
  *   bias, stride_bias, epi   as gemm_grouped, but ReLU keeps a NaN, so that a token or a
